@@ -284,10 +284,7 @@ def _own_prefill(st):
 
 def _own_verify(st):
     import paged_split_kv_attn_gb300 as pskv
-    if "workspace" not in st:
-        st["workspace"] = pskv.verify_drafts_workspace(st["case"]["rows"], st["case"]["vocab"])
-    tokens, accepted = pskv.verify_drafts(st["target"], st["draft"], st["drafts"], st["u"], num_drafts=st["given"],
-                                          workspace=st["workspace"])
+    tokens, accepted = pskv.verify_drafts(st["target"], st["draft"], st["drafts"], st["u"], num_drafts=st["given"])
     return dict(tokens=tokens, accepted=accepted)
 
 
