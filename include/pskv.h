@@ -65,6 +65,12 @@ typedef struct CUevent_st *pskv_event_t;
 #define PSKV_FORMAT_SPLIT 0   /* K and V rows kept whole, one region each */
 #define PSKV_FORMAT_FOLDED 1  /* K keeps only its first head_dim_v/4 columns (pegainfer #1055's
                                  640-column row at head dim 512), V in full; bf16 only */
+#define PSKV_FORMAT_LATENT 2  /* one region: a latent vector and one rotated key per token, shared by
+                                 all query heads; bf16 only */
+
+/* ---- which columns the rotation of kv_prep_append_latent pairs ----------------- */
+#define PSKV_PAIRS_HALVES 0    /* (i, i + 32) */
+#define PSKV_PAIRS_ADJACENT 1  /* (2i, 2i + 1) */
 
 /* ---- device fault bits, ORed into status[0] of the layout's status word ------ */
 #define PSKV_FAULT_BAD_PAGE 1u      /* a table entry outside [0, num_pages): that tile or row skipped */
@@ -75,6 +81,7 @@ typedef struct CUevent_st *pskv_event_t;
 #define PSKV_FAULT_BAD_STATE 32u    /* merge input with m = -inf but l != 0, or a NaN m: treated as empty */
 #define PSKV_FAULT_BAD_POSITION 64u /* a prep token whose rotation position is outside the table: skipped */
 #define PSKV_FAULT_BAD_MASK 128u    /* a tree mask without its own bit or with a later one: later bits ignored */
+#define PSKV_FAULT_BAD_TOKEN 256u   /* a drafted token outside the vocabulary: refused like any other */
 
 /* ---- limits ---------------------------------------------------------------- */
 #define PSKV_MAX_SPLITS 1024       /* most partitions one decode call may use */
@@ -82,6 +89,10 @@ typedef struct CUevent_st *pskv_event_t;
 #define PSKV_MERGE_GROUP 16        /* partials folded per level-1 group of the merge */
 #define PSKV_KEY_TILE 16           /* keys per kernel tile; partitions are whole tiles */
 #define PSKV_MAX_WINDOW_TOKENS 64  /* query tokens per row of decode_attn_multirow */
+#define PSKV_LATENT_ROT 64         /* rotated columns of a latent row (and of its queries) */
+#define PSKV_LATENT_MAX_HEADS 128  /* query heads of decode_attn_latent */
+#define PSKV_EXPANDED_NOPE 128     /* unrotated columns of an expanded query or key */
+#define PSKV_EXPANDED_V 128        /* columns of an expanded value */
 
 /* Description of one paged KV pool.
  *
@@ -104,17 +115,25 @@ typedef struct CUevent_st *pskv_event_t;
  * are head_dim_v wide and the score of key i is
  *     scale * (q[0:Dr] . k_i[0:Dr] + q[Dr:Dv] . v_i[Dr:Dv]),  Dr = Dv/4,
  * i.e. the key is taken to equal V outside the rotated quarter once the norm
- * weight sits in q (this library's reading of the page). */
+ * weight sits in q (this library's reading of the page).
+ *
+ * Latent format: a token keeps one row of head_dim_v + PSKV_LATENT_ROT columns,
+ * its normalised latent vector c (head_dim_v columns) and one rotated key r,
+ * which every query head shares (num_kv_heads = 1).  k_pool holds the rows,
+ * [num_pages][page_size][head_dim_k]; v_pool is NULL: the values are the rows'
+ * first head_dim_v columns.  Written by kv_prep_append_latent, read by
+ * decode_attn_latent; every other call refuses the format (UNSUPPORTED). */
 typedef struct pskv_layout_desc {
   int64_t num_pages;   /* pages in each region, >= 1 */
   int32_t page_size;   /* keys per page: a multiple of PSKV_KEY_TILE */
   int32_t num_kv_heads;
-  int32_t head_dim_k;  /* stored K columns: head_dim_v (split) or head_dim_v / 4 (folded) */
+  int32_t head_dim_k;  /* stored K columns: head_dim_v (split), head_dim_v / 4 (folded) or
+                          head_dim_v + PSKV_LATENT_ROT (latent) */
   int32_t head_dim_v;  /* 256 or 512 */
   int32_t kv_dtype;    /* PSKV_DTYPE_F32 or PSKV_DTYPE_BF16 (queries use the same type) */
-  int32_t format;      /* PSKV_FORMAT_SPLIT or PSKV_FORMAT_FOLDED */
+  int32_t format;      /* PSKV_FORMAT_SPLIT, PSKV_FORMAT_FOLDED or PSKV_FORMAT_LATENT */
   void *k_pool;        /* device, 16-byte aligned */
-  void *v_pool;        /* device, 16-byte aligned */
+  void *v_pool;        /* device, 16-byte aligned (latent: NULL) */
   int32_t *status;     /* device int32[4] or NULL */
 } pskv_layout_desc;
 
@@ -148,7 +167,8 @@ typedef struct pskv_decode_opts {
  * Errors: INVALID_ARG (null pointers, sizes < 1, misaligned pools,
  * page_size not a multiple of PSKV_KEY_TILE, unknown format), UNSUPPORTED
  * (head_dim_v not 256/512; split with head_dim_k != head_dim_v; folded with
- * head_dim_k != head_dim_v / 4 or an f32 pool). */
+ * head_dim_k != head_dim_v / 4 or an f32 pool; latent with head_dim_k !=
+ * head_dim_v + PSKV_LATENT_ROT, num_kv_heads != 1 or an f32 pool). */
 int paged_kv_layout_create(const pskv_layout_desc *desc, pskv_layout **out);
 
 /* Free a handle (NULL is ignored).  The pools are the caller's. */
@@ -371,6 +391,144 @@ int prefill_attn_paged(const pskv_layout *layout, const void *q, const int32_t *
                        int32_t num_q_heads, int32_t window, float scale, int32_t num_splits,
                        void *workspace, size_t workspace_bytes, void *out, int32_t out_dtype,
                        const pskv_decode_opts *opts, pskv_stream_t stream);
+
+/* ---- the latent cache --------------------------------------------------------
+ *
+ * Latent attention keeps one latent vector c and one rotated key r a token
+ * instead of keys and values per head.  Head h's key is [U_h c, r] and its
+ * value W_h c for up-projections U_h, W_h.  In the absorbed form the query is
+ * taken through U_h^T once, q_h = [U_h^T qn_h, qr_h], so that the score of key i
+ * is scale * q_h . [c_i, r_i] and the output sum_i softmax_i c_i, taken through
+ * W_h afterwards by the caller (decode_attn_latent reads the cache alone).  In
+ * the expanded form keys and values are formed for every head first
+ * (prefill_attn_expanded): fewer operations for long chunks.  Both forms give
+ * the same attention. */
+
+/* Parameters of kv_prep_append_latent. */
+typedef struct pskv_latent_prep_desc {
+  float eps;              /* added to the mean square before the square root, >= 0 */
+  int32_t pairs;          /* PSKV_PAIRS_HALVES or PSKV_PAIRS_ADJACENT */
+  const float *w;         /* device float[head_dim_v], 16-byte aligned: the latent's norm
+                             multiplier, or NULL (1) */
+  const float *rope_cos;  /* device float[max_pos][PSKV_LATENT_ROT / 2], 16-byte aligned */
+  const float *rope_sin;  /* the same */
+  int32_t max_pos;        /* rows of the tables */
+  int32_t num_q_heads;    /* query heads to rotate, 0 = none */
+  const void *q;          /* device bf16, the queries' rotated columns: PSKV_LATENT_ROT of head h
+                             of token t at q + t * q_token + h * q_head (elements) */
+  int64_t q_token, q_head;
+  void *q_out;            /* where they go, same form (q_out = q with equal strides: in place) */
+  int64_t q_out_token, q_out_head;
+} pskv_latent_prep_desc;
+
+/* The prep and page write of a latent pool (kv_prep_append's place there).
+ * For each new token t (n of them) it takes the down-projection's row
+ *   x          device bf16, head_dim_v latent columns then PSKV_LATENT_ROT key columns at
+ *              x + t * x_token (elements); 16-byte aligned, x_token a multiple of 8
+ * and forms c' = c / sqrt(mean(c^2) + eps) * w and r', r turned by the angle of
+ * position p = first_pos[row_of[t]] + pos_of[t] (first_pos NULL: 0): for each
+ * pair (a, b), number i, with cos and sin = table row p, column i,
+ *   a' = a cos - b sin,  b' = b cos + a sin.
+ * [c', r'] goes into page slot pos_of[t] of table row row_of[t], and also to
+ * dense + t * head_dim_k (bf16, 16-byte aligned) unless dense is NULL (the
+ * up-projection's input and the rotated keys of prefill_attn_expanded).  The
+ * queries' rotated columns are turned by the same angle.  q, q_out: 16-byte
+ * aligned, strides multiples of 8.  Computed in f32, rounded once to nearest
+ * even bf16.  A row that is refused (its page, lease or position) writes
+ * nothing at all.  Checks, host copies and fault bits are those of
+ * kv_prep_append; (row, pos) pairs must be distinct within one call.
+ * Errors: INVALID_ARG, UNSUPPORTED (not a latent pool), PAST_PAGES, CUDA. */
+int kv_prep_append_latent(const pskv_layout *layout, const pskv_latent_prep_desc *prep,
+                          const void *x, int64_t x_token, int32_t n, const int32_t *row_of,
+                          const int32_t *pos_of, const int32_t *first_pos,
+                          const int32_t *page_tables, int32_t table_stride,
+                          const int32_t *pages_of_row, int32_t batch, const int32_t *row_of_host,
+                          const int32_t *pos_of_host, const int32_t *pages_of_row_host,
+                          void *dense, pskv_stream_t stream);
+
+/* Absorbed attention over a latent pool, num_tokens query tokens per row: the
+ * row's last num_tokens keys, causal inside the window, as for
+ * decode_attn_multirow (num_tokens = 1: single-token decode).  As there, except:
+ *   q            device bf16 [batch][num_tokens][num_q_heads][head_dim_k]
+ *   out          device [batch][num_tokens][num_q_heads][head_dim_v] of out_dtype
+ *   num_q_heads  1..PSKV_LATENT_MAX_HEADS (any number)
+ *   num_tokens   1..PSKV_MAX_WINDOW_TOKENS
+ *   seq_lens     each at least num_tokens, or 0: a row of a padded batch, whose
+ *                outputs are zeros (no fault bit)
+ *   workspace    decode_attn_latent_workspace_bytes(...) bytes, 16-byte aligned
+ *                (NULL is fine where that is 0)
+ * The softmax weights meet the values as bf16 when the output is bf16 (their
+ * rounding adds to the output about what its own rounding does), as a bf16
+ * pair when it is f32; scores, maxima, sums and outputs accumulate in f32.
+ * The result is run-to-run deterministic for a fixed split count.
+ * Errors: INVALID_ARG, UNSUPPORTED (not a latent pool, an appending option, more
+ * than 2^31 - 1 pool rows), WORKSPACE_TOO_SMALL, CUDA. */
+int decode_attn_latent(const pskv_layout *layout, const void *q, const int32_t *page_tables,
+                       int32_t table_stride, const int32_t *seq_lens_host,
+                       const int32_t *seq_lens, int32_t batch, int32_t num_tokens,
+                       int32_t num_q_heads, float scale, int32_t num_splits, void *workspace,
+                       size_t workspace_bytes, void *out, int32_t out_dtype,
+                       const pskv_decode_opts *opts, pskv_stream_t stream);
+
+/* The workspace a decode_attn_latent call needs under its plan (0 when one
+ * partition writes the output directly).  Nothing is enqueued. */
+int decode_attn_latent_workspace_bytes(const pskv_layout *layout, const int32_t *seq_lens_host,
+                                       int32_t table_stride, int32_t batch, int32_t num_tokens,
+                                       int32_t num_q_heads, int32_t num_splits, size_t *bytes);
+
+/* Expanded latent attention of variable-length chunks: row b's queries are
+ * rows [cu_q[b], cu_q[b+1]) of q, its keys rows [cu_k[b], cu_k[b+1]) of kv and
+ * k_rot; the queries are the row's last keys (as many keys as queries at
+ * least), each attending keys up to its own.
+ *   q       device bf16 [total_q][num_heads][PSKV_EXPANDED_NOPE + PSKV_LATENT_ROT]
+ *   kv      device bf16 [total_k][num_heads][PSKV_EXPANDED_NOPE + PSKV_EXPANDED_V]: the
+ *           up-projection's rows, a head's key columns then its value columns
+ *   k_rot   device bf16, the rotated keys (all heads share them): token j's
+ *           PSKV_LATENT_ROT columns at k_rot + j * k_rot_token (elements, a multiple of 8)
+ *   cu_q_host, cu_k_host  host int32[batch + 1]: 0, then non-decreasing
+ *   cu_q, cu_k            device int32[batch + 1]: the same, read by the kernel (rows
+ *                         outside the host totals are never addressed)
+ *   out     device [total_q][num_heads][PSKV_EXPANDED_V] of out_dtype
+ * All 16-byte aligned.  The score of query i and key j is scale * (qn_i . kn_j
+ * + qr_i . r_j).  The weights' precision is decode_attn_latent's.  A device
+ * offset that disagrees with the host copies raises PSKV_FAULT_BAD_LENGTH in
+ * status (device int32[4] or NULL), and that row is skipped.  No workspace.
+ * Errors: INVALID_ARG (also a row with more queries than keys), CUDA. */
+int prefill_attn_expanded(const void *q, const void *kv, const void *k_rot, int64_t k_rot_token,
+                          const int32_t *cu_q_host, const int32_t *cu_q, const int32_t *cu_k_host,
+                          const int32_t *cu_k, int32_t batch, int32_t num_heads, float scale,
+                          void *out, int32_t out_dtype, int32_t *status, pskv_stream_t stream);
+
+/* Verification of a drafted chain against the target's probabilities (what
+ * follows the verify windows of decode_attn_multirow and decode_attn_latent:
+ * speculative sampling, whose output has the target's distribution).  Row b has
+ * drafts x_0 .. x_{d-1}, d = num_drafts[b].  With p_t the target's distribution
+ * at draft t, q_t the draft's and u_t given uniform numbers, draft t stands
+ * while every earlier one stood and u_t * q_t(x_t) < p_t(x_t).  With a drafts
+ * standing, one more token comes from the weights
+ *   r(v) = max(p_a(v) - q_a(v), 0)  when a < d,   r = p_a  when a = d
+ * (when these are all 0: r = p_a): the lowest v with sum_{w <= v} r(w) >
+ * u_D * sum r, D = max_drafts.  Products and comparisons are exact and the sums
+ * are whole numbers of 2^-62, so the result does not depend on their order.
+ *   target_probs  device [batch][max_drafts + 1][vocab] of dtype (F32 or BF16)
+ *   draft_probs   device [batch][max_drafts][vocab] of dtype, or NULL: the draft
+ *                 has no distribution, q_t is 1 at x_t and 0 elsewhere
+ *   drafts        device int32[batch][max_drafts]
+ *   num_drafts    device int32[batch], 0..max_drafts each, or NULL (max_drafts)
+ *   u             device float[batch][max_drafts + 1], in [0, 1)
+ *   tokens        device int32[batch][max_drafts + 1]: the standing drafts, the drawn
+ *                 token, then -1
+ *   accepted      device int32[batch]: drafts standing
+ *   status        device int32[4] fault word or NULL
+ * max_drafts 0..PSKV_MAX_WINDOW_TOKENS (drafts may be NULL when 0).  Values outside [0, 1] count as the nearer end,
+ * NaN as 0.  A draft outside the vocabulary does not stand
+ * (PSKV_FAULT_BAD_TOKEN); a count outside its range is clamped
+ * (PSKV_FAULT_BAD_LENGTH); a row without any weight draws -1
+ * (PSKV_FAULT_EMPTY_ROW).  No workspace.  Errors: INVALID_ARG, CUDA. */
+int verify_drafts(const void *target_probs, const void *draft_probs, int32_t dtype,
+                  const int32_t *drafts, const int32_t *num_drafts, const float *u, int32_t batch,
+                  int32_t max_drafts, int32_t vocab, int32_t *tokens, int32_t *accepted,
+                  int32_t *status, pskv_stream_t stream);
 
 /* Merge P partials per row in two levels by the exact rescaling identity and
  * normalise (gem design, "Candidate ownership and storage"; pegainfer #1055,

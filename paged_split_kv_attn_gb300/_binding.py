@@ -27,6 +27,9 @@ PSKV_DTYPE_F32 = 0
 PSKV_DTYPE_BF16 = 1
 PSKV_FORMAT_SPLIT = 0
 PSKV_FORMAT_FOLDED = 1
+PSKV_FORMAT_LATENT = 2
+PSKV_PAIRS_HALVES = 0
+PSKV_PAIRS_ADJACENT = 1
 
 PSKV_FAULT_BAD_PAGE = 1
 PSKV_FAULT_PAST_PAGES = 2
@@ -36,18 +39,25 @@ PSKV_FAULT_EMPTY_ROW = 16
 PSKV_FAULT_BAD_STATE = 32
 PSKV_FAULT_BAD_POSITION = 64
 PSKV_FAULT_BAD_MASK = 128
+PSKV_FAULT_BAD_TOKEN = 256
 
 PSKV_MAX_SPLITS = 1024
 PSKV_AUTO_MAX_SPLITS = 256
 PSKV_MERGE_GROUP = 16
 PSKV_KEY_TILE = 16
 PSKV_MAX_WINDOW_TOKENS = 64
+PSKV_LATENT_ROT = 64
+PSKV_LATENT_MAX_HEADS = 128
+PSKV_EXPANDED_NOPE = 128
+PSKV_EXPANDED_V = 128
 PSKV_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 # Every function the header declares, in the header's order.
 EXPORTS = ("paged_kv_layout_create", "paged_kv_layout_destroy", "kv_append_rows", "kv_prep_append",
            "decode_attn_splitkv", "decode_attn_windowed", "decode_attn_multirow",
-           "decode_attn_tree", "prefill_attn_paged", "merge_partials",
+           "decode_attn_tree", "prefill_attn_paged", "kv_prep_append_latent", "decode_attn_latent",
+           "decode_attn_latent_workspace_bytes", "prefill_attn_expanded", "verify_drafts",
+           "merge_partials",
            "decode_attn_workspace_bytes", "merge_partials_workspace_bytes",
            "prefill_attn_workspace_bytes", "decode_attn_multirow_workspace_bytes",
            "pskv_partial_scratch_bytes", "pskv_plan_splits", "decode_attn_splitkv_static",
@@ -77,6 +87,15 @@ class PrepDesc(ctypes.Structure):
     _fields_ = [("rot_dims", ctypes.c_int32), ("eps", ctypes.c_float), ("w_q", ctypes.c_void_p),
                 ("w_k", ctypes.c_void_p), ("rope_cos", ctypes.c_void_p),
                 ("rope_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int32)]
+
+
+class LatentPrepDesc(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("pairs", ctypes.c_int32), ("w", ctypes.c_void_p),
+                ("rope_cos", ctypes.c_void_p), ("rope_sin", ctypes.c_void_p),
+                ("max_pos", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("q_out_token", ctypes.c_int64),
+                ("q_out_head", ctypes.c_int64)]
 
 
 class DecodeOpts(ctypes.Structure):
@@ -114,6 +133,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                      P, P]
     lib.prefill_attn_paged.argtypes = [P, P, P, P, P, I32, P, P, I32, I32, I32, F, I32, P, SZ, P,
                                        I32, P, P]
+    lib.kv_prep_append_latent.argtypes = [P, ctypes.POINTER(LatentPrepDesc), P, I64, I32, P, P, P,
+                                          P, I32, P, I32, P, P, P, P, P]
+    lib.decode_attn_latent.argtypes = [P, P, P, I32, P, P, I32, I32, I32, F, I32, P, SZ, P, I32, P,
+                                       P]
+    lib.decode_attn_latent_workspace_bytes.argtypes = [P, P, I32, I32, I32, I32, I32,
+                                                       ctypes.POINTER(SZ)]
+    lib.prefill_attn_expanded.argtypes = [P, P, P, I64, P, P, P, P, I32, I32, F, P, I32, P, P]
+    lib.verify_drafts.argtypes = [P, P, I32, P, P, P, I32, I32, I32, P, P, P, P]
     lib.merge_partials.argtypes = [P, P, P, I32, I32, I32, P, I32, P, SZ, P, P, P]
     lib.decode_attn_workspace_bytes.argtypes = [I32, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.merge_partials_workspace_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(SZ)]
@@ -161,8 +188,8 @@ def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
 
 def _host_i32(x, name: str):
     """Host int32 array (list, numpy array or CPU tensor) -> ctypes array kept alive by the caller."""
-    if x is None:
-        return None
+    if x is None or (isinstance(x, ctypes.Array) and x._type_ is ctypes.c_int32):
+        return x
     if isinstance(x, torch.Tensor):
         if x.is_cuda:
             raise TypeError(f"{name} must be host memory")
@@ -249,11 +276,23 @@ class Layout:
             pass
 
 
-def paged_kv_layout_create(k_pool: torch.Tensor, v_pool: torch.Tensor,
+def paged_kv_layout_create(k_pool: torch.Tensor, v_pool: torch.Tensor | None,
                            status: torch.Tensor | None = None, fmt: int | None = None) -> Layout:
     """Wrap pools shaped [num_pages, num_kv_heads, page_size, head_dim]; a K pool
-    narrower than the V pool is a folded pool unless ``fmt`` says otherwise."""
+    narrower than the V pool is a folded pool unless ``fmt`` says otherwise.
+    Without a V pool it is a latent pool: [num_pages, 1, page_size, latent + 64]."""
     lib = load_library()
+    if v_pool is None:
+        if k_pool.dim() != 4:
+            raise ValueError("a latent pool must be [num_pages, 1, page_size, latent + 64]")
+        desc = LayoutDesc(k_pool.shape[0], k_pool.shape[2], k_pool.shape[1], k_pool.shape[3],
+                          k_pool.shape[3] - PSKV_LATENT_ROT, _dtype_code(k_pool.dtype),
+                          PSKV_FORMAT_LATENT if fmt is None else fmt, _dev(k_pool, "k_pool"), None,
+                          None if status is None else _dev(status, "status", torch.int32))
+        handle = ctypes.c_void_p()
+        _check(lib.paged_kv_layout_create(ctypes.byref(desc), ctypes.byref(handle)),
+               "paged_kv_layout_create")
+        return Layout(handle, k_pool, None, status, desc)
     if k_pool.dim() != 4 or v_pool.dim() != 4 or k_pool.shape[:3] != v_pool.shape[:3]:
         raise ValueError("pools must be [num_pages, num_kv_heads, page_size, head_dim]")
     if fmt is None:
@@ -551,6 +590,206 @@ def prefill_attn_paged(layout: Layout, q, cu_q, cu_q_host, page_tables, seq_lens
         _dev(out, "out"), _dtype_code(out.dtype), None if opts is None else ctypes.byref(opts),
         _stream(stream)), "prefill_attn_paged")
     return out
+
+
+# ---- the latent cache and the drafts' verification --------------------------------
+
+def _here(name: str, *tensors) -> None:
+    """The tensors of one call lie on the current device, where its kernels run."""
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != current:
+            raise ValueError(f"{name}: a tensor on {t.device}, the current device is cuda:{current}")
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype=torch.bfloat16) -> int:
+    """A tensor of the given shape whose last dimension is contiguous (others may be strided)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr()
+
+
+def _shaped(t: torch.Tensor, name: str, shape, dtype) -> int:
+    """A contiguous CUDA tensor of the given shape and type."""
+    ptr = _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return ptr
+
+
+def kv_prep_append_latent(layout: Layout, x, row_of, pos_of, page_tables, pages_of_row, eps: float,
+                          w, rope_cos, rope_sin, pairs: str = "halves", first_pos=None, q=None,
+                          q_out=None, dense=None, host=None, stream=None) -> None:
+    """The prep and page write of a latent pool: ``x`` [n, latent + 64] holds the
+    down-projection's rows (rows may be strided); the normalised latent and the
+    rotated key of each go into its page slot, and to ``dense`` [n, latent + 64]
+    if given.  ``q`` and ``q_out`` [n, heads, 64] (strided views are fine, the same
+    tensor twice turns in place) are the queries' rotated columns.  ``pairs`` is
+    "halves" (i, i + 32) or "adjacent" (2i, 2i + 1).  ``host`` = (row_of, pos_of,
+    pages_of_row) host copies for the up-front refusal."""
+    lib = load_library()
+    n, d = int(row_of.numel()), layout.desc.head_dim_k
+    _here("kv_prep_append_latent", x, row_of, pos_of, page_tables, pages_of_row, w, rope_cos, rope_sin,
+          first_pos, q, q_out, dense, layout.k_pool)
+    if pairs not in ("halves", "adjacent"):
+        raise ValueError("pairs must be 'halves' or 'adjacent'")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    hr = hp = hl = None
+    if host is not None:
+        hr, hp, hl = (_host_i32(v, name) for v, name in zip(host, ("row_of", "pos_of", "pages")))
+        if len(hr) != n or len(hp) != n or len(hl) != pages_of_row.numel():
+            raise ValueError("host copies must be as long as the arrays they copy")
+    half = PSKV_LATENT_ROT // 2
+    if rope_cos.dim() != 2 or rope_cos.shape != rope_sin.shape or rope_cos.shape[1] != half:
+        raise ValueError(f"rope_cos and rope_sin must be [positions, {half}]")
+    desc = LatentPrepDesc(eps=eps, pairs=PSKV_PAIRS_ADJACENT if pairs == "adjacent" else
+                          PSKV_PAIRS_HALVES,
+                          w=None if w is None else _shaped(w, "w", (d - PSKV_LATENT_ROT,), torch.float32),
+                          rope_cos=_dev(rope_cos, "rope_cos", torch.float32),
+                          rope_sin=_dev(rope_sin, "rope_sin", torch.float32),
+                          max_pos=rope_cos.shape[0])
+    if q is not None and q.shape[1] > 0:
+        desc.num_q_heads = q.shape[1]
+        desc.q = _rows(q, "q", (n, q.shape[1], PSKV_LATENT_ROT))
+        desc.q_out = _rows(q_out, "q_out", (n, q.shape[1], PSKV_LATENT_ROT))
+        desc.q_token, desc.q_head = q.stride(0), q.stride(1)
+        desc.q_out_token, desc.q_out_head = q_out.stride(0), q_out.stride(1)
+        if n > 1 and desc.q_out_token < PSKV_LATENT_ROT or \
+                q.shape[1] > 1 and desc.q_out_head < PSKV_LATENT_ROT:
+            raise ValueError("q_out's rows must not overlap")
+    _check(lib.kv_prep_append_latent(
+        layout.handle, ctypes.byref(desc), _rows(x, "x", (n, d)), x.stride(0) if n > 1 else d, n,
+        _dev(row_of, "row_of", torch.int32), _shaped(pos_of, "pos_of", row_of.shape, torch.int32),
+        None if first_pos is None else _shaped(first_pos, "first_pos", pages_of_row.shape, torch.int32),
+        _dev(page_tables, "page_tables", torch.int32), page_tables.shape[1],
+        _shaped(pages_of_row, "pages_of_row", page_tables.shape[:1], torch.int32),
+        pages_of_row.numel(), hr, hp, hl,
+        None if dense is None else _shaped(dense, "dense", (n, d), torch.bfloat16),
+        _stream(stream)), "kv_prep_append_latent")
+
+
+def decode_attn_latent_workspace_bytes(layout: Layout, seq_lens_host, table_stride: int,
+                                       num_tokens: int, num_q_heads: int,
+                                       num_splits: int = 0) -> int:
+    """Workspace bytes a decode_attn_latent call needs under its plan."""
+    lens_h = _host_i32(seq_lens_host, "seq_lens_host")
+    out = ctypes.c_size_t()
+    _check(load_library().decode_attn_latent_workspace_bytes(
+        layout.handle, lens_h, table_stride, len(lens_h), num_tokens, num_q_heads, num_splits,
+        ctypes.byref(out)), "decode_attn_latent_workspace_bytes")
+    return int(out.value)
+
+
+def latent_workspace(layout: Layout, seq_lens_host, num_tokens: int, num_q_heads: int,
+                     table_stride: int | None = None, num_splits: int = 0):
+    """A scratch tensor for decode_attn_latent calls of these lengths (None: none needed)."""
+    lens_h = _host_i32(seq_lens_host, "seq_lens_host")
+    if table_stride is None:
+        table_stride = max(1, -(-max(lens_h) // layout.page_size))
+    n = decode_attn_latent_workspace_bytes(layout, lens_h, table_stride, num_tokens, num_q_heads,
+                                           num_splits)
+    return _planned_workspace(n, layout.k_pool.device)
+
+
+def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, scale,
+                       num_splits: int = 0, workspace=None, out=None, out_dtype=None,
+                       merge_group: int = 0, events=None, stream=None) -> torch.Tensor:
+    """Absorbed attention over a latent pool: ``q`` [batch, tokens, heads, latent +
+    64], token t of row b at key ``seq_lens[b] - tokens + t``.  Returns ``out``
+    [batch, tokens, heads, latent]; a row of length 0 gets zeros."""
+    lib = load_library()
+    if q.dim() != 4 or q.shape[3] != layout.desc.head_dim_k:
+        raise ValueError(f"q must be [batch, tokens, heads, {layout.desc.head_dim_k}]")
+    batch, tokens, hq = q.shape[0], q.shape[1], q.shape[2]
+    _here("decode_attn_latent", q, page_tables, seq_lens, workspace, out, layout.k_pool)
+    lens_h = _host_i32(seq_lens_host, "seq_lens_host")
+    if len(lens_h) != batch:
+        raise ValueError("seq_lens_host must have one entry per row")
+    shape = (batch, tokens, hq, layout.desc.head_dim_v)
+    if out is None:
+        out = torch.empty(shape, device=q.device, dtype=out_dtype or torch.bfloat16)
+    stride = page_tables.shape[1]
+    if workspace is None:
+        workspace = _planned_workspace(decode_attn_latent_workspace_bytes(
+            layout, lens_h, stride, tokens, hq, num_splits), q.device)
+    opts = _opts(merge_group, events)
+    _check(lib.decode_attn_latent(
+        layout.handle, _dev(q, "q", torch.bfloat16),
+        _shaped(page_tables, "page_tables", (batch, stride), torch.int32), stride, lens_h,
+        _shaped(seq_lens, "seq_lens", (batch,), torch.int32), batch, tokens, hq, float(scale),
+        num_splits, None if workspace is None else _dev(workspace, "workspace"),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _shaped(out, "out", shape, out.dtype), _dtype_code(out.dtype),
+        None if opts is None else ctypes.byref(opts), _stream(stream)), "decode_attn_latent")
+    return out
+
+
+def prefill_attn_expanded(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale, out=None,
+                          out_dtype=None, status=None, stream=None) -> torch.Tensor:
+    """Expanded latent attention of packed chunks: ``q`` [total_q, heads, 192], ``kv``
+    [total_k, heads, 256] (each head's keys then values), ``k_rot`` [total_k, 64] (rows
+    may be strided); row b's queries are the last of its keys.  Returns ``out``
+    [total_q, heads, 128]."""
+    lib = load_library()
+    if q.dim() != 3 or kv.dim() != 3:
+        raise ValueError("q and kv must be [tokens, heads, columns]")
+    _here("prefill_attn_expanded", q, kv, k_rot, cu_q, cu_k, out, status)
+    heads, cq, ck = q.shape[1], _host_i32(cu_q_host, "cu_q_host"), _host_i32(cu_k_host, "cu_k_host")
+    batch = len(cq) - 1
+    if batch < 1 or len(ck) != batch + 1:
+        raise ValueError("cu_q_host and cu_k_host must have batch + 1 entries each")
+    shape = (cq[batch], heads, PSKV_EXPANDED_V)
+    if out is None:
+        out = torch.empty(shape, device=q.device, dtype=out_dtype or torch.bfloat16)
+    _check(lib.prefill_attn_expanded(
+        _shaped(q, "q", (cq[batch], heads, PSKV_EXPANDED_NOPE + PSKV_LATENT_ROT), torch.bfloat16),
+        _shaped(kv, "kv", (ck[batch], heads, PSKV_EXPANDED_NOPE + PSKV_EXPANDED_V), torch.bfloat16),
+        _rows(k_rot, "k_rot", (ck[batch], PSKV_LATENT_ROT)),
+        k_rot.stride(0) if ck[batch] > 1 else PSKV_LATENT_ROT, cq,
+        _shaped(cu_q, "cu_q", (batch + 1,), torch.int32), ck,
+        _shaped(cu_k, "cu_k", (batch + 1,), torch.int32), batch, heads, float(scale),
+        _shaped(out, "out", shape, out.dtype), _dtype_code(out.dtype),
+        None if status is None else _dev(status, "status", torch.int32), _stream(stream)),
+        "prefill_attn_expanded")
+    return out
+
+
+def verify_drafts(target_probs, draft_probs, drafts, u, num_drafts=None, tokens=None,
+                  accepted=None, status=None, stream=None):
+    """Verify drafted tokens against the target's probabilities (speculative
+    sampling): ``target_probs`` [batch, drafts + 1, vocab] (f32 or bf16),
+    ``draft_probs`` [batch, drafts, vocab] or None (a draft without a
+    distribution), ``drafts`` int32 [batch, drafts], ``u`` f32 [batch, drafts + 1]
+    uniform numbers.  Returns (``tokens`` int32 [batch, drafts + 1]: standing
+    drafts, the drawn token, -1s; ``accepted`` int32 [batch])."""
+    lib = load_library()
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        raise ValueError("target_probs must be [batch, drafts + 1, vocab]")
+    batch, t, vocab = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
+    _here("verify_drafts", target_probs, draft_probs, drafts, u, num_drafts, tokens, accepted, status)
+    kind = target_probs.dtype
+    if tokens is None:
+        tokens = torch.empty((batch, t + 1), dtype=torch.int32, device=target_probs.device)
+    if accepted is None:
+        accepted = torch.empty(batch, dtype=torch.int32, device=target_probs.device)
+    _check(lib.verify_drafts(
+        _dev(target_probs, "target_probs"),
+        None if draft_probs is None else _shaped(draft_probs, "draft_probs", (batch, t, vocab), kind),
+        _dtype_code(kind), _shaped(drafts, "drafts", (batch, t), torch.int32),
+        None if num_drafts is None else _shaped(num_drafts, "num_drafts", (batch,), torch.int32),
+        _shaped(u, "u", (batch, t + 1), torch.float32), batch, t, vocab,
+        _shaped(tokens, "tokens", (batch, t + 1), torch.int32),
+        _shaped(accepted, "accepted", (batch,), torch.int32),
+        None if status is None else _dev(status, "status", torch.int32), _stream(stream)),
+        "verify_drafts")
+    return tokens, accepted
 
 
 def decode_attn_splitkv_static(layout: Layout, q, page_tables, seq_lens, seq_lens_host, scale,

@@ -11,6 +11,7 @@
 #include <new>
 
 #include "attn_tc.h"
+#include "latent.h"
 #include "pskv_internal.cuh"
 #include "pskv_plan.h"
 
@@ -157,6 +158,7 @@ int decode_common(const pskv_layout *layout, const void *q, const int32_t *page_
   if (out_dtype != PSKV_DTYPE_F32 && out_dtype != PSKV_DTYPE_BF16) return PSKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(workspace, 16) || !aligned(out, 16)) return PSKV_ERR_INVALID_ARG;
   const pskv_layout_desc &d = layout->d;
+  if (d.format == PSKV_FORMAT_LATENT) return PSKV_ERR_UNSUPPORTED;
   if (num_q_heads % d.num_kv_heads != 0) return PSKV_ERR_UNSUPPORTED;
   if (d.num_kv_heads > 65535) return PSKV_ERR_UNSUPPORTED;
   const int group = num_q_heads / d.num_kv_heads;
@@ -369,6 +371,106 @@ int decode_common(const pskv_layout *layout, const void *q, const int32_t *page_
   return PSKV_OK;
 }
 
+// decode_attn_latent's checks, plan and launches; with `plan_bytes` set only
+// the host-visible checks and the plan, as for decode_common.
+int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_tables,
+                  int32_t table_stride, const int32_t *seq_lens_host, const int32_t *seq_lens,
+                  int32_t batch, int32_t num_tokens, int32_t num_q_heads, float scale,
+                  int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
+                  int32_t out_dtype, const pskv_decode_opts *opts, pskv_stream_t stream,
+                  size_t *plan_bytes = nullptr) {
+  if (!layout || !seq_lens_host) return PSKV_ERR_INVALID_ARG;
+  if (!plan_bytes && (!q || !page_tables || !seq_lens || !out)) return PSKV_ERR_INVALID_ARG;
+  if (batch < 1 || batch > 65535 || table_stride < 1 || num_q_heads < 1 || num_tokens < 1 ||
+      num_tokens > PSKV_MAX_WINDOW_TOKENS || !std::isfinite(scale) || num_splits < 0 ||
+      num_splits > PSKV_MAX_SPLITS)
+    return PSKV_ERR_INVALID_ARG;
+  if (out_dtype != PSKV_DTYPE_F32 && out_dtype != PSKV_DTYPE_BF16) return PSKV_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(workspace, 16) || !aligned(out, 16)) return PSKV_ERR_INVALID_ARG;
+  const pskv_layout_desc &d = layout->d;
+  if (d.format != PSKV_FORMAT_LATENT || num_q_heads > PSKV_LATENT_MAX_HEADS)
+    return PSKV_ERR_UNSUPPORTED;
+  if (opts && opts->append_k) return PSKV_ERR_UNSUPPORTED;  // kv_prep_append_latent writes the rows
+  if (d.num_pages * d.page_size > INT32_MAX) return PSKV_ERR_UNSUPPORTED;  // tensor coordinates
+  const int64_t cap = (int64_t)table_stride * d.page_size;
+  if (cap > INT32_MAX) return PSKV_ERR_INVALID_ARG;
+  int64_t longest = 0;
+  for (int32_t b = 0; b < batch; ++b) {
+    const int64_t len = seq_lens_host[b];
+    if (len < 0 || len > cap || (len > 0 && len < num_tokens)) return PSKV_ERR_INVALID_ARG;
+    longest = len > longest ? len : longest;
+  }
+  const int64_t columns = (int64_t)num_tokens * num_q_heads, rows = (int64_t)batch * columns;
+  if (rows > INT32_MAX) return PSKV_ERR_INVALID_ARG;
+  int mgroup = 0, rc;
+  if ((rc = merge_group_of(opts, &mgroup))) return rc;
+  int P = num_splits;
+  if (P == 0) {
+    int n_sm = 0;
+    if ((rc = sm_count(&n_sm))) return rc;
+    P = plan_latent_splits(((columns + 127) / 128) * batch, n_sm / 2, (longest + 63) / 64);
+  }
+  const bool direct = P == 1;
+  WorkspacePlan w;
+  if ((rc = plan_workspace(rows, 1, d.head_dim_v, P, mgroup, &w))) return rc;
+  if (w.groups > kMaxGroups) return PSKV_ERR_INVALID_ARG;
+  if (plan_bytes) {
+    *plan_bytes = direct ? 0 : w.total;
+    return PSKV_OK;
+  }
+  if (!direct && (!workspace || workspace_bytes < w.total)) return PSKV_ERR_WORKSPACE_TOO_SMALL;
+  char *ws = static_cast<char *>(workspace);
+  LatentAttnArgs a;
+  a.q = q;
+  a.pool = d.k_pool;
+  a.page_tables = page_tables;
+  a.seq_lens = seq_lens;
+  a.status = d.status;
+  a.ws_m = direct ? nullptr : reinterpret_cast<float *>(ws + w.m_off);
+  a.ws_l = direct ? nullptr : reinterpret_cast<float *>(ws + w.l_off);
+  a.ws_o = direct ? nullptr : reinterpret_cast<float *>(ws + w.o_off);
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.direct = direct ? 1 : 0;
+  a.num_pages = d.num_pages;
+  a.table_stride = table_stride;
+  a.page_size = d.page_size;
+  a.batch = batch;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_splits = P;
+  a.scale_log2 = scale * kLog2e;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (opts && opts->partial_begin) {
+    e = cudaEventRecord(reinterpret_cast<cudaEvent_t>(opts->partial_begin), s);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  e = launch_attn_latent(a, d.head_dim_v, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  if (opts && opts->partial_end) {
+    e = cudaEventRecord(reinterpret_cast<cudaEvent_t>(opts->partial_end), s);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (direct) return PSKV_OK;
+  MergeArgs m;
+  m.m = a.ws_m;
+  m.l = a.ws_l;
+  m.o = a.ws_o;
+  m.rows = (int)rows;
+  m.count = P;
+  m.dv = d.head_dim_v;
+  m.group = mgroup;
+  m.out = out;
+  m.out_dtype = out_dtype;
+  m.status = nullptr;  // a padded batch's row (length 0) is no fault
+  int launched = 0;
+  e = launch_merge(m, s, &launched);
+  g_launches.fetch_add((uint64_t)launched, std::memory_order_relaxed);
+  return e == cudaSuccess ? PSKV_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -397,6 +499,7 @@ int kv_append_rows(const pskv_layout *layout, const void *k_new, const void *v_n
                    const int32_t *pos_of_host, const int32_t *pages_of_row_host,
                    pskv_stream_t stream) {
   if (!layout || n < 0 || batch < 1 || table_stride < 1) return PSKV_ERR_INVALID_ARG;
+  if (layout->d.format == PSKV_FORMAT_LATENT) return PSKV_ERR_UNSUPPORTED;
   if (n == 0) return PSKV_OK;
   if (!k_new || !v_new || !row_of || !pos_of || !page_tables || !pages_of_row)
     return PSKV_ERR_INVALID_ARG;
@@ -443,7 +546,7 @@ int kv_prep_append(const pskv_layout *layout, const pskv_prep_desc *prep, const 
   if (!layout || !prep || n < 0 || batch < 1 || table_stride < 1 || num_q_heads < 1)
     return PSKV_ERR_INVALID_ARG;
   const pskv_layout_desc &d = layout->d;
-  if (d.kv_dtype != PSKV_DTYPE_BF16) return PSKV_ERR_UNSUPPORTED;
+  if (d.kv_dtype != PSKV_DTYPE_BF16 || d.format == PSKV_FORMAT_LATENT) return PSKV_ERR_UNSUPPORTED;
   if (num_q_heads % d.num_kv_heads != 0) return PSKV_ERR_UNSUPPORTED;
   const int hd = d.head_dim_v, rot = prep->rot_dims;
   const bool folded = d.format == PSKV_FORMAT_FOLDED;
@@ -602,6 +705,173 @@ int decode_attn_multirow_workspace_bytes(const pskv_layout *layout, const int32_
                        nullptr, PSKV_DTYPE_BF16, nullptr, nullptr, bytes);
 }
 
+int kv_prep_append_latent(const pskv_layout *layout, const pskv_latent_prep_desc *prep,
+                          const void *x, int64_t x_token, int32_t n, const int32_t *row_of,
+                          const int32_t *pos_of, const int32_t *first_pos,
+                          const int32_t *page_tables, int32_t table_stride,
+                          const int32_t *pages_of_row, int32_t batch, const int32_t *row_of_host,
+                          const int32_t *pos_of_host, const int32_t *pages_of_row_host,
+                          void *dense, pskv_stream_t stream) {
+  if (!layout || !prep || n < 0 || batch < 1 || table_stride < 1) return PSKV_ERR_INVALID_ARG;
+  const pskv_layout_desc &d = layout->d;
+  if (d.format != PSKV_FORMAT_LATENT) return PSKV_ERR_UNSUPPORTED;
+  if (!(prep->eps >= 0.f) || !std::isfinite(prep->eps) || !prep->rope_cos || !prep->rope_sin ||
+      prep->max_pos < 1 || prep->num_q_heads < 0)
+    return PSKV_ERR_INVALID_ARG;
+  if (prep->pairs != PSKV_PAIRS_HALVES && prep->pairs != PSKV_PAIRS_ADJACENT)
+    return PSKV_ERR_INVALID_ARG;
+  if (x_token < d.head_dim_k || x_token % 8 != 0) return PSKV_ERR_INVALID_ARG;
+  if (prep->num_q_heads > 0 && (prep->q_token % 8 || prep->q_head % 8 || prep->q_out_token % 8 ||
+                                prep->q_out_head % 8))
+    return PSKV_ERR_INVALID_ARG;
+  if (n == 0) return PSKV_OK;
+  if (!x || !row_of || !pos_of || !page_tables || !pages_of_row) return PSKV_ERR_INVALID_ARG;
+  if (prep->num_q_heads > 0 && (!prep->q || !prep->q_out)) return PSKV_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(dense, 16) || !aligned(prep->w, 16) ||
+      !aligned(prep->rope_cos, 16) || !aligned(prep->rope_sin, 16) || !aligned(prep->q, 16) ||
+      !aligned(prep->q_out, 16))
+    return PSKV_ERR_INVALID_ARG;
+  const int hosts = (row_of_host != nullptr) + (pos_of_host != nullptr) +
+                    (pages_of_row_host != nullptr);
+  if (hosts != 0 && hosts != 3) return PSKV_ERR_INVALID_ARG;
+  if (hosts == 3) {
+    const int rc = check_append_host(layout, n, table_stride, batch, row_of_host, pos_of_host,
+                                     pages_of_row_host);
+    if (rc) return rc;
+  }
+  LatentPrepArgs a;
+  a.x = x;
+  a.x_token = x_token;
+  a.n = n;
+  a.dc = d.head_dim_v;
+  a.eps = prep->eps;
+  a.adjacent = prep->pairs == PSKV_PAIRS_ADJACENT;
+  a.w = prep->w;
+  a.rope_cos = prep->rope_cos;
+  a.rope_sin = prep->rope_sin;
+  a.max_pos = prep->max_pos;
+  a.num_q_heads = prep->num_q_heads;
+  a.q = prep->q;
+  a.q_token = prep->q_token;
+  a.q_head = prep->q_head;
+  a.q_out = prep->q_out;
+  a.q_out_token = prep->q_out_token;
+  a.q_out_head = prep->q_out_head;
+  a.row_of = row_of;
+  a.pos_of = pos_of;
+  a.first_pos = first_pos;
+  a.page_tables = page_tables;
+  a.table_stride = table_stride;
+  a.pages_of_row = pages_of_row;
+  a.batch = batch;
+  a.pool = d.k_pool;
+  a.num_pages = d.num_pages;
+  a.page_size = d.page_size;
+  a.dense = dense;
+  a.status = d.status;
+  const cudaError_t e = launch_latent_prep(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PSKV_OK;
+}
+
+int decode_attn_latent(const pskv_layout *layout, const void *q, const int32_t *page_tables,
+                       int32_t table_stride, const int32_t *seq_lens_host,
+                       const int32_t *seq_lens, int32_t batch, int32_t num_tokens,
+                       int32_t num_q_heads, float scale, int32_t num_splits, void *workspace,
+                       size_t workspace_bytes, void *out, int32_t out_dtype,
+                       const pskv_decode_opts *opts, pskv_stream_t stream) {
+  return decode_latent(layout, q, page_tables, table_stride, seq_lens_host, seq_lens, batch,
+                       num_tokens, num_q_heads, scale, num_splits, workspace, workspace_bytes, out,
+                       out_dtype, opts, stream);
+}
+
+int decode_attn_latent_workspace_bytes(const pskv_layout *layout, const int32_t *seq_lens_host,
+                                       int32_t table_stride, int32_t batch, int32_t num_tokens,
+                                       int32_t num_q_heads, int32_t num_splits, size_t *bytes) {
+  if (!bytes) return PSKV_ERR_INVALID_ARG;
+  return decode_latent(layout, nullptr, nullptr, table_stride, seq_lens_host, nullptr, batch,
+                       num_tokens, num_q_heads, 1.f, num_splits, nullptr, 0, nullptr,
+                       PSKV_DTYPE_BF16, nullptr, nullptr, bytes);
+}
+
+int prefill_attn_expanded(const void *q, const void *kv, const void *k_rot, int64_t k_rot_token,
+                          const int32_t *cu_q_host, const int32_t *cu_q, const int32_t *cu_k_host,
+                          const int32_t *cu_k, int32_t batch, int32_t num_heads, float scale,
+                          void *out, int32_t out_dtype, int32_t *status, pskv_stream_t stream) {
+  if (!cu_q_host || !cu_q || !cu_k_host || !cu_k) return PSKV_ERR_INVALID_ARG;
+  if (batch < 1 || batch > 65535 || num_heads < 1 || num_heads > 65535 || !std::isfinite(scale))
+    return PSKV_ERR_INVALID_ARG;
+  if (out_dtype != PSKV_DTYPE_F32 && out_dtype != PSKV_DTYPE_BF16) return PSKV_ERR_INVALID_ARG;
+  if (k_rot_token < PSKV_LATENT_ROT || k_rot_token % 8 != 0) return PSKV_ERR_INVALID_ARG;
+  if (cu_q_host[0] != 0 || cu_k_host[0] != 0) return PSKV_ERR_INVALID_ARG;
+  int64_t max_q = 0;
+  for (int32_t b = 0; b < batch; ++b) {
+    const int64_t nq = (int64_t)cu_q_host[b + 1] - cu_q_host[b];
+    const int64_t nk = (int64_t)cu_k_host[b + 1] - cu_k_host[b];
+    if (nq < 0 || nk < nq) return PSKV_ERR_INVALID_ARG;
+    max_q = nq > max_q ? nq : max_q;
+  }
+  if (max_q == 0) return PSKV_OK;  // no query
+  if (!q || !kv || !k_rot || !out) return PSKV_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(k_rot, 16) || !aligned(out, 16) ||
+      !aligned(status, 4))
+    return PSKV_ERR_INVALID_ARG;
+  ExpandedAttnArgs a;
+  a.q = q;
+  a.kv = kv;
+  a.k_rot = k_rot;
+  a.k_rot_token = k_rot_token;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.batch = batch;
+  a.num_heads = num_heads;
+  a.total_q = cu_q_host[batch];
+  a.total_k = cu_k_host[batch];
+  a.max_q = (int)max_q;
+  a.scale_log2 = scale * kLog2e;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.status = status;
+  const cudaError_t e = launch_attn_expanded(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PSKV_OK;
+}
+
+int verify_drafts(const void *target_probs, const void *draft_probs, int32_t dtype,
+                  const int32_t *drafts, const int32_t *num_drafts, const float *u, int32_t batch,
+                  int32_t max_drafts, int32_t vocab, int32_t *tokens, int32_t *accepted,
+                  int32_t *status, pskv_stream_t stream) {
+  if (!target_probs || !u || !tokens || !accepted || batch < 1 || batch > (1 << 20) ||
+      max_drafts < 0 || max_drafts > PSKV_MAX_WINDOW_TOKENS || vocab < 1 || vocab > (1 << 30))
+    return PSKV_ERR_INVALID_ARG;
+  if (max_drafts > 0 && !drafts) return PSKV_ERR_INVALID_ARG;
+  if (dtype != PSKV_DTYPE_F32 && dtype != PSKV_DTYPE_BF16) return PSKV_ERR_INVALID_ARG;
+  const uintptr_t size = dtype == PSKV_DTYPE_BF16 ? 2 : 4;
+  if (!aligned(target_probs, size) || !aligned(draft_probs, size) || !aligned(drafts, 4) ||
+      !aligned(num_drafts, 4) || !aligned(u, 4) || !aligned(tokens, 4) || !aligned(accepted, 4) ||
+      !aligned(status, 4))
+    return PSKV_ERR_INVALID_ARG;
+  VerifyArgs a;
+  a.target = target_probs;
+  a.draft = max_drafts > 0 ? draft_probs : nullptr;
+  a.dtype = dtype;
+  a.drafts = drafts;
+  a.num_drafts = num_drafts;
+  a.u = u;
+  a.batch = batch;
+  a.max_drafts = max_drafts;
+  a.vocab = vocab;
+  a.tokens = tokens;
+  a.accepted = accepted;
+  a.status = status;
+  const cudaError_t e = launch_verify_drafts(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PSKV_OK;
+}
+
 int merge_partials(const float *m, const float *l, const float *o, int32_t rows,
                    int32_t num_splits, int32_t head_dim_v, void *out, int32_t out_dtype,
                    void *workspace, size_t workspace_bytes, int32_t *status,
@@ -691,6 +961,7 @@ int pskv_plan_splits(const pskv_layout *layout, int32_t batch, int32_t num_q_hea
                      const int32_t *seq_lens_host, int32_t *num_splits) {
   if (!layout || !seq_lens_host || !num_splits || batch < 1 || num_q_heads < 1)
     return PSKV_ERR_INVALID_ARG;
+  if (layout->d.format == PSKV_FORMAT_LATENT) return PSKV_ERR_UNSUPPORTED;
   if (num_q_heads % layout->d.num_kv_heads != 0) return PSKV_ERR_UNSUPPORTED;
   const int group = num_q_heads / layout->d.num_kv_heads;
   // single-token decode: one column per query head of the KV group
@@ -718,7 +989,7 @@ const char *pskv_last_cuda_error(void) { return g_cuda_error; }
 
 uint64_t pskv_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 
-int pskv_version(void) { return 102; }
+int pskv_version(void) { return 103; }
 
 int pskv_check_flags(const pskv_layout *layout, int32_t clear, pskv_stream_t stream,
                      uint32_t *flags) {

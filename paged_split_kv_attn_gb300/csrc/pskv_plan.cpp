@@ -8,17 +8,23 @@ namespace pskv {
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_layout_desc(const pskv_layout_desc *d) {
-  if (!d || !d->k_pool || !d->v_pool) return PSKV_ERR_INVALID_ARG;
+  if (!d || !d->k_pool) return PSKV_ERR_INVALID_ARG;
+  const bool latent = d->format == PSKV_FORMAT_LATENT;
+  if (latent != (d->v_pool == nullptr)) return PSKV_ERR_INVALID_ARG;
   if (d->num_pages < 1 || d->page_size < 1 || d->num_kv_heads < 1 || d->head_dim_k < 1 ||
       d->head_dim_v < 1)
     return PSKV_ERR_INVALID_ARG;
   if (d->page_size % PSKV_KEY_TILE != 0) return PSKV_ERR_INVALID_ARG;
   if (d->kv_dtype != PSKV_DTYPE_F32 && d->kv_dtype != PSKV_DTYPE_BF16) return PSKV_ERR_INVALID_ARG;
-  if (d->format != PSKV_FORMAT_SPLIT && d->format != PSKV_FORMAT_FOLDED) return PSKV_ERR_INVALID_ARG;
+  if (d->format != PSKV_FORMAT_SPLIT && d->format != PSKV_FORMAT_FOLDED && !latent)
+    return PSKV_ERR_INVALID_ARG;
   if (d->head_dim_v != 256 && d->head_dim_v != 512) return PSKV_ERR_UNSUPPORTED;
   if (d->format == PSKV_FORMAT_SPLIT && d->head_dim_k != d->head_dim_v) return PSKV_ERR_UNSUPPORTED;
   if (d->format == PSKV_FORMAT_FOLDED &&
       (d->head_dim_k * 4 != d->head_dim_v || d->kv_dtype != PSKV_DTYPE_BF16))
+    return PSKV_ERR_UNSUPPORTED;
+  if (latent && (d->head_dim_k != d->head_dim_v + PSKV_LATENT_ROT || d->num_kv_heads != 1 ||
+                 d->kv_dtype != PSKV_DTYPE_BF16))
     return PSKV_ERR_UNSUPPORTED;
   if (!aligned16(d->k_pool) || !aligned16(d->v_pool)) return PSKV_ERR_INVALID_ARG;
   if (d->status && (reinterpret_cast<uintptr_t>(d->status) & 3u)) return PSKV_ERR_INVALID_ARG;
@@ -26,7 +32,7 @@ int check_layout_desc(const pskv_layout_desc *d) {
   size_t rows, elems;
   if (__builtin_mul_overflow((size_t)d->num_pages, (size_t)d->num_kv_heads, &rows) ||
       __builtin_mul_overflow(rows, (size_t)d->page_size, &rows) ||
-      __builtin_mul_overflow(rows, (size_t)d->head_dim_v * 4, &elems))
+      __builtin_mul_overflow(rows, (size_t)(latent ? d->head_dim_k : d->head_dim_v) * 4, &elems))
     return PSKV_ERR_OVERFLOW;
   if (d->num_pages > 0x7fffffffLL) return PSKV_ERR_UNSUPPORTED;  // page ids are int32
   return PSKV_OK;
@@ -106,6 +112,7 @@ int check_append_host(const pskv_layout *layout, int32_t n, int32_t table_stride
 }
 
 int pick_kernel(int kv_dtype, int head_dim, int group, int format) {
+  if (format == PSKV_FORMAT_LATENT) return -1;  // served by decode_attn_latent alone
   const bool mma_group = group == 1 || group == 2 || group == 4 || group == 8;
   if (kv_dtype == PSKV_DTYPE_BF16 && mma_group && (head_dim == 256 || head_dim == 512))
     return kKernelMma;
@@ -131,6 +138,13 @@ int plan_verify_splits(int64_t units, int slots, int64_t max_tiles) {
   const int64_t cap = max_tiles / 2 < PSKV_MAX_SPLITS ? max_tiles / 2 : PSKV_MAX_SPLITS;
   if (p > cap) p = cap;
   return p < 1 ? 1 : (int)p;
+}
+
+int plan_latent_splits(int64_t units, int clusters, int64_t max_tiles) {
+  if (units < 1 || clusters < 1 || units >= clusters) return 1;
+  const int64_t p = clusters / units;
+  const int64_t cap = max_tiles / 2 < PSKV_AUTO_MAX_SPLITS ? max_tiles / 2 : PSKV_AUTO_MAX_SPLITS;
+  return (int)(p < cap ? p : (cap < 1 ? 1 : cap));
 }
 
 }  // namespace pskv

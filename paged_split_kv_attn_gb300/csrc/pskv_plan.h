@@ -58,6 +58,10 @@ int plan_tc_splits(int64_t units, int slots, int64_t max_tiles);
 // max_tiles 128-key tiles.  One wave: P = floor(slots / units), at least 1,
 // at most max_tiles / 2 (two tiles per partition) and PSKV_MAX_SPLITS.
 int plan_verify_splits(int64_t units, int slots, int64_t max_tiles);
+// Partitions per (row, block of query columns) for decode_attn_latent: `units`
+// blocks over `clusters` concurrent workers, rows of at most max_tiles 64-key
+// tiles; one wave, at least two tiles a partition.
+int plan_latent_splits(int64_t units, int clusters, int64_t max_tiles);
 int plan_splits(int slots, int32_t batch, int32_t num_kv_heads, const int32_t *seq_lens_host,
                 int fill32 = 32);
 

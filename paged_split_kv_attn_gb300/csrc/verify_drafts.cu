@@ -1,0 +1,279 @@
+// verify_drafts.cu -- speculative sampling's verification of a drafted chain.
+//
+// A draft x_t stands while u_t q_t(x_t) < p_t(x_t); behind the standing ones a
+// token is drawn from r = max(p - q, 0) (or from p when all stood) by inverting
+// the running sum of r at u S, S = sum r.  Only the rows p and q of that one
+// place are read whole, once: the call is bound by those bytes, or for a few rows
+// by its chain of loads.
+//
+// The draw has to be the same however the sum is split, so the weights are whole
+// numbers: a probability in [0, 1] is m 2^e with a 24-bit m, taken as a multiple of
+// 2^-62 (exact from 2^-38 up, cut below: at most vocab * 2^-62 in all), and
+// sums are 128-bit integers, whose order does not matter.  u is a 24-bit integer
+// times a power of two, so floor(u S) is exact as well.
+//
+// One cluster of eight CTAs takes a row: warp W of its 64 sums the W-th piece of the
+// vocabulary and writes its sum into every CTA's shared memory (distributed shared
+// memory); after one cluster barrier every warp knows all 64 sums and with them
+// the piece that holds the drawn token, whose CTA goes over it once more (from L2).
+// No workspace, no second launch, no atomics but fault bits.
+#include "latent.h"
+#include "pskv_internal.cuh"
+
+namespace pskv {
+
+namespace {
+
+using u128 = unsigned __int128;
+
+constexpr int kCluster = 8;
+constexpr int kWarps = 8;
+constexpr int kPieces = kCluster * kWarps;
+
+// A probability as a multiple of 2^-62: NaN and below 0 as 0, above 1 as 1.
+__device__ __forceinline__ uint64_t fixed_point(float p) {
+  if (!(p > 0.f)) return 0;
+  if (p >= 1.f) return 1ull << 62;
+  const uint32_t bits = __float_as_uint(p), e = bits >> 23;
+  const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+  const int shift = (int)(e ? e : 1) - 88;  // m * 2^(e - 150) * 2^62
+  return shift >= 0 ? m << shift : (shift > -32 ? m >> -shift : 0);
+}
+
+// The row being drawn from.
+template <typename T>
+struct Weights {
+  const T *p, *q;  // q null: nothing taken off but 1 at `point` (-1: nothing)
+  int point;
+
+  __device__ static float value(T x) {
+    if constexpr (sizeof(T) == 2)
+      return __uint_as_float((uint32_t)x << 16);
+    else
+      return x;
+  }
+  __device__ uint64_t at(int v, T pv, T qv) const {
+    const uint64_t a = fixed_point(value(pv));
+    const uint64_t b = q ? fixed_point(value(qv)) : (v == point ? 1ull << 62 : 0);
+    return a > b ? a - b : 0;
+  }
+  __device__ uint64_t at(int v) const { return at(v, p[v], q ? q[v] : T(0)); }
+};
+
+__device__ __forceinline__ u128 shfl_xor_128(u128 x, int m) {
+  const uint64_t lo = __shfl_xor_sync(0xffffffffu, (unsigned long long)x, m);
+  const uint64_t hi = __shfl_xor_sync(0xffffffffu, (unsigned long long)(x >> 64), m);
+  return ((u128)hi << 64) | lo;
+}
+__device__ __forceinline__ u128 shfl_up_128(u128 x, int d) {
+  const uint64_t lo = __shfl_up_sync(0xffffffffu, (unsigned long long)x, d);
+  const uint64_t hi = __shfl_up_sync(0xffffffffu, (unsigned long long)(x >> 64), d);
+  return ((u128)hi << 64) | lo;
+}
+__device__ __forceinline__ u128 shfl_128(u128 x, int l) {
+  const uint64_t lo = __shfl_sync(0xffffffffu, (unsigned long long)x, l);
+  const uint64_t hi = __shfl_sync(0xffffffffu, (unsigned long long)(x >> 64), l);
+  return ((u128)hi << 64) | lo;
+}
+__device__ __forceinline__ u128 warp_sum(u128 x) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) x += shfl_xor_128(x, m);
+  return x;
+}
+__device__ __forceinline__ u128 warp_scan(u128 x, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const u128 y = shfl_up_128(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// floor(u * sum), below sum: u in [0, 1) exactly, anything else the nearer end.
+__device__ __forceinline__ u128 threshold(float u, u128 sum) {
+  if (!(u > 0.f)) return 0;
+  if (u >= 1.f) return sum - 1;
+  const uint32_t bits = __float_as_uint(u), e = bits >> 23;
+  const uint32_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+  const int shift = 150 - (int)(e ? e : 1);
+  return shift >= 128 ? (u128)0 : (sum * m) >> shift;
+}
+
+// The sum over [lo, hi), 16 bytes a lane and step where both rows are aligned.
+template <typename T, bool kVec>
+__device__ __forceinline__ u128 sum_range(const Weights<T> &w, int lo, int hi, int lane) {
+  constexpr int kN = 16 / sizeof(T);
+  u128 sum = 0;
+  if constexpr (kVec) {
+#pragma unroll 4
+    for (int v = lo + kN * lane; v < hi; v += 32 * kN) {
+      T pv[kN], qv[kN];
+      *reinterpret_cast<uint4 *>(pv) = __ldg(reinterpret_cast<const uint4 *>(w.p + v));
+      if (w.q) *reinterpret_cast<uint4 *>(qv) = __ldg(reinterpret_cast<const uint4 *>(w.q + v));
+#pragma unroll
+      for (int e = 0; e < kN; ++e) sum += w.at(v + e, pv[e], w.q ? qv[e] : T(0));
+    }
+  } else {
+#pragma unroll 8
+    for (int v = lo + lane; v < hi; v += 32) sum += w.at(v);
+  }
+  return warp_sum(sum);
+}
+
+__device__ __forceinline__ uint32_t rank_in_cluster() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void store_remote(uint64_t *p, uint32_t rank, u128 x) {
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.v2.u64 [a], {%2, %3};\n\t}" ::"r"(smem_u32(p)),
+      "r"(rank), "l"((uint64_t)x), "l"((uint64_t)(x >> 64))
+      : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+}  // namespace
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kWarps * 32) __cluster_dims__(kCluster, 1, 1)
+    pskv_verify_drafts(const VerifyArgs a) {
+  __shared__ __align__(16) uint64_t piece_sum[2][kPieces][2];  // (low, high) of each piece; second try
+  __shared__ __align__(16) uint64_t part_sum[kWarps][2];
+  const int b = blockIdx.x / kCluster, rank = (int)rank_in_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T_ = a.max_drafts, V = a.vocab;
+  pdl_wait();
+  pdl_launch_dependents();
+  // ---- which drafts stand (every warp for itself)
+  int d = a.num_drafts ? a.num_drafts[b] : T_;
+  const bool bad_count = d < 0 || d > T_;
+  d = min(max(d, 0), T_);
+  const T *target = static_cast<const T *>(a.target) + (size_t)b * (T_ + 1) * V;
+  const T *draft = a.draft ? static_cast<const T *>(a.draft) + (size_t)b * T_ * V : nullptr;
+  const int32_t *drafts = a.drafts + (size_t)b * T_;
+  const float *u = a.u + (size_t)b * (T_ + 1);
+  int taken = 0;
+  bool bad_token = false;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int t = lane + 32 * half;
+    bool stands = false;
+    if (t < d) {
+      const int x = drafts[t];
+      if (x >= 0 && x < V) {
+        // f32 products in f64 and fixed-point comparisons of values in [0, 1] are exact; the
+        // clamping is the one of the weights
+        const float p = Weights<T>::value(target[(size_t)t * V + x]);
+        const float q = draft ? Weights<T>::value(draft[(size_t)t * V + x]) : 1.f;
+        const float ut = u[t];
+        const double uc = !(ut > 0.f) ? 0.0 : (ut >= 1.f ? 1.0 : (double)ut);
+        const double qc = !(q > 0.f) ? 0.0 : (q >= 1.f ? 1.0 : (double)q);
+        const double pc = !(p > 0.f) ? 0.0 : (p >= 1.f ? 1.0 : (double)p);
+        stands = uc * qc < pc;
+      } else {
+        bad_token = true;
+      }
+    }
+    const uint32_t yes = __ballot_sync(0xffffffffu, stands);
+    if (taken == 32 * half) taken += __ffs(~yes) ? __ffs(~yes) - 1 : 32;
+  }
+  Weights<T> w;
+  w.p = target + (size_t)taken * V;
+  w.q = taken < d && draft ? draft + (size_t)taken * V : nullptr;
+  w.point = taken < d && !draft ? drafts[taken] : -1;
+  const bool less = taken < d;  // something is taken off
+  // ---- the pieces' sums
+  const int seg = ((V + kPieces - 1) / kPieces + 7) & ~7;
+  const int W = rank * kWarps + warp;
+  u128 before = 0, total = 0;
+  int tries = 0;
+  for (;; ++tries) {
+    const int lo = (int)min((long long)W * seg, (long long)V);
+    const int hi = (int)min((long long)(W + 1) * seg, (long long)V);
+    const u128 own = sum_range<T, kVec>(w, lo, hi, lane);
+    if (lane < kCluster) store_remote(piece_sum[tries][W], lane, own);
+    cluster_barrier();
+    const uint64_t(*ps)[2] = piece_sum[tries];
+    const u128 s0 = ((u128)ps[2 * lane][1] << 64) | ps[2 * lane][0];
+    const u128 s1 = ((u128)ps[2 * lane + 1][1] << 64) | ps[2 * lane + 1][0];
+    const u128 incl = warp_scan(s0 + s1, lane);
+    total = shfl_128(incl, 31);
+    if (total != 0) {
+      // the piece where the running sum first passes the threshold
+      const u128 thr = threshold(u[T_], total);
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > thr);
+      const int l = __ffs(past) - 1;  // some lane: thr < total
+      const u128 base = shfl_128(incl - s0 - s1, l), first = shfl_128(s0, l);
+      const bool second = thr >= base + first;
+      const int hit = 2 * l + (second ? 1 : 0);
+      before = thr - (second ? base + first : base);  // what is left to pass inside the piece
+      if (hit / kWarps != rank) return;
+
+      // ---- the CTA that holds it: an eighth of the piece a warp
+      const int p0 = hit * seg, p1 = (int)min((long long)p0 + seg, (long long)V);
+      const int sub = ((p1 - p0 + kWarps - 1) / kWarps + 7) & ~7;
+      const int s_lo = min(p0 + warp * sub, p1), s_hi = min(s_lo + sub, p1);
+      const u128 mine = sum_range<T, kVec>(w, s_lo, s_hi, lane);
+      if (lane == 0) {
+        part_sum[warp][0] = (uint64_t)mine;
+        part_sum[warp][1] = (uint64_t)(mine >> 64);
+      }
+      __syncthreads();
+      u128 at = 0;
+      for (int k = 0; k < warp; ++k) at += ((u128)part_sum[k][1] << 64) | part_sum[k][0];
+      if (before < at || before >= at + mine) return;
+      u128 rest = before - at;
+      int token = -1;
+      for (int v0 = s_lo; v0 < s_hi; v0 += 32) {
+        const int v = v0 + lane;
+        const u128 x = warp_scan(v < s_hi ? (u128)w.at(v) : (u128)0, lane);
+        const uint32_t over = __ballot_sync(0xffffffffu, x > rest);
+        if (over) {
+          token = v0 + __ffs(over) - 1;
+          break;
+        }
+        rest -= shfl_128(x, 31);
+      }
+      for (int t = lane; t <= T_; t += 32)
+        a.tokens[(size_t)b * (T_ + 1) + t] = t < taken ? drafts[t] : (t == taken ? token : -1);
+      if (lane == 0) {
+        a.accepted[b] = taken;
+        if (bad_count) raise_fault(a.status, PSKV_FAULT_BAD_LENGTH);
+      }
+      if (bad_token) raise_fault(a.status, PSKV_FAULT_BAD_TOKEN);
+      return;
+    }
+    if (tries == 1 || !less) break;
+    w.q = nullptr;  // nothing is left of p: the draw is from p itself
+    w.point = -1;
+  }
+  // ---- no weight at all
+  if (W != 0) return;
+  for (int t = lane; t <= T_; t += 32)
+    a.tokens[(size_t)b * (T_ + 1) + t] = t < taken ? drafts[t] : -1;
+  if (lane == 0) {
+    a.accepted[b] = taken;
+    raise_fault(a.status, PSKV_FAULT_EMPTY_ROW | (bad_count ? PSKV_FAULT_BAD_LENGTH : 0u));
+  }
+  if (bad_token) raise_fault(a.status, PSKV_FAULT_BAD_TOKEN);
+}
+
+cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
+  const dim3 grid((unsigned)a.batch * kCluster), block(kWarps * 32);
+  const int size = a.dtype == PSKV_DTYPE_BF16 ? 2 : 4;
+  // 16-byte loads need every row on a 16-byte boundary
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15u) == 0 &&
+                   (long long)a.vocab * size % 16 == 0;
+  if (size == 2)
+    return vec ? launch_pdl(pskv_verify_drafts<uint16_t, true>, grid, block, 0, s, a)
+               : launch_pdl(pskv_verify_drafts<uint16_t, false>, grid, block, 0, s, a);
+  return vec ? launch_pdl(pskv_verify_drafts<float, true>, grid, block, 0, s, a)
+             : launch_pdl(pskv_verify_drafts<float, false>, grid, block, 0, s, a);
+}
+
+}  // namespace pskv
