@@ -5,23 +5,36 @@
 // heads share the rows, so a block of 128 query columns meets each cached row once:
 // per key 2 * 128 * (2 dc + 64) operations against 2 (dc + 64) bytes.
 //
-// A cluster of two CTAs takes 128 columns of one row and a partition of its keys,
-// as one tcgen05 product of M = 128 over the pair (cta_group::2): CTA r holds
-// columns 64 r .. + 63 of Q (dc + 64 wide) in shared memory, and of O (64 x dc
-// in f32: 256 tensor-memory columns, half of the lanes holding half of the
-// columns each), which one CTA alone could not hold beside the scores (128 x 512 f32
-// fill its tensor memory).  Per tile j of 64 keys:
-//   S = Q K^T     N = 64 keys, CTA r brings the tile's keys 32 r .. + 31
-//   softmax       thread (row i, half of the keys) masks its 32 scores; the two threads
-//                 of a row exchange their maxima; the reference maximum moves only
-//                 past a slack of 8 (log2 units), so O is rarely rescaled; P goes
+// A cluster of two CTAs takes 128 columns of one row and a piece of its keys, as one
+// tcgen05 product of M = 128 over the pair (cta_group::2): CTA r holds columns
+// 64 r .. + 63 of Q (dc + 64 wide) in shared memory, and of O (64 x dc in f32: 256
+// tensor-memory columns, half of the lanes holding half of the columns each),
+// which one CTA alone could not hold beside the scores (128 x 512 f32 fill its tensor
+// memory).  Per tile j of 128 keys:
+//   S = Q K^T     N = 128 keys, CTA r brings the tile's keys 64 r .. + 63
+//   softmax       thread (row i, half kh of the keys) masks its 64 scores; the two
+//                 threads of a row exchange their maxima; the reference maximum moves
+//                 only past a slack of 8 (log2 units), so O is rarely rescaled; P goes
 //                 to shared memory as bf16 (f32 output: a hi + lo pair)
-//   O += P V      per 256 columns: CTA r brings columns 128 r .. + 127 of each, all 64 keys
+//   O += P V      per half of the keys and 256 columns: CTA r brings columns
+//                 128 r .. + 127 of them, 64 keys
+// A product of M = 128 over a pair runs at the full rate of both SMs from N = 128 on
+// (measured: 32 cycles per K = 16 step at N = 128 and 64 at N = 256; 25 instead of 16
+// at N = 64, where reading the operands binds; M = 64 on one CTA runs at half rate).
 // The two products want a row in different CTAs (scores: by key, values: by column),
 // so a CTA copies both shares: 1.9x of a row's bytes from L2, each byte once from
-// HBM (the copies of the scores' share run ahead by a prefetch into L2).  Each of
-// the rings has its own copy warp and its own issuing warp in the even CTA, so
-// S(j + 1) runs while the softmax works on tile j.
+// HBM (a warp prefetches the scores' share into L2 some tiles ahead).  K moves in
+// chunks of a few 64-column slabs and V in chunks of 64 keys, through
+// rings of their own with their own copy warps and issuing warps, so a chunk's place
+// is refilled as soon as its products are done and S(j + 1) runs while the softmax works
+// on tile j.
+//
+// A row's keys are cut into pieces of `tiles_per_piece` tiles, one piece per cluster
+// (pskv_plan.cpp picks the size that fills the clusters in one wave); a row of one
+// piece is written at once, longer ones leave f32 partials (m, l, O) that
+// pskv_merge_latent folds in index order.  O leaves through the drained rings, so that
+// whole rows go out as bulk copies (16-byte stores straight from the
+// registers took 7.8 us for 64 KB a warp at 40,002 keys).
 //
 // P is rounded to bf16 when the output is (the weights' rounding then adds about
 // what the output's own does; the sum takes the rounded weights, so a lone key gives
@@ -34,6 +47,7 @@
 
 #include "latent.h"
 #include "pskv_internal.cuh"
+#include "pskv_plan.h"
 #include "tc_common.cuh"
 #include "tc_ops.cuh"
 #include "tc_pair.cuh"
@@ -46,266 +60,356 @@ using tc::elect_one;
 using tc::ex2;
 using tc::PageCache;
 
-constexpr int kKeys = 64;        // keys per tile
-constexpr int kHalfKeys = 32;    // of which each CTA brings half to the scores
-constexpr int kRows = 64;        // query columns per CTA (128 per pair)
-constexpr int kThreads = 256;    // warps: 0 S, 1 K copies, 2-5 softmax, 6 V copies, 7 PV
+constexpr int kKeys = kLatentTile;  // keys per tile (128)
+constexpr int kHalf = kKeys / 2;   // of which each CTA brings half to the scores
+constexpr int kRows = 64;          // query columns per CTA (128 per pair)
+constexpr int kThreads = 288;      // warps: 0 S, 1 K copies, 2-5 softmax, 6 V copies, 7 PV, 8 prefetch
 constexpr int kTmemCols = 512;
-constexpr int kOCol = 0;         // O: DC / 2 columns
-constexpr int kSCol = 256;       // score region r at kSCol + 32 r
+constexpr int kOCol = 0;           // O: DC / 2 columns
+constexpr int kSCol = 256;         // score region r at kSCol + 64 r
 constexpr float kSlack = 8.f;
-constexpr int kInfo = 8;         // tile records in flight: K runs kStages ahead of S, S two ahead of the softmax
-constexpr int kAhead = 4;        // tiles the L2 prefetch runs ahead of the copies
+constexpr int kInfo = 8;           // tile records in flight: K runs at most 2 tiles ahead of S, S 2 ahead of the softmax
+constexpr int kAhead = 4;          // tiles the L2 prefetch runs ahead of the scores
+constexpr int kSlab = kHalf * 128;  // 64 rows (of Q, K, V or P) of 64 columns: 8 KB
 
 template <int DC, bool kLo>
 struct Lay {
   static constexpr int kSlabs = DC / 64 + 1;             // 64-column slabs of a row
-  static constexpr int kQSlab = kRows * 128;             // 8 KB
-  static constexpr int kKSlab = kHalfKeys * 128;         // 4 KB
-  static constexpr int kVSlab = kKeys * 128;             // 8 KB
-  static constexpr int kBlocks = DC / 256;               // value products per tile
-  static constexpr int kVSlabs = 2 * kBlocks;            // this CTA's value slabs
-  static constexpr int kQBytes = kSlabs * kQSlab;
-  static constexpr int kKBytes = kSlabs * kKSlab;
-  static constexpr int kVBytes = kVSlabs * kVSlab;
-  static constexpr int kPBytes = kRows * 128;            // a tile's P (hi or lo)
-  static constexpr int kPBufs = kLo ? 1 : 2;
-  static constexpr int kStages = DC == 512 ? 2 : 4;      // of K and of V
+  static constexpr int kChunkSlabs = DC == 512 ? 3 : 5;  // of them in a K chunk
+  static constexpr int kChunks = kSlabs / kChunkSlabs;   // K chunks per tile
+  static constexpr int kBlocks = DC / 256;               // 256-column blocks of O
+  static constexpr int kQBytes = kSlabs * kSlab;
+  static constexpr int kKBytes = kChunkSlabs * kSlab;
+  static constexpr int kVBytes = 2 * kBlocks * kSlab;    // 64 keys of this CTA's columns
+  static constexpr int kRingK = DC == 512 && !kLo ? 3 : 2;
+  static constexpr int kRingV = DC == 512 ? 2 : 4;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kQBytes;
-  static constexpr int kOffV = kOffK + kStages * kKBytes;
-  static constexpr int kOffP = kOffV + kStages * kVBytes;
+  static constexpr int kOffV = kOffK + kRingK * kKBytes;
+  static constexpr int kOffP = kOffV + kRingV * kVBytes;  // P: half h at h * kSlab; the lo part behind
+  static constexpr int kOffBar = kOffP + (kLo ? 4 : 2) * kSlab;
+  // O on its way out: rows padded by 16 bytes against bank conflicts, over the rings and P
+  static constexpr int kStagePitch = DC * 4 + 16;
+  static_assert(kOffK + kRows * kStagePitch <= kOffBar, "staging");
   // barrier slots
   static constexpr int kFullK = 0;                       // (even CTA) both CTAs' K landed
-  static constexpr int kFullV = kFullK + kStages;        // (even CTA) both CTAs' V landed
-  static constexpr int kEmptyK = kFullV + kStages;       // S of the stage's tile done
-  static constexpr int kEmptyV = kEmptyK + kStages;      // PV of the stage's tile done
-  static constexpr int kSFull = kEmptyV + kStages;       // [2] S of region r done
+  static constexpr int kFullV = kFullK + kRingK;         // (even CTA) both CTAs' V landed
+  static constexpr int kEmptyK = kFullV + kRingV;        // the scores of the chunk done
+  static constexpr int kEmptyV = kEmptyK + kRingK;       // the values of the chunk done
+  static constexpr int kSFull = kEmptyV + kRingV;        // [2] S of region r done
   static constexpr int kSFree = kSFull + 2;              // [2] (even CTA) region r read in both CTAs
-  static constexpr int kPFull = kSFree + 2;              // [2] (even CTA) P written in both CTAs
-  static constexpr int kPvDone = kPFull + 2;             // [2] PV of the P buffer's tile done
+  static constexpr int kPFull = kSFree + 2;              // (even CTA) P written in both CTAs
+  static constexpr int kPvDone = kPFull + 1;             // [2] the values of half h of a tile done
   static constexpr int kInfoFull = kPvDone + 2;          // [8] a tile's record written
   static constexpr int kQFull = kInfoFull + kInfo;       // (even CTA) both CTAs' Q landed
-  static constexpr int kRagged = kQFull + 1;             // this CTA's V of a tile that is not whole
+  static constexpr int kQFree = kQFull + 1;              // the piece's score products done
+  static constexpr int kOut = kQFree + 1;                // this CTA's O has left the rings
+  static constexpr int kRagged = kOut + 1;               // this CTA's V of a chunk that is not whole
   static constexpr int kDrainS = kRagged + 1;
   static constexpr int kDrainV = kDrainS + 1;
   static constexpr int kNumBars = kDrainV + 1;
-  static constexpr int kOffBar = kOffP + (kLo ? 2 : kPBufs) * kPBytes;
   static constexpr int kOffInfo = (kOffBar + kNumBars * 8 + 15) & ~15;
-  static constexpr int kOffRed = kOffInfo + kInfo * 16;  // float[2][2][64] maxima (then sums)
+  static constexpr int kOffRed = kOffInfo + kInfo * 8;   // float[2][2][64] maxima (then sums)
   static constexpr int kOffSlot = kOffRed + 2 * 2 * kRows * 4;
   static constexpr int kOffAbort = kOffSlot + 4;
-  static constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // + alignment of the dynamic base
+  static constexpr int kOffScored = kOffAbort + 4;       // tiles whose scores are in (paces the prefetch)
+  static constexpr int kSmemBytes = kOffScored + 4 + 1024;  // + alignment of the dynamic base
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static_assert(kInfo >= kStages + 2, "tile records");
-  static_assert(kQSlab % 1024 == 0 && kKSlab % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+  static_assert(kSlabs % kChunkSlabs == 0, "whole chunks");
   static constexpr uint32_t kIdescS = tc::instr_desc(2 * kRows, kKeys, false, false);
   static constexpr uint32_t kIdescPV = tc::instr_desc(2 * kRows, 256, false, true);
 };
 
-// Rows [0, vhi) of the tile hold keys of the partition; bit c of `bad` marks a
-// 16-key group whose page id lies outside the pool (not loaded).
+// Bit c of `bad` marks a 16-key group of the tile whose page id lies outside the pool (not loaded).
 struct TileInfo {
-  int vhi;
-  uint32_t bad;
-  int pad[2];
+  uint32_t bad, pad;
 };
 
-// The pair's share of the work, the same in every thread of both CTAs.
-struct Plan {
-  int b, cb, p;    // row, block of 128 columns, partition
-  int cols, len;   // the row's query columns and keys
-  int t0, n;       // tiles [t0, t0 + n)
-  bool ok;
+// One piece of the work, the same in every thread of both CTAs.
+struct Piece {
+  int b, cb, p, count;  // row, block of 128 columns, piece of the row's `count`
+  int len;              // the row's keys
+  int t0, n;            // tiles [t0, t0 + n)
 };
 
-__device__ __forceinline__ Plan make_plan(const LatentAttnArgs &a) {
-  Plan pl;
+__device__ __forceinline__ int tiles_of(int len) { return (len + kKeys - 1) / kKeys; }
+
+// Lengths as the kernels use them: clamped into the table, `bad` where that changes one or a row
+// is shorter than its window.
+__device__ __forceinline__ int usable_len(const LatentAttnArgs &a, int b, bool *bad) {
+  const long long cap = (long long)a.table_stride * a.page_size, len = a.seq_lens[b];
+  *bad = len < 0 || len > cap || (len > 0 && len < a.num_tokens);
+  return (int)(len < 0 ? 0 : (len > cap ? cap : len));
+}
+
+// Tiles per piece: the plan's, or more if a device length outgrew the planned ones (at
+// most num_splits pieces a row).  Every warp computes it alike.
+__device__ __forceinline__ int piece_tiles(const LatentAttnArgs &a, int lane, bool report) {
+  int most = 0;
+  bool any_bad = false;
+  for (int b = lane; b < a.batch; b += 32) {
+    bool bad;
+    most = max(most, tiles_of(usable_len(a, b, &bad)));
+    any_bad |= bad;
+  }
+  if (report && any_bad) raise_fault(a.status, PSKV_FAULT_BAD_LENGTH);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  return max(max(a.tiles_per_piece, (most + a.num_splits - 1) / a.num_splits), 1);
+}
+
+// Piece u in the order (row, piece, block of columns), the last fastest; false past the end.
+__device__ __forceinline__ bool find_piece(const LatentAttnArgs &a, int u, int q, int lane,
+                                           Piece &pc) {
   const int blocks = (a.num_tokens * a.num_q_heads + 127) / 128;
-  const int x = blockIdx.x >> 1;
-  pl.cb = x % blocks;
-  pl.p = x / blocks;
-  pl.b = blockIdx.y;
-  pl.cols = a.num_tokens * a.num_q_heads;
-  const long long cap = (long long)a.table_stride * a.page_size;
-  long long len = a.seq_lens[pl.b];
-  pl.ok = !(len < 0 || len > cap || (len > 0 && len < a.num_tokens));
-  len = len < 0 ? 0 : (len > cap ? cap : len);
-  pl.len = (int)len;
-  const int tiles = (pl.len + kKeys - 1) / kKeys, per = (tiles + a.num_splits - 1) / a.num_splits;
-  pl.t0 = min(pl.p * per, tiles);
-  pl.n = min(pl.t0 + per, tiles) - pl.t0;
-  return pl;
+  const int unit = blocks == 1 ? u : u / blocks;
+  int base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    bool bad;
+    const int len = b0 + lane < a.batch ? usable_len(a, b0 + lane, &bad) : 0;
+    int n = b0 + lane < a.batch ? max(1, (tiles_of(len) + q - 1) / q) : 0;
+    int incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + incl > unit);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      pc.b = b0 + l;
+      pc.cb = u - unit * blocks;
+      pc.len = __shfl_sync(0xffffffffu, len, l);
+      pc.count = __shfl_sync(0xffffffffu, n, l);
+      pc.p = unit - base - __shfl_sync(0xffffffffu, incl - n, l);
+      const int tiles = tiles_of(pc.len);
+      pc.t0 = min(pc.p * q, tiles);
+      pc.n = min(pc.t0 + q, tiles) - pc.t0;
+      return true;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
 }
 
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, ahead;
+};
+
+// Where a tile's keys lie: the table slot and the row in its page, stepped from tile to tile
+// without a division.
+struct Place {
+  int slot, row;
+  __device__ Place(int key, int page_size) : slot(key / page_size), row(key % page_size) {}
+  __device__ void step(int keys, int page_size) {
+    row += keys;
+    while (row >= page_size) {
+      row -= page_size;
+      ++slot;
+    }
+  }
 };
 
 // A copy warp (all lanes converged; one elected lane issues) of one CTA: the
-// scores' share of each tile (keys 32 r .. + 31, all columns) or the values' (all
-// keys, the CTA's columns).
+// scores' share of each tile (keys 64 r .. + 63, all columns, in chunks of slabs) or
+// the values' (in chunks of 64 keys, all the CTA's columns).  A copy costs its issuing warp ~365
+// cycles whatever its size (measured: 8 KB a copy 23 bytes a cycle and warp, 24 KB 67; the
+// SM's own limit is 85 to 118), so chunks are single copies of 24 and 32 KB.
 template <int DC, bool kLo, bool kV>
 struct Loader {
   using L = Lay<DC, kLo>;
-  static constexpr int kBoxes = kKeys / 16;
+  static constexpr int kRing = kV ? L::kRingV : L::kRingK;
   const LatentAttnArgs &a;
-  const Plan &pl;
   const CUtensorMap *map;
   unsigned char *sm;
   uint64_t *bars;
   volatile int *abort_flag;
   uint32_t rank;
-  int lane, n_slots;
-  bool whole;  // pages of whole tiles: one box of all slabs (else 16 rows of a slab each)
+  int lane;
+  bool whole;  // pages of whole half tiles: boxes of 64 rows (else of 16)
   PageCache pages;
-  int issued = 0, ragged = 0;  // tiles begun; of them landed on kRagged
+  int seq = 0, tile = 0, ragged = 0;  // chunks, tiles, chunks landed on kRagged, over all pieces
 
-  __device__ Loader(const LatentAttnArgs &a_, const Plan &pl_, const CUtensorMap *m,
-                    unsigned char *sm_, uint64_t *bars_, volatile int *ab, uint32_t rank_)
-      : a(a_), pl(pl_), map(m), sm(sm_), bars(bars_), abort_flag(ab), rank(rank_) {
+  __device__ Loader(const LatentAttnArgs &a_, const CUtensorMap *m, unsigned char *sm_,
+                    uint64_t *bars_, volatile int *ab, uint32_t rank_)
+      : a(a_), map(m), sm(sm_), bars(bars_), abort_flag(ab), rank(rank_) {
     lane = threadIdx.x & 31;
-    n_slots = (pl.len + a.page_size - 1) / a.page_size;
-    whole = a.page_size % kKeys == 0;
+    whole = a.page_size % kHalf == 0;
   }
 
-  // Pool rows of the tile's 16-key groups (whole pages: of the tile, in ys[0]); -1: not loaded.
-  __device__ void find(int j, int (&ys)[kBoxes], TileInfo &inf) {
-    const int32_t *tbl = a.page_tables + (size_t)pl.b * a.table_stride;
-    const int key0 = (pl.t0 + j) * kKeys;
-    inf.vhi = min(kKeys, pl.len - key0);
-    inf.bad = 0;
-    const int step = whole ? kKeys : 16;
+  // Pool rows of a tile's boxes (whole: two of 64 rows; else eight of 16); -1: not loaded.
+  // `left`: the row's keys from the tile's first on.
+  __device__ uint32_t find(const int32_t *tbl, int n_slots, int left, Place at, int (&ys)[8]) {
+    uint32_t bad = 0;
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < kBoxes; ++i) {
-      ys[i] = -1;
-      if (i * step >= inf.vhi) continue;
-      const int key = key0 + i * step;
-      const int page = pages.get(tbl, key / a.page_size, n_slots, lane);
-      if (page < 0 || (long long)page >= a.num_pages)
-        inf.bad |= whole ? 0xFu : 1u << i;
-      else
-        ys[i] = page * a.page_size + key % a.page_size;
+      for (int i = 0; i < 2; ++i) {
+        ys[i] = -1;
+        if (i * kHalf >= left) break;
+        const int page = pages.get(tbl, at.slot, n_slots, lane);
+        if (page < 0 || (long long)page >= a.num_pages)
+          bad |= 0xFu << (4 * i);
+        else
+          ys[i] = page * a.page_size + at.row;
+        at.step(kHalf, a.page_size);
+      }
+      return bad;
     }
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      int y = -1;
+      if (16 * i < left) {
+        const int page = pages.get(tbl, at.slot, n_slots, lane);
+        if (page < 0 || (long long)page >= a.num_pages)
+          bad |= 1u << i;
+        else
+          y = page * a.page_size + at.row;
+      }
+      at.step(16, a.page_size);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k == i) ys[k] = y;
+    }
+    return bad;
   }
 
-  __device__ bool wait(int slot, uint32_t parity) {
-    return tc2::warp_wait(bars + slot, parity, abort_flag, a.status);
+  __device__ bool free_stage(int st) {
+    return seq < kRing || tc::warp_wait(bars + (kV ? L::kEmptyV : L::kEmptyK) + st,
+                                        (seq / kRing - 1) & 1, abort_flag, a.status);
   }
 
-  __device__ void run() {
-    for (int j = 0; j < pl.n; ++j) {
-      const int st = j % L::kStages;
-      if (j >= L::kStages &&
-          !wait((kV ? L::kEmptyV : L::kEmptyK) + st, ((j / L::kStages) - 1) & 1))
-        return;
-      int ys[kBoxes];
-      TileInfo inf;
-      find(j, ys, inf);
-      issued = j + 1;
-      if (kV)
-        load_v(j, st, ys, inf);
-      else
-        load_k(j, st, ys, inf);
+  __device__ bool run(const Piece &pc) {
+    pages.base = -1;  // another row's table
+    const int32_t *tbl = a.page_tables + (size_t)pc.b * a.table_stride;
+    const int n_slots = (pc.len + a.page_size - 1) / a.page_size;
+    Place at(pc.t0 * kKeys, a.page_size);
+    for (int j = 0; j < pc.n; ++j, ++tile) {
+      const int left = pc.len - (pc.t0 + j) * kKeys;
+      int ys[8];
+      const uint32_t bad = find(tbl, n_slots, left, at, ys);
+      at.step(kKeys, a.page_size);
+      if (!(kV ? load_v(min(left, kKeys), ys, bad) : load_k(ys, bad))) return false;
     }
+    return true;
+  }
+
+  __device__ bool load_k(const int (&ys)[8], uint32_t bad) {
+    // rows behind the row's end (inside a page) may come along: their scores are masked
+    uint32_t rows = 0;  // both CTAs'
+    if (whole)
+      rows = (ys[0] >= 0 ? kHalf : 0) + (ys[1] >= 0 ? kHalf : 0);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rows += ys[i] >= 0 ? 16 : 0;
+#pragma unroll 1
+    for (int c = 0; c < L::kChunks; ++c, ++seq) {
+      const int st = seq % kRing;
+      if (!free_stage(st)) return false;
+      const uint32_t dst = smem_u32(sm + L::kOffK + st * L::kKBytes);
+      const uint32_t bar = tc2::map_to(smem_u32(bars + L::kFullK + st), 0);
+      if (elect_one()) {
+        if (rank == 0) mbar_arrive_expect_tx(bars + L::kFullK + st, rows * 128 * L::kChunkSlabs);
+        if (whole) {
+          const int y = rank == 0 ? ys[0] : ys[1];
+          if (y >= 0) tc2::tma_load_3d(dst, map, 0, y, c * L::kChunkSlabs, bar);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int y = rank == 0 ? ys[i] : ys[4 + i];
+            if (y < 0) continue;
+            for (int s = 0; s < L::kChunkSlabs; ++s)
+              tc2::tma_load_3d(dst + s * kSlab + i * 16 * 128, map, 0, y, c * L::kChunkSlabs + s,
+                               bar);
+          }
+        }
+        if (c == 0) {
+          if (bad && rank == 0) raise_fault(a.status, PSKV_FAULT_BAD_PAGE);
+          reinterpret_cast<TileInfo *>(sm + L::kOffInfo)[tile % kInfo].bad = bad;
+          mbar_arrive(bars + L::kInfoFull + tile % kInfo);
+        }
+      }
+      __syncwarp();
+    }
+    return true;
+  }
+
+  __device__ bool load_v(int vhi, const int (&ys)[8], uint32_t bad) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      if (vhi <= h * kHalf) break;  // no key in this half
+      const int st = seq % kRing;
+      if (!free_stage(st)) return false;
+      ++seq;
+      unsigned char *stage = sm + L::kOffV + st * L::kVBytes;
+      const uint32_t dst = smem_u32(stage);
+      const uint32_t full = tc2::map_to(smem_u32(bars + L::kFullV + st), 0);
+      const uint32_t hbad = (bad >> (4 * h)) & 0xFu;
+      const bool plain = vhi >= (h + 1) * kHalf && hbad == 0;
+      // a chunk with rows that must not be met lands on a barrier of this CTA first
+      const uint32_t bar = plain ? full : smem_u32(bars + L::kRagged);
+      if (elect_one()) {
+        uint32_t rows = 0;
+        if (whole)
+          rows = (h == 0 ? ys[0] : ys[1]) >= 0 ? kHalf : 0;
+        else
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rows += (h == 0 ? ys[i] : ys[4 + i]) >= 0 ? 16 : 0;
+        const uint32_t bytes = rows * 256 * L::kBlocks;
+        if (!plain)
+          mbar_arrive_expect_tx(bars + L::kRagged, bytes);
+        else if (rank == 0)
+          mbar_arrive_expect_tx(bars + L::kFullV + st, 2 * bytes);
+        if (whole) {
+          const int y = h == 0 ? ys[0] : ys[1];
+          if (y >= 0) tc2::tma_load_4d(dst, map, 0, y, 2 * (int)rank, 0, bar);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int y = h == 0 ? ys[i] : ys[4 + i];
+            if (y < 0) continue;
+            for (int s = 0; s < 2 * L::kBlocks; ++s)
+              tc2::tma_load_4d(dst + s * kSlab + i * 16 * 128, map, 0, y, 2 * (int)rank + (s & 1),
+                               s >> 1, bar);
+          }
+        }
+      }
+      __syncwarp();
+      if (!plain) {
+        // rows behind the end or of skipped groups may hold anything and meet P = 0: zero them
+        mbar_wait(bars + L::kRagged, ragged & 1);  // (bounded; landed or given up on, the chunk is passed on)
+        ++ragged;
+        for (int e = lane; e < kHalf * 16 * L::kBlocks; e += 32) {
+          const int row = e & (kHalf - 1), piece = e >> 6;
+          if (row + h * kHalf >= vhi || ((hbad >> (row >> 4)) & 1u))
+            *reinterpret_cast<uint4 *>(stage + (piece >> 3) * kSlab + row * 128 + (piece & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_smem_for_async();
+        __syncwarp();
+        if (rank == 0 && lane == 0) mbar_arrive(bars + L::kFullV + st);  // in place of the copies' count
+      }
+      if (lane == 0) tc2::arrive_pair(full);
+    }
+    return true;
   }
 
   // Wait (bounded) for the last copies into each stage, of both CTAs (their count is the even CTA's).
   __device__ void drain() {
     if (rank != 0) return;
-    for (int j = max(0, issued - L::kStages); j < issued; ++j)
-      mbar_wait(bars + (kV ? L::kFullV : L::kFullK) + j % L::kStages, (j / L::kStages) & 1);
-  }
-
-  __device__ void load_k(int j, int st, const int (&ys)[kBoxes], const TileInfo &inf) {
-    const uint32_t dst = smem_u32(sm + L::kOffK + st * L::kKBytes);
-    const uint32_t bar = tc2::map_to(smem_u32(bars + L::kFullK + st), 0);
-    if (elect_one()) {
-      if (inf.bad && rank == 0) raise_fault(a.status, PSKV_FAULT_BAD_PAGE);
-      TileInfo &t = *reinterpret_cast<TileInfo *>(sm + L::kOffInfo + (j % kInfo) * 16);
-      t.vhi = inf.vhi;
-      t.bad = inf.bad;
-      mbar_arrive(bars + L::kInfoFull + j % kInfo);
-      if (whole) {
-        // both CTAs' 32 rows, whatever of them lies behind the row's end (inside the page)
-        if (rank == 0) mbar_arrive_expect_tx(bars + L::kFullK + st, ys[0] < 0 ? 0 : 2 * L::kKBytes);
-        if (ys[0] >= 0) tc2::tma_load_3d(dst, map, 0, ys[0] + kHalfKeys * (int)rank, 0, bar);
-      } else {
-        int loaded = 0;
-#pragma unroll
-        for (int i = 0; i < kBoxes; ++i) loaded += ys[i] >= 0;
-        if (rank == 0) mbar_arrive_expect_tx(bars + L::kFullK + st, loaded * L::kSlabs * 16 * 128);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int y = rank == 0 ? ys[i] : ys[i + 2];
-          if (y < 0) continue;
-          for (int s = 0; s < L::kSlabs; ++s)
-            tc2::tma_load_3d(dst + s * L::kKSlab + i * 16 * 128, map, 0, y, s, bar);
-        }
-      }
-    }
-    __syncwarp();
-    if (whole && j + kAhead < pl.n) {  // the same share of a later tile into L2
-      const int key = (pl.t0 + j + kAhead) * kKeys;
-      const int page = pages.get(a.page_tables + (size_t)pl.b * a.table_stride, key / a.page_size,
-                                 n_slots, lane);
-      if (page >= 0 && (long long)page < a.num_pages && elect_one())
-        tc2::tma_prefetch_3d(map, 0, page * a.page_size + key % a.page_size + kHalfKeys * (int)rank, 0);
-      __syncwarp();
-    }
-  }
-
-  // Value slab s of this CTA: columns of block s / 2, 128 rank + 64 (s % 2).
-  __device__ int slab_of(int s) { return 4 * (s >> 1) + 2 * (int)rank + (s & 1); }
-
-  __device__ void load_v(int j, int st, const int (&ys)[kBoxes], const TileInfo &inf) {
-    unsigned char *stage = sm + L::kOffV + st * L::kVBytes;
-    const uint32_t dst = smem_u32(stage);
-    const uint32_t full = tc2::map_to(smem_u32(bars + L::kFullV + st), 0);
-    const bool plain = inf.vhi == kKeys && inf.bad == 0;
-    int loaded = 0;
-#pragma unroll
-    for (int i = 0; i < kBoxes; ++i) loaded += ys[i] >= 0;
-    const uint32_t bytes = (uint32_t)(loaded * (whole ? kKeys : 16) * 128 * L::kVSlabs);
-    // a tile with rows that must not be met lands on a barrier of this CTA first
-    const uint32_t bar = plain ? full : smem_u32(bars + L::kRagged);
-    if (elect_one()) {
-      if (plain) {
-        if (rank == 0) mbar_arrive_expect_tx(bars + L::kFullV + st, 2 * bytes);
-      } else {
-        mbar_arrive_expect_tx(bars + L::kRagged, bytes);
-      }
-      if (whole) {
-        if (ys[0] >= 0)
-#pragma unroll
-          for (int k = 0; k < L::kBlocks; ++k)
-            tc2::tma_load_3d(dst + 2 * k * L::kVSlab, map, 0, ys[0], 4 * k + 2 * (int)rank, bar);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kBoxes; ++i)
-          if (ys[i] >= 0)
-            for (int s = 0; s < L::kVSlabs; ++s)
-              tc2::tma_load_3d(dst + s * L::kVSlab + i * 16 * 128, map, 0, ys[i], slab_of(s), bar);
-      }
-    }
-    __syncwarp();
-    if (!plain) {
-      // rows behind the end or of skipped groups may hold anything and meet P = 0: zero them
-      mbar_wait(bars + L::kRagged, ragged & 1);  // (bounded; landed or given up on, the tile is passed on)
-      ++ragged;
-      for (int e = lane; e < kKeys * L::kVSlabs * 8; e += 32) {
-        const int row = e & (kKeys - 1), piece = e >> 6;
-        if (row >= inf.vhi || ((inf.bad >> (row >> 4)) & 1u))
-          *reinterpret_cast<uint4 *>(stage + (piece >> 3) * L::kVSlab + row * 128 +
-                                     (piece & 7) * 16) = make_uint4(0, 0, 0, 0);
-      }
-      tc::fence_smem_for_async();
-      __syncwarp();
-    }
-    if (lane == 0) tc2::arrive_cluster(full);
-    if (!plain && rank == 0 && lane == 0) mbar_arrive(bars + L::kFullV + st);  // in place of the copies' count
+    for (int s = max(0, seq - kRing); s < seq; ++s)
+      mbar_wait(bars + (kV ? L::kFullV : L::kFullK) + s % kRing, (s / kRing) & 1);
   }
 };
+
+// Bulk copy shared -> global (16-byte aligned, bytes a multiple of 16), tracked by this thread's group.
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit_and_wait_read() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
 
 }  // namespace
 
@@ -319,55 +423,46 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kOffBar);
   uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::kOffSlot);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kOffAbort);
+  volatile int *scored = reinterpret_cast<volatile int *>(sm + L::kOffScored);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc2::cluster_rank();
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-  pdl_wait();
-  pdl_launch_dependents();
-  const Plan pl = make_plan(a);
-  if (!pl.ok && threadIdx.x == 0 && blockIdx.x == 0) raise_fault(a.status, PSKV_FAULT_BAD_LENGTH);
-  const int w = warp & 3, i = (32 * w + lane) & (kRows - 1), kh = w >> 1;  // softmax thread: row, half
-  const int col = pl.cb * 128 + (int)rank * kRows + i;
-  const size_t row = (size_t)pl.b * pl.cols + col, part = row * a.num_splits + pl.p;
-  if (pl.n <= 0) {  // (both CTAs leave here together) the empty state, or zeros
-    if (warp < 2 || warp > 5 || col >= pl.cols) return;
-    if (a.direct) {
-      if (pl.len > 0 && kh == 0) raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
-      const int es = a.out_dtype == PSKV_DTYPE_BF16 ? 2 : 4;
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + row * DC * es);
-      for (int e = kh; e < DC * es / 16; e += 2) dst[e] = make_uint4(0, 0, 0, 0);
-    } else if (kh == 0) {
-      a.ws_m[part] = -CUDART_INF_F;
-      a.ws_l[part] = 0.f;
-    }
-    return;
-  }
-
+  // set up before the previous kernel's results are waited for
   if (warp == 1) {
     if (lane == 0) {
-      for (int s = 0; s < L::kStages; ++s) {
+      tc2::prefetch_map(&maps.q);
+      tc2::prefetch_map(&maps.k);
+      for (int s = 0; s < L::kRingK; ++s) {
         mbar_init(&bars[L::kFullK + s], 1);
-        mbar_init(&bars[L::kFullV + s], 3);  // the expected bytes, and a word from either V copy warp
         mbar_init(&bars[L::kEmptyK + s], 1);
+      }
+      for (int s = 0; s < L::kRingV; ++s) {
+        mbar_init(&bars[L::kFullV + s], 3);  // the expected bytes, and a word from either V copy warp
         mbar_init(&bars[L::kEmptyV + s], 1);
       }
       for (int r = 0; r < 2; ++r) {
         mbar_init(&bars[L::kSFull + r], 1);
         mbar_init(&bars[L::kSFree + r], 8);  // four softmax warps in each CTA
-        mbar_init(&bars[L::kPFull + r], 8);
         mbar_init(&bars[L::kPvDone + r], 1);
       }
+      mbar_init(&bars[L::kPFull], 8);
       for (int k = 0; k < kInfo; ++k) mbar_init(&bars[L::kInfoFull + k], 1);
       mbar_init(&bars[L::kQFull], 1);
+      mbar_init(&bars[L::kQFree], 1);
+      mbar_init(&bars[L::kOut], 4);
       mbar_init(&bars[L::kRagged], 1);
       mbar_init(&bars[L::kDrainS], 1);
       mbar_init(&bars[L::kDrainV], 1);
       *abort_flag = 0;
+      *scored = 0;
       mbar_fence_init();
     }
     __syncwarp();
   } else if (warp == 0) {
     tc2::alloc(slot, kTmemCols);
+  } else if (warp == 6 && lane == 0) {
+    tc2::prefetch_map(&maps.v);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -375,30 +470,48 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *slot;
   auto wait = [&](int s, uint32_t parity) {
-    return tc2::warp_wait(bars + s, parity, abort_flag, a.status);
+    return tc::warp_wait(bars + s, parity, abort_flag, a.status);
   };
+  pdl_wait();
+  pdl_launch_dependents();
+  const int q = piece_tiles(a, lane, blockIdx.x == 0 && warp == 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.ws_tiles) *a.ws_tiles = q;  // for the merge
+  Piece pc;
 
   if (warp == 0 && rank == 0) {
     // ---- the score products
-    bool ok = wait(L::kQFull, 0);
-    const uint32_t q0 = smem_u32(sm + L::kOffQ);
-    for (int j = 0; ok && j < pl.n; ++j) {
-      const int st = j % L::kStages, r = j & 1;
-      ok = wait(L::kFullK + st, (j / L::kStages) & 1) &&
-           (j < 2 || wait(L::kSFree + r, ((j - 2) >> 1) & 1));
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t k0 = smem_u32(sm + L::kOffK + st * L::kKBytes);
-      if (elect_one()) {
+    bool ok = true;
+    int seq = 0, g = 0, k = 0;  // chunks, tiles, pieces so far
+    for (int u = first; ok && find_piece(a, u, q, lane, pc); u += step) {
+      if (pc.n == 0) continue;
+      ok = wait(L::kQFull, k & 1);
+      ++k;
+      const uint32_t q0 = smem_u32(sm + L::kOffQ);
+      for (int j = 0; ok && j < pc.n; ++j, ++g) {
+        const int r = g & 1;
+        if (g >= 2) ok = wait(L::kSFree + r, (g / 2 - 1) & 1);
+#pragma unroll 1
+        for (int c = 0; ok && c < L::kChunks; ++c, ++seq) {
+          const int st = seq % L::kRingK;
+          ok = wait(L::kFullK + st, (seq / L::kRingK) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t k0 = smem_u32(sm + L::kOffK + st * L::kKBytes);
+          const uint32_t qc = q0 + c * L::kKBytes;
+          if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4 * L::kSlabs; ++kk)
-          tc2::mma(tmem + kSCol + kHalfKeys * r,
-                   tc::smem_desc(q0 + (kk >> 2) * L::kQSlab + (kk & 3) * 32, 16, 1024),
-                   tc::smem_desc(k0 + (kk >> 2) * L::kKSlab + (kk & 3) * 32, 16, 1024), L::kIdescS,
-                   kk > 0);
-        tc2::commit_both(bars + L::kSFull + r);
-        tc2::commit_both(bars + L::kEmptyK + st);
+            for (int kk = 0; kk < 4 * L::kChunkSlabs; ++kk) {
+              const uint32_t at = (kk >> 2) * kSlab + (kk & 3) * 32;
+              tc2::mma(tmem + kSCol + kHalf * r, tc::smem_desc(qc + at, 16, 1024),
+                       tc::smem_desc(k0 + at, 16, 1024), L::kIdescS, c > 0 || kk > 0);
+            }
+            tc2::commit_both(bars + L::kEmptyK + st);
+            if (c == L::kChunks - 1) tc2::commit_both(bars + L::kSFull + r);
+          }
+          __syncwarp();
+        }
       }
+      if (elect_one()) tc2::commit_both(bars + L::kQFree);
       __syncwarp();
     }
     if (elect_one()) tc2::commit_both(bars + L::kDrainS);
@@ -406,204 +519,278 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == 7 && rank == 0) {
     // ---- the value products
     bool ok = true;
-    for (int j = 0; ok && j < pl.n; ++j) {
-      const int st = j % L::kStages, pb = j % L::kPBufs;
-      ok = wait(L::kPFull + pb, (j / L::kPBufs) & 1) && wait(L::kFullV + st, (j / L::kStages) & 1);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t v0 = smem_u32(sm + L::kOffV + st * L::kVBytes);
-      const uint32_t p0 = smem_u32(sm + L::kOffP + pb * L::kPBytes);
-      if (elect_one()) {
+    int seq = 0, g = 0;
+    for (int u = first; ok && find_piece(a, u, q, lane, pc); u += step)
+      for (int j = 0; ok && j < pc.n; ++j, ++g) {
+        const int halves = pc.len - (pc.t0 + j) * kKeys > kHalf ? 2 : 1;
+        ok = wait(L::kPFull, g & 1);
+        const uint32_t p0 = smem_u32(sm + L::kOffP);
+#pragma unroll 1
+        for (int h = 0; ok && h < halves; ++h, ++seq) {
+          const int st = seq % L::kRingV;
+          ok = wait(L::kFullV + st, (seq / L::kRingV) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t v0 = smem_u32(sm + L::kOffV + st * L::kVBytes);
+          if (elect_one()) {
 #pragma unroll
-        for (int nb = 0; nb < L::kBlocks; ++nb)
+            for (int nb = 0; nb < L::kBlocks; ++nb)
 #pragma unroll
-          for (int part_ = 0; part_ < (kLo ? 2 : 1); ++part_)
+              for (int part = 0; part < (kLo ? 2 : 1); ++part)
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              tc2::mma(tmem + kOCol + 128 * nb,
-                       tc::smem_desc(p0 + part_ * L::kPBytes + kk * 32, 16, 1024),
-                       tc::smem_desc(v0 + 2 * nb * L::kVSlab + kk * 2048, L::kVSlab, 1024),
-                       L::kIdescPV, j > 0 || part_ > 0 || kk > 0);
-        tc2::commit_both(bars + L::kPvDone + pb);
-        tc2::commit_both(bars + L::kEmptyV + st);
+                for (int kk = 0; kk < kHalf / 16; ++kk)
+                  tc2::mma(tmem + kOCol + 128 * nb,
+                           tc::smem_desc(p0 + (2 * part + h) * kSlab + kk * 32, 16, 1024),
+                           tc::smem_desc(v0 + 2 * nb * kSlab + kk * 2048, kSlab, 1024),
+                           L::kIdescPV, j > 0 || h > 0 || part > 0 || kk > 0);
+            tc2::commit_both(bars + L::kEmptyV + st);
+            tc2::commit_both(bars + L::kPvDone + h);
+            if (halves == 1) tc2::commit_both(bars + L::kPvDone + 1);  // a half without keys
+          }
+          __syncwarp();
+        }
       }
-      __syncwarp();
-    }
     if (elect_one()) tc2::commit_both(bars + L::kDrainV);
     __syncwarp();
   } else if (warp == 1) {
-    // ---- Q (this CTA's 64 columns; behind the row's last column: other rows' or zeros), then K
-    if (elect_one()) {
-      if (rank == 0) mbar_arrive_expect_tx(bars + L::kQFull, 2 * L::kQBytes);
-      tc2::tma_load_3d(smem_u32(sm + L::kOffQ), &maps.q, 0,
-                       pl.b * pl.cols + pl.cb * 128 + (int)rank * kRows, 0,
-                       tc2::map_to(smem_u32(bars + L::kQFull), 0));
+    Loader<DC, kLo, false> ld(a, &maps.k, sm, bars, abort_flag, rank);
+    int k = 0;
+    for (int u = first; find_piece(a, u, q, lane, pc); u += step) {
+      if (pc.n == 0) continue;
+      // Q once the last piece's scores are done, K once its O has left the rings
+      if (k > 0 && (!wait(L::kQFree, (k - 1) & 1) || !wait(L::kOut, (k - 1) & 1))) break;
+      if (elect_one()) {
+        // this CTA's 64 columns (behind the row's last column: other rows' or zeros)
+        if (rank == 0) mbar_arrive_expect_tx(bars + L::kQFull, 2 * L::kQBytes);
+        tc2::tma_load_3d(smem_u32(sm + L::kOffQ), &maps.q, 0,
+                         pc.b * (a.num_tokens * a.num_q_heads) + pc.cb * 128 + (int)rank * kRows, 0,
+                         tc2::map_to(smem_u32(bars + L::kQFull), 0));
+      }
+      __syncwarp();
+      ++k;
+      if (!ld.run(pc)) break;
     }
-    __syncwarp();
-    Loader<DC, kLo, false> ld(a, pl, &maps.k, sm, bars, abort_flag, rank);
-    ld.run();
     ld.drain();
-    if (rank == 0) mbar_wait(bars + L::kQFull, 0);
+    if (rank == 0 && k > 0) mbar_wait(bars + L::kQFull, (k - 1) & 1);
   } else if (warp == 6) {
-    Loader<DC, kLo, true> ld(a, pl, &maps.v, sm, bars, abort_flag, rank);
-    ld.run();
+    Loader<DC, kLo, true> ld(a, &maps.v, sm, bars, abort_flag, rank);
+    int k = 0;
+    for (int u = first; find_piece(a, u, q, lane, pc); u += step) {
+      if (pc.n == 0) continue;
+      if (k > 0 && !wait(L::kOut, (k - 1) & 1)) break;
+      ++k;
+      if (!ld.run(pc)) break;
+    }
     ld.drain();
+  } else if (warp == 8) {
+    // ---- this CTA's share of the scores' tiles into L2, kAhead tiles before their scores
+    PageCache pages;
+    int g = 0;
+    for (int u = first; a.page_size % kHalf == 0 && find_piece(a, u, q, lane, pc); u += step) {
+      pages.base = -1;
+      const int n_slots = (pc.len + a.page_size - 1) / a.page_size;
+      int key = pc.t0 * kKeys + kHalf * (int)rank;
+      Place at(key, a.page_size);
+      for (int j = 0; j < pc.n; ++j, ++g) {
+        for (uint32_t i = 0; i < kWaitPolls && *scored < g - kAhead && !*abort_flag; ++i) __nanosleep(64);
+        if (j >= 1 && key < pc.len) {  // (the first tile's copies are already on their way)
+          const int page = pages.get(a.page_tables + (size_t)pc.b * a.table_stride, at.slot, n_slots, lane);
+          if (page >= 0 && (long long)page < a.num_pages && elect_one())
+            tc2::tma_prefetch_3d(&maps.ahead, 0, page * a.page_size + at.row, 0);
+          __syncwarp();
+        }
+        key += kKeys;
+        at.step(kKeys, a.page_size);
+      }
+    }
   } else if (warp >= 2 && warp <= 5) {
-    // ---- the softmax: thread (row i, keys 32 kh .. + 31 of the tile).  The loop never
-    // leaves early (the two warps of a row's halves meet every tile); after a failed wait its
+    // ---- the softmax: thread (row i, keys 64 kh .. + 63 of the tile).  The loops never
+    // leave early (the two warps of a row's halves meet every tile); after a failed wait
     // results are not written.
+    const int w = warp & 3, i = (32 * w + lane) & (kRows - 1), kh = w >> 1;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
     float *red = reinterpret_cast<float *>(sm + L::kOffRed);
-    const int t = col / a.num_q_heads;
-    const int lim = col < pl.cols ? pl.len - a.num_tokens + t + 1 : 0;  // keys below lim are seen
+    const TileInfo *info = reinterpret_cast<const TileInfo *>(sm + L::kOffInfo);
     const float sc = a.scale_log2;
     const uint32_t s_free = tc2::map_to(smem_u32(bars + L::kSFree), 0);
     const uint32_t p_full = tc2::map_to(smem_u32(bars + L::kPFull), 0);
-    float m = -CUDART_INF_F, l = 0.f;
+    const int cols = a.num_tokens * a.num_q_heads;
     bool ok = true;
-    for (int j = 0; j < pl.n; ++j) {
-      const int r = j & 1, pb = j % L::kPBufs;
-      ok = ok && wait(L::kSFull + r, (j >> 1) & 1);
-      ok = ok && wait(L::kInfoFull + j % kInfo, (j / kInfo) & 1);
-      const TileInfo inf = *reinterpret_cast<const TileInfo *>(sm + L::kOffInfo + (j % kInfo) * 16);
-      tc::fence_after_sync();
-      uint32_t v[32];
-      tc::ld32(lane_base + kSCol + kHalfKeys * r, v);
-      tc::wait_ld();
-      tc::reg_fence(v);
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc2::arrive_cluster(s_free + 8 * r);
-      const int key0 = (pl.t0 + j) * kKeys + kHalfKeys * kh;
-      float x[32];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]) * sc;
-      if (key0 + 32 > lim || inf.bad != 0) {  // (by selection: rows never loaded may hold anything)
-        const uint32_t bad = inf.bad >> (2 * kh);
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          x[c] = key0 + c < lim && !((bad >> (c >> 4)) & 1u) ? x[c] : -CUDART_INF_F;
+    int g = 0;  // tiles so far
+    int meets = 0;
+    for (int u = first; find_piece(a, u, q, lane, pc); u += step) {
+      const int col = pc.cb * 128 + (int)rank * kRows + i;
+      const int lim =  // keys below lim are seen
+          col < cols ? pc.len - a.num_tokens + col / a.num_q_heads + 1 : 0;
+      const size_t row0 = (size_t)pc.b * cols + pc.cb * 128 + rank * kRows;
+      if (pc.n == 0) {  // a row without keys (of one piece): zeros
+        if (col >= cols) continue;
+        const int es = a.out_dtype == PSKV_DTYPE_BF16 ? 2 : 4;
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + (row0 + i) * DC * es);
+        for (int e = kh; e < DC * es / 16; e += 2) dst[e] = make_uint4(0, 0, 0, 0);
+        continue;
       }
-      float mt = x[0];
-#pragma unroll
-      for (int c = 1; c < 32; ++c) mt = fmaxf(mt, x[c]);
-      float *mine = red + (j & 1) * 2 * kRows;
-      mine[kh * kRows + i] = mt;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 1)) : "memory");
-      mt = fmaxf(mt, mine[(kh ^ 1) * kRows + i]);
-      float alpha = 1.f;
-      bool rescale = false;
-      if (mt > m + kSlack) {
-        rescale = m != -CUDART_INF_F;  // with m = -inf the row's O and l are still 0
-        alpha = rescale ? ex2(m - mt) : 1.f;
-        l *= alpha;
-        m = mt;
-      }
-      const float u = m == -CUDART_INF_F ? 0.f : m;
-      uint32_t hi[16], lo[16];
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float p0 = ex2(x[2 * e] - u), p1 = ex2(x[2 * e + 1] - u);
-        hi[e] = pack_bf16x2(p0, p1);
-        if (kLo) {
-          lo[e] = pack_bf16x2(p0 - bf16_lo(hi[e]), p1 - bf16_hi(hi[e]));
-          sum += p0 + p1;
-        } else {
-          sum += bf16_lo(hi[e]) + bf16_hi(hi[e]);
-        }
-      }
-      l += sum;
-      // the P buffer is free once the values of tile j - kPBufs are done
-      if (j >= L::kPBufs) ok = ok && wait(L::kPvDone + pb, (j / L::kPBufs - 1) & 1);
-      unsigned char *prow = sm + L::kOffP + pb * L::kPBytes + i * 128;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int at = ((4 * kh + c) ^ (i & 7)) << 4;
-        *reinterpret_cast<uint4 *>(prow + at) =
-            make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-        if (kLo)
-          *reinterpret_cast<uint4 *>(prow + L::kPBytes + at) =
-              make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-      }
-      if (__any_sync(0xffffffffu, rescale)) {
-        ok = ok && wait(L::kPvDone + (j - 1) % L::kPBufs, ((j - 1) / L::kPBufs) & 1);
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int j = 0; j < pc.n; ++j, ++g, ++meets) {
+        const int r = g & 1;
+        ok = ok && wait(L::kSFull + r, (g >> 1) & 1);
+        ok = ok && wait(L::kInfoFull + g % kInfo, (g / kInfo) & 1);
+        const uint32_t bad = info[g % kInfo].bad >> (4 * kh);
         tc::fence_after_sync();
-#pragma unroll 1
-        for (int c = 0; c < DC / 64; ++c) {
-          uint32_t o[32];
-          tc::ld32(lane_base + kOCol + 32 * c, o);
-          tc::wait_ld();
-          tc::reg_fence(o);
+        uint32_t va[32], vb[32];
+        tc::ld32(lane_base + kSCol + kHalf * r, va);
+        tc::ld32(lane_base + kSCol + kHalf * r + 32, vb);
+        tc::wait_ld();
+        tc::reg_fence(va);
+        tc::reg_fence(vb);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc2::arrive_pair(s_free + 8 * r);
+        if (lane == 0 && w == 0) *scored = g + 1;
+        float x[kHalf];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tc::st32(lane_base + kOCol + 32 * c, o);
-          tc::wait_st();
+        for (int c = 0; c < 32; ++c) {
+          x[c] = __uint_as_float(va[c]);
+          x[32 + c] = __uint_as_float(vb[c]);
         }
+        // scores in log2 units are mul * x: whole tiles leave the product to the exponent's
+        // multiply-add, others (and scales that are not positive) take it before the mask (by
+        // selection: rows never loaded may hold anything)
+        const int key0 = (pc.t0 + j) * kKeys + kHalf * kh;
+        float mul = sc;
+        if (key0 + kHalf > lim || (bad & 0xFu) != 0 || !(sc > 0.f)) {
+          mul = 1.f;
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c)
+            x[c] = key0 + c < lim && !((bad >> (c >> 4)) & 1u) ? x[c] * sc : -CUDART_INF_F;
+        }
+        float mx[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mx[c] = x[c];
+#pragma unroll
+        for (int c = 8; c < kHalf; ++c) mx[c & 7] = fmaxf(mx[c & 7], x[c]);
+        float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * mul;
+        float *mine = red + (meets & 1) * 2 * kRows;
+        mine[kh * kRows + i] = mt;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 1)) : "memory");
+        mt = fmaxf(mt, mine[(kh ^ 1) * kRows + i]);
+        float alpha = 1.f;
+        bool rescale = false;
+        if (mt > m + kSlack) {
+          rescale = m != -CUDART_INF_F;  // with m = -inf the row's O and l are still 0
+          alpha = rescale ? ex2(m - mt) : 1.f;
+          l *= alpha;
+          m = mt;
+        }
+        const float off = m == -CUDART_INF_F ? 0.f : -m;
+        uint32_t hi[kHalf / 2], lo[kLo ? kHalf / 2 : 1];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < kHalf / 2; ++e) {
+          const float p0 = ex2(fmaf(x[2 * e], mul, off)), p1 = ex2(fmaf(x[2 * e + 1], mul, off));
+          hi[e] = pack_bf16x2(p0, p1);
+          if (kLo) {
+            lo[e] = pack_bf16x2(p0 - bf16_lo(hi[e]), p1 - bf16_hi(hi[e]));
+            s0 += p0;
+            s1 += p1;
+          } else {
+            s0 += bf16_lo(hi[e]);
+            s1 += bf16_hi(hi[e]);
+          }
+        }
+        l += s0 + s1;
+        // half kh of P is free once its values of the last tile are done
+        if (g >= 1) ok = ok && wait(L::kPvDone + kh, (g - 1) & 1);
+        unsigned char *prow = sm + L::kOffP + kh * kSlab + i * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int at = (c ^ (i & 7)) << 4;
+          *reinterpret_cast<uint4 *>(prow + at) =
+              make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+          if constexpr (kLo)
+            *reinterpret_cast<uint4 *>(prow + 2 * kSlab + at) =
+                make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          ok = ok && wait(L::kPvDone + 1, (g - 1) & 1);  // (and with the second half the first)
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < DC / 64; ++c) {
+            uint32_t o[32];
+            tc::ld32(lane_base + kOCol + 32 * c, o);
+            tc::wait_ld();
+            tc::reg_fence(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tc::st32(lane_base + kOCol + 32 * c, o);
+            tc::wait_st();
+          }
+        }
+        tc::fence_smem_for_async();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc2::arrive_pair(p_full);
       }
-      tc::fence_smem_for_async();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc2::arrive_cluster(p_full + 8 * pb);
-    }
-    // ---- the row's sum over both halves, and its columns: 128 kh + [0, 128) of every 256
-    float *sums = red + (pl.n & 1) * 2 * kRows;
-    sums[kh * kRows + i] = l;
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 1)) : "memory");
-    l = sums[i] + sums[kRows + i];
-    ok = ok && wait(L::kPvDone + (pl.n - 1) % L::kPBufs, ((pl.n - 1) / L::kPBufs) & 1);
-    if (ok) {
+      // ---- the row's sum over both halves, then its columns: 128 kh + [0, 128) of every 256
+      float *sums = red + (meets & 1) * 2 * kRows;
+      ++meets;
+      sums[kh * kRows + i] = l;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 1)) : "memory");
+      l = sums[i] + sums[kRows + i];
+      ok = ok && wait(L::kPvDone + 1, (g - 1) & 1);
       tc::fence_after_sync();
-      const bool real = col < pl.cols, empty = m == -CUDART_INF_F;
-      const float inv = empty ? 0.f : 1.f / l;
-      const uint64_t keep = make_evict_last_policy();
+      const bool empty = m == -CUDART_INF_F, final = pc.count == 1;
+      const float mul = empty ? 0.f : (final ? 1.f / l : 1.f);
+      const bool bf16_rows = final && a.out_dtype == PSKV_DTYPE_BF16;
+      const int pitch = (bf16_rows ? DC * 2 : DC * 4) + 16;
+      unsigned char *stage = sm + L::kOffK + i * pitch;
 #pragma unroll 1
       for (int c = 0; c < DC / 64; ++c) {
         uint32_t o[32];
         tc::ld32(lane_base + kOCol + 32 * c, o);
         tc::wait_ld();
         tc::reg_fence(o);
-        if (!real) continue;
         const int d = 256 * (c >> 2) + 128 * kh + 32 * (c & 3);
-        if (!a.direct) {
-          float4 *dst = reinterpret_cast<float4 *>(a.ws_o + part * DC + d);
+        float f[32];  // (a column that met no key may hold anything: zeros by selection)
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            st_keep(dst + q,
-                    make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                                __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3])),
-                    keep);
-        } else if (a.out_dtype == PSKV_DTYPE_BF16) {
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * DC + d);
+        for (int k = 0; k < 32; ++k) f[k] = empty ? 0.f : __uint_as_float(o[k]) * mul;
+        if (bf16_rows) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = empty ? 0u
-                           : pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv,
-                                         __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
-            dst[q] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4 *>(stage + 2 * d + 16 * k) =
+                make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                           pack_bf16x2(f[8 * k + 4], f[8 * k + 5]),
+                           pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
         } else {
-          float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * DC + d);
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = empty ? make_float4(0.f, 0.f, 0.f, 0.f)
-                           : make_float4(__uint_as_float(o[4 * q]) * inv,
-                                         __uint_as_float(o[4 * q + 1]) * inv,
-                                         __uint_as_float(o[4 * q + 2]) * inv,
-                                         __uint_as_float(o[4 * q + 3]) * inv);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4 *>(stage + 4 * d + 16 * k) =
+                make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
         }
       }
-      if (real && kh == 0) {
-        if (a.direct) {
-          if (empty) raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
-        } else {
-          a.ws_m[part] = empty ? -CUDART_INF_F : m * kLn2;
-          a.ws_l[part] = l;
+      if (ok && kh == 0 && col < cols) {
+        if (!final) {
+          const size_t at = (row0 + i) * a.num_splits + pc.p;
+          a.ws_m[at] = empty ? -CUDART_INF_F : m;
+          a.ws_l[at] = l;
+        } else if (empty && pc.len > 0) {
+          raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
         }
       }
+      tc::fence_smem_for_async();
+      tc::fence_before_sync();
+      asm volatile("bar.sync 3, 128;" ::: "memory");
+      const int r = 16 * w + lane;  // rows 16 w .. + 15 of the staging leave by this warp's lanes
+      if (ok && lane < 16 && pc.cb * 128 + (int)rank * kRows + r < cols) {
+        const int bytes = pitch - 16;
+        char *dst = final ? static_cast<char *>(a.out) + (row0 + r) * bytes
+                          : reinterpret_cast<char *>(a.ws_o + ((row0 + r) * a.num_splits + pc.p) * DC);
+        bulk_s2g(dst, sm + L::kOffK + r * pitch, bytes);
+        bulk_commit_and_wait_read();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + L::kOut);
     }
   }
   // every product done (both CTAs learn it; every copy has landed) before the memory is released
@@ -617,6 +804,80 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tc::fence_after_sync();
     tc2::dealloc(tmem, kTmemCols);
   }
+}
+
+// Folds the pieces of a row (those longer than one piece; the others are final):
+//   M = max m_p,  l = sum l_p 2^(m_p - M),  out = sum O_p 2^(m_p - M) / l,
+// the exact rescaling identity, in index order within each of eight interleaved
+// sums and then over these, so the result is deterministic.  A block takes 64 columns of
+// one query column's row: 16 threads across, eight pieces at a time.  Bound by the
+// partials' bytes (L2) and its three dependent loads.
+constexpr int kMergeLanes = 8;
+constexpr int kMergeThreads = 16 * kMergeLanes;
+
+template <int DC>
+__global__ void __launch_bounds__(kMergeThreads) pskv_merge_latent(const LatentAttnArgs a) {
+  __shared__ float most[kMergeThreads / 32];
+  __shared__ float4 acc_s[kMergeLanes][16];
+  __shared__ float l_s[kMergeLanes];
+  const int c = threadIdx.x & 15, s = threadIdx.x >> 4;
+  const int cols = a.num_tokens * a.num_q_heads;
+  const size_t row = blockIdx.x;
+  const int b = (int)(row / cols);
+  pdl_wait();
+  pdl_launch_dependents();
+  bool bad;
+  const int q = *a.ws_tiles, len = usable_len(a, b, &bad);
+  const int count = (tiles_of(len) + q - 1) / q;
+  if (count <= 1) return;
+  const float *m = a.ws_m + row * a.num_splits, *l = a.ws_l + row * a.num_splits;
+  const float4 *o = reinterpret_cast<const float4 *>(a.ws_o + row * a.num_splits * DC) +
+                    blockIdx.y * 16 + c;
+  float M = -CUDART_INF_F;
+  for (int p = threadIdx.x; p < count; p += kMergeThreads) M = fmaxf(M, m[p]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, most[w]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 8
+  for (int p = s; p < count; p += kMergeLanes) {
+    const float mp = m[p], lp = l[p];
+    const float4 v = __ldcs(o + (size_t)p * (DC / 4));
+    if (mp != -CUDART_INF_F) {  // an empty piece's O is never used
+      const float w = exp2f(mp - M);
+      sum = fmaf(lp, w, sum);
+      acc.x = fmaf(v.x, w, acc.x);
+      acc.y = fmaf(v.y, w, acc.y);
+      acc.z = fmaf(v.z, w, acc.z);
+      acc.w = fmaf(v.w, w, acc.w);
+    }
+  }
+  acc_s[s][c] = acc;
+  if (c == 0) l_s[s] = sum;
+  __syncthreads();
+  if (s != 0) return;
+#pragma unroll
+  for (int k = 1; k < kMergeLanes; ++k) {
+    const float4 v = acc_s[k][c];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+    sum += l_s[k];
+  }
+  const bool empty = M == -CUDART_INF_F;
+  if (empty && c == 0 && blockIdx.y == 0) raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
+  const float inv = empty ? 0.f : 1.f / sum;
+  const size_t at = row * (DC / 4) + blockIdx.y * 16 + c;
+  if (a.out_dtype == PSKV_DTYPE_BF16)
+    static_cast<uint2 *>(a.out)[at] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  else
+    static_cast<float4 *>(a.out)[at] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
 namespace {
@@ -634,17 +895,18 @@ cudaError_t launch(const LatentAttnArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const bool whole = a.page_size % kKeys == 0;
+  const bool whole = a.page_size % kHalf == 0;
   const long long cols = (long long)a.num_tokens * a.num_q_heads;
   Maps maps;
   if (!tc2::make_slab_map(&maps.q, a.q, a.batch * cols, DC + 64, kRows, L::kSlabs) ||
-      !tc2::make_slab_map(&maps.k, a.pool, a.num_pages * a.page_size, DC + 64,
-                          whole ? kHalfKeys : 16, whole ? L::kSlabs : 1) ||
-      !tc2::make_slab_map(&maps.v, a.pool, a.num_pages * a.page_size, DC + 64, whole ? kKeys : 16,
-                          whole ? 2 : 1))
+      !tc2::make_slab_map(&maps.k, a.pool, a.num_pages * a.page_size, DC + 64, whole ? kHalf : 16,
+                          whole ? L::kChunkSlabs : 1) ||
+      !tc2::make_block_map(&maps.v, a.pool, a.num_pages * a.page_size, DC + 64, DC / 256,
+                           whole ? kHalf : 16, whole ? 2 : 1, whole ? DC / 256 : 1) ||
+      !tc2::make_slab_map(&maps.ahead, a.pool, a.num_pages * a.page_size, DC + 64, kHalf, L::kSlabs))
     return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)(2 * ((cols + 127) / 128) * a.num_splits), a.batch);
-  return launch_pdl(pskv_attn_latent<DC, kLo>, grid, dim3(kThreads), L::kSmemBytes, s, a, maps);
+  return launch_pdl(pskv_attn_latent<DC, kLo>, dim3(2 * (unsigned)a.clusters), dim3(kThreads),
+                    L::kSmemBytes, s, a, maps);
 }
 
 }  // namespace
@@ -653,6 +915,13 @@ cudaError_t launch_attn_latent(const LatentAttnArgs &a, int dc, cudaStream_t s) 
   const bool lo = a.out_dtype == PSKV_DTYPE_F32;
   if (dc == 512) return lo ? launch<512, true>(a, s) : launch<512, false>(a, s);
   if (dc == 256) return lo ? launch<256, true>(a, s) : launch<256, false>(a, s);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_merge_latent(const LatentAttnArgs &a, int dc, cudaStream_t s) {
+  const dim3 grid((unsigned)(a.batch * a.num_tokens * a.num_q_heads), dc / 64);
+  if (dc == 512) return launch_pdl(pskv_merge_latent<512>, grid, dim3(kMergeThreads), 0, s, a);
+  if (dc == 256) return launch_pdl(pskv_merge_latent<256>, grid, dim3(kMergeThreads), 0, s, a);
   return cudaErrorInvalidValue;
 }
 

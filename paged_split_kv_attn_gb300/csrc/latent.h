@@ -35,20 +35,23 @@ struct LatentPrepArgs {
   int32_t *status;
 };
 
-// Absorbed attention: grid of partitions, blocks of query columns and rows.
+// Absorbed attention: pieces of rows, blocks of 128 query columns.
 struct LatentAttnArgs {
   const void *q;               // bf16 [B][T][Hq][dc + 64]
   const void *pool;            // bf16 [num_pages][page_size][dc + 64]
   const int32_t *page_tables;  // [B][table_stride]
   const int32_t *seq_lens;     // [B]
   int32_t *status;
-  float *ws_m, *ws_l, *ws_o;   // partials [B][T][Hq][P] (o: x dc) when not direct
-  void *out;                   // [B][T][Hq][dc] of out_dtype when direct
+  float *ws_m, *ws_l, *ws_o;   // partials [B][T][Hq][num_splits] (o: x dc), m in log2 units; null:
+  int32_t *ws_tiles;           //   one piece a row.  Tiles per piece, for the merge
+  void *out;                   // [B][T][Hq][dc] of out_dtype
   int out_dtype;
-  int direct;
   long long num_pages;
   int table_stride, page_size;
-  int batch, num_tokens, num_q_heads, num_splits;
+  int batch, num_tokens, num_q_heads;
+  int num_splits;              // most pieces of a row
+  int tiles_per_piece;
+  int clusters;                // CTA pairs to launch
   float scale_log2;
 };
 
@@ -82,6 +85,7 @@ struct VerifyArgs {
 
 cudaError_t launch_latent_prep(const LatentPrepArgs &a, cudaStream_t s);
 cudaError_t launch_attn_latent(const LatentAttnArgs &a, int dc, cudaStream_t s);
+cudaError_t launch_merge_latent(const LatentAttnArgs &a, int dc, cudaStream_t s);
 cudaError_t launch_attn_expanded(const ExpandedAttnArgs &a, cudaStream_t s);
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s);
 

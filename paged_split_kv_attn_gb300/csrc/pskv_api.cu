@@ -403,17 +403,14 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   const int64_t columns = (int64_t)num_tokens * num_q_heads, rows = (int64_t)batch * columns;
   if (rows > INT32_MAX) return PSKV_ERR_INVALID_ARG;
   int mgroup = 0, rc;
-  if ((rc = merge_group_of(opts, &mgroup))) return rc;
-  int P = num_splits;
-  if (P == 0) {
-    int n_sm = 0;
-    if ((rc = sm_count(&n_sm))) return rc;
-    P = plan_latent_splits(((columns + 127) / 128) * batch, n_sm / 2, (longest + 63) / 64);
-  }
-  const bool direct = P == 1;
+  if ((rc = merge_group_of(opts, &mgroup))) return rc;  // (checked; the pieces fold in one level)
+  int n_sm = 2;
+  if (num_splits == 0 && (rc = sm_count(&n_sm))) return rc;
+  const LatentPlan plan = plan_latent(n_sm / 2, batch, seq_lens_host, (columns + 127) / 128, num_splits);
+  const bool direct = plan.splits == 1;
   WorkspacePlan w;
-  if ((rc = plan_workspace(rows, 1, d.head_dim_v, P, mgroup, &w))) return rc;
-  if (w.groups > kMaxGroups) return PSKV_ERR_INVALID_ARG;
+  if ((rc = plan_workspace(rows, 1, d.head_dim_v, plan.splits, 1, &w))) return rc;
+  w.total += 256;  // the tiles per piece, for the merge
   if (plan_bytes) {
     *plan_bytes = direct ? 0 : w.total;
     return PSKV_OK;
@@ -429,16 +426,18 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   a.ws_m = direct ? nullptr : reinterpret_cast<float *>(ws + w.m_off);
   a.ws_l = direct ? nullptr : reinterpret_cast<float *>(ws + w.l_off);
   a.ws_o = direct ? nullptr : reinterpret_cast<float *>(ws + w.o_off);
+  a.ws_tiles = direct ? nullptr : reinterpret_cast<int32_t *>(ws + w.total - 256);
   a.out = out;
   a.out_dtype = out_dtype;
-  a.direct = direct ? 1 : 0;
   a.num_pages = d.num_pages;
   a.table_stride = table_stride;
   a.page_size = d.page_size;
   a.batch = batch;
   a.num_tokens = num_tokens;
   a.num_q_heads = num_q_heads;
-  a.num_splits = P;
+  a.num_splits = plan.splits;
+  a.tiles_per_piece = plan.tiles_per_piece;
+  a.clusters = plan.clusters;
   a.scale_log2 = scale * kLog2e;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -454,21 +453,10 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
     if (e != cudaSuccess) return cuda_fail(e);
   }
   if (direct) return PSKV_OK;
-  MergeArgs m;
-  m.m = a.ws_m;
-  m.l = a.ws_l;
-  m.o = a.ws_o;
-  m.rows = (int)rows;
-  m.count = P;
-  m.dv = d.head_dim_v;
-  m.group = mgroup;
-  m.out = out;
-  m.out_dtype = out_dtype;
-  m.status = nullptr;  // a padded batch's row (length 0) is no fault
-  int launched = 0;
-  e = launch_merge(m, s, &launched);
-  g_launches.fetch_add((uint64_t)launched, std::memory_order_relaxed);
-  return e == cudaSuccess ? PSKV_OK : cuda_fail(e);
+  e = launch_merge_latent(a, d.head_dim_v, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PSKV_OK;
 }
 
 }  // namespace

@@ -140,11 +140,48 @@ int plan_verify_splits(int64_t units, int slots, int64_t max_tiles) {
   return p < 1 ? 1 : (int)p;
 }
 
-int plan_latent_splits(int64_t units, int clusters, int64_t max_tiles) {
-  if (units < 1 || clusters < 1 || units >= clusters) return 1;
-  const int64_t p = clusters / units;
-  const int64_t cap = max_tiles / 2 < PSKV_AUTO_MAX_SPLITS ? max_tiles / 2 : PSKV_AUTO_MAX_SPLITS;
-  return (int)(p < cap ? p : (cap < 1 ? 1 : cap));
+LatentPlan plan_latent(int clusters, int32_t batch, const int32_t *seq_lens_host, int64_t blocks,
+                       int32_t num_splits) {
+  if (clusters < 1) clusters = 1;
+  auto tiles = [&](int32_t b) { return ((int64_t)seq_lens_host[b] + kLatentTile - 1) / kLatentTile; };
+  int64_t most = 1;
+  for (int32_t b = 0; b < batch; ++b) most = tiles(b) > most ? tiles(b) : most;
+  auto pieces = [&](int64_t q) {
+    int64_t n = 0;
+    for (int32_t b = 0; b < batch; ++b) n += tiles(b) > q ? (tiles(b) + q - 1) / q : 1;
+    return n * blocks;
+  };
+  int64_t q = most;  // one piece a row
+  if (num_splits > 0) {
+    q = (most + num_splits - 1) / num_splits;
+  } else if (most > 1) {
+    double best = (double)((pieces(most) + clusters - 1) / clusters) * (kLatentPieceTiles + most);
+    for (int64_t waves = 1; waves <= 4; ++waves) {
+      int64_t lo = 1, hi = most;  // the smallest piece that takes this many waves
+      while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (pieces(mid) <= waves * clusters)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      const int64_t cap = (most + PSKV_AUTO_MAX_SPLITS - 1) / PSKV_AUTO_MAX_SPLITS;
+      if (lo < cap) lo = cap;
+      if (lo >= most) continue;
+      const double cost = (double)((pieces(lo) + clusters - 1) / clusters) * (kLatentPieceTiles + lo) +
+                          kLatentMergeTiles;
+      if (cost < best) {
+        best = cost;
+        q = lo;
+      }
+    }
+  }
+  LatentPlan p;
+  p.tiles_per_piece = (int)q;
+  p.splits = (int)((most + q - 1) / q);
+  const int64_t n = pieces(q);
+  p.clusters = (int)(n < INT32_MAX / 2 ? n : INT32_MAX / 2);
+  return p;
 }
 
 }  // namespace pskv

@@ -58,10 +58,21 @@ int plan_tc_splits(int64_t units, int slots, int64_t max_tiles);
 // max_tiles 128-key tiles.  One wave: P = floor(slots / units), at least 1,
 // at most max_tiles / 2 (two tiles per partition) and PSKV_MAX_SPLITS.
 int plan_verify_splits(int64_t units, int slots, int64_t max_tiles);
-// Partitions per (row, block of query columns) for decode_attn_latent: `units`
-// blocks over `clusters` concurrent workers, rows of at most max_tiles 64-key
-// tiles; one wave, at least two tiles a partition.
-int plan_latent_splits(int64_t units, int clusters, int64_t max_tiles);
+// decode_attn_latent's pieces: each row's tiles of kLatentTile keys are cut into
+// pieces of tiles_per_piece, one per CTA pair (`clusters` run at a time) and block of
+// 128 query columns (`blocks` of them).  The automatic size is the one of the lowest
+// estimate among one piece a row and the smallest pieces that take one to four waves: waves
+// x (a piece's start and end, about kLatentPieceTiles tiles, + its tiles), and the
+// merge, about kLatentMergeTiles, where a row has several.  Given num_splits, the longest
+// row's tiles are cut into that many.
+constexpr int kLatentTile = 128;
+constexpr double kLatentPieceTiles = 3.0;
+constexpr double kLatentMergeTiles = 2.5;
+struct LatentPlan {
+  int tiles_per_piece, splits, clusters;  // splits: most pieces of a row
+};
+LatentPlan plan_latent(int clusters, int32_t batch, const int32_t *seq_lens_host, int64_t blocks,
+                       int32_t num_splits);
 int plan_splits(int slots, int32_t batch, int32_t num_kv_heads, const int32_t *seq_lens_host,
                 int fill32 = 32);
 

@@ -32,41 +32,12 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
-// Arrive on a barrier of any CTA of the cluster, releasing this thread's writes at cluster scope.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
-      "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait with cluster-scope acquire, one answer for the whole warp.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                          int32_t *status) {
-  bool ok = !*abort_flag;
-  if (ok && !try_wait_cluster(bar, parity)) {
-    ok = false;
-    for (uint32_t i = 0; i < kWaitPolls; ++i) {
-      if (try_wait_cluster(bar, parity)) {
-        ok = true;
-        break;
-      }
-      if (*abort_flag) break;
-    }
-    if (!ok) {
-      *abort_flag = 1;
-      raise_fault(status, PSKV_FAULT_WAIT_TIMEOUT);
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
+// Arrive on a barrier of any CTA of the cluster.  No ordinary load ever reads the other
+// CTA's memory here: what crosses is read by the tensor core, after the writer's
+// fence.proxy.async, so the arrival keeps the CTA-scope release of a local one (a cluster-scope
+// one waits for a memory barrier of ~1,000 cycles, twice a tile).
+__device__ __forceinline__ void arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // D[tmem] (+)= A * B over the pair, issued by one thread of the even CTA.
@@ -111,6 +82,21 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// The same for a 4-D map.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// Fetch a tensor map's descriptor ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // The same box into L2 only.
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
@@ -130,6 +116,22 @@ inline bool make_slab_map(CUtensorMap *m, const void *base, long long rows, int 
   const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_slabs};
   const cuuint32_t elem[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+             elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The first 256 * blocks columns of the same rows as (64, rows, 4 slabs, blocks): a box of
+// box_slabs neighbouring slabs of box_blocks blocks lands block by block.
+inline bool make_block_map(CUtensorMap *m, const void *base, long long rows, int cols, int blocks,
+                           int box_rows, int box_slabs, int box_blocks) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tc::encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {64, (cuuint64_t)rows, 4, (cuuint64_t)blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)cols * 2, 128, 512};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_slabs,
+                             (cuuint32_t)box_blocks};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -108,8 +108,8 @@ def decode_rc(lib, h, lens, **kw):
     ([100], dict(hq=0), INVALID), ([100], dict(hq=129), UNSUPPORTED),
     ([100], dict(scale=float("nan")), INVALID), ([100], dict(splits=-1), INVALID),
     ([100], dict(splits=1025), INVALID), ([100], dict(dtype=7), INVALID),
-    ([100], dict(ws=None), B.PSKV_ERR_WORKSPACE_TOO_SMALL),
-    ([100], dict(ws_bytes=1000), B.PSKV_ERR_WORKSPACE_TOO_SMALL),
+    ([200], dict(ws=None), B.PSKV_ERR_WORKSPACE_TOO_SMALL),
+    ([200], dict(ws_bytes=1000), B.PSKV_ERR_WORKSPACE_TOO_SMALL),
     ([100], dict(stride=1 << 26), INVALID),  # positions past 32 bits
     ([100], dict(batch=0), INVALID),
 ])
@@ -126,12 +126,12 @@ def test_decode_refuses_an_appending_option(lib, latent):
 
 def test_workspace_bytes(lib, latent):
     n = ctypes.c_size_t()
-    get = lambda splits, lens=(100, 0), tokens=2, hq=3: (lib.decode_attn_latent_workspace_bytes(
+    get = lambda splits, lens=(250, 0), tokens=2, hq=3: (lib.decode_attn_latent_workspace_bytes(
         latent, i32s(*lens), 4, len(lens), tokens, hq, splits, ctypes.byref(n)), n.value)
     assert get(1) == (0, 0)
     rc, size = get(4)
-    partial = pskv.pskv_partial_scratch_bytes(2 * 2, 3, 512, 4)[3]
-    assert rc == 0 and partial <= size <= partial + 3 * 256
+    partial = pskv.pskv_partial_scratch_bytes(2 * 2, 3, 512, 2)[3]  # 250 keys: two tiles of 128
+    assert rc == 0 and partial <= size <= partial + 4 * 256
     assert get(4, lens=(1,), tokens=2)[0] == INVALID
 
 
