@@ -12,10 +12,10 @@
 // which one CTA alone could not hold beside the scores (128 x 512 f32 fill its tensor
 // memory).  Per tile j of 128 keys:
 //   S = Q K^T     N = 128 keys, CTA r brings the tile's keys 64 r .. + 63
-//   softmax       thread (row i, half kh of the keys) masks its 64 scores; the two
-//                 threads of a row exchange their maxima; the reference maximum moves
-//                 only past a slack of 8 (log2 units), so O is rarely rescaled; P goes
-//                 to shared memory as bf16 (f32 output: a hi + lo pair)
+//   softmax       a row's 128 scores lie in four threads (halves by lane, halves of these by
+//                 warp group), which mask them and exchange their maxima; the reference
+//                 maximum moves only past a slack of 8 (log2 units), so O is rarely
+//                 rescaled; P goes to shared memory as bf16 (f32 output: a hi + lo pair)
 //   O += P V      per half of the keys and 256 columns: CTA r brings columns
 //                 128 r .. + 127 of them, 64 keys
 // A product of M = 128 over a pair runs at the full rate of both SMs from N = 128 on
@@ -30,11 +30,11 @@
 // on tile j.
 //
 // A row's keys are cut into pieces of `tiles_per_piece` tiles, one piece per cluster
-// (pskv_plan.cpp picks the size that fills the clusters in one wave); a row of one
-// piece is written at once, longer ones leave f32 partials (m, l, O) that
-// pskv_merge_latent folds in index order.  O leaves through the drained rings, so that
-// whole rows go out as bulk copies (16-byte stores straight from the
-// registers took 7.8 us for 64 KB a warp at 40,002 keys).
+// (pskv_plan.cpp picks the size that fills the clusters in one wave).  A row of one
+// piece is written at once; longer ones leave f32 partials (m, l, O) in groups of 32 query
+// columns, [group][piece][column / 4][32] float4, which a warp writes from its registers
+// and pskv_merge_latent reads back in whole 512-byte lines (through shared memory and
+// row-wise bulk copies the same bytes took 3 us more).
 //
 // P is rounded to bf16 when the output is (the weights' rounding then adds about
 // what the output's own does; the sum takes the rounded weights, so a lone key gives
@@ -63,7 +63,10 @@ using tc::PageCache;
 constexpr int kKeys = kLatentTile;  // keys per tile (128)
 constexpr int kHalf = kKeys / 2;   // of which each CTA brings half to the scores
 constexpr int kRows = 64;          // query columns per CTA (128 per pair)
-constexpr int kThreads = 288;      // warps: 0 S, 1 K copies, 2-5 softmax, 6 V copies, 7 PV, 8 prefetch
+// warps: 0 score products, 1 value products, 2 Q's copy and the prefetch, 3, 12 and 13 K copies,
+// 14 and 15 V copies, 4-11 softmax (two groups of four; warp w reads tensor-memory lanes 32 (w % 4) ..)
+constexpr int kThreads = 512;
+constexpr int kSoftWarps = 8;
 constexpr int kTmemCols = 512;
 constexpr int kOCol = 0;           // O: DC / 2 columns
 constexpr int kSCol = 256;         // score region r at kSCol + 64 r
@@ -104,17 +107,20 @@ struct Lay {
   static constexpr int kQFull = kInfoFull + kInfo;       // (even CTA) both CTAs' Q landed
   static constexpr int kQFree = kQFull + 1;              // the piece's score products done
   static constexpr int kOut = kQFree + 1;                // this CTA's O has left the rings
-  static constexpr int kRagged = kOut + 1;               // this CTA's V of a chunk that is not whole
-  static constexpr int kDrainS = kRagged + 1;
+  static constexpr int kRagged = kOut + 1;               // [2] this CTA's V of a chunk that is not whole
+  static constexpr int kDrainS = kRagged + 2;
   static constexpr int kDrainV = kDrainS + 1;
   static constexpr int kNumBars = kDrainV + 1;
   static constexpr int kOffInfo = (kOffBar + kNumBars * 8 + 15) & ~15;
-  static constexpr int kOffRed = kOffInfo + kInfo * 8;   // float[2][2][64] maxima (then sums)
-  static constexpr int kOffSlot = kOffRed + 2 * 2 * kRows * 4;
+  static constexpr int kOffRed = kOffInfo + kInfo * 8;   // float[2][4][64] maxima (then sums)
+  static constexpr int kOffSlot = kOffRed + 2 * 4 * kRows * 4;
   static constexpr int kOffAbort = kOffSlot + 4;
   static constexpr int kOffScored = kOffAbort + 4;       // tiles whose scores are in (paces the prefetch)
-  static constexpr int kSmemBytes = kOffScored + 4 + 1024;  // + alignment of the dynamic base
-  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static constexpr int kUsed = kOffScored + 4;
+  // + alignment of the dynamic base, as far as a CTA's limit leaves room (the base is in fact
+  // aligned; the kernel checks)
+  static constexpr int kSmemBytes = kUsed + 1024 < 232448 ? kUsed + 1024 : 232448;
+  static_assert(kUsed <= 232448, "shared memory per CTA");
   static_assert(kSlabs % kChunkSlabs == 0, "whole chunks");
   static constexpr uint32_t kIdescS = tc::instr_desc(2 * kRows, kKeys, false, false);
   static constexpr uint32_t kIdescPV = tc::instr_desc(2 * kRows, 256, false, true);
@@ -142,32 +148,43 @@ __device__ __forceinline__ int usable_len(const LatentAttnArgs &a, int b, bool *
   return (int)(len < 0 ? 0 : (len > cap ? cap : len));
 }
 
+// The rows' lengths as this lane holds them (up to 32 rows; longer batches are read again).
+struct Rows {
+  int len;  // of row `lane`, 0 past the batch
+  int q;    // tiles per piece
+};
+
 // Tiles per piece: the plan's, or more if a device length outgrew the planned ones (at
 // most num_splits pieces a row).  Every warp computes it alike.
-__device__ __forceinline__ int piece_tiles(const LatentAttnArgs &a, int lane, bool report) {
+__device__ __forceinline__ Rows read_rows(const LatentAttnArgs &a, int lane, bool report) {
   int most = 0;
   bool any_bad = false;
+  Rows r;
+  r.len = 0;
   for (int b = lane; b < a.batch; b += 32) {
     bool bad;
-    most = max(most, tiles_of(usable_len(a, b, &bad)));
+    const int len = usable_len(a, b, &bad);
+    if (b < 32) r.len = len;
+    most = max(most, tiles_of(len));
     any_bad |= bad;
   }
   if (report && any_bad) raise_fault(a.status, PSKV_FAULT_BAD_LENGTH);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  return max(max(a.tiles_per_piece, (most + a.num_splits - 1) / a.num_splits), 1);
+  most = __reduce_max_sync(0xffffffffu, most);
+  r.q = a.tiles_per_piece;
+  if ((long long)r.q * a.num_splits < most) r.q = (most + a.num_splits - 1) / a.num_splits;
+  return r;
 }
 
 // Piece u in the order (row, piece, block of columns), the last fastest; false past the end.
-__device__ __forceinline__ bool find_piece(const LatentAttnArgs &a, int u, int q, int lane,
+__device__ __forceinline__ bool find_piece(const LatentAttnArgs &a, int u, const Rows &r, int lane,
                                            Piece &pc) {
   const int blocks = (a.num_tokens * a.num_q_heads + 127) / 128;
   const int unit = blocks == 1 ? u : u / blocks;
   int base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     bool bad;
-    const int len = b0 + lane < a.batch ? usable_len(a, b0 + lane, &bad) : 0;
-    int n = b0 + lane < a.batch ? max(1, (tiles_of(len) + q - 1) / q) : 0;
+    const int len = b0 == 0 ? r.len : (b0 + lane < a.batch ? usable_len(a, b0 + lane, &bad) : 0);
+    const int n = b0 + lane < a.batch ? max(1, (tiles_of(len) + r.q - 1) / r.q) : 0;
     int incl = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -183,8 +200,8 @@ __device__ __forceinline__ bool find_piece(const LatentAttnArgs &a, int u, int q
       pc.count = __shfl_sync(0xffffffffu, n, l);
       pc.p = unit - base - __shfl_sync(0xffffffffu, incl - n, l);
       const int tiles = tiles_of(pc.len);
-      pc.t0 = min(pc.p * q, tiles);
-      pc.n = min(pc.t0 + q, tiles) - pc.t0;
+      pc.t0 = min(pc.p * r.q, tiles);
+      pc.n = min(pc.t0 + r.q, tiles) - pc.t0;
       return true;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -214,11 +231,15 @@ struct Place {
 // scores' share of each tile (keys 64 r .. + 63, all columns, in chunks of slabs) or
 // the values' (in chunks of 64 keys, all the CTA's columns).  A copy costs its issuing warp ~365
 // cycles whatever its size (measured: 8 KB a copy 23 bytes a cycle and warp, 24 KB 67; the
-// SM's own limit is 85 to 118), so chunks are single copies of 24 and 32 KB.
+// SM's own limit is 85 to 118), so chunks are single copies of 24 and 32 KB, and the
+// chunks of a ring are dealt out to several warps, each with stages of its own.
 template <int DC, bool kLo, bool kV>
 struct Loader {
   using L = Lay<DC, kLo>;
   static constexpr int kRing = kV ? L::kRingV : L::kRingK;
+  static constexpr int kWarps = kV ? 2 : L::kRingK;      // warps the chunks are dealt to
+  static constexpr int kChunks = kV ? 2 : L::kChunks;    // chunks per tile
+  static_assert(kRing % kWarps == 0, "a stage belongs to one warp");
   const LatentAttnArgs &a;
   const CUtensorMap *map;
   unsigned char *sm;
@@ -228,11 +249,12 @@ struct Loader {
   int lane;
   bool whole;  // pages of whole half tiles: boxes of 64 rows (else of 16)
   PageCache pages;
-  int seq = 0, tile = 0, ragged = 0;  // chunks, tiles, chunks landed on kRagged, over all pieces
+  int which;                 // of the kWarps
+  int seq = 0, ragged = 0;   // chunks of all warps, chunks of this one landed on kRagged, over all pieces
 
   __device__ Loader(const LatentAttnArgs &a_, const CUtensorMap *m, unsigned char *sm_,
-                    uint64_t *bars_, volatile int *ab, uint32_t rank_)
-      : a(a_), map(m), sm(sm_), bars(bars_), abort_flag(ab), rank(rank_) {
+                    uint64_t *bars_, volatile int *ab, uint32_t rank_, int which_)
+      : a(a_), map(m), sm(sm_), bars(bars_), abort_flag(ab), rank(rank_), which(which_) {
     lane = threadIdx.x & 31;
     whole = a.page_size % kHalf == 0;
   }
@@ -283,133 +305,139 @@ struct Loader {
     const int32_t *tbl = a.page_tables + (size_t)pc.b * a.table_stride;
     const int n_slots = (pc.len + a.page_size - 1) / a.page_size;
     Place at(pc.t0 * kKeys, a.page_size);
-    for (int j = 0; j < pc.n; ++j, ++tile) {
+    for (int j = 0; j < pc.n; ++j) {
       const int left = pc.len - (pc.t0 + j) * kKeys;
       int ys[8];
       const uint32_t bad = find(tbl, n_slots, left, at, ys);
       at.step(kKeys, a.page_size);
-      if (!(kV ? load_v(min(left, kKeys), ys, bad) : load_k(ys, bad))) return false;
-    }
-    return true;
-  }
-
-  __device__ bool load_k(const int (&ys)[8], uint32_t bad) {
-    // rows behind the row's end (inside a page) may come along: their scores are masked
-    uint32_t rows = 0;  // both CTAs'
-    if (whole)
-      rows = (ys[0] >= 0 ? kHalf : 0) + (ys[1] >= 0 ? kHalf : 0);
-    else
-#pragma unroll
-      for (int i = 0; i < 8; ++i) rows += ys[i] >= 0 ? 16 : 0;
 #pragma unroll 1
-    for (int c = 0; c < L::kChunks; ++c, ++seq) {
-      const int st = seq % kRing;
-      if (!free_stage(st)) return false;
-      const uint32_t dst = smem_u32(sm + L::kOffK + st * L::kKBytes);
-      const uint32_t bar = tc2::map_to(smem_u32(bars + L::kFullK + st), 0);
-      if (elect_one()) {
-        if (rank == 0) mbar_arrive_expect_tx(bars + L::kFullK + st, rows * 128 * L::kChunkSlabs);
-        if (whole) {
-          const int y = rank == 0 ? ys[0] : ys[1];
-          if (y >= 0) tc2::tma_load_3d(dst, map, 0, y, c * L::kChunkSlabs, bar);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int y = rank == 0 ? ys[i] : ys[4 + i];
-            if (y < 0) continue;
-            for (int s = 0; s < L::kChunkSlabs; ++s)
-              tc2::tma_load_3d(dst + s * kSlab + i * 16 * 128, map, 0, y, c * L::kChunkSlabs + s,
-                               bar);
-          }
-        }
-        if (c == 0) {
-          if (bad && rank == 0) raise_fault(a.status, PSKV_FAULT_BAD_PAGE);
-          reinterpret_cast<TileInfo *>(sm + L::kOffInfo)[tile % kInfo].bad = bad;
-          mbar_arrive(bars + L::kInfoFull + tile % kInfo);
-        }
-      }
-      __syncwarp();
-    }
-    return true;
-  }
-
-  __device__ bool load_v(int vhi, const int (&ys)[8], uint32_t bad) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      if (vhi <= h * kHalf) break;  // no key in this half
-      const int st = seq % kRing;
-      if (!free_stage(st)) return false;
-      ++seq;
-      unsigned char *stage = sm + L::kOffV + st * L::kVBytes;
-      const uint32_t dst = smem_u32(stage);
-      const uint32_t full = tc2::map_to(smem_u32(bars + L::kFullV + st), 0);
-      const uint32_t hbad = (bad >> (4 * h)) & 0xFu;
-      const bool plain = vhi >= (h + 1) * kHalf && hbad == 0;
-      // a chunk with rows that must not be met lands on a barrier of this CTA first
-      const uint32_t bar = plain ? full : smem_u32(bars + L::kRagged);
-      if (elect_one()) {
-        uint32_t rows = 0;
-        if (whole)
-          rows = (h == 0 ? ys[0] : ys[1]) >= 0 ? kHalf : 0;
+      for (int c = 0; c < kChunks; ++c, ++seq) {
+        if (seq % kWarps != which) continue;
+        if (!free_stage(seq % kRing)) return false;
+        if (kV)
+          load_v(c, min(left, kKeys), ys, bad);
         else
-#pragma unroll
-          for (int i = 0; i < 4; ++i) rows += (h == 0 ? ys[i] : ys[4 + i]) >= 0 ? 16 : 0;
-        const uint32_t bytes = rows * 256 * L::kBlocks;
-        if (!plain)
-          mbar_arrive_expect_tx(bars + L::kRagged, bytes);
-        else if (rank == 0)
-          mbar_arrive_expect_tx(bars + L::kFullV + st, 2 * bytes);
-        if (whole) {
-          const int y = h == 0 ? ys[0] : ys[1];
-          if (y >= 0) tc2::tma_load_4d(dst, map, 0, y, 2 * (int)rank, 0, bar);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int y = h == 0 ? ys[i] : ys[4 + i];
-            if (y < 0) continue;
-            for (int s = 0; s < 2 * L::kBlocks; ++s)
-              tc2::tma_load_4d(dst + s * kSlab + i * 16 * 128, map, 0, y, 2 * (int)rank + (s & 1),
-                               s >> 1, bar);
-          }
-        }
+          load_k(c, ys, bad);
       }
-      __syncwarp();
-      if (!plain) {
-        // rows behind the end or of skipped groups may hold anything and meet P = 0: zero them
-        mbar_wait(bars + L::kRagged, ragged & 1);  // (bounded; landed or given up on, the chunk is passed on)
-        ++ragged;
-        for (int e = lane; e < kHalf * 16 * L::kBlocks; e += 32) {
-          const int row = e & (kHalf - 1), piece = e >> 6;
-          if (row + h * kHalf >= vhi || ((hbad >> (row >> 4)) & 1u))
-            *reinterpret_cast<uint4 *>(stage + (piece >> 3) * kSlab + row * 128 + (piece & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_smem_for_async();
-        __syncwarp();
-        if (rank == 0 && lane == 0) mbar_arrive(bars + L::kFullV + st);  // in place of the copies' count
-      }
-      if (lane == 0) tc2::arrive_pair(full);
     }
     return true;
+  }
+
+  __device__ void load_k(int c, const int (&ys)[8], uint32_t bad) {
+    // rows behind the row's end (inside a page) may come along: their scores are masked
+    const int st = seq % kRing;
+    const uint32_t dst = smem_u32(sm + L::kOffK + st * L::kKBytes);
+    const uint32_t bar = tc2::map_to(smem_u32(bars + L::kFullK + st), 0);
+    if (elect_one()) {
+      uint32_t rows = 0;  // both CTAs'
+      if (whole)
+        rows = (ys[0] >= 0 ? kHalf : 0) + (ys[1] >= 0 ? kHalf : 0);
+      else
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rows += ys[i] >= 0 ? 16 : 0;
+      if (rank == 0) mbar_arrive_expect_tx(bars + L::kFullK + st, rows * 128 * L::kChunkSlabs);
+      if (whole) {
+        const int y = rank == 0 ? ys[0] : ys[1];
+        if (y >= 0) tc2::tma_load_3d(dst, map, 0, y, c * L::kChunkSlabs, bar);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int y = rank == 0 ? ys[i] : ys[4 + i];
+          if (y < 0) continue;
+          for (int s = 0; s < L::kChunkSlabs; ++s)
+            tc2::tma_load_3d(dst + s * kSlab + i * 16 * 128, map, 0, y, c * L::kChunkSlabs + s, bar);
+        }
+      }
+      if (c == 0) {
+        const int tile = seq / kChunks;
+        if (bad && rank == 0) raise_fault(a.status, PSKV_FAULT_BAD_PAGE);
+        reinterpret_cast<TileInfo *>(sm + L::kOffInfo)[tile % kInfo].bad = bad;
+        mbar_arrive(bars + L::kInfoFull + tile % kInfo);
+      }
+    }
+    __syncwarp();
+  }
+
+  __device__ void load_v(int h, int vhi, const int (&ys)[8], uint32_t bad) {
+    const int st = seq % kRing;
+    unsigned char *stage = sm + L::kOffV + st * L::kVBytes;
+    const uint32_t dst = smem_u32(stage);
+    uint64_t *own_full = bars + L::kFullV + st;
+    const uint32_t full = tc2::map_to(smem_u32(own_full), 0);
+    const uint32_t hbad = (bad >> (4 * h)) & 0xFu;
+    const bool plain = vhi >= (h + 1) * kHalf && hbad == 0;
+    // a chunk with rows that must not be met lands on a barrier of this CTA first; one
+    // without any key is passed on as it is and not met at all
+    const bool dead = vhi <= h * kHalf;
+    uint64_t *rag = bars + L::kRagged + which;
+    const uint32_t bar = plain ? full : smem_u32(rag);
+    if (!dead && elect_one()) {
+      uint32_t rows = 0;
+      if (whole)
+        rows = (h == 0 ? ys[0] : ys[1]) >= 0 ? kHalf : 0;
+      else
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows += (h == 0 ? ys[i] : ys[4 + i]) >= 0 ? 16 : 0;
+      const uint32_t bytes = rows * 256 * L::kBlocks;
+      if (!plain)
+        mbar_arrive_expect_tx(rag, bytes);
+      else if (rank == 0)
+        mbar_arrive_expect_tx(own_full, 2 * bytes);
+      if (whole) {
+        const int y = h == 0 ? ys[0] : ys[1];
+        if (y >= 0) tc2::tma_load_4d(dst, map, 0, y, 2 * (int)rank, 0, bar);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int y = h == 0 ? ys[i] : ys[4 + i];
+          if (y < 0) continue;
+          for (int s = 0; s < 2 * L::kBlocks; ++s)
+            tc2::tma_load_4d(dst + s * kSlab + i * 16 * 128, map, 0, y, 2 * (int)rank + (s & 1),
+                             s >> 1, bar);
+        }
+      }
+    }
+    __syncwarp();
+    if (!plain && !dead) {
+      // rows behind the end or of skipped groups may hold anything and meet P = 0: zero them
+      mbar_wait(rag, ragged & 1);  // (bounded; landed or given up on, the chunk is passed on)
+      ++ragged;
+      for (int e = lane; e < kHalf * 16 * L::kBlocks; e += 32) {
+        const int row = e & (kHalf - 1), piece = e >> 6;
+        if (row + h * kHalf >= vhi || ((hbad >> (row >> 4)) & 1u))
+          *reinterpret_cast<uint4 *>(stage + (piece >> 3) * kSlab + row * 128 + (piece & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+      }
+      tc::fence_smem_for_async();
+      __syncwarp();
+    }
+    if (lane == 0) {
+      if (!plain && rank == 0) mbar_arrive(own_full);  // in place of the copies' count
+      tc2::arrive_pair(full);
+    }
   }
 
   // Wait (bounded) for the last copies into each stage, of both CTAs (their count is the even CTA's).
   __device__ void drain() {
     if (rank != 0) return;
     for (int s = max(0, seq - kRing); s < seq; ++s)
-      mbar_wait(bars + (kV ? L::kFullV : L::kFullK) + s % kRing, (s / kRing) & 1);
+      if (s % kWarps == which) mbar_wait(bars + (kV ? L::kFullV : L::kFullK) + s % kRing, (s / kRing) & 1);
+  }
+
+  // All of the cluster's pieces.
+  __device__ void run_all(const Rows &rows, int first, int step) {
+    int k = 0;
+    Piece pc;
+    for (int u = first; find_piece(a, u, rows, lane, pc); u += step) {
+      if (pc.n == 0) continue;
+      // the last piece's O may be leaving through the rings
+      if (k > 0 && !tc::warp_wait(bars + L::kOut, (k - 1) & 1, abort_flag, a.status)) break;
+      ++k;
+      if (!run(pc)) break;
+    }
+    drain();
   }
 };
-
-// Bulk copy shared -> global (16-byte aligned, bytes a multiple of 16), tracked by this thread's group.
-__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-               "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit_and_wait_read() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
-}
 
 }  // namespace
 
@@ -426,6 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   volatile int *scored = reinterpret_cast<volatile int *>(sm + L::kOffScored);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc2::cluster_rank();
+  if (sm + L::kUsed > smem_raw + L::kSmemBytes) {  // (never seen) no room for the alignment
+    raise_fault(a.status, PSKV_FAULT_WAIT_TIMEOUT);
+    return;
+  }
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   // set up before the previous kernel's results are waited for
@@ -443,15 +475,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
       for (int r = 0; r < 2; ++r) {
         mbar_init(&bars[L::kSFull + r], 1);
-        mbar_init(&bars[L::kSFree + r], 8);  // four softmax warps in each CTA
+        mbar_init(&bars[L::kSFree + r], 2 * kSoftWarps);  // the softmax warps of both CTAs
+        mbar_init(&bars[L::kRagged + r], 1);
         mbar_init(&bars[L::kPvDone + r], 1);
       }
-      mbar_init(&bars[L::kPFull], 8);
+      mbar_init(&bars[L::kPFull], 2 * kSoftWarps);
       for (int k = 0; k < kInfo; ++k) mbar_init(&bars[L::kInfoFull + k], 1);
       mbar_init(&bars[L::kQFull], 1);
       mbar_init(&bars[L::kQFree], 1);
-      mbar_init(&bars[L::kOut], 4);
-      mbar_init(&bars[L::kRagged], 1);
+      mbar_init(&bars[L::kOut], kSoftWarps);
       mbar_init(&bars[L::kDrainS], 1);
       mbar_init(&bars[L::kDrainV], 1);
       *abort_flag = 0;
@@ -461,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
   } else if (warp == 0) {
     tc2::alloc(slot, kTmemCols);
-  } else if (warp == 6 && lane == 0) {
+  } else if (warp == 14 && lane == 0) {
     tc2::prefetch_map(&maps.v);
   }
   tc::fence_before_sync();
@@ -474,15 +506,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   };
   pdl_wait();
   pdl_launch_dependents();
-  const int q = piece_tiles(a, lane, blockIdx.x == 0 && warp == 0);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && a.ws_tiles) *a.ws_tiles = q;  // for the merge
+  const Rows rows = read_rows(a, lane, blockIdx.x == 0 && warp == 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.ws_tiles) *a.ws_tiles = rows.q;  // for the merge
   Piece pc;
 
   if (warp == 0 && rank == 0) {
     // ---- the score products
     bool ok = true;
     int seq = 0, g = 0, k = 0;  // chunks, tiles, pieces so far
-    for (int u = first; ok && find_piece(a, u, q, lane, pc); u += step) {
+    for (int u = first; ok && find_piece(a, u, rows, lane, pc); u += step) {
       if (pc.n == 0) continue;
       ok = wait(L::kQFull, k & 1);
       ++k;
@@ -516,77 +548,60 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     if (elect_one()) tc2::commit_both(bars + L::kDrainS);
     __syncwarp();
-  } else if (warp == 7 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---- the value products
     bool ok = true;
     int seq = 0, g = 0;
-    for (int u = first; ok && find_piece(a, u, q, lane, pc); u += step)
+    for (int u = first; ok && find_piece(a, u, rows, lane, pc); u += step)
       for (int j = 0; ok && j < pc.n; ++j, ++g) {
-        const int halves = pc.len - (pc.t0 + j) * kKeys > kHalf ? 2 : 1;
+        const bool both = pc.len - (pc.t0 + j) * kKeys > kHalf;  // keys in the second half
         ok = wait(L::kPFull, g & 1);
         const uint32_t p0 = smem_u32(sm + L::kOffP);
 #pragma unroll 1
-        for (int h = 0; ok && h < halves; ++h, ++seq) {
+        for (int h = 0; ok && h < 2; ++h, ++seq) {
           const int st = seq % L::kRingV;
           ok = wait(L::kFullV + st, (seq / L::kRingV) & 1);
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t v0 = smem_u32(sm + L::kOffV + st * L::kVBytes);
           if (elect_one()) {
+            if (h == 0 || both)
 #pragma unroll
-            for (int nb = 0; nb < L::kBlocks; ++nb)
+              for (int nb = 0; nb < L::kBlocks; ++nb)
 #pragma unroll
-              for (int part = 0; part < (kLo ? 2 : 1); ++part)
+                for (int part = 0; part < (kLo ? 2 : 1); ++part)
 #pragma unroll
-                for (int kk = 0; kk < kHalf / 16; ++kk)
-                  tc2::mma(tmem + kOCol + 128 * nb,
-                           tc::smem_desc(p0 + (2 * part + h) * kSlab + kk * 32, 16, 1024),
-                           tc::smem_desc(v0 + 2 * nb * kSlab + kk * 2048, kSlab, 1024),
-                           L::kIdescPV, j > 0 || h > 0 || part > 0 || kk > 0);
+                  for (int kk = 0; kk < kHalf / 16; ++kk)
+                    tc2::mma(tmem + kOCol + 128 * nb,
+                             tc::smem_desc(p0 + (2 * part + h) * kSlab + kk * 32, 16, 1024),
+                             tc::smem_desc(v0 + 2 * nb * kSlab + kk * 2048, kSlab, 1024),
+                             L::kIdescPV, j > 0 || h > 0 || part > 0 || kk > 0);
             tc2::commit_both(bars + L::kEmptyV + st);
             tc2::commit_both(bars + L::kPvDone + h);
-            if (halves == 1) tc2::commit_both(bars + L::kPvDone + 1);  // a half without keys
           }
           __syncwarp();
         }
       }
     if (elect_one()) tc2::commit_both(bars + L::kDrainV);
     __syncwarp();
-  } else if (warp == 1) {
-    Loader<DC, kLo, false> ld(a, &maps.k, sm, bars, abort_flag, rank);
-    int k = 0;
-    for (int u = first; find_piece(a, u, q, lane, pc); u += step) {
+  } else if (warp == 2) {
+    // ---- Q of every piece (this CTA's 64 columns; behind the row's last column: other rows' or
+    // zeros), and this CTA's share of the scores' tiles into L2, kAhead tiles before their scores
+    PageCache pages;
+    int g = 0, k = 0;
+    const int cols = a.num_tokens * a.num_q_heads;
+    for (int u = first; find_piece(a, u, rows, lane, pc); u += step) {
       if (pc.n == 0) continue;
-      // Q once the last piece's scores are done, K once its O has left the rings
-      if (k > 0 && (!wait(L::kQFree, (k - 1) & 1) || !wait(L::kOut, (k - 1) & 1))) break;
+      if (k > 0 && !wait(L::kQFree, (k - 1) & 1)) break;
       if (elect_one()) {
-        // this CTA's 64 columns (behind the row's last column: other rows' or zeros)
         if (rank == 0) mbar_arrive_expect_tx(bars + L::kQFull, 2 * L::kQBytes);
         tc2::tma_load_3d(smem_u32(sm + L::kOffQ), &maps.q, 0,
-                         pc.b * (a.num_tokens * a.num_q_heads) + pc.cb * 128 + (int)rank * kRows, 0,
+                         pc.b * cols + pc.cb * 128 + (int)rank * kRows, 0,
                          tc2::map_to(smem_u32(bars + L::kQFull), 0));
       }
       __syncwarp();
       ++k;
-      if (!ld.run(pc)) break;
-    }
-    ld.drain();
-    if (rank == 0 && k > 0) mbar_wait(bars + L::kQFull, (k - 1) & 1);
-  } else if (warp == 6) {
-    Loader<DC, kLo, true> ld(a, &maps.v, sm, bars, abort_flag, rank);
-    int k = 0;
-    for (int u = first; find_piece(a, u, q, lane, pc); u += step) {
-      if (pc.n == 0) continue;
-      if (k > 0 && !wait(L::kOut, (k - 1) & 1)) break;
-      ++k;
-      if (!ld.run(pc)) break;
-    }
-    ld.drain();
-  } else if (warp == 8) {
-    // ---- this CTA's share of the scores' tiles into L2, kAhead tiles before their scores
-    PageCache pages;
-    int g = 0;
-    for (int u = first; a.page_size % kHalf == 0 && find_piece(a, u, q, lane, pc); u += step) {
+      if (a.page_size % kHalf != 0) continue;
       pages.base = -1;
       const int n_slots = (pc.len + a.page_size - 1) / a.page_size;
       int key = pc.t0 * kKeys + kHalf * (int)rank;
@@ -603,11 +618,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         at.step(kKeys, a.page_size);
       }
     }
-  } else if (warp >= 2 && warp <= 5) {
-    // ---- the softmax: thread (row i, keys 64 kh .. + 63 of the tile).  The loops never
-    // leave early (the two warps of a row's halves meet every tile); after a failed wait
+    if (rank == 0 && k > 0) mbar_wait(bars + L::kQFull, (k - 1) & 1);
+  } else if (warp == 3 || warp == 12 || warp == 13) {
+    const int which = warp == 3 ? 0 : warp - 11;
+    if (which < L::kRingK)
+      Loader<DC, kLo, false>(a, &maps.k, sm, bars, abort_flag, rank, which).run_all(rows, first, step);
+  } else if (warp >= 14) {
+    Loader<DC, kLo, true>(a, &maps.v, sm, bars, abort_flag, rank, warp - 14).run_all(rows, first, step);
+  } else if (warp >= 4 && warp <= 11) {
+    // ---- the softmax: thread (row i, keys 64 kh + 32 gr .. + 31 of the tile).  The loops never
+    // leave early (the four warps of a row's threads meet every tile); after a failed wait
     // results are not written.
-    const int w = warp & 3, i = (32 * w + lane) & (kRows - 1), kh = w >> 1;
+    const int w = warp & 3, gr = (warp - 4) >> 2, i = (32 * w + lane) & (kRows - 1), kh = w >> 1;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
     float *red = reinterpret_cast<float *>(sm + L::kOffRed);
     const TileInfo *info = reinterpret_cast<const TileInfo *>(sm + L::kOffInfo);
@@ -616,65 +638,56 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t p_full = tc2::map_to(smem_u32(bars + L::kPFull), 0);
     const int cols = a.num_tokens * a.num_q_heads;
     bool ok = true;
-    int g = 0;  // tiles so far
-    int meets = 0;
-    for (int u = first; find_piece(a, u, q, lane, pc); u += step) {
-      const int col = pc.cb * 128 + (int)rank * kRows + i;
-      const int lim =  // keys below lim are seen
-          col < cols ? pc.len - a.num_tokens + col / a.num_q_heads + 1 : 0;
-      const size_t row0 = (size_t)pc.b * cols + pc.cb * 128 + rank * kRows;
+    int g = 0;      // tiles so far
+    int meets = 0;  // meetings so far: their buffers alternate
+    for (int u = first; find_piece(a, u, rows, lane, pc); u += step) {
+      const int col0 = pc.cb * 128 + (int)rank * kRows, col = col0 + i;
+      const size_t row0 = (size_t)pc.b * cols + col0;
       if (pc.n == 0) {  // a row without keys (of one piece): zeros
         if (col >= cols) continue;
         const int es = a.out_dtype == PSKV_DTYPE_BF16 ? 2 : 4;
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + (row0 + i) * DC * es);
-        for (int e = kh; e < DC * es / 16; e += 2) dst[e] = make_uint4(0, 0, 0, 0);
+        for (int e = 2 * gr + kh; e < DC * es / 16; e += 4) dst[e] = make_uint4(0, 0, 0, 0);
         continue;
       }
+      const int lim =  // keys below lim are seen
+          col < cols ? pc.len - a.num_tokens + col / a.num_q_heads + 1 : 0;
       float m = -CUDART_INF_F, l = 0.f;
       for (int j = 0; j < pc.n; ++j, ++g, ++meets) {
         const int r = g & 1;
         ok = ok && wait(L::kSFull + r, (g >> 1) & 1);
         ok = ok && wait(L::kInfoFull + g % kInfo, (g / kInfo) & 1);
-        const uint32_t bad = info[g % kInfo].bad >> (4 * kh);
+        const uint32_t bad = (info[g % kInfo].bad >> (4 * kh + 2 * gr)) & 3u;
         tc::fence_after_sync();
-        uint32_t va[32], vb[32];
-        tc::ld32(lane_base + kSCol + kHalf * r, va);
-        tc::ld32(lane_base + kSCol + kHalf * r + 32, vb);
+        uint32_t v[32];
+        tc::ld32(lane_base + kSCol + kHalf * r + 32 * gr, v);
         tc::wait_ld();
-        tc::reg_fence(va);
-        tc::reg_fence(vb);
+        tc::reg_fence(v);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc2::arrive_pair(s_free + 8 * r);
-        if (lane == 0 && w == 0) *scored = g + 1;
-        float x[kHalf];
+        if (threadIdx.x == 128) *scored = g + 1;
+        float x[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          x[c] = __uint_as_float(va[c]);
-          x[32 + c] = __uint_as_float(vb[c]);
-        }
+        for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]);
         // scores in log2 units are mul * x: whole tiles leave the product to the exponent's
         // multiply-add, others (and scales that are not positive) take it before the mask (by
         // selection: rows never loaded may hold anything)
-        const int key0 = (pc.t0 + j) * kKeys + kHalf * kh;
+        const int key0 = (pc.t0 + j) * kKeys + kHalf * kh + 32 * gr;
         float mul = sc;
-        if (key0 + kHalf > lim || (bad & 0xFu) != 0 || !(sc > 0.f)) {
+        if (key0 + 32 > lim || bad != 0 || !(sc > 0.f)) {
           mul = 1.f;
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c)
+          for (int c = 0; c < 32; ++c)
             x[c] = key0 + c < lim && !((bad >> (c >> 4)) & 1u) ? x[c] * sc : -CUDART_INF_F;
         }
-        float mx[8];
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 0; c < 8; ++c) mx[c] = x[c];
-#pragma unroll
-        for (int c = 8; c < kHalf; ++c) mx[c & 7] = fmaxf(mx[c & 7], x[c]);
-        float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * mul;
-        float *mine = red + (meets & 1) * 2 * kRows;
-        mine[kh * kRows + i] = mt;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 1)) : "memory");
-        mt = fmaxf(mt, mine[(kh ^ 1) * kRows + i]);
+        for (int c = 4; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+        float *mine = red + (meets & 1) * 4 * kRows + i;
+        mine[(2 * kh + gr) * kRows] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + (w & 1)) : "memory");
+        const float mt = fmaxf(fmaxf(mine[0], mine[kRows]), fmaxf(mine[2 * kRows], mine[3 * kRows]));
         float alpha = 1.f;
         bool rescale = false;
         if (mt > m + kSlack) {
@@ -684,10 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           m = mt;
         }
         const float off = m == -CUDART_INF_F ? 0.f : -m;
-        uint32_t hi[kHalf / 2], lo[kLo ? kHalf / 2 : 1];
+        uint32_t hi[16], lo[kLo ? 16 : 1];
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int e = 0; e < kHalf / 2; ++e) {
+        for (int e = 0; e < 16; ++e) {
           const float p0 = ex2(fmaf(x[2 * e], mul, off)), p1 = ex2(fmaf(x[2 * e + 1], mul, off));
           hi[e] = pack_bf16x2(p0, p1);
           if (kLo) {
@@ -704,8 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (g >= 1) ok = ok && wait(L::kPvDone + kh, (g - 1) & 1);
         unsigned char *prow = sm + L::kOffP + kh * kSlab + i * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int at = (c ^ (i & 7)) << 4;
+        for (int c = 0; c < 4; ++c) {
+          const int at = ((4 * gr + c) ^ (i & 7)) << 4;
           *reinterpret_cast<uint4 *>(prow + at) =
               make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
           if constexpr (kLo)
@@ -716,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           ok = ok && wait(L::kPvDone + 1, (g - 1) & 1);  // (and with the second half the first)
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int c = 0; c < DC / 64; ++c) {
+          for (int c = gr * (DC / 128); c < (gr + 1) * (DC / 128); ++c) {
             uint32_t o[32];
             tc::ld32(lane_base + kOCol + 32 * c, o);
             tc::wait_ld();
@@ -732,70 +745,90 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
         if (lane == 0) tc2::arrive_pair(p_full);
       }
-      // ---- the row's sum over both halves, then its columns: 128 kh + [0, 128) of every 256
-      float *sums = red + (meets & 1) * 2 * kRows;
+      // ---- the row's sum over its four threads, then its columns: this thread's are
+      // 128 kh + [0, 128) of one 256 (DC = 256: half of them)
+      float *sums = red + (meets & 1) * 4 * kRows + i;
       ++meets;
-      sums[kh * kRows + i] = l;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 1)) : "memory");
-      l = sums[i] + sums[kRows + i];
+      sums[(2 * kh + gr) * kRows] = l;
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + (w & 1)) : "memory");
+      l = (sums[0] + sums[kRows]) + (sums[2 * kRows] + sums[3 * kRows]);
       ok = ok && wait(L::kPvDone + 1, (g - 1) & 1);
       tc::fence_after_sync();
-      const bool empty = m == -CUDART_INF_F, final = pc.count == 1;
-      const float mul = empty ? 0.f : (final ? 1.f / l : 1.f);
-      const bool bf16_rows = final && a.out_dtype == PSKV_DTYPE_BF16;
-      const int pitch = (bf16_rows ? DC * 2 : DC * 4) + 16;
-      unsigned char *stage = sm + L::kOffK + i * pitch;
+      const bool empty = m == -CUDART_INF_F;
+      if (pc.count > 1) {
+        // a partial: [column / 4][32 query columns] of this warp's group of 32
+        const int groups = (cols + 31) / 32, group = col0 / 32 + (w & 1);
+        if (ok && group < groups) {
+          const size_t at = ((size_t)pc.b * groups + group) * a.num_splits + pc.p;
+          const uint64_t keep = make_evict_last_policy();
+          float4 *dst = reinterpret_cast<float4 *>(a.ws_o) + at * (DC / 4 * 32) + lane;
+#pragma unroll 2
+          for (int c = gr * (DC / 128); c < (gr + 1) * (DC / 128); ++c) {
+            uint32_t o[32];
+            tc::ld32(lane_base + kOCol + 32 * c, o);
+            tc::wait_ld();
+            tc::reg_fence(o);
+            const int d4 = 64 * (c >> 2) + 32 * kh + 8 * (c & 3);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              st_keep(dst + (d4 + k) * 32,
+                      make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                  __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])),
+                      keep);
+          }
+          if (kh == 0 && gr == 0) {
+            a.ws_m[at * 32 + lane] = m;
+            a.ws_l[at * 32 + lane] = l;
+          }
+        }
+      } else {
+        // final rows, put together in the drained rings so that they leave in whole lines
+        const float mul = empty ? 0.f : 1.f / l;
+        const bool bf16_rows = a.out_dtype == PSKV_DTYPE_BF16;
+        const int bytes = bf16_rows ? DC * 2 : DC * 4, pitch = bytes + 16;
+        unsigned char *stage = sm + L::kOffK;
 #pragma unroll 1
-      for (int c = 0; c < DC / 64; ++c) {
-        uint32_t o[32];
-        tc::ld32(lane_base + kOCol + 32 * c, o);
-        tc::wait_ld();
-        tc::reg_fence(o);
-        const int d = 256 * (c >> 2) + 128 * kh + 32 * (c & 3);
-        float f[32];  // (a column that met no key may hold anything: zeros by selection)
+        for (int c = gr * (DC / 128); c < (gr + 1) * (DC / 128); ++c) {
+          uint32_t o[32];
+          tc::ld32(lane_base + kOCol + 32 * c, o);
+          tc::wait_ld();
+          tc::reg_fence(o);
+          const int d = 256 * (c >> 2) + 128 * kh + 32 * (c & 3);
+          float f[32];  // (a column that met no key may hold anything: zeros by selection)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) f[k] = empty ? 0.f : __uint_as_float(o[k]) * mul;
-        if (bf16_rows) {
+          for (int k = 0; k < 32; ++k) f[k] = empty ? 0.f : __uint_as_float(o[k]) * mul;
+          if (bf16_rows) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4 *>(stage + 2 * d + 16 * k) =
-                make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
-                           pack_bf16x2(f[8 * k + 4], f[8 * k + 5]),
-                           pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
-        } else {
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4 *>(stage + i * pitch + 2 * d + 16 * k) =
+                  make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]),
+                             pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                             pack_bf16x2(f[8 * k + 4], f[8 * k + 5]),
+                             pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
+          } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<float4 *>(stage + 4 * d + 16 * k) =
-                make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4 *>(stage + i * pitch + 4 * d + 16 * k) =
+                  make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+          }
         }
+        if (ok && empty && col < cols && kh == 0 && gr == 0) raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        if (ok)
+          for (int r = warp - 4; r < kRows && col0 + r < cols; r += kSoftWarps)
+            for (int e = 16 * lane; e < bytes; e += 512)
+              *reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + (row0 + r) * bytes + e) =
+                  *reinterpret_cast<const uint4 *>(stage + r * pitch + e);
+        tc::fence_smem_for_async();  // these accesses before the next piece's copies
       }
-      if (ok && kh == 0 && col < cols) {
-        if (!final) {
-          const size_t at = (row0 + i) * a.num_splits + pc.p;
-          a.ws_m[at] = empty ? -CUDART_INF_F : m;
-          a.ws_l[at] = l;
-        } else if (empty && pc.len > 0) {
-          raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
-        }
-      }
-      tc::fence_smem_for_async();
       tc::fence_before_sync();
-      asm volatile("bar.sync 3, 128;" ::: "memory");
-      const int r = 16 * w + lane;  // rows 16 w .. + 15 of the staging leave by this warp's lanes
-      if (ok && lane < 16 && pc.cb * 128 + (int)rank * kRows + r < cols) {
-        const int bytes = pitch - 16;
-        char *dst = final ? static_cast<char *>(a.out) + (row0 + r) * bytes
-                          : reinterpret_cast<char *>(a.ws_o + ((row0 + r) * a.num_splits + pc.p) * DC);
-        bulk_s2g(dst, sm + L::kOffK + r * pitch, bytes);
-        bulk_commit_and_wait_read();
-      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + L::kOut);
     }
   }
   // every product done (both CTAs learn it; every copy has landed) before the memory is released
   if (warp == 0) mbar_wait(bars + L::kDrainS, 0);
-  if (warp == 7) mbar_wait(bars + L::kDrainV, 0);
+  if (warp == 1) mbar_wait(bars + L::kDrainV, 0);
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
@@ -808,76 +841,99 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
 // Folds the pieces of a row (those longer than one piece; the others are final):
 //   M = max m_p,  l = sum l_p 2^(m_p - M),  out = sum O_p 2^(m_p - M) / l,
-// the exact rescaling identity, in index order within each of eight interleaved
-// sums and then over these, so the result is deterministic.  A block takes 64 columns of
-// one query column's row: 16 threads across, eight pieces at a time.  Bound by the
-// partials' bytes (L2) and its three dependent loads.
-constexpr int kMergeLanes = 8;
-constexpr int kMergeThreads = 16 * kMergeLanes;
-
-template <int DC>
-__global__ void __launch_bounds__(kMergeThreads) pskv_merge_latent(const LatentAttnArgs a) {
-  __shared__ float most[kMergeThreads / 32];
-  __shared__ float4 acc_s[kMergeLanes][16];
-  __shared__ float l_s[kMergeLanes];
-  const int c = threadIdx.x & 15, s = threadIdx.x >> 4;
-  const int cols = a.num_tokens * a.num_q_heads;
-  const size_t row = blockIdx.x;
-  const int b = (int)(row / cols);
+// the exact rescaling identity, in index order within each of kLanes interleaved
+// states and then over these, so the result is deterministic.  A block takes a group of 32 query
+// columns and 16 of their output columns: a warp reads four output columns of all 32 as one
+// 512-byte line.  Bound by the partials' bytes (L2) and its three dependent loads.
+template <int DC, int kLanes>
+__global__ void __launch_bounds__(128 * kLanes) pskv_merge_latent(const LatentAttnArgs a) {
+  __shared__ float m_s[kLanes][32], l_s[kLanes][32];
+  __shared__ float4 o_s[kLanes][4][32];
+  const int i = threadIdx.x & 31, f = (threadIdx.x >> 5) & 3, s = threadIdx.x >> 7;
+  const int cols = a.num_tokens * a.num_q_heads, groups = (cols + 31) / 32;
+  const int b = blockIdx.x / groups, group = blockIdx.x - b * groups;
   pdl_wait();
   pdl_launch_dependents();
   bool bad;
   const int q = *a.ws_tiles, len = usable_len(a, b, &bad);
   const int count = (tiles_of(len) + q - 1) / q;
   if (count <= 1) return;
-  const float *m = a.ws_m + row * a.num_splits, *l = a.ws_l + row * a.num_splits;
-  const float4 *o = reinterpret_cast<const float4 *>(a.ws_o + row * a.num_splits * DC) +
-                    blockIdx.y * 16 + c;
-  float M = -CUDART_INF_F;
-  for (int p = threadIdx.x; p < count; p += kMergeThreads) M = fmaxf(M, m[p]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, most[w]);
+  const size_t at = (size_t)blockIdx.x * a.num_splits;
+  const float *m = a.ws_m + at * 32 + i, *l = a.ws_l + at * 32 + i;
+  const float4 *o = reinterpret_cast<const float4 *>(a.ws_o) +
+                    (at * (DC / 4) + blockIdx.y * 4 + f) * 32 + i;
+  constexpr int kMany = kLanes == 8 ? 5 : 8;  // pieces a lane loads at once (registers)
+  float M = -CUDART_INF_F, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 8
-  for (int p = s; p < count; p += kMergeLanes) {
-    const float mp = m[p], lp = l[p];
-    const float4 v = __ldcs(o + (size_t)p * (DC / 4));
-    if (mp != -CUDART_INF_F) {  // an empty piece's O is never used
-      const float w = exp2f(mp - M);
-      sum = fmaf(lp, w, sum);
+  for (int p0 = s; p0 < count; p0 += kMany * kLanes) {
+    float mp[kMany], lp[kMany];
+    float4 v[kMany];
+#pragma unroll
+    for (int k = 0; k < kMany; ++k) {
+      const int p = p0 + k * kLanes;
+      mp[k] = -CUDART_INF_F;
+      if (p < count) {
+        mp[k] = m[p * 32];
+        lp[k] = l[p * 32];
+        v[k] = __ldcs(o + (size_t)p * (DC / 4 * 32));
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kMany; ++k) top = fmaxf(top, mp[k]);
+    if (top == -CUDART_INF_F) continue;
+    const float w0 = exp2f(M - top);
+    L *= w0;
+    acc.x *= w0;
+    acc.y *= w0;
+    acc.z *= w0;
+    acc.w *= w0;
+    M = top;
+#pragma unroll
+    for (int k = 0; k < kMany; ++k)
+      if (mp[k] != -CUDART_INF_F) {  // an empty piece's O is never used
+        const float w = exp2f(mp[k] - top);
+        L = fmaf(lp[k], w, L);
+        acc.x = fmaf(v[k].x, w, acc.x);
+        acc.y = fmaf(v[k].y, w, acc.y);
+        acc.z = fmaf(v[k].z, w, acc.z);
+        acc.w = fmaf(v[k].w, w, acc.w);
+      }
+  }
+  o_s[s][f][i] = acc;
+  if (f == 0) {
+    m_s[s][i] = M;
+    l_s[s][i] = L;
+  }
+  __syncthreads();
+  // thread (column i, four output columns f): 32 bytes of a row from four neighbouring threads
+  if (threadIdx.x >= 128) return;
+  const int r = threadIdx.x >> 2, k4 = threadIdx.x & 3, col = group * 32 + r;
+  if (col >= cols) return;
+  float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kLanes; ++k) top = fmaxf(top, m_s[k][r]);
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kLanes; ++k)
+    if (m_s[k][r] != -CUDART_INF_F) {
+      const float w = exp2f(m_s[k][r] - top);
+      const float4 v = o_s[k][k4][r];
+      sum = fmaf(l_s[k][r], w, sum);
       acc.x = fmaf(v.x, w, acc.x);
       acc.y = fmaf(v.y, w, acc.y);
       acc.z = fmaf(v.z, w, acc.z);
       acc.w = fmaf(v.w, w, acc.w);
     }
-  }
-  acc_s[s][c] = acc;
-  if (c == 0) l_s[s] = sum;
-  __syncthreads();
-  if (s != 0) return;
-#pragma unroll
-  for (int k = 1; k < kMergeLanes; ++k) {
-    const float4 v = acc_s[k][c];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-    sum += l_s[k];
-  }
-  const bool empty = M == -CUDART_INF_F;
-  if (empty && c == 0 && blockIdx.y == 0) raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
+  const bool empty = top == -CUDART_INF_F;
+  if (empty && k4 == 0 && blockIdx.y == 0) raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
   const float inv = empty ? 0.f : 1.f / sum;
-  const size_t at = row * (DC / 4) + blockIdx.y * 16 + c;
+  const size_t dst = ((size_t)b * cols + col) * (DC / 4) + blockIdx.y * 4 + k4;
   if (a.out_dtype == PSKV_DTYPE_BF16)
-    static_cast<uint2 *>(a.out)[at] =
+    static_cast<uint2 *>(a.out)[dst] =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   else
-    static_cast<float4 *>(a.out)[at] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    static_cast<float4 *>(a.out)[dst] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
 namespace {
@@ -919,9 +975,16 @@ cudaError_t launch_attn_latent(const LatentAttnArgs &a, int dc, cudaStream_t s) 
 }
 
 cudaError_t launch_merge_latent(const LatentAttnArgs &a, int dc, cudaStream_t s) {
-  const dim3 grid((unsigned)(a.batch * a.num_tokens * a.num_q_heads), dc / 64);
-  if (dc == 512) return launch_pdl(pskv_merge_latent<512>, grid, dim3(kMergeThreads), 0, s, a);
-  if (dc == 256) return launch_pdl(pskv_merge_latent<256>, grid, dim3(kMergeThreads), 0, s, a);
+  const int groups = (a.num_tokens * a.num_q_heads + 31) / 32;
+  const dim3 grid((unsigned)(a.batch * groups), dc / 16);
+  // eight states a block for many pieces (a lane then loads its share at once), two for few
+  const bool many = a.num_splits > 16;
+  if (dc == 512)
+    return many ? launch_pdl(pskv_merge_latent<512, 8>, grid, dim3(1024), 0, s, a)
+                : launch_pdl(pskv_merge_latent<512, 2>, grid, dim3(256), 0, s, a);
+  if (dc == 256)
+    return many ? launch_pdl(pskv_merge_latent<256, 8>, grid, dim3(1024), 0, s, a)
+                : launch_pdl(pskv_merge_latent<256, 2>, grid, dim3(256), 0, s, a);
   return cudaErrorInvalidValue;
 }
 

@@ -42,8 +42,11 @@ struct LatentAttnArgs {
   const int32_t *page_tables;  // [B][table_stride]
   const int32_t *seq_lens;     // [B]
   int32_t *status;
-  float *ws_m, *ws_l, *ws_o;   // partials [B][T][Hq][num_splits] (o: x dc), m in log2 units; null:
-  int32_t *ws_tiles;           //   one piece a row.  Tiles per piece, for the merge
+  // partials of groups of 32 query columns (null: one piece a row): m (log2 units) and l
+  // [B][groups][num_splits][32], o [B][groups][num_splits][dc / 4][32] float4; then the tiles per
+  // piece, for the merge
+  float *ws_m, *ws_l, *ws_o;
+  int32_t *ws_tiles;
   void *out;                   // [B][T][Hq][dc] of out_dtype
   int out_dtype;
   long long num_pages;

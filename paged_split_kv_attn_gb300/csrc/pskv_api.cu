@@ -409,7 +409,9 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   const LatentPlan plan = plan_latent(n_sm / 2, batch, seq_lens_host, (columns + 127) / 128, num_splits);
   const bool direct = plan.splits == 1;
   WorkspacePlan w;
-  if ((rc = plan_workspace(rows, 1, d.head_dim_v, plan.splits, 1, &w))) return rc;
+  // partials in groups of 32 query columns
+  if ((rc = plan_workspace((columns + 31) / 32 * 32 * batch, 1, d.head_dim_v, plan.splits, 1, &w)))
+    return rc;
   w.total += 256;  // the tiles per piece, for the merge
   if (plan_bytes) {
     *plan_bytes = direct ? 0 : w.total;

@@ -130,7 +130,7 @@ def test_workspace_bytes(lib, latent):
         latent, i32s(*lens), 4, len(lens), tokens, hq, splits, ctypes.byref(n)), n.value)
     assert get(1) == (0, 0)
     rc, size = get(4)
-    partial = pskv.pskv_partial_scratch_bytes(2 * 2, 3, 512, 2)[3]  # 250 keys: two tiles of 128
+    partial = pskv.pskv_partial_scratch_bytes(2, 32, 512, 2)[3]  # 2 x 3 columns in a group of 32; 250 keys: two tiles
     assert rc == 0 and partial <= size <= partial + 4 * 256
     assert get(4, lens=(1,), tokens=2)[0] == INVALID
 
