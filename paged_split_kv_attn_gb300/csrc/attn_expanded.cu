@@ -1,70 +1,469 @@
-// attn_expanded.cu -- expanded latent attention of variable-length chunks.
+// attn_expanded.cu -- expanded latent attention of variable-length chunks on the
+// fifth-generation tensor cores.
 //
-// A first, simple kernel: one warp per (row, token, head) walks the keys up to
-// the token's own with a running maximum and sum; lane l holds columns 64 i + 2 l, + 1.
+// Per row, head h and query i: s_ij = scale * (qn_i . kn_j + qr_i . r_j) over the keys
+// j up to the query's own, o_i = sum_j softmax(s_i)_j v_j; 192 score columns (the rotated
+// 64 shared by all heads) and 128 value columns.  2 * (192 + 128) operations a (query, key)
+// pair and head: compute-bound from a few hundred tokens on.
+//
+// A CTA takes 256 queries of one head as two blocks A and B of 128 (the MMAs' M; f32 output:
+// one block) and walks the keys in tiles of 128.  Tensor memory, 512 columns: one score
+// region of 128 that both blocks use in turn, a P region of 64 for each (bf16 pairs, the
+// MMAs' A operand) and O, 128 f32 columns each.  The tensor pipe's order is
+//   S_A(j)  PV_B(j-1)  S_B(j)  PV_A(j)  S_A(j+1) ...
+// so that while a block's scores are read into registers the other block's values run, and
+// every product waits only for something issued a whole product earlier.  (Two score
+// regions with P over them would make S_x(j+1) wait for PV_x(j) itself.)  Per tile
+// of both blocks the pipe works 2 * (12 * 64 + 16 * 32) = 2,560 cycles (S from shared
+// memory at N = 128, PV with A from tensor memory at N = 64: both at the full rate).
+// One softmax thread per query: it reads its 128 scores, masks them, moves the
+// reference maximum only past a slack of 8 (log2 units) and writes P.  K and V come
+// in 64-column slabs of 128 rows (16 KB), K (two unrotated slabs and the rotated one a tile)
+// through a ring of five and V (two a tile) through one of three, each filled in the order
+// its products free it by a warp of its own (365 cycles a copy).
+//
+// P is rounded to bf16 when the output is (it adds about what the output's own
+// rounding does; f32 output: a bf16 pair), everything else is f32.  Every wait is bounded; on
+// expiry the CTA flags PSKV_FAULT_WAIT_TIMEOUT, lets what it issued finish and
+// frees its tensor memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <math_constants.h>
 
 #include "latent.h"
 #include "pskv_internal.cuh"
+#include "tc_common.cuh"
+#include "tc_ops.cuh"
 
 namespace pskv {
 
-__global__ void __launch_bounds__(128) pskv_attn_expanded(const ExpandedAttnArgs a) {
-  constexpr int kQ = PSKV_EXPANDED_NOPE + PSKV_LATENT_ROT, kKV = PSKV_EXPANDED_NOPE + PSKV_EXPANDED_V;
-  const int lane = threadIdx.x & 31;
+namespace {
+
+using tc::elect_one;
+using tc::ex2;
+using tc::warp_wait;
+
+constexpr int kRows = 128;             // queries per block (MMA M)
+constexpr int kKeys = 128;             // keys per tile
+constexpr int kQSlabs = 3;             // 64-column slabs of a query or key
+constexpr int kSlab = 128 * 128;       // 128 rows of 64 columns: 16 KB
+constexpr int kRingK = 5, kRingV = 3;  // K and V slabs in flight (3 and 2 a tile)
+constexpr int kDv = PSKV_EXPANDED_V;
+constexpr int kThreads = 384;          // warps: 0 MMA, 1 Q and K copies, 2 V copies, 4-7 softmax A, 8-11 B
+constexpr int kTmemCols = 512;
+constexpr float kSlack = 8.f;
+// tensor memory: S, then P of the blocks (f32 output: hi and lo of the one), then O
+constexpr int kSCol = 0, kPCol = 128, kOCol = 256;
+
+constexpr int kOffQ = 0;                             // block x at x * 3 slabs
+constexpr int kOffK = kOffQ + 2 * kQSlabs * kSlab;
+constexpr int kOffV = kOffK + kRingK * kSlab;
+constexpr int kOffBar = kOffV + kRingV * kSlab;
+enum : int {
+  kFullK = 0,                // [5] slab landed
+  kFullV = kFullK + kRingK,  // [3]
+  kEmptyK = kFullV + kRingV,  // [5] its products done
+  kEmptyV = kEmptyK + kRingK,  // [3]
+  kQFull = kEmptyV + kRingV,  // [2] block x's queries landed
+  kSFull = kQFull + 2,       // [2] block x's scores in
+  kSFree = kSFull + 2,       // the score region read
+  kPFull = kSFree + 1,       // [2] block x's P written
+  kPvDone = kPFull + 2,      // [2] block x's values done
+  kRagged = kPvDone + 2,     // V of the tile with the row's end
+  kDrain = kRagged + 1,
+  kNumBars = kDrain + 1
+};
+constexpr int kOffSlot = kOffBar + kNumBars * 8;
+constexpr int kOffAbort = kOffSlot + 4;
+constexpr int kSmemBytes = kOffAbort + 4 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+constexpr uint32_t kIdescS = tc::instr_desc(kRows, kKeys, false, false);
+constexpr uint32_t kIdescPV = tc::instr_desc(kRows, 64, false, true);
+
+struct Maps {
+  CUtensorMap q, kv, rot;
+};
+
+// The CTA's share, the same in every thread.
+struct Plan {
+  int q0, nq, k0, nk;  // the row's first query and key, and how many
+  int t0;              // the CTA's first query in the row
+  int n[2];            // key tiles of each block
+  int tiles;           // of either
+};
+
+__device__ __forceinline__ int tiles_below(int keys) { return keys > 0 ? (keys + kKeys - 1) / kKeys : 0; }
+
+}  // namespace
+
+template <bool kLo>
+__global__ void __launch_bounds__(kThreads, 1)
+    pskv_attn_expanded(const ExpandedAttnArgs a, const __grid_constant__ Maps maps) {
+  constexpr int kBlocks = kLo ? 1 : 2;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *sm = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
+  uint32_t *slot = reinterpret_cast<uint32_t *>(sm + kOffSlot);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffAbort);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x, b = blockIdx.z;
+
   pdl_wait();
   pdl_launch_dependents();
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
-  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-  if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 > a.total_k || k1 - k0 < q1 - q0) {
-    if (t == 0 && h == 0 && lane == 0) raise_fault(a.status, PSKV_FAULT_BAD_LENGTH);
+  Plan pl;
+  pl.q0 = a.cu_q[b];
+  pl.k0 = a.cu_k[b];
+  const int q1 = a.cu_q[b + 1], k1 = a.cu_k[b + 1];
+  pl.nq = q1 - pl.q0;
+  pl.nk = k1 - pl.k0;
+  constexpr int per = kBlocks * kRows;
+  // offsets that the host copies do not allow: the row is left out
+  if (pl.q0 < 0 || q1 < pl.q0 || q1 > a.total_q || pl.k0 < 0 || k1 < pl.k0 || k1 > a.total_k ||
+      pl.nk < pl.nq || pl.nq > (long long)gridDim.y * per) {
+    if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0) raise_fault(a.status, PSKV_FAULT_BAD_LENGTH);
     return;
   }
-  if (t >= q1 - q0) return;
-  const size_t row = (size_t)(q0 + t) * a.num_heads + h;
-  const uint32_t *q = static_cast<const uint32_t *>(a.q) + row * (kQ / 2) + lane;
-  float qf[3][2], o[2][2] = {}, m = -CUDART_INF_F, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    qf[i][0] = bf16_lo(q[32 * i]);
-    qf[i][1] = bf16_hi(q[32 * i]);
+  // later queries see more keys: they go first
+  const int blocks = (pl.nq + per - 1) / per;
+  if ((int)blockIdx.y >= blocks) return;
+  pl.t0 = (blocks - 1 - (int)blockIdx.y) * per;
+
+  if (warp == 1) {
+    if (lane == 0) {
+      for (int s = 0; s < kQFull; ++s) mbar_init(&bars[s], 1);  // full and empty
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&bars[kQFull + x], 1);
+        mbar_init(&bars[kSFull + x], 1);
+        mbar_init(&bars[kPFull + x], 4);
+        mbar_init(&bars[kPvDone + x], 1);
+      }
+      mbar_init(&bars[kSFree], 4);
+      mbar_init(&bars[kRagged], 1);
+      mbar_init(&bars[kDrain], 1);
+      *abort_flag = 0;
+      mbar_fence_init();
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    tc::alloc(slot, kTmemCols);
   }
-  const int n = (k1 - k0) - (q1 - q0) + t + 1;
-  for (int j = 0; j < n; ++j) {
-    const uint32_t *kv = static_cast<const uint32_t *>(a.kv) +
-                         ((size_t)(k0 + j) * a.num_heads + h) * (kKV / 2) + lane;
-    const uint32_t r = *(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.k_rot) +
-                                                            (size_t)(k0 + j) * a.k_rot_token) + lane);
-    const uint32_t x0 = kv[0], x1 = kv[32], v0 = kv[64], v1 = kv[96];
-    float s = qf[0][0] * bf16_lo(x0) + qf[0][1] * bf16_hi(x0) + qf[1][0] * bf16_lo(x1) +
-              qf[1][1] * bf16_hi(x1) + qf[2][0] * bf16_lo(r) + qf[2][1] * bf16_hi(r);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *slot;
+  auto wait = [&](int s, uint32_t parity) {
+    return warp_wait(bars + s, parity, abort_flag, a.status);
+  };
+
+  // queries [t0, t0 + 128 kBlocks) of the row; key tiles up to each block's last own key
+  const int before = pl.nk - pl.nq;  // keys before the row's first query
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-    l = l * f + w;
-    o[0][0] = o[0][0] * f + w * bf16_lo(v0);
-    o[0][1] = o[0][1] * f + w * bf16_hi(v0);
-    o[1][0] = o[1][0] * f + w * bf16_lo(v1);
-    o[1][1] = o[1][1] * f + w * bf16_hi(v1);
-    m = mn;
+  for (int x = 0; x < 2; ++x) {
+    const int t = pl.t0 + x * kRows;
+    pl.n[x] = x < kBlocks && t < pl.nq ? tiles_below(before + min(pl.nq, t + kRows)) : 0;
   }
-  const float inv = 1.f / l;
+  pl.tiles = max(pl.n[0], pl.n[1]);
+
+  if (warp == 0) {
+    // ---- the products
+    bool ok = true;
+    int s_ops = 0;  // score products so far: the region is free once the last one's scores are read
+    auto scores = [&](int x, int j) {
+      ok = ok && (s_ops == 0 || wait(kSFree, (s_ops - 1) & 1));
+      ok = ok && (j > 0 || wait(kQFull + x, 0));
+      const uint32_t q = smem_u32(sm + kOffQ + x * kQSlabs * kSlab);
+      const bool frees = x == 1 || j >= pl.n[1];  // the tile's last scores
+#pragma unroll 1
+      for (int c = 0; ok && c < kQSlabs; ++c) {
+        const int s = kQSlabs * j + c, st = s % kRingK;
+        ok = wait(kFullK + st, (s / kRingK) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t k = smem_u32(sm + kOffK + st * kSlab);
+        if (elect_one()) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float y0 = o[i][0] * inv, y1 = o[i][1] * inv;
-    if (a.out_dtype == PSKV_DTYPE_BF16)
-      (static_cast<uint32_t *>(a.out) + row * (PSKV_EXPANDED_V / 2))[32 * i + lane] =
-          pack_bf16x2(y0, y1);
-    else
-      reinterpret_cast<float2 *>(static_cast<float *>(a.out) + row * PSKV_EXPANDED_V)[32 * i + lane] =
-          make_float2(y0, y1);
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma(tmem + kSCol, tc::smem_desc(q + c * kSlab + kk * 32, 16, 1024),
+                    tc::smem_desc(k + kk * 32, 16, 1024), kIdescS, c > 0 || kk > 0);
+          if (frees) tc::commit(bars + kEmptyK + st);
+          if (c == kQSlabs - 1) tc::commit(bars + kSFull + x);
+        }
+        __syncwarp();
+      }
+      ++s_ops;
+    };
+    auto values = [&](int x, int j) {
+      ok = ok && wait(kPFull + x, j & 1);
+      const bool frees = x == 1 || j >= pl.n[1];
+#pragma unroll 1
+      for (int c = 0; ok && c < 2; ++c) {
+        const int s = 2 * j + c, st = s % kRingV;
+        ok = wait(kFullV + st, (s / kRingV) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t v = smem_u32(sm + kOffV + st * kSlab);
+        if (elect_one()) {
+#pragma unroll
+          for (int part = 0; part < (kLo ? 2 : 1); ++part)
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              tc::mma_ts(tmem + kOCol + kDv * x + 64 * c, tmem + kPCol + 64 * (x + part) + 8 * kk,
+                         tc::smem_desc(v + kk * 2048, kSlab, 1024), kIdescPV,
+                         j > 0 || part > 0 || kk > 0);
+          if (frees) tc::commit(bars + kEmptyV + st);
+          if (c == 1) tc::commit(bars + kPvDone + x);
+        }
+        __syncwarp();
+      }
+    };
+    if (pl.n[1] == 0) {  // one block: its next scores go ahead of its values
+      for (int j = 0; ok && j <= pl.tiles; ++j) {
+        if (j < pl.tiles) scores(0, j);
+        if (j > 0) values(0, j - 1);
+      }
+    } else {
+      for (int j = 0; ok && j <= pl.tiles; ++j) {
+        if (j < pl.n[0]) scores(0, j);
+        if (j > 0 && j - 1 < pl.n[1]) values(1, j - 1);
+        if (j < pl.n[1]) scores(1, j);
+        if (j < pl.n[0]) values(0, j);
+      }
+    }
+    if (elect_one()) tc::commit(bars + kDrain);
+    __syncwarp();
+    mbar_wait(bars + kDrain, 0);  // every product done before the memory is released
+  } else if (warp == 1 || warp == 2) {
+    // ---- the copies
+    const bool is_v = warp == 2;
+    const int ring = is_v ? kRingV : kRingK, full = is_v ? kFullV : kFullK;
+    const int per_tile = is_v ? 2 : kQSlabs;
+    if (!is_v && elect_one())
+      for (int x = 0; x < kBlocks; ++x)
+        if (pl.n[x] > 0) {
+          mbar_arrive_expect_tx(bars + kQFull + x, kQSlabs * kSlab);
+          tc::tma_load_3d(sm + kOffQ + x * kQSlabs * kSlab, &maps.q, 0, pl.q0 + pl.t0 + x * kRows,
+                          kQSlabs * h, bars + kQFull + x);
+        }
+    __syncwarp();
+    int issued = 0;
+    bool ok = true;
+    for (int j = 0; ok && j < pl.tiles; ++j) {
+      const int y = pl.k0 + j * kKeys, left = pl.nk - j * kKeys;
+#pragma unroll 1
+      for (int c = 0; c < per_tile; ++c) {
+        const int s = per_tile * j + c, st = s % ring;
+        if (s >= ring) ok = wait((is_v ? kEmptyV : kEmptyK) + st, (s / ring - 1) & 1);
+        if (!ok) break;
+        unsigned char *dst = sm + (is_v ? kOffV : kOffK) + st * kSlab;
+        // the tile with the row's last key: rows behind it are another row's and meet P = 0
+        const bool ragged = is_v && left < kKeys;
+        uint64_t *bar = bars + (ragged ? (int)kRagged : full + st);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, kSlab);
+          if (is_v)
+            tc::tma_load_3d(dst, &maps.kv, 0, y, 4 * h + 2 + c, bar);
+          else if (c < 2)
+            tc::tma_load_3d(dst, &maps.kv, 0, y, 4 * h + c, bar);
+          else
+            tc::tma_load_3d(dst, &maps.rot, 0, y, 0, bar);
+        }
+        __syncwarp();
+        if (ragged) {
+          mbar_wait(bars + kRagged, c & 1);  // (bounded; landed or given up on, the slab is passed on)
+          for (int e = lane; e < (kKeys - left) * 8; e += 32)
+            *reinterpret_cast<uint4 *>(dst + (left + (e >> 3)) * 128 + (e & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          tc::fence_smem_for_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + full + st);
+        }
+        issued = s + 1;
+      }
+    }
+    // every copy landed before the CTA leaves
+    for (int s = max(0, issued - ring); s < issued; ++s)
+      mbar_wait(bars + full + s % ring, (s / ring) & 1);
+    if (!is_v)
+      for (int x = 0; x < kBlocks; ++x)
+        if (pl.n[x] > 0) mbar_wait(bars + kQFull + x, 0);
+    __syncwarp();
+  } else if (warp >= 4 && (warp - 4) / 4 < kBlocks) {
+    // ---- the softmax: one thread per query
+    const int x = (warp - 4) >> 2, w = warp & 3, i = 32 * w + lane;
+    const int t = pl.t0 + x * kRows + i;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
+    const int lim = t < pl.nq ? before + t + 1 : 0;  // keys below lim are seen
+    const float sc = a.scale_log2;
+    float m = -CUDART_INF_F, l = 0.f;
+    bool ok = true;
+    for (int j = 0; ok && j < pl.n[x]; ++j) {
+      if (!(ok = wait(kSFull + x, j & 1))) break;
+      tc::fence_after_sync();
+      uint32_t v[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tc::ld32(lane_base + kSCol + 32 * q, v[q]);
+      tc::wait_ld();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tc::reg_fence(v[q]);
+      float f[kKeys];
+#pragma unroll
+      for (int c = 0; c < kKeys; ++c) f[c] = __uint_as_float(v[c >> 5][c & 31]);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kSFree);
+      const int key0 = j * kKeys;
+      // scores in log2 units are mul * f: whole tiles leave the product to the exponent's
+      // multiply-add, others (and scales that are not positive) take it before the mask
+      float mul = sc;
+      if (key0 + kKeys > lim || !(sc > 0.f)) {
+        mul = 1.f;
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c) f[c] = key0 + c < lim ? f[c] * sc : -CUDART_INF_F;
+      }
+      float mx[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+      for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], f[c]);
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+      float alpha = 1.f;
+      bool rescale = false;
+      if (mt > m + kSlack) {
+        rescale = m != -CUDART_INF_F;  // with m = -inf the row's O and l are still 0
+        alpha = rescale ? ex2(m - mt) : 1.f;
+        l *= alpha;
+        m = mt;
+      }
+      // P's region is free, and O may be rescaled, once the last tile's values are done
+      if (j > 0 && !(ok = wait(kPvDone + x, (j - 1) & 1))) break;
+      tc::fence_after_sync();
+      if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+        for (int c = 0; c < kDv / 32; ++c) {
+          uint32_t o[32];
+          tc::ld32(lane_base + kOCol + kDv * x + 32 * c, o);
+          tc::wait_ld();
+          tc::reg_fence(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tc::st32(lane_base + kOCol + kDv * x + 32 * c, o);
+        }
+      }
+      const float off = m == -CUDART_INF_F ? 0.f : -m;
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t hi[32], lo[kLo ? 32 : 1];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float p0 = ex2(fmaf(f[64 * q + 2 * e], mul, off));
+          const float p1 = ex2(fmaf(f[64 * q + 2 * e + 1], mul, off));
+          hi[e] = pack_bf16x2(p0, p1);
+          if constexpr (kLo) lo[e] = pack_bf16x2(p0 - bf16_lo(hi[e]), p1 - bf16_hi(hi[e]));
+          s0 += p0;
+          s1 += p1;
+        }
+        tc::st32(lane_base + kPCol + 64 * x + 32 * q, hi);
+        if constexpr (kLo) tc::st32(lane_base + kPCol + 64 + 32 * q, lo);
+      }
+      l += s0 + s1;
+      tc::wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kPFull + x);
+    }
+    // ---- O / l, put together in the queries' place (their products are done) by warps, each
+    // its own 32 rows, so that they leave in whole lines
+    if (pl.n[x] > 0) ok = ok && wait(kPvDone + x, (pl.n[x] - 1) & 1);
+    if (ok && pl.n[x] > 0) {
+      tc::fence_after_sync();
+      const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
+      constexpr int kBytes = kDv * (kLo ? 4 : 2), kPitch = kBytes + 16;
+      unsigned char *stage = sm + kOffQ + x * kQSlabs * kSlab + 32 * w * kPitch;
+      static_assert(kRows * kPitch <= (kLo ? 2 : 1) * kQSlabs * kSlab, "staging");
+#pragma unroll 1
+      for (int c = 0; c < kDv / 32; ++c) {
+        uint32_t o[32];
+        tc::ld32(lane_base + kOCol + kDv * x + 32 * c, o);
+        tc::wait_ld();
+        tc::reg_fence(o);
+        uint4 *dst = reinterpret_cast<uint4 *>(stage + lane * kPitch + c * (kLo ? 128 : 64));
+        float y[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * inv;
+        if constexpr (kLo) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<float4 *>(dst)[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
+                                pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
+        }
+      }
+      __syncwarp();
+      constexpr int kPieces = kBytes / 16;  // per row
+      const int first = pl.t0 + x * kRows + 32 * w;
+      for (int e = lane; e < 32 * kPieces; e += 32) {
+        const int r = e / kPieces, piece = e % kPieces;
+        if (first + r < pl.nq)
+          reinterpret_cast<uint4 *>(a.out)[((size_t)(pl.q0 + first + r) * a.num_heads + h) * kPieces + piece] =
+              *reinterpret_cast<const uint4 *>(stage + r * kPitch + piece * 16);
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::dealloc(tmem, kTmemCols);
   }
 }
 
+namespace {
+
+// Rows of `pitch` bytes as (64, rows, slabs): a box of 128 rows and box_slabs slabs.
+bool make_map(CUtensorMap *m, const void *base, long long rows, long long pitch, int slabs,
+              int box_slabs) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tc::encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)slabs};
+  const cuuint64_t strides[2] = {(cuuint64_t)pitch, 128};
+  const cuuint32_t box[3] = {64, 128, (cuuint32_t)box_slabs};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+             elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kLo>
+cudaError_t launch(const ExpandedAttnArgs &a, cudaStream_t s) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(dev >= 0 && dev < 64 && attr_set[dev])) {
+    e = cudaFuncSetAttribute(pskv_attn_expanded<kLo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const long long h = a.num_heads;
+  Maps maps;
+  if (!make_map(&maps.q, a.q, a.total_q, h * kQSlabs * 128, (int)h * kQSlabs, kQSlabs) ||
+      !make_map(&maps.kv, a.kv, a.total_k, h * 512, (int)h * 4, 1) ||
+      !make_map(&maps.rot, a.k_rot, a.total_k, a.k_rot_token * 2, 1, 1))
+    return cudaErrorInvalidValue;
+  const int per = (kLo ? 1 : 2) * kRows;
+  return launch_pdl(pskv_attn_expanded<kLo>, dim3(a.num_heads, (a.max_q + per - 1) / per, a.batch),
+                    dim3(kThreads), kSmemBytes, s, a, maps);
+}
+
+}  // namespace
+
 cudaError_t launch_attn_expanded(const ExpandedAttnArgs &a, cudaStream_t s) {
-  return launch_pdl(pskv_attn_expanded, dim3((a.max_q + 3) / 4, a.num_heads, a.batch), dim3(128), 0,
-                    s, a);
+  return a.out_dtype == PSKV_DTYPE_F32 ? launch<true>(a, s) : launch<false>(a, s);
 }
 
 }  // namespace pskv
