@@ -14,13 +14,15 @@
 // so that while a block's scores are read into registers the other block's values run, and
 // every product waits only for something issued a whole product earlier.  (Two score
 // regions with P over them would make S_x(j+1) wait for PV_x(j) itself.)  Per tile
-// of both blocks the pipe works 2 * (12 * 64 + 16 * 32) = 2,560 cycles (S from shared
-// memory at N = 128, PV with A from tensor memory at N = 64: both at the full rate).
+// of both blocks the pipe works 2 * (12 + 8) * 64 = 2,560 cycles (S from shared memory, PV with A
+// from tensor memory, both at the full rate).
 // One softmax thread per query: it reads its 128 scores, masks them, moves the
 // reference maximum only past a slack of 8 (log2 units) and writes P.  K and V come
-// in 64-column slabs of 128 rows (16 KB), K (two unrotated slabs and the rotated one a tile)
-// through a ring of five and V (two a tile) through one of three, each filled in the order
-// its products free it by a warp of its own (365 cycles a copy).
+// in 64-column slabs of 128 rows (16 KB): K (two unrotated slabs and the rotated one a tile)
+// through a ring of four, V (both slabs in one copy) through one of two tiles.  The products
+// and the copies are each issued by a single thread that runs its whole loop (with a
+// whole-warp wait and an election per slab the same products took three times as long to issue
+// as to run).
 //
 // P is rounded to bf16 when the output is (it adds about what the output's own
 // rounding does; f32 output: a bf16 pair), everything else is f32.  Every wait is bounded; on
@@ -41,13 +43,13 @@ namespace {
 
 using tc::elect_one;
 using tc::ex2;
-using tc::warp_wait;
 
 constexpr int kRows = 128;             // queries per block (MMA M)
 constexpr int kKeys = 128;             // keys per tile
 constexpr int kQSlabs = 3;             // 64-column slabs of a query or key
 constexpr int kSlab = 128 * 128;       // 128 rows of 64 columns: 16 KB
-constexpr int kRingK = 5, kRingV = 3;  // K and V slabs in flight (3 and 2 a tile)
+constexpr int kRingK = 4;              // K slabs in flight (three a tile)
+constexpr int kRingV = 2;              // V tiles in flight (two slabs)
 constexpr int kDv = PSKV_EXPANDED_V;
 constexpr int kThreads = 384;          // warps: 0 MMA, 1 Q and K copies, 2 V copies, 4-7 softmax A, 8-11 B
 constexpr int kTmemCols = 512;
@@ -58,12 +60,12 @@ constexpr int kSCol = 0, kPCol = 128, kOCol = 256;
 constexpr int kOffQ = 0;                             // block x at x * 3 slabs
 constexpr int kOffK = kOffQ + 2 * kQSlabs * kSlab;
 constexpr int kOffV = kOffK + kRingK * kSlab;
-constexpr int kOffBar = kOffV + kRingV * kSlab;
+constexpr int kOffBar = kOffV + kRingV * 2 * kSlab;
 enum : int {
-  kFullK = 0,                // [5] slab landed
-  kFullV = kFullK + kRingK,  // [3]
-  kEmptyK = kFullV + kRingV,  // [5] its products done
-  kEmptyV = kEmptyK + kRingK,  // [3]
+  kFullK = 0,                // [4] slab landed
+  kFullV = kFullK + kRingK,  // [2] tile landed
+  kEmptyK = kFullV + kRingV,  // [4] its products done
+  kEmptyV = kEmptyK + kRingK,  // [2]
   kQFull = kEmptyV + kRingV,  // [2] block x's queries landed
   kSFull = kQFull + 2,       // [2] block x's scores in
   kSFree = kSFull + 2,       // the score region read
@@ -79,10 +81,10 @@ constexpr int kSmemBytes = kOffAbort + 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 constexpr uint32_t kIdescS = tc::instr_desc(kRows, kKeys, false, false);
-constexpr uint32_t kIdescPV = tc::instr_desc(kRows, 64, false, true);
+constexpr uint32_t kIdescPV = tc::instr_desc(kRows, kDv, false, true);
 
 struct Maps {
-  CUtensorMap q, kv, rot;
+  CUtensorMap q, k, v, rot;
 };
 
 // The CTA's share, the same in every thread.
@@ -154,7 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *slot;
   auto wait = [&](int s, uint32_t parity) {
-    return warp_wait(bars + s, parity, abort_flag, a.status);
+    return tc::all_wait(bars + s, parity, abort_flag, a.status);
+  };
+  auto wait1 = [&](int s, uint32_t parity) {
+    return tc::one_wait(bars + s, parity, abort_flag, a.status);
   };
 
   // queries [t0, t0 + 128 kBlocks) of the row; key tiles up to each block's last own key
@@ -167,128 +172,126 @@ __global__ void __launch_bounds__(kThreads, 1)
   pl.tiles = max(pl.n[0], pl.n[1]);
 
   if (warp == 0) {
-    // ---- the products
-    bool ok = true;
-    int s_ops = 0;  // score products so far: the region is free once the last one's scores are read
-    auto scores = [&](int x, int j) {
-      ok = ok && (s_ops == 0 || wait(kSFree, (s_ops - 1) & 1));
-      ok = ok && (j > 0 || wait(kQFull + x, 0));
-      const uint32_t q = smem_u32(sm + kOffQ + x * kQSlabs * kSlab);
-      const bool frees = x == 1 || j >= pl.n[1];  // the tile's last scores
-#pragma unroll 1
-      for (int c = 0; ok && c < kQSlabs; ++c) {
-        const int s = kQSlabs * j + c, st = s % kRingK;
-        ok = wait(kFullK + st, (s / kRingK) & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t k = smem_u32(sm + kOffK + st * kSlab);
-        if (elect_one()) {
+    if (elect_one()) {
+      // ---- the products
+      bool ok = true;
+      int s_ops = 0;  // score products so far: the region is free once the last one's scores are read
+      const uint32_t q0 = smem_u32(sm + kOffQ), k0 = smem_u32(sm + kOffK), v0 = smem_u32(sm + kOffV);
+      auto scores = [&](int x, int j) {
+        if (s_ops > 0) ok = ok && wait1(kSFree, (s_ops - 1) & 1);
+        if (j == 0) ok = ok && wait1(kQFull + x, 0);
+        ++s_ops;
+        const bool frees = x == 1 || j >= pl.n[1];  // the tile's last scores
+#pragma unroll
+        for (int c = 0; c < kQSlabs; ++c) {
+          const int s = kQSlabs * j + c, st = s % kRingK;
+          ok = ok && wait1(kFullK + st, (s / kRingK) & 1);
+          if (!ok) return;
+          tc::fence_after_sync();
+          const uint32_t q = q0 + (x * kQSlabs + c) * kSlab, k = k0 + st * kSlab;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc::mma(tmem + kSCol, tc::smem_desc(q + c * kSlab + kk * 32, 16, 1024),
+            tc::mma(tmem + kSCol, tc::smem_desc(q + kk * 32, 16, 1024),
                     tc::smem_desc(k + kk * 32, 16, 1024), kIdescS, c > 0 || kk > 0);
           if (frees) tc::commit(bars + kEmptyK + st);
-          if (c == kQSlabs - 1) tc::commit(bars + kSFull + x);
         }
-        __syncwarp();
-      }
-      ++s_ops;
-    };
-    auto values = [&](int x, int j) {
-      ok = ok && wait(kPFull + x, j & 1);
-      const bool frees = x == 1 || j >= pl.n[1];
-#pragma unroll 1
-      for (int c = 0; ok && c < 2; ++c) {
-        const int s = 2 * j + c, st = s % kRingV;
-        ok = wait(kFullV + st, (s / kRingV) & 1);
-        if (!ok) break;
+        tc::commit(bars + kSFull + x);
+      };
+      auto values = [&](int x, int j) {
+        const int st = j % kRingV;
+        ok = ok && wait1(kPFull + x, j & 1) && wait1(kFullV + st, (j / kRingV) & 1);
+        if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t v = smem_u32(sm + kOffV + st * kSlab);
-        if (elect_one()) {
+        const uint32_t v = v0 + st * 2 * kSlab;
 #pragma unroll
-          for (int part = 0; part < (kLo ? 2 : 1); ++part)
+        for (int part = 0; part < (kLo ? 2 : 1); ++part)
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              tc::mma_ts(tmem + kOCol + kDv * x + 64 * c, tmem + kPCol + 64 * (x + part) + 8 * kk,
-                         tc::smem_desc(v + kk * 2048, kSlab, 1024), kIdescPV,
-                         j > 0 || part > 0 || kk > 0);
-          if (frees) tc::commit(bars + kEmptyV + st);
-          if (c == 1) tc::commit(bars + kPvDone + x);
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            tc::mma_ts(tmem + kOCol + kDv * x, tmem + kPCol + 64 * (x + part) + 8 * kk,
+                       tc::smem_desc(v + kk * 2048, kSlab, 1024), kIdescPV,
+                       j > 0 || part > 0 || kk > 0);
+        if (x == 1 || j >= pl.n[1]) tc::commit(bars + kEmptyV + st);
+        tc::commit(bars + kPvDone + x);
+      };
+      if (pl.n[1] == 0) {  // one block: its next scores go ahead of its values
+        for (int j = 0; ok && j <= pl.tiles; ++j) {
+          if (j < pl.tiles) scores(0, j);
+          if (j > 0) values(0, j - 1);
         }
-        __syncwarp();
+      } else {
+        for (int j = 0; ok && j <= pl.tiles; ++j) {
+          if (j < pl.n[0]) scores(0, j);
+          if (j > 0 && j - 1 < pl.n[1]) values(1, j - 1);
+          if (j < pl.n[1]) scores(1, j);
+          if (j < pl.n[0]) values(0, j);
+        }
       }
-    };
-    if (pl.n[1] == 0) {  // one block: its next scores go ahead of its values
-      for (int j = 0; ok && j <= pl.tiles; ++j) {
-        if (j < pl.tiles) scores(0, j);
-        if (j > 0) values(0, j - 1);
-      }
-    } else {
-      for (int j = 0; ok && j <= pl.tiles; ++j) {
-        if (j < pl.n[0]) scores(0, j);
-        if (j > 0 && j - 1 < pl.n[1]) values(1, j - 1);
-        if (j < pl.n[1]) scores(1, j);
-        if (j < pl.n[0]) values(0, j);
-      }
+      tc::commit(bars + kDrain);
+      mbar_wait(bars + kDrain, 0);  // every product done before the memory is released
     }
-    if (elect_one()) tc::commit(bars + kDrain);
     __syncwarp();
-    mbar_wait(bars + kDrain, 0);  // every product done before the memory is released
-  } else if (warp == 1 || warp == 2) {
-    // ---- the copies
-    const bool is_v = warp == 2;
-    const int ring = is_v ? kRingV : kRingK, full = is_v ? kFullV : kFullK;
-    const int per_tile = is_v ? 2 : kQSlabs;
-    if (!is_v && elect_one())
+  } else if (warp == 1) {
+    if (elect_one()) {
+      // ---- Q, and K's slabs
+#pragma unroll
       for (int x = 0; x < kBlocks; ++x)
         if (pl.n[x] > 0) {
           mbar_arrive_expect_tx(bars + kQFull + x, kQSlabs * kSlab);
           tc::tma_load_3d(sm + kOffQ + x * kQSlabs * kSlab, &maps.q, 0, pl.q0 + pl.t0 + x * kRows,
                           kQSlabs * h, bars + kQFull + x);
         }
-    __syncwarp();
-    int issued = 0;
-    bool ok = true;
-    for (int j = 0; ok && j < pl.tiles; ++j) {
-      const int y = pl.k0 + j * kKeys, left = pl.nk - j * kKeys;
-#pragma unroll 1
-      for (int c = 0; c < per_tile; ++c) {
-        const int s = per_tile * j + c, st = s % ring;
-        if (s >= ring) ok = wait((is_v ? kEmptyV : kEmptyK) + st, (s / ring - 1) & 1);
-        if (!ok) break;
-        unsigned char *dst = sm + (is_v ? kOffV : kOffK) + st * kSlab;
-        // the tile with the row's last key: rows behind it are another row's and meet P = 0
-        const bool ragged = is_v && left < kKeys;
-        uint64_t *bar = bars + (ragged ? (int)kRagged : full + st);
-        if (elect_one()) {
+      int s = 0;
+      bool ok = true;
+      for (int j = 0; ok && j < pl.tiles; ++j)
+#pragma unroll
+        for (int c = 0; c < kQSlabs; ++c) {
+          const int st = s % kRingK;
+          if (s >= kRingK) ok = ok && wait1(kEmptyK + st, (s / kRingK - 1) & 1);
+          if (!ok) break;
+          uint64_t *bar = bars + kFullK + st;
+          unsigned char *dst = sm + kOffK + st * kSlab;
           mbar_arrive_expect_tx(bar, kSlab);
-          if (is_v)
-            tc::tma_load_3d(dst, &maps.kv, 0, y, 4 * h + 2 + c, bar);
-          else if (c < 2)
-            tc::tma_load_3d(dst, &maps.kv, 0, y, 4 * h + c, bar);
+          if (c < 2)
+            tc::tma_load_3d(dst, &maps.k, 0, pl.k0 + j * kKeys, 4 * h + c, bar);
           else
-            tc::tma_load_3d(dst, &maps.rot, 0, y, 0, bar);
+            tc::tma_load_3d(dst, &maps.rot, 0, pl.k0 + j * kKeys, 0, bar);
+          ++s;
         }
-        __syncwarp();
-        if (ragged) {
-          mbar_wait(bars + kRagged, c & 1);  // (bounded; landed or given up on, the slab is passed on)
-          for (int e = lane; e < (kKeys - left) * 8; e += 32)
-            *reinterpret_cast<uint4 *>(dst + (left + (e >> 3)) * 128 + (e & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          tc::fence_smem_for_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + full + st);
-        }
-        issued = s + 1;
-      }
-    }
-    // every copy landed before the CTA leaves
-    for (int s = max(0, issued - ring); s < issued; ++s)
-      mbar_wait(bars + full + s % ring, (s / ring) & 1);
-    if (!is_v)
+      // every copy landed before the CTA leaves
+      for (int r = max(0, s - kRingK); r < s; ++r) mbar_wait(bars + kFullK + r % kRingK, (r / kRingK) & 1);
+#pragma unroll
       for (int x = 0; x < kBlocks; ++x)
         if (pl.n[x] > 0) mbar_wait(bars + kQFull + x, 0);
+    }
     __syncwarp();
+  } else if (warp == 2) {
+    // ---- V's tiles.  The one with the row's last key: rows behind it are another row's and
+    // meet P = 0, so they are zeroed first.
+    const bool ragged = pl.tiles * kKeys > pl.nk;
+    const int last = pl.tiles - 1, left = pl.nk - last * kKeys;
+    if (elect_one()) {
+      int j = 0;
+      for (; j < pl.tiles; ++j) {
+        const int st = j % kRingV;
+        if (j >= kRingV && !wait1(kEmptyV + st, (j / kRingV - 1) & 1)) break;
+        uint64_t *bar = bars + (ragged && j == last ? (int)kRagged : kFullV + st);
+        mbar_arrive_expect_tx(bar, 2 * kSlab);
+        tc::tma_load_3d(sm + kOffV + st * 2 * kSlab, &maps.v, 0, pl.k0 + j * kKeys, 4 * h + 2, bar);
+      }
+      if (ragged && j == pl.tiles) mbar_wait(bars + kRagged, 0);  // (bounded)
+      for (int r = max(0, j - kRingV); r < j; ++r)  // every copy landed before the CTA leaves
+        if (!(ragged && r == last)) mbar_wait(bars + kFullV + r % kRingV, (r / kRingV) & 1);
+    }
+    __syncwarp();
+    if (ragged) {
+      unsigned char *dst = sm + kOffV + (last % kRingV) * 2 * kSlab;
+      for (int e = lane; e < (kKeys - left) * 16; e += 32)
+        *reinterpret_cast<uint4 *>(dst + ((e >> 3) & 1) * kSlab + (left + (e >> 4)) * 128 + (e & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      tc::fence_smem_for_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kFullV + last % kRingV);
+    }
   } else if (warp >= 4 && (warp - 4) / 4 < kBlocks) {
     // ---- the softmax: one thread per query
     const int x = (warp - 4) >> 2, w = warp & 3, i = 32 * w + lane;
@@ -452,7 +455,8 @@ cudaError_t launch(const ExpandedAttnArgs &a, cudaStream_t s) {
   const long long h = a.num_heads;
   Maps maps;
   if (!make_map(&maps.q, a.q, a.total_q, h * kQSlabs * 128, (int)h * kQSlabs, kQSlabs) ||
-      !make_map(&maps.kv, a.kv, a.total_k, h * 512, (int)h * 4, 1) ||
+      !make_map(&maps.k, a.kv, a.total_k, h * 512, (int)h * 4, 1) ||
+      !make_map(&maps.v, a.kv, a.total_k, h * 512, (int)h * 4, 2) ||
       !make_map(&maps.rot, a.k_rot, a.total_k, a.k_rot_token * 2, 1, 1))
     return cudaErrorInvalidValue;
   const int per = (kLo ? 1 : 2) * kRows;
