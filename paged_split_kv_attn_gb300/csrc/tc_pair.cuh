@@ -2,7 +2,8 @@
 // cluster share one product.  With M = 128 each CTA holds 64 rows of A and half
 // of B's N rows in its own shared memory at the same offsets, one thread of the
 // even CTA issues, and each CTA's tensor memory receives its 64 rows: lanes 0-63
-// columns [0, N/2), lanes 64-127 (the same rows) columns [N/2, N).
+// columns [0, N/2), lanes 64-127 (the same rows) columns [N/2, N); with M = 256 each holds
+// 128 rows of A, and its tensor memory receives them as a CTA's own product would.
 #pragma once
 
 #include <cuda.h>
@@ -47,6 +48,15 @@ __device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t a, uint64_t b, uin
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+}
+
+// The same with A (each CTA's own rows, bf16 pairs per 32-bit column) read from tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b,
+                                       uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
 }
 
 // Arrive on `bar` of both CTAs once every tcgen05 operation this thread issued so far is complete.
