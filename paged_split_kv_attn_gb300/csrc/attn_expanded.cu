@@ -19,8 +19,7 @@
 // that now take two tiles.)
 // A row's 128 scores lie in two threads (halves of the keys by warp group), which
 // mask them and exchange their maxima; the reference maximum moves only past a slack of
-// 8 (log2 units), so O is rarely rescaled.  Products and copies are each issued by a single
-// thread that runs its whole loop.
+// 8 (log2 units), so O is rarely rescaled.
 //
 // P is rounded to bf16 when the output is (it adds about what the output's own
 // rounding does; f32 output: a bf16 pair), everything else is f32.  Every wait is bounded; on
@@ -159,15 +158,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     return tc::one_wait(bars + s, parity, abort_flag, a.status);
   };
 
+  auto wait = [&](int s, uint32_t parity) {
+    return tc::all_wait(bars + s, parity, abort_flag, a.status);
+  };
+
   if (warp == 0) {
-    if (rank == 0 && elect_one()) {
-      // ---- the score products
-      bool ok = wait1(kQFull, 0);
+    if (rank == 0) {
+      // ---- the score products (all lanes alike, one issues)
+      const bool lead = elect_one();
+      bool ok = wait(kQFull, 0);
       const uint32_t q = smem_u32(sm + kOffQ), k = smem_u32(sm + kOffK);
       for (int j = 0; ok && j < n; ++j) {
         const int st = j % kRing, r = j & 1;
-        ok = wait1(kFullK + st, (j / kRing) & 1) &&
-             (j < 2 || wait1(kSFree + r, (j / 2 - 1) & 1));
+        ok = wait(kFullK + st, (j / kRing) & 1) && (j < 2 || wait(kSFree + r, (j / 2 - 1) & 1));
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t kt = k + st * kKBytes;
@@ -175,21 +178,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int kk = 0; kk < 4 * kQSlabs; ++kk)
           tc2::mma(tmem + kSCol + kKeys * r,
                    tc::smem_desc(q + (kk >> 2) * kQSlab + (kk & 3) * 32, 16, 1024),
-                   tc::smem_desc(kt + (kk >> 2) * kKSlab + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0);
-        tc2::commit_both(bars + kSFull + r);
-        tc2::commit_both(bars + kEmptyK + st);
+                   tc::smem_desc(kt + (kk >> 2) * kKSlab + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0,
+                   lead);
+        tc2::commit_both(bars + kSFull + r, lead);
+        tc2::commit_both(bars + kEmptyK + st, lead);
       }
-      tc2::commit_both(bars + kDrainS);
+      tc2::commit_both(bars + kDrainS, lead);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && elect_one()) {
+    if (rank == 0) {
       // ---- the value products
+      const bool lead = elect_one();
       bool ok = true;
       const uint32_t v = smem_u32(sm + kOffV);
       for (int j = 0; ok && j < n; ++j) {
         const int st = j % kRing, pb = j % kPBufs;
-        ok = wait1(kFullV + st, (j / kRing) & 1) && wait1(kPFull + pb, (j / kPBufs) & 1);
+        ok = wait(kFullV + st, (j / kRing) & 1) && wait(kPFull + pb, (j / kPBufs) & 1);
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t vt = v + st * kVBytes;
@@ -199,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           for (int kk = 0; kk < kKeys / 16; ++kk)
             tc2::mma_ts(tmem + kOCol, tmem + kPCol + 64 * (pb + part) + 8 * kk,
                         tc::smem_desc(vt + kk * 2048, kVBytes, 1024), kIdescPV,
-                        j > 0 || part > 0 || kk > 0);
-        tc2::commit_both(bars + kPvDone + pb);
-        tc2::commit_both(bars + kEmptyV + st);
+                        j > 0 || part > 0 || kk > 0, lead);
+        tc2::commit_both(bars + kPvDone + pb, lead);
+        tc2::commit_both(bars + kEmptyV + st, lead);
       }
-      tc2::commit_both(bars + kDrainV);
+      tc2::commit_both(bars + kDrainV, lead);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -280,9 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     float *red = reinterpret_cast<float *>(sm + kOffRed);
     const uint32_t s_free = tc2::map_to(smem_u32(bars + kSFree), 0);
     const uint32_t p_full = tc2::map_to(smem_u32(bars + kPFull), 0);
-    auto wait = [&](int s, uint32_t parity) {
-      return tc::all_wait(bars + s, parity, abort_flag, a.status);
-    };
     float m = -CUDART_INF_F, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {

@@ -23,11 +23,10 @@
 // at N = 64, where reading the operands binds; M = 64 on one CTA runs at half rate).
 // The two products want a row in different CTAs (scores: by key, values: by column),
 // so a CTA copies both shares: 1.9x of a row's bytes from L2, each byte once from
-// HBM (a warp prefetches the scores' share into L2 some tiles ahead).  K moves in
-// chunks of a few 64-column slabs and V in chunks of 64 keys, through
-// rings of their own with their own copy warps and issuing warps, so a chunk's place
-// is refilled as soon as its products are done and S(j + 1) runs while the softmax works
-// on tile j.
+// HBM (a prefetch into L2 some tiles ahead only slowed the copies down, warm or cold).  K
+// moves in chunks of a few 64-column slabs and V in chunks of 64 keys, through rings of their
+// own with their own copy warps and issuing warps, so a chunk's place is refilled as soon as
+// its products are done, and S(j + 1) runs while the softmax works on tile j.
 //
 // A row's keys are cut into pieces of `tiles_per_piece` tiles, one piece per cluster
 // (pskv_plan.cpp picks the size that fills the clusters in one wave).  A row of one
@@ -63,7 +62,7 @@ using tc::PageCache;
 constexpr int kKeys = kLatentTile;  // keys per tile (128)
 constexpr int kHalf = kKeys / 2;   // of which each CTA brings half to the scores
 constexpr int kRows = 64;          // query columns per CTA (128 per pair)
-// warps: 0 score products, 1 value products, 2 Q's copy and the prefetch, 3, 12 and 13 K copies,
+// warps: 0 score products, 1 value products, 2 Q's copies, 3, 12 and 13 K copies,
 // 14 and 15 V copies, 4-11 softmax (two groups of four; warp w reads tensor-memory lanes 32 (w % 4) ..)
 constexpr int kThreads = 512;
 constexpr int kSoftWarps = 8;
@@ -72,7 +71,6 @@ constexpr int kOCol = 0;           // O: DC / 2 columns
 constexpr int kSCol = 256;         // score region r at kSCol + 64 r
 constexpr float kSlack = 8.f;
 constexpr int kInfo = 8;           // tile records in flight: K runs at most 2 tiles ahead of S, S 2 ahead of the softmax
-constexpr int kAhead = 4;          // tiles the L2 prefetch runs ahead of the scores
 constexpr int kSlab = kHalf * 128;  // 64 rows (of Q, K, V or P) of 64 columns: 8 KB
 
 template <int DC, bool kLo>
@@ -108,15 +106,14 @@ struct Lay {
   static constexpr int kQFree = kQFull + 1;              // the piece's score products done
   static constexpr int kOut = kQFree + 1;                // this CTA's O has left the rings
   static constexpr int kRagged = kOut + 1;               // [2] this CTA's V of a chunk that is not whole
-  static constexpr int kDrainS = kRagged + 2;
+  static constexpr int kDrainS = kRagged + 2;            // every product done
   static constexpr int kDrainV = kDrainS + 1;
   static constexpr int kNumBars = kDrainV + 1;
   static constexpr int kOffInfo = (kOffBar + kNumBars * 8 + 15) & ~15;
   static constexpr int kOffRed = kOffInfo + kInfo * 8;   // float[2][4][64] maxima (then sums)
   static constexpr int kOffSlot = kOffRed + 2 * 4 * kRows * 4;
   static constexpr int kOffAbort = kOffSlot + 4;
-  static constexpr int kOffScored = kOffAbort + 4;       // tiles whose scores are in (paces the prefetch)
-  static constexpr int kUsed = kOffScored + 4;
+  static constexpr int kUsed = kOffAbort + 4;
   // + alignment of the dynamic base, as far as a CTA's limit leaves room (the base is in fact
   // aligned; the kernel checks)
   static constexpr int kSmemBytes = kUsed + 1024 < 232448 ? kUsed + 1024 : 232448;
@@ -210,7 +207,7 @@ __device__ __forceinline__ bool find_piece(const LatentAttnArgs &a, int u, const
 }
 
 struct Maps {
-  CUtensorMap q, k, v, ahead;
+  CUtensorMap q, k, v;
 };
 
 // Where a tile's keys lie: the table slot and the row in its page, stepped from tile to tile
@@ -296,7 +293,7 @@ struct Loader {
   }
 
   __device__ bool free_stage(int st) {
-    return seq < kRing || tc::warp_wait(bars + (kV ? L::kEmptyV : L::kEmptyK) + st,
+    return seq < kRing || tc::all_wait(bars + (kV ? L::kEmptyV : L::kEmptyK) + st,
                                         (seq / kRing - 1) & 1, abort_flag, a.status);
   }
 
@@ -431,7 +428,7 @@ struct Loader {
     for (int u = first; find_piece(a, u, rows, lane, pc); u += step) {
       if (pc.n == 0) continue;
       // the last piece's O may be leaving through the rings
-      if (k > 0 && !tc::warp_wait(bars + L::kOut, (k - 1) & 1, abort_flag, a.status)) break;
+      if (k > 0 && !tc::all_wait(bars + L::kOut, (k - 1) & 1, abort_flag, a.status)) break;
       ++k;
       if (!run(pc)) break;
     }
@@ -451,7 +448,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kOffBar);
   uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::kOffSlot);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kOffAbort);
-  volatile int *scored = reinterpret_cast<volatile int *>(sm + L::kOffScored);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc2::cluster_rank();
   if (sm + L::kUsed > smem_raw + L::kSmemBytes) {  // (never seen) no room for the alignment
@@ -487,7 +483,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&bars[L::kDrainS], 1);
       mbar_init(&bars[L::kDrainV], 1);
       *abort_flag = 0;
-      *scored = 0;
       mbar_fence_init();
     }
     __syncwarp();
@@ -502,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *slot;
   auto wait = [&](int s, uint32_t parity) {
-    return tc::warp_wait(bars + s, parity, abort_flag, a.status);
+    return tc::all_wait(bars + s, parity, abort_flag, a.status);
   };
   pdl_wait();
   pdl_launch_dependents();
@@ -511,14 +506,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   Piece pc;
 
   if (warp == 0 && rank == 0) {
-    // ---- the score products
+    // ---- the score products (all lanes alike, one issues)
+    const bool lead = elect_one();
     bool ok = true;
     int seq = 0, g = 0, k = 0;  // chunks, tiles, pieces so far
+    const uint32_t q0 = smem_u32(sm + L::kOffQ), k0 = smem_u32(sm + L::kOffK);
     for (int u = first; ok && find_piece(a, u, rows, lane, pc); u += step) {
       if (pc.n == 0) continue;
       ok = wait(L::kQFull, k & 1);
       ++k;
-      const uint32_t q0 = smem_u32(sm + L::kOffQ);
       for (int j = 0; ok && j < pc.n; ++j, ++g) {
         const int r = g & 1;
         if (g >= 2) ok = wait(L::kSFree + r, (g / 2 - 1) & 1);
@@ -528,67 +524,58 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           ok = wait(L::kFullK + st, (seq / L::kRingK) & 1);
           if (!ok) break;
           tc::fence_after_sync();
-          const uint32_t k0 = smem_u32(sm + L::kOffK + st * L::kKBytes);
-          const uint32_t qc = q0 + c * L::kKBytes;
-          if (elect_one()) {
+          const uint32_t kc = k0 + st * L::kKBytes, qc = q0 + c * L::kKBytes;
 #pragma unroll
-            for (int kk = 0; kk < 4 * L::kChunkSlabs; ++kk) {
-              const uint32_t at = (kk >> 2) * kSlab + (kk & 3) * 32;
-              tc2::mma(tmem + kSCol + kHalf * r, tc::smem_desc(qc + at, 16, 1024),
-                       tc::smem_desc(k0 + at, 16, 1024), L::kIdescS, c > 0 || kk > 0);
-            }
-            tc2::commit_both(bars + L::kEmptyK + st);
-            if (c == L::kChunks - 1) tc2::commit_both(bars + L::kSFull + r);
+          for (int kk = 0; kk < 4 * L::kChunkSlabs; ++kk) {
+            const uint32_t at = (kk >> 2) * kSlab + (kk & 3) * 32;
+            tc2::mma(tmem + kSCol + kHalf * r, tc::smem_desc(qc + at, 16, 1024),
+                     tc::smem_desc(kc + at, 16, 1024), L::kIdescS, c > 0 || kk > 0, lead);
           }
-          __syncwarp();
+          tc2::commit_both(bars + L::kEmptyK + st, lead);
         }
+        if (ok) tc2::commit_both(bars + L::kSFull + r, lead);
       }
-      if (elect_one()) tc2::commit_both(bars + L::kQFree);
-      __syncwarp();
+      tc2::commit_both(bars + L::kQFree, lead);
     }
-    if (elect_one()) tc2::commit_both(bars + L::kDrainS);
+    tc2::commit_both(bars + L::kDrainS, lead);
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ---- the value products
+    const bool lead = elect_one();
     bool ok = true;
-    int seq = 0, g = 0;
+    int g = 0;
+    const uint32_t p0 = smem_u32(sm + L::kOffP), v0 = smem_u32(sm + L::kOffV);
     for (int u = first; ok && find_piece(a, u, rows, lane, pc); u += step)
       for (int j = 0; ok && j < pc.n; ++j, ++g) {
         const bool both = pc.len - (pc.t0 + j) * kKeys > kHalf;  // keys in the second half
         ok = wait(L::kPFull, g & 1);
-        const uint32_t p0 = smem_u32(sm + L::kOffP);
 #pragma unroll 1
-        for (int h = 0; ok && h < 2; ++h, ++seq) {
-          const int st = seq % L::kRingV;
-          ok = wait(L::kFullV + st, (seq / L::kRingV) & 1);
+        for (int h = 0; ok && h < 2; ++h) {
+          const int sq = 2 * g + h, st = sq % L::kRingV;
+          ok = wait(L::kFullV + st, (sq / L::kRingV) & 1);
           if (!ok) break;
           tc::fence_after_sync();
-          const uint32_t v0 = smem_u32(sm + L::kOffV + st * L::kVBytes);
-          if (elect_one()) {
-            if (h == 0 || both)
+          const uint32_t vc = v0 + st * L::kVBytes;
+          if (h == 0 || both)
 #pragma unroll
-              for (int nb = 0; nb < L::kBlocks; ++nb)
+            for (int nb = 0; nb < L::kBlocks; ++nb)
 #pragma unroll
-                for (int part = 0; part < (kLo ? 2 : 1); ++part)
+              for (int part = 0; part < (kLo ? 2 : 1); ++part)
 #pragma unroll
-                  for (int kk = 0; kk < kHalf / 16; ++kk)
-                    tc2::mma(tmem + kOCol + 128 * nb,
-                             tc::smem_desc(p0 + (2 * part + h) * kSlab + kk * 32, 16, 1024),
-                             tc::smem_desc(v0 + 2 * nb * kSlab + kk * 2048, kSlab, 1024),
-                             L::kIdescPV, j > 0 || h > 0 || part > 0 || kk > 0);
-            tc2::commit_both(bars + L::kEmptyV + st);
-            tc2::commit_both(bars + L::kPvDone + h);
-          }
-          __syncwarp();
+                for (int kk = 0; kk < kHalf / 16; ++kk)
+                  tc2::mma(tmem + kOCol + 128 * nb,
+                           tc::smem_desc(p0 + (2 * part + h) * kSlab + kk * 32, 16, 1024),
+                           tc::smem_desc(vc + 2 * nb * kSlab + kk * 2048, kSlab, 1024), L::kIdescPV,
+                           j > 0 || h > 0 || part > 0 || kk > 0, lead);
+          tc2::commit_both(bars + L::kEmptyV + st, lead);
+          tc2::commit_both(bars + L::kPvDone + h, lead);
         }
       }
-    if (elect_one()) tc2::commit_both(bars + L::kDrainV);
+    tc2::commit_both(bars + L::kDrainV, lead);
     __syncwarp();
   } else if (warp == 2) {
-    // ---- Q of every piece (this CTA's 64 columns; behind the row's last column: other rows' or
-    // zeros), and this CTA's share of the scores' tiles into L2, kAhead tiles before their scores
-    PageCache pages;
-    int g = 0, k = 0;
+    // ---- Q of every piece (this CTA's 64 columns; behind the row's last column: other rows' or zeros)
+    int k = 0;
     const int cols = a.num_tokens * a.num_q_heads;
     for (int u = first; find_piece(a, u, rows, lane, pc); u += step) {
       if (pc.n == 0) continue;
@@ -601,22 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
       __syncwarp();
       ++k;
-      if (a.page_size % kHalf != 0) continue;
-      pages.base = -1;
-      const int n_slots = (pc.len + a.page_size - 1) / a.page_size;
-      int key = pc.t0 * kKeys + kHalf * (int)rank;
-      Place at(key, a.page_size);
-      for (int j = 0; j < pc.n; ++j, ++g) {
-        for (uint32_t i = 0; i < kWaitPolls && *scored < g - kAhead && !*abort_flag; ++i) __nanosleep(64);
-        if (j >= 1 && key < pc.len) {  // (the first tile's copies are already on their way)
-          const int page = pages.get(a.page_tables + (size_t)pc.b * a.table_stride, at.slot, n_slots, lane);
-          if (page >= 0 && (long long)page < a.num_pages && elect_one())
-            tc2::tma_prefetch_3d(&maps.ahead, 0, page * a.page_size + at.row, 0);
-          __syncwarp();
-        }
-        key += kKeys;
-        at.step(kKeys, a.page_size);
-      }
     }
     if (rank == 0 && k > 0) mbar_wait(bars + L::kQFull, (k - 1) & 1);
   } else if (warp == 3 || warp == 12 || warp == 13) {
@@ -665,8 +636,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::reg_fence(v);
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc2::arrive_pair(s_free + 8 * r);
-        if (threadIdx.x == 128) *scored = g + 1;
         float x[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]);
@@ -743,7 +712,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::fence_smem_for_async();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc2::arrive_pair(p_full);
+        if (lane == 0) {
+          tc2::arrive_pair(p_full);
+          // S(j + 2) may take the region: not earlier, as the tensor pipe takes products in order
+          // and scores that are not needed yet would hold up this tile's values
+          tc2::arrive_pair(s_free + 8 * r);
+        }
       }
       // ---- the row's sum over its four threads, then its columns: this thread's are
       // 128 kh + [0, 128) of one 256 (DC = 256: half of them)
@@ -958,8 +932,7 @@ cudaError_t launch(const LatentAttnArgs &a, cudaStream_t s) {
       !tc2::make_slab_map(&maps.k, a.pool, a.num_pages * a.page_size, DC + 64, whole ? kHalf : 16,
                           whole ? L::kChunkSlabs : 1) ||
       !tc2::make_block_map(&maps.v, a.pool, a.num_pages * a.page_size, DC + 64, DC / 256,
-                           whole ? kHalf : 16, whole ? 2 : 1, whole ? DC / 256 : 1) ||
-      !tc2::make_slab_map(&maps.ahead, a.pool, a.num_pages * a.page_size, DC + 64, kHalf, L::kSlabs))
+                           whole ? kHalf : 16, whole ? 2 : 1, whole ? DC / 256 : 1))
     return cudaErrorInvalidValue;
   return launch_pdl(pskv_attn_latent<DC, kLo>, dim3(2 * (unsigned)a.clusters), dim3(kThreads),
                     L::kSmemBytes, s, a, maps);

@@ -31,6 +31,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
+// Whether a phase is complete, without suspending the thread.
+__device__ __forceinline__ bool phase_done(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The wait of a thread that runs a role by itself: the abort flag is looked at only
 // where the phase is not yet complete (a whole-warp tc_wait with its vote costs 188
 // cycles on a phase that is, this one 52).
