@@ -102,8 +102,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
   uint32_t *slot = reinterpret_cast<uint32_t *>(sm + kOffSlot);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffAbort);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc2::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = tc2::cluster_rank();
+  const bool lead = elect_one();  // one thread of each warp
   const int h = blockIdx.x >> 1, b = blockIdx.z;
 
   pdl_wait();
@@ -154,10 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   tc2::cluster_sync();  // both CTAs' barriers are set up
   tc::fence_after_sync();
   const uint32_t tmem = *slot;
-  auto wait1 = [&](int s, uint32_t parity) {
-    return tc::one_wait(bars + s, parity, abort_flag, a.status);
-  };
-
   auto wait = [&](int s, uint32_t parity) {
     return tc::all_wait(bars + s, parity, abort_flag, a.status);
   };
@@ -165,7 +162,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (warp == 0) {
     if (rank == 0) {
       // ---- the score products (all lanes alike, one issues)
-      const bool lead = elect_one();
       bool ok = wait(kQFull, 0);
       const uint32_t q = smem_u32(sm + kOffQ), k = smem_u32(sm + kOffK);
       for (int j = 0; ok && j < n; ++j) {
@@ -189,7 +185,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == 1) {
     if (rank == 0) {
       // ---- the value products
-      const bool lead = elect_one();
       bool ok = true;
       const uint32_t v = smem_u32(sm + kOffV);
       for (int j = 0; ok && j < n; ++j) {
@@ -212,27 +207,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    if (elect_one()) {
-      // ---- Q (queries behind the row's last: other rows' or zeros), then K: this CTA's half
-      if (rank == 0) mbar_arrive_expect_tx(bars + kQFull, 2 * kQBytes);
-      tc2::tma_load_3d(smem_u32(sm + kOffQ), &maps.q, 0, q0 + t0 + (int)rank * kRows, kQSlabs * h,
-                       tc2::map_to(smem_u32(bars + kQFull), 0));
-      int j = 0;
-      for (; j < n; ++j) {
-        const int st = j % kRing;
-        if (j >= kRing && !wait1(kEmptyK + st, (j / kRing - 1) & 1)) break;
-        const uint32_t dst = smem_u32(sm + kOffK + st * kKBytes);
-        const uint32_t bar = tc2::map_to(smem_u32(bars + kFullK + st), 0);
-        const int y = k0 + j * kKeys + kHalf * (int)rank;
-        if (rank == 0) mbar_arrive_expect_tx(bars + kFullK + st, 2 * kKBytes);
-        tc2::tma_load_3d(dst, &maps.k, 0, y, 4 * h, bar);
-        tc2::tma_load_3d(dst + 2 * kKSlab, &maps.rot, 0, y, 0, bar);
-      }
-      // every copy of both CTAs landed before they leave (their count is the even CTA's)
-      if (rank == 0) {
-        for (int s = max(0, j - kRing); s < j; ++s) mbar_wait(bars + kFullK + s % kRing, (s / kRing) & 1);
-        mbar_wait(bars + kQFull, 0);
-      }
+    // ---- Q (queries behind the row's last: other rows' or zeros), then K: this CTA's half
+    tc2::expect_tx(bars + kQFull, 2 * kQBytes, lead && rank == 0);
+    tc2::tma_load_3d(smem_u32(sm + kOffQ), &maps.q, 0, q0 + t0 + (int)rank * kRows, kQSlabs * h,
+                     tc2::map_to(smem_u32(bars + kQFull), 0), lead);
+    int j = 0;
+    for (; j < n; ++j) {
+      const int st = j % kRing;
+      if (j >= kRing && !wait(kEmptyK + st, (j / kRing - 1) & 1)) break;
+      const uint32_t dst = smem_u32(sm + kOffK + st * kKBytes);
+      const uint32_t bar = tc2::map_to(smem_u32(bars + kFullK + st), 0);
+      const int y = k0 + j * kKeys + kHalf * (int)rank;
+      tc2::expect_tx(bars + kFullK + st, 2 * kKBytes, lead && rank == 0);
+      tc2::tma_load_3d(dst, &maps.k, 0, y, 4 * h, bar, lead);
+      tc2::tma_load_3d(dst + 2 * kKSlab, &maps.rot, 0, y, 0, bar, lead);
+    }
+    // every copy of both CTAs landed before they leave (their count is the even CTA's)
+    if (rank == 0) {
+      for (int s = max(0, j - kRing); s < j; ++s) mbar_wait(bars + kFullK + s % kRing, (s / kRing) & 1);
+      mbar_wait(bars + kQFull, 0);
     }
     __syncwarp();
   } else if (warp == 3) {
@@ -240,26 +233,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // behind it are another row's and meet P = 0, so they are zeroed first.
     const bool ragged = n * kKeys > nk;
     const int last = n - 1;
-    if (elect_one()) {
-      int j = 0;
-      for (; j < n; ++j) {
-        const int st = j % kRing;
-        if (j >= kRing && !wait1(kEmptyV + st, (j / kRing - 1) & 1)) break;
-        const uint32_t full = tc2::map_to(smem_u32(bars + kFullV + st), 0);
-        const bool whole = !(ragged && j == last);
-        if (!whole)
-          mbar_arrive_expect_tx(bars + kRagged, kVBytes);
-        else if (rank == 0)
-          mbar_arrive_expect_tx(bars + kFullV + st, 2 * kVBytes);
-        tc2::tma_load_3d(smem_u32(sm + kOffV + st * kVBytes), &maps.v, 0, k0 + j * kKeys,
-                         4 * h + 2 + (int)rank, whole ? full : smem_u32(bars + kRagged));
-        if (whole) tc2::arrive_pair(full);
-      }
-      if (ragged && j == n) mbar_wait(bars + kRagged, 0);  // (bounded)
-      if (rank == 0)
-        for (int s = max(0, j - kRing); s < j; ++s)
-          if (!(ragged && s == last)) mbar_wait(bars + kFullV + s % kRing, (s / kRing) & 1);
+    int j = 0;
+    for (; j < n; ++j) {
+      const int st = j % kRing;
+      if (j >= kRing && !wait(kEmptyV + st, (j / kRing - 1) & 1)) break;
+      const uint32_t full = tc2::map_to(smem_u32(bars + kFullV + st), 0);
+      const bool whole = !(ragged && j == last);
+      if (!whole)
+        tc2::expect_tx(bars + kRagged, kVBytes, lead);
+      else
+        tc2::expect_tx(bars + kFullV + st, 2 * kVBytes, lead && rank == 0);
+      tc2::tma_load_3d(smem_u32(sm + kOffV + st * kVBytes), &maps.v, 0, k0 + j * kKeys,
+                       4 * h + 2 + (int)rank, whole ? full : smem_u32(bars + kRagged), lead);
+      tc2::arrive_pair(full, lead && whole);
     }
+    __syncwarp();
+    if (ragged && j == n) mbar_wait(bars + kRagged, 0);  // (bounded)
+    if (rank == 0)
+      for (int s = max(0, j - kRing); s < j; ++s)
+        if (!(ragged && s == last)) mbar_wait(bars + kFullV + s % kRing, (s / kRing) & 1);
     __syncwarp();
     if (ragged) {
       const int st = last % kRing, left = nk - last * kKeys;
@@ -268,10 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         *reinterpret_cast<uint4 *>(dst + (left + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
       tc::fence_smem_for_async();
       __syncwarp();
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive(bars + kFullV + st);  // in place of the copies' count
-        tc2::arrive_pair(tc2::map_to(smem_u32(bars + kFullV + st), 0));
-      }
+      if (rank == 0 && lead) mbar_arrive(bars + kFullV + st);  // in place of the copies' count
+      tc2::arrive_pair(tc2::map_to(smem_u32(bars + kFullV + st), 0), lead);
     }
   } else {
     // ---- the softmax: thread (query i, keys 64 gr .. + 63 of the tile).  The loop never leaves
@@ -299,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       tc::reg_fence(vb);
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc2::arrive_pair(s_free + 8 * r);
+      tc2::arrive_pair(s_free + 8 * r, lead);
       float f[kHalf];
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
@@ -310,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       // scores in log2 units are mul * f: whole tiles leave the product to the exponent's
       // multiply-add, others (and scales that are not positive) take it before the mask
       float mul = sc;
-      if (key0 + kHalf > lim || !(sc > 0.f)) {
+      if (__any_sync(0xffffffffu, key0 + kHalf > lim || !(sc > 0.f))) {
         mul = 1.f;
 #pragma unroll
         for (int c = 0; c < kHalf; ++c) f[c] = key0 + c < lim ? f[c] * sc : -CUDART_INF_F;
@@ -365,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc2::arrive_pair(p_full + 8 * pb);
+      tc2::arrive_pair(p_full + 8 * pb, lead);
     }
     // ---- the sum over both threads, then O / l, put together in the queries' place and the K
     // ring (their products are done) so that rows leave in whole lines

@@ -177,6 +177,17 @@ __device__ __forceinline__ bool find_piece(const LatentAttnArgs &a, int u, const
                                            Piece &pc) {
   const int blocks = (a.num_tokens * a.num_q_heads + 127) / 128;
   const int unit = blocks == 1 ? u : u / blocks;
+  if (a.batch == 1) {
+    pc.b = 0;
+    pc.cb = u - unit * blocks;
+    pc.len = tc2::uniform(r.len);
+    const int tiles = tiles_of(pc.len);
+    pc.count = max(1, (tiles + r.q - 1) / r.q);
+    pc.p = unit;
+    pc.t0 = min(unit * r.q, tiles);
+    pc.n = min(pc.t0 + r.q, tiles) - pc.t0;
+    return unit < pc.count;
+  }
   int base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     bool bad;
@@ -193,9 +204,9 @@ __device__ __forceinline__ bool find_piece(const LatentAttnArgs &a, int u, const
       const int l = __ffs(past) - 1;
       pc.b = b0 + l;
       pc.cb = u - unit * blocks;
-      pc.len = __shfl_sync(0xffffffffu, len, l);
-      pc.count = __shfl_sync(0xffffffffu, n, l);
-      pc.p = unit - base - __shfl_sync(0xffffffffu, incl - n, l);
+      pc.len = tc2::uniform(__shfl_sync(0xffffffffu, len, l));
+      pc.count = tc2::uniform(__shfl_sync(0xffffffffu, n, l));
+      pc.p = tc2::uniform(unit - base - __shfl_sync(0xffffffffu, incl - n, l));
       const int tiles = tiles_of(pc.len);
       pc.t0 = min(pc.p * r.q, tiles);
       pc.n = min(pc.t0 + r.q, tiles) - pc.t0;
@@ -214,7 +225,7 @@ struct Maps {
 // without a division.
 struct Place {
   int slot, row;
-  __device__ Place(int key, int page_size) : slot(key / page_size), row(key % page_size) {}
+  __device__ Place(int key, int page_size) : slot(key / page_size) { row = key - slot * page_size; }
   __device__ void step(int keys, int page_size) {
     row += keys;
     while (row >= page_size) {
@@ -244,14 +255,15 @@ struct Loader {
   volatile int *abort_flag;
   uint32_t rank;
   int lane;
+  bool lead;
   bool whole;  // pages of whole half tiles: boxes of 64 rows (else of 16)
   PageCache pages;
   int which;                 // of the kWarps
   int seq = 0, ragged = 0;   // chunks of all warps, chunks of this one landed on kRagged, over all pieces
 
   __device__ Loader(const LatentAttnArgs &a_, const CUtensorMap *m, unsigned char *sm_,
-                    uint64_t *bars_, volatile int *ab, uint32_t rank_, int which_)
-      : a(a_), map(m), sm(sm_), bars(bars_), abort_flag(ab), rank(rank_), which(which_) {
+                    uint64_t *bars_, volatile int *ab, uint32_t rank_, bool lead_, int which_)
+      : a(a_), map(m), sm(sm_), bars(bars_), abort_flag(ab), rank(rank_), lead(lead_), which(which_) {
     lane = threadIdx.x & 31;
     whole = a.page_size % kHalf == 0;
   }
@@ -325,32 +337,30 @@ struct Loader {
     const int st = seq % kRing;
     const uint32_t dst = smem_u32(sm + L::kOffK + st * L::kKBytes);
     const uint32_t bar = tc2::map_to(smem_u32(bars + L::kFullK + st), 0);
-    if (elect_one()) {
-      uint32_t rows = 0;  // both CTAs'
-      if (whole)
-        rows = (ys[0] >= 0 ? kHalf : 0) + (ys[1] >= 0 ? kHalf : 0);
-      else
+    uint32_t rows = 0;  // both CTAs'
+    if (whole)
+      rows = (ys[0] >= 0 ? kHalf : 0) + (ys[1] >= 0 ? kHalf : 0);
+    else
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rows += ys[i] >= 0 ? 16 : 0;
-      if (rank == 0) mbar_arrive_expect_tx(bars + L::kFullK + st, rows * 128 * L::kChunkSlabs);
-      if (whole) {
-        const int y = rank == 0 ? ys[0] : ys[1];
-        if (y >= 0) tc2::tma_load_3d(dst, map, 0, y, c * L::kChunkSlabs, bar);
-      } else {
+      for (int i = 0; i < 8; ++i) rows += ys[i] >= 0 ? 16 : 0;
+    tc2::expect_tx(bars + L::kFullK + st, rows * 128 * L::kChunkSlabs, lead && rank == 0);
+    if (whole) {
+      const int y = rank == 0 ? ys[0] : ys[1];
+      tc2::tma_load_3d(dst, map, 0, y, c * L::kChunkSlabs, bar, lead && y >= 0);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int y = rank == 0 ? ys[i] : ys[4 + i];
-          if (y < 0) continue;
-          for (int s = 0; s < L::kChunkSlabs; ++s)
-            tc2::tma_load_3d(dst + s * kSlab + i * 16 * 128, map, 0, y, c * L::kChunkSlabs + s, bar);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int y = rank == 0 ? ys[i] : ys[4 + i];
+        for (int s = 0; s < L::kChunkSlabs; ++s)
+          tc2::tma_load_3d(dst + s * kSlab + i * 16 * 128, map, 0, y, c * L::kChunkSlabs + s, bar,
+                           lead && y >= 0);
       }
-      if (c == 0) {
-        const int tile = seq / kChunks;
-        if (bad && rank == 0) raise_fault(a.status, PSKV_FAULT_BAD_PAGE);
-        reinterpret_cast<TileInfo *>(sm + L::kOffInfo)[tile % kInfo].bad = bad;
-        mbar_arrive(bars + L::kInfoFull + tile % kInfo);
-      }
+    }
+    if (c == 0 && lead) {
+      const int tile = seq / kChunks;
+      if (bad && rank == 0) raise_fault(a.status, PSKV_FAULT_BAD_PAGE);
+      reinterpret_cast<TileInfo *>(sm + L::kOffInfo)[tile % kInfo].bad = bad;
+      mbar_arrive(bars + L::kInfoFull + tile % kInfo);
     }
     __syncwarp();
   }
@@ -368,7 +378,7 @@ struct Loader {
     const bool dead = vhi <= h * kHalf;
     uint64_t *rag = bars + L::kRagged + which;
     const uint32_t bar = plain ? full : smem_u32(rag);
-    if (!dead && elect_one()) {
+    if (!dead) {
       uint32_t rows = 0;
       if (whole)
         rows = (h == 0 ? ys[0] : ys[1]) >= 0 ? kHalf : 0;
@@ -377,26 +387,25 @@ struct Loader {
         for (int i = 0; i < 4; ++i) rows += (h == 0 ? ys[i] : ys[4 + i]) >= 0 ? 16 : 0;
       const uint32_t bytes = rows * 256 * L::kBlocks;
       if (!plain)
-        mbar_arrive_expect_tx(rag, bytes);
-      else if (rank == 0)
-        mbar_arrive_expect_tx(own_full, 2 * bytes);
+        tc2::expect_tx(rag, bytes, lead);
+      else
+        tc2::expect_tx(own_full, 2 * bytes, lead && rank == 0);
       if (whole) {
         const int y = h == 0 ? ys[0] : ys[1];
-        if (y >= 0) tc2::tma_load_4d(dst, map, 0, y, 2 * (int)rank, 0, bar);
+        tc2::tma_load_4d(dst, map, 0, y, 2 * (int)rank, 0, bar, lead && y >= 0);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int y = h == 0 ? ys[i] : ys[4 + i];
-          if (y < 0) continue;
           for (int s = 0; s < 2 * L::kBlocks; ++s)
             tc2::tma_load_4d(dst + s * kSlab + i * 16 * 128, map, 0, y, 2 * (int)rank + (s & 1),
-                             s >> 1, bar);
+                             s >> 1, bar, lead && y >= 0);
         }
       }
     }
-    __syncwarp();
     if (!plain && !dead) {
       // rows behind the end or of skipped groups may hold anything and meet P = 0: zero them
+      __syncwarp();
       mbar_wait(rag, ragged & 1);  // (bounded; landed or given up on, the chunk is passed on)
       ++ragged;
       for (int e = lane; e < kHalf * 16 * L::kBlocks; e += 32) {
@@ -408,10 +417,9 @@ struct Loader {
       tc::fence_smem_for_async();
       __syncwarp();
     }
-    if (lane == 0) {
-      if (!plain && rank == 0) mbar_arrive(own_full);  // in place of the copies' count
-      tc2::arrive_pair(full);
-    }
+    if (!plain && lead && rank == 0) mbar_arrive(own_full);  // in place of the copies' count
+    tc2::arrive_pair(full, lead);
+    __syncwarp();
   }
 
   // Wait (bounded) for the last copies into each stage, of both CTAs (their count is the even CTA's).
@@ -448,8 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kOffBar);
   uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::kOffSlot);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kOffAbort);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc2::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = tc2::cluster_rank();
+  const bool lead = elect_one();  // one thread of each warp
   if (sm + L::kUsed > smem_raw + L::kSmemBytes) {  // (never seen) no room for the alignment
     raise_fault(a.status, PSKV_FAULT_WAIT_TIMEOUT);
     return;
@@ -507,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (warp == 0 && rank == 0) {
     // ---- the score products (all lanes alike, one issues)
-    const bool lead = elect_one();
     bool ok = true;
     int seq = 0, g = 0, k = 0;  // chunks, tiles, pieces so far
     const uint32_t q0 = smem_u32(sm + L::kOffQ), k0 = smem_u32(sm + L::kOffK);
@@ -541,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ---- the value products
-    const bool lead = elect_one();
     bool ok = true;
     int g = 0;
     const uint32_t p0 = smem_u32(sm + L::kOffP), v0 = smem_u32(sm + L::kOffV);
@@ -580,12 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int u = first; find_piece(a, u, rows, lane, pc); u += step) {
       if (pc.n == 0) continue;
       if (k > 0 && !wait(L::kQFree, (k - 1) & 1)) break;
-      if (elect_one()) {
-        if (rank == 0) mbar_arrive_expect_tx(bars + L::kQFull, 2 * L::kQBytes);
-        tc2::tma_load_3d(smem_u32(sm + L::kOffQ), &maps.q, 0,
-                         pc.b * cols + pc.cb * 128 + (int)rank * kRows, 0,
-                         tc2::map_to(smem_u32(bars + L::kQFull), 0));
-      }
+      tc2::expect_tx(bars + L::kQFull, 2 * L::kQBytes, lead && rank == 0);
+      tc2::tma_load_3d(smem_u32(sm + L::kOffQ), &maps.q, 0,
+                       pc.b * cols + pc.cb * 128 + (int)rank * kRows, 0,
+                       tc2::map_to(smem_u32(bars + L::kQFull), 0), lead);
       __syncwarp();
       ++k;
     }
@@ -593,9 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == 3 || warp == 12 || warp == 13) {
     const int which = warp == 3 ? 0 : warp - 11;
     if (which < L::kRingK)
-      Loader<DC, kLo, false>(a, &maps.k, sm, bars, abort_flag, rank, which).run_all(rows, first, step);
+      Loader<DC, kLo, false>(a, &maps.k, sm, bars, abort_flag, rank, lead, which).run_all(rows, first, step);
   } else if (warp >= 14) {
-    Loader<DC, kLo, true>(a, &maps.v, sm, bars, abort_flag, rank, warp - 14).run_all(rows, first, step);
+    Loader<DC, kLo, true>(a, &maps.v, sm, bars, abort_flag, rank, lead, warp - 14).run_all(rows, first, step);
   } else if (warp >= 4 && warp <= 11) {
     // ---- the softmax: thread (row i, keys 64 kh + 32 gr .. + 31 of the tile).  The loops never
     // leave early (the four warps of a row's threads meet every tile); after a failed wait
@@ -644,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // selection: rows never loaded may hold anything)
         const int key0 = (pc.t0 + j) * kKeys + kHalf * kh + 32 * gr;
         float mul = sc;
-        if (key0 + 32 > lim || bad != 0 || !(sc > 0.f)) {
+        if (__any_sync(0xffffffffu, key0 + 32 > lim || bad != 0 || !(sc > 0.f))) {
           mul = 1.f;
 #pragma unroll
           for (int c = 0; c < 32; ++c)
@@ -712,12 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::fence_smem_for_async();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
-          tc2::arrive_pair(p_full);
-          // S(j + 2) may take the region: not earlier, as the tensor pipe takes products in order
-          // and scores that are not needed yet would hold up this tile's values
-          tc2::arrive_pair(s_free + 8 * r);
-        }
+        tc2::arrive_pair(p_full, lead);
+        // S(j + 2) may take the region: not earlier, as the tensor pipe takes products in order
+        // and scores that are not needed yet would hold up this tile's values
+        tc2::arrive_pair(s_free + 8 * r, lead);
       }
       // ---- the row's sum over its four threads, then its columns: this thread's are
       // 128 kh + [0, 128) of one 256 (DC = 256: half of them)

@@ -58,13 +58,18 @@ __device__ __forceinline__ bool one_wait(uint64_t *bar, uint32_t parity, volatil
   return false;
 }
 
-// The same for a whole warp, one answer for all lanes.
+// The same for a whole warp that stays together: every poll ends in a vote, so the code
+// around it keeps its uniform registers.  (One lane polling for the others takes the warp apart and
+// made the latent kernel's tiles twice as slow.)
 __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                          int32_t *status) {
-  const bool now = mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, now)) return true;
-  const bool later = now || one_wait(bar, parity, abort_flag, status);
-  return __all_sync(0xffffffffu, later);
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 15u) == 15u && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
+  }
+  *abort_flag = 1;
+  raise_fault(status, PSKV_FAULT_WAIT_TIMEOUT);
+  return false;
 }
 
 __device__ __forceinline__ bool elect_one() {

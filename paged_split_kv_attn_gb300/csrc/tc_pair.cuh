@@ -15,6 +15,10 @@
 namespace pskv {
 namespace tc2 {
 
+// Operations of one thread take `lead` and are predicated on it: the warp that issues them
+// stays together, and addresses and descriptors stay in uniform registers (inside a branch of one
+// thread the same instructions ran several times slower).
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -37,9 +41,16 @@ __device__ __forceinline__ void cluster_sync() {
 // CTA's memory here: what crosses is read by the tensor core, after the writer's
 // fence.proxy.async, so the arrival keeps the CTA-scope release of a local one (a cluster-scope
 // one waits for a memory barrier of ~1,000 cycles, twice a tile).
-__device__ __forceinline__ void arrive_pair(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void arrive_pair(uint32_t bar, bool lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"((uint32_t)lead)
+      : "memory");
 }
+
+// A value that is the same in every lane, known as such to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // D[tmem] (+)= A * B over the pair.  The whole warp calls; the thread with `lead` (one of the
 // even CTA's) issues.  Called so, in code that all lanes run alike, the descriptors stay in
@@ -84,24 +95,36 @@ __device__ __forceinline__ void dealloc(uint32_t tmem, uint32_t cols) {
                : "memory");
 }
 
-// 3-D tensor copy global -> this CTA's shared memory, completion counted on a
-// barrier of either CTA of the pair.  x * 2 bytes is a multiple of 16.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                            int z, uint32_t bar) {
+// The leading thread arrives and expects `bytes` more.
+__device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes, bool lead) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "{\n\t.reg .pred q;\n\t.reg .b64 st;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes), "r"((uint32_t)lead)
+      : "memory");
+}
+
+// 3-D tensor copy global -> this CTA's shared memory, completion counted on a
+// barrier of either CTA of the pair, by the leading thread.  x * 2 bytes is a multiple of 16.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, uint32_t bar, bool lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"((uint32_t)lead)
       : "memory");
 }
 
 // The same for a 4-D map.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                            int z, int w, uint32_t bar) {
+                                            int z, int w, uint32_t bar, bool lead) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar),
+      "r"((uint32_t)lead)
       : "memory");
 }
 
