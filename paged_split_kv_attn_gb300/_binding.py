@@ -593,34 +593,74 @@ def prefill_attn_paged(layout: Layout, q, cu_q, cu_q_host, page_tables, seq_lens
 
 
 # ---- the latent cache and the drafts' verification --------------------------------
+#
+# These calls are short on the GPU, so their checks are written to cost little on the host: one
+# comparison per property, the reason found out only where one fails.
 
-def _here(name: str, *tensors) -> None:
-    """The tensors of one call lie on the current device, where its kernels run."""
-    current = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != current:
-            raise ValueError(f"{name}: a tensor on {t.device}, the current device is cuda:{current}")
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype=torch.bfloat16) -> int:
-    """A tensor of the given shape whose last dimension is contiguous (others may be strided)."""
+def _complain(t, name: str, shape, dtype, dev: int):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _shaped(t: torch.Tensor, name: str, shape, dtype) -> int:
-    """A contiguous CUDA tensor of the given shape and type."""
-    ptr = _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return ptr
+def _ptr(t, name: str, shape, dtype, dev: int) -> int:
+    """A contiguous tensor of this shape and type on the current device: its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _complain(t, name, shape, dtype, dev)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name: str, shape, dev: int) -> int:
+    """The same for bf16 rows: only the last dimension has to be contiguous."""
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev and \
+                (shape[-1] == 1 or t.stride(-1) == 1):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _complain(t, name, shape, torch.bfloat16, dev)
+    raise ValueError(f"{name} must have unit column stride")
+
+
+def _lens_i32(x, name: str):
+    """Host int32 array: a list of whole numbers at once, anything else as _host_i32 takes it."""
+    if type(x) is list:
+        try:
+            return (ctypes.c_int32 * len(x))(*x)
+        except TypeError:
+            pass
+    return _host_i32(x, name)
+
+
+def _stream_on(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else _stream(stream)
+
+
+_OUT_CODES = {torch.bfloat16: PSKV_DTYPE_BF16, torch.float32: PSKV_DTYPE_F32}
+
+
+def _out_like(out, shape, like, out_dtype, dev: int):
+    """The output tensor (made if not given), its address and its dtype's code."""
+    if out is None:
+        out = like.new_empty(shape) if out_dtype is None or out_dtype is like.dtype else \
+            torch.empty(shape, device=like.device, dtype=out_dtype)
+    code = _OUT_CODES.get(out.dtype)
+    if code is None:
+        code = _dtype_code(out.dtype)
+    return out, _ptr(out, "out", shape, out.dtype, dev), code
 
 
 def kv_prep_append_latent(layout: Layout, x, row_of, pos_of, page_tables, pages_of_row, eps: float,
@@ -633,53 +673,53 @@ def kv_prep_append_latent(layout: Layout, x, row_of, pos_of, page_tables, pages_
     tensor twice turns in place) are the queries' rotated columns.  ``pairs`` is
     "halves" (i, i + 32) or "adjacent" (2i, 2i + 1).  ``host`` = (row_of, pos_of,
     pages_of_row) host copies for the up-front refusal."""
-    lib = load_library()
-    n, d = int(row_of.numel()), layout.desc.head_dim_k
-    _here("kv_prep_append_latent", x, row_of, pos_of, page_tables, pages_of_row, w, rope_cos, rope_sin,
-          first_pos, q, q_out, dense, layout.k_pool)
+    lib = _LIB or load_library()
+    dev = _current_device()
+    i32, f32, d = torch.int32, torch.float32, layout.desc.head_dim_k
+    if layout.k_pool.get_device() != dev:
+        raise ValueError(f"the pool is on {layout.k_pool.device}, the current device is cuda:{dev}")
+    n, half = row_of.numel(), PSKV_LATENT_ROT // 2
+    shape = (n,)
+    batch, stride = page_tables.shape
     if pairs not in ("halves", "adjacent"):
         raise ValueError("pairs must be 'halves' or 'adjacent'")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     hr = hp = hl = None
     if host is not None:
-        hr, hp, hl = (_host_i32(v, name) for v, name in zip(host, ("row_of", "pos_of", "pages")))
-        if len(hr) != n or len(hp) != n or len(hl) != pages_of_row.numel():
+        hr, hp, hl = (_lens_i32(v, name) for v, name in zip(host, ("row_of", "pos_of", "pages")))
+        if len(hr) != n or len(hp) != n or len(hl) != batch:
             raise ValueError("host copies must be as long as the arrays they copy")
-    half = PSKV_LATENT_ROT // 2
-    if rope_cos.dim() != 2 or rope_cos.shape != rope_sin.shape or rope_cos.shape[1] != half:
-        raise ValueError(f"rope_cos and rope_sin must be [positions, {half}]")
-    desc = LatentPrepDesc(eps=eps, pairs=PSKV_PAIRS_ADJACENT if pairs == "adjacent" else
-                          PSKV_PAIRS_HALVES,
-                          w=None if w is None else _shaped(w, "w", (d - PSKV_LATENT_ROT,), torch.float32),
-                          rope_cos=_dev(rope_cos, "rope_cos", torch.float32),
-                          rope_sin=_dev(rope_sin, "rope_sin", torch.float32),
-                          max_pos=rope_cos.shape[0])
+    table = (rope_cos.shape[0], half)
+    desc = LatentPrepDesc(eps, PSKV_PAIRS_ADJACENT if pairs == "adjacent" else PSKV_PAIRS_HALVES,
+                          None if w is None else _ptr(w, "w", (d - PSKV_LATENT_ROT,), f32, dev),
+                          _ptr(rope_cos, "rope_cos", table, f32, dev),
+                          _ptr(rope_sin, "rope_sin", table, f32, dev), table[0])
     if q is not None and q.shape[1] > 0:
-        desc.num_q_heads = q.shape[1]
-        desc.q = _rows(q, "q", (n, q.shape[1], PSKV_LATENT_ROT))
-        desc.q_out = _rows(q_out, "q_out", (n, q.shape[1], PSKV_LATENT_ROT))
-        desc.q_token, desc.q_head = q.stride(0), q.stride(1)
-        desc.q_out_token, desc.q_out_head = q_out.stride(0), q_out.stride(1)
-        if n > 1 and desc.q_out_token < PSKV_LATENT_ROT or \
-                q.shape[1] > 1 and desc.q_out_head < PSKV_LATENT_ROT:
+        heads = q.shape[1]
+        desc.num_q_heads = heads
+        desc.q = _rows(q, "q", (n, heads, PSKV_LATENT_ROT), dev)
+        desc.q_out = _rows(q_out, "q_out", (n, heads, PSKV_LATENT_ROT), dev)
+        desc.q_token, desc.q_head, _ = q.stride()
+        token, head, _ = q_out.stride()
+        desc.q_out_token, desc.q_out_head = token, head
+        if n > 1 and token < PSKV_LATENT_ROT or heads > 1 and head < PSKV_LATENT_ROT:
             raise ValueError("q_out's rows must not overlap")
     _check(lib.kv_prep_append_latent(
-        layout.handle, ctypes.byref(desc), _rows(x, "x", (n, d)), x.stride(0) if n > 1 else d, n,
-        _dev(row_of, "row_of", torch.int32), _shaped(pos_of, "pos_of", row_of.shape, torch.int32),
-        None if first_pos is None else _shaped(first_pos, "first_pos", pages_of_row.shape, torch.int32),
-        _dev(page_tables, "page_tables", torch.int32), page_tables.shape[1],
-        _shaped(pages_of_row, "pages_of_row", page_tables.shape[:1], torch.int32),
-        pages_of_row.numel(), hr, hp, hl,
-        None if dense is None else _shaped(dense, "dense", (n, d), torch.bfloat16),
-        _stream(stream)), "kv_prep_append_latent")
+        layout.handle, ctypes.byref(desc), _rows(x, "x", (n, d), dev), x.stride(0) if n > 1 else d, n,
+        _ptr(row_of, "row_of", shape, i32, dev), _ptr(pos_of, "pos_of", shape, i32, dev),
+        None if first_pos is None else _ptr(first_pos, "first_pos", (batch,), i32, dev),
+        _ptr(page_tables, "page_tables", (batch, stride), i32, dev), stride,
+        _ptr(pages_of_row, "pages_of_row", (batch,), i32, dev), batch, hr, hp, hl,
+        None if dense is None else _ptr(dense, "dense", (n, d), torch.bfloat16, dev),
+        _stream_on(stream, dev)), "kv_prep_append_latent")
 
 
 def decode_attn_latent_workspace_bytes(layout: Layout, seq_lens_host, table_stride: int,
                                        num_tokens: int, num_q_heads: int,
                                        num_splits: int = 0) -> int:
     """Workspace bytes a decode_attn_latent call needs under its plan."""
-    lens_h = _host_i32(seq_lens_host, "seq_lens_host")
+    lens_h = _lens_i32(seq_lens_host, "seq_lens_host")
     out = ctypes.c_size_t()
     _check(load_library().decode_attn_latent_workspace_bytes(
         layout.handle, lens_h, table_stride, len(lens_h), num_tokens, num_q_heads, num_splits,
@@ -690,7 +730,7 @@ def decode_attn_latent_workspace_bytes(layout: Layout, seq_lens_host, table_stri
 def latent_workspace(layout: Layout, seq_lens_host, num_tokens: int, num_q_heads: int,
                      table_stride: int | None = None, num_splits: int = 0):
     """A scratch tensor for decode_attn_latent calls of these lengths (None: none needed)."""
-    lens_h = _host_i32(seq_lens_host, "seq_lens_host")
+    lens_h = _lens_i32(seq_lens_host, "seq_lens_host")
     if table_stride is None:
         table_stride = max(1, -(-max(lens_h) // layout.page_size))
     n = decode_attn_latent_workspace_bytes(layout, lens_h, table_stride, num_tokens, num_q_heads,
@@ -704,30 +744,33 @@ def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, 
     """Absorbed attention over a latent pool: ``q`` [batch, tokens, heads, latent +
     64], token t of row b at key ``seq_lens[b] - tokens + t``.  Returns ``out``
     [batch, tokens, heads, latent]; a row of length 0 gets zeros."""
-    lib = load_library()
-    if q.dim() != 4 or q.shape[3] != layout.desc.head_dim_k:
-        raise ValueError(f"q must be [batch, tokens, heads, {layout.desc.head_dim_k}]")
-    batch, tokens, hq = q.shape[0], q.shape[1], q.shape[2]
-    _here("decode_attn_latent", q, page_tables, seq_lens, workspace, out, layout.k_pool)
-    lens_h = _host_i32(seq_lens_host, "seq_lens_host")
+    lib = _LIB or load_library()
+    dev, desc = _current_device(), layout.desc
+    if q.dim() != 4:
+        raise ValueError(f"q must be [batch, tokens, heads, {desc.head_dim_k}]")
+    if layout.k_pool.get_device() != dev:
+        raise ValueError(f"the pool is on {layout.k_pool.device}, the current device is cuda:{dev}")
+    batch, tokens, hq, _ = q.shape
+    lens_h = _lens_i32(seq_lens_host, "seq_lens_host")
     if len(lens_h) != batch:
         raise ValueError("seq_lens_host must have one entry per row")
-    shape = (batch, tokens, hq, layout.desc.head_dim_v)
-    if out is None:
-        out = torch.empty(shape, device=q.device, dtype=out_dtype or torch.bfloat16)
+    qp = _ptr(q, "q", (batch, tokens, hq, desc.head_dim_k), torch.bfloat16, dev)
+    out, op, code = _out_like(out, (batch, tokens, hq, desc.head_dim_v), q, out_dtype, dev)
     stride = page_tables.shape[1]
     if workspace is None:
         workspace = _planned_workspace(decode_attn_latent_workspace_bytes(
             layout, lens_h, stride, tokens, hq, num_splits), q.device)
+    if workspace is None:
+        wp, size = None, 0
+    else:
+        wp = _ptr(workspace, "workspace", workspace.shape, workspace.dtype, dev)
+        size = workspace.numel() * workspace.element_size()
     opts = _opts(merge_group, events)
     _check(lib.decode_attn_latent(
-        layout.handle, _dev(q, "q", torch.bfloat16),
-        _shaped(page_tables, "page_tables", (batch, stride), torch.int32), stride, lens_h,
-        _shaped(seq_lens, "seq_lens", (batch,), torch.int32), batch, tokens, hq, float(scale),
-        num_splits, None if workspace is None else _dev(workspace, "workspace"),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _shaped(out, "out", shape, out.dtype), _dtype_code(out.dtype),
-        None if opts is None else ctypes.byref(opts), _stream(stream)), "decode_attn_latent")
+        layout._handle, qp, _ptr(page_tables, "page_tables", (batch, stride), torch.int32, dev), stride,
+        lens_h, _ptr(seq_lens, "seq_lens", (batch,), torch.int32, dev), batch, tokens, hq, scale,
+        num_splits, wp, size, op, code, None if opts is None else ctypes.byref(opts),
+        _stream_on(stream, dev)), "decode_attn_latent")
     return out
 
 
@@ -737,26 +780,23 @@ def prefill_attn_expanded(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale,
     [total_k, heads, 256] (each head's keys then values), ``k_rot`` [total_k, 64] (rows
     may be strided); row b's queries are the last of its keys.  Returns ``out``
     [total_q, heads, 128]."""
-    lib = load_library()
+    lib = _LIB or load_library()
+    dev, bf16, i32 = _current_device(), torch.bfloat16, torch.int32
     if q.dim() != 3 or kv.dim() != 3:
         raise ValueError("q and kv must be [tokens, heads, columns]")
-    _here("prefill_attn_expanded", q, kv, k_rot, cu_q, cu_k, out, status)
-    heads, cq, ck = q.shape[1], _host_i32(cu_q_host, "cu_q_host"), _host_i32(cu_k_host, "cu_k_host")
+    heads, cq, ck = q.shape[1], _lens_i32(cu_q_host, "cu_q_host"), _lens_i32(cu_k_host, "cu_k_host")
     batch = len(cq) - 1
     if batch < 1 or len(ck) != batch + 1:
         raise ValueError("cu_q_host and cu_k_host must have batch + 1 entries each")
-    shape = (cq[batch], heads, PSKV_EXPANDED_V)
-    if out is None:
-        out = torch.empty(shape, device=q.device, dtype=out_dtype or torch.bfloat16)
+    total_q, total_k, ends = cq[batch], ck[batch], (batch + 1,)
+    qp = _ptr(q, "q", (total_q, heads, PSKV_EXPANDED_NOPE + PSKV_LATENT_ROT), bf16, dev)
+    out, op, code = _out_like(out, (total_q, heads, PSKV_EXPANDED_V), q, out_dtype, dev)
     _check(lib.prefill_attn_expanded(
-        _shaped(q, "q", (cq[batch], heads, PSKV_EXPANDED_NOPE + PSKV_LATENT_ROT), torch.bfloat16),
-        _shaped(kv, "kv", (ck[batch], heads, PSKV_EXPANDED_NOPE + PSKV_EXPANDED_V), torch.bfloat16),
-        _rows(k_rot, "k_rot", (ck[batch], PSKV_LATENT_ROT)),
-        k_rot.stride(0) if ck[batch] > 1 else PSKV_LATENT_ROT, cq,
-        _shaped(cu_q, "cu_q", (batch + 1,), torch.int32), ck,
-        _shaped(cu_k, "cu_k", (batch + 1,), torch.int32), batch, heads, float(scale),
-        _shaped(out, "out", shape, out.dtype), _dtype_code(out.dtype),
-        None if status is None else _dev(status, "status", torch.int32), _stream(stream)),
+        qp, _ptr(kv, "kv", (total_k, heads, PSKV_EXPANDED_NOPE + PSKV_EXPANDED_V), bf16, dev),
+        _rows(k_rot, "k_rot", (total_k, PSKV_LATENT_ROT), dev),
+        k_rot.stride(0) if total_k > 1 else PSKV_LATENT_ROT, cq, _ptr(cu_q, "cu_q", ends, i32, dev), ck,
+        _ptr(cu_k, "cu_k", ends, i32, dev), batch, heads, scale, op, code,
+        None if status is None else _dev(status, "status", i32), _stream_on(stream, dev)),
         "prefill_attn_expanded")
     return out
 
@@ -769,25 +809,24 @@ def verify_drafts(target_probs, draft_probs, drafts, u, num_drafts=None, tokens=
     distribution), ``drafts`` int32 [batch, drafts], ``u`` f32 [batch, drafts + 1]
     uniform numbers.  Returns (``tokens`` int32 [batch, drafts + 1]: standing
     drafts, the drawn token, -1s; ``accepted`` int32 [batch])."""
-    lib = load_library()
+    lib = _LIB or load_library()
+    dev, i32 = _current_device(), torch.int32
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError("target_probs must be [batch, drafts + 1, vocab]")
-    batch, t, vocab = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
-    _here("verify_drafts", target_probs, draft_probs, drafts, u, num_drafts, tokens, accepted, status)
-    kind = target_probs.dtype
+    batch, t1, vocab = target_probs.shape
+    kind, t = target_probs.dtype, t1 - 1
+    tp = _ptr(target_probs, "target_probs", (batch, t1, vocab), kind, dev)
     if tokens is None:
-        tokens = torch.empty((batch, t + 1), dtype=torch.int32, device=target_probs.device)
+        tokens = torch.empty((batch, t1), dtype=i32, device=target_probs.device)
     if accepted is None:
-        accepted = torch.empty(batch, dtype=torch.int32, device=target_probs.device)
+        accepted = torch.empty(batch, dtype=i32, device=target_probs.device)
     _check(lib.verify_drafts(
-        _dev(target_probs, "target_probs"),
-        None if draft_probs is None else _shaped(draft_probs, "draft_probs", (batch, t, vocab), kind),
-        _dtype_code(kind), _shaped(drafts, "drafts", (batch, t), torch.int32),
-        None if num_drafts is None else _shaped(num_drafts, "num_drafts", (batch,), torch.int32),
-        _shaped(u, "u", (batch, t + 1), torch.float32), batch, t, vocab,
-        _shaped(tokens, "tokens", (batch, t + 1), torch.int32),
-        _shaped(accepted, "accepted", (batch,), torch.int32),
-        None if status is None else _dev(status, "status", torch.int32), _stream(stream)),
+        tp, None if draft_probs is None else _ptr(draft_probs, "draft_probs", (batch, t, vocab), kind, dev),
+        _dtype_code(kind), _ptr(drafts, "drafts", (batch, t), i32, dev),
+        None if num_drafts is None else _ptr(num_drafts, "num_drafts", (batch,), i32, dev),
+        _ptr(u, "u", (batch, t1), torch.float32, dev), batch, t, vocab,
+        _ptr(tokens, "tokens", (batch, t1), i32, dev), _ptr(accepted, "accepted", (batch,), i32, dev),
+        None if status is None else _dev(status, "status", i32), _stream_on(stream, dev)),
         "verify_drafts")
     return tokens, accepted
 
