@@ -655,12 +655,13 @@ _OUT_CODES = {torch.bfloat16: PSKV_DTYPE_BF16, torch.float32: PSKV_DTYPE_F32}
 def _out_like(out, shape, like, out_dtype, dev: int):
     """The output tensor (made if not given), its address and its dtype's code."""
     if out is None:
-        out = like.new_empty(shape) if out_dtype is None or out_dtype is like.dtype else \
-            torch.empty(shape, device=like.device, dtype=out_dtype)
-    code = _OUT_CODES.get(out.dtype)
-    if code is None:
-        code = _dtype_code(out.dtype)
-    return out, _ptr(out, "out", shape, out.dtype, dev), code
+        kind = torch.bfloat16 if out_dtype is None else out_dtype
+        code = _OUT_CODES.get(kind) if kind in _OUT_CODES else _dtype_code(kind)
+        out = torch.empty(shape, dtype=kind, device=like.device)
+        return out, out.data_ptr(), code
+    kind = out.dtype
+    code = _OUT_CODES.get(kind) if kind in _OUT_CODES else _dtype_code(kind)
+    return out, _ptr(out, "out", shape, kind, dev), code
 
 
 def kv_prep_append_latent(layout: Layout, x, row_of, pos_of, page_tables, pages_of_row, eps: float,
@@ -818,15 +819,20 @@ def verify_drafts(target_probs, draft_probs, drafts, u, num_drafts=None, tokens=
     tp = _ptr(target_probs, "target_probs", (batch, t1, vocab), kind, dev)
     if tokens is None:
         tokens = torch.empty((batch, t1), dtype=i32, device=target_probs.device)
+        kp = tokens.data_ptr()
+    else:
+        kp = _ptr(tokens, "tokens", (batch, t1), i32, dev)
     if accepted is None:
-        accepted = torch.empty(batch, dtype=i32, device=target_probs.device)
+        accepted = torch.empty((batch,), dtype=i32, device=target_probs.device)
+        ap = accepted.data_ptr()
+    else:
+        ap = _ptr(accepted, "accepted", (batch,), i32, dev)
     _check(lib.verify_drafts(
         tp, None if draft_probs is None else _ptr(draft_probs, "draft_probs", (batch, t, vocab), kind, dev),
         _dtype_code(kind), _ptr(drafts, "drafts", (batch, t), i32, dev),
         None if num_drafts is None else _ptr(num_drafts, "num_drafts", (batch,), i32, dev),
         _ptr(u, "u", (batch, t1), torch.float32, dev), batch, t, vocab,
-        _ptr(tokens, "tokens", (batch, t1), i32, dev), _ptr(accepted, "accepted", (batch,), i32, dev),
-        None if status is None else _dev(status, "status", i32), _stream_on(stream, dev)),
+        kp, ap, None if status is None else _dev(status, "status", i32), _stream_on(stream, dev)),
         "verify_drafts")
     return tokens, accepted
 

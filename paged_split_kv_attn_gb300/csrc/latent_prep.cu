@@ -11,9 +11,11 @@
 // and key -> page and angle -> store) for a decode step, so every load that
 // does not wait for another is issued first.  One warp writes a token's row
 // (lane l: 16-byte pieces l, l + 32 of the latent; lanes 0-7 a piece of the
-// rotated key each); the queries take a warp for four heads (8 lanes of 16 bytes
-// a head), so a pair (i, i + 32) lies in two lanes, four apart, and a pair (2i, 2i + 1)
-// inside one lane.
+// rotated key each); the queries take a warp for sixteen heads (8 lanes of 16 bytes
+// a head, four heads at a time, all loaded before the chain of page and angle loads is
+// waited for: with four heads a warp a chunk of 8,168 tokens under 32 heads took 30.5 us,
+// bound by that chain), so a pair (i, i + 32) lies in two lanes, four apart, and a pair
+// (2i, 2i + 1) inside one lane.
 #include "latent.h"
 #include "pskv_internal.cuh"
 
@@ -23,7 +25,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kRot = PSKV_LATENT_ROT;
-constexpr int kHeadsPerWarp = 4;
+constexpr int kHeadSteps = 4;                  // four heads at a time
+constexpr int kHeadsPerWarp = 4 * kHeadSteps;
 
 __device__ __forceinline__ void unpack8(const uint4 x, float (&f)[8]) {
   const uint32_t u[4] = {x.x, x.y, x.z, x.w};
@@ -91,10 +94,10 @@ __global__ void __launch_bounds__(kWarps * 32) pskv_latent_prep(const LatentPrep
   if (item >= (long long)a.n * slots) return;
   const int t = (int)(item / slots), s = (int)(item % slots);
   const int b = a.row_of[t], key = a.pos_of[t];
-  uint4 c[kPieces], r = make_uint4(0, 0, 0, 0);
+  uint4 c[kPieces], r = make_uint4(0, 0, 0, 0), rq[kHeadSteps];
   float4 w[kPieces][2];
-  const int head = (s - 1) * kHeadsPerWarp + (lane >> 3);
-  const bool mine = s == 0 ? lane < 8 : head < a.num_q_heads;  // this lane holds a piece to turn
+  const int head = (s - 1) * kHeadsPerWarp + (lane >> 3);  // then every fourth
+  const bool mine = lane < 8;  // (s = 0) this lane holds a piece of the key to turn
   if (s == 0) {
     const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) +
                                                      (size_t)t * (size_t)a.x_token);
@@ -109,10 +112,14 @@ __global__ void __launch_bounds__(kWarps * 32) pskv_latent_prep(const LatentPrep
       }
     }
     if (mine) r = x[DC / 8 + lane];
-  } else if (mine) {
-    r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
-                                         (size_t)t * (size_t)a.q_token +
-                                         (size_t)head * (size_t)a.q_head + 8 * piece);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kHeadSteps; ++k)
+      rq[k] = head + 4 * k < a.num_q_heads
+                  ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
+                                                     (size_t)t * (size_t)a.q_token +
+                                                     (size_t)(head + 4 * k) * (size_t)a.q_head + 8 * piece)
+                  : make_uint4(0, 0, 0, 0);
   }
   // the token's place, checked the same way by all its warps: a refused row writes nothing
   uint32_t fault = 0;
@@ -138,14 +145,18 @@ __global__ void __launch_bounds__(kWarps * 32) pskv_latent_prep(const LatentPrep
   }
   Angles g;
   load_angles(g, a, pos, piece);
-  r = turn(r, g, a.adjacent != 0, piece);
   if (s > 0) {
-    if (mine)
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.q_out) +
-                                 (size_t)t * (size_t)a.q_out_token +
-                                 (size_t)head * (size_t)a.q_out_head + 8 * piece) = r;
+#pragma unroll
+    for (int k = 0; k < kHeadSteps; ++k) {
+      const uint4 y = turn(rq[k], g, a.adjacent != 0, piece);
+      if (head + 4 * k < a.num_q_heads)
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.q_out) +
+                                   (size_t)t * (size_t)a.q_out_token +
+                                   (size_t)(head + 4 * k) * (size_t)a.q_out_head + 8 * piece) = y;
+    }
     return;
   }
+  r = turn(r, g, a.adjacent != 0, piece);
   float f[kPieces][8], ss = 0.f;
 #pragma unroll
   for (int k = 0; k < kPieces; ++k) {

@@ -30,14 +30,17 @@ constexpr int kCluster = 8;
 constexpr int kWarps = 8;
 constexpr int kPieces = kCluster * kWarps;
 
-// A probability as a multiple of 2^-62: NaN and below 0 as 0, above 1 as 1.
+// A probability as a multiple of 2^-62 (cut): NaN and below 0 as 0, above 1 as 1.  With the
+// 24-bit mantissa m at the top of a 32-bit word, the value is that word shifted right by
+// 128 - e in a 64-bit register whose high word it starts in (p = 1: e = 127, 2^62).
 __device__ __forceinline__ uint64_t fixed_point(float p) {
-  if (!(p > 0.f)) return 0;
-  if (p >= 1.f) return 1ull << 62;
-  const uint32_t bits = __float_as_uint(p), e = bits >> 23;
-  const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
-  const int shift = (int)(e ? e : 1) - 88;  // m * 2^(e - 150) * 2^62
-  return shift >= 0 ? m << shift : (shift > -32 ? m >> -shift : 0);
+  const uint32_t bits = __float_as_uint(__saturatef(p));  // [0, 1], NaN as 0
+  const uint32_t m = (bits << 8) | 0x80000000u, k = 128u - (bits >> 23);
+  uint32_t hi, lo;  // (shifts by 32 and more give 0; e = 0 gives k = 128)
+  asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(m), "r"(k));
+  asm("shf.r.clamp.b32 %0, 0, %1, %2;" : "=r"(lo) : "r"(m), "r"(k));           // k <= 32
+  asm("shr.u32 %0, %1, %2;" : "=r"(lo) : "r"(lo), "r"(k > 32u ? k - 32u : 0u));
+  return ((uint64_t)hi << 32) | lo;
 }
 
 // The row being drawn from.
@@ -99,25 +102,61 @@ __device__ __forceinline__ u128 threshold(float u, u128 sum) {
   return shift >= 128 ? (u128)0 : (sum * m) >> shift;
 }
 
+// A running sum of weights: 96 bits hold 2^34 of them.
+struct Sum {
+  uint32_t a = 0, b = 0, c = 0;
+  __device__ void add(uint64_t x) {
+    asm("add.cc.u32 %0, %0, %3;\n\taddc.cc.u32 %1, %1, %4;\n\taddc.u32 %2, %2, 0;"
+        : "+r"(a), "+r"(b), "+r"(c)
+        : "r"((uint32_t)x), "r"((uint32_t)(x >> 32)));
+  }
+  // Add x - y, or nothing where that is negative.
+  __device__ void add_excess(uint64_t x, uint64_t y) {
+    uint32_t lo, hi, none;
+    asm("sub.cc.u32 %0, %3, %5;\n\tsubc.cc.u32 %1, %4, %6;\n\tsubc.u32 %2, 0, 0;"
+        : "=r"(lo), "=r"(hi), "=r"(none)  // all ones after a borrow
+        : "r"((uint32_t)x), "r"((uint32_t)(x >> 32)), "r"((uint32_t)y), "r"((uint32_t)(y >> 32)));
+    add(((uint64_t)(hi & ~none) << 32) | (lo & ~none));
+  }
+  __device__ u128 value() const { return ((u128)c << 64) | ((uint64_t)b << 32) | a; }
+};
+
 // The sum over [lo, hi), 16 bytes a lane and step where both rows are aligned.
 template <typename T, bool kVec>
 __device__ __forceinline__ u128 sum_range(const Weights<T> &w, int lo, int hi, int lane) {
-  constexpr int kN = 16 / sizeof(T);
-  u128 sum = 0;
-  if constexpr (kVec) {
+  constexpr int kN = kVec ? 16 / sizeof(T) : 1;  // values a lane takes at once
+  Sum sum;
+  if (w.q) {
 #pragma unroll 4
     for (int v = lo + kN * lane; v < hi; v += 32 * kN) {
       T pv[kN], qv[kN];
-      *reinterpret_cast<uint4 *>(pv) = __ldg(reinterpret_cast<const uint4 *>(w.p + v));
-      if (w.q) *reinterpret_cast<uint4 *>(qv) = __ldg(reinterpret_cast<const uint4 *>(w.q + v));
+      if constexpr (kVec) {
+        *reinterpret_cast<uint4 *>(pv) = __ldg(reinterpret_cast<const uint4 *>(w.p + v));
+        *reinterpret_cast<uint4 *>(qv) = __ldg(reinterpret_cast<const uint4 *>(w.q + v));
+      } else {
+        pv[0] = w.p[v];
+        qv[0] = w.q[v];
+      }
 #pragma unroll
-      for (int e = 0; e < kN; ++e) sum += w.at(v + e, pv[e], w.q ? qv[e] : T(0));
+      for (int e = 0; e < kN; ++e)
+        sum.add_excess(fixed_point(Weights<T>::value(pv[e])), fixed_point(Weights<T>::value(qv[e])));
     }
   } else {
-#pragma unroll 8
-    for (int v = lo + lane; v < hi; v += 32) sum += w.at(v);
+#pragma unroll 4
+    for (int v = lo + kN * lane; v < hi; v += 32 * kN) {
+      T pv[kN];
+      if constexpr (kVec)
+        *reinterpret_cast<uint4 *>(pv) = __ldg(reinterpret_cast<const uint4 *>(w.p + v));
+      else
+        pv[0] = w.p[v];
+#pragma unroll
+      for (int e = 0; e < kN; ++e) sum.add(fixed_point(Weights<T>::value(pv[e])));
+    }
   }
-  return warp_sum(sum);
+  u128 total = warp_sum(sum.value());
+  // the guessed token has no weight left (1 is taken off): what was counted for it goes again
+  if (!w.q && w.point >= lo && w.point < hi) total -= fixed_point(Weights<T>::value(w.p[w.point]));
+  return total;
 }
 
 __device__ __forceinline__ uint32_t rank_in_cluster() {
@@ -227,17 +266,34 @@ __global__ void __launch_bounds__(kWarps * 32) __cluster_dims__(kCluster, 1, 1)
       u128 at = 0;
       for (int k = 0; k < warp; ++k) at += ((u128)part_sum[k][1] << 64) | part_sum[k][0];
       if (before < at || before >= at + mine) return;
+      // eight neighbouring tokens a lane: one scan finds the lane, which finds the token
       u128 rest = before - at;
       int token = -1;
-      for (int v0 = s_lo; v0 < s_hi; v0 += 32) {
-        const int v = v0 + lane;
-        const u128 x = warp_scan(v < s_hi ? (u128)w.at(v) : (u128)0, lane);
-        const uint32_t over = __ballot_sync(0xffffffffu, x > rest);
-        if (over) {
-          token = v0 + __ffs(over) - 1;
-          break;
+      for (int v0 = s_lo; token < 0 && v0 < s_hi; v0 += 32 * 8) {
+        uint64_t x[8];
+        u128 own8 = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int v = v0 + 8 * lane + e;
+          x[e] = v < s_hi ? w.at(v) : 0;
+          own8 += x[e];
         }
-        rest -= shfl_128(x, 31);
+        const u128 incl8 = warp_scan(own8, lane);
+        const uint32_t over = __ballot_sync(0xffffffffu, incl8 > rest);
+        if (over) {
+          const int l8 = __ffs(over) - 1;
+          u128 left = rest - (incl8 - own8);  // (meant in lane l8)
+          int e8 = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e == e8 && x[e] <= left) {
+              left -= x[e];
+              e8 = e + 1;
+            }
+          token = __shfl_sync(0xffffffffu, v0 + 8 * lane + e8, l8);
+        } else {
+          rest -= shfl_128(incl8, 31);
+        }
       }
       for (int t = lane; t <= T_; t += 32)
         a.tokens[(size_t)b * (T_ + 1) + t] = t < taken ? drafts[t] : (t == taken ? token : -1);
