@@ -508,8 +508,9 @@ int prefill_attn_expanded(const void *q, const void *kv, const void *k_rot, int6
  * standing, one more token comes from the weights
  *   r(v) = max(p_a(v) - q_a(v), 0)  when a < d,   r = p_a  when a = d
  * (when these are all 0: r = p_a): the lowest v with sum_{w <= v} r(w) >
- * u_D * sum r, D = max_drafts.  Products and comparisons are exact and the sums
- * are whole numbers of 2^-62, so the result does not depend on their order.
+ * u_D * sum r, D = max_drafts.  Products and comparisons are exact, and the sums
+ * are of probabilities rounded to the nearest multiple of 2^-60, whole numbers,
+ * so the result does not depend on their order.
  *   target_probs  device [batch][max_drafts + 1][vocab] of dtype (F32 or BF16)
  *   draft_probs   device [batch][max_drafts][vocab] of dtype, or NULL: the draft
  *                 has no distribution, q_t is 1 at x_t and 0 elsewhere

@@ -7,16 +7,27 @@
 // by its chain of loads.
 //
 // The draw has to be the same however the sum is split, so the weights are whole
-// numbers: a probability in [0, 1] is m 2^e with a 24-bit m, taken as a multiple of
-// 2^-62 (exact from 2^-38 up, cut below: at most vocab * 2^-62 in all), and
-// sums are 128-bit integers, whose order does not matter.  u is a 24-bit integer
-// times a power of two, so floor(u S) is exact as well.
+// numbers: a probability in [0, 1] is taken as the nearest multiple of 2^-60 (exact from 2^-37
+// up; ties to the even one), and sums are 128-bit integers, whose order does not matter.
+// u is a 24-bit integer times a power of two, so floor(u S) is exact as well.  The multiple
+// comes as three signed 20-bit digits, each read off the low bits of a float add to
+// 1.5 * 2^3, whose last place is 2^-20, with the exact remainder carried to the next
+// (7 floating operations; shifting the mantissa into place took 12 integer ones, which run at
+// half the rate).
 //
 // One cluster of eight CTAs takes a row: warp W of its 64 sums the W-th piece of the
 // vocabulary and writes its sum into every CTA's shared memory (distributed shared
 // memory); after one cluster barrier every warp knows all 64 sums and with them
 // the piece that holds the drawn token, whose CTA goes over it once more (from L2).
 // No workspace, no second launch, no atomics but fault bits.
+//
+// Measured: 64 rows of 131,072 f32 (67 MB of p and q) 18.1 us with the rows in L2, 22.9 from
+// memory (2.9 TB/s); one row of 32,001 bf16, which is the chain launch, drafts, rows, barrier,
+// rows again, 6.0 us, and about the same chain stands before and behind the large call's
+// stream.  Eight CTAs of eight warps: sixteen CTAs 25.6 and 6.2 us, four of sixteen warps 18.6
+// and 7.1.
+#include <type_traits>
+
 #include "latent.h"
 #include "pskv_internal.cuh"
 
@@ -30,17 +41,26 @@ constexpr int kCluster = 8;
 constexpr int kWarps = 8;
 constexpr int kPieces = kCluster * kWarps;
 
-// A probability as a multiple of 2^-62 (cut): NaN and below 0 as 0, above 1 as 1.  With the
-// 24-bit mantissa m at the top of a 32-bit word, the value is that word shifted right by
-// 128 - e in a 64-bit register whose high word it starts in (p = 1: e = 127, 2^62).
+// The digits of a probability p (NaN and below 0 as 0, above 1 as 1), p * 2^60 rounded =
+// (x - K) * 2^40 + (y - K) * 2^20 + (z - K), K the bits of 12.0f.
+struct Digits {
+  int x, y, z;
+  __device__ explicit Digits(float p) {
+    const float s = __saturatef(p);
+    const float t1 = s + 12.f, r1 = s - (t1 - 12.f);
+    const float t2 = fmaf(r1, 0x1p20f, 12.f), r2 = fmaf(t2 - 12.f, -0x1p-20f, r1);
+    const float t3 = fmaf(r2, 0x1p40f, 12.f);
+    x = __float_as_int(t1);
+    y = __float_as_int(t2);
+    z = __float_as_int(t3);
+  }
+};
+constexpr int kTwelve = 0x41400000;
+
 __device__ __forceinline__ uint64_t fixed_point(float p) {
-  const uint32_t bits = __float_as_uint(__saturatef(p));  // [0, 1], NaN as 0
-  const uint32_t m = (bits << 8) | 0x80000000u, k = 128u - (bits >> 23);
-  uint32_t hi, lo;  // (shifts by 32 and more give 0; e = 0 gives k = 128)
-  asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(m), "r"(k));
-  asm("shf.r.clamp.b32 %0, 0, %1, %2;" : "=r"(lo) : "r"(m), "r"(k));           // k <= 32
-  asm("shr.u32 %0, %1, %2;" : "=r"(lo) : "r"(lo), "r"(k > 32u ? k - 32u : 0u));
-  return ((uint64_t)hi << 32) | lo;
+  const Digits d(p);
+  return (uint64_t)(((long long)(d.x - kTwelve) << 40) + ((long long)(d.y - kTwelve) << 20) +
+                    (d.z - kTwelve));
 }
 
 // The row being drawn from.
@@ -57,7 +77,7 @@ struct Weights {
   }
   __device__ uint64_t at(int v, T pv, T qv) const {
     const uint64_t a = fixed_point(value(pv));
-    const uint64_t b = q ? fixed_point(value(qv)) : (v == point ? 1ull << 62 : 0);
+    const uint64_t b = q ? fixed_point(value(qv)) : (v == point ? 1ull << 60 : 0);
     return a > b ? a - b : 0;
   }
   __device__ uint64_t at(int v) const { return at(v, p[v], q ? q[v] : T(0)); }
@@ -102,56 +122,76 @@ __device__ __forceinline__ u128 threshold(float u, u128 sum) {
   return shift >= 128 ? (u128)0 : (sum * m) >> shift;
 }
 
-// A running sum of weights: 96 bits hold 2^34 of them.
+// A running sum of weights by digits: 2^20 * kFlush stays below 2^31 in each.
 struct Sum {
-  uint32_t a = 0, b = 0, c = 0;
-  __device__ void add(uint64_t x) {
-    asm("add.cc.u32 %0, %0, %3;\n\taddc.cc.u32 %1, %1, %4;\n\taddc.u32 %2, %2, 0;"
-        : "+r"(a), "+r"(b), "+r"(c)
-        : "r"((uint32_t)x), "r"((uint32_t)(x >> 32)));
+  static constexpr int kFlush = 1024;  // weights between carries
+  int x = 0, y = 0, z = 0, n = 0;
+  __int128 total = 0;
+  __device__ void add(const Digits &p) {
+    x += p.x - kTwelve;
+    y += p.y - kTwelve;
+    z += p.z - kTwelve;
   }
-  // Add x - y, or nothing where that is negative.
-  __device__ void add_excess(uint64_t x, uint64_t y) {
-    uint32_t lo, hi, none;
-    asm("sub.cc.u32 %0, %3, %5;\n\tsubc.cc.u32 %1, %4, %6;\n\tsubc.u32 %2, 0, 0;"
-        : "=r"(lo), "=r"(hi), "=r"(none)  // all ones after a borrow
-        : "r"((uint32_t)x), "r"((uint32_t)(x >> 32)), "r"((uint32_t)y), "r"((uint32_t)(y >> 32)));
-    add(((uint64_t)(hi & ~none) << 32) | (lo & ~none));
+  // Add p - q where p > q.
+  __device__ void add_excess(const Digits &p, const Digits &q, bool more) {
+    if (more) {
+      x += p.x - q.x;
+      y += p.y - q.y;
+      z += p.z - q.z;
+    }
   }
-  __device__ u128 value() const { return ((u128)c << 64) | ((uint64_t)b << 32) | a; }
+  __device__ void carry() {
+    total += (((__int128)x) << 40) + (((long long)y) << 20) + z;
+    x = y = z = n = 0;
+  }
+  // (called after `count` more weights, which divides kFlush)
+  __device__ void counted(int count) {
+    if ((n += count) == kFlush) carry();
+  }
+  __device__ u128 value() {
+    carry();
+    return (u128)total;
+  }
 };
 
 // The sum over [lo, hi), 16 bytes a lane and step where both rows are aligned.
 template <typename T, bool kVec>
 __device__ __forceinline__ u128 sum_range(const Weights<T> &w, int lo, int hi, int lane) {
-  constexpr int kN = kVec ? 16 / sizeof(T) : 1;  // values a lane takes at once
+  using Load = typename std::conditional<kVec, uint4, T>::type;
+  constexpr int kN = sizeof(Load) / sizeof(T);  // values a lane takes at once
+  constexpr int kDepth = kVec ? 4 : 8;          // loads of each row in flight
   Sum sum;
-  if (w.q) {
-#pragma unroll 4
-    for (int v = lo + kN * lane; v < hi; v += 32 * kN) {
-      T pv[kN], qv[kN];
-      if constexpr (kVec) {
-        *reinterpret_cast<uint4 *>(pv) = __ldg(reinterpret_cast<const uint4 *>(w.p + v));
-        *reinterpret_cast<uint4 *>(qv) = __ldg(reinterpret_cast<const uint4 *>(w.q + v));
-      } else {
-        pv[0] = w.p[v];
-        qv[0] = w.q[v];
-      }
+  auto row = [](const T *p, int v) {
+    if constexpr (kVec)
+      return __ldg(reinterpret_cast<const uint4 *>(p + v));
+    else
+      return p[v];
+  };
+  const Load none = Load{};
+  for (int v0 = lo + kN * lane; v0 < hi; v0 += 32 * kN * kDepth) {
+    Load pl[kDepth], ql[kDepth];
 #pragma unroll
-      for (int e = 0; e < kN; ++e)
-        sum.add_excess(fixed_point(Weights<T>::value(pv[e])), fixed_point(Weights<T>::value(qv[e])));
-    }
-  } else {
-#pragma unroll 4
-    for (int v = lo + kN * lane; v < hi; v += 32 * kN) {
-      T pv[kN];
-      if constexpr (kVec)
-        *reinterpret_cast<uint4 *>(pv) = __ldg(reinterpret_cast<const uint4 *>(w.p + v));
-      else
-        pv[0] = w.p[v];
+    for (int d = 0; d < kDepth; ++d) pl[d] = v0 + 32 * kN * d < hi ? row(w.p, v0 + 32 * kN * d) : none;
+    if (w.q) {
 #pragma unroll
-      for (int e = 0; e < kN; ++e) sum.add(fixed_point(Weights<T>::value(pv[e])));
+      for (int d = 0; d < kDepth; ++d) ql[d] = v0 + 32 * kN * d < hi ? row(w.q, v0 + 32 * kN * d) : none;
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          const float pv = Weights<T>::value(reinterpret_cast<const T *>(&pl[d])[e]);
+          const float qv = Weights<T>::value(reinterpret_cast<const T *>(&ql[d])[e]);
+          // (clamped values: a NaN counts as 0)
+          sum.add_excess(Digits(pv), Digits(qv), __saturatef(pv) > __saturatef(qv));
+        }
+    } else {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+        for (int e = 0; e < kN; ++e)
+          sum.add(Digits(Weights<T>::value(reinterpret_cast<const T *>(&pl[d])[e])));
     }
+    sum.counted(kN * kDepth);
   }
   u128 total = warp_sum(sum.value());
   // the guessed token has no weight left (1 is taken off): what was counted for it goes again
@@ -179,8 +219,7 @@ __device__ __forceinline__ void cluster_barrier() {
 }  // namespace
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kWarps * 32) __cluster_dims__(kCluster, 1, 1)
-    pskv_verify_drafts(const VerifyArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) pskv_verify_drafts(const VerifyArgs a) {
   __shared__ __align__(16) uint64_t piece_sum[2][kPieces][2];  // (low, high) of each piece; second try
   __shared__ __align__(16) uint64_t part_sum[kWarps][2];
   const int b = blockIdx.x / kCluster, rank = (int)rank_in_cluster();
@@ -205,7 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32) __cluster_dims__(kCluster, 1, 1)
     if (t < d) {
       const int x = drafts[t];
       if (x >= 0 && x < V) {
-        // f32 products in f64 and fixed-point comparisons of values in [0, 1] are exact; the
+        // f32 products in f64 and comparisons of values in [0, 1] are exact; the
         // clamping is the one of the weights
         const float p = Weights<T>::value(target[(size_t)t * V + x]);
         const float q = draft ? Weights<T>::value(draft[(size_t)t * V + x]) : 1.f;
@@ -238,19 +277,30 @@ __global__ void __launch_bounds__(kWarps * 32) __cluster_dims__(kCluster, 1, 1)
     if (lane < kCluster) store_remote(piece_sum[tries][W], lane, own);
     cluster_barrier();
     const uint64_t(*ps)[2] = piece_sum[tries];
-    const u128 s0 = ((u128)ps[2 * lane][1] << 64) | ps[2 * lane][0];
-    const u128 s1 = ((u128)ps[2 * lane + 1][1] << 64) | ps[2 * lane + 1][0];
-    const u128 incl = warp_scan(s0 + s1, lane);
+    constexpr int kEach = kPieces / 32;  // pieces a lane looks at
+    u128 part[kEach], four = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      part[k] = ((u128)ps[kEach * lane + k][1] << 64) | ps[kEach * lane + k][0];
+      four += part[k];
+    }
+    const u128 incl = warp_scan(four, lane);
     total = shfl_128(incl, 31);
     if (total != 0) {
       // the piece where the running sum first passes the threshold
       const u128 thr = threshold(u[T_], total);
       const uint32_t past = __ballot_sync(0xffffffffu, incl > thr);
       const int l = __ffs(past) - 1;  // some lane: thr < total
-      const u128 base = shfl_128(incl - s0 - s1, l), first = shfl_128(s0, l);
-      const bool second = thr >= base + first;
-      const int hit = 2 * l + (second ? 1 : 0);
-      before = thr - (second ? base + first : base);  // what is left to pass inside the piece
+      u128 left = thr - (incl - four);  // (meant in lane l)
+      int k = 0;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e)
+        if (e == k && part[e] <= left) {
+          left -= part[e];
+          k = e + 1;
+        }
+      const int hit = __shfl_sync(0xffffffffu, kEach * lane + k, l);
+      before = shfl_128(left, l);  // what is left to pass inside the piece
       if (hit / kWarps != rank) return;
 
       // ---- the CTA that holds it: an eighth of the piece a warp
@@ -319,17 +369,35 @@ __global__ void __launch_bounds__(kWarps * 32) __cluster_dims__(kCluster, 1, 1)
   if (bad_token) raise_fault(a.status, PSKV_FAULT_BAD_TOKEN);
 }
 
+namespace {
+
+template <typename T, bool kVec>
+cudaError_t launch(const VerifyArgs &a, cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.batch * kCluster);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, pskv_verify_drafts<T, kVec>, a);
+}
+
+}  // namespace
+
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t s) {
-  const dim3 grid((unsigned)a.batch * kCluster), block(kWarps * 32);
   const int size = a.dtype == PSKV_DTYPE_BF16 ? 2 : 4;
   // 16-byte loads need every row on a 16-byte boundary
   const bool vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15u) == 0 &&
                    (long long)a.vocab * size % 16 == 0;
-  if (size == 2)
-    return vec ? launch_pdl(pskv_verify_drafts<uint16_t, true>, grid, block, 0, s, a)
-               : launch_pdl(pskv_verify_drafts<uint16_t, false>, grid, block, 0, s, a);
-  return vec ? launch_pdl(pskv_verify_drafts<float, true>, grid, block, 0, s, a)
-             : launch_pdl(pskv_verify_drafts<float, false>, grid, block, 0, s, a);
+  if (size == 2) return vec ? launch<uint16_t, true>(a, s) : launch<uint16_t, false>(a, s);
+  return vec ? launch<float, true>(a, s) : launch<float, false>(a, s);
 }
 
 }  // namespace pskv

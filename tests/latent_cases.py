@@ -99,14 +99,12 @@ def check_attention(out, ref, values_max):
 # ---- the drafts' verification, in whole numbers ----------------------------------
 
 def fixed(p) -> int:
-    """A probability in units of 2^-62 (cut), NaN and below 0 as 0, above 1 as 1."""
+    """The nearest multiple of 2^-60 (ties to the even one), NaN and below 0 as 0, above 1 as 1."""
+    from fractions import Fraction
     p = float(p)
     if not p > 0:
         return 0
-    if p >= 1:
-        return 1 << 62
-    num, den = p.as_integer_ratio()
-    return (num << 62) // den
+    return 1 << 60 if p >= 1 else round(Fraction(p) * (1 << 60))
 
 
 def verify_reference(target, draft, drafts, u, num_drafts=None):
