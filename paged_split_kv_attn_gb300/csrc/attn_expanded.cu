@@ -68,20 +68,28 @@ enum : int {
   kEmptyK = kFullV + kRing,  // [4] the tile's scores done
   kEmptyV = kEmptyK + kRing,  // [4] the tile's values done
   kQFull = kEmptyV + kRing,  // (even CTA) both CTAs' queries landed
-  kSFull = kQFull + 1,       // [2] scores of region r in
+  kQFree = kQFull + 1,       // the block's scores done
+  kSFull = kQFree + 1,       // [2] scores of region r in
   kSFree = kSFull + 2,       // [2] (even CTA) region r read in both CTAs
   kPFull = kSFree + 2,       // [2] (even CTA) P written in both CTAs
   kPvDone = kPFull + 2,      // [2] the values of P's tile done
   kRagged = kPvDone + 2,     // this CTA's V of the tile with the row's end
-  kDrainS = kRagged + 1,
+  kWorkFull = kRagged + 1,   // [2] the block's numbers written
+  kWorkFree = kWorkFull + 2,  // [2] and read by all warps
+  kReply = kWorkFree + 2,    // the answer to a request for a block landed
+  kReplyRead = kReply + 1,   // (even CTA) and was read in both CTAs
+  kDrainS = kReplyRead + 1,
   kDrainV = kDrainS + 1,
   kNumBars = kDrainV + 1
 };
-constexpr int kOffRed = kOffBar + kNumBars * 8;          // float[2][2][128] maxima (then sums)
+constexpr int kOffWork = (kOffBar + kNumBars * 8 + 15) & ~15;  // Work[2]
+constexpr int kOffReply = kOffWork + 2 * 32;                   // 16 bytes
+constexpr int kOffRed = kOffReply + 16;                        // float[2][2][128] maxima (then sums)
 constexpr int kOffSlot = kOffRed + 2 * 2 * kRows * 4;
 constexpr int kOffAbort = kOffSlot + 4;
 constexpr int kSmemBytes = kOffAbort + 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr int kReaders = 3 + kSoftWarps;  // warps that read a block's numbers
 
 constexpr uint32_t kIdescS = tc::instr_desc(2 * kRows, kKeys, false, false);
 constexpr uint32_t kIdescPV = tc::instr_desc(2 * kRows, kDv, false, true);
@@ -89,6 +97,127 @@ constexpr uint32_t kIdescPV = tc::instr_desc(2 * kRows, kDv, false, true);
 struct Maps {
   CUtensorMap q, k, v, rot;
 };
+
+// A block of 2 * kRows queries of one head, as its CTAs' warps take it up.
+struct __align__(16) Work {
+  int q0, k0, nq, nk;  // the row's first query and key, its queries and keys
+  int h, t0, n, more;  // head, the block's first query in the row, tiles (0: nothing to do); 0: the end
+};
+static_assert(sizeof(Work) == 32, "two 16-byte words");
+
+// The rows' blocks in the order in which they are given out (whole warp).  Up to 32 rows, a lane
+// each: by their number of tiles, the longest first, so that the last to run are short (block
+// c of a row has before / 256 + c pairs of tiles, its level; the k-th block's level is found
+// by bisection over the count of blocks above).  More rows: one after the other, each
+// from its last block on.
+struct Blocks {
+  int base = 0;       // first row held
+  int skipped = 0;    // blocks of the rows before
+  int q0, k0, nq, nk, blocks, level;
+  bool bad = false;
+
+  __device__ void load(const ExpandedAttnArgs &a, int first, int lane) {
+    base = first;
+    q0 = k0 = nq = nk = blocks = level = 0;
+    bad = false;
+    const int b = first + lane;
+    if (b >= a.batch) return;
+    const int qa = a.cu_q[b], qb = a.cu_q[b + 1], ka = a.cu_k[b], kb = a.cu_k[b + 1];
+    bad = qa < 0 || qb < qa || qb > a.total_q || ka < 0 || kb < ka || kb > a.total_k ||
+          kb - ka < qb - qa;
+    if (bad) return;  // (the row is left out)
+    q0 = qa;
+    k0 = ka;
+    nq = qb - qa;
+    nk = kb - ka;
+    blocks = (nq + 2 * kRows - 1) / (2 * kRows);
+    level = (nk - nq) / (2 * kRows);
+  }
+  __device__ int held() const { return (int)__reduce_add_sync(0xffffffffu, (uint32_t)blocks); }
+
+  // Block number k's row as a lane, and its first query in the row; -1: there is none.
+  __device__ int find(const ExpandedAttnArgs &a, int k, int lane, int &t0) {
+    int row, c;
+    if (a.batch <= 32) {
+      int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (uint32_t)(blocks ? level + blocks : 0));
+      auto above = [&](int l) {  // blocks of level l and more
+        return (int)__reduce_add_sync(0xffffffffu, (uint32_t)min(blocks, max(0, level + blocks - l)));
+      };
+      if (k >= held()) return -1;
+      while (hi - lo > 1) {  // above(lo) > k >= above(hi)
+        const int mid = (lo + hi) >> 1;
+        if (above(mid) > k)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int left = k - above(hi);
+      const bool in = level <= lo && lo < level + blocks;
+      const uint32_t rows = __ballot_sync(0xffffffffu, in);
+      row = __ffs(__ballot_sync(0xffffffffu, in && __popc(rows & ((1u << lane) - 1)) == left)) - 1;
+      c = lo - __shfl_sync(0xffffffffu, level, row);
+    } else {
+      if (k < skipped) {
+        skipped = 0;
+        load(a, 0, lane);
+      }
+      int sum = held();
+      while (k - skipped >= sum) {
+        if (base + 32 >= a.batch) return -1;
+        skipped += sum;
+        load(a, base + 32, lane);
+        sum = held();
+      }
+      int incl = blocks;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+      }
+      row = __ffs(__ballot_sync(0xffffffffu, incl > k - skipped)) - 1;
+      c = __shfl_sync(0xffffffffu, incl, row) - 1 - (k - skipped);
+    }
+    t0 = c * 2 * kRows;
+    return row;
+  }
+};
+
+// Whether any thread of two warps says so, told to all of them (named barrier `id`).
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+// Ask for a cluster of the grid that has not started, in both CTAs' shared memory, counted
+// on both's barriers (one thread of the pair).
+__device__ __forceinline__ void ask_for_cluster(uint32_t reply, uint32_t bar, bool lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+      ".multicast::cluster::all.b128 [%0], [%1];\n\t}" ::"r"(reply),
+      "r"(bar), "r"((uint32_t)lead)
+      : "memory");
+}
+// The answer: that cluster's first blockIdx.x, or -1 when none is left.
+__device__ __forceinline__ int cluster_given(uint32_t reply) {
+  uint32_t x, got;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\tmov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=&r"(x), "=&r"(got)
+      : "r"(reply)
+      : "memory");
+  return got ? (int)x : -1;
+}
 
 }  // namespace
 
@@ -105,26 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int warp = tc2::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = tc2::cluster_rank();
   const bool lead = elect_one();  // one thread of each warp
-  const int h = blockIdx.x >> 1, b = blockIdx.z;
-
-  pdl_wait();
-  pdl_launch_dependents();
-  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-  const int nq = q1 - q0, nk = k1 - k0;
-  // offsets that the host copies do not allow: the row is left out (by both CTAs)
-  if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k || nk < nq ||
-      nq > (long long)gridDim.y * 2 * kRows) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-      raise_fault(a.status, PSKV_FAULT_BAD_LENGTH);
-    return;
-  }
-  // later queries see more keys: they go first
-  const int blocks = (nq + 2 * kRows - 1) / (2 * kRows);
-  if ((int)blockIdx.y >= blocks) return;
-  const int t0 = (blocks - 1 - (int)blockIdx.y) * 2 * kRows;  // the pair's first query in the row
-  const int before = nk - nq;                                 // keys before the row's first query
-  const int n = (before + min(nq, t0 + 2 * kRows) + kKeys - 1) / kKeys;  // tiles up to the last own key
-
   if (warp == 2) {
     if (lane == 0) {
       for (int s = 0; s < kRing; ++s) {
@@ -134,12 +243,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         mbar_init(&bars[kEmptyV + s], 1);
       }
       mbar_init(&bars[kQFull], 1);
+      mbar_init(&bars[kQFree], 1);
       for (int r = 0; r < 2; ++r) {
         mbar_init(&bars[kSFull + r], 1);
         mbar_init(&bars[kSFree + r], 2 * kSoftWarps);
         mbar_init(&bars[kPFull + r], 2 * kSoftWarps);
         mbar_init(&bars[kPvDone + r], 1);
+        mbar_init(&bars[kWorkFull + r], 1);
+        mbar_init(&bars[kWorkFree + r], kReaders);
       }
+      mbar_init(&bars[kReply], 1);
+      mbar_init(&bars[kReplyRead], 2);
       mbar_init(&bars[kRagged], 1);
       mbar_init(&bars[kDrainS], 1);
       mbar_init(&bars[kDrainV], 1);
@@ -147,8 +261,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_fence_init();
     }
     __syncwarp();
+    tc2::prefetch_map(&maps.q);
+    tc2::prefetch_map(&maps.k);
+    tc2::prefetch_map(&maps.rot);
   } else if (warp == 0) {
     tc2::alloc(slot, kTmemCols);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  Blocks rows;
+  if (warp == 2) {
+    rows.load(a, 0, lane);
+    if (blockIdx.x == 0) {
+      // offsets that the host copies do not allow: those rows, or the blocks past the grid's, are
+      // left out
+      bool bad = __any_sync(0xffffffffu, rows.bad);
+      long long blocks = rows.held();
+      for (int b = 32; b < a.batch; b += 32) {
+        rows.load(a, b, lane);
+        bad = bad || __any_sync(0xffffffffu, rows.bad);
+        blocks += rows.held();
+      }
+      if ((bad || blocks > gridDim.x / (2 * a.num_heads)) && lead) raise_fault(a.status, PSKV_FAULT_BAD_LENGTH);
+      if (a.batch > 32) rows.load(a, 0, lane);
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -158,15 +294,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   auto wait = [&](int s, uint32_t parity) {
     return tc::all_wait(bars + s, parity, abort_flag, a.status);
   };
+  // The numbers of this CTA's block number i; false: a wait failed.
+  Work *works = reinterpret_cast<Work *>(sm + kOffWork);
+  auto next = [&](int i, Work &w) {
+    const int s = i & 1;
+    if (!wait(kWorkFull + s, (i >> 1) & 1)) return false;
+    const int4 x = reinterpret_cast<const int4 *>(works + s)[0];
+    const int4 y = reinterpret_cast<const int4 *>(works + s)[1];
+    __syncwarp();
+    if (lead) mbar_arrive(bars + kWorkFree + s);
+    w = Work{x.x, x.y, x.z, x.w, y.x, y.y, tc2::uniform(y.z), tc2::uniform(y.w)};
+    return true;
+  };
 
+  // g counts a CTA's tiles over all its blocks: rings, regions and parities go by it
   if (warp == 0) {
-    if (rank == 0) {
-      // ---- the score products (all lanes alike, one issues)
-      bool ok = wait(kQFull, 0);
-      const uint32_t q = smem_u32(sm + kOffQ), k = smem_u32(sm + kOffK);
-      for (int j = 0; ok && j < n; ++j) {
-        const int st = j % kRing, r = j & 1;
-        ok = wait(kFullK + st, (j / kRing) & 1) && (j < 2 || wait(kSFree + r, (j / 2 - 1) & 1));
+    // ---- the score products (all lanes alike, one issues)
+    bool ok = true;
+    const uint32_t q = smem_u32(sm + kOffQ), k = smem_u32(sm + kOffK);
+    Work w;
+    for (int i = 0, g = 0, nb = 0; ok; ++i) {
+      ok = next(i, w);
+      if (!ok || !w.more) break;
+      if (rank != 0 || w.n == 0) continue;
+      ok = wait(kQFull, nb++ & 1);
+      for (int j = 0; ok && j < w.n; ++j, ++g) {
+        const int st = g % kRing, r = g & 1;
+        ok = wait(kFullK + st, (g / kRing) & 1) && (g < 2 || wait(kSFree + r, (g / 2 - 1) & 1));
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t kt = k + st * kKBytes;
@@ -179,17 +333,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc2::commit_both(bars + kSFull + r, lead);
         tc2::commit_both(bars + kEmptyK + st, lead);
       }
-      tc2::commit_both(bars + kDrainS, lead);
+      tc2::commit_both(bars + kQFree, lead);
     }
+    if (rank == 0) tc2::commit_both(bars + kDrainS, lead);
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0) {
-      // ---- the value products
-      bool ok = true;
-      const uint32_t v = smem_u32(sm + kOffV);
-      for (int j = 0; ok && j < n; ++j) {
-        const int st = j % kRing, pb = j % kPBufs;
-        ok = wait(kFullV + st, (j / kRing) & 1) && wait(kPFull + pb, (j / kPBufs) & 1);
+    // ---- the value products
+    bool ok = true;
+    const uint32_t v = smem_u32(sm + kOffV);
+    Work w;
+    for (int i = 0, g = 0; ok; ++i) {
+      ok = next(i, w);
+      if (!ok || !w.more) break;
+      if (rank != 0) continue;
+      for (int j = 0; ok && j < w.n; ++j, ++g) {
+        const int st = g % kRing, pb = g % kPBufs;
+        ok = wait(kFullV + st, (g / kRing) & 1) && wait(kPFull + pb, (g / kPBufs) & 1);
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t vt = v + st * kVBytes;
@@ -203,203 +362,259 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc2::commit_both(bars + kPvDone + pb, lead);
         tc2::commit_both(bars + kEmptyV + st, lead);
       }
-      tc2::commit_both(bars + kDrainV, lead);
     }
+    if (rank == 0) tc2::commit_both(bars + kDrainV, lead);
     __syncwarp();
   } else if (warp == 2) {
-    // ---- Q (queries behind the row's last: other rows' or zeros), then K: this CTA's half
-    tc2::expect_tx(bars + kQFull, 2 * kQBytes, lead && rank == 0);
-    tc2::tma_load_3d(smem_u32(sm + kOffQ), &maps.q, 0, q0 + t0 + (int)rank * kRows, kQSlabs * h,
-                     tc2::map_to(smem_u32(bars + kQFull), 0), lead);
-    int j = 0;
-    for (; j < n; ++j) {
-      const int st = j % kRing;
-      if (j >= kRing && !wait(kEmptyK + st, (j / kRing - 1) & 1)) break;
-      const uint32_t dst = smem_u32(sm + kOffK + st * kKBytes);
-      const uint32_t bar = tc2::map_to(smem_u32(bars + kFullK + st), 0);
-      const int y = k0 + j * kKeys + kHalf * (int)rank;
-      tc2::expect_tx(bars + kFullK + st, 2 * kKBytes, lead && rank == 0);
-      tc2::tma_load_3d(dst, &maps.k, 0, y, 4 * h, bar, lead);
-      tc2::tma_load_3d(dst + 2 * kKSlab, &maps.rot, 0, y, 0, bar, lead);
+    // ---- the blocks; Q (queries behind the row's last: other rows' or zeros), then K: this
+    // CTA's half.  The next block is asked for when one begins and looked at behind its copies.
+    const uint32_t reply = smem_u32(sm + kOffReply);
+    int x = blockIdx.x, g = 0, nb = 0, i = 0;
+    bool ok = true, asked = false;
+    for (;; ++i) {
+      Work w{};
+      w.more = x >= 0;
+      if (x >= 0) {
+        const int pair = x >> 1;
+        w.h = pair % a.num_heads;
+        const int row = rows.find(a, pair / a.num_heads, lane, w.t0);
+        if (row >= 0) {
+          w.q0 = __shfl_sync(0xffffffffu, rows.q0, row);
+          w.k0 = __shfl_sync(0xffffffffu, rows.k0, row);
+          w.nq = __shfl_sync(0xffffffffu, rows.nq, row);
+          w.nk = __shfl_sync(0xffffffffu, rows.nk, row);
+          // tiles up to the last own key
+          w.n = (w.nk - w.nq + min(w.nq, w.t0 + 2 * kRows) + kKeys - 1) / kKeys;
+        }
+      }
+      ok = i < 2 || wait(kWorkFree + (i & 1), (i / 2 - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) works[i & 1] = w;
+      __syncwarp();
+      if (lead) mbar_arrive(bars + kWorkFull + (i & 1));
+      if (!w.more) break;
+      if (rank == 0) {
+        ok = i == 0 || wait(kReplyRead, (i - 1) & 1);
+        if (!ok) break;
+        ask_for_cluster(reply, smem_u32(bars + kReply), lead);
+      }
+      tc2::expect_tx(bars + kReply, 16, lead);
+      asked = true;
+      if (w.n > 0) {
+        ok = nb == 0 || wait(kQFree, (nb - 1) & 1);
+        if (!ok) break;
+        ++nb;
+        tc2::expect_tx(bars + kQFull, 2 * kQBytes, lead && rank == 0);
+        tc2::tma_load_3d(smem_u32(sm + kOffQ), &maps.q, 0, w.q0 + w.t0 + (int)rank * kRows, kQSlabs * w.h,
+                         tc2::map_to(smem_u32(bars + kQFull), 0), lead);
+      }
+      for (int j = 0; j < w.n; ++j, ++g) {
+        const int st = g % kRing;
+        ok = g < kRing || wait(kEmptyK + st, (g / kRing - 1) & 1);
+        if (!ok) break;
+        const uint32_t dst = smem_u32(sm + kOffK + st * kKBytes);
+        const uint32_t bar = tc2::map_to(smem_u32(bars + kFullK + st), 0);
+        const int y = w.k0 + j * kKeys + kHalf * (int)rank;
+        tc2::expect_tx(bars + kFullK + st, 2 * kKBytes, lead && rank == 0);
+        tc2::tma_load_3d(dst, &maps.k, 0, y, 4 * w.h, bar, lead);
+        tc2::tma_load_3d(dst + 2 * kKSlab, &maps.rot, 0, y, 0, bar, lead);
+      }
+      if (!ok) break;
+      ok = wait(kReply, i & 1);
+      if (!ok) break;
+      asked = false;
+      x = cluster_given(reply);
+      __syncwarp();
+      tc::fence_smem_for_async();  // read before the next answer lands
+      tc2::arrive_pair(tc2::map_to(smem_u32(bars + kReplyRead), 0), lead);
     }
     // every copy of both CTAs landed before they leave (their count is the even CTA's)
+    if (asked) mbar_wait(bars + kReply, i & 1);
     if (rank == 0) {
-      for (int s = max(0, j - kRing); s < j; ++s) mbar_wait(bars + kFullK + s % kRing, (s / kRing) & 1);
-      mbar_wait(bars + kQFull, 0);
+      for (int s = max(0, g - kRing); s < g; ++s) mbar_wait(bars + kFullK + s % kRing, (s / kRing) & 1);
+      if (nb > 0) mbar_wait(bars + kQFull, (nb - 1) & 1);
     }
     __syncwarp();
   } else if (warp == 3) {
     // ---- V: this CTA's 64 columns of every tile.  The tile with the row's last key: rows
     // behind it are another row's and meet P = 0, so they are zeroed first.
-    const bool ragged = n * kKeys > nk;
-    const int last = n - 1;
-    int j = 0;
-    for (; j < n; ++j) {
-      const int st = j % kRing;
-      if (j >= kRing && !wait(kEmptyV + st, (j / kRing - 1) & 1)) break;
-      const uint32_t full = tc2::map_to(smem_u32(bars + kFullV + st), 0);
-      const bool whole = !(ragged && j == last);
-      if (!whole)
-        tc2::expect_tx(bars + kRagged, kVBytes, lead);
-      else
-        tc2::expect_tx(bars + kFullV + st, 2 * kVBytes, lead && rank == 0);
-      tc2::tma_load_3d(smem_u32(sm + kOffV + st * kVBytes), &maps.v, 0, k0 + j * kKeys,
-                       4 * h + 2 + (int)rank, whole ? full : smem_u32(bars + kRagged), lead);
-      tc2::arrive_pair(full, lead && whole);
+    bool ok = true;
+    Work w;
+    int g = 0, seen = 0;
+    for (int i = 0; ok; ++i) {
+      ok = next(i, w);
+      if (!ok || !w.more) break;
+      const bool ragged = w.n * kKeys > w.nk;
+      for (int j = 0; ok && j < w.n; ++j, ++g) {
+        const int st = g % kRing;
+        ok = g < kRing || wait(kEmptyV + st, (g / kRing - 1) & 1);
+        if (!ok) break;
+        const uint32_t full = tc2::map_to(smem_u32(bars + kFullV + st), 0);
+        unsigned char *dst = sm + kOffV + st * kVBytes;
+        const bool whole = !(ragged && j == w.n - 1);
+        if (!whole)
+          tc2::expect_tx(bars + kRagged, kVBytes, lead);
+        else
+          tc2::expect_tx(bars + kFullV + st, 2 * kVBytes, lead && rank == 0);
+        tc2::tma_load_3d(smem_u32(dst), &maps.v, 0, w.k0 + j * kKeys, 4 * w.h + 2 + (int)rank,
+                         whole ? full : smem_u32(bars + kRagged), lead);
+        if (!whole) {
+          ok = wait(kRagged, seen & 1);
+          if (!ok) {
+            mbar_wait(bars + kRagged, seen & 1);
+            break;
+          }
+          ++seen;
+          const int left = w.nk - j * kKeys;
+          for (int e = lane; e < (kKeys - left) * 8; e += 32)
+            *reinterpret_cast<uint4 *>(dst + (left + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_smem_for_async();
+          __syncwarp();
+          if (rank == 0 && lead) mbar_arrive(bars + kFullV + st);  // in place of the copies' count
+        }
+        tc2::arrive_pair(full, lead);
+      }
     }
     __syncwarp();
-    if (ragged && j == n) mbar_wait(bars + kRagged, 0);  // (bounded)
     if (rank == 0)
-      for (int s = max(0, j - kRing); s < j; ++s)
-        if (!(ragged && s == last)) mbar_wait(bars + kFullV + s % kRing, (s / kRing) & 1);
+      for (int s = max(0, g - kRing); s < g; ++s) mbar_wait(bars + kFullV + s % kRing, (s / kRing) & 1);
     __syncwarp();
-    if (ragged) {
-      const int st = last % kRing, left = nk - last * kKeys;
-      unsigned char *dst = sm + kOffV + st * kVBytes;
-      for (int e = lane; e < (kKeys - left) * 8; e += 32)
-        *reinterpret_cast<uint4 *>(dst + (left + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-      tc::fence_smem_for_async();
-      __syncwarp();
-      if (rank == 0 && lead) mbar_arrive(bars + kFullV + st);  // in place of the copies' count
-      tc2::arrive_pair(tc2::map_to(smem_u32(bars + kFullV + st), 0), lead);
-    }
   } else {
-    // ---- the softmax: thread (query i, keys 64 gr .. + 63 of the tile).  The loop never leaves
-    // early (the two warps of a query's threads meet every tile); after a failed wait nothing
-    // is written.
-    const int w = warp & 3, gr = (warp - 4) >> 2, i = 32 * w + lane;
-    const int t = t0 + (int)rank * kRows + i;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
-    const int lim = t < nq ? before + t + 1 : 0;  // keys below lim are seen
+    // ---- the softmax: thread (query i, keys 64 gr .. + 63 of the tile).  A block's loop never
+    // leaves early (the two warps of a query's threads meet every tile); after a failed wait
+    // nothing is written, and both warps leave before the next block.
+    const int w4 = warp & 3, gr = (warp - 4) >> 2, row = 32 * w4 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
     const float sc = a.scale_log2;
     float *red = reinterpret_cast<float *>(sm + kOffRed);
     const uint32_t s_free = tc2::map_to(smem_u32(bars + kSFree), 0);
     const uint32_t p_full = tc2::map_to(smem_u32(bars + kPFull), 0);
-    float m = -CUDART_INF_F, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int r = j & 1, pb = j % kPBufs;
-      ok = ok && wait(kSFull + r, (j >> 1) & 1);
-      tc::fence_after_sync();
-      uint32_t va[32], vb[32];
-      tc::ld32(lane_base + kSCol + kKeys * r + kHalf * gr, va);
-      tc::ld32(lane_base + kSCol + kKeys * r + kHalf * gr + 32, vb);
-      tc::wait_ld();
-      tc::reg_fence(va);
-      tc::reg_fence(vb);
-      tc::fence_before_sync();
-      __syncwarp();
-      tc2::arrive_pair(s_free + 8 * r, lead);
-      float f[kHalf];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        f[c] = __uint_as_float(va[c]);
-        f[32 + c] = __uint_as_float(vb[c]);
-      }
-      const int key0 = j * kKeys + kHalf * gr;
-      // scores in log2 units are mul * f: whole tiles leave the product to the exponent's
-      // multiply-add, others (and scales that are not positive) take it before the mask
-      float mul = sc;
-      if (__any_sync(0xffffffffu, key0 + kHalf > lim || !(sc > 0.f))) {
-        mul = 1.f;
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c) f[c] = key0 + c < lim ? f[c] * sc : -CUDART_INF_F;
-      }
-      float mx[4] = {f[0], f[1], f[2], f[3]};
-#pragma unroll
-      for (int c = 4; c < kHalf; ++c) mx[c & 3] = fmaxf(mx[c & 3], f[c]);
-      float *mine = red + r * 2 * kRows + i;
-      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
-      mine[gr * kRows] = mt;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory");
-      mt = fmaxf(mt, mine[(gr ^ 1) * kRows]);
-      float alpha = 1.f;
-      bool rescale = false;
-      if (mt > m + kSlack) {
-        rescale = m != -CUDART_INF_F;  // with m = -inf the row's O and l are still 0
-        alpha = rescale ? ex2(m - mt) : 1.f;
-        l *= alpha;
-        m = mt;
-      }
-      const float off = m == -CUDART_INF_F ? 0.f : -m;
-      uint32_t hi[32], lo[kLo ? 32 : 1];
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const float p0 = ex2(fmaf(f[2 * e], mul, off)), p1 = ex2(fmaf(f[2 * e + 1], mul, off));
-        hi[e] = pack_bf16x2(p0, p1);
-        if constexpr (kLo) lo[e] = pack_bf16x2(p0 - bf16_lo(hi[e]), p1 - bf16_hi(hi[e]));
-        s0 += p0;
-        s1 += p1;
-      }
-      l += s0 + s1;
-      // P's buffer is free once the values of tile j - kPBufs are done
-      if (j >= kPBufs) ok = ok && wait(kPvDone + pb, (j / kPBufs - 1) & 1);
-      if (__any_sync(0xffffffffu, rescale)) {
-        ok = ok && wait(kPvDone + (j - 1) % kPBufs, ((j - 1) / kPBufs) & 1);
+    Work w;
+    for (int i = 0, g = 0;; ++i) {
+      ok = ok && next(i, w);
+      if (pair_any(1 + w4, !ok) || !w.more) break;
+      if (w.n == 0) continue;
+      const int t = w.t0 + (int)rank * kRows + row;
+      const int lim = t < w.nq ? w.nk - w.nq + t + 1 : 0;  // keys below lim are seen
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int j = 0; j < w.n; ++j, ++g) {
+        const int r = g & 1, pb = g % kPBufs;
+        ok = ok && wait(kSFull + r, (g >> 1) & 1);
         tc::fence_after_sync();
-#pragma unroll 1
-        for (int c = 2 * gr; c < 2 * gr + 2; ++c) {
-          uint32_t o[32];
-          tc::ld32(lane_base + kOCol + 32 * c, o);
-          tc::wait_ld();
-          tc::reg_fence(o);
+        uint32_t va[32], vb[32];
+        tc::ld32(lane_base + kSCol + kKeys * r + kHalf * gr, va);
+        tc::ld32(lane_base + kSCol + kKeys * r + kHalf * gr + 32, vb);
+        tc::wait_ld();
+        tc::reg_fence(va);
+        tc::reg_fence(vb);
+        tc::fence_before_sync();
+        __syncwarp();
+        tc2::arrive_pair(s_free + 8 * r, lead);
+        float f[kHalf];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tc::st32(lane_base + kOCol + 32 * c, o);
+        for (int c = 0; c < 32; ++c) {
+          f[c] = __uint_as_float(va[c]);
+          f[32 + c] = __uint_as_float(vb[c]);
+        }
+        const int key0 = j * kKeys + kHalf * gr;
+        // scores in log2 units are mul * f: whole tiles leave the product to the exponent's
+        // multiply-add, others (and scales that are not positive) take it before the mask
+        float mul = sc;
+        if (__any_sync(0xffffffffu, key0 + kHalf > lim || !(sc > 0.f))) {
+          mul = 1.f;
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c) f[c] = key0 + c < lim ? f[c] * sc : -CUDART_INF_F;
+        }
+        float mx[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+        for (int c = 4; c < kHalf; ++c) mx[c & 3] = fmaxf(mx[c & 3], f[c]);
+        float *mine = red + r * 2 * kRows + row;
+        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+        mine[gr * kRows] = mt;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + w4) : "memory");
+        mt = fmaxf(mt, mine[(gr ^ 1) * kRows]);
+        float alpha = 1.f;
+        bool rescale = false;
+        if (mt > m + kSlack) {
+          rescale = m != -CUDART_INF_F;  // with m = -inf the row's O and l are still 0
+          alpha = rescale ? ex2(m - mt) : 1.f;
+          l *= alpha;
+          m = mt;
+        }
+        const float off = m == -CUDART_INF_F ? 0.f : -m;
+        uint32_t hi[32], lo[kLo ? 32 : 1];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float p0 = ex2(fmaf(f[2 * e], mul, off)), p1 = ex2(fmaf(f[2 * e + 1], mul, off));
+          hi[e] = pack_bf16x2(p0, p1);
+          if constexpr (kLo) lo[e] = pack_bf16x2(p0 - bf16_lo(hi[e]), p1 - bf16_hi(hi[e]));
+          s0 += p0;
+          s1 += p1;
+        }
+        l += s0 + s1;
+        // P's buffer is free once the values of tile g - kPBufs are done
+        if (g >= kPBufs) ok = ok && wait(kPvDone + pb, (g / kPBufs - 1) & 1);
+        if (__any_sync(0xffffffffu, rescale)) {
+          ok = ok && wait(kPvDone + (g - 1) % kPBufs, ((g - 1) / kPBufs) & 1);
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c = 2 * gr; c < 2 * gr + 2; ++c) {
+            uint32_t o[32];
+            tc::ld32(lane_base + kOCol + 32 * c, o);
+            tc::wait_ld();
+            tc::reg_fence(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tc::st32(lane_base + kOCol + 32 * c, o);
+          }
+        }
+        tc::fence_after_sync();
+        tc::st32(lane_base + kPCol + 64 * pb + 32 * gr, hi);
+        if constexpr (kLo) tc::st32(lane_base + kPCol + 64 + 32 * gr, lo);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        tc2::arrive_pair(p_full + 8 * pb, lead);
+      }
+      // ---- the sum over both threads, then O / l
+      float *sums = red + (g & 1) * 2 * kRows + row;
+      sums[gr * kRows] = l;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + w4) : "memory");
+      l = sums[0] + sums[kRows];
+      ok = ok && wait(kPvDone + (g - 1) % kPBufs, ((g - 1) / kPBufs) & 1);
+      tc::fence_after_sync();
+      const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
+      uint4 *dst = reinterpret_cast<uint4 *>(
+          static_cast<unsigned char *>(a.out) +
+          (((size_t)(w.q0 + min(t, w.nq - 1)) * a.num_heads + w.h) * kDv + kDv / 2 * gr) * (kLo ? 4 : 2));
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t o[32];
+        tc::ld32(lane_base + kOCol + kDv / 2 * gr + 32 * c, o);
+        tc::wait_ld();
+        tc::reg_fence(o);
+        float y[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * inv;
+        if (ok && t < w.nq) {
+          if constexpr (kLo) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              reinterpret_cast<float4 *>(dst)[8 * c + k] =
+                  make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[4 * c + k] =
+                  make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
+                             pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
+          }
         }
       }
-      tc::fence_after_sync();
-      tc::st32(lane_base + kPCol + 64 * pb + 32 * gr, hi);
-      if constexpr (kLo) tc::st32(lane_base + kPCol + 64 + 32 * gr, lo);
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      tc2::arrive_pair(p_full + 8 * pb, lead);
+      tc::fence_before_sync();  // (the next block's first P tells the tensor core that O is read)
     }
-    // ---- the sum over both threads, then O / l, put together in the queries' place and the K
-    // ring (their products are done) so that rows leave in whole lines
-    float *sums = red + (n & 1) * 2 * kRows + i;
-    sums[gr * kRows] = l;
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory");
-    l = sums[0] + sums[kRows];
-    ok = ok && wait(kPvDone + (n - 1) % kPBufs, ((n - 1) / kPBufs) & 1);
-    tc::fence_after_sync();
-    const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
-    constexpr int kBytes = kDv * (kLo ? 4 : 2), kPitch = kBytes + 16;
-    static_assert(kRows * kPitch <= kOffV, "staging");
-    unsigned char *stage = sm + kOffQ + 32 * w * kPitch;
-#pragma unroll 1
-    for (int c = 2 * gr; c < 2 * gr + 2; ++c) {
-      uint32_t o[32];
-      tc::ld32(lane_base + kOCol + 32 * c, o);
-      tc::wait_ld();
-      tc::reg_fence(o);
-      uint4 *dst = reinterpret_cast<uint4 *>(stage + lane * kPitch + c * (kLo ? 128 : 64));
-      float y[32];
-#pragma unroll
-      for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * inv;
-      if constexpr (kLo) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          reinterpret_cast<float4 *>(dst)[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          dst[k] = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
-                              pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
-      }
-    }
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory");
-    constexpr int kPieces = kBytes / 16;  // per row
-    const int first = t0 + (int)rank * kRows + 32 * w;
-    if (ok)
-      for (int e = 32 * gr + lane; e < 32 * kPieces; e += 64) {
-        const int r = e / kPieces, piece = e % kPieces;
-        if (first + r < nq)
-          reinterpret_cast<uint4 *>(a.out)[((size_t)(q0 + first + r) * a.num_heads + h) * kPieces + piece] =
-              *reinterpret_cast<const uint4 *>(stage + r * kPitch + piece * 16);
-      }
   }
   // every product done (both CTAs learn it; every copy has landed) before the memory is released
   if (warp == 0) mbar_wait(bars + kDrainS, 0);
@@ -450,7 +665,7 @@ cudaError_t launch(const ExpandedAttnArgs &a, cudaStream_t s) {
       !make_map(&maps.rot, a.k_rot, a.total_k, a.k_rot_token * 2, 1, kHalf, 1))
     return cudaErrorInvalidValue;
   return launch_pdl(pskv_attn_expanded<kLo>,
-                    dim3(2 * a.num_heads, (a.max_q + 2 * kRows - 1) / (2 * kRows), a.batch),
+                    dim3((unsigned)(2 * h * a.blocks)),
                     dim3(kThreads), kSmemBytes, s, a, maps);
 }
 

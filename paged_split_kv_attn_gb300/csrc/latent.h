@@ -66,7 +66,7 @@ struct ExpandedAttnArgs {
   const int32_t *cu_q, *cu_k;  // [B + 1]
   int batch, num_heads;
   int total_q, total_k;
-  int max_q;            // the longest row's queries
+  long long blocks;     // of 256 queries of a row, over all rows
   float scale_log2;
   void *out;            // [total_q][H][128] of out_dtype
   int out_dtype;

@@ -795,14 +795,15 @@ int prefill_attn_expanded(const void *q, const void *kv, const void *k_rot, int6
   if (out_dtype != PSKV_DTYPE_F32 && out_dtype != PSKV_DTYPE_BF16) return PSKV_ERR_INVALID_ARG;
   if (k_rot_token < PSKV_LATENT_ROT || k_rot_token % 8 != 0) return PSKV_ERR_INVALID_ARG;
   if (cu_q_host[0] != 0 || cu_k_host[0] != 0) return PSKV_ERR_INVALID_ARG;
-  int64_t max_q = 0;
+  int64_t blocks = 0;  // a cluster's work, a head: 256 queries of a row
   for (int32_t b = 0; b < batch; ++b) {
     const int64_t nq = (int64_t)cu_q_host[b + 1] - cu_q_host[b];
     const int64_t nk = (int64_t)cu_k_host[b + 1] - cu_k_host[b];
     if (nq < 0 || nk < nq) return PSKV_ERR_INVALID_ARG;
-    max_q = nq > max_q ? nq : max_q;
+    blocks += (nq + 255) / 256;
   }
-  if (max_q == 0) return PSKV_OK;  // no query
+  if (blocks == 0) return PSKV_OK;  // no query
+  if (2 * blocks * num_heads > INT32_MAX) return PSKV_ERR_INVALID_ARG;
   if (!q || !kv || !k_rot || !out) return PSKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(k_rot, 16) || !aligned(out, 16) ||
       !aligned(status, 4))
@@ -818,7 +819,7 @@ int prefill_attn_expanded(const void *q, const void *kv, const void *k_rot, int6
   a.num_heads = num_heads;
   a.total_q = cu_q_host[batch];
   a.total_k = cu_k_host[batch];
-  a.max_q = (int)max_q;
+  a.blocks = blocks;
   a.scale_log2 = scale * kLog2e;
   a.out = out;
   a.out_dtype = out_dtype;
