@@ -13,13 +13,25 @@
 // so a tile is copied once for 256 queries, half by each CTA (40 KB a CTA), and each CTA's
 // tensor memory has room for two score regions beside P and its own O:
 // S [0, 256), P [256, 384) (two of bf16 pairs; f32 output: one hi and one lo), O [384, 512).
-// S(j + 1) runs while the softmax works on tile j.  Per tile the pipe works (12 + 8) * 64 = 1,280
-// cycles on both SMs.  (One CTA with two blocks of 128 queries has no room for that: sharing one
-// score region between the blocks took 5,500 cycles for the same 2 * 256 * 128 pairs
-// that now take two tiles.)
-// A row's 128 scores lie in two threads (halves of the keys by warp group), which
-// mask them and exchange their maxima; the reference maximum moves only past a slack of
-// 8 (log2 units), so O is rarely rescaled.
+// S(j + 1) runs while the softmax works on tile j.  (One CTA with two blocks of 128 queries has no
+// room for that: sharing one score region between the blocks took 5,500 cycles for the same
+// 2 * 256 * 128 pairs that two tiles take 3,150 for.)
+//
+// Resident clusters take one block of queries after another: while a block runs, the next is asked
+// for (cluster launch control), and its first copies and scores run behind the last softmax.
+// Launching a cluster a block cost 8,500 cycles a block (one prompt of 4,096 tokens and 32 heads:
+// 138.7 us against 120.8).  Up to 32 rows the longest blocks are given out first.
+//
+// A query's 128 scores lie in two threads, which mask them and exchange their maxima; the reference
+// maximum moves only past a slack of 8 (log2 units), so O is rarely rescaled.
+//
+// Per tile the tensor pipe works (12 + 8) * 64 = 1,280 cycles, and the softmax takes 1,500: 512
+// of the special-function unit (4 cycles a warp's exponent), as many of single-issue
+// operations, and the latencies of the barriers between them.  Measured for that prompt: 113.0 us
+// (1.52 PFLOP/s); of 117.8 before the last step 103 were left without the exponents and 108 with a
+// third of the score products.
+// Other splits of the softmax were no faster: four threads a query 120.6, one thread with
+// the next tile's scores in flight 131, two warps on alternate tiles 133 us.
 //
 // P is rounded to bf16 when the output is (it adds about what the output's own
 // rounding does; f32 output: a bf16 pair), everything else is f32.  Every wait is bounded; on
@@ -27,6 +39,8 @@
 // frees its tensor memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 #include <math_constants.h>
 
 #include "latent.h"
@@ -52,8 +66,11 @@ constexpr int kKSlab = kHalf * 128;    // 8 KB
 constexpr int kQBytes = kQSlabs * kQSlab, kKBytes = kQSlabs * kKSlab;
 constexpr int kVBytes = kKeys * 128;   // this CTA's 64 value columns
 constexpr int kRing = 4;               // tiles in flight, of K and of V
-constexpr int kThreads = 384;          // warps: 0 S, 1 PV, 2 Q and K copies, 3 V copies, 4-11 softmax
-constexpr int kSoftWarps = 8;
+constexpr int kSplit = 2;              // softmax threads of a query
+constexpr int kSoftWarps = 4 * kSplit;
+constexpr int kCols = kKeys / kSplit;  // scores (and output columns) a thread
+constexpr int kScores = kSoftWarps, kValues = kScores + 1, kKeyCopies = kScores + 2, kValueCopies = kScores + 3;
+constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kTmemCols = 512;
 constexpr float kSlack = 8.f;
 constexpr int kSCol = 0, kPCol = 256, kOCol = 384;
@@ -78,17 +95,19 @@ enum : int {
   kWorkFree = kWorkFull + 2,  // [2] and read by all warps
   kReply = kWorkFree + 2,    // the answer to a request for a block landed
   kReplyRead = kReply + 1,   // (even CTA) and was read in both CTAs
-  kDrainS = kReplyRead + 1,
+  kDrainS = kReplyRead + 1,  // all products done
   kDrainV = kDrainS + 1,
   kNumBars = kDrainV + 1
 };
 constexpr int kOffWork = (kOffBar + kNumBars * 8 + 15) & ~15;  // Work[2]
 constexpr int kOffReply = kOffWork + 2 * 32;                   // 16 bytes
-constexpr int kOffRed = kOffReply + 16;                        // float[2][2][128] maxima (then sums)
-constexpr int kOffSlot = kOffRed + 2 * 2 * kRows * 4;
+constexpr int kOffRed = kOffReply + 16;        // float[2][kSplit][128] maxima (then sums)
+constexpr int kOffSlot = kOffRed + 2 * kSplit * kRows * 4;
 constexpr int kOffAbort = kOffSlot + 4;
-constexpr int kSmemBytes = kOffAbort + 4 + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr int kUsed = kOffAbort + 4;
+// the launch asks for what there is of the 1,023 bytes that the base's alignment could take
+constexpr int kSmemBytes = kUsed + 1024 < 232448 ? kUsed + 1024 : 232448;
+static_assert(kUsed <= 232448, "shared memory per CTA");
 constexpr int kReaders = 3 + kSoftWarps;  // warps that read a block's numbers
 
 constexpr uint32_t kIdescS = tc::instr_desc(2 * kRows, kKeys, false, false);
@@ -182,16 +201,36 @@ struct Blocks {
   }
 };
 
-// Whether any thread of two warps says so, told to all of them (named barrier `id`).
-__device__ __forceinline__ bool pair_any(int id, bool x) {
+// Whether any thread of a query's warps says so, told to all of them (named barrier `id`).
+__device__ __forceinline__ bool any_of(int id, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(id), "r"((uint32_t)x)
+      : "r"(id), "n"(32 * kSplit), "r"((uint32_t)x)
       : "memory");
   return r != 0;
+}
+
+// Lane i of four neighbours has piece k of row i in y[k] and gets piece i of row k.
+__device__ __forceinline__ void transpose4(uint32_t (&y)[4][4], int lane) {
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (!(k & d))
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t give = upper ? y[k][e] : y[k + d][e];
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, give, d);
+          if (upper)
+            y[k][e] = got;
+          else
+            y[k + d][e] = got;
+        }
+  }
 }
 
 // Ask for a cluster of the grid that has not started, in both CTAs' shared memory, counted
@@ -228,13 +267,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *sm = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  if (sm + kUsed > smem_raw + kSmemBytes) {  // (never seen) no room for the alignment
+    if (threadIdx.x == 0) raise_fault(a.status, PSKV_FAULT_WAIT_TIMEOUT);
+    return;
+  }
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
   uint32_t *slot = reinterpret_cast<uint32_t *>(sm + kOffSlot);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffAbort);
   const int warp = tc2::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = tc2::cluster_rank();
   const bool lead = elect_one();  // one thread of each warp
-  if (warp == 2) {
+  if (warp == kKeyCopies) {
     if (lane == 0) {
       for (int s = 0; s < kRing; ++s) {
         mbar_init(&bars[kFullK + s], 1);
@@ -264,13 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tc2::prefetch_map(&maps.q);
     tc2::prefetch_map(&maps.k);
     tc2::prefetch_map(&maps.rot);
-  } else if (warp == 0) {
+  } else if (warp == kScores) {
     tc2::alloc(slot, kTmemCols);
   }
   pdl_wait();
   pdl_launch_dependents();
   Blocks rows;
-  if (warp == 2) {
+  if (warp == kKeyCopies) {
     rows.load(a, 0, lane);
     if (blockIdx.x == 0) {
       // offsets that the host copies do not allow: those rows, or the blocks past the grid's, are
@@ -308,232 +351,246 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   };
 
   // g counts a CTA's tiles over all its blocks: rings, regions and parities go by it
-  if (warp == 0) {
-    // ---- the score products (all lanes alike, one issues)
-    bool ok = true;
-    const uint32_t q = smem_u32(sm + kOffQ), k = smem_u32(sm + kOffK);
-    Work w;
-    for (int i = 0, g = 0, nb = 0; ok; ++i) {
-      ok = next(i, w);
-      if (!ok || !w.more) break;
-      if (rank != 0 || w.n == 0) continue;
-      ok = wait(kQFull, nb++ & 1);
-      for (int j = 0; ok && j < w.n; ++j, ++g) {
-        const int st = g % kRing, r = g & 1;
-        ok = wait(kFullK + st, (g / kRing) & 1) && (g < 2 || wait(kSFree + r, (g / 2 - 1) & 1));
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t kt = k + st * kKBytes;
+  if (warp >= kSoftWarps) {
+    if (warp == kScores) {
+      // ---- the score products (all lanes alike, one of the even CTA's issues)
+      bool ok = true;
+      const uint32_t q = smem_u32(sm + kOffQ), k = smem_u32(sm + kOffK);
+      Work w;
+      for (int i = 0, g = 0, nb = 0; ok; ++i) {
+        ok = next(i, w);
+        if (!ok || !w.more) break;
+        if (rank != 0 || w.n == 0) continue;
+        ok = wait(kQFull, nb++ & 1);
+        for (int j = 0; ok && j < w.n; ++j, ++g) {
+          const int st = g % kRing, r = g & 1;
+          ok = wait(kFullK + st, (g / kRing) & 1) && (g < 2 || wait(kSFree + r, (g / 2 - 1) & 1));
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t kt = k + st * kKBytes;
 #pragma unroll
-        for (int kk = 0; kk < 4 * kQSlabs; ++kk)
-          tc2::mma(tmem + kSCol + kKeys * r,
-                   tc::smem_desc(q + (kk >> 2) * kQSlab + (kk & 3) * 32, 16, 1024),
-                   tc::smem_desc(kt + (kk >> 2) * kKSlab + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0,
-                   lead);
-        tc2::commit_both(bars + kSFull + r, lead);
-        tc2::commit_both(bars + kEmptyK + st, lead);
+          for (int kk = 0; kk < 4 * kQSlabs; ++kk)
+            tc2::mma(tmem + kSCol + kKeys * r,
+                     tc::smem_desc(q + (kk >> 2) * kQSlab + (kk & 3) * 32, 16, 1024),
+                     tc::smem_desc(kt + (kk >> 2) * kKSlab + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0,
+                     lead);
+          tc2::commit_both(bars + kSFull + r, lead);
+          tc2::commit_both(bars + kEmptyK + st, lead);
+        }
+        tc2::commit_both(bars + kQFree, lead);
       }
-      tc2::commit_both(bars + kQFree, lead);
-    }
-    if (rank == 0) tc2::commit_both(bars + kDrainS, lead);
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---- the value products
-    bool ok = true;
-    const uint32_t v = smem_u32(sm + kOffV);
-    Work w;
-    for (int i = 0, g = 0; ok; ++i) {
-      ok = next(i, w);
-      if (!ok || !w.more) break;
-      if (rank != 0) continue;
-      for (int j = 0; ok && j < w.n; ++j, ++g) {
-        const int st = g % kRing, pb = g % kPBufs;
-        ok = wait(kFullV + st, (g / kRing) & 1) && wait(kPFull + pb, (g / kPBufs) & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t vt = v + st * kVBytes;
+      if (rank == 0) tc2::commit_both(bars + kDrainS, lead);
+      __syncwarp();
+    } else if (warp == kValues) {
+      // ---- the value products
+      bool ok = true;
+      const uint32_t v = smem_u32(sm + kOffV);
+      Work w;
+      for (int i = 0, g = 0; ok; ++i) {
+        ok = next(i, w);
+        if (!ok || !w.more) break;
+        if (rank != 0) continue;
+        for (int j = 0; ok && j < w.n; ++j, ++g) {
+          const int st = g % kRing, pb = g % kPBufs;
+          ok = wait(kFullV + st, (g / kRing) & 1) && wait(kPFull + pb, (g / kPBufs) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t vt = v + st * kVBytes;
 #pragma unroll
-        for (int part = 0; part < (kLo ? 2 : 1); ++part)
+          for (int part = 0; part < (kLo ? 2 : 1); ++part)
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc2::mma_ts(tmem + kOCol, tmem + kPCol + 64 * (pb + part) + 8 * kk,
-                        tc::smem_desc(vt + kk * 2048, kVBytes, 1024), kIdescPV,
-                        j > 0 || part > 0 || kk > 0, lead);
-        tc2::commit_both(bars + kPvDone + pb, lead);
-        tc2::commit_both(bars + kEmptyV + st, lead);
-      }
-    }
-    if (rank == 0) tc2::commit_both(bars + kDrainV, lead);
-    __syncwarp();
-  } else if (warp == 2) {
-    // ---- the blocks; Q (queries behind the row's last: other rows' or zeros), then K: this
-    // CTA's half.  The next block is asked for when one begins and looked at behind its copies.
-    const uint32_t reply = smem_u32(sm + kOffReply);
-    int x = blockIdx.x, g = 0, nb = 0, i = 0;
-    bool ok = true, asked = false;
-    for (;; ++i) {
-      Work w{};
-      w.more = x >= 0;
-      if (x >= 0) {
-        const int pair = x >> 1;
-        w.h = pair % a.num_heads;
-        const int row = rows.find(a, pair / a.num_heads, lane, w.t0);
-        if (row >= 0) {
-          w.q0 = __shfl_sync(0xffffffffu, rows.q0, row);
-          w.k0 = __shfl_sync(0xffffffffu, rows.k0, row);
-          w.nq = __shfl_sync(0xffffffffu, rows.nq, row);
-          w.nk = __shfl_sync(0xffffffffu, rows.nk, row);
-          // tiles up to the last own key
-          w.n = (w.nk - w.nq + min(w.nq, w.t0 + 2 * kRows) + kKeys - 1) / kKeys;
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              tc2::mma_ts(tmem + kOCol, tmem + kPCol + 64 * (pb + part) + 8 * kk,
+                          tc::smem_desc(vt + kk * 2048, kVBytes, 1024), kIdescPV,
+                          j > 0 || part > 0 || kk > 0, lead);
+          tc2::commit_both(bars + kPvDone + (g & 1), lead);
+          tc2::commit_both(bars + kEmptyV + st, lead);
         }
       }
-      ok = i < 2 || wait(kWorkFree + (i & 1), (i / 2 - 1) & 1);
-      if (!ok) break;
-      if (lane == 0) works[i & 1] = w;
+      if (rank == 0) tc2::commit_both(bars + kDrainV, lead);
       __syncwarp();
-      if (lead) mbar_arrive(bars + kWorkFull + (i & 1));
-      if (!w.more) break;
-      if (rank == 0) {
-        ok = i == 0 || wait(kReplyRead, (i - 1) & 1);
-        if (!ok) break;
-        ask_for_cluster(reply, smem_u32(bars + kReply), lead);
-      }
-      tc2::expect_tx(bars + kReply, 16, lead);
-      asked = true;
-      if (w.n > 0) {
-        ok = nb == 0 || wait(kQFree, (nb - 1) & 1);
-        if (!ok) break;
-        ++nb;
-        tc2::expect_tx(bars + kQFull, 2 * kQBytes, lead && rank == 0);
-        tc2::tma_load_3d(smem_u32(sm + kOffQ), &maps.q, 0, w.q0 + w.t0 + (int)rank * kRows, kQSlabs * w.h,
-                         tc2::map_to(smem_u32(bars + kQFull), 0), lead);
-      }
-      for (int j = 0; j < w.n; ++j, ++g) {
-        const int st = g % kRing;
-        ok = g < kRing || wait(kEmptyK + st, (g / kRing - 1) & 1);
-        if (!ok) break;
-        const uint32_t dst = smem_u32(sm + kOffK + st * kKBytes);
-        const uint32_t bar = tc2::map_to(smem_u32(bars + kFullK + st), 0);
-        const int y = w.k0 + j * kKeys + kHalf * (int)rank;
-        tc2::expect_tx(bars + kFullK + st, 2 * kKBytes, lead && rank == 0);
-        tc2::tma_load_3d(dst, &maps.k, 0, y, 4 * w.h, bar, lead);
-        tc2::tma_load_3d(dst + 2 * kKSlab, &maps.rot, 0, y, 0, bar, lead);
-      }
-      if (!ok) break;
-      ok = wait(kReply, i & 1);
-      if (!ok) break;
-      asked = false;
-      x = cluster_given(reply);
-      __syncwarp();
-      tc::fence_smem_for_async();  // read before the next answer lands
-      tc2::arrive_pair(tc2::map_to(smem_u32(bars + kReplyRead), 0), lead);
-    }
-    // every copy of both CTAs landed before they leave (their count is the even CTA's)
-    if (asked) mbar_wait(bars + kReply, i & 1);
-    if (rank == 0) {
-      for (int s = max(0, g - kRing); s < g; ++s) mbar_wait(bars + kFullK + s % kRing, (s / kRing) & 1);
-      if (nb > 0) mbar_wait(bars + kQFull, (nb - 1) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 3) {
-    // ---- V: this CTA's 64 columns of every tile.  The tile with the row's last key: rows
-    // behind it are another row's and meet P = 0, so they are zeroed first.
-    bool ok = true;
-    Work w;
-    int g = 0, seen = 0;
-    for (int i = 0; ok; ++i) {
-      ok = next(i, w);
-      if (!ok || !w.more) break;
-      const bool ragged = w.n * kKeys > w.nk;
-      for (int j = 0; ok && j < w.n; ++j, ++g) {
-        const int st = g % kRing;
-        ok = g < kRing || wait(kEmptyV + st, (g / kRing - 1) & 1);
-        if (!ok) break;
-        const uint32_t full = tc2::map_to(smem_u32(bars + kFullV + st), 0);
-        unsigned char *dst = sm + kOffV + st * kVBytes;
-        const bool whole = !(ragged && j == w.n - 1);
-        if (!whole)
-          tc2::expect_tx(bars + kRagged, kVBytes, lead);
-        else
-          tc2::expect_tx(bars + kFullV + st, 2 * kVBytes, lead && rank == 0);
-        tc2::tma_load_3d(smem_u32(dst), &maps.v, 0, w.k0 + j * kKeys, 4 * w.h + 2 + (int)rank,
-                         whole ? full : smem_u32(bars + kRagged), lead);
-        if (!whole) {
-          ok = wait(kRagged, seen & 1);
-          if (!ok) {
-            mbar_wait(bars + kRagged, seen & 1);
-            break;
+    } else if (warp == kKeyCopies) {
+      // ---- the blocks; Q (queries behind the row's last: other rows' or zeros), then K: this
+      // CTA's half.  The next block is asked for when one begins and looked at behind its copies.
+      const uint32_t reply = smem_u32(sm + kOffReply);
+      int x = blockIdx.x, g = 0, nb = 0, i = 0;
+      bool ok = true, asked = false;
+      for (;; ++i) {
+        Work w{};
+        w.more = x >= 0;
+        if (x >= 0) {
+          const int pair = x >> 1;
+          w.h = pair % a.num_heads;
+          const int row = rows.find(a, pair / a.num_heads, lane, w.t0);
+          if (row >= 0) {
+            w.q0 = __shfl_sync(0xffffffffu, rows.q0, row);
+            w.k0 = __shfl_sync(0xffffffffu, rows.k0, row);
+            w.nq = __shfl_sync(0xffffffffu, rows.nq, row);
+            w.nk = __shfl_sync(0xffffffffu, rows.nk, row);
+            // tiles up to the last own key
+            w.n = (w.nk - w.nq + min(w.nq, w.t0 + 2 * kRows) + kKeys - 1) / kKeys;
           }
-          ++seen;
-          const int left = w.nk - j * kKeys;
-          for (int e = lane; e < (kKeys - left) * 8; e += 32)
-            *reinterpret_cast<uint4 *>(dst + (left + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-          tc::fence_smem_for_async();
-          __syncwarp();
-          if (rank == 0 && lead) mbar_arrive(bars + kFullV + st);  // in place of the copies' count
         }
-        tc2::arrive_pair(full, lead);
+        ok = i < 2 || wait(kWorkFree + (i & 1), (i / 2 - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) works[i & 1] = w;
+        __syncwarp();
+        if (lead) mbar_arrive(bars + kWorkFull + (i & 1));
+        if (!w.more) break;
+        if (rank == 0) {
+          ok = i == 0 || wait(kReplyRead, (i - 1) & 1);
+          if (!ok) break;
+          ask_for_cluster(reply, smem_u32(bars + kReply), lead);
+        }
+        tc2::expect_tx(bars + kReply, 16, lead);
+        asked = true;
+        if (w.n > 0) {
+          ok = nb == 0 || wait(kQFree, (nb - 1) & 1);
+          if (!ok) break;
+          ++nb;
+          tc2::expect_tx(bars + kQFull, 2 * kQBytes, lead && rank == 0);
+          tc2::tma_load_3d(smem_u32(sm + kOffQ), &maps.q, 0, w.q0 + w.t0 + (int)rank * kRows, kQSlabs * w.h,
+                           tc2::map_to(smem_u32(bars + kQFull), 0), lead);
+        }
+        for (int j = 0; j < w.n; ++j, ++g) {
+          const int st = g % kRing;
+          ok = g < kRing || wait(kEmptyK + st, (g / kRing - 1) & 1);
+          if (!ok) break;
+          const uint32_t dst = smem_u32(sm + kOffK + st * kKBytes);
+          const uint32_t bar = tc2::map_to(smem_u32(bars + kFullK + st), 0);
+          const int y = w.k0 + j * kKeys + kHalf * (int)rank;
+          tc2::expect_tx(bars + kFullK + st, 2 * kKBytes, lead && rank == 0);
+          tc2::tma_load_3d(dst, &maps.k, 0, y, 4 * w.h, bar, lead);
+          tc2::tma_load_3d(dst + 2 * kKSlab, &maps.rot, 0, y, 0, bar, lead);
+        }
+        if (!ok) break;
+        ok = wait(kReply, i & 1);
+        if (!ok) break;
+        asked = false;
+        x = cluster_given(reply);
+        __syncwarp();
+        tc::fence_smem_for_async();  // read before the next answer lands
+        tc2::arrive_pair(tc2::map_to(smem_u32(bars + kReplyRead), 0), lead);
       }
+      // every copy of both CTAs landed before they leave (their count is the even CTA's)
+      if (asked) mbar_wait(bars + kReply, i & 1);
+      if (rank == 0) {
+        for (int s = max(0, g - kRing); s < g; ++s) mbar_wait(bars + kFullK + s % kRing, (s / kRing) & 1);
+        if (nb > 0) mbar_wait(bars + kQFull, (nb - 1) & 1);
+      }
+      __syncwarp();
+    } else if (warp == kValueCopies) {
+      // ---- V: this CTA's 64 columns of every tile.  The tile with the row's last key: rows
+      // behind it are another row's and meet P = 0, so they are zeroed first.
+      bool ok = true;
+      Work w;
+      int g = 0, seen = 0;
+      for (int i = 0; ok; ++i) {
+        ok = next(i, w);
+        if (!ok || !w.more) break;
+        const bool ragged = w.n * kKeys > w.nk;
+        for (int j = 0; ok && j < w.n; ++j, ++g) {
+          const int st = g % kRing;
+          ok = g < kRing || wait(kEmptyV + st, (g / kRing - 1) & 1);
+          if (!ok) break;
+          const uint32_t full = tc2::map_to(smem_u32(bars + kFullV + st), 0);
+          unsigned char *dst = sm + kOffV + st * kVBytes;
+          const bool whole = !(ragged && j == w.n - 1);
+          if (!whole)
+            tc2::expect_tx(bars + kRagged, kVBytes, lead);
+          else
+            tc2::expect_tx(bars + kFullV + st, 2 * kVBytes, lead && rank == 0);
+          tc2::tma_load_3d(smem_u32(dst), &maps.v, 0, w.k0 + j * kKeys, 4 * w.h + 2 + (int)rank,
+                           whole ? full : smem_u32(bars + kRagged), lead);
+          if (!whole) {
+            ok = wait(kRagged, seen & 1);
+            if (!ok) {
+              mbar_wait(bars + kRagged, seen & 1);
+              break;
+            }
+            ++seen;
+            const int left = w.nk - j * kKeys;
+            for (int e = lane; e < (kKeys - left) * 8; e += 32)
+              *reinterpret_cast<uint4 *>(dst + (left + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+            tc::fence_smem_for_async();
+            __syncwarp();
+            if (rank == 0 && lead) mbar_arrive(bars + kFullV + st);  // in place of the copies' count
+          }
+          tc2::arrive_pair(full, lead);
+        }
+      }
+      __syncwarp();
+      if (rank == 0)
+        for (int s = max(0, g - kRing); s < g; ++s) mbar_wait(bars + kFullV + s % kRing, (s / kRing) & 1);
+      __syncwarp();
     }
-    __syncwarp();
-    if (rank == 0)
-      for (int s = max(0, g - kRing); s < g; ++s) mbar_wait(bars + kFullV + s % kRing, (s / kRing) & 1);
-    __syncwarp();
   } else {
-    // ---- the softmax: thread (query i, keys 64 gr .. + 63 of the tile).  A block's loop never
-    // leaves early (the two warps of a query's threads meet every tile); after a failed wait
-    // nothing is written, and both warps leave before the next block.
-    const int w4 = warp & 3, gr = (warp - 4) >> 2, row = 32 * w4 + lane;
+    // ---- the softmax: thread (query, keys kCols part .. of the tile; at the end, as many output
+    // columns).  A block's loop never leaves early (the warps of a query's threads meet every
+    // tile); after a failed wait nothing is written, and all leave before the next block.
+    const int w4 = warp & 3, part = warp >> 2, row = 32 * w4 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * w4) << 16);
-    const float sc = a.scale_log2;
-    float *red = reinterpret_cast<float *>(sm + kOffRed);
+    // scores in log2 units are mul * f; scales that are not positive are taken before the mask
+    const float sc = a.scale_log2, mul = sc > 0.f ? sc : 1.f;
+    float *red = reinterpret_cast<float *>(sm + kOffRed) + row;
     const uint32_t s_free = tc2::map_to(smem_u32(bars + kSFree), 0);
     const uint32_t p_full = tc2::map_to(smem_u32(bars + kPFull), 0);
+    auto wait = [&](int s, uint32_t parity) {  // (one vote, not one a poll)
+      if (__all_sync(0xffffffffu, mbar_wait(bars + s, parity))) return true;
+      *abort_flag = 1;
+      raise_fault(a.status, PSKV_FAULT_WAIT_TIMEOUT);
+      return false;
+    };
+    auto values_done = [&](int tile) { return wait(kPvDone + (tile & 1), (tile >> 1) & 1); };
     bool ok = true;
     Work w;
     for (int i = 0, g = 0;; ++i) {
       ok = ok && next(i, w);
-      if (pair_any(1 + w4, !ok) || !w.more) break;
+      if (any_of(1 + w4, !ok) || !w.more) break;
       if (w.n == 0) continue;
       const int t = w.t0 + (int)rank * kRows + row;
       const int lim = t < w.nq ? w.nk - w.nq + t + 1 : 0;  // keys below lim are seen
+      const int all_see = (int)__reduce_min_sync(0xffffffffu, (uint32_t)lim);
       float m = -CUDART_INF_F, l = 0.f;
       for (int j = 0; j < w.n; ++j, ++g) {
         const int r = g & 1, pb = g % kPBufs;
         ok = ok && wait(kSFull + r, (g >> 1) & 1);
         tc::fence_after_sync();
-        uint32_t va[32], vb[32];
-        tc::ld32(lane_base + kSCol + kKeys * r + kHalf * gr, va);
-        tc::ld32(lane_base + kSCol + kKeys * r + kHalf * gr + 32, vb);
+        uint32_t f[kCols / 32][32];
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c)
+          tc::ld32(lane_base + kSCol + kKeys * r + kCols * part + 32 * c, f[c]);
         tc::wait_ld();
-        tc::reg_fence(va);
-        tc::reg_fence(vb);
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) tc::reg_fence(f[c]);
         tc::fence_before_sync();
         __syncwarp();
         tc2::arrive_pair(s_free + 8 * r, lead);
-        float f[kHalf];
+        // P's buffer of tile g - 2 (the f32 form's one buffer is waited for below)
+        if (g >= 2) ok = ok && values_done(g - 2);
+        tc::fence_after_sync();
+        const int key0 = j * kKeys + kCols * part;
+        if (key0 + kCols > all_see || !(sc > 0.f)) {
+          const int seen = lim - key0;  // of this thread's keys
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          f[c] = __uint_as_float(va[c]);
-          f[32 + c] = __uint_as_float(vb[c]);
+          for (int c = 0; c < kCols; ++c) {
+            float x = __uint_as_float(f[c >> 5][c & 31]);
+            if (!(sc > 0.f)) x *= sc;
+            f[c >> 5][c & 31] = c < seen ? __float_as_uint(x) : 0xff800000u;
+          }
         }
-        const int key0 = j * kKeys + kHalf * gr;
-        // scores in log2 units are mul * f: whole tiles leave the product to the exponent's
-        // multiply-add, others (and scales that are not positive) take it before the mask
-        float mul = sc;
-        if (__any_sync(0xffffffffu, key0 + kHalf > lim || !(sc > 0.f))) {
-          mul = 1.f;
+        float mx[4];
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c) f[c] = key0 + c < lim ? f[c] * sc : -CUDART_INF_F;
+        for (int c = 0; c < kCols; ++c) {
+          const float x = __uint_as_float(f[c >> 5][c & 31]);
+          mx[c & 3] = c < 4 ? x : fmaxf(mx[c & 3], x);
         }
-        float mx[4] = {f[0], f[1], f[2], f[3]};
+        float *all = red + r * kSplit * kRows;
+        all[part * kRows] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + w4), "n"(32 * kSplit) : "memory");
+        float mt = all[0];
 #pragma unroll
-        for (int c = 4; c < kHalf; ++c) mx[c & 3] = fmaxf(mx[c & 3], f[c]);
-        float *mine = red + r * 2 * kRows + row;
-        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
-        mine[gr * kRows] = mt;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + w4) : "memory");
-        mt = fmaxf(mt, mine[(gr ^ 1) * kRows]);
+        for (int c = 1; c < kSplit; ++c) mt = fmaxf(mt, all[c * kRows]);
         float alpha = 1.f;
         bool rescale = false;
         if (mt > m + kSlack) {
@@ -543,87 +600,103 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           m = mt;
         }
         const float off = m == -CUDART_INF_F ? 0.f : -m;
-        uint32_t hi[32], lo[kLo ? 32 : 1];
+        const uint32_t weights = lane_base + kPCol + 64 * pb + kCols / 2 * part;
+        uint32_t hi[kCols / 32][16], lo[kLo ? kCols / 32 : 1][16];
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float p0 = ex2(fmaf(f[2 * e], mul, off)), p1 = ex2(fmaf(f[2 * e + 1], mul, off));
-          hi[e] = pack_bf16x2(p0, p1);
-          if constexpr (kLo) lo[e] = pack_bf16x2(p0 - bf16_lo(hi[e]), p1 - bf16_hi(hi[e]));
-          s0 += p0;
-          s1 += p1;
+        for (int c = 0; c < kCols / 32; ++c) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = ex2(fmaf(__uint_as_float(f[c][2 * e]), mul, off));
+            const float p1 = ex2(fmaf(__uint_as_float(f[c][2 * e + 1]), mul, off));
+            const uint32_t p = pack_bf16x2(p0, p1);
+            hi[c][e] = p;
+            if constexpr (kLo) lo[c][e] = pack_bf16x2(p0 - bf16_lo(p), p1 - bf16_hi(p));
+            s0 += p0;
+            s1 += p1;
+          }
+          if constexpr (!kLo) tc::st16(weights + 16 * c, hi[c]);
         }
         l += s0 + s1;
-        // P's buffer is free once the values of tile g - kPBufs are done
-        if (g >= kPBufs) ok = ok && wait(kPvDone + pb, (g / kPBufs - 1) & 1);
         if (__any_sync(0xffffffffu, rescale)) {
-          ok = ok && wait(kPvDone + (g - 1) % kPBufs, ((g - 1) / kPBufs) & 1);
+          ok = ok && values_done(g - 1);
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int c = 2 * gr; c < 2 * gr + 2; ++c) {
+          for (int c = 0; c < kCols / 32; ++c) {
             uint32_t o[32];
-            tc::ld32(lane_base + kOCol + 32 * c, o);
+            tc::ld32(lane_base + kOCol + kCols * part + 32 * c, o);
             tc::wait_ld();
             tc::reg_fence(o);
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tc::st32(lane_base + kOCol + 32 * c, o);
+            tc::st32(lane_base + kOCol + kCols * part + 32 * c, o);
           }
         }
-        tc::fence_after_sync();
-        tc::st32(lane_base + kPCol + 64 * pb + 32 * gr, hi);
-        if constexpr (kLo) tc::st32(lane_base + kPCol + 64 + 32 * gr, lo);
+        if constexpr (kLo) {
+          if (g >= 1) ok = ok && values_done(g - 1);
+          tc::fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) {
+            tc::st16(weights + 16 * c, hi[c]);
+            tc::st16(weights + 64 + 16 * c, lo[c]);
+          }
+        }
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
         tc2::arrive_pair(p_full + 8 * pb, lead);
       }
-      // ---- the sum over both threads, then O / l
-      float *sums = red + (g & 1) * 2 * kRows + row;
-      sums[gr * kRows] = l;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + w4) : "memory");
-      l = sums[0] + sums[kRows];
-      ok = ok && wait(kPvDone + (g - 1) % kPBufs, ((g - 1) / kPBufs) & 1);
+      // ---- the sum over the query's threads, then O / l
+      float *sums = red + (g & 1) * kSplit * kRows;
+      sums[part * kRows] = l;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + w4), "n"(32 * kSplit) : "memory");
+      l = sums[0];
+#pragma unroll
+      for (int c = 1; c < kSplit; ++c) l += sums[c * kRows];
+      if (g > 1) ok = ok && values_done(g - 2);
+      ok = ok && values_done(g - 1);
       tc::fence_after_sync();
       const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
-      uint4 *dst = reinterpret_cast<uint4 *>(
-          static_cast<unsigned char *>(a.out) +
-          (((size_t)(w.q0 + min(t, w.nq - 1)) * a.num_heads + w.h) * kDv + kDv / 2 * gr) * (kLo ? 4 : 2));
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t o[32];
-        tc::ld32(lane_base + kOCol + kDv / 2 * gr + 32 * c, o);
-        tc::wait_ld();
-        tc::reg_fence(o);
-        float y[32];
+      uint32_t o[kCols / 32][32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * inv;
-        if (ok && t < w.nq) {
-          if constexpr (kLo) {
+      for (int c = 0; c < kCols / 32; ++c) tc::ld32(lane_base + kOCol + kCols * part + 32 * c, o[c]);
+      tc::wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              reinterpret_cast<float4 *>(dst)[8 * c + k] =
-                  make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[4 * c + k] =
-                  make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
-                             pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
-          }
-        }
-      }
+      for (int c = 0; c < kCols / 32; ++c) tc::reg_fence(o[c]);
       tc::fence_before_sync();  // (the next block's first P tells the tensor core that O is read)
+      // 64 bytes a row and pass; four lanes exchange their 16-byte pieces so that the four write one
+      // row's (lanes storing their own rows took 3,000 cycles a block)
+      const int first = w.t0 + (int)rank * kRows + 32 * w4 + (lane & ~3);
+#pragma unroll
+      for (int pass = 0; pass < kCols / (kLo ? 16 : 32); ++pass) {
+        uint32_t y[4][4];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          if constexpr (kLo)
+            y[k >> 2][k & 3] = __float_as_uint(__uint_as_float(o[pass >> 1][16 * (pass & 1) + k]) * inv);
+          else
+            y[k >> 2][k & 3] = pack_bf16x2(__uint_as_float(o[kLo ? 0 : pass][2 * k]) * inv,
+                                           __uint_as_float(o[kLo ? 0 : pass][2 * k + 1]) * inv);
+        }
+        transpose4(y, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (ok && first + k < w.nq)
+            *reinterpret_cast<uint4 *>(
+                static_cast<unsigned char *>(a.out) +
+                (((size_t)(w.q0 + first + k) * a.num_heads + w.h) * kDv + kCols * part) * (kLo ? 4 : 2) +
+                64 * pass + 16 * (lane & 3)) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+      }
     }
   }
   // every product done (both CTAs learn it; every copy has landed) before the memory is released
-  if (warp == 0) mbar_wait(bars + kDrainS, 0);
-  if (warp == 1) mbar_wait(bars + kDrainV, 0);
+  if (warp == kScores) mbar_wait(bars + kDrainS, 0);
+  if (warp == kValues) mbar_wait(bars + kDrainV, 0);
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
   tc2::cluster_sync();
-  if (warp == 0) {
+  if (warp == kScores) {
     tc::fence_after_sync();
     tc2::dealloc(tmem, kTmemCols);
   }

@@ -305,6 +305,36 @@ def test_expanded_matches_f64(new, old, heads, dtype):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("new,old,heads", [
+    ([600, 520, 700], [130, 0, 64], 40),                    # more blocks than clusters fit the GPU
+    ([300] + [1, 0, 7, 33] * 10, [5] + [200, 0, 1, 90] * 10, 16),   # more rows than a warp's lanes
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_expanded_blocks_follow_one_another(new, old, heads, dtype):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(len(new))
+    cq = [0] + np.cumsum(new).tolist()
+    ck = [0] + np.cumsum([a + b for a, b in zip(new, old)]).tolist()
+    q, kv, rot = normal(gen, cq[-1], heads, 192), normal(gen, ck[-1], heads, 256), normal(gen, ck[-1], 64)
+    dev = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    out = pskv.prefill_attn_expanded(q, kv, rot, dev(cq), cq, dev(ck), ck, 192 ** -0.5, out_dtype=dtype, status=status)
+    check_attention(out, expanded_reference(q, kv, rot, cq, ck, 192 ** -0.5), float(kv.abs().max()))
+    again = [pskv.prefill_attn_expanded(q, kv, rot, dev(cq), cq, dev(ck), ck, 192 ** -0.5, out_dtype=dtype)
+             for _ in range(3)]
+    assert all(torch.equal(out, o) for o in again) and int(status[0]) == 0
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0])
+def test_expanded_scales_that_are_not_positive(scale):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    q, kv, rot = normal(gen, 200, 2, 192), normal(gen, 270, 2, 256), normal(gen, 270, 64)
+    dev = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    out = pskv.prefill_attn_expanded(q, kv, rot, dev([0, 200]), [0, 200], dev([0, 270]), [0, 270], scale)
+    check_attention(out, expanded_reference(q, kv, rot, [0, 200], [0, 270], scale), float(kv.abs().max()))
+
+
 def test_expanded_growing_scores():
     gen = torch.Generator(device="cuda")
     gen.manual_seed(2)
