@@ -455,8 +455,14 @@ int kv_prep_append_latent(const pskv_layout *layout, const pskv_latent_prep_desc
  *   num_tokens   1..PSKV_MAX_WINDOW_TOKENS
  *   seq_lens     each at least num_tokens, or 0: a row of a padded batch, whose
  *                outputs are zeros (no fault bit)
+ *   num_splits   0: chosen from the host lengths; else pieces of whole 128-key tiles,
+ *                this many at most for the longest row (shorter rows have fewer)
  *   workspace    decode_attn_latent_workspace_bytes(...) bytes, 16-byte aligned
- *                (NULL is fine where that is 0)
+ *                (NULL is fine where that is 0); its contents are this call's own (the
+ *                pieces are folded in one level: opts->merge_group is only checked)
+ * Keys that a token does not attend take no part, whatever their scores; those of the
+ * row's own later tokens have to hold finite values (they share its tiles), and
+ * slots behind the row's last key may hold anything.
  * The softmax weights meet the values as bf16 when the output is bf16 (their
  * rounding adds to the output about what its own rounding does), as a bf16
  * pair when it is f32; scores, maxima, sums and outputs accumulate in f32.
@@ -490,9 +496,11 @@ int decode_attn_latent_workspace_bytes(const pskv_layout *layout, const int32_t 
  *                         outside the host totals are never addressed)
  *   out     device [total_q][num_heads][PSKV_EXPANDED_V] of out_dtype
  * All 16-byte aligned.  The score of query i and key j is scale * (qn_i . kn_j
- * + qr_i . r_j).  The weights' precision is decode_attn_latent's.  A device
- * offset that disagrees with the host copies raises PSKV_FAULT_BAD_LENGTH in
- * status (device int32[4] or NULL), and that row is skipped.  No workspace.
+ * + qr_i . r_j).  The weights' precision is decode_attn_latent's, and so is what
+ * keys that are not attended may hold.  Device offsets that are not such offsets
+ * within the host totals raise PSKV_FAULT_BAD_LENGTH in status (device int32[4] or
+ * NULL), and those rows are left out; so do rows that take more blocks of 256 queries
+ * than the host's, and blocks past that count are left out.  No workspace.
  * Errors: INVALID_ARG (also a row with more queries than keys), CUDA. */
 int prefill_attn_expanded(const void *q, const void *kv, const void *k_rot, int64_t k_rot_token,
                           const int32_t *cu_q_host, const int32_t *cu_q, const int32_t *cu_k_host,
@@ -521,8 +529,8 @@ int prefill_attn_expanded(const void *q, const void *kv, const void *k_rot, int6
  *                 token, then -1
  *   accepted      device int32[batch]: drafts standing
  *   status        device int32[4] fault word or NULL
- * max_drafts 0..PSKV_MAX_WINDOW_TOKENS (drafts may be NULL when 0).  Values outside [0, 1] count as the nearer end,
- * NaN as 0.  A draft outside the vocabulary does not stand
+ * max_drafts 0..PSKV_MAX_WINDOW_TOKENS (drafts may be NULL when 0).  Values
+ * outside [0, 1] count as the nearer end, NaN as 0.  A draft outside the vocabulary does not stand
  * (PSKV_FAULT_BAD_TOKEN); a count outside its range is clamped
  * (PSKV_FAULT_BAD_LENGTH); a row without any weight draws -1
  * (PSKV_FAULT_EMPTY_ROW).  No workspace.  Errors: INVALID_ARG, CUDA. */

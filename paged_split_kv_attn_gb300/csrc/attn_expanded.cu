@@ -39,8 +39,6 @@
 // frees its tensor memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
-
-#include <type_traits>
 #include <math_constants.h>
 
 #include "latent.h"
@@ -128,7 +126,7 @@ static_assert(sizeof(Work) == 32, "two 16-byte words");
 // each: by their number of tiles, the longest first, so that the last to run are short (block
 // c of a row has before / 256 + c pairs of tiles, its level; the k-th block's level is found
 // by bisection over the count of blocks above).  More rows: one after the other, each
-// from its last block on.
+// from its last block on (six ragged chunks of 332 to 517 queries: 51.7 us against 45.2).
 struct Blocks {
   int base = 0;       // first row held
   int skipped = 0;    // blocks of the rows before

@@ -31,34 +31,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-// Whether a phase is complete, without suspending the thread.
-__device__ __forceinline__ bool phase_done(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// The wait of a thread that runs a role by itself: the abort flag is looked at only
-// where the phase is not yet complete (a whole-warp tc_wait with its vote costs 188
-// cycles on a phase that is, this one 52).
-__device__ __forceinline__ bool one_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                         int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-  }
-  *abort_flag = 1;
-  raise_fault(status, PSKV_FAULT_WAIT_TIMEOUT);
-  return false;
-}
-
-// The same for a whole warp that stays together: every poll ends in a vote, so the code
+// The wait of a whole warp that stays together: the abort flag is looked at only where the
+// phase is not yet complete, and every poll ends in a vote, so the code
 // around it keeps its uniform registers.  (One lane polling for the others takes the warp apart and
 // made the latent kernel's tiles twice as slow.)
 __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
