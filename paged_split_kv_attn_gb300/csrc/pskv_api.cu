@@ -406,7 +406,7 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   if ((rc = merge_group_of(opts, &mgroup))) return rc;  // (checked; the pieces fold in one level)
   int n_sm = 2;
   if (num_splits == 0 && (rc = sm_count(&n_sm))) return rc;
-  const LatentPlan plan = plan_latent(n_sm / 2, batch, seq_lens_host, (columns + 127) / 128, num_splits);
+  const LatentPlan plan = plan_latent(n_sm / 2, d.head_dim_v, batch, seq_lens_host, (columns + 127) / 128, num_splits);
   const bool direct = plan.splits == 1;
   WorkspacePlan w;
   // partials in groups of 32 query columns

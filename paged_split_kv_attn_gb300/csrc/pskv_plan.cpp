@@ -140,9 +140,12 @@ int plan_verify_splits(int64_t units, int slots, int64_t max_tiles) {
   return p < 1 ? 1 : (int)p;
 }
 
-LatentPlan plan_latent(int clusters, int32_t batch, const int32_t *seq_lens_host, int64_t blocks,
-                       int32_t num_splits) {
+LatentPlan plan_latent(int clusters, int head_dim_v, int32_t batch, const int32_t *seq_lens_host,
+                       int64_t blocks, int32_t num_splits) {
   if (clusters < 1) clusters = 1;
+  // in tiles of this width
+  const double piece_tiles = kLatentPieceTiles * 512 / head_dim_v;
+  const double merge_tiles = kLatentMergeTiles * 512 / head_dim_v;
   auto tiles = [&](int32_t b) { return ((int64_t)seq_lens_host[b] + kLatentTile - 1) / kLatentTile; };
   int64_t most = 1;
   for (int32_t b = 0; b < batch; ++b) most = tiles(b) > most ? tiles(b) : most;
@@ -155,7 +158,7 @@ LatentPlan plan_latent(int clusters, int32_t batch, const int32_t *seq_lens_host
   if (num_splits > 0) {
     q = (most + num_splits - 1) / num_splits;
   } else if (most > 1) {
-    double best = (double)((pieces(most) + clusters - 1) / clusters) * (kLatentPieceTiles + most);
+    double best = (double)((pieces(most) + clusters - 1) / clusters) * (piece_tiles + most);
     for (int64_t waves = 1; waves <= 4; ++waves) {
       int64_t lo = 1, hi = most;  // the smallest piece that takes this many waves
       while (lo < hi) {
@@ -168,8 +171,7 @@ LatentPlan plan_latent(int clusters, int32_t batch, const int32_t *seq_lens_host
       const int64_t cap = (most + PSKV_AUTO_MAX_SPLITS - 1) / PSKV_AUTO_MAX_SPLITS;
       if (lo < cap) lo = cap;
       if (lo >= most) continue;
-      const double cost = (double)((pieces(lo) + clusters - 1) / clusters) * (kLatentPieceTiles + lo) +
-                          kLatentMergeTiles;
+      const double cost = (double)((pieces(lo) + clusters - 1) / clusters) * (piece_tiles + lo) + merge_tiles;
       if (cost < best) {
         best = cost;
         q = lo;
