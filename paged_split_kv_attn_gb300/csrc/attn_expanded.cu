@@ -547,7 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (any_of(1 + w4, !ok) || !w.more) break;
       if (w.n == 0) continue;
       const int t = w.t0 + (int)rank * kRows + row;
-      const int lim = t < w.nq ? w.nk - w.nq + t + 1 : 0;  // keys below lim are seen
+      // keys below lim are seen (queries behind the last, whose results go nowhere, see all: a
+      // warp of theirs would mask every tile for nothing)
+      const int lim = t < w.nq ? w.nk - w.nq + t + 1 : w.nk;
       const int all_see = (int)__reduce_min_sync(0xffffffffu, (uint32_t)lim);
       float m = -CUDART_INF_F, l = 0.f;
       for (int j = 0; j < w.n; ++j, ++g) {

@@ -626,8 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int e = 2 * gr + kh; e < DC * es / 16; e += 4) dst[e] = make_uint4(0, 0, 0, 0);
         continue;
       }
-      const int lim =  // keys below lim are seen
-          col < cols ? pc.len - a.num_tokens + col / a.num_q_heads + 1 : 0;
+      // keys below lim are seen (columns behind the last, whose results go nowhere, see all: a
+      // warp of theirs would mask every tile for nothing)
+      const int lim = col < cols ? pc.len - a.num_tokens + col / a.num_q_heads + 1 : pc.len;
       float m = -CUDART_INF_F, l = 0.f;
       for (int j = 0; j < pc.n; ++j, ++g, ++meets) {
         const int r = g & 1;
