@@ -131,6 +131,50 @@ def test_shorter_and_longer_device_lengths_replay_one_plan():
     assert int(c.status[0]) == 0
 
 
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_many_rows(splits):
+    """More rows than a warp's lanes, two blocks of columns, rows of one piece between rows of several."""
+    c = LatentCase(13, [2 + 37 * b % 700 if b % 9 else 0 for b in range(45)], dc=256, page=32, heads=70, tokens=2)
+    out = c.run(num_splits=splits)
+    check_attention(out, c.reference(), vmax(c))
+    assert int(c.status[0]) == 0 and torch.equal(out, c.run(num_splits=splits))
+
+
+def test_bad_pages_between_pieces():
+    c = LatentCase(14, [3000, 1500], page=64)
+    c.table[0, 20:30] = c.pool.shape[0] + 3       # whole pieces of them
+    c.table[1, 7] = -2 ** 31
+    hidden = [torch.zeros(n, dtype=torch.bool, device="cuda") for n in (3000, 1500)]
+    hidden[0][1280:1920] = True
+    hidden[1][448:512] = True
+    for splits in (0, 1, 24):
+        check_attention(c.run(num_splits=splits), c.reference(hidden), vmax(c))
+        assert pskv.pskv_check_flags(c.layout, clear=True) == pskv.PSKV_FAULT_BAD_PAGE
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured calls of different shapes, replayed in turn on one stream over one scratch tensor."""
+    cases = [LatentCase(15, [900, 2000]), LatentCase(16, [3000], heads=50, tokens=3)]
+    size = max(pskv.latent_workspace(c.layout, c.lens_host, c.tokens, c.heads, table_stride=c.table.shape[1]).numel()
+               for c in cases)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    side, graphs, outs = torch.cuda.Stream(), [], []
+    for c in cases:
+        out = c.run(workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            c.run(workspace=ws, out=out)
+        graphs.append(graph)
+        outs.append(out)
+    for _ in range(3):
+        for graph, out in zip(graphs, outs):
+            out.fill_(float("nan"))
+            graph.replay()
+    for c, out in zip(cases, outs):
+        check_attention(out, c.reference(), vmax(c))
+
+
 def test_workspace_and_output_guards():
     """Nothing outside the workspace's bytes or the output is written."""
     c = LatentCase(11, [700, 300], heads=24, tokens=2)
@@ -347,6 +391,56 @@ def test_expanded_growing_scores():
     # |q.k| up to about 250: 192 * 2^-24 * 250 = 2.9e-3 of a score at worst
     assert (out.double() - ref).abs().max() <= 2 * (2.9e-3 + 2.0 ** -16) * float(kv.abs().max())
     assert float((out.double() - ref).norm() / ref.norm()) <= 2e-4
+
+
+def test_expanded_rows_do_not_meet():
+    """Another row's queries, keys and values may be anything: neighbours of a row that ends inside a tile."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    cq, ck = [0, 70, 100, 180], [0, 70, 130, 330]
+    q, kv, rot = normal(gen, 180, 3, 192), normal(gen, 330, 3, 256), normal(gen, 330, 64)
+    ref = expanded_reference(q, kv, rot, cq, ck, 0.07)
+    top = float(kv.abs().max())
+    dev = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    q[70:100], kv[70:130], rot[70:130] = float("nan"), float("inf"), float("nan")
+    for dtype in (torch.bfloat16, torch.float32):
+        out = pskv.prefill_attn_expanded(q, kv, rot, dev(cq), cq, dev(ck), ck, 0.07, out_dtype=dtype)
+        for a, e in ((0, 70), (100, 180)):
+            check_attention(out[a:e], ref[a:e], top)
+
+
+def test_expanded_captured_and_on_two_streams():
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    dev = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    cq, ck = [0, 300, 900], [0, 500, 1100]
+    q, kv, rot = normal(gen, 900, 40, 192), normal(gen, 1100, 40, 256), normal(gen, 1100, 64)
+    cu = dev(cq), dev(ck)
+    call = lambda out, **kw: pskv.prefill_attn_expanded(q, kv, rot, cu[0], cq, cu[1], ck, 0.07, out=out, **kw)
+    outs = [torch.empty(900, 40, 128, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    call(outs[0])
+    check_attention(outs[0], expanded_reference(q, kv, rot, cq, ck, 0.07), float(kv.abs().max()))
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):  # at once
+        for s, o in zip(sides, outs[1:]):
+            call(o, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=sides[0]):
+        call(outs[1])
+        call(outs[2])
+    cu[0].copy_(dev([0, 250, 850]))  # other offsets within the host's blocks
+    cu[1].copy_(dev([0, 410, 1010]))
+    for _ in range(3):
+        for o in outs[1:]:
+            o.fill_(7.0)
+        graph.replay()
+    ref = expanded_reference(q, kv, rot, [0, 250, 850], [0, 410, 1010], 0.07)
+    for o in outs[1:]:
+        check_attention(o[:850], ref[:850], float(kv.abs().max()))
+        assert (o[850:] == 7).all()
 
 
 def test_expanded_offsets_that_disagree_are_skipped_and_flagged():
