@@ -159,8 +159,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pskv_kernel_launches.argtypes = []
     lib.pskv_kernel_launches.restype = ctypes.c_uint64
     lib.pskv_version.argtypes = []
+    _bind_calls(lib)
     _LIB = lib
     return lib
+
+
+_calls = None
+
+
+def _bind_calls(lib) -> None:
+    """The compiled forms of the latent operators' calls, entering this library."""
+    global _calls
+    try:
+        from . import _calls as calls
+    except ImportError as e:
+        raise RuntimeError("the compiled calls are missing or do not fit this PyTorch: build them with "
+                           "`python -m paged_split_kv_attn_gb300.build --force`") from e
+    calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.kv_prep_append_latent, lib.decode_attn_latent, lib.prefill_attn_expanded, lib.verify_drafts)])
+    _calls = calls
 
 
 def _check(rc: int, what: str) -> None:
@@ -239,6 +256,7 @@ class Layout:
     def __init__(self, handle, k_pool, v_pool, status, desc):
         self._handle = handle
         self.k_pool, self.v_pool, self.status, self.desc = k_pool, v_pool, status, desc
+        self._pool = (handle.value, k_pool.get_device(), desc.head_dim_k, desc.head_dim_v)
 
     @property
     def handle(self):
@@ -268,6 +286,7 @@ class Layout:
         if self._handle is not None and _LIB is not None:
             _LIB.paged_kv_layout_destroy(self._handle)
         self._handle = None
+        self._pool = (None, -1, 0, 0)
 
     def __del__(self):
         try:
@@ -649,6 +668,7 @@ def _stream_on(stream, dev: int) -> int:
     return _raw_stream(dev) if stream is None else _stream(stream)
 
 
+_PAIRS = {"halves": 0, "adjacent": 1}
 _OUT_CODES = {torch.bfloat16: PSKV_DTYPE_BF16, torch.float32: PSKV_DTYPE_F32}
 
 
@@ -675,6 +695,12 @@ def kv_prep_append_latent(layout: Layout, x, row_of, pos_of, page_tables, pages_
     "halves" (i, i + 32) or "adjacent" (2i, 2i + 1).  ``host`` = (row_of, pos_of,
     pages_of_row) host copies for the up-front refusal."""
     lib = _LIB or load_library()
+    if host is None:
+        rc = _calls.append(*layout._pool, x, row_of, pos_of, page_tables, pages_of_row, eps, w, rope_cos, rope_sin,
+                           _PAIRS.get(pairs, -1), first_pos, q, q_out, dense,
+                           None if stream is None else _stream(stream))
+        if rc is not None:
+            return _check(rc, "kv_prep_append_latent")
     dev = _current_device()
     i32, f32, d = torch.int32, torch.float32, layout.desc.head_dim_k
     if layout.k_pool.get_device() != dev:
@@ -746,6 +772,12 @@ def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, 
     64], token t of row b at key ``seq_lens[b] - tokens + t``.  Returns ``out``
     [batch, tokens, heads, latent]; a row of length 0 gets zeros."""
     lib = _LIB or load_library()
+    if not merge_group and events is None:
+        r = _calls.decode(*layout._pool, q, page_tables, seq_lens, seq_lens_host, scale, num_splits, workspace, out,
+                          PSKV_DTYPE_BF16 if out_dtype is None else _OUT_CODES.get(out_dtype, -1),
+                          None if stream is None else _stream(stream))
+        if r is not None:
+            return r if type(r) is not int else _check(r, "decode_attn_latent")
     dev, desc = _current_device(), layout.desc
     if q.dim() != 4:
         raise ValueError(f"q must be [batch, tokens, heads, {desc.head_dim_k}]")
@@ -782,6 +814,11 @@ def prefill_attn_expanded(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale,
     may be strided); row b's queries are the last of its keys.  Returns ``out``
     [total_q, heads, 128]."""
     lib = _LIB or load_library()
+    r = _calls.prefill(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale, out,
+                       PSKV_DTYPE_BF16 if out_dtype is None else _OUT_CODES.get(out_dtype, -1), status,
+                       None if stream is None else _stream(stream))
+    if r is not None:
+        return r if type(r) is not int else _check(r, "prefill_attn_expanded")
     dev, bf16, i32 = _current_device(), torch.bfloat16, torch.int32
     if q.dim() != 3 or kv.dim() != 3:
         raise ValueError("q and kv must be [tokens, heads, columns]")
@@ -811,6 +848,10 @@ def verify_drafts(target_probs, draft_probs, drafts, u, num_drafts=None, tokens=
     uniform numbers.  Returns (``tokens`` int32 [batch, drafts + 1]: standing
     drafts, the drawn token, -1s; ``accepted`` int32 [batch])."""
     lib = _LIB or load_library()
+    r = _calls.verify(target_probs, draft_probs, drafts, u, num_drafts, tokens, accepted, status,
+                      None if stream is None else _stream(stream))
+    if r is not None:
+        return r if type(r) is not int else _check(r, "verify_drafts")
     dev, i32 = _current_device(), torch.int32
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError("target_probs must be [batch, drafts + 1, vocab]")

@@ -1,5 +1,6 @@
 """Build ``libpskv.so`` in-tree: every CUDA source compiled for sm_103a with nvcc,
-in parallel, then linked into one shared library (static CUDA runtime).
+in parallel, then linked into one shared library (static CUDA runtime), and ``_calls.so``, the
+latent operators' Python calls in compiled form.
 
 Usage: ``python -m paged_split_kv_attn_gb300.build [--force] [--verbose-ptxas]``.
 """
@@ -17,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpskv.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
@@ -42,9 +44,9 @@ def _deps() -> list[str]:
 
 
 def _up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -61,6 +63,26 @@ def _compile(src: str, verbose_ptxas: bool, extra: list[str], build_dir: str) ->
     return obj, res.stdout + res.stderr
 
 
+def _build_calls() -> None:
+    """The compiled Python calls (module ``_calls``), against the installed PyTorch."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-shared", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+           "-I", os.path.join(cuda, "include"), os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compiling torch_calls.cpp failed:\n{' '.join(cmd)}\n{res.stdout}{res.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, defines: dict | None = None,
           out: str = LIB) -> str:
     """Compile and link the library unless it is newer than every source; return its path.
@@ -73,8 +95,11 @@ def build(force: bool = False, verbose_ptxas: bool = False, defines: dict | None
         return LIB
     build_dir = BUILD if out == LIB else out + ".objs"
     os.makedirs(build_dir, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls) if out == LIB else None
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas, extra, build_dir), SOURCES))
+        if calls:
+            calls.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stdout.write(log)

@@ -459,6 +459,43 @@ def test_expanded_offsets_that_disagree_are_skipped_and_flagged():
         assert (out[20:] == 7).all()
 
 
+def test_compiled_and_python_calls_agree():
+    """Calls of the plain form are compiled; host lengths of other types, host copies and options take
+    the Python form."""
+    c = LatentCase(17, [700, 65, 0], heads=24, tokens=2)
+    ws = pskv.latent_workspace(c.layout, c.lens_host, 2, 24, table_stride=c.table.shape[1])
+    plain = c.run(workspace=ws)
+    with_arrays = pskv.decode_attn_latent(c.layout, c.q, c.table, c.lens, np.array(c.lens_host), c.scale)
+    assert torch.equal(plain, with_arrays) and torch.equal(plain, c.run(workspace=ws, merge_group=8))
+    assert torch.equal(plain, c.run())                                       # no workspace given
+    one = c.run(num_splits=1)                                                # and none needed
+    assert torch.equal(one, c.run(num_splits=1, workspace=ws)) and not one[2].any()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(8)
+    dev = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    q, kv, rot = normal(gen, 90, 2, 192), normal(gen, 120, 2, 256), normal(gen, 120, 64)
+    cu = dev([0, 30, 90]), dev([0, 50, 120])
+    a = pskv.prefill_attn_expanded(q, kv, rot, cu[0], [0, 30, 90], cu[1], [0, 50, 120], 0.1)
+    b = pskv.prefill_attn_expanded(q, kv, rot, cu[0], np.array([0, 30, 90]), cu[1], (0, 50, 120), 0.1)
+    assert torch.equal(a, b)
+    layout, ang = c.layout, torch.rand(800, 32, device="cuda")
+    x, lease = normal(gen, 2, 576), dev([11, 2, 0])
+    rows = dev([0, 1]), dev([650, 3])
+    pools = []
+    for host in (None, ([0, 1], [650, 3], [11, 2, 0])):
+        qo = torch.empty(2, 5, 64, dtype=torch.bfloat16, device="cuda")
+        pskv.kv_prep_append_latent(layout, x, *rows, c.table, lease, 1e-6, None, ang, ang, q=q[:2, :1, :64].expand(2, 5, 64),
+                                   q_out=qo, host=host)
+        pools.append((c.pool.clone(), qo))
+    assert torch.equal(pools[0][0].view(torch.int16), pools[1][0].view(torch.int16)) and torch.equal(pools[0][1], pools[1][1])
+    with pytest.raises(pskv.PskvError):
+        pskv.decode_attn_latent(layout, c.q, c.table, c.lens, [700, 65, 1], c.scale, workspace=ws)
+    with pytest.raises(ValueError):
+        c.run(workspace=ws, out=plain[:2])
+    with pytest.raises(TypeError):
+        c.run(workspace=ws, out_dtype=torch.float16)
+
+
 # ---- together ------------------------------------------------------------------------
 
 def test_a_speculative_step_over_a_latent_cache():
