@@ -262,8 +262,10 @@ struct Loader {
   int seq = 0, ragged = 0;   // chunks of all warps, chunks of this one landed on kRagged, over all pieces
 
   __device__ Loader(const LatentAttnArgs &a_, const CUtensorMap *m, unsigned char *sm_,
-                    uint64_t *bars_, volatile int *ab, uint32_t rank_, bool lead_, int which_)
-      : a(a_), map(m), sm(sm_), bars(bars_), abort_flag(ab), rank(rank_), lead(lead_), which(which_) {
+                    uint64_t *bars_, volatile int *ab, uint32_t rank_, bool lead_, int which_,
+                    const PageCache &pages_)
+      : a(a_), map(m), sm(sm_), bars(bars_), abort_flag(ab), rank(rank_), lead(lead_), pages(pages_),
+        which(which_) {
     lane = threadIdx.x & 31;
     whole = a.page_size % kHalf == 0;
   }
@@ -310,7 +312,7 @@ struct Loader {
   }
 
   __device__ bool run(const Piece &pc) {
-    pages.base = -1;  // another row's table
+    if (a.batch > 1) pages.base = -1;  // another row's table
     const int32_t *tbl = a.page_tables + (size_t)pc.b * a.table_stride;
     const int n_slots = (pc.len + a.page_size - 1) / a.page_size;
     Place at(pc.t0 * kKeys, a.page_size);
@@ -508,8 +510,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   auto wait = [&](int s, uint32_t parity) {
     return tc::all_wait(bars + s, parity, abort_flag, a.status);
   };
+  // a single row's copy warps read its page ids beside its length, not behind it (0.2 us)
+  PageCache pages;
+  if (a.batch == 1)
+    pages.base = (int)((long long)(first / ((a.num_tokens * a.num_q_heads + 127) / 128)) *
+                       a.tiles_per_piece * kKeys / a.page_size);
   pdl_wait();
   pdl_launch_dependents();
+  if (a.batch == 1 && (warp == 3 || warp >= 12))
+    pages.val = pages.base + lane < a.table_stride ? __ldg(a.page_tables + pages.base + lane) : -1;
   const Rows rows = read_rows(a, lane, blockIdx.x == 0 && warp == 0);
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.ws_tiles) *a.ws_tiles = rows.q;  // for the merge
   Piece pc;
@@ -598,9 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == 3 || warp == 12 || warp == 13) {
     const int which = warp == 3 ? 0 : warp - 11;
     if (which < L::kRingK)
-      Loader<DC, kLo, false>(a, &maps.k, sm, bars, abort_flag, rank, lead, which).run_all(rows, first, step);
+      Loader<DC, kLo, false>(a, &maps.k, sm, bars, abort_flag, rank, lead, which, pages).run_all(rows, first, step);
   } else if (warp >= 14) {
-    Loader<DC, kLo, true>(a, &maps.v, sm, bars, abort_flag, rank, lead, warp - 14).run_all(rows, first, step);
+    Loader<DC, kLo, true>(a, &maps.v, sm, bars, abort_flag, rank, lead, warp - 14, pages).run_all(rows, first, step);
   } else if (warp >= 4 && warp <= 11) {
     // ---- the softmax: thread (row i, keys 64 kh + 32 gr .. + 31 of the tile).  The loops never
     // leave early (the four warps of a row's threads meet every tile); after a failed wait
