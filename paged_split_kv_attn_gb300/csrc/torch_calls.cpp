@@ -125,17 +125,17 @@ bool output(PyObject *given, long long code, const at::Tensor &like, int dev, Sh
   return true;
 }
 
-// None where the arguments are not plain; an exception of the tensor library's own becomes Python's.
+// None where the arguments are not plain, or where the tensor library throws (out of memory, no
+// device: the Python form then raises what belongs there).
 template <typename F>
 PyObject *guarded(F f) {
   try {
     PyObject *r = f();
     if (r || PyErr_Occurred()) return r;
-    Py_RETURN_NONE;
-  } catch (const std::exception &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
+  } catch (...) {
+    PyErr_Clear();
   }
+  Py_RETURN_NONE;
 }
 
 PyObject *result(int rc, PyObject *kept, const at::Tensor &out) {
