@@ -14,8 +14,9 @@
 // rotated key each); the queries take a warp for sixteen heads (8 lanes of 16 bytes
 // a head, four heads at a time, all loaded before the chain of page and angle loads is
 // waited for: with four heads a warp a chunk of 8,168 tokens under 32 heads took 30.5 us,
-// bound by that chain), so a pair (i, i + 32) lies in two lanes, four apart, and a pair
-// (2i, 2i + 1) inside one lane.
+// bound by that chain; with 72 registers a thread and blocks of eight warps 18.5, with 64
+// and four 15.7, 6.2 TB/s, or 20.9 from memory), so a pair (i, i + 32) lies in two lanes,
+// four apart, and a pair (2i, 2i + 1) inside one lane.
 #include "latent.h"
 #include "pskv_internal.cuh"
 
@@ -23,7 +24,8 @@ namespace pskv {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kBlocksPerSm = 8;  // 64 registers a thread, 32 warps an SM
 constexpr int kRot = PSKV_LATENT_ROT;
 constexpr int kHeadSteps = 4;                  // four heads at a time
 constexpr int kHeadsPerWarp = 4 * kHeadSteps;
@@ -84,7 +86,7 @@ __device__ __forceinline__ uint4 turn(const uint4 x, const Angles &g, bool adjac
 }  // namespace
 
 template <int DC>
-__global__ void __launch_bounds__(kWarps * 32) pskv_latent_prep(const LatentPrepArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) pskv_latent_prep(const LatentPrepArgs a) {
   constexpr int kPieces = DC / 256;  // 16-byte pieces of the latent per lane
   const int lane = threadIdx.x & 31, piece = lane & 7;
   const int slots = 1 + (a.num_q_heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
