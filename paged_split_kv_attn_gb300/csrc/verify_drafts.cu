@@ -19,6 +19,9 @@
 // vocabulary and writes its sum into every CTA's shared memory (distributed shared
 // memory); after one cluster barrier every warp knows all 64 sums and with them
 // the piece that holds the drawn token, whose CTA goes over it once more (from L2).
+// A CTA's shared memory may be written only once the CTA has started: all arrive on the
+// cluster's barrier as they start and wait for it before the first remote store, behind the
+// sums' loads.
 // No workspace, no second launch, no atomics but fault bits.
 //
 // Measured: 64 rows of 131,072 f32 (67 MB of p and q) 18.1 us with the rows in L2, 22.9 from
@@ -211,9 +214,14 @@ __device__ __forceinline__ void store_remote(uint64_t *p, uint32_t rank, u128 x)
       "r"(rank), "l"((uint64_t)x), "l"((uint64_t)(x >> 64))
       : "memory");
 }
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+__device__ __forceinline__ void cluster_arrive_started() {  // nothing written yet: no release
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace
@@ -225,6 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32) pskv_verify_drafts(const VerifyAr
   const int b = blockIdx.x / kCluster, rank = (int)rank_in_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T_ = a.max_drafts, V = a.vocab;
+  cluster_arrive_started();
   pdl_wait();
   pdl_launch_dependents();
   // ---- which drafts stand (every warp for itself)
@@ -274,8 +283,14 @@ __global__ void __launch_bounds__(kWarps * 32) pskv_verify_drafts(const VerifyAr
     const int lo = (int)min((long long)W * seg, (long long)V);
     const int hi = (int)min((long long)(W + 1) * seg, (long long)V);
     const u128 own = sum_range<T, kVec>(w, lo, hi, lane);
+    if (tries == 0) {
+      __syncwarp();
+      cluster_wait();  // and so have the others
+    }
     if (lane < kCluster) store_remote(piece_sum[tries][W], lane, own);
-    cluster_barrier();
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
     const uint64_t(*ps)[2] = piece_sum[tries];
     constexpr int kEach = kPieces / 32;  // pieces a lane looks at
     u128 part[kEach], four = 0;
