@@ -335,6 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   auto wait = [&](int s, uint32_t parity) {
     return tc::all_wait(bars + s, parity, abort_flag, a.status);
   };
+  auto wait_pair = [&](int s, uint32_t parity) {  // for what the other CTA's threads and copies bring
+    return tc2::all_wait(bars + s, parity, abort_flag, a.status);
+  };
   // The numbers of this CTA's block number i; false: a wait failed.
   Work *works = reinterpret_cast<Work *>(sm + kOffWork);
   auto next = [&](int i, Work &w) {
@@ -359,10 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         ok = next(i, w);
         if (!ok || !w.more) break;
         if (rank != 0 || w.n == 0) continue;
-        ok = wait(kQFull, nb++ & 1);
+        ok = wait_pair(kQFull, nb++ & 1);
         for (int j = 0; ok && j < w.n; ++j, ++g) {
           const int st = g % kRing, r = g & 1;
-          ok = wait(kFullK + st, (g / kRing) & 1) && (g < 2 || wait(kSFree + r, (g / 2 - 1) & 1));
+          ok = wait_pair(kFullK + st, (g / kRing) & 1) && (g < 2 || wait_pair(kSFree + r, (g / 2 - 1) & 1));
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t kt = k + st * kKBytes;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (rank != 0) continue;
         for (int j = 0; ok && j < w.n; ++j, ++g) {
           const int st = g % kRing, pb = g % kPBufs;
-          ok = wait(kFullV + st, (g / kRing) & 1) && wait(kPFull + pb, (g / kPBufs) & 1);
+          ok = wait_pair(kFullV + st, (g / kRing) & 1) && wait_pair(kPFull + pb, (g / kPBufs) & 1);
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t vt = v + st * kVBytes;
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (lead) mbar_arrive(bars + kWorkFull + (i & 1));
         if (!w.more) break;
         if (rank == 0) {
-          ok = i == 0 || wait(kReplyRead, (i - 1) & 1);
+          ok = i == 0 || wait_pair(kReplyRead, (i - 1) & 1);
           if (!ok) break;
           ask_for_cluster(reply, smem_u32(bars + kReply), lead);
         }
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         x = cluster_given(reply);
         __syncwarp();
         tc::fence_smem_for_async();  // read before the next answer lands
-        tc2::arrive_pair(tc2::map_to(smem_u32(bars + kReplyRead), 0), lead);
+        tc2::arrive_pair_release(tc2::map_to(smem_u32(bars + kReplyRead), 0), lead);
       }
       // every copy of both CTAs landed before they leave (their count is the even CTA's)
       if (asked) mbar_wait(bars + kReply, i & 1);
@@ -514,7 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (rank == 0 && lead) mbar_arrive(bars + kFullV + st);  // in place of the copies' count
           }
-          tc2::arrive_pair(full, lead);
+          if (whole)
+            tc2::arrive_pair(full, lead);
+          else
+            tc2::arrive_pair_release(full, lead);
         }
       }
       __syncwarp();

@@ -423,7 +423,10 @@ struct Loader {
       __syncwarp();
     }
     if (!plain && lead && rank == 0) mbar_arrive(own_full);  // in place of the copies' count
-    tc2::arrive_pair(full, lead);
+    if (plain || dead)
+      tc2::arrive_pair(full, lead);
+    else
+      tc2::arrive_pair_release(full, lead);
     __syncwarp();
   }
 
@@ -513,6 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   auto wait = [&](int s, uint32_t parity) {
     return tc::all_wait(bars + s, parity, abort_flag, a.status);
   };
+  auto wait_pair = [&](int s, uint32_t parity) {  // for what the other CTA's threads and copies bring
+    return tc2::all_wait(bars + s, parity, abort_flag, a.status);
+  };
   // a single row's copy warps read its page ids beside its length, not behind it (0.2 us)
   PageCache pages;
   if (a.batch == 1)
@@ -533,15 +539,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t q0 = smem_u32(sm + L::kOffQ), k0 = smem_u32(sm + L::kOffK);
     for (int u = first; ok && find_piece(a, u, rows, lane, pc); u += step) {
       if (pc.n == 0) continue;
-      ok = wait(L::kQFull, k & 1);
+      ok = wait_pair(L::kQFull, k & 1);
       ++k;
       for (int j = 0; ok && j < pc.n; ++j, ++g) {
         const int r = g & 1;
-        if (g >= 2) ok = wait(L::kSFree + r, (g / 2 - 1) & 1);
+        if (g >= 2) ok = wait_pair(L::kSFree + r, (g / 2 - 1) & 1);
 #pragma unroll 1
         for (int c = 0; ok && c < L::kChunks; ++c, ++seq) {
           const int st = seq % L::kRingK;
-          ok = wait(L::kFullK + st, (seq / L::kRingK) & 1);
+          ok = wait_pair(L::kFullK + st, (seq / L::kRingK) & 1);
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t kc = k0 + st * L::kKBytes, qc = q0 + c * L::kKBytes;
@@ -567,11 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int u = first; ok && find_piece(a, u, rows, lane, pc); u += step)
       for (int j = 0; ok && j < pc.n; ++j, ++g) {
         const bool both = pc.len - (pc.t0 + j) * kKeys > kHalf;  // keys in the second half
-        ok = wait(L::kPFull, g & 1);
+        ok = wait_pair(L::kPFull, g & 1);
 #pragma unroll 1
         for (int h = 0; ok && h < 2; ++h) {
           const int sq = 2 * g + h, st = sq % L::kRingV;
-          ok = wait(L::kFullV + st, (sq / L::kRingV) & 1);
+          ok = wait_pair(L::kFullV + st, (sq / L::kRingV) & 1);
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t vc = v0 + st * L::kVBytes;
@@ -730,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc::fence_smem_for_async();
         tc::fence_before_sync();
         __syncwarp();
-        tc2::arrive_pair(p_full, lead);
+        tc2::arrive_pair_release(p_full, lead);
         // S(j + 2) may take the region: not earlier, as the tensor pipe takes products in order
         // and scores that are not needed yet would hold up this tile's values
         tc2::arrive_pair(s_free + 8 * r, lead);
