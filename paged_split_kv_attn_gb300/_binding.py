@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the computation runs in the
 library's CUDA kernels.  PyTorch supplies device memory and the current
 stream; nothing here computes attention, and there is no CPU path: if the
-library is missing the calls raise.
+library is missing the calls raise.  ``stream`` is a torch stream or a stream's
+address (None: the current one); outputs and scratch that a call allocates
+belong to that stream.
 """
 from __future__ import annotations
 
@@ -224,6 +226,20 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """New device memory for a call on ``stream`` (None: the current one).  It belongs to that
+    stream: memory of the current one could still be in use by earlier work there when the call
+    writes it, or, freed with the call's last reference, be given out again before the call has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)  # (0 and 1 name the default stream)
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else \
+            torch.cuda.ExternalStream(handle, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _event(ev):
     if ev is None:
         return None
@@ -363,7 +379,7 @@ def kv_prep_append(layout: Layout, x, q_col: int, k_col: int, v_col: int, num_q_
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be [n, stride] with unit column stride")
     if q_out is None:
-        q_out = torch.empty((n, num_q_heads, d), dtype=torch.bfloat16, device=x.device)
+        q_out = _empty((n, num_q_heads, d), torch.bfloat16, x.device, stream)
     hr = hp = hl = None
     if host is not None:
         hr, hp, hl = (_host_i32(v, name) for v, name in zip(host, ("row_of", "pos_of", "pages")))
@@ -422,8 +438,8 @@ def decode_attn_multirow_workspace_bytes(layout: Layout, seq_lens_host, table_st
     return int(out.value)
 
 
-def _planned_workspace(nbytes: int, device):
-    return None if nbytes == 0 else torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _planned_workspace(nbytes: int, device, stream=None):
+    return None if nbytes == 0 else _empty(nbytes, torch.uint8, device, stream)
 
 
 def pskv_partial_scratch_bytes(batch: int, num_q_heads: int, head_dim_v: int, num_splits: int):
@@ -461,10 +477,10 @@ def _decode(windowed: bool, layout: Layout, q, page_tables, seq_lens, seq_lens_h
         raise ValueError("q must be [batch, num_q_heads, head_dim]")
     batch, hq = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty((batch, hq, layout.desc.head_dim_v), device=q.device,
-                          dtype=out_dtype or torch.bfloat16)
+        out = _empty((batch, hq, layout.desc.head_dim_v), out_dtype or torch.bfloat16, q.device, stream)
     if workspace_t is None:
-        workspace_t = workspace(batch, hq, layout.desc.head_dim_v, num_splits, q.device)
+        workspace_t = _empty(decode_attn_workspace_bytes(batch, hq, layout.desc.head_dim_v, num_splits),
+                             torch.uint8, q.device, stream)
     lens_h = _host_i32(seq_lens_host, "seq_lens_host")
     if len(lens_h) != batch:
         raise ValueError("seq_lens_host must have one entry per row")
@@ -517,14 +533,13 @@ def decode_attn_multirow(layout: Layout, q, page_tables, seq_lens, seq_lens_host
     batch, tokens, hq = q.shape[0], q.shape[1], q.shape[2]
     dv = layout.desc.head_dim_v
     if out is None:
-        out = torch.empty((batch, tokens, hq, dv), device=q.device,
-                          dtype=out_dtype or torch.bfloat16)
+        out = _empty((batch, tokens, hq, dv), out_dtype or torch.bfloat16, q.device, stream)
     lens_h = _host_i32(seq_lens_host, "seq_lens_host")
     if len(lens_h) != batch:
         raise ValueError("seq_lens_host must have one entry per row")
     if workspace is None:
         workspace = _planned_workspace(decode_attn_multirow_workspace_bytes(
-            layout, lens_h, page_tables.shape[1], tokens, hq, False, num_splits), q.device)
+            layout, lens_h, page_tables.shape[1], tokens, hq, False, num_splits), q.device, stream)
     opts = _opts(merge_group, events)
     _check(lib.decode_attn_multirow(
         layout.handle, _dev(q, "q", layout.dtype), _dev(page_tables, "page_tables", torch.int32),
@@ -555,14 +570,13 @@ def decode_attn_tree(layout: Layout, q, page_tables, seq_lens, seq_lens_host, tr
         raise TypeError("tree_mask must hold 64-bit integers (int64 or uint64 bit patterns)")
     dv = layout.desc.head_dim_v
     if out is None:
-        out = torch.empty((batch, tokens, hq, dv), device=q.device,
-                          dtype=out_dtype or torch.bfloat16)
+        out = _empty((batch, tokens, hq, dv), out_dtype or torch.bfloat16, q.device, stream)
     lens_h = _host_i32(seq_lens_host, "seq_lens_host")
     if len(lens_h) != batch:
         raise ValueError("seq_lens_host must have one entry per row")
     if workspace is None:
         workspace = _planned_workspace(decode_attn_multirow_workspace_bytes(
-            layout, lens_h, page_tables.shape[1], tokens, hq, True, num_splits), q.device)
+            layout, lens_h, page_tables.shape[1], tokens, hq, True, num_splits), q.device, stream)
     opts = _opts(merge_group, events)
     _check(lib.decode_attn_tree(
         layout.handle, _dev(q, "q", layout.dtype), _dev(page_tables, "page_tables", torch.int32),
@@ -590,7 +604,7 @@ def prefill_attn_paged(layout: Layout, q, cu_q, cu_q_host, page_tables, seq_lens
     total, hq = q.shape[0], q.shape[1]
     dv = layout.desc.head_dim_v
     if out is None:
-        out = torch.empty((total, hq, dv), device=q.device, dtype=out_dtype or torch.bfloat16)
+        out = _empty((total, hq, dv), out_dtype or torch.bfloat16, q.device, stream)
     cu_h = _host_i32(cu_q_host, "cu_q_host")
     lens_h = _host_i32(seq_lens_host, "seq_lens_host")
     batch = len(lens_h)
@@ -598,7 +612,7 @@ def prefill_attn_paged(layout: Layout, q, cu_q, cu_q_host, page_tables, seq_lens
         raise ValueError("cu_q_host must have batch + 1 entries")
     if workspace is None and num_splits != 1:
         workspace = _planned_workspace(prefill_attn_workspace_bytes(
-            layout, cu_h, lens_h, page_tables.shape[1], hq, window, num_splits), q.device)
+            layout, cu_h, lens_h, page_tables.shape[1], hq, window, num_splits), q.device, stream)
     opts = _opts(merge_group, events)
     _check(lib.prefill_attn_paged(
         layout.handle, _dev(q, "q", layout.dtype), cu_h, _dev(cu_q, "cu_q", torch.int32),
@@ -672,12 +686,12 @@ _PAIRS = {"halves": 0, "adjacent": 1}
 _OUT_CODES = {torch.bfloat16: PSKV_DTYPE_BF16, torch.float32: PSKV_DTYPE_F32}
 
 
-def _out_like(out, shape, like, out_dtype, dev: int):
+def _out_like(out, shape, like, out_dtype, dev: int, stream):
     """The output tensor (made if not given), its address and its dtype's code."""
     if out is None:
         kind = torch.bfloat16 if out_dtype is None else out_dtype
         code = _OUT_CODES.get(kind) if kind in _OUT_CODES else _dtype_code(kind)
-        out = torch.empty(shape, dtype=kind, device=like.device)
+        out = _empty(shape, kind, like.device, stream)
         return out, out.data_ptr(), code
     kind = out.dtype
     code = _OUT_CODES.get(kind) if kind in _OUT_CODES else _dtype_code(kind)
@@ -788,11 +802,11 @@ def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, 
     if len(lens_h) != batch:
         raise ValueError("seq_lens_host must have one entry per row")
     qp = _ptr(q, "q", (batch, tokens, hq, desc.head_dim_k), torch.bfloat16, dev)
-    out, op, code = _out_like(out, (batch, tokens, hq, desc.head_dim_v), q, out_dtype, dev)
+    out, op, code = _out_like(out, (batch, tokens, hq, desc.head_dim_v), q, out_dtype, dev, stream)
     stride = page_tables.shape[1]
     if workspace is None:
         workspace = _planned_workspace(decode_attn_latent_workspace_bytes(
-            layout, lens_h, stride, tokens, hq, num_splits), q.device)
+            layout, lens_h, stride, tokens, hq, num_splits), q.device, stream)
     if workspace is None:
         wp, size = None, 0
     else:
@@ -828,7 +842,7 @@ def prefill_attn_expanded(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale,
         raise ValueError("cu_q_host and cu_k_host must have batch + 1 entries each")
     total_q, total_k, ends = cq[batch], ck[batch], (batch + 1,)
     qp = _ptr(q, "q", (total_q, heads, PSKV_EXPANDED_NOPE + PSKV_LATENT_ROT), bf16, dev)
-    out, op, code = _out_like(out, (total_q, heads, PSKV_EXPANDED_V), q, out_dtype, dev)
+    out, op, code = _out_like(out, (total_q, heads, PSKV_EXPANDED_V), q, out_dtype, dev, stream)
     _check(lib.prefill_attn_expanded(
         qp, _ptr(kv, "kv", (total_k, heads, PSKV_EXPANDED_NOPE + PSKV_EXPANDED_V), bf16, dev),
         _rows(k_rot, "k_rot", (total_k, PSKV_LATENT_ROT), dev),
@@ -859,12 +873,12 @@ def verify_drafts(target_probs, draft_probs, drafts, u, num_drafts=None, tokens=
     kind, t = target_probs.dtype, t1 - 1
     tp = _ptr(target_probs, "target_probs", (batch, t1, vocab), kind, dev)
     if tokens is None:
-        tokens = torch.empty((batch, t1), dtype=i32, device=target_probs.device)
+        tokens = _empty((batch, t1), i32, target_probs.device, stream)
         kp = tokens.data_ptr()
     else:
         kp = _ptr(tokens, "tokens", (batch, t1), i32, dev)
     if accepted is None:
-        accepted = torch.empty((batch,), dtype=i32, device=target_probs.device)
+        accepted = _empty((batch,), i32, target_probs.device, stream)
         ap = accepted.data_ptr()
     else:
         ap = _ptr(accepted, "accepted", (batch,), i32, dev)
@@ -888,8 +902,7 @@ def decode_attn_splitkv_static(layout: Layout, q, page_tables, seq_lens, seq_len
         raise ValueError("q must be [batch, num_q_heads, head_dim]")
     batch, hq = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty((batch, hq, layout.desc.head_dim_v), device=q.device,
-                          dtype=out_dtype or torch.bfloat16)
+        out = _empty((batch, hq, layout.desc.head_dim_v), out_dtype or torch.bfloat16, q.device, stream)
     lens_h = _host_i32(seq_lens_host, "seq_lens_host")
     if len(lens_h) != batch:
         raise ValueError("seq_lens_host must have one entry per row")
@@ -907,7 +920,7 @@ def merge_partials(m, l, o, out=None, out_dtype=None, workspace=None, status=Non
     lib = load_library()
     rows, p, dv = o.shape
     if out is None:
-        out = torch.empty((rows, dv), device=o.device, dtype=out_dtype or torch.float32)
+        out = _empty((rows, dv), out_dtype or torch.float32, o.device, stream)
     opts = _opts(merge_group, events)
     _check(lib.merge_partials(_dev(m, "m", torch.float32), _dev(l, "l", torch.float32),
                               _dev(o, "o", torch.float32), rows, p, dv, _dev(out, "out"),

@@ -12,6 +12,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -108,9 +109,22 @@ bool stream_of(PyObject *o, int dev, pskv_stream_t *s) {
   return false;
 }
 
+// New memory on the tensor's device; it belongs to the stream of the call (`given`: its argument).
+at::Tensor fresh(const at::Tensor &like, at::ScalarType kind, Shape shape, PyObject *given, pskv_stream_t s, int dev) {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (given != Py_None) {
+    // (0 and 1 name the default stream)
+    cudaStream_t raw = reinterpret_cast<cudaStream_t>(s);
+    guard.reset_stream(reinterpret_cast<uintptr_t>(raw) <= 1
+                           ? c10::cuda::getDefaultCUDAStream((c10::DeviceIndex)dev)
+                           : c10::cuda::getStreamFromExternal(raw, (c10::DeviceIndex)dev));
+  }
+  return at::empty(shape, like.options().dtype(kind));
+}
+
 // The output: the given tensor, or a new one of `code`'s type (-1: the caller's to refuse).
-bool output(PyObject *given, long long code, const at::Tensor &like, int dev, Shape shape, at::Tensor *out,
-            int32_t *dtype) {
+bool output(PyObject *given, long long code, const at::Tensor &like, int dev, Shape shape, PyObject *stream,
+            pskv_stream_t s, at::Tensor *out, int32_t *dtype) {
   if (given != Py_None) {
     const at::Tensor *t = tensor(given);
     if (!t || !(on(*t, kBf16, dev, shape) || on(*t, at::kFloat, dev, shape)) || !t->is_contiguous())
@@ -121,7 +135,7 @@ bool output(PyObject *given, long long code, const at::Tensor &like, int dev, Sh
   }
   if (code != PSKV_DTYPE_BF16 && code != PSKV_DTYPE_F32) return false;
   *dtype = (int32_t)code;
-  *out = at::empty(shape, like.options().dtype(code == PSKV_DTYPE_BF16 ? kBf16 : at::kFloat));
+  *out = fresh(like, code == PSKV_DTYPE_BF16 ? kBf16 : at::kFloat, shape, stream, s, dev);
   return true;
 }
 
@@ -196,7 +210,7 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     NEED(stream_of(a[13], dev, &s));
     at::Tensor out;
     int32_t dtype;
-    NEED(output(a[11], code, *q, dev, {batch, tokens, heads, pool.dv}, &out, &dtype));
+    NEED(output(a[11], code, *q, dev, {batch, tokens, heads, pool.dv}, a[13], s, &out, &dtype));
     void *op = out.data_ptr();
     int rc;
     Py_BEGIN_ALLOW_THREADS
@@ -296,7 +310,7 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
     NEED(stream_of(a[11], dev, &s));
     at::Tensor out;
     int32_t dtype;
-    NEED(output(a[8], code, *q, dev, {tq, heads, PSKV_EXPANDED_V}, &out, &dtype));
+    NEED(output(a[8], code, *q, dev, {tq, heads, PSKV_EXPANDED_V}, a[11], s, &out, &dtype));
     void *op = out.data_ptr(), *rp = rot->data_ptr();
     const int64_t r_token = tk > 1 ? rot->stride(0) : PSKV_LATENT_ROT;
     int rc;
@@ -331,13 +345,13 @@ PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
     NEED(stream_of(a[8], dev, &s));
     at::Tensor tokens, accepted;
     if (a[5] == Py_None) {
-      tokens = at::empty({batch, t1}, target->options().dtype(kI32));
+      tokens = fresh(*target, kI32, {batch, t1}, a[8], s, dev);
       kp = tokens.data_ptr();
     } else {
       NEED(whole(a[5], kI32, dev, {batch, t1}, &kp));
     }
     if (a[6] == Py_None) {
-      accepted = at::empty({batch}, target->options().dtype(kI32));
+      accepted = fresh(*target, kI32, {batch}, a[8], s, dev);
       ap = accepted.data_ptr();
     } else {
       NEED(whole(a[6], kI32, dev, {batch}, &ap));
