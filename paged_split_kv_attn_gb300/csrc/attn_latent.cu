@@ -411,7 +411,10 @@ struct Loader {
     if (!plain && !dead) {
       // rows behind the end or of skipped groups may hold anything and meet P = 0: zero them
       __syncwarp();
-      mbar_wait(rag, ragged & 1);  // (bounded; landed or given up on, the chunk is passed on)
+      if (!mbar_wait(rag, ragged & 1)) {  // (given up on, the chunk is passed on all the same)
+        *abort_flag = 1;
+        raise_fault(a.status, PSKV_FAULT_WAIT_TIMEOUT);
+      }
       ++ragged;
       for (int e = lane; e < kHalf * 16 * L::kBlocks; e += 32) {
         const int row = e & (kHalf - 1), piece = e >> 6;
@@ -638,10 +641,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int col0 = pc.cb * 128 + (int)rank * kRows, col = col0 + i;
       const size_t row0 = (size_t)pc.b * cols + col0;
       if (pc.n == 0) {  // a row without keys (of one piece): zeros
-        if (col >= cols) continue;
         const int es = a.out_dtype == PSKV_DTYPE_BF16 ? 2 : 4;
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + (row0 + i) * DC * es);
-        for (int e = 2 * gr + kh; e < DC * es / 16; e += 4) dst[e] = make_uint4(0, 0, 0, 0);
+        if (col < cols)
+          for (int e = 2 * gr + kh; e < DC * es / 16; e += 4) dst[e] = make_uint4(0, 0, 0, 0);
+        __syncwarp();  // (the next piece's tensor-memory loads want the warp together)
         continue;
       }
       // keys below lim are seen (columns behind the last, whose results go nowhere, see all: a
