@@ -205,6 +205,21 @@ def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
     return t.data_ptr()
 
 
+def _int32(x, name: str):
+    """A number that has to fit 32 bits (ctypes would keep its low ones)."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
+def _i32_array(x: list, name: str):
+    """A list of whole numbers as a ctypes array; each has to fit 32 bits."""
+    if x:
+        _int32(min(x), name)
+        _int32(max(x), name)
+    return (ctypes.c_int32 * len(x))(*x)
+
+
 def _host_i32(x, name: str):
     """Host int32 array (list, numpy array or CPU tensor) -> ctypes array kept alive by the caller."""
     if x is None or (isinstance(x, ctypes.Array) and x._type_ is ctypes.c_int32):
@@ -212,10 +227,10 @@ def _host_i32(x, name: str):
     if isinstance(x, torch.Tensor):
         if x.is_cuda:
             raise TypeError(f"{name} must be host memory")
-        x = x.to(torch.int32).tolist()
+        x = x.tolist()
     elif hasattr(x, "tolist"):
         x = x.tolist()
-    return (ctypes.c_int32 * len(x))(*[int(v) for v in x])
+    return _i32_array([int(v) for v in x], name)
 
 
 def _stream(stream) -> int:
@@ -261,7 +276,7 @@ def _opts(merge_group: int = 0, events=None, append=None, dtype=None):
         k_new, v_new, pages = append
         ak, av = _dev(k_new, "k_new", dtype), _dev(v_new, "v_new", dtype)
         ap = _dev(pages, "pages_of_row", torch.int32)
-    return DecodeOpts(merge_group, _event(begin), _event(end), ak, av, ap)
+    return DecodeOpts(_int32(merge_group, "merge_group"), _event(begin), _event(end), ak, av, ap)
 
 
 # ---- layout ------------------------------------------------------------------
@@ -401,8 +416,8 @@ def kv_prep_append(layout: Layout, x, q_col: int, k_col: int, v_col: int, num_q_
 def decode_attn_workspace_bytes(batch: int, num_q_heads: int, head_dim_v: int,
                                 num_splits: int = 0) -> int:
     out = ctypes.c_size_t()
-    _check(load_library().decode_attn_workspace_bytes(batch, num_q_heads, head_dim_v, num_splits,
-                                                      ctypes.byref(out)),
+    _check(load_library().decode_attn_workspace_bytes(batch, num_q_heads, head_dim_v,
+                                                      _int32(num_splits, "num_splits"), ctypes.byref(out)),
            "decode_attn_workspace_bytes")
     return int(out.value)
 
@@ -421,8 +436,8 @@ def prefill_attn_workspace_bytes(layout: Layout, cu_q_host, seq_lens_host, table
     cu_h, lens_h = _host_i32(cu_q_host, "cu_q_host"), _host_i32(seq_lens_host, "seq_lens_host")
     out = ctypes.c_size_t()
     _check(load_library().prefill_attn_workspace_bytes(
-        layout.handle, cu_h, lens_h, table_stride, len(lens_h), num_q_heads, int(window),
-        num_splits, ctypes.byref(out)), "prefill_attn_workspace_bytes")
+        layout.handle, cu_h, lens_h, _int32(table_stride, "table_stride"), len(lens_h), num_q_heads,
+        _int32(int(window), "window"), _int32(num_splits, "num_splits"), ctypes.byref(out)), "prefill_attn_workspace_bytes")
     return int(out.value)
 
 
@@ -433,8 +448,8 @@ def decode_attn_multirow_workspace_bytes(layout: Layout, seq_lens_host, table_st
     lens_h = _host_i32(seq_lens_host, "seq_lens_host")
     out = ctypes.c_size_t()
     _check(load_library().decode_attn_multirow_workspace_bytes(
-        layout.handle, lens_h, table_stride, len(lens_h), num_tokens, num_q_heads, int(tree),
-        num_splits, ctypes.byref(out)), "decode_attn_multirow_workspace_bytes")
+        layout.handle, lens_h, _int32(table_stride, "table_stride"), len(lens_h), num_tokens, num_q_heads,
+        int(tree), _int32(num_splits, "num_splits"), ctypes.byref(out)), "decode_attn_multirow_workspace_bytes")
     return int(out.value)
 
 
@@ -487,7 +502,7 @@ def _decode(windowed: bool, layout: Layout, q, page_tables, seq_lens, seq_lens_h
     opts = _opts(merge_group, events, append, layout.dtype)
     common = (_dev(q, "q", layout.dtype), _dev(page_tables, "page_tables", torch.int32),
               page_tables.shape[1], lens_h, _dev(seq_lens, "seq_lens", torch.int32))
-    tail = (batch, hq, float(scale), num_splits, _dev(workspace_t, "workspace"),
+    tail = (batch, hq, float(scale), _int32(num_splits, "num_splits"), _dev(workspace_t, "workspace"),
             workspace_t.numel() * workspace_t.element_size(), _dev(out, "out"),
             _dtype_code(out.dtype), None if opts is None else ctypes.byref(opts), _stream(stream))
     if windowed:
@@ -544,7 +559,7 @@ def decode_attn_multirow(layout: Layout, q, page_tables, seq_lens, seq_lens_host
     _check(lib.decode_attn_multirow(
         layout.handle, _dev(q, "q", layout.dtype), _dev(page_tables, "page_tables", torch.int32),
         page_tables.shape[1], lens_h, _dev(seq_lens, "seq_lens", torch.int32), batch, tokens, hq,
-        float(scale), num_splits, None if workspace is None else _dev(workspace, "workspace"),
+        float(scale), _int32(num_splits, "num_splits"), None if workspace is None else _dev(workspace, "workspace"),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _dev(out, "out"), _dtype_code(out.dtype), None if opts is None else ctypes.byref(opts),
         _stream(stream)), "decode_attn_multirow")
@@ -581,7 +596,7 @@ def decode_attn_tree(layout: Layout, q, page_tables, seq_lens, seq_lens_host, tr
     _check(lib.decode_attn_tree(
         layout.handle, _dev(q, "q", layout.dtype), _dev(page_tables, "page_tables", torch.int32),
         page_tables.shape[1], lens_h, _dev(seq_lens, "seq_lens", torch.int32),
-        _dev(tree_mask, "tree_mask"), batch, tokens, hq, float(scale), num_splits,
+        _dev(tree_mask, "tree_mask"), batch, tokens, hq, float(scale), _int32(num_splits, "num_splits"),
         None if workspace is None else _dev(workspace, "workspace"),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _dev(out, "out"), _dtype_code(out.dtype), None if opts is None else ctypes.byref(opts),
@@ -617,8 +632,8 @@ def prefill_attn_paged(layout: Layout, q, cu_q, cu_q_host, page_tables, seq_lens
     _check(lib.prefill_attn_paged(
         layout.handle, _dev(q, "q", layout.dtype), cu_h, _dev(cu_q, "cu_q", torch.int32),
         _dev(page_tables, "page_tables", torch.int32), page_tables.shape[1], lens_h,
-        _dev(seq_lens, "seq_lens", torch.int32), batch, hq, int(window), float(scale),
-        num_splits, None if workspace is None else _dev(workspace, "workspace"),
+        _dev(seq_lens, "seq_lens", torch.int32), batch, hq, _int32(int(window), "window"), float(scale),
+        _int32(num_splits, "num_splits"), None if workspace is None else _dev(workspace, "workspace"),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _dev(out, "out"), _dtype_code(out.dtype), None if opts is None else ctypes.byref(opts),
         _stream(stream)), "prefill_attn_paged")
@@ -672,7 +687,7 @@ def _lens_i32(x, name: str):
     """Host int32 array: a list of whole numbers at once, anything else as _host_i32 takes it."""
     if type(x) is list:
         try:
-            return (ctypes.c_int32 * len(x))(*x)
+            return _i32_array(x, name)
         except TypeError:
             pass
     return _host_i32(x, name)
@@ -763,8 +778,9 @@ def decode_attn_latent_workspace_bytes(layout: Layout, seq_lens_host, table_stri
     lens_h = _lens_i32(seq_lens_host, "seq_lens_host")
     out = ctypes.c_size_t()
     _check(load_library().decode_attn_latent_workspace_bytes(
-        layout.handle, lens_h, table_stride, len(lens_h), num_tokens, num_q_heads, num_splits,
-        ctypes.byref(out)), "decode_attn_latent_workspace_bytes")
+        layout.handle, lens_h, _int32(table_stride, "table_stride"), len(lens_h), _int32(num_tokens, "num_tokens"),
+        _int32(num_q_heads, "num_q_heads"), _int32(num_splits, "num_splits"), ctypes.byref(out)),
+        "decode_attn_latent_workspace_bytes")
     return int(out.value)
 
 
@@ -816,7 +832,7 @@ def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, 
     _check(lib.decode_attn_latent(
         layout._handle, qp, _ptr(page_tables, "page_tables", (batch, stride), torch.int32, dev), stride,
         lens_h, _ptr(seq_lens, "seq_lens", (batch,), torch.int32, dev), batch, tokens, hq, scale,
-        num_splits, wp, size, op, code, None if opts is None else ctypes.byref(opts),
+        _int32(num_splits, "num_splits"), wp, size, op, code, None if opts is None else ctypes.byref(opts),
         _stream_on(stream, dev)), "decode_attn_latent")
     return out
 
@@ -909,7 +925,7 @@ def decode_attn_splitkv_static(layout: Layout, q, page_tables, seq_lens, seq_len
     _check(lib.decode_attn_splitkv_static(
         layout.handle, _dev(q, "q", layout.dtype), _dev(page_tables, "page_tables", torch.int32),
         page_tables.shape[1], lens_h, _dev(seq_lens, "seq_lens", torch.int32), batch, hq,
-        float(scale), num_splits, _dev(out, "out"), _dtype_code(out.dtype), _stream(stream)),
+        float(scale), _int32(num_splits, "num_splits"), _dev(out, "out"), _dtype_code(out.dtype), _stream(stream)),
         "decode_attn_splitkv_static")
     return out
 
