@@ -457,7 +457,8 @@ int kv_prep_append_latent(const pskv_layout *layout, const pskv_latent_prep_desc
  *                outputs are zeros (no fault bit)
  *   num_splits   0: chosen from the host lengths; else pieces of whole 128-key tiles,
  *                this many at most for the longest row (shorter rows have fewer)
- *   workspace    decode_attn_latent_workspace_bytes(...) bytes, 16-byte aligned
+ *   workspace    decode_attn_latent_workspace_bytes(...) bytes of these lengths, or
+ *                decode_attn_latent_workspace_bound(...), 16-byte aligned
  *                (NULL is fine where that is 0); its contents are this call's own (the
  *                pieces are folded in one level: opts->merge_group is only checked)
  * Keys that a token does not attend take no part, whatever their scores; those of the
@@ -477,9 +478,18 @@ int decode_attn_latent(const pskv_layout *layout, const void *q, const int32_t *
                        const pskv_decode_opts *opts, pskv_stream_t stream);
 
 /* The workspace a decode_attn_latent call needs under its plan (0 when one
- * partition writes the output directly).  Nothing is enqueued. */
+ * partition writes the output directly).  It does not grow with the lengths: even rows that
+ * fill the GPU are left whole and need none, one long row between short ones is cut.
+ * Nothing is enqueued. */
 int decode_attn_latent_workspace_bytes(const pskv_layout *layout, const int32_t *seq_lens_host,
                                        int32_t table_stride, int32_t batch, int32_t num_tokens,
+                                       int32_t num_q_heads, int32_t num_splits, size_t *bytes);
+
+/* A workspace that every decode_attn_latent call with this num_splits can use that has up to
+ * max_batch rows, up to max_tokens tokens a row and no length above max_len (what a serving loop
+ * sizes once). */
+int decode_attn_latent_workspace_bound(const pskv_layout *layout, int32_t max_len,
+                                       int32_t max_batch, int32_t max_tokens,
                                        int32_t num_q_heads, int32_t num_splits, size_t *bytes);
 
 /* Expanded latent attention of variable-length chunks: row b's queries are

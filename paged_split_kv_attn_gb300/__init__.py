@@ -7,7 +7,7 @@ entry-point names.  PyTorch provides device memory and streams only.
 from ._binding import *  # noqa: F401,F403
 from ._binding import (EXPORTS, Layout, PskvError, decode_attn_multirow, decode_attn_splitkv,
                        decode_attn_tree, decode_attn_latent, decode_attn_latent_workspace_bytes,
-                       kv_prep_append_latent, latent_workspace, prefill_attn_expanded, verify_drafts,
+                       decode_attn_latent_workspace_bound, kv_prep_append_latent, latent_workspace, prefill_attn_expanded, verify_drafts,
                        decode_attn_splitkv_static, decode_attn_windowed,
                        decode_attn_workspace_bytes, kv_append_rows, kv_prep_append, load_library,
                        merge_partials, merge_partials_workspace_bytes, paged_kv_layout_create,
@@ -19,7 +19,7 @@ from ._binding import (EXPORTS, Layout, PskvError, decode_attn_multirow, decode_
 
 __all__ = ["EXPORTS", "Layout", "PskvError", "decode_attn_multirow", "decode_attn_splitkv",
            "decode_attn_tree", "decode_attn_latent", "decode_attn_latent_workspace_bytes",
-           "kv_prep_append_latent", "latent_workspace", "prefill_attn_expanded", "verify_drafts",
+           "decode_attn_latent_workspace_bound", "kv_prep_append_latent", "latent_workspace", "prefill_attn_expanded", "verify_drafts",
            "decode_attn_splitkv_static", "decode_attn_windowed",
            "decode_attn_workspace_bytes", "kv_append_rows", "kv_prep_append", "load_library",
            "merge_partials",

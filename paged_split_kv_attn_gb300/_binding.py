@@ -58,7 +58,8 @@ PSKV_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 EXPORTS = ("paged_kv_layout_create", "paged_kv_layout_destroy", "kv_append_rows", "kv_prep_append",
            "decode_attn_splitkv", "decode_attn_windowed", "decode_attn_multirow",
            "decode_attn_tree", "prefill_attn_paged", "kv_prep_append_latent", "decode_attn_latent",
-           "decode_attn_latent_workspace_bytes", "prefill_attn_expanded", "verify_drafts",
+           "decode_attn_latent_workspace_bytes", "decode_attn_latent_workspace_bound",
+           "prefill_attn_expanded", "verify_drafts",
            "merge_partials",
            "decode_attn_workspace_bytes", "merge_partials_workspace_bytes",
            "prefill_attn_workspace_bytes", "decode_attn_multirow_workspace_bytes",
@@ -141,6 +142,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                        P]
     lib.decode_attn_latent_workspace_bytes.argtypes = [P, P, I32, I32, I32, I32, I32,
                                                        ctypes.POINTER(SZ)]
+    lib.decode_attn_latent_workspace_bound.argtypes = [P, I32, I32, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.prefill_attn_expanded.argtypes = [P, P, P, I64, P, P, P, P, I32, I32, F, P, I32, P, P]
     lib.verify_drafts.argtypes = [P, P, I32, P, P, P, I32, I32, I32, P, P, P, P]
     lib.merge_partials.argtypes = [P, P, P, I32, I32, I32, P, I32, P, SZ, P, P, P]
@@ -784,10 +786,28 @@ def decode_attn_latent_workspace_bytes(layout: Layout, seq_lens_host, table_stri
     return int(out.value)
 
 
+def decode_attn_latent_workspace_bound(layout: Layout, max_len: int, max_batch: int, max_tokens: int,
+                                       num_q_heads: int, num_splits: int = 0) -> int:
+    """Workspace bytes for every decode_attn_latent call with this ``num_splits`` that has up to so many
+    rows and tokens and no longer row."""
+    out = ctypes.c_size_t()
+    _check(load_library().decode_attn_latent_workspace_bound(
+        layout.handle, _int32(max_len, "max_len"), _int32(max_batch, "max_batch"), _int32(max_tokens, "max_tokens"),
+        _int32(num_q_heads, "num_q_heads"), _int32(num_splits, "num_splits"), ctypes.byref(out)),
+        "decode_attn_latent_workspace_bound")
+    return int(out.value)
+
+
 def latent_workspace(layout: Layout, seq_lens_host, num_tokens: int, num_q_heads: int,
-                     table_stride: int | None = None, num_splits: int = 0):
-    """A scratch tensor for decode_attn_latent calls of these lengths (None: none needed)."""
+                     table_stride: int | None = None, num_splits: int = 0, bound: bool = False):
+    """A scratch tensor for decode_attn_latent calls of these lengths (None: none needed).  Other
+    lengths, shorter ones too, may need more; with ``bound`` it does for every call of up to so many rows and
+    tokens with no row longer than the longest of these."""
     lens_h = _lens_i32(seq_lens_host, "seq_lens_host")
+    if bound:
+        n = decode_attn_latent_workspace_bound(layout, max(1, *lens_h), len(lens_h), num_tokens, num_q_heads,
+                                               num_splits)
+        return _planned_workspace(n, layout.k_pool.device)
     if table_stride is None:
         table_stride = max(1, -(-max(lens_h) // layout.page_size))
     n = decode_attn_latent_workspace_bytes(layout, lens_h, table_stride, num_tokens, num_q_heads,

@@ -371,6 +371,14 @@ int decode_common(const pskv_layout *layout, const void *q, const int32_t *page_
   return PSKV_OK;
 }
 
+// decode_attn_latent's scratch: partials in groups of 32 query columns, and the tiles per piece
+// (256 bytes), for the merge.
+int plan_latent_workspace(int64_t columns, int32_t batch, int head_dim_v, int splits, WorkspacePlan *w) {
+  const int rc = plan_workspace((columns + 31) / 32 * 32 * batch, 1, head_dim_v, splits, 1, w);
+  if (rc == PSKV_OK) w->total += 256;
+  return rc;
+}
+
 // decode_attn_latent's checks, plan and launches; with `plan_bytes` set only
 // the host-visible checks and the plan, as for decode_common.
 int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_tables,
@@ -409,10 +417,7 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   const LatentPlan plan = plan_latent(n_sm / 2, d.head_dim_v, batch, seq_lens_host, (columns + 127) / 128, num_splits);
   const bool direct = plan.splits == 1;
   WorkspacePlan w;
-  // partials in groups of 32 query columns
-  if ((rc = plan_workspace((columns + 31) / 32 * 32 * batch, 1, d.head_dim_v, plan.splits, 1, &w)))
-    return rc;
-  w.total += 256;  // the tiles per piece, for the merge
+  if ((rc = plan_latent_workspace(columns, batch, d.head_dim_v, plan.splits, &w))) return rc;
   if (plan_bytes) {
     *plan_bytes = direct ? 0 : w.total;
     return PSKV_OK;
@@ -785,6 +790,35 @@ int decode_attn_latent_workspace_bytes(const pskv_layout *layout, const int32_t 
                        PSKV_DTYPE_BF16, nullptr, nullptr, bytes);
 }
 
+int decode_attn_latent_workspace_bound(const pskv_layout *layout, int32_t max_len,
+                                       int32_t max_batch, int32_t max_tokens,
+                                       int32_t num_q_heads, int32_t num_splits, size_t *bytes) {
+  if (!layout || !bytes || max_len < 1 || max_batch < 1 || max_batch > 65535 || max_tokens < 1 ||
+      max_tokens > PSKV_MAX_WINDOW_TOKENS || num_q_heads < 1 || num_splits < 0 ||
+      num_splits > PSKV_MAX_SPLITS)
+    return PSKV_ERR_INVALID_ARG;
+  const pskv_layout_desc &d = layout->d;
+  if (d.format != PSKV_FORMAT_LATENT || num_q_heads > PSKV_LATENT_MAX_HEADS)
+    return PSKV_ERR_UNSUPPORTED;
+  int n_sm = 2, rc;
+  if (num_splits == 0 && (rc = sm_count(&n_sm))) return rc;
+  size_t most = 0;
+  for (int64_t t = 1; t <= max_tokens; ++t) {
+    const int64_t columns = t * num_q_heads, blocks = (columns + 127) / 128;
+    for (int32_t b = max_batch; b >= 1; --b) {
+      const int splits = latent_most_splits(n_sm / 2, b, max_len, blocks, num_splits);
+      if (splits > 1) {
+        WorkspacePlan w;
+        if ((rc = plan_latent_workspace(columns, b, d.head_dim_v, splits, &w))) return rc;
+        most = w.total > most ? w.total : most;
+      }
+      if (num_splits > 0) break;  // fewer rows have no more pieces
+    }
+  }
+  *bytes = most;
+  return PSKV_OK;
+}
+
 int prefill_attn_expanded(const void *q, const void *kv, const void *k_rot, int64_t k_rot_token,
                           const int32_t *cu_q_host, const int32_t *cu_q, const int32_t *cu_k_host,
                           const int32_t *cu_k, int32_t batch, int32_t num_heads, float scale,
@@ -980,7 +1014,7 @@ const char *pskv_last_cuda_error(void) { return g_cuda_error; }
 
 uint64_t pskv_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 
-int pskv_version(void) { return 103; }
+int pskv_version(void) { return 104; }
 
 int pskv_check_flags(const pskv_layout *layout, int32_t clear, pskv_stream_t stream,
                      uint32_t *flags) {

@@ -186,4 +186,17 @@ LatentPlan plan_latent(int clusters, int head_dim_v, int32_t batch, const int32_
   return p;
 }
 
+int latent_most_splits(int clusters, int32_t batch, int64_t longest, int64_t blocks, int32_t num_splits) {
+  if (clusters < 1) clusters = 1;
+  const int64_t tiles = (longest + kLatentTile - 1) / kLatentTile;
+  int64_t most = num_splits;
+  if (num_splits == 0) {
+    // four waves of pieces at most, and each other row has one
+    most = 4 * (int64_t)clusters / blocks - (batch - 1);
+    if (most > PSKV_AUTO_MAX_SPLITS) most = PSKV_AUTO_MAX_SPLITS;
+  }
+  if (most > tiles) most = tiles;
+  return most < 1 ? 1 : (int)most;
+}
+
 }  // namespace pskv

@@ -75,6 +75,10 @@ struct LatentPlan {
 };
 LatentPlan plan_latent(int clusters, int head_dim_v, int32_t batch, const int32_t *seq_lens_host, int64_t blocks,
                        int32_t num_splits);
+// No plan of `batch` rows with up to `longest` keys has more pieces of a row than this.  (The pieces do
+// not grow with the lengths: a batch of even rows that fills the pairs is left whole, and one
+// long row between short ones is cut.)
+int latent_most_splits(int clusters, int32_t batch, int64_t longest, int64_t blocks, int32_t num_splits);
 int plan_splits(int slots, int32_t batch, int32_t num_kv_heads, const int32_t *seq_lens_host,
                 int fill32 = 32);
 
