@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -163,25 +164,38 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pskv_kernel_launches.argtypes = []
     lib.pskv_kernel_launches.restype = ctypes.c_uint64
     lib.pskv_version.argtypes = []
-    _bind_calls(lib)
     _LIB = lib
     return lib
 
 
-_calls = None
+class _PythonCalls:
+    """Stands for the compiled calls where there are none: each leaves its call to the Python form."""
+
+    append = decode = prefill = verify = staticmethod(lambda *args: None)
 
 
-def _bind_calls(lib) -> None:
-    """The compiled forms of the latent operators' calls, entering this library."""
+_calls = None  # bound by the first call of a latent operator
+
+
+def _bind_calls(lib):
+    """The compiled forms of the latent operators' calls, entering this library; where they are missing
+    or were built for another Python or PyTorch, the Python forms do their work."""
     global _calls
-    try:
-        from . import _calls as calls
-    except ImportError as e:
-        raise RuntimeError("the compiled calls are missing or do not fit this PyTorch: build them with "
-                           "`python -m paged_split_kv_attn_gb300.build --force`") from e
-    calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-        lib.kv_prep_append_latent, lib.decode_attn_latent, lib.prefill_attn_expanded, lib.verify_drafts)])
+    from . import build
+
+    calls, why = _PythonCalls, "they are missing or were built for another Python or PyTorch"
+    if build.calls_fit():
+        try:
+            from . import _calls as calls
+            calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.kv_prep_append_latent, lib.decode_attn_latent, lib.prefill_attn_expanded, lib.verify_drafts)])
+        except ImportError as e:
+            calls, why = _PythonCalls, str(e)
+    if calls is _PythonCalls:
+        warnings.warn(f"the latent operators run without their compiled calls ({why}), some microseconds slower a "
+                      "call; `python -m paged_split_kv_attn_gb300.build` makes them", RuntimeWarning)
     _calls = calls
+    return calls
 
 
 def _check(rc: int, what: str) -> None:
@@ -727,7 +741,7 @@ def kv_prep_append_latent(layout: Layout, x, row_of, pos_of, page_tables, pages_
     pages_of_row) host copies for the up-front refusal."""
     lib = _LIB or load_library()
     if host is None:
-        rc = _calls.append(*layout._pool, x, row_of, pos_of, page_tables, pages_of_row, eps, w, rope_cos, rope_sin,
+        rc = (_calls or _bind_calls(lib)).append(*layout._pool, x, row_of, pos_of, page_tables, pages_of_row, eps, w, rope_cos, rope_sin,
                            _PAIRS.get(pairs, -1), first_pos, q, q_out, dense,
                            None if stream is None else _stream(stream))
         if rc is not None:
@@ -823,7 +837,7 @@ def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, 
     [batch, tokens, heads, latent]; a row of length 0 gets zeros."""
     lib = _LIB or load_library()
     if not merge_group and events is None:
-        r = _calls.decode(*layout._pool, q, page_tables, seq_lens, seq_lens_host, scale, num_splits, workspace, out,
+        r = (_calls or _bind_calls(lib)).decode(*layout._pool, q, page_tables, seq_lens, seq_lens_host, scale, num_splits, workspace, out,
                           PSKV_DTYPE_BF16 if out_dtype is None else _OUT_CODES.get(out_dtype, -1),
                           None if stream is None else _stream(stream))
         if r is not None:
@@ -864,7 +878,7 @@ def prefill_attn_expanded(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale,
     may be strided); row b's queries are the last of its keys.  Returns ``out``
     [total_q, heads, 128]."""
     lib = _LIB or load_library()
-    r = _calls.prefill(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale, out,
+    r = (_calls or _bind_calls(lib)).prefill(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale, out,
                        PSKV_DTYPE_BF16 if out_dtype is None else _OUT_CODES.get(out_dtype, -1), status,
                        None if stream is None else _stream(stream))
     if r is not None:
@@ -898,7 +912,7 @@ def verify_drafts(target_probs, draft_probs, drafts, u, num_drafts=None, tokens=
     uniform numbers.  Returns (``tokens`` int32 [batch, drafts + 1]: standing
     drafts, the drawn token, -1s; ``accepted`` int32 [batch])."""
     lib = _LIB or load_library()
-    r = _calls.verify(target_probs, draft_probs, drafts, u, num_drafts, tokens, accepted, status,
+    r = (_calls or _bind_calls(lib)).verify(target_probs, draft_probs, drafts, u, num_drafts, tokens, accepted, status,
                       None if stream is None else _stream(stream))
     if r is not None:
         return r if type(r) is not int else _check(r, "verify_drafts")

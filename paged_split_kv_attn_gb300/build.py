@@ -1,6 +1,8 @@
 """Build ``libpskv.so`` in-tree: every CUDA source compiled for sm_103a with nvcc,
 in parallel, then linked into one shared library (static CUDA runtime), and ``_calls.so``, the
-latent operators' Python calls in compiled form.
+latent operators' Python calls in compiled form.  The library needs nvcc alone; the compiled calls need
+PyTorch's and Python's headers and fit one version of both.  Without them the operators' Python forms
+do the same work, some microseconds of host time a call slower.
 
 Usage: ``python -m paged_split_kv_attn_gb300.build [--force] [--verbose-ptxas]``.
 """
@@ -8,9 +10,11 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import platform
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpskv.so")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_TAG = os.path.join(BUILD, "_calls.tag")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
@@ -44,10 +49,32 @@ def _deps() -> list[str]:
 
 
 def _up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    if not os.path.exists(LIB):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    t = os.path.getmtime(LIB)
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def calls_tag() -> str:
+    """What the compiled calls of this interpreter and PyTorch are built for."""
+    import torch
+
+    return (f"{sys.implementation.cache_tag} {platform.machine()} torch {torch.__version__} "
+            f"c++ abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
+def calls_fit() -> bool:
+    """Whether ``_calls.so`` is there and was built for this interpreter and PyTorch."""
+    try:
+        with open(CALLS_TAG) as f:
+            return os.path.exists(CALLS) and f.read() == calls_tag()
+    except OSError:
+        return False
+
+
+def _calls_up_to_date() -> bool:
+    files = [os.path.join(CSRC, "torch_calls.cpp"), os.path.join(INCLUDE, "pskv.h"), os.path.abspath(__file__)]
+    return calls_fit() and all(os.path.getmtime(f) <= os.path.getmtime(CALLS) for f in files)
 
 
 def _compile(src: str, verbose_ptxas: bool, extra: list[str], build_dir: str) -> tuple[str, str]:
@@ -80,7 +107,20 @@ def _build_calls() -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"compiling torch_calls.cpp failed:\n{' '.join(cmd)}\n{res.stdout}{res.stderr}")
+    os.makedirs(BUILD, exist_ok=True)
+    if os.path.exists(CALLS_TAG):
+        os.remove(CALLS_TAG)
     os.replace(tmp, CALLS)
+    with open(CALLS_TAG, "w") as f:
+        f.write(calls_tag())
+
+
+def _try_calls() -> None:
+    """Build the compiled calls; where that is not possible, say so and go on without."""
+    try:
+        _build_calls()
+    except Exception as e:
+        warnings.warn(f"the compiled calls were not built; the Python forms are used instead: {e}", RuntimeWarning)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, defines: dict | None = None,
@@ -92,11 +132,13 @@ def build(force: bool = False, verbose_ptxas: bool = False, defines: dict | None
     always rebuilt."""
     extra = [f"-D{k}={v}" for k, v in (defines or {}).items()]
     if not force and not verbose_ptxas and not extra and out == LIB and _up_to_date():
+        if not _calls_up_to_date():
+            _try_calls()
         return LIB
     build_dir = BUILD if out == LIB else out + ".objs"
     os.makedirs(build_dir, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_build_calls) if out == LIB else None
+        calls = ex.submit(_try_calls) if out == LIB else None
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas, extra, build_dir), SOURCES))
         if calls:
             calls.result()
