@@ -236,6 +236,16 @@ def _i32_array(x: list, name: str):
     return (ctypes.c_int32 * len(x))(*x)
 
 
+def _status(t, dev: int):
+    """The fault word's address (None: none), on the device whose kernels raise bits in it."""
+    if t is None:
+        return None
+    p = _dev(t, "status", torch.int32)
+    if t.get_device() != dev:
+        raise ValueError(f"status is on {t.device}, the call's device is cuda:{dev}")
+    return p
+
+
 def _host_i32(x, name: str):
     """Host int32 array (list, numpy array or CPU tensor) -> ctypes array kept alive by the caller."""
     if x is None or (isinstance(x, ctypes.Array) and x._type_ is ctypes.c_int32):
@@ -354,7 +364,7 @@ def paged_kv_layout_create(k_pool: torch.Tensor, v_pool: torch.Tensor | None,
         desc = LayoutDesc(k_pool.shape[0], k_pool.shape[2], k_pool.shape[1], k_pool.shape[3],
                           k_pool.shape[3] - PSKV_LATENT_ROT, _dtype_code(k_pool.dtype),
                           PSKV_FORMAT_LATENT if fmt is None else fmt, _dev(k_pool, "k_pool"), None,
-                          None if status is None else _dev(status, "status", torch.int32))
+                          _status(status, k_pool.get_device()))
         handle = ctypes.c_void_p()
         _check(lib.paged_kv_layout_create(ctypes.byref(desc), ctypes.byref(handle)),
                "paged_kv_layout_create")
@@ -368,7 +378,7 @@ def paged_kv_layout_create(k_pool: torch.Tensor, v_pool: torch.Tensor | None,
     desc = LayoutDesc(k_pool.shape[0], k_pool.shape[2], k_pool.shape[1], k_pool.shape[3],
                       v_pool.shape[3], _dtype_code(k_pool.dtype), fmt,
                       _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"),
-                      None if status is None else _dev(status, "status", torch.int32))
+                      _status(status, k_pool.get_device()))
     handle = ctypes.c_void_p()
     _check(lib.paged_kv_layout_create(ctypes.byref(desc), ctypes.byref(handle)),
            "paged_kv_layout_create")
@@ -898,8 +908,7 @@ def prefill_attn_expanded(q, kv, k_rot, cu_q, cu_q_host, cu_k, cu_k_host, scale,
         _rows(k_rot, "k_rot", (total_k, PSKV_LATENT_ROT), dev),
         k_rot.stride(0) if total_k > 1 else PSKV_LATENT_ROT, cq, _ptr(cu_q, "cu_q", ends, i32, dev), ck,
         _ptr(cu_k, "cu_k", ends, i32, dev), batch, heads, scale, op, code,
-        None if status is None else _dev(status, "status", i32), _stream_on(stream, dev)),
-        "prefill_attn_expanded")
+        _status(status, dev), _stream_on(stream, dev)), "prefill_attn_expanded")
     return out
 
 
@@ -937,8 +946,7 @@ def verify_drafts(target_probs, draft_probs, drafts, u, num_drafts=None, tokens=
         _dtype_code(kind), _ptr(drafts, "drafts", (batch, t), i32, dev),
         None if num_drafts is None else _ptr(num_drafts, "num_drafts", (batch,), i32, dev),
         _ptr(u, "u", (batch, t1), torch.float32, dev), batch, t, vocab,
-        kp, ap, None if status is None else _dev(status, "status", i32), _stream_on(stream, dev)),
-        "verify_drafts")
+        kp, ap, _status(status, dev), _stream_on(stream, dev)), "verify_drafts")
     return tokens, accepted
 
 
@@ -977,7 +985,7 @@ def merge_partials(m, l, o, out=None, out_dtype=None, workspace=None, status=Non
                               _dtype_code(out.dtype),
                               None if workspace is None else _dev(workspace, "workspace"),
                               0 if workspace is None else workspace.numel() * workspace.element_size(),
-                              None if status is None else _dev(status, "status", torch.int32),
+                              _status(status, o.get_device()),
                               None if opts is None else ctypes.byref(opts), _stream(stream)),
            "merge_partials")
     return out

@@ -304,7 +304,7 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
     NEED(number(a[7], &scale) && integer(a[9], -1, 1 << 20, &code) && heads <= INT32_MAX);
     if (a[10] != Py_None) {
       const at::Tensor *st = tensor(a[10]);
-      NEED(st && st->is_cuda() && st->scalar_type() == kI32 && st->is_contiguous());
+      NEED(st && st->is_cuda() && st->get_device() == dev && st->scalar_type() == kI32 && st->is_contiguous());
       sp = st->data_ptr();
     }
     NEED(stream_of(a[11], dev, &s));
@@ -339,7 +339,7 @@ PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
     NEED(maybe(a[4], kI32, dev, {batch}, &np));
     if (a[7] != Py_None) {
       const at::Tensor *st = tensor(a[7]);
-      NEED(st && st->is_cuda() && st->scalar_type() == kI32 && st->is_contiguous());
+      NEED(st && st->is_cuda() && st->get_device() == dev && st->scalar_type() == kI32 && st->is_contiguous());
       sp = st->data_ptr();
     }
     NEED(stream_of(a[8], dev, &s));
