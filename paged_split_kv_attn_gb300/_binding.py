@@ -782,10 +782,11 @@ def kv_prep_append_latent(layout: Layout, x, row_of, pos_of, page_tables, pages_
         desc.num_q_heads = heads
         desc.q = _rows(q, "q", (n, heads, PSKV_LATENT_ROT), dev)
         desc.q_out = _rows(q_out, "q_out", (n, heads, PSKV_LATENT_ROT), dev)
-        desc.q_token, desc.q_head, _ = q.stride()
-        token, head, _ = q_out.stride()
-        desc.q_out_token, desc.q_out_head = token, head
-        if n > 1 and token < PSKV_LATENT_ROT or heads > 1 and head < PSKV_LATENT_ROT:
+        # (a stride over a single row says nothing)
+        step = lambda t, dim: t.stride(dim) if t.shape[dim] > 1 else PSKV_LATENT_ROT
+        desc.q_token, desc.q_head = step(q, 0), step(q, 1)
+        desc.q_out_token, desc.q_out_head = step(q_out, 0), step(q_out, 1)
+        if desc.q_out_token < PSKV_LATENT_ROT or desc.q_out_head < PSKV_LATENT_ROT:
             raise ValueError("q_out's rows must not overlap")
     _check(lib.kv_prep_append_latent(
         layout.handle, ctypes.byref(desc), _rows(x, "x", (n, d), dev), x.stride(0) if n > 1 else d, n,

@@ -261,14 +261,16 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
       const at::Tensor *q = rows(a[15], dev, {t, heads, PSKV_LATENT_ROT});
       const at::Tensor *o = rows(a[16], dev, {t, heads, PSKV_LATENT_ROT});
       NEED(q && o && heads >= 1 && heads <= INT32_MAX);
-      NEED(!(t > 1 && o->stride(0) < PSKV_LATENT_ROT) && !(heads > 1 && o->stride(1) < PSKV_LATENT_ROT));
       p.num_q_heads = (int32_t)heads;
       p.q = q->data_ptr();
-      p.q_token = q->stride(0);
-      p.q_head = q->stride(1);
+      // (a stride over a single row says nothing)
+      auto step = [](const at::Tensor *r, int64_t dim) { return r->size(dim) > 1 ? r->stride(dim) : PSKV_LATENT_ROT; };
+      p.q_token = step(q, 0);
+      p.q_head = step(q, 1);
       p.q_out = o->data_ptr();
-      p.q_out_token = o->stride(0);
-      p.q_out_head = o->stride(1);
+      p.q_out_token = step(o, 0);
+      p.q_out_head = step(o, 1);
+      NEED(p.q_out_token >= PSKV_LATENT_ROT && p.q_out_head >= PSKV_LATENT_ROT);
     }
     NEED(stream_of(a[18], dev, &st));
     void *xp = x->data_ptr();
