@@ -41,6 +41,8 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "latent.h"
 #include "pskv_internal.cuh"
 #include "tc_common.cuh"
@@ -726,7 +728,7 @@ bool make_map(CUtensorMap *m, const void *base, long long rows, long long pitch,
 
 template <bool kLo>
 cudaError_t launch(const ExpandedAttnArgs &a, cudaStream_t s) {
-  static bool attr_set[64] = {};
+  static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -47,6 +47,8 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "latent.h"
 #include "pskv_internal.cuh"
 #include "pskv_plan.h"
@@ -941,7 +943,7 @@ namespace {
 template <int DC, bool kLo>
 cudaError_t launch(const LatentAttnArgs &a, cudaStream_t s) {
   using L = Lay<DC, kLo>;
-  static bool attr_set[64] = {};
+  static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
