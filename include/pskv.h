@@ -454,7 +454,7 @@ int kv_prep_append_latent(const pskv_layout *layout, const pskv_latent_prep_desc
  *   num_q_heads  1..PSKV_LATENT_MAX_HEADS (any number)
  *   num_tokens   1..PSKV_MAX_WINDOW_TOKENS
  *   seq_lens     each at least num_tokens, or 0: a row of a padded batch, whose
- *                outputs are zeros (no fault bit)
+ *                outputs are zeros (no fault bit); table_stride * page_size at most 2^31 - 129
  *   num_splits   0: chosen from the host lengths; else pieces of whole 128-key tiles,
  *                this many at most for the longest row (shorter rows have fewer)
  *   workspace    decode_attn_latent_workspace_bytes(...) bytes of these lengths, or

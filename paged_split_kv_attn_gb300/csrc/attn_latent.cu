@@ -319,7 +319,7 @@ struct Loader {
   __device__ bool run(const Piece &pc) {
     if (a.batch > 1) pages.base = -1;  // another row's table
     const int32_t *tbl = a.page_tables + (size_t)pc.b * a.table_stride;
-    const int n_slots = (pc.len + a.page_size - 1) / a.page_size;
+    const int n_slots = (pc.len - 1) / a.page_size + 1;
     Place at(pc.t0 * kKeys, a.page_size);
     for (int j = 0; j < pc.n; ++j) {
       const int left = pc.len - (pc.t0 + j) * kKeys;

@@ -401,7 +401,7 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   if (opts && opts->append_k) return PSKV_ERR_UNSUPPORTED;  // kv_prep_append_latent writes the rows
   if (d.num_pages * d.page_size > INT32_MAX) return PSKV_ERR_UNSUPPORTED;  // tensor coordinates
   const int64_t cap = (int64_t)table_stride * d.page_size;
-  if (cap > INT32_MAX) return PSKV_ERR_INVALID_ARG;
+  if (cap > INT32_MAX - kLatentTile) return PSKV_ERR_INVALID_ARG;  // a row's last tile ends in 32 bits
   int64_t longest = 0;
   for (int32_t b = 0; b < batch; ++b) {
     const int64_t len = seq_lens_host[b];
