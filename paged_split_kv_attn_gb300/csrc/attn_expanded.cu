@@ -27,9 +27,9 @@
 //
 // Per tile the tensor pipe works (12 + 8) * 64 = 1,280 cycles, and the softmax takes 1,500: 512
 // of the special-function unit (4 cycles a warp's exponent), as many of single-issue
-// operations, and the latencies of the barriers between them.  Measured for that prompt: 113.0 us
-// (1.52 PFLOP/s); of 117.8 before the last step 103 were left without the exponents and 108 with a
-// third of the score products.
+// operations, and the latencies of the barriers between them.  Measured for that prompt: 113.4 us
+// replayed back to back (1.51 PFLOP/s), 126.5 as one call among others (1.36); of 117.8 before the
+// last step 103 were left without the exponents and 108 with a third of the score products.
 // Other splits of the softmax were no faster: four threads a query 120.6, one thread with
 // the next tile's scores in flight 131, two warps on alternate tiles 133 us.
 //

@@ -29,7 +29,7 @@
 // its products are done, and S(j + 1) runs while the softmax works on tile j.  Measured at dc = 512:
 // a tile costs a pair 1.42 us until 56 pairs run (the rings' turnaround), 1.97 us with all
 // 76, which is 5.7 TB/s of cached rows; a call costs 7.5 to 10 us beside its tiles (one
-// row of 40,002 keys, 32 heads: 63 pieces of five tiles and the merge, 19.7 us).
+// row of 40,002 keys, 32 heads: 63 pieces of five tiles and the merge, 19.8 us).
 //
 // A row's keys are cut into pieces of `tiles_per_piece` tiles, one piece per cluster
 // (pskv_plan.cpp picks the size that fills the clusters in one wave).  A row of one

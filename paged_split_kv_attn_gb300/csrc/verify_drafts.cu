@@ -24,9 +24,9 @@
 // sums' loads.
 // No workspace, no second launch, no atomics but fault bits.
 //
-// Measured: 64 rows of 131,072 f32 (67 MB of p and q) 18.1 us with the rows in L2, 22.9 from
+// Measured: 64 rows of 131,072 f32 (67 MB of p and q) 18.2 us with the rows in L2, 22.9 from
 // memory (2.9 TB/s); one row of 32,001 bf16, which is the chain launch, drafts, rows, barrier,
-// rows again, 6.0 us, and about the same chain stands before and behind the large call's
+// rows again, 6.2 us, and about the same chain stands before and behind the large call's
 // stream.  Eight CTAs of eight warps: sixteen CTAs 25.6 and 6.2 us, four of sixteen warps 18.6
 // and 7.1.
 #include <type_traits>
