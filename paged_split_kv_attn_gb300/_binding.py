@@ -830,7 +830,7 @@ def latent_workspace(layout: Layout, seq_lens_host, num_tokens: int, num_q_heads
     tokens with no row longer than the longest of these."""
     lens_h = _lens_i32(seq_lens_host, "seq_lens_host")
     if bound:
-        n = decode_attn_latent_workspace_bound(layout, max(1, *lens_h), len(lens_h), num_tokens, num_q_heads,
+        n = decode_attn_latent_workspace_bound(layout, max([1, *lens_h]), len(lens_h), num_tokens, num_q_heads,
                                                num_splits)
         return _planned_workspace(n, layout.k_pool.device)
     if table_stride is None:

@@ -120,6 +120,8 @@ def _try_calls() -> None:
     try:
         _build_calls()
     except Exception as e:
+        if os.path.exists(CALLS_TAG):  # (what an earlier build left may not fit this library)
+            os.remove(CALLS_TAG)
         warnings.warn(f"the compiled calls were not built; the Python forms are used instead: {e}", RuntimeWarning)
 
 

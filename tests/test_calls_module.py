@@ -65,3 +65,20 @@ def test_a_library_elsewhere_binds_them_to_itself(unbound):
     """The calls enter the library that was loaded, wherever it lies."""
     calls = B._bind_calls(pskv.load_library())
     assert calls is not B._PythonCalls and calls.decode() is None  # (not a call's arguments)
+
+
+def test_what_an_earlier_build_left_is_not_used(monkeypatch, tmp_path):
+    """Calls that could not be rebuilt beside a new library are not called into it."""
+    tag = tmp_path / "_calls.tag"
+    tag.write_text(pskv_build.calls_tag())
+    pskv_build.build()
+    monkeypatch.setattr(pskv_build, "CALLS_TAG", str(tag))
+    assert pskv_build.calls_fit()
+
+    def fails():
+        raise RuntimeError("no compiler")
+
+    monkeypatch.setattr(pskv_build, "_build_calls", fails)
+    with pytest.warns(RuntimeWarning, match="no compiler"):
+        pskv_build._try_calls()
+    assert not pskv_build.calls_fit()
