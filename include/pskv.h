@@ -82,6 +82,8 @@ typedef struct CUevent_st *pskv_event_t;
 #define PSKV_FAULT_BAD_POSITION 64u /* a prep token whose rotation position is outside the table: skipped */
 #define PSKV_FAULT_BAD_MASK 128u    /* a tree mask without its own bit or with a later one: later bits ignored */
 #define PSKV_FAULT_BAD_TOKEN 256u   /* a drafted token outside the vocabulary: refused like any other */
+#define PSKV_FAULT_BAD_ROW 512u     /* a fork's row outside the batch, or one it may not write: that fork skipped */
+#define PSKV_FAULT_BAD_PATH 1024u   /* a path that does not go up through its window: that row left as it was */
 
 /* ---- limits ---------------------------------------------------------------- */
 #define PSKV_MAX_SPLITS 1024       /* most partitions one decode call may use */
@@ -93,6 +95,7 @@ typedef struct CUevent_st *pskv_event_t;
 #define PSKV_LATENT_MAX_HEADS 128  /* query heads of decode_attn_latent */
 #define PSKV_EXPANDED_NOPE 128     /* unrotated columns of an expanded query or key */
 #define PSKV_EXPANDED_V 128        /* columns of an expanded value */
+#define PSKV_MAX_LAYOUTS 128       /* layouts (layers) of one kv_keep_tokens or kv_fork_rows call */
 
 /* Description of one paged KV pool.
  *
@@ -122,7 +125,8 @@ typedef struct CUevent_st *pskv_event_t;
  * which every query head shares (num_kv_heads = 1).  k_pool holds the rows,
  * [num_pages][page_size][head_dim_k]; v_pool is NULL: the values are the rows'
  * first head_dim_v columns.  Written by kv_prep_append_latent, read by
- * decode_attn_latent; every other call refuses the format (UNSUPPORTED). */
+ * decode_attn_latent and decode_attn_latent_tree, moved by kv_keep_tokens and kv_fork_rows; every
+ * other call refuses the format (UNSUPPORTED). */
 typedef struct pskv_layout_desc {
   int64_t num_pages;   /* pages in each region, >= 1 */
   int32_t page_size;   /* keys per page: a multiple of PSKV_KEY_TILE */
@@ -492,6 +496,25 @@ int decode_attn_latent_workspace_bound(const pskv_layout *layout, int32_t max_le
                                        int32_t max_batch, int32_t max_tokens,
                                        int32_t num_q_heads, int32_t num_splits, size_t *bytes);
 
+/* Tree attention over a drafted window of a latent pool: decode_attn_latent with the masks of
+ * decode_attn_tree.  Token t of row b attends every key before the window (the row's last
+ * num_tokens keys) and the window keys whose bits its mask holds.
+ *   tree_mask   device uint64[batch][num_tokens], 8-byte aligned, as for decode_attn_tree: a valid mask
+ *               holds bit t (the token itself) and no bit above t; one without bit t or
+ *               with a later bit sets PSKV_FAULT_BAD_MASK (the later bits are ignored, the token
+ *               attends what is left; with nothing left its output is zeros and
+ *               PSKV_FAULT_EMPTY_ROW is set)
+ * A chain (the mask of token t = bits 0..t) gives decode_attn_latent's bits.  All else, the workspace
+ * with its sizes included, is decode_attn_latent's; every token's key in a row's own window
+ * has to hold finite values.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
+int decode_attn_latent_tree(const pskv_layout *layout, const void *q, const int32_t *page_tables,
+                            int32_t table_stride, const int32_t *seq_lens_host,
+                            const int32_t *seq_lens, const uint64_t *tree_mask, int32_t batch,
+                            int32_t num_tokens, int32_t num_q_heads, float scale,
+                            int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
+                            int32_t out_dtype, const pskv_decode_opts *opts, pskv_stream_t stream);
+
 /* Expanded latent attention of variable-length chunks: row b's queries are
  * rows [cu_q[b], cu_q[b+1]) of q, its keys rows [cu_k[b], cu_k[b+1]) of kv and
  * k_rot; the queries are the row's last keys (as many keys as queries at
@@ -548,6 +571,105 @@ int verify_drafts(const void *target_probs, const void *draft_probs, int32_t dty
                   const int32_t *drafts, const int32_t *num_drafts, const float *u, int32_t batch,
                   int32_t max_drafts, int32_t vocab, int32_t *tokens, int32_t *accepted,
                   int32_t *status, pskv_stream_t stream);
+
+/* Filters of sample_tokens: one value a request each, or NULL (off for all). */
+typedef struct pskv_sample_desc {
+  const float *temperature; /* device float[requests]: logits are divided by it; one that is not above
+                               0 (0, NaN, or so small that its reciprocal is not finite) takes the
+                               likeliest token.  NULL: 1 */
+  const int32_t *top_k;     /* device int32[requests]: tokens kept; below 1 or from vocab on: all */
+  const float *top_p;       /* device float[requests]: share of the weight kept; 1 and above, or NaN: all */
+  const float *min_p;       /* device float[requests]: least weight, of the likeliest token's; 0 and below,
+                               or NaN: all; above 1 counts as 1 */
+} pskv_sample_desc;
+
+/* Sampling from logits: a token from a given uniform number, the filtered distribution, or both
+ * (what verify_drafts takes as target_probs or draft_probs).  For a row l of logits with M its
+ * largest (NaN counts as -inf):
+ *   x(v) = (l(v) - M) * (1 / temperature), each step rounded to f32 (0 where l(v) = M)
+ *   w(v) = expf(x(v)), W(v) = w(v) rounded to the nearest multiple of 2^-40 (ties to the even one)
+ * Tokens are ordered by x, the largest first, equal ones by index.  top_k keeps the first k of
+ * them.  Of these, with S their sum of W, top_p keeps the ones whose predecessors sum to less than
+ * floor(top_p * S) (in units of 2^-40), and always the first.  Of these, min_p keeps the ones with
+ * w(v) >= min_p.  With S the sum of W over what is kept,
+ *   token = the lowest kept v with sum_{w <= v} W(w) > floor(u * S),   probs(v) = W(v) / S, 0 elsewhere.
+ * Products and sums are exact, so the token does not depend on how the work is split.
+ *   logits        device, dtype (F32 or BF16): row r (of requests * tokens_per_request) begins at
+ *                 logits + r * logits_row (elements, >= vocab); only the first vocab of a row are read
+ *   filters       or NULL (no filter, temperature 1)
+ *   u             device float[rows] in [0, 1) (values outside count as the nearer end, NaN as 0), or NULL:
+ *                 no token is drawn
+ *   tokens        device int32[rows], or NULL when u is
+ *   probs         device [rows][vocab] of probs_dtype (F32 or BF16), or NULL
+ *   status        device int32[4] fault word or NULL
+ * A row without any finite or +inf logit gives token -1, zeros and PSKV_FAULT_EMPTY_ROW; several logits
+ * of +inf share the weight.  vocab 1 .. 2^22.  No workspace.  Errors: INVALID_ARG (also neither tokens
+ * nor probs asked for), CUDA. */
+int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t requests,
+                  int32_t tokens_per_request, int32_t vocab, const pskv_sample_desc *filters,
+                  const float *u, int32_t *tokens, void *probs, int32_t probs_dtype,
+                  int32_t *status, pskv_stream_t stream);
+
+/* The path of a drafted tree that stands, given the target's own token behind each window token
+ * (sample_tokens on the window's logits; what follows decode_attn_tree and decode_attn_latent_tree).
+ * The window's token 0 is no draft: it stands.  The parent of token t > 0 is the highest bit below t
+ * of its mask (none: it never stands); t stands if its parent does, drafts[t] = sampled[parent] >= 0, and no
+ * lower token with the same parent has the same draft.  So the tokens that stand are one path, and the
+ * text goes on with what the target says along it.
+ *   drafts     device int32[batch][num_tokens]: the window's tokens (drafts[0] is not looked at)
+ *   tree_mask  device uint64[batch][num_tokens], 8-byte aligned, as for decode_attn_tree (same faults)
+ *   sampled    device int32[batch][num_tokens]
+ *   tokens     device int32[batch][num_tokens]: sampled[path[0]], sampled[path[1]], ..., then -1
+ *   path       device int32[batch][num_tokens]: the standing tokens' places, going up, then -1
+ *   kept       device int32[batch]: how many stand (1 at least)
+ *   status     device int32[4] fault word or NULL
+ * num_tokens 1..PSKV_MAX_WINDOW_TOKENS.  No workspace.  Errors: INVALID_ARG, CUDA. */
+int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t *sampled,
+                int32_t batch, int32_t num_tokens, int32_t *tokens, int32_t *path, int32_t *kept,
+                int32_t *status, pskv_stream_t stream);
+
+/* Keep some of each row's last num_tokens keys (a drafted window's standing path) and drop the
+ * others: key w0 + path[b][i] of row b becomes key w0 + i for i < kept[b], w0 = seq_lens[b] -
+ * num_tokens, in the pools of all the layouts (layers that share the page tables), bit for bit, and the
+ * row's new length is w0 + kept[b].
+ *   layouts    host array of num_layouts (1..PSKV_MAX_LAYOUTS) layouts of one description but for
+ *              their pools and status words; any format.  Faults go to the first one's status word
+ *   path       device int32[batch][num_tokens]: path[b][0 .. kept[b]) goes up, within [0, num_tokens);
+ *              the rest is not looked at.  Else PSKV_FAULT_BAD_PATH
+ *   kept       device int32[batch], 0..num_tokens each (else PSKV_FAULT_BAD_PATH)
+ *   seq_lens   device int32[batch]: each at least num_tokens, or 0 (a padded batch's row: nothing is
+ *              done, its new length is 0); else PSKV_FAULT_BAD_LENGTH
+ *   new_lens   device int32[batch]; not one of the arrays read
+ * A row refused (these, or a page id outside the pool: PSKV_FAULT_BAD_PAGE) keeps its rows and its
+ * length.  The window's pages must belong to the row alone (kv_fork_rows' last pages do).  num_tokens
+ * 1..PSKV_MAX_WINDOW_TOKENS.  Errors: INVALID_ARG (also layouts that differ), UNSUPPORTED (pages of more
+ * than 16 GB), CUDA. */
+int kv_keep_tokens(const pskv_layout *const *layouts, int32_t num_layouts,
+                   const int32_t *page_tables, int32_t table_stride, const int32_t *seq_lens,
+                   const int32_t *path, const int32_t *kept, int32_t batch, int32_t num_tokens,
+                   int32_t *new_lens, pskv_stream_t stream);
+
+/* Rows that continue another row's keys: for each fork i, table row dst[i] becomes a copy of row src[i].
+ * Whole pages are shared (their ids are copied); the page that the keys end in, when they end
+ * inside one, is copied (its seq_lens % page_size first rows, all heads, all layouts) into page
+ * new_pages[i], so that both rows go on in pages of their own.  Then seq_lens[dst] =
+ * seq_lens[src] and pages_of_row[dst] = the pages that hold keys; table entries past these are left as they are.
+ * Who holds which page, and when one is free again, is the caller's to count.
+ *   layouts       as for kv_keep_tokens
+ *   src, dst      device int32[n]: rows of the tables.  A dst that is out of range or that another fork of
+ *                 the call has as its src or dst, or equals its own src, is refused
+ *                 (PSKV_FAULT_BAD_ROW), and so is a src out of range
+ *   new_pages     device int32[n]: pages no row holds, distinct; not looked at where the keys fill their pages
+ *   page_tables   device int32[batch][table_stride], read and written; seq_lens, pages_of_row device
+ *                 int32[batch], too
+ * A fork is also refused for a length outside [0, table_stride * page_size] (PSKV_FAULT_BAD_LENGTH), a lease
+ * of fewer pages than its keys need (PSKV_FAULT_PAST_PAGES), or a page to copy from or to that is outside the
+ * pool or the same (PSKV_FAULT_BAD_PAGE).  A refused fork writes nothing.  n 0..65535.
+ * Errors: INVALID_ARG (also layouts that differ), UNSUPPORTED (pages of more than 16 GB), CUDA. */
+int kv_fork_rows(const pskv_layout *const *layouts, int32_t num_layouts, const int32_t *src,
+                 const int32_t *dst, const int32_t *new_pages, int32_t n, int32_t *page_tables,
+                 int32_t table_stride, int32_t *seq_lens, int32_t *pages_of_row, int32_t batch,
+                 pskv_stream_t stream);
 
 /* Merge P partials per row in two levels by the exact rescaling identity and
  * normalise (gem design, "Candidate ownership and storage"; pegainfer #1055,

@@ -8,6 +8,7 @@ from ._binding import *  # noqa: F401,F403
 from ._binding import (EXPORTS, Layout, PskvError, decode_attn_multirow, decode_attn_splitkv,
                        decode_attn_tree, decode_attn_latent, decode_attn_latent_workspace_bytes,
                        decode_attn_latent_workspace_bound, kv_prep_append_latent, latent_workspace, prefill_attn_expanded, verify_drafts,
+                       decode_attn_latent_tree, sample_tokens, verify_tree, kv_keep_tokens, kv_fork_rows,
                        decode_attn_splitkv_static, decode_attn_windowed,
                        decode_attn_workspace_bytes, kv_append_rows, kv_prep_append, load_library,
                        merge_partials, merge_partials_workspace_bytes, paged_kv_layout_create,
@@ -20,6 +21,7 @@ from ._binding import (EXPORTS, Layout, PskvError, decode_attn_multirow, decode_
 __all__ = ["EXPORTS", "Layout", "PskvError", "decode_attn_multirow", "decode_attn_splitkv",
            "decode_attn_tree", "decode_attn_latent", "decode_attn_latent_workspace_bytes",
            "decode_attn_latent_workspace_bound", "kv_prep_append_latent", "latent_workspace", "prefill_attn_expanded", "verify_drafts",
+           "decode_attn_latent_tree", "sample_tokens", "verify_tree", "kv_keep_tokens", "kv_fork_rows",
            "decode_attn_splitkv_static", "decode_attn_windowed",
            "decode_attn_workspace_bytes", "kv_append_rows", "kv_prep_append", "load_library",
            "merge_partials",

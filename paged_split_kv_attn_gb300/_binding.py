@@ -43,6 +43,8 @@ PSKV_FAULT_BAD_STATE = 32
 PSKV_FAULT_BAD_POSITION = 64
 PSKV_FAULT_BAD_MASK = 128
 PSKV_FAULT_BAD_TOKEN = 256
+PSKV_FAULT_BAD_ROW = 512
+PSKV_FAULT_BAD_PATH = 1024
 
 PSKV_MAX_SPLITS = 1024
 PSKV_AUTO_MAX_SPLITS = 256
@@ -53,6 +55,7 @@ PSKV_LATENT_ROT = 64
 PSKV_LATENT_MAX_HEADS = 128
 PSKV_EXPANDED_NOPE = 128
 PSKV_EXPANDED_V = 128
+PSKV_MAX_LAYOUTS = 128
 PSKV_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 # Every function the header declares, in the header's order.
@@ -60,7 +63,8 @@ EXPORTS = ("paged_kv_layout_create", "paged_kv_layout_destroy", "kv_append_rows"
            "decode_attn_splitkv", "decode_attn_windowed", "decode_attn_multirow",
            "decode_attn_tree", "prefill_attn_paged", "kv_prep_append_latent", "decode_attn_latent",
            "decode_attn_latent_workspace_bytes", "decode_attn_latent_workspace_bound",
-           "prefill_attn_expanded", "verify_drafts",
+           "decode_attn_latent_tree", "prefill_attn_expanded", "verify_drafts", "sample_tokens",
+           "verify_tree", "kv_keep_tokens", "kv_fork_rows",
            "merge_partials",
            "decode_attn_workspace_bytes", "merge_partials_workspace_bytes",
            "prefill_attn_workspace_bytes", "decode_attn_multirow_workspace_bytes",
@@ -108,6 +112,11 @@ class DecodeOpts(ctypes.Structure):
                 ("append_v", ctypes.c_void_p), ("append_pages", ctypes.c_void_p)]
 
 
+class SampleDesc(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
+
+
 _LIB = None
 
 
@@ -144,8 +153,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.decode_attn_latent_workspace_bytes.argtypes = [P, P, I32, I32, I32, I32, I32,
                                                        ctypes.POINTER(SZ)]
     lib.decode_attn_latent_workspace_bound.argtypes = [P, I32, I32, I32, I32, I32, ctypes.POINTER(SZ)]
+    lib.decode_attn_latent_tree.argtypes = [P, P, P, I32, P, P, P, I32, I32, I32, F, I32, P, SZ, P, I32,
+                                            P, P]
     lib.prefill_attn_expanded.argtypes = [P, P, P, I64, P, P, P, P, I32, I32, F, P, I32, P, P]
     lib.verify_drafts.argtypes = [P, P, I32, P, P, P, I32, I32, I32, P, P, P, P]
+    lib.sample_tokens.argtypes = [P, I32, I64, I32, I32, I32, ctypes.POINTER(SampleDesc), P, P, P, I32, P, P]
+    lib.verify_tree.argtypes = [P, P, P, I32, I32, P, P, P, P, P]
+    lib.kv_keep_tokens.argtypes = [ctypes.POINTER(P), I32, P, I32, P, P, P, I32, I32, P, P]
+    lib.kv_fork_rows.argtypes = [ctypes.POINTER(P), I32, P, P, P, I32, P, I32, P, P, I32, P]
     lib.merge_partials.argtypes = [P, P, P, I32, I32, I32, P, I32, P, SZ, P, P, P]
     lib.decode_attn_workspace_bytes.argtypes = [I32, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.merge_partials_workspace_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(SZ)]
@@ -853,6 +868,32 @@ def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, 
                           None if stream is None else _stream(stream))
         if r is not None:
             return r if type(r) is not int else _check(r, "decode_attn_latent")
+    return _decode_latent(False, layout, q, page_tables, seq_lens, seq_lens_host, None, scale, num_splits, workspace,
+                          out, out_dtype, merge_group, events, stream)
+
+
+def decode_attn_latent_tree(layout: Layout, q, page_tables, seq_lens, seq_lens_host, tree_mask, scale,
+                            num_splits: int = 0, workspace=None, out=None, out_dtype=None,
+                            merge_group: int = 0, events=None, stream=None) -> torch.Tensor:
+    """Tree attention over a drafted window of a latent pool: decode_attn_latent with ``tree_mask``
+    (device int64 or uint64 [batch, tokens]), each token's ancestor bits, itself included.  Token t
+    attends every key before the window and the window tokens its mask marks.  Workspaces are
+    decode_attn_latent's."""
+    return _decode_latent(True, layout, q, page_tables, seq_lens, seq_lens_host, tree_mask, scale, num_splits,
+                          workspace, out, out_dtype, merge_group, events, stream)
+
+
+def _masks(tree_mask, batch: int, tokens: int, dev: int) -> int:
+    """A window's ancestor masks: their address."""
+    kind = getattr(tree_mask, "dtype", None)
+    if kind not in (torch.int64, getattr(torch, "uint64", torch.int64)):
+        raise TypeError("tree_mask must hold 64-bit integers (int64 or uint64 bit patterns)")
+    return _ptr(tree_mask, "tree_mask", (batch, tokens), kind, dev)
+
+
+def _decode_latent(tree: bool, layout: Layout, q, page_tables, seq_lens, seq_lens_host, tree_mask, scale,
+                   num_splits, workspace, out, out_dtype, merge_group, events, stream):
+    lib = _LIB or load_library()
     dev, desc = _current_device(), layout.desc
     if q.dim() != 4:
         raise ValueError(f"q must be [batch, tokens, heads, {desc.head_dim_k}]")
@@ -862,6 +903,7 @@ def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, 
     lens_h = _lens_i32(seq_lens_host, "seq_lens_host")
     if len(lens_h) != batch:
         raise ValueError("seq_lens_host must have one entry per row")
+    masks = (_masks(tree_mask, batch, tokens, dev),) if tree else ()
     qp = _ptr(q, "q", (batch, tokens, hq, desc.head_dim_k), torch.bfloat16, dev)
     out, op, code = _out_like(out, (batch, tokens, hq, desc.head_dim_v), q, out_dtype, dev, stream)
     stride = page_tables.shape[1]
@@ -874,11 +916,11 @@ def decode_attn_latent(layout: Layout, q, page_tables, seq_lens, seq_lens_host, 
         wp = _ptr(workspace, "workspace", workspace.shape, workspace.dtype, dev)
         size = workspace.numel() * workspace.element_size()
     opts = _opts(merge_group, events)
-    _check(lib.decode_attn_latent(
+    _check((lib.decode_attn_latent_tree if tree else lib.decode_attn_latent)(
         layout._handle, qp, _ptr(page_tables, "page_tables", (batch, stride), torch.int32, dev), stride,
-        lens_h, _ptr(seq_lens, "seq_lens", (batch,), torch.int32, dev), batch, tokens, hq, scale,
+        lens_h, _ptr(seq_lens, "seq_lens", (batch,), torch.int32, dev), *masks, batch, tokens, hq, scale,
         _int32(num_splits, "num_splits"), wp, size, op, code, None if opts is None else ctypes.byref(opts),
-        _stream_on(stream, dev)), "decode_attn_latent")
+        _stream_on(stream, dev)), "decode_attn_latent_tree" if tree else "decode_attn_latent")
     return out
 
 
@@ -949,6 +991,110 @@ def verify_drafts(target_probs, draft_probs, drafts, u, num_drafts=None, tokens=
         _ptr(u, "u", (batch, t1), torch.float32, dev), batch, t, vocab,
         kp, ap, _status(status, dev), _stream_on(stream, dev)), "verify_drafts")
     return tokens, accepted
+
+
+def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
+                  probs=None, status=None, stream=None):
+    """Sample from ``logits`` [batch, vocab] or [batch, tokens, vocab] (f32 or bf16; rows may be
+    padded) by the given uniform numbers ``u`` (f32, logits' shape without its last dimension).  The filters
+    hold one value a batch entry: ``temperature``, ``top_p``, ``min_p`` f32 [batch], ``top_k`` int32 [batch]; None: off.
+    ``probs`` (f32 or bf16, of logits' shape) is filled with the filtered distribution, as
+    verify_drafts takes it.  Returns ``tokens`` int32 of u's shape; with ``u`` None only ``probs`` is made."""
+    lib = _LIB or load_library()
+    dev = _current_device()
+    shape = logits.shape
+    if len(shape) not in (2, 3):
+        raise ValueError("logits must be [batch, vocab] or [batch, tokens, vocab]")
+    batch, each, vocab = shape[0], 1 if len(shape) == 2 else shape[1], shape[-1]
+    code = _dtype_code(logits.dtype)
+    _complain(logits, "logits", shape, logits.dtype, dev)
+    # one step from row to row (a stride over a single one says nothing)
+    steps = ([logits.stride(1)] if each > 1 else []) + ([logits.stride(0) / each] if batch > 1 and each > 0 else [])
+    if (vocab > 1 and logits.stride(-1) != 1) or len({*steps}) > 1 or min(steps, default=vocab) < vocab:
+        raise ValueError("logits must be rows of unit column stride, evenly spaced")
+    head = tuple(shape[:-1])
+    per = lambda t, name, kind: None if t is None else _ptr(t, name, (batch,), kind, dev)
+    filters = SampleDesc(per(temperature, "temperature", torch.float32), per(top_k, "top_k", torch.int32),
+                         per(top_p, "top_p", torch.float32), per(min_p, "min_p", torch.float32))
+    up = None if u is None else _ptr(u, "u", head, torch.float32, dev)
+    if tokens is None and u is not None:
+        tokens = _empty(head, torch.int32, logits.device, stream)
+    _check(lib.sample_tokens(
+        logits.data_ptr(), code, int(steps[0]) if steps else vocab, batch, each, vocab, ctypes.byref(filters), up,
+        None if tokens is None else _ptr(tokens, "tokens", head, torch.int32, dev),
+        None if probs is None else _ptr(probs, "probs", shape, probs.dtype, dev),
+        0 if probs is None else _dtype_code(probs.dtype), _status(status, dev), _stream_on(stream, dev)), "sample_tokens")
+    return tokens
+
+
+def verify_tree(drafts, tree_mask, sampled, tokens=None, path=None, kept=None, status=None, stream=None):
+    """The path of a drafted tree that stands: ``drafts`` int32 [batch, tokens] (the window's tokens, the
+    first one no draft), ``tree_mask`` as for decode_attn_tree, ``sampled`` int32 [batch, tokens], the target's
+    token behind each (sample_tokens).  Returns (``tokens`` int32 [batch, tokens]: what the text goes on with, then
+    -1s; ``path`` int32 [batch, tokens]: the standing tokens' places, then -1s; ``kept`` int32 [batch])."""
+    lib = _LIB or load_library()
+    dev, i32 = _current_device(), torch.int32
+    if drafts.dim() != 2:
+        raise ValueError("drafts must be [batch, tokens]")
+    batch, t = shape = tuple(drafts.shape)
+    dp, mp = _ptr(drafts, "drafts", shape, i32, dev), _masks(tree_mask, batch, t, dev)
+    sp = _ptr(sampled, "sampled", shape, i32, dev)
+    tokens = _empty(shape, i32, drafts.device, stream) if tokens is None else tokens
+    path = _empty(shape, i32, drafts.device, stream) if path is None else path
+    kept = _empty((batch,), i32, drafts.device, stream) if kept is None else kept
+    _check(lib.verify_tree(dp, mp, sp, batch, t, _ptr(tokens, "tokens", shape, i32, dev), _ptr(path, "path", shape, i32, dev),
+                           _ptr(kept, "kept", (batch,), i32, dev), _status(status, dev), _stream_on(stream, dev)),
+           "verify_tree")
+    return tokens, path, kept
+
+
+def _handles(layouts, dev: int):
+    """The handles of one layout or a list of them (layers that share the page tables)."""
+    layouts = [layouts] if isinstance(layouts, Layout) else layouts
+    for l in layouts:
+        if l._pool[1] != dev:
+            raise ValueError(f"a pool is on {l.k_pool.device}, the current device is cuda:{dev}")
+    return (ctypes.c_void_p * len(layouts))(*[l._pool[0] for l in layouts]), len(layouts)
+
+
+def kv_keep_tokens(layouts, page_tables, seq_lens, path, kept, new_lens=None, stream=None) -> torch.Tensor:
+    """Keep a path of each row's drafted window and drop its other tokens: with w0 = seq_lens[b] - tokens, key
+    w0 + path[b, i] becomes key w0 + i for i < kept[b], in the pools of ``layouts`` (a Layout, or a list of layers'
+    that share ``page_tables``).  ``path`` int32 [batch, tokens] and ``kept`` int32 [batch] are
+    verify_tree's.  Returns ``new_lens`` int32 [batch], w0 + kept (its own memory, not ``seq_lens``)."""
+    lib = _LIB or load_library()
+    dev, i32 = _current_device(), torch.int32
+    handles, n = _handles(layouts, dev)
+    if path.dim() != 2 or page_tables.dim() != 2:
+        raise ValueError("path must be [batch, tokens], page_tables [batch, stride]")
+    batch, t = path.shape
+    stride = page_tables.shape[1]
+    if new_lens is None:
+        new_lens = _empty((batch,), i32, path.device, stream)
+    _check(lib.kv_keep_tokens(handles, n, _ptr(page_tables, "page_tables", (batch, stride), i32, dev), stride,
+                              _ptr(seq_lens, "seq_lens", (batch,), i32, dev), _ptr(path, "path", (batch, t), i32, dev),
+                              _ptr(kept, "kept", (batch,), i32, dev), batch, t,
+                              _ptr(new_lens, "new_lens", (batch,), i32, dev), _stream_on(stream, dev)), "kv_keep_tokens")
+    return new_lens
+
+
+def kv_fork_rows(layouts, src, dst, new_pages, page_tables, seq_lens, pages_of_row, stream=None) -> None:
+    """Let table rows ``dst`` [n] continue the keys of rows ``src`` [n]: whole pages are shared, the page the
+    keys end inside of is copied into ``new_pages`` [n], in the pools of ``layouts`` (a Layout, or a list of layers').
+    ``page_tables``, ``seq_lens`` and ``pages_of_row`` (int32, on the device) are updated in place."""
+    lib = _LIB or load_library()
+    dev, i32 = _current_device(), torch.int32
+    handles, layers = _handles(layouts, dev)
+    if page_tables.dim() != 2:
+        raise ValueError("page_tables must be [batch, stride]")
+    batch, stride = page_tables.shape
+    n = src.numel()
+    _check(lib.kv_fork_rows(handles, layers, _ptr(src, "src", (n,), i32, dev), _ptr(dst, "dst", (n,), i32, dev),
+                            _ptr(new_pages, "new_pages", (n,), i32, dev), n,
+                            _ptr(page_tables, "page_tables", (batch, stride), i32, dev), stride,
+                            _ptr(seq_lens, "seq_lens", (batch,), i32, dev),
+                            _ptr(pages_of_row, "pages_of_row", (batch,), i32, dev), batch, _stream_on(stream, dev)),
+           "kv_fork_rows")
 
 
 def decode_attn_splitkv_static(layout: Layout, q, page_tables, seq_lens, seq_lens_host, scale,

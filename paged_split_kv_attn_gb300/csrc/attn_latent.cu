@@ -459,7 +459,7 @@ struct Loader {
 
 }  // namespace
 
-template <int DC, bool kLo>
+template <int DC, bool kLo, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     pskv_attn_latent(const LatentAttnArgs a, const __grid_constant__ Maps maps) {
   using L = Lay<DC, kLo>;
@@ -652,7 +652,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
       // keys below lim are seen (columns behind the last, whose results go nowhere, see all: a
       // warp of theirs would mask every tile for nothing)
-      const int lim = col < cols ? pc.len - a.num_tokens + col / a.num_q_heads + 1 : pc.len;
+      // (of a drafted tree: the keys before the window, and in it what the token's mask holds)
+      const int token = col / a.num_q_heads, w0 = pc.len - a.num_tokens;
+      const int lim = col < cols ? (kTree ? w0 : w0 + token + 1) : pc.len;
+      unsigned long long sees = 0;
+      if (kTree && col < cols) {
+        const unsigned long long mask = a.tree_mask[(size_t)pc.b * a.num_tokens + token], own = 1ull << token;
+        sees = mask & (own | (own - 1));
+        if (sees != mask || !(mask & own)) raise_fault(a.status, PSKV_FAULT_BAD_MASK);
+      }
+      __syncwarp();
       float m = -CUDART_INF_F, l = 0.f;
       for (int j = 0; j < pc.n; ++j, ++g, ++meets) {
         const int r = g & 1;
@@ -674,11 +683,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // selection: rows never loaded may hold anything)
         const int key0 = (pc.t0 + j) * kKeys + kHalf * kh + 32 * gr;
         float mul = sc;
-        if (__any_sync(0xffffffffu, key0 + 32 > lim || bad != 0 || !(sc > 0.f))) {
+        bool some = key0 + 32 > lim;  // of these keys are not seen
+        uint32_t vis = ~0u;           // (a tree's) bit c: key0 + c is seen, before the window or by the mask
+        if constexpr (kTree) {
+          const int d = key0 - lim;
+          if (some) vis = d >= 64 ? 0u : d >= 0 ? (uint32_t)(sees >> d) : (uint32_t)(sees << -d) | ((1u << -d) - 1u);
+          some = vis != ~0u;
+        }
+        if (__any_sync(0xffffffffu, some || bad != 0 || !(sc > 0.f))) {
           mul = 1.f;
+          if constexpr (kTree) {
+            if (bad & 1u) vis &= 0xffff0000u;
+            if (bad & 2u) vis &= 0x0000ffffu;
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            x[c] = key0 + c < lim && !((bad >> (c >> 4)) & 1u) ? x[c] * sc : -CUDART_INF_F;
+            for (int c = 0; c < 32; ++c) x[c] = (vis >> c) & 1u ? x[c] * sc : -CUDART_INF_F;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              x[c] = key0 + c < lim && !((bad >> (c >> 4)) & 1u) ? x[c] * sc : -CUDART_INF_F;
+          }
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -940,7 +963,7 @@ __global__ void __launch_bounds__(128 * kLanes) pskv_merge_latent(const LatentAt
 
 namespace {
 
-template <int DC, bool kLo>
+template <int DC, bool kLo, bool kTree>
 cudaError_t launch(const LatentAttnArgs &a, cudaStream_t s) {
   using L = Lay<DC, kLo>;
   static std::atomic<bool> attr_set[64] = {};
@@ -948,7 +971,7 @@ cudaError_t launch(const LatentAttnArgs &a, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(dev >= 0 && dev < 64 && attr_set[dev])) {
-    e = cudaFuncSetAttribute(pskv_attn_latent<DC, kLo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(pskv_attn_latent<DC, kLo, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              L::kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
@@ -962,16 +985,18 @@ cudaError_t launch(const LatentAttnArgs &a, cudaStream_t s) {
       !tc2::make_block_map(&maps.v, a.pool, a.num_pages * a.page_size, DC + 64, DC / 256,
                            whole ? kHalf : 16, whole ? 2 : 1, whole ? DC / 256 : 1))
     return cudaErrorInvalidValue;
-  return launch_pdl(pskv_attn_latent<DC, kLo>, dim3(2 * (unsigned)a.clusters), dim3(kThreads),
+  return launch_pdl(pskv_attn_latent<DC, kLo, kTree>, dim3(2 * (unsigned)a.clusters), dim3(kThreads),
                     L::kSmemBytes, s, a, maps);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_latent(const LatentAttnArgs &a, int dc, cudaStream_t s) {
-  const bool lo = a.out_dtype == PSKV_DTYPE_F32;
-  if (dc == 512) return lo ? launch<512, true>(a, s) : launch<512, false>(a, s);
-  if (dc == 256) return lo ? launch<256, true>(a, s) : launch<256, false>(a, s);
+  const bool lo = a.out_dtype == PSKV_DTYPE_F32, tree = a.tree_mask != nullptr;
+  if (dc == 512 && tree) return lo ? launch<512, true, true>(a, s) : launch<512, false, true>(a, s);
+  if (dc == 256 && tree) return lo ? launch<256, true, true>(a, s) : launch<256, false, true>(a, s);
+  if (dc == 512) return lo ? launch<512, true, false>(a, s) : launch<512, false, false>(a, s);
+  if (dc == 256) return lo ? launch<256, true, false>(a, s) : launch<256, false, false>(a, s);
   return cudaErrorInvalidValue;
 }
 

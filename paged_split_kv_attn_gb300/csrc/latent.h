@@ -56,6 +56,7 @@ struct LatentAttnArgs {
   int tiles_per_piece;
   int clusters;                // CTA pairs to launch
   float scale_log2;
+  const unsigned long long *tree_mask;  // [B][T] window tokens each token sees, or null: causal
 };
 
 struct ExpandedAttnArgs {

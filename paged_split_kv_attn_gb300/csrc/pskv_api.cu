@@ -14,6 +14,7 @@
 #include "latent.h"
 #include "pskv_internal.cuh"
 #include "pskv_plan.h"
+#include "tree.h"
 
 using namespace pskv;
 
@@ -148,7 +149,7 @@ int decode_common(const pskv_layout *layout, const void *q, const int32_t *page_
                   int32_t batch, const QuerySpec &qs, int32_t num_q_heads, float scale,
                   int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
                   int32_t out_dtype, const pskv_decode_opts *opts, pskv_stream_t stream,
-                  size_t *plan_bytes = nullptr) {
+                  size_t *plan_bytes = nullptr, const uint64_t *tree_mask = nullptr) {
   if (!layout || !seq_lens_host) return PSKV_ERR_INVALID_ARG;
   if (!plan_bytes && (!q || !page_tables || !seq_lens || !out)) return PSKV_ERR_INVALID_ARG;
   if (windowed && !plan_bytes && (!first_pos || !window_lo)) return PSKV_ERR_INVALID_ARG;
@@ -386,7 +387,7 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
                   int32_t batch, int32_t num_tokens, int32_t num_q_heads, float scale,
                   int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
                   int32_t out_dtype, const pskv_decode_opts *opts, pskv_stream_t stream,
-                  size_t *plan_bytes = nullptr) {
+                  size_t *plan_bytes = nullptr, const uint64_t *tree_mask = nullptr) {
   if (!layout || !seq_lens_host) return PSKV_ERR_INVALID_ARG;
   if (!plan_bytes && (!q || !page_tables || !seq_lens || !out)) return PSKV_ERR_INVALID_ARG;
   if (batch < 1 || batch > 65535 || table_stride < 1 || num_q_heads < 1 || num_tokens < 1 ||
@@ -446,6 +447,7 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   a.tiles_per_piece = plan.tiles_per_piece;
   a.clusters = plan.clusters;
   a.scale_log2 = scale * kLog2e;
+  a.tree_mask = reinterpret_cast<const unsigned long long *>(tree_mask);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (opts && opts->partial_begin) {
@@ -464,6 +466,38 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   if (e != cudaSuccess) return cuda_fail(e);
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return PSKV_OK;
+}
+
+// The pools of layers that share page tables: one description but for pools and status words.
+int gather_pools(const pskv_layout *const *layouts, int32_t num_layouts, Pools *p) {
+  if (!layouts || num_layouts < 1 || num_layouts > PSKV_MAX_LAYOUTS) return PSKV_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < num_layouts; ++i) {
+    if (!layouts[i]) return PSKV_ERR_INVALID_ARG;
+    const pskv_layout_desc &d = layouts[i]->d, &first = layouts[0]->d;
+    if (d.num_pages != first.num_pages || d.page_size != first.page_size ||
+        d.num_kv_heads != first.num_kv_heads || d.head_dim_k != first.head_dim_k ||
+        d.head_dim_v != first.head_dim_v || d.kv_dtype != first.kv_dtype || d.format != first.format)
+      return PSKV_ERR_INVALID_ARG;
+    p->k[i] = d.k_pool;
+    p->v[i] = d.v_pool;
+  }
+  const pskv_layout_desc &d = layouts[0]->d;
+  p->count = num_layouts;
+  p->heads = d.num_kv_heads;
+  p->page_size = d.page_size;
+  p->k_vecs = layouts[0]->k_row_bytes / 16;
+  p->v_vecs = d.format == PSKV_FORMAT_LATENT ? 0 : layouts[0]->v_row_bytes / 16;
+  p->num_pages = d.num_pages;
+  p->status = d.status;
+  // a page's vectors are counted in 32 bits
+  if ((int64_t)p->heads * (p->k_vecs + p->v_vecs) > (1 << 30) / p->page_size) return PSKV_ERR_UNSUPPORTED;
+  return PSKV_OK;
+}
+
+// Whether [p, p + n) and [q, q + m) (bytes) share any.
+bool overlap(const void *p, size_t n, const void *q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
 }
 
 }  // namespace
@@ -781,6 +815,18 @@ int decode_attn_latent(const pskv_layout *layout, const void *q, const int32_t *
                        out_dtype, opts, stream);
 }
 
+int decode_attn_latent_tree(const pskv_layout *layout, const void *q, const int32_t *page_tables,
+                            int32_t table_stride, const int32_t *seq_lens_host,
+                            const int32_t *seq_lens, const uint64_t *tree_mask, int32_t batch,
+                            int32_t num_tokens, int32_t num_q_heads, float scale,
+                            int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
+                            int32_t out_dtype, const pskv_decode_opts *opts, pskv_stream_t stream) {
+  if (!tree_mask || !aligned(tree_mask, 8)) return PSKV_ERR_INVALID_ARG;
+  return decode_latent(layout, q, page_tables, table_stride, seq_lens_host, seq_lens, batch,
+                       num_tokens, num_q_heads, scale, num_splits, workspace, workspace_bytes, out,
+                       out_dtype, opts, stream, nullptr, tree_mask);
+}
+
 int decode_attn_latent_workspace_bytes(const pskv_layout *layout, const int32_t *seq_lens_host,
                                        int32_t table_stride, int32_t batch, int32_t num_tokens,
                                        int32_t num_q_heads, int32_t num_splits, size_t *bytes) {
@@ -892,6 +938,115 @@ int verify_drafts(const void *target_probs, const void *draft_probs, int32_t dty
   a.accepted = accepted;
   a.status = status;
   const cudaError_t e = launch_verify_drafts(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PSKV_OK;
+}
+
+int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t requests,
+                  int32_t tokens_per_request, int32_t vocab, const pskv_sample_desc *filters,
+                  const float *u, int32_t *tokens, void *probs, int32_t probs_dtype,
+                  int32_t *status, pskv_stream_t stream) {
+  if (!logits || requests < 1 || tokens_per_request < 1 || vocab < 1 || vocab > (1 << 22) ||
+      logits_row < vocab || (int64_t)requests * tokens_per_request > (1 << 24))
+    return PSKV_ERR_INVALID_ARG;
+  if ((dtype != PSKV_DTYPE_F32 && dtype != PSKV_DTYPE_BF16) || (!tokens && !probs) ||
+      (tokens == nullptr) != (u == nullptr))
+    return PSKV_ERR_INVALID_ARG;
+  if (probs && probs_dtype != PSKV_DTYPE_F32 && probs_dtype != PSKV_DTYPE_BF16)
+    return PSKV_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype == PSKV_DTYPE_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(tokens, 4) ||
+      !aligned(probs, probs_dtype == PSKV_DTYPE_BF16 ? 2 : 4) || !aligned(status, 4))
+    return PSKV_ERR_INVALID_ARG;
+  SampleArgs a;
+  a.logits = logits;
+  a.logits_row = logits_row;
+  a.dtype = dtype;
+  a.rows = requests * tokens_per_request;
+  a.per_request = tokens_per_request;
+  a.vocab = vocab;
+  a.temperature = filters ? filters->temperature : nullptr;
+  a.top_k = filters ? filters->top_k : nullptr;
+  a.top_p = filters ? filters->top_p : nullptr;
+  a.min_p = filters ? filters->min_p : nullptr;
+  if (!aligned(a.temperature, 4) || !aligned(a.top_k, 4) || !aligned(a.top_p, 4) || !aligned(a.min_p, 4))
+    return PSKV_ERR_INVALID_ARG;
+  a.u = u;
+  a.tokens = tokens;
+  a.probs = probs;
+  a.probs_dtype = probs_dtype;
+  a.status = status;
+  const cudaError_t e = launch_sample(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PSKV_OK;
+}
+
+int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t *sampled,
+                int32_t batch, int32_t num_tokens, int32_t *tokens, int32_t *path, int32_t *kept,
+                int32_t *status, pskv_stream_t stream) {
+  if (!drafts || !tree_mask || !sampled || !tokens || !path || !kept || batch < 1 ||
+      batch > (1 << 20) || num_tokens < 1 || num_tokens > PSKV_MAX_WINDOW_TOKENS)
+    return PSKV_ERR_INVALID_ARG;
+  if (!aligned(tree_mask, 8) || !aligned(drafts, 4) || !aligned(sampled, 4) || !aligned(tokens, 4) ||
+      !aligned(path, 4) || !aligned(kept, 4) || !aligned(status, 4))
+    return PSKV_ERR_INVALID_ARG;
+  VerifyTreeArgs a;
+  a.drafts = drafts;
+  a.tree_mask = reinterpret_cast<const unsigned long long *>(tree_mask);
+  a.sampled = sampled;
+  a.batch = batch;
+  a.num_tokens = num_tokens;
+  a.tokens = tokens;
+  a.path = path;
+  a.kept = kept;
+  a.status = status;
+  const cudaError_t e = launch_verify_tree(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PSKV_OK;
+}
+
+int kv_keep_tokens(const pskv_layout *const *layouts, int32_t num_layouts,
+                   const int32_t *page_tables, int32_t table_stride, const int32_t *seq_lens,
+                   const int32_t *path, const int32_t *kept, int32_t batch, int32_t num_tokens,
+                   int32_t *new_lens, pskv_stream_t stream) {
+  Pools p;
+  const int rc = gather_pools(layouts, num_layouts, &p);
+  if (rc) return rc;
+  if (!page_tables || !seq_lens || !path || !kept || !new_lens || table_stride < 1 || batch < 1 ||
+      batch > 65535 || num_tokens < 1 || num_tokens > PSKV_MAX_WINDOW_TOKENS)
+    return PSKV_ERR_INVALID_ARG;
+  if (!aligned(page_tables, 4) || !aligned(seq_lens, 4) || !aligned(path, 4) || !aligned(kept, 4) ||
+      !aligned(new_lens, 4))
+    return PSKV_ERR_INVALID_ARG;
+  const size_t row = 4 * (size_t)batch;
+  if (overlap(new_lens, row, seq_lens, row) || overlap(new_lens, row, kept, row) ||
+      overlap(new_lens, row, path, row * num_tokens) || overlap(new_lens, row, page_tables, row * table_stride))
+    return PSKV_ERR_INVALID_ARG;  // (blocks of a row read what another one writes)
+  const KeepArgs a = {page_tables, table_stride, seq_lens, path, kept, batch, num_tokens, new_lens};
+  const cudaError_t e = launch_keep(a, p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PSKV_OK;
+}
+
+int kv_fork_rows(const pskv_layout *const *layouts, int32_t num_layouts, const int32_t *src,
+                 const int32_t *dst, const int32_t *new_pages, int32_t n, int32_t *page_tables,
+                 int32_t table_stride, int32_t *seq_lens, int32_t *pages_of_row, int32_t batch,
+                 pskv_stream_t stream) {
+  Pools p;
+  const int rc = gather_pools(layouts, num_layouts, &p);
+  if (rc) return rc;
+  if (n < 0 || n > 65535 || table_stride < 1 || batch < 1) return PSKV_ERR_INVALID_ARG;
+  if (n == 0) return PSKV_OK;
+  if (!src || !dst || !new_pages || !page_tables || !seq_lens || !pages_of_row)
+    return PSKV_ERR_INVALID_ARG;
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(new_pages, 4) || !aligned(page_tables, 4) ||
+      !aligned(seq_lens, 4) || !aligned(pages_of_row, 4))
+    return PSKV_ERR_INVALID_ARG;
+  const ForkArgs a = {src, dst, new_pages, n, page_tables, table_stride, seq_lens, pages_of_row, batch};
+  const cudaError_t e = launch_fork(a, p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return PSKV_OK;
@@ -1014,7 +1169,7 @@ const char *pskv_last_cuda_error(void) { return g_cuda_error; }
 
 uint64_t pskv_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 
-int pskv_version(void) { return 104; }
+int pskv_version(void) { return 105; }
 
 int pskv_check_flags(const pskv_layout *layout, int32_t clear, pskv_stream_t stream,
                      uint32_t *flags) {

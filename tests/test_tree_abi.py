@@ -1,0 +1,122 @@
+"""Refusals of sampling, drafted trees and forked rows, all decided on the host before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import paged_split_kv_attn_gb300 as pskv
+from paged_split_kv_attn_gb300 import _binding as B
+from paged_split_kv_attn_gb300 import build as pskv_build
+
+INVALID, UNSUPPORTED = B.PSKV_ERR_INVALID_ARG, B.PSKV_ERR_UNSUPPORTED
+P = 0x30000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pskv_build.build()
+    return pskv.load_library()
+
+
+@pytest.fixture()
+def make(lib):
+    made = []
+
+    def one(**kw):
+        base = dict(num_pages=8, page_size=64, num_kv_heads=1, head_dim_k=576, head_dim_v=512,
+                    kv_dtype=B.PSKV_DTYPE_BF16, format=B.PSKV_FORMAT_LATENT, k_pool=0x10000, v_pool=None, status=None)
+        base.update(kw)
+        d, h = B.LayoutDesc(*[base[f] for f, _ in B.LayoutDesc._fields_]), ctypes.c_void_p()
+        assert lib.paged_kv_layout_create(ctypes.byref(d), ctypes.byref(h)) == 0
+        made.append(h)
+        return h
+
+    yield one
+    for h in made:
+        lib.paged_kv_layout_destroy(h)
+
+
+def handles(*hs):
+    return (ctypes.c_void_p * len(hs))(*[h if h is None else h.value for h in hs]), len(hs)
+
+
+SAMPLE = dict(logits=P, dtype=0, row=100, requests=2, each=3, vocab=100, filters=None, u=P, tokens=P, probs=None,
+              probs_dtype=0, status=None)
+
+
+def sample(lib, **kw):
+    a = {**SAMPLE, **kw}
+    f = None if a["filters"] is None else ctypes.byref(B.SampleDesc(*a["filters"]))
+    return lib.sample_tokens(a["logits"], a["dtype"], a["row"], a["requests"], a["each"], a["vocab"], f, a["u"],
+                             a["tokens"], a["probs"], a["probs_dtype"], a["status"], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(logits=None), dict(dtype=2), dict(dtype=-1), dict(row=99), dict(row=-1), dict(requests=0), dict(each=0),
+    dict(vocab=0), dict(vocab=(1 << 22) + 1, row=1 << 23), dict(requests=1 << 13, each=1 << 12), dict(u=None),
+    dict(tokens=None), dict(u=None, tokens=None), dict(probs=P, probs_dtype=5), dict(logits=P + 2), dict(u=P + 1),
+    dict(tokens=P + 2), dict(probs=P + 2), dict(probs=P + 1, probs_dtype=1), dict(status=P + 1),
+    dict(filters=(P + 2, None, None, None)), dict(filters=(None, P + 1, None, None)),
+    dict(filters=(None, None, P + 3, None)), dict(filters=(None, None, None, P + 2))])
+def test_sample_refusals(lib, kw):
+    assert sample(lib, **kw) == INVALID
+
+
+def test_walk_refusals(lib):
+    base = [P, P, P, 2, 4, P, P, P, None, None]
+    for at, bad in [(0, None), (1, None), (2, None), (3, 0), (3, (1 << 20) + 1), (4, 0), (4, 65), (5, None), (6, None),
+                    (7, None), (0, P + 2), (1, P + 4), (2, P + 1), (5, P + 2), (6, P + 2), (7, P + 2), (8, P + 2)]:
+        args = list(base)
+        args[at] = bad
+        assert lib.verify_tree(*args) == INVALID, (at, bad)
+
+
+def test_tree_over_other_pools_and_without_masks(lib, make):
+    lens = (ctypes.c_int32 * 1)(100)
+    call = lambda h, mask, n=8: lib.decode_attn_latent_tree(h, P, P, 4, lens, P, mask, 1, n, 8, 0.1, 1, P, 1 << 30, P, 1, None, None)
+    latent = make()
+    assert call(latent, None) == call(latent, P + 4) == call(latent, P, 65) == call(None, P) == INVALID
+    split = make(format=B.PSKV_FORMAT_SPLIT, head_dim_k=512, v_pool=0x20000, num_kv_heads=4)
+    assert call(split, P) == UNSUPPORTED
+    lens[0] = 7  # shorter than its window
+    assert call(latent, P) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(num_pages=9), dict(page_size=32), dict(head_dim_k=320, head_dim_v=256),
+                                dict(format=B.PSKV_FORMAT_SPLIT, head_dim_k=512, v_pool=0x20000)])
+def test_layers_have_one_description(lib, make, kw):
+    hs = handles(make(), make(k_pool=0x90000), make(**kw))
+    assert lib.kv_keep_tokens(*hs, P, 4, P, P, P, 2, 8, 0x50000, None) == INVALID
+    assert lib.kv_fork_rows(*hs, P, P, P, 2, P, 4, P, P, 2, None) == INVALID
+
+
+def test_layouts_given_wrongly(lib, make):
+    h = make()
+    huge = make(page_size=1 << 24)  # more vectors a page than 32 bits count
+    for hs, code in [((None, 1), INVALID), (handles(h, None), INVALID), (handles(*[h] * 129), INVALID),
+                     ((handles(h)[0], 0), INVALID), (handles(huge), UNSUPPORTED)]:
+        assert lib.kv_keep_tokens(*hs, P, 4, P, P, P, 2, 8, 0x50000, None) == code
+        assert lib.kv_fork_rows(*hs, P, P, P, 2, P, 4, P, P, 2, None) == code
+
+
+def test_keep_refusals(lib, make):
+    #        0 table 1 stride 2 lens 3 path 4 kept 5 batch 6 tokens 7 new lens
+    base = [P, 4, P + 0x1000, P + 0x2000, P + 0x3000, 2, 8, P + 0x4000]
+    hs = handles(make())
+    for at, bad in [(0, None), (1, 0), (2, None), (3, None), (4, None), (5, 0), (5, 65536), (6, 0), (6, 65), (7, None),
+                    (0, P + 2), (2, P + 1), (3, P + 1), (4, P + 1), (7, P + 0x4002), (7, P + 0x1004), (7, P + 0x2000 + 60),
+                    (7, P + 0x3004), (7, P + 28)]:
+        args = list(base)
+        args[at] = bad
+        assert lib.kv_keep_tokens(*hs, *args, None) == INVALID, (at, bad)
+
+
+def test_fork_refusals(lib, make):
+    #       0 src 1 dst 2 new 3 n 4 table 5 stride 6 lens 7 leases 8 batch
+    base = [P, P, P, 2, P, 4, P, P, 2]
+    hs = handles(make())
+    for at, bad in [(0, None), (1, None), (2, None), (3, -1), (3, 65536), (4, None), (5, 0), (6, None), (7, None), (8, 0),
+                    (0, P + 1), (1, P + 1), (2, P + 2), (4, P + 2), (6, P + 1), (7, P + 3)]:
+        args = list(base)
+        args[at] = bad
+        assert lib.kv_fork_rows(*hs, *args, None) == INVALID, (at, bad)
+    assert lib.kv_fork_rows(*hs, None, None, None, 0, None, 4, None, None, 2, None) == 0  # no fork
