@@ -976,7 +976,10 @@ int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t
   a.probs = probs;
   a.probs_dtype = probs_dtype;
   a.status = status;
-  const cudaError_t e = launch_sample(a, reinterpret_cast<cudaStream_t>(stream));
+  int n_sm = 0;
+  const int rc = sm_count(&n_sm);
+  if (rc) return rc;
+  const cudaError_t e = launch_sample(a, n_sm, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return PSKV_OK;

@@ -65,7 +65,7 @@ struct ForkArgs {
   int batch;
 };
 
-cudaError_t launch_sample(const SampleArgs &a, cudaStream_t s);
+cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t s);
 cudaError_t launch_verify_tree(const VerifyTreeArgs &a, cudaStream_t s);
 cudaError_t launch_keep(const KeepArgs &a, const Pools &p, cudaStream_t s);
 cudaError_t launch_fork(const ForkArgs &a, const Pools &p, cudaStream_t s);
