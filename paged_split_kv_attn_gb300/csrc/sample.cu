@@ -7,18 +7,20 @@
 //
 // A cluster of up to eight CTAs takes a row, each warp a piece of the vocabulary.  The row is
 // read from memory once, for M; the later passes find it in L1 and L2 (staged in shared memory, fewer
-// CTAs fit on an SM: 64 rows of 131,072 would take two waves).  Passes:
-//   1  M
-//   2  the sum of W, and a histogram of |x| by its leading bits (256 bins an octave from 2^-3 to 2^5:
-//      counts only, a shared-memory atomic a token, beside the exponentials)
-//   3  the bin that holds the border: from the counts (top-k), or by the bins' estimated weight
-//      (top-p).  The pass sums W exactly over what lies before the bin and lists the bin's own tokens.
-//      An estimate that was off shows in the exact sum, and the next bin is tried from there
-//   -  the bin's tokens (some hundred) are ranked against each other.  More than fit in the list: the
-//      bin is cut into 2,048 finer ones (pass 2's counts again, for its tokens alone), down to a
-//      single |x|, whose tokens' border is a matter of counting
+// CTAs fit on an SM: 64 rows of 131,072 would take two waves).
+//   1  M, and the largest logit of each of a piece's 32 chunks: later passes leave out chunks below what they look for
+//   2  the sum of W, and a histogram of |x| in steps of 1/64 (counts: a shared-memory atomic a token,
+//      beside the exponentials)
+//   3  the bin that holds the border: by the counts (top-k), or by the bins' estimated weight (top-p).
+//      If all tokens up to that bin's end fit in a list, they are listed, and all that is left
+//      (top-k's border, top-p's, the draw) is found in the list by every CTA for itself.  Else the pass
+//      sums W exactly over what lies before the bin and lists the bin alone; an estimate that was off shows in the
+//      exact sum, and another bin is tried from there.  A bin that does not fit is cut into
+//      2,048 finer ones, down to a single |x|, whose tokens' border is a matter of counting
 //   4  the drawn token's piece again, and the probabilities where they are asked for.
 // Between passes the warps' results cross the cluster through distributed shared memory, one barrier each.
+// A token in a list is found by 256 bins of its key (|x|'s bits, then the index) at a time.
+#include <float.h>
 #include <limits.h>
 #include <math_constants.h>
 
@@ -38,13 +40,19 @@ constexpr int kMaxPieces = kMaxCluster * kWarps;
 constexpr int kPerSm = 4;        // CTAs an SM holds (registers)
 constexpr int kBins = 2048;
 constexpr int kList = 1024;      // listed tokens of a cluster
-constexpr uint32_t kFirst = 0x3e000000u >> 15;  // the first level's bin 1: |x| from 2^-3, by its 17 leading bits
+constexpr int kEach = 8;         // elements a lane takes in a step
+constexpr int kStep = 32 * kEach;
+constexpr int kQueue = 32 + 4 * 32;
+constexpr float kDeepest = 31.98f;        // what lies deeper has no weight: expf(-31.98) is under 2^-46
+constexpr uint32_t kDeep = 0x41ffd70au;   // its bits
 
-// The bits of |x| for a logit, M the row's largest and inv = 1 / T: they go up as x falls.  No weight: infinity's.
-__device__ __forceinline__ uint32_t depth(float l, float M, float inv) {
-  const float x = __fmul_rn(__fsub_rn(l, M), inv);
-  return l == M ? 0u : __float_as_uint(fminf(fabsf(x), CUDART_INF_F));  // (a NaN: infinity)
+// |x| of a logit, up to kDeepest (NaN and -inf: that), M the row's largest and inv = 1 / T.  (M = +inf: its
+// tokens have 0, all others kDeepest, by the largest finite number as M and inv = +inf.)
+__device__ __forceinline__ float depth_of(float l, float M, float inv) {
+  return fabsf(fminf(fmaxf(__fmul_rn(__fsub_rn(l, M), inv), -kDeepest), 0.f));
 }
+// Its bits, which go up as x falls.
+__device__ __forceinline__ uint32_t depth(float l, float M, float inv) { return __float_as_uint(depth_of(l, M, inv)); }
 __device__ __forceinline__ float weight(uint32_t d) { return expf(-__uint_as_float(d)); }
 
 // W = hi * 2^20 + lo by two float adds whose last place is 2^-20: hi the nearest multiple, lo of the exact rest.
@@ -100,6 +108,12 @@ __device__ __forceinline__ u64 warp_scan(u64 x, int lane) {  // inclusive
   return x;
 }
 
+// The largest of the lanes' floats (none of them NaN), as integers of the same order.
+__device__ __forceinline__ float warp_max(float x) {
+  const int i = __float_as_int(x), m = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
+  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -144,91 +158,120 @@ struct Shared {
     uint2 all[kList];              // the cluster's listed tokens, once the counts are read
   };
   uint32_t total[kBins];           // the cluster's counts
-  uint2 list[kList];               // this CTA's listed tokens (|x|'s bits, index): kList / cluster of them at most
-  u64 all_w[kList];                // their W
+  uint2 list[kList];               // this CTA's listed tokens (|x|'s bits, index)
+  union {
+    u64 all_w[kList];              // W of `all`
+    float queue[kWarps][kQueue];   // |x| of tokens before the bin, before their weights are formed
+  };
   u64 post[2][3][kMaxPieces];      // what the pieces' warps told last, and before that
   uint32_t border[2];
-  u64 border_sum;
-  u64 part[kWarps];
+  u64 scan_s[kWarps];
   uint32_t scan_n[kWarps];
   float scan_e[kWarps];
   int listed, bin;
   uint32_t before_n;
   float before_e;
+  uint32_t sub_n[kThreads], sub_hi[kThreads], sub_lo[kThreads];  // a list's bins: tokens, W by 20-bit digits
+  int first_of[kMaxCluster + 1];   // where a CTA's listed tokens lie in `all`
+  int sub_bin, few_n;
+  u64 sub_before_s;
+  uint32_t sub_before_n, sub_count;
+  int few[32];
 };
 
-// A row as a warp sees it: elements at `base`, 16-byte aligned, of which [skip, skip + vocab) are the row.
+// A row as a warp sees it: elements at `base`, 16-byte aligned, of which [skip, end) are the row.
 template <typename T>
 struct Row {
   const T *base;
-  int skip, end;      // the row's elements
+  int skip, end;
   int lo, hi;         // this warp's piece, whole vectors (but for the last one's end)
+  int per_chunk;      // steps of a chunk
+  float chunk_top;    // lane c: the largest logit of chunk c
   float M, inv;
   uint32_t border;    // kept: |x| above the border's, or equal and index up to `last`
   uint32_t last;
   float least;        // and weight at least this
 
-  static constexpr int kN = 16 / sizeof(T);  // elements of a vector
+  static constexpr int kN = 16 / sizeof(T);      // elements of a vector
+  static constexpr int kVecs = kEach / kN;
   __device__ static float value(T x) {
     if constexpr (sizeof(T) == 2)
       return __uint_as_float((uint32_t)x << 16);
     else
       return x;
   }
-  __device__ bool inside(uint32_t d, int v) const { return d < border || (d == border && (uint32_t)v <= last); }
+  __device__ bool inside(uint32_t d, uint32_t v) const { return d < border || (d == border && v <= last); }
   __device__ float kept(uint32_t d, int v) const {  // weight, 0 where it is not kept
-    if (!inside(d, v)) return 0.f;
+    if (!inside(d, (uint32_t)v)) return 0.f;
     const float w = weight(d);
     return w >= least ? w : 0.f;
   }
-  // Logits of a vector's elements; those that are not the row's: -inf.
-  __device__ void load(int i, float (&x)[kN]) const {
-    if (i >= skip && i + kN <= end) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4 *>(base + i));
+  // A lane's vectors of the step at i0: raw, and what a guarded one could not read.
+  // Logits of a step's elements [i0, b): those that are not the row's or behind b: -inf.
+  __device__ void load(int i0, int b, int lane, float (&x)[kEach]) const {
 #pragma unroll
-      for (int e = 0; e < kN; ++e) x[e] = value(reinterpret_cast<const T *>(&q)[e]);
-    } else {
+    for (int k = 0; k < kVecs; ++k) {
+      const int i = i0 + (32 * k + lane) * kN;
+      if (i >= skip && i + kN <= b) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(base + i));
 #pragma unroll
-      for (int e = 0; e < kN; ++e) x[e] = i + e >= skip && i + e < end ? value(base[i + e]) : -CUDART_INF_F;
-    }
-  }
-  // f(logit, index) for the elements [a, b) (a at a vector), kDepth vectors of a lane in flight; g() after each step.
-  template <int kDepth, typename F, typename G>
-  __device__ void each(int a, int b, int lane, F f, G g) const {
-    for (int i0 = a; i0 < b; i0 += 32 * kN * kDepth) {
-      float x[kDepth][kN];
+        for (int e = 0; e < kN; ++e) x[k * kN + e] = value(reinterpret_cast<const T *>(&q)[e]);
+      } else {
 #pragma unroll
-      for (int k = 0; k < kDepth; ++k) {
-        const int i = i0 + (32 * k + lane) * kN;
-        if (i < b)
-          load(i, x[k]);
-        else
-#pragma unroll
-          for (int e = 0; e < kN; ++e) x[k][e] = -CUDART_INF_F;
+        for (int e = 0; e < kN; ++e)
+          x[k * kN + e] = i + e >= skip && i + e < b ? value(base[i + e]) : -CUDART_INF_F;
       }
-#pragma unroll
-      for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-        for (int e = 0; e < kN; ++e) f(x[k][e], i0 + (32 * k + lane) * kN + e - skip);
-      g();
     }
   }
+  // The index of element j of a lane's step at i0.
+  __device__ int index(int i0, int j, int lane) const { return i0 + (32 * (j / kN) + lane) * kN + j % kN - skip; }
+
+  // The first step from s on whose chunk is alive.
+  __device__ int next(int s, int steps, uint32_t alive) const {
+    while (s < steps && !((alive >> (s / per_chunk)) & 1u)) ++s;
+    return s;
+  }
+  // f(logit, index) for this piece's elements in live chunks, one step's loads ahead; g(whether the step is
+  // done) after every four.
+  template <typename F, typename G>
+  __device__ void each(uint32_t alive, int lane, F f, G g) const {
+    const int steps = (hi - lo + kStep - 1) / kStep;
+    int s = next(0, steps, alive);
+    float x[kEach], y[kEach];
+    if (s < steps) load(lo + s * kStep, hi, lane, y);
+    while (s < steps) {
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) x[j] = y[j];
+      const int at = lo + s * kStep;
+      s = next(s + 1, steps, alive);
+      if (s < steps) load(lo + s * kStep, hi, lane, y);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        f(x[j], index(at, j, lane));
+        if (j % 4 == 3) g(j == kEach - 1);
+      }
+    }
+  }
+  // The chunks that have tokens with |x|'s bits below d.
+  __device__ uint32_t alive(uint32_t d) const { return __ballot_sync(0xffffffffu, depth(chunk_top, M, inv) < d); }
 };
 
-// A level of bins: |x|'s bits d in [lo, hi) belong to bin (d - lo) >> shift; the first level's bins are kFirst's.
+// A level of bins.  The first: |x| to the nearest 1/64, up to 2,047; finer ones: |x|'s bits d in [lo, hi), bin
+// (d - lo) >> shift.
 struct Level {
   uint32_t lo, hi;
-  int shift;  // 0..20, or -1: the first level
-  __device__ int bin(uint32_t d) const {
-    return shift < 0 ? min(max((int)(d >> 15) - (int)kFirst + 1, 0), kBins - 1) : (int)((d - lo) >> shift);
+  int shift;  // -1: the first level
+  __device__ static int first_bin(uint32_t d) {
+    return (int)(__float_as_uint(__uint_as_float(d) + 131072.f) - 0x48000000u);  // (a last place of 1/64)
   }
   __device__ uint32_t begin(int b) const {
-    return shift < 0 ? (b == 0 ? 0u : (kFirst + b - 1) << 15) : min((uint32_t)b << shift, hi - lo) + lo;
+    if (shift >= 0) return min((uint32_t)b << shift, hi - lo) + lo;
+    // halfway goes to the even bin
+    return b == 0 ? 0u : b == kBins ? kDeep + 1 : __float_as_uint(((float)b - 0.5f) * 0x1p-6f) + (b & 1);
   }
   // an estimate of a bin's weights: the middle's
   __device__ float middle(int b) const {
-    const uint32_t a = begin(b), z = begin(b + 1);
-    return weight(a == 0 ? __float_as_uint(0.5f * __uint_as_float(z)) : a + (z - a) / 2);
+    return shift < 0 ? expf((float)b * -0x1p-6f) : weight(min(lo + ((uint32_t)b << shift) + ((1u << shift) >> 1), hi));
   }
 };
 
@@ -239,8 +282,9 @@ struct Sampler {
   Row<T> r;
   int cluster, rank, warp, lane, piece, pieces;
   int turn = 0;  // exchanges so far: their buffers alternate
+  bool coarse = true;  // sh.total has the first level's counts
 
-  // Tell the cluster up to three numbers of this piece; afterwards `told(k)` holds everybody's.
+  // Tell the cluster up to three numbers of this piece; afterwards all of them are in post.
   template <int kNumbers>
   __device__ void exchange(u64 x, u64 y = 0, u64 z = 0) {
     u64(*p)[kMaxPieces] = sh.post[turn & 1];
@@ -252,12 +296,11 @@ struct Sampler {
     ++turn;
     cluster_barrier();
   }
+  __device__ u64 posted(int k, int i) const { return i < pieces ? sh.post[(turn - 1) & 1][k][i] : 0; }
   // Sums of number k of the last exchange over all pieces, and over those before this one.
-  __device__ void told(int k, u64 &all, u64 &before) const {
-    const u64 *p = sh.post[(turn - 1) & 1][k];
-    const u64 x0 = lane < pieces ? p[lane] : 0, x1 = lane + 32 < pieces ? p[lane + 32] : 0;
-    all = warp_sum(x0 + x1);
-    before = warp_sum((lane < piece ? x0 : 0) + (lane + 32 < piece ? x1 : 0));
+  __device__ u64 told(int k) const { return warp_sum(posted(k, lane) + posted(k, lane + 32)); }
+  __device__ u64 told_before(int k) const {
+    return warp_sum((lane < piece ? posted(k, lane) : 0) + (lane + 32 < piece ? posted(k, lane + 32) : 0));
   }
 
   // The cluster's counts of each bin, from the CTAs' (each sums a share of them and hands it to all).
@@ -278,12 +321,12 @@ struct Sampler {
   // The bin at which the running count reaches `many`, or (by_sum) the running estimate e0 + w times all bins'
   // estimate over `all_w`; within [first, last].  sh.before_n and sh.before_e: what lies before it.
   __device__ int seek(const Level &lv, bool by_sum, u64 many, float e0, float w, u64 all_w, int first, int last) {
-    constexpr int kEach = kBins / kThreads;
-    const int b0 = threadIdx.x * kEach;
-    uint32_t n[kEach], n_all = 0;
-    float m[kEach], e_all = 0.f;
+    constexpr int kMine = kBins / kThreads;
+    const int b0 = threadIdx.x * kMine;
+    uint32_t n[kMine], n_all = 0;
+    float m[kMine], e_all = 0.f;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
+    for (int k = 0; k < kMine; ++k) {
       n[k] = sh.total[b0 + k];
       m[k] = n[k] ? (float)n[k] * lv.middle(b0 + k) : 0.f;
       n_all += n[k];
@@ -303,6 +346,7 @@ struct Sampler {
     n_run -= n_all;
     e_run -= e_all;
     float everything = 0.f;
+#pragma unroll
     for (int k = 0; k < kWarps; ++k) {
       if (k < warp) n_run += sh.scan_n[k], e_run += sh.scan_e[k];
       everything += sh.scan_e[k];
@@ -311,7 +355,7 @@ struct Sampler {
     const uint32_t n_at = n_run;
     const float e_at = e_run;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
+    for (int k = 0; k < kMine; ++k) {
       n_run += n[k];
       e_run += m[k];
       if (n[k] && (by_sum ? e_run >= e : n_run >= many)) {
@@ -324,7 +368,7 @@ struct Sampler {
     n_run = n_at;
     e_run = e_at;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
+    for (int k = 0; k < kMine; ++k) {
       if (b0 + k == bin) sh.before_n = n_run, sh.before_e = e_run;
       n_run += n[k];
       e_run += m[k];
@@ -333,59 +377,147 @@ struct Sampler {
     return bin;
   }
 
-  // Tokens that CTA c listed in the last pass.
-  __device__ int listed(int c) const {
-    const u64 *counts = sh.post[(turn - 1) & 1][2];
-    int n = 0;
-    for (int i = 0; i < kWarps; ++i) n += (int)counts[c * kWarps + i];
-    return n;
+  // ---- lists
+
+  // Append this piece's tokens with |x|'s bits in [from, to), inside the border, to the CTA's list.
+  __device__ void append(uint32_t d, int v) {
+    const int at = atomicAdd(&sh.listed, 1);
+    if (at < kList) sh.list[at] = make_uint2(d, (uint32_t)v);
   }
 
-  // The border among the listed tokens (A: the sum before them, `before` tokens): each CTA ranks its own against all.
-  __device__ void rank_listed(bool by_sum, u64 limit, u64 A, u64 before, u64 above_here, u64 &part_sum, u64 &mine) {
-    int all = 0, first = 0;
-    for (int c = 0; c < cluster; ++c) {
-      const int n = listed(c);
-      if (c == rank) first = all;
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint2 q = load_remote(remote(&sh.list[i], c));
-        sh.all[all + i] = q;
-        sh.all_w[all + i] = whole(weight(q.x));
+  // All CTAs' lists in one (number 2 of the last exchange: each piece's tokens): returns how many.
+  __device__ int gather() {
+    int n = 0, incl;
+    if (lane < cluster)
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) n += (int)posted(2, lane * kWarps + i);
+    incl = n;
+#pragma unroll
+    for (int d = 1; d < kMaxCluster; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, incl, kMaxCluster - 1);
+    if (warp == 0 && lane < kMaxCluster) sh.first_of[lane] = incl - n;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i < all) {
+        int c = 0;
+        while (c + 1 < cluster && sh.first_of[c + 1] <= i) ++c;
+        const uint2 q = load_remote(remote(&sh.list[i - sh.first_of[c]], c));
+        sh.all[i] = q;
+        sh.all_w[i] = whole(weight(q.x));
       }
-      all += n;
     }
     __syncthreads();
-    const int own = listed(rank);
-    for (int j = first + warp; j < first + own; j += kWarps) {
-      const uint2 q = sh.all[j];
-      u64 w = 0;
-      uint32_t n = 0;
-      for (int i = lane; i < all; i += 32) {
-        const uint2 o = sh.all[i];
-        const bool less = o.x < q.x || (o.x == q.x && o.y < q.y);
-        n += less;
-        w += less ? sh.all_w[i] : 0;
+    return all;
+  }
+
+  // Of the list's n tokens that lie inside the border (and weigh `least`), in their order (or by index), the one at
+  // which their running number (or the sum of their W) reaches `target`.  base: what the sum begins with; `with`:
+  // the sum up to that token, it included (by number: left as it is).  [lo, lo + 2^bits): where its key lies.
+  __device__ uint2 pick(int n, bool by_index, bool by_sum, u64 target, u64 base, uint32_t lo, int bits, u64 &with) {
+    u64 before_n = 0, before_s = base;
+    uint32_t fixed = 0;      // |x|'s bits, once these are down to one value
+    bool on_v = by_index, tied = false;
+    auto in = [&](int i, uint2 &q, uint32_t &key) {
+      q = sh.all[i];
+      key = on_v ? q.y : q.x;
+      return r.inside(q.x, q.y) && (!tied || q.x == fixed) && !(r.least > 0.f && weight(q.x) < r.least);
+    };
+    int shift = max(0, bits - 8);
+    for (;;) {
+      sh.sub_n[threadIdx.x] = sh.sub_hi[threadIdx.x] = sh.sub_lo[threadIdx.x] = 0;
+      if (threadIdx.x == 0) sh.sub_bin = kThreads - 1, sh.few_n = 0, sh.sub_count = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        uint2 q;
+        uint32_t key;
+        if (in(i, q, key) && key - lo < (256u << shift)) {
+          const uint32_t b = (key - lo) >> shift;
+          atomicAdd(&sh.sub_n[b], 1u);
+          if (by_sum) {  // (64-bit atomics on one word hold each other up; a digit's sums stay below 2^31)
+            atomicAdd(&sh.sub_hi[b], (uint32_t)(sh.all_w[i] >> 20));
+            atomicAdd(&sh.sub_lo[b], (uint32_t)sh.all_w[i] & 0xfffffu);
+          }
+        }
       }
-      w = A + warp_sum(w);
-      n = __reduce_add_sync(0xffffffffu, n);
-      const u64 with = w + sh.all_w[j];
-      if ((by_sum ? w < limit && limit <= with : before + n + 1 == limit) && lane < cluster) {
-        store_remote(remote(&sh.border[0], lane), q.x);
-        store_remote(remote(&sh.border[1], lane), q.y);
-        store_remote(remote(&sh.border_sum, lane), with);
+      __syncthreads();
+      const uint32_t my_n = sh.sub_n[threadIdx.x];
+      const u64 my_s = ((u64)sh.sub_hi[threadIdx.x] << 20) + sh.sub_lo[threadIdx.x];
+      uint32_t n_run = my_n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, n_run, d);
+        if (lane >= d) n_run += y;
       }
+      u64 s_run = by_sum ? warp_scan(my_s, lane) : 0;
+      if (lane == 31) sh.scan_n[warp] = n_run, sh.scan_s[warp] = s_run;
+      __syncthreads();
+      s_run += before_s;
+      for (int k = 0; k < warp; ++k) n_run += sh.scan_n[k], s_run += sh.scan_s[k];
+      const u64 at = by_sum ? s_run : before_n + n_run, was = by_sum ? s_run - my_s : before_n + n_run - my_n;
+      if (was < target && target <= at) {
+        sh.sub_bin = threadIdx.x;
+        sh.sub_before_n = n_run - my_n;
+        sh.sub_before_s = s_run - my_s;
+        sh.sub_count = my_n;
+      }
+      __syncthreads();
+      const int count = (int)sh.sub_count;
+      before_n += sh.sub_before_n;
+      before_s = sh.sub_before_s;
+      lo += (uint32_t)sh.sub_bin << shift;
+      if (count <= 32) break;
+      if (shift == 0) {  // many of one |x|: by index
+        fixed = lo;
+        tied = on_v = true;
+        lo = 0;
+        shift = 14;
+      } else {
+        shift = max(0, shift - 8);
+      }
+      __syncthreads();
     }
-    cluster_barrier();
-    r.border = sh.border[0];
-    r.last = sh.border[1];
-    part_sum = sh.border_sum;
-    u64 x = 0;
-    for (int j = first + lane; j < first + own; j += 32) {
+    // a few: ranked in every warp's lanes
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      uint2 q;
+      uint32_t key;
+      if (in(i, q, key) && key - lo < (1u << shift)) sh.few[atomicAdd(&sh.few_n, 1) & 31] = i;
+    }
+    __syncthreads();
+    const int count = min(sh.few_n, 32), mine = lane < count ? sh.few[lane] : 0;
+    const uint2 q = sh.all[mine];
+    const u64 w = sh.all_w[mine];
+    u64 sum = before_s + w, place = before_n + 1;
+    for (int k = 0; k < count; ++k) {
+      const uint32_t d = __shfl_sync(0xffffffffu, q.x, k), v = __shfl_sync(0xffffffffu, q.y, k);
+      const u64 o = __shfl_sync(0xffffffffu, w, k);
+      if (by_index ? v < q.y : d < q.x || (d == q.x && v < q.y)) sum += o, ++place;
+    }
+    const bool hit = lane < count && (by_sum ? sum - w < target && target <= sum : place == target);
+    const uint32_t who = __ballot_sync(0xffffffffu, hit);
+    const int l = who ? __ffs(who) - 1 : 0;
+    if (by_sum) with = __shfl_sync(0xffffffffu, sum, l);
+    const uint2 found = make_uint2(__shfl_sync(0xffffffffu, q.x, l), __shfl_sync(0xffffffffu, q.y, l));
+    __syncthreads();
+    return found;
+  }
+
+  // The sum of W of the list's tokens that lie inside the border (and weigh `least`), and of this piece's alone.
+  __device__ u64 list_sum(int n, u64 &mine) {
+    u64 x = 0, y = 0;
+    for (int j = lane; j < n; j += 32) {
       const uint2 q = sh.all[j];
+      if (!r.inside(q.x, q.y) || (r.least > 0.f && weight(q.x) < r.least)) continue;
       const int at = (int)q.y + r.skip;
-      if (at >= r.lo && at < r.hi && r.inside(q.x, (int)q.y)) x += sh.all_w[j];
+      x += sh.all_w[j];
+      if (at >= r.lo && at < r.hi) y += sh.all_w[j];
     }
-    mine = above_here + warp_sum(x);
+    mine = warp_sum(y);
+    return warp_sum(x);
   }
 
   // The border among tokens of one |x| (bits d): the first `ties` of them stay.
@@ -394,7 +526,7 @@ struct Sampler {
       u64 run = before_here;
       for (int i = r.lo; i < r.hi; i += 32) {
         const int at = i + lane;
-        const bool eq = at >= r.skip && at < r.hi && r.inside(d, at - r.skip) &&
+        const bool eq = at >= r.skip && at < r.hi && r.inside(d, (uint32_t)(at - r.skip)) &&
                         depth(Row<T>::value(r.base[at]), r.M, r.inv) == d;
         uint32_t who = __ballot_sync(0xffffffffu, eq);
         if (ties <= run + __popc(who)) {
@@ -410,50 +542,81 @@ struct Sampler {
     r.last = sh.border[1];
   }
 
+  // The level's counts, of the tokens with |x|'s bits in [from, to).
+  __device__ void count(const Level &lv, uint32_t from, uint32_t to) {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
+    __syncthreads();
+    r.each(r.alive(to), lane, [&](float l, int) {
+      const uint32_t d = depth(l, r.M, r.inv);
+      if (d - from < to - from) {
+        const int b = lv.shift < 0 ? Level::first_bin(d) : (int)((d - from) >> lv.shift);
+        atomicAdd(&sh.hist[b], 1u);
+      }
+    }, [](bool) {});
+    cluster_barrier();
+    add_up();
+  }
+
   // Move the border to the last token of the order's first part: the `limit` first ones (by_sum false), or the
-  // shortest part whose W sum to `limit` at least (1 .. their sum); S: the sum of all W.  part_sum: that part's sum,
-  // mine: this piece's share of it.  False: nothing with weight is left out, the border stays.
-  __device__ bool find_border(bool by_sum, u64 limit, u64 S, u64 &part_sum, u64 &mine) {
+  // shortest part whose W sum to `limit` at least (1 .. their sum); S: the sum of all W.  sum: that part's, mine:
+  // this piece's share of it.  Returns how many tokens are listed when the list holds all of that part (sum and
+  // mine then say nothing where the border is not moved), else 0.
+  __device__ int find_border(bool by_sum, u64 limit, u64 S, u64 &sum, u64 &mine) {
     Level lv{0u, 0u, -1};
     int first = 0, last = kBins - 1, tries = 0;
+    if (!coarse) count(lv, 0u, kDeep + 1);
+    coarse = true;
     int bin = seek(lv, by_sum, limit, 0.f, (float)limit, S, first, last);
     u64 skipped = 0;  // tokens before the level's first bin
     for (;;) {
-      if (!by_sum && lv.shift < 0 && bin == kBins - 1) return false;
-      const uint32_t from = lv.begin(bin), to = lv.begin(bin + 1);
+      if (!by_sum && lv.shift < 0 && bin == kBins - 1) return 0;  // nothing with weight is left out
+      const uint32_t to = lv.begin(bin + 1);
       const u64 before = skipped + sh.before_n;
       const float e_before = sh.before_e;
+      // the whole first part is listed where it fits
+      const bool whole_part = before + sh.total[bin] <= kList;
+      const uint32_t from = whole_part ? 0u : lv.begin(bin);
       // ---- exact sums, and the bin's tokens
       if (threadIdx.x == 0) sh.listed = 0;
       __syncthreads();
-      const int room = kList / cluster;
       Sum above, within;
       uint32_t n = 0;
-      r.template each<2>(r.lo, r.hi, lane, [&](float l, int v) {
-        const uint32_t d = depth(l, r.M, r.inv);
-        if (d < from) above.add(weight(d));
-        if (d - from < to - from && r.inside(d, v)) {
+      int queued = 0;
+      float *queue = sh.queue[warp];
+      r.each(r.alive(to), lane, [&](float l, int v) {
+        const float x = depth_of(l, r.M, r.inv);
+        const uint32_t d = __float_as_uint(x);
+        // tokens before the bin are packed first: mostly few of a warp's are
+        const uint32_t who = __ballot_sync(0xffffffffu, d < from);
+        if (d < from) queue[queued + __popc(who & ((1u << lane) - 1))] = x;
+        queued += __popc(who);
+        if (d - from < to - from && r.inside(d, (uint32_t)v)) {
           within.add(weight(d));
           ++n;
-          const int at = atomicAdd(&sh.listed, 1);
-          if (at < room) sh.list[at] = make_uint2(d, (uint32_t)v);
+          append(d, v);
         }
-      }, [&] { above.carry(), within.carry(); });
+      }, [&](bool) {
+        __syncwarp();
+        while (queued >= 32) above.add(expf(-queue[(queued -= 32) + lane]));
+        __syncwarp();
+        above.carry();
+        within.carry();
+      });
+      if (lane < queued) above.add(expf(-queue[lane]));
+      above.carry();
       const u64 above_here = warp_sum(above.total), here = __reduce_add_sync(0xffffffffu, n);
       exchange<3>(above_here, warp_sum(within.total), here);
-      u64 A, B, N, N_before, other;
-      told(0, A, other);
-      told(1, B, other);
-      told(2, N, N_before);
+      const u64 A = told(0), B = told(1), N = told(2);
       if (by_sum && !(A < limit && limit <= A + B)) {
         // the estimate was off: on from the exact sum, after some tries by halves
         if (A >= limit)
           last = bin - 1;
         else
           first = bin + 1;
-        if (first > last) return false;  // (cannot be)
+        if (first > last) return 0;  // (cannot be)
         if (++tries < 5) {
-          const float off = A >= limit ? -(float)(A - limit) : (float)(limit - A);
+          // (of a whole part the sum ends at the bin's end)
+          const float off = A >= limit ? -(float)(A - limit) : whole_part ? (float)(limit - B) : (float)(limit - A);
           bin = seek(lv, true, 0, e_before, off, S, first, last);
         } else {
           const int middle = (first + last) / 2;
@@ -461,32 +624,31 @@ struct Sampler {
         }
         continue;
       }
-      bool fits = true;
-      for (int c = 0; c < cluster; ++c) fits &= listed(c) <= room;
-      if (fits) {
-        rank_listed(by_sum, limit, A, before, above_here, part_sum, mine);
-        return true;
+      if (N <= kList) {
+        const int listed = gather();
+        const uint2 b = pick(listed, false, by_sum, by_sum ? limit : limit - (whole_part ? 0 : before), A, from,
+                             32 - __clz((int)(to - from - 1) | 255), sum);
+        r.border = b.x;
+        r.last = b.y;
+        sum = A + list_sum(listed, mine);
+        mine += above_here;
+        return whole_part ? listed : 0;
       }
       if (to - from == 1) {
         const u64 w = whole(weight(from)), ties = by_sum ? (limit - A + w - 1) / w : limit - before;
+        const u64 N_before = told_before(2);
         rank_ties(from, ties, N_before, here);
-        part_sum = A + ties * w;
+        sum = A + ties * w;
         mine = above_here + (ties > N_before ? min(ties - N_before, here) : 0) * w;
-        return true;
+        return 0;
       }
       // ---- finer bins
       skipped = before;
       lv = Level{from, to, max(0, 21 - __clz((int)(to - from - 1)))};
-      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
-      __syncthreads();
-      r.template each<2>(r.lo, r.hi, lane, [&](float l, int v) {
-        const uint32_t d = depth(l, r.M, r.inv);
-        if (d - from < to - from) atomicAdd(&sh.hist[lv.bin(d)], 1u);
-      }, [] {});
-      cluster_barrier();
-      add_up();
+      coarse = false;
+      count(lv, from, to);
       first = tries = 0;
-      last = lv.bin(to - 1);
+      last = (int)((to - 1 - from) >> lv.shift);
       S = B > 0 ? B : 1;  // (without what top-k left out: a first guess that this puts off is tried again)
       bin = seek(lv, by_sum, limit - skipped, 0.f, by_sum ? (float)(limit - A) : 0.f, S, first, last);
     }
@@ -519,16 +681,31 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   const int seg = ((r.end + s.pieces - 1) / s.pieces + kN - 1) / kN * kN;
   r.lo = min(s.piece * seg, r.end);
   r.hi = min(r.lo + seg, r.end);
+  r.per_chunk = max(1, (seg + 32 * kStep - 1) / (32 * kStep));
   const int req = row / a.per_request;
   float heat = a.temperature ? a.temperature[req] : 1.f, p = a.top_p ? a.top_p[req] : 1.f;
   float least = a.min_p ? a.min_p[req] : 0.f;
   int k = a.top_k ? a.top_k[req] : 0;
   const float u = a.u ? a.u[row] : 0.f;
   // ---- M
-  float top = -CUDART_INF_F;
-  r.template each<4>(r.lo, r.hi, lane, [&](float x, int) { top = fmaxf(top, x); }, [] {});
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+  r.chunk_top = -CUDART_INF_F;
+  {
+    float chunk = -CUDART_INF_F;
+    int left = r.per_chunk, c = 0;
+    r.each(~0u, lane, [&](float x, int) { chunk = fmaxf(chunk, x); }, [&](bool done) {
+      if (!done || --left > 0) return;
+      chunk = warp_max(chunk);
+      if (lane == c) r.chunk_top = chunk;
+      chunk = -CUDART_INF_F;
+      left = r.per_chunk;
+      ++c;
+    });
+    if (left < r.per_chunk) {
+      chunk = warp_max(chunk);
+      if (lane == c) r.chunk_top = chunk;
+    }
+  }
+  float top = warp_max(r.chunk_top);
   __syncwarp();
   cluster_wait();  // the others have started too
   // (the settings are the ones that the first piece read: the CTAs go the same way whoever writes to them meanwhile)
@@ -541,25 +718,27 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   k = (int)(uint32_t)sh.post[0][2][0];
   if (lane < s.pieces) top = fmaxf(top, __uint_as_float((uint32_t)tops[lane]));
   if (lane + 32 < s.pieces) top = fmaxf(top, __uint_as_float((uint32_t)tops[lane + 32]));
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+  top = warp_max(top);
   const bool empty = top == -CUDART_INF_F;
   if (empty && s.rank == 0 && threadIdx.x == 0) {
     if (a.tokens) a.tokens[row] = -1;
     raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
   }
-  r.M = top;
+  const bool endless = top == CUDART_INF_F;
+  r.M = endless ? FLT_MAX : top;
   r.inv = __fdiv_rn(1.f, heat);
-  r.border = 0x7f800000u;
+  r.border = kDeep;
   r.last = UINT_MAX;
   r.least = least > 0.f ? fminf(least, 1.f) : 0.f;
   u64 total = 1;
+  int listed = 0;  // the list's tokens, where it holds all that is kept
   if (empty) {
+    r.border = r.last = 0;
   } else if (!(heat > 0.f) || r.inv == CUDART_INF_F) {
     // ---- the likeliest token, the lowest index of M
-    r.inv = 1.f;
+    r.inv = endless ? CUDART_INF_F : 1.f;
     uint32_t at = UINT_MAX;
-    r.template each<2>(r.lo, r.hi, lane, [&](float x, int v) { at = x == top ? min(at, (uint32_t)v) : at; }, [] {});
+    r.each(r.alive(1u), lane, [&](float x, int v) { at = x == top ? min(at, (uint32_t)v) : at; }, [](bool) {});
     s.template exchange<1>((u64)__reduce_min_sync(0xffffffffu, at));
     const u64 *ats = sh.post[1][0];
     if (lane < s.pieces) at = min(at, (uint32_t)ats[lane]);
@@ -571,111 +750,139 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     if (a.tokens && s.rank == 0 && threadIdx.x == 0) a.tokens[row] = (int)at;
   } else {
     const bool some = k > 0 && k < a.vocab, part = p < 1.f, filters = some || part;
+    if (endless) r.inv = CUDART_INF_F;
     // ---- the sum of W, and where the tokens lie
     if (filters) {
       for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
       __syncthreads();
     }
-    const Level coarse{0u, 0u, -1};
-    Sum sum;
-    if (filters)
-      r.template each<2>(r.lo, r.hi, lane, [&](float x, int) {
-        const uint32_t d = depth(x, r.M, r.inv);
-        sum.add(weight(d));
-        const int b = coarse.bin(d);
-        if (b < kBins - 1) atomicAdd(&sh.hist[b], 1u);  // (behind lies no weight)
-      }, [&] { sum.carry(); });
-    else
-      r.template each<2>(r.lo, r.hi, lane, [&](float x, int) {
-        const float w = weight(depth(x, r.M, r.inv));
-        sum.add(w >= r.least ? w : 0.f);
-      }, [&] { sum.carry(); });
-    u64 mine = warp_sum(sum.total), before;
+    Sum all;
+    r.each(~0u, lane, [&](float x, int) {
+      const uint32_t d = depth(x, r.M, r.inv);
+      const float w = weight(d);
+      if (filters) {
+        all.add(w);
+        atomicAdd(&sh.hist[Level::first_bin(d)], 1u);
+      } else {
+        all.add(w >= r.least ? w : 0.f);
+      }
+    }, [&](bool done) { if (done) all.carry(); });
+    u64 mine = warp_sum(all.total);
     s.template exchange<1>(mine);
-    s.told(0, total, before);
+    total = s.told(0);
     if (filters) {
       s.add_up();
       const u64 S = total;
-      if (some) s.find_border(false, (u64)k, S, total, mine);
-      if (part) s.find_border(true, max(share(p, total), 1ull), S, total, mine);
-      if (r.least > 0.f) {
-        Sum kept;
-        r.template each<2>(r.lo, r.hi, lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); },
-                           [&] { kept.carry(); });
-        mine = warp_sum(kept.total);
+      const float least_w = r.least;  // (min_p comes last)
+      r.least = 0.f;
+      if (some) listed = s.find_border(false, (u64)k, S, total, mine);
+      if (part) {
+        const u64 limit = max(share(p, total), 1ull);
+        if (listed) {
+          const uint2 b = s.pick(listed, false, true, limit, 0, 0u, 31, total);
+          r.border = b.x;
+          r.last = b.y;
+        } else {
+          listed = s.find_border(true, limit, S, total, mine);
+        }
       }
-      s.template exchange<1>(mine);
-      s.told(0, total, before);
+      r.least = least_w;
+      if (listed) {
+        if (r.least > 0.f) total = s.list_sum(listed, mine);
+      } else {
+        if (r.least > 0.f) {
+          Sum kept;
+          r.each(r.alive(r.border + 1), lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); },
+                 [&](bool done) { if (done) kept.carry(); });
+          mine = warp_sum(kept.total);
+        }
+        s.template exchange<1>(mine);
+        total = s.told(0);
+      }
     }
-    // ---- the draw: the piece in which the running sum passes u's share
-    if (a.tokens) {
-      const u64 thr = u >= 1.f ? total - 1 : share(u, total);
+    // ---- the draw: where the running sum passes u's share
+    const u64 thr = u >= 1.f ? total - 1 : share(u, total);
+    if (a.tokens && listed) {
+      u64 with;
+      const uint2 t = s.pick(listed, true, true, thr + 1, 0, 0u, 22, with);
+      if (s.rank == 0 && threadIdx.x == 0) a.tokens[row] = (int)t.y;
+    } else if (a.tokens) {
+      const u64 before = s.told_before(0);
       if (threadIdx.x == 0) sh.bin = -1;
       __syncthreads();
       if (lane == 0 && before <= thr && thr < before + mine) {
         sh.bin = s.piece;
-        sh.border_sum = thr - before;
+        sh.sub_before_s = thr - before;
       }
       __syncthreads();
       const int hit = sh.bin;
       if (hit >= 0) {
         // its CTA: an eighth a warp
-        const u64 left = sh.border_sum;
+        const u64 left = sh.sub_before_s;
         const int p0 = min(hit * seg, r.end), p1 = min(p0 + seg, r.end);
         const int sub = ((p1 - p0 + kWarps - 1) / kWarps + kN - 1) / kN * kN;
-        const int s0 = min(p0 + warp * sub, p1), s1 = min(s0 + sub, p1);
+        r.lo = min(p0 + warp * sub, p1);
+        r.hi = min(r.lo + sub, p1);
+        r.per_chunk = INT_MAX;
         Sum kept;
-        r.template each<1>(s0, s1, lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); },
-                           [&] { kept.carry(); });
+        r.each(1u, lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); }, [&](bool done) { if (done) kept.carry(); });
         const u64 own = warp_sum(kept.total);
-        if (lane == 0) sh.part[warp] = own;
+        if (lane == 0) sh.scan_s[warp] = own;
         __syncthreads();
         u64 at = 0;
-        for (int i = 0; i < warp; ++i) at += sh.part[i];
+        for (int i = 0; i < warp; ++i) at += sh.scan_s[i];
         if (at <= left && left < at + own) {
-          for (int i0 = s0; i0 < s1; i0 += 32 * kN) {
-            float x[kN];
-            u64 w[kN], w_all = 0;
+          for (int i0 = r.lo; i0 < r.hi && at <= left; i0 += 32 * kN) {
             const int i = i0 + lane * kN;
-            if (i < s1) r.load(i, x);
+            u64 w[kN], w_all = 0;
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
-              w[e] = i < s1 ? whole(r.kept(depth(x[e], r.M, r.inv), i + e - r.skip)) : 0;
+              const bool real = i + e >= r.skip && i + e < r.hi;
+              const float x = real ? Row<T>::value(r.base[i + e]) : -CUDART_INF_F;
+              w[e] = real ? whole(r.kept(depth(x, r.M, r.inv), i + e - r.skip)) : 0;
               w_all += w[e];
             }
             const u64 incl = at + warp_scan(w_all, lane);
             u64 run = incl - w_all;
-            if (run <= left && left < incl) {
 #pragma unroll
-              for (int e = 0; e < kN; ++e) {
-                if (run <= left && left < run + w[e]) a.tokens[row] = i + e - r.skip;
-                run += w[e];
-              }
+            for (int e = 0; e < kN; ++e) {
+              if (run <= left && left < run + w[e]) a.tokens[row] = i + e - r.skip;
+              run += w[e];
             }
             at = __shfl_sync(0xffffffffu, incl, 31);
-            if (at > left) break;
           }
         }
+        r.lo = min(s.piece * seg, r.end);
+        r.hi = min(r.lo + seg, r.end);
       }
     }
   }
   if (a.probs) {
     // W / S, W being floats: 1 / S as a float pair
-    const double inv = empty ? 0.0 : 1.0 / (double)total;
+    const double inv = 1.0 / (double)total;
     const float hi = (float)inv, lo = (float)(inv - (double)hi);
     const size_t out = (size_t)row * a.vocab;
-    for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) {
-      const int v = i - r.skip;
-      float w = 0.f;
-      if (!empty) {
-        const uint32_t d = depth(Row<T>::value(r.base[i]), r.M, r.inv);
-        if (r.inside(d, v)) w = (float)whole(r.kept(d, v));
-      }
+    auto put = [&](int v, float w) {
       const float q = fmaf(w, hi, w * lo);
       if (a.probs_dtype == PSKV_DTYPE_BF16)
         static_cast<__nv_bfloat16 *>(a.probs)[out + v] = __float2bfloat16_rn(q);
       else
         static_cast<float *>(a.probs)[out + v] = q;
+    };
+    for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) {
+      const int v = i - r.skip;
+      float w = 0.f;
+      if (!empty && !listed) {
+        const uint32_t d = depth(Row<T>::value(r.base[i]), r.M, r.inv);
+        if (r.inside(d, (uint32_t)v)) w = (float)whole(r.kept(d, v));
+      }
+      put(v, w);
+    }
+    __syncwarp();
+    for (int j = lane; j < listed; j += 32) {
+      const uint2 q = sh.all[j];
+      const int i = (int)q.y + r.skip;
+      if (i >= r.lo && i < r.hi) put((int)q.y, (float)whole(r.kept(q.x, (int)q.y)));
     }
   }
 }
