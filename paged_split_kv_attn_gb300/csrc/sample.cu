@@ -42,7 +42,7 @@ constexpr int kBins = 2048;
 constexpr int kList = 1024;      // listed tokens of a cluster
 constexpr int kEach = 8;         // elements a lane takes in a step
 constexpr int kStep = 32 * kEach;
-constexpr int kQueue = 32 + 4 * 32;
+constexpr float kSlack = 2.5e-4f;  // of an estimated sum: half a bin's width off in some of the likeliest tokens
 constexpr float kDeepest = 31.98f;        // what lies deeper has no weight: expf(-31.98) is under 2^-46
 constexpr uint32_t kDeep = 0x41ffd70au;   // its bits
 
@@ -65,7 +65,7 @@ struct Digits {
     lo = __float_as_uint(t2);
   }
 };
-__device__ __forceinline__ u64 whole(float w) {
+__device__ __forceinline__ u64 whole_weight(float w) {
   const Digits g(w);
   return ((u64)(g.hi - kTwelve) << 20) + (u64)(long long)(int)(g.lo - kTwelve);
 }
@@ -94,10 +94,12 @@ __device__ __forceinline__ u64 share(float x, u64 s) {
   return shift >= 128 ? 0 : (u64)(((unsigned __int128)s * m) >> shift);
 }
 
+// The sum of the lanes' numbers, by 24-bit digits.
 __device__ __forceinline__ u64 warp_sum(u64 x) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  return x;
+  const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)x & 0xffffffu);
+  const uint32_t b = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 24) & 0xffffffu);
+  const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 48));
+  return a + ((u64)b << 24) + ((u64)c << 48);
 }
 __device__ __forceinline__ u64 warp_scan(u64 x, int lane) {  // inclusive
 #pragma unroll
@@ -152,6 +154,40 @@ __device__ __forceinline__ void cluster_barrier() {
   cluster_wait();
 }
 
+// A level of bins.  The first: |x| to the nearest 1/64, up to 2,047; finer ones: |x|'s bits d in [lo, hi), bin
+// (d - lo) >> shift.
+struct Level {
+  uint32_t lo, hi;
+  int shift;  // -1: the first level
+  __device__ static int first_bin(uint32_t d) {
+    return (int)(__float_as_uint(__uint_as_float(d) + 131072.f) - 0x48000000u);  // (a last place of 1/64)
+  }
+  __device__ uint32_t begin(int b) const {
+    if (shift >= 0) return min((uint32_t)b << shift, hi - lo) + lo;
+    // halfway goes to the even bin
+    return b == 0 ? 0u : b == kBins ? kDeep + 1 : __float_as_uint(((float)b - 0.5f) * 0x1p-6f) + (b & 1);
+  }
+  // an estimate of a bin's weights: the middle's
+  __device__ float middle(int b) const {
+    return shift < 0 ? expf((float)b * -0x1p-6f) : weight(min(lo + ((uint32_t)b << shift) + ((1u << shift) >> 1), hi));
+  }
+};
+
+// Where the search for a border stands (the same in all CTAs; in shared memory, as the passes over the logits
+// need the registers).  Written by one thread between barriers.
+struct Search {
+  Level lv;
+  bool by_sum, counted;  // the border is one of weight, not of number; the level's counts are in
+  bool whole;            // from is 0: the list is to hold all of the first part
+  int first, last, tries;  // bins in question
+  int bin, bin_to;         // those taken
+  u64 limit, many;       // the border's sum or number, and its number within the level
+  u64 S;                 // the sum of the level's W
+  u64 skipped, before;   // tokens before the level's first bin, and before the taken ones
+  float e0, w, slack, e_before;  // the estimate looked for: e0 + w's share, give or take slack
+  uint32_t from, to;     // |x|'s bits of the taken bins
+};
+
 struct Shared {
   union {
     uint32_t hist[kBins];          // this CTA's counts
@@ -159,17 +195,15 @@ struct Shared {
   };
   uint32_t total[kBins];           // the cluster's counts
   uint2 list[kList];               // this CTA's listed tokens (|x|'s bits, index)
-  union {
-    u64 all_w[kList];              // W of `all`
-    float queue[kWarps][kQueue];   // |x| of tokens before the bin, before their weights are formed
-  };
+  u64 all_w[kList];                // W of `all`
   u64 post[2][3][kMaxPieces];      // what the pieces' warps told last, and before that
   uint32_t border[2];
   u64 scan_s[kWarps];
   uint32_t scan_n[kWarps];
   float scan_e[kWarps];
-  int listed, bin;
-  uint32_t before_n;
+  Search q;
+  int listed, hit;
+  uint32_t before_n, until_n;
   float before_e;
   uint32_t sub_n[kThreads], sub_hi[kThreads], sub_lo[kThreads];  // a list's bins: tokens, W by 20-bit digits
   int first_of[kMaxCluster + 1];   // where a CTA's listed tokens lie in `all`
@@ -185,7 +219,7 @@ struct Row {
   const T *base;
   int skip, end;
   int lo, hi;         // this warp's piece, whole vectors (but for the last one's end)
-  int per_chunk;      // steps of a chunk
+  int chunk_log;      // steps of a chunk: 2^chunk_log
   float chunk_top;    // lane c: the largest logit of chunk c
   float M, inv;
   uint32_t border;    // kept: |x| above the border's, or equal and index up to `last`
@@ -206,17 +240,20 @@ struct Row {
     const float w = weight(d);
     return w >= least ? w : 0.f;
   }
-  // A lane's vectors of the step at i0: raw, and what a guarded one could not read.
   // Logits of a step's elements [i0, b): those that are not the row's or behind b: -inf.
   __device__ void load(int i0, int b, int lane, float (&x)[kEach]) const {
+    if (i0 >= skip && i0 + kStep <= b) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(base + i0) + lane;
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int i = i0 + (32 * k + lane) * kN;
-      if (i >= skip && i + kN <= b) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(base + i));
+      for (int k = 0; k < kVecs; ++k) {
+        const uint4 q = __ldg(p + 32 * k);
 #pragma unroll
         for (int e = 0; e < kN; ++e) x[k * kN + e] = value(reinterpret_cast<const T *>(&q)[e]);
-      } else {
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const int i = i0 + (32 * k + lane) * kN;
 #pragma unroll
         for (int e = 0; e < kN; ++e)
           x[k * kN + e] = i + e >= skip && i + e < b ? value(base[i + e]) : -CUDART_INF_F;
@@ -228,11 +265,11 @@ struct Row {
 
   // The first step from s on whose chunk is alive.
   __device__ int next(int s, int steps, uint32_t alive) const {
-    while (s < steps && !((alive >> (s / per_chunk)) & 1u)) ++s;
+    while (s < steps && !((alive >> (s >> chunk_log)) & 1u)) ++s;
     return s;
   }
-  // f(logit, index) for this piece's elements in live chunks, one step's loads ahead; g(whether the step is
-  // done) after every four.
+  // f(logit, index) for this piece's elements in live chunks, one step's loads ahead; g(its place) after each
+  // step.
   template <typename F, typename G>
   __device__ void each(uint32_t alive, int lane, F f, G g) const {
     const int steps = (hi - lo + kStep - 1) / kStep;
@@ -246,33 +283,12 @@ struct Row {
       s = next(s + 1, steps, alive);
       if (s < steps) load(lo + s * kStep, hi, lane, y);
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        f(x[j], index(at, j, lane));
-        if (j % 4 == 3) g(j == kEach - 1);
-      }
+      for (int j = 0; j < kEach; ++j) f(x[j], index(at, j, lane));
+      g(at);
     }
   }
   // The chunks that have tokens with |x|'s bits below d.
   __device__ uint32_t alive(uint32_t d) const { return __ballot_sync(0xffffffffu, depth(chunk_top, M, inv) < d); }
-};
-
-// A level of bins.  The first: |x| to the nearest 1/64, up to 2,047; finer ones: |x|'s bits d in [lo, hi), bin
-// (d - lo) >> shift.
-struct Level {
-  uint32_t lo, hi;
-  int shift;  // -1: the first level
-  __device__ static int first_bin(uint32_t d) {
-    return (int)(__float_as_uint(__uint_as_float(d) + 131072.f) - 0x48000000u);  // (a last place of 1/64)
-  }
-  __device__ uint32_t begin(int b) const {
-    if (shift >= 0) return min((uint32_t)b << shift, hi - lo) + lo;
-    // halfway goes to the even bin
-    return b == 0 ? 0u : b == kBins ? kDeep + 1 : __float_as_uint(((float)b - 0.5f) * 0x1p-6f) + (b & 1);
-  }
-  // an estimate of a bin's weights: the middle's
-  __device__ float middle(int b) const {
-    return shift < 0 ? expf((float)b * -0x1p-6f) : weight(min(lo + ((uint32_t)b << shift) + ((1u << shift) >> 1), hi));
-  }
 };
 
 template <typename T>
@@ -282,7 +298,7 @@ struct Sampler {
   Row<T> r;
   int cluster, rank, warp, lane, piece, pieces;
   int turn = 0;  // exchanges so far: their buffers alternate
-  bool coarse = true;  // sh.total has the first level's counts
+  bool counted = true;  // sh.total has the first level's counts
 
   // Tell the cluster up to three numbers of this piece; afterwards all of them are in post.
   template <int kNumbers>
@@ -318,22 +334,26 @@ struct Sampler {
     cluster_barrier();
   }
 
-  // The bin at which the running count reaches `many`, or (by_sum) the running estimate e0 + w times all bins'
-  // estimate over `all_w`; within [first, last].  sh.before_n and sh.before_e: what lies before it.
-  __device__ int seek(const Level &lv, bool by_sum, u64 many, float e0, float w, u64 all_w, int first, int last) {
+  // Takes the bins that may hold the border: the one at which the running count reaches q.many, or (by_sum) those at
+  // which the running estimate may pass q.e0 + q.w's share of all bins' (S), give or take q.slack of it.
+  __device__ void seek() {
+    Search &q = sh.q;
     constexpr int kMine = kBins / kThreads;
     const int b0 = threadIdx.x * kMine;
-    uint32_t n[kMine], n_all = 0;
-    float m[kMine], e_all = 0.f;
+    const bool by_sum = q.by_sum;
+    uint32_t n[kMine], n_run = 0;
+    float m[kMine], e_run = 0.f;  // (by number: the counts, below 2^23)
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) n[k] = sh.total[b0 + k];
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
-      n[k] = sh.total[b0 + k];
-      m[k] = n[k] ? (float)n[k] * lv.middle(b0 + k) : 0.f;
-      n_all += n[k];
-      e_all += m[k];
+      m[k] = (float)n[k];
+      if (by_sum && n[k]) m[k] *= q.lv.middle(b0 + k);
+      n_run += n[k];
+      e_run += m[k];
     }
-    uint32_t n_run = n_all;
-    float e_run = e_all;
+    const uint32_t n_all = n_run;
+    const float e_all = e_run;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, n_run, d);
@@ -341,7 +361,9 @@ struct Sampler {
       if (lane >= d) n_run += y, e_run += z;
     }
     if (lane == 31) sh.scan_n[warp] = n_run, sh.scan_e[warp] = e_run;
-    if (threadIdx.x == 0) sh.bin = last;
+    // (after some wrong guesses by halves)
+    const int first = q.tries < 5 ? q.first : (q.first + q.last) / 2, last = q.tries < 5 ? q.last : first;
+    if (threadIdx.x == 0) q.bin = q.bin_to = last;
     __syncthreads();
     n_run -= n_all;
     e_run -= e_all;
@@ -351,46 +373,42 @@ struct Sampler {
       if (k < warp) n_run += sh.scan_n[k], e_run += sh.scan_e[k];
       everything += sh.scan_e[k];
     }
-    const float e = e0 + w * (everything / (float)all_w);
-    const uint32_t n_at = n_run;
-    const float e_at = e_run;
+    float e = (float)q.many, slack = 0.f;
+    if (by_sum) {
+      e = q.e0 + q.w * (everything / (float)q.S);
+      slack = e * q.slack;
+    }
+    float run = e_run;
+    int low = kBins, high = kBins;
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
-      n_run += n[k];
-      e_run += m[k];
-      if (n[k] && (by_sum ? e_run >= e : n_run >= many)) {
-        atomicMin(&sh.bin, max(b0 + k, first));
-        break;
+      run += m[k];
+      if (n[k] && run >= e - slack) low = min(low, b0 + k);
+      if (n[k] && run >= e + slack) high = min(high, b0 + k);
+    }
+    if (low < kBins) atomicMin(&q.bin, max(low, first));
+    if (high < kBins) atomicMin(&q.bin_to, max(high, first));
+    __syncthreads();
+    const int bin = q.bin - b0, bin_to = q.bin_to - b0;
+    if ((uint32_t)bin < kMine || (uint32_t)bin_to < kMine)
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        if (k == bin) sh.before_n = n_run, sh.before_e = e_run;
+        n_run += n[k];
+        e_run += m[k];
+        if (k == bin_to) sh.until_n = n_run;
       }
-    }
     __syncthreads();
-    const int bin = sh.bin;
-    n_run = n_at;
-    e_run = e_at;
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      if (b0 + k == bin) sh.before_n = n_run, sh.before_e = e_run;
-      n_run += n[k];
-      e_run += m[k];
-    }
-    __syncthreads();
-    return bin;
   }
 
   // ---- lists
 
-  // Append this piece's tokens with |x|'s bits in [from, to), inside the border, to the CTA's list.
-  __device__ void append(uint32_t d, int v) {
-    const int at = atomicAdd(&sh.listed, 1);
-    if (at < kList) sh.list[at] = make_uint2(d, (uint32_t)v);
-  }
-
-  // All CTAs' lists in one (number 2 of the last exchange: each piece's tokens): returns how many.
+  // All CTAs' lists in one (number 1 of the last exchange: each piece's tokens): returns how many.
   __device__ int gather() {
     int n = 0, incl;
     if (lane < cluster)
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) n += (int)posted(2, lane * kWarps + i);
+      for (int i = 0; i < kWarps; ++i) n += (int)posted(1, lane * kWarps + i);
     incl = n;
 #pragma unroll
     for (int d = 1; d < kMaxCluster; d <<= 1) {
@@ -408,7 +426,7 @@ struct Sampler {
         while (c + 1 < cluster && sh.first_of[c + 1] <= i) ++c;
         const uint2 q = load_remote(remote(&sh.list[i - sh.first_of[c]], c));
         sh.all[i] = q;
-        sh.all_w[i] = whole(weight(q.x));
+        sh.all_w[i] = whole_weight(weight(q.x));
       }
     }
     __syncthreads();
@@ -416,10 +434,11 @@ struct Sampler {
   }
 
   // Of the list's n tokens that lie inside the border (and weigh `least`), in their order (or by index), the one at
-  // which their running number (or the sum of their W) reaches `target`.  base: what the sum begins with; `with`:
-  // the sum up to that token, it included (by number: left as it is).  [lo, lo + 2^bits): where its key lies.
+  // which their running number (or the sum of their W) reaches `target`.  base: the number (sum) before those with
+  // key lo; `with`: the sum up to that token, it included (by number: left as it is).  [lo, lo + 2^bits): where its
+  // key lies; bits -1: anywhere, by |x| in steps of 1/8 first.
   __device__ uint2 pick(int n, bool by_index, bool by_sum, u64 target, u64 base, uint32_t lo, int bits, u64 &with) {
-    u64 before_n = 0, before_s = base;
+    u64 before_n = by_sum ? 0 : base, before_s = by_sum ? base : 0;
     uint32_t fixed = 0;      // |x|'s bits, once these are down to one value
     bool on_v = by_index, tied = false;
     auto in = [&](int i, uint2 &q, uint32_t &key) {
@@ -427,6 +446,8 @@ struct Sampler {
       key = on_v ? q.y : q.x;
       return r.inside(q.x, q.y) && (!tied || q.x == fixed) && !(r.least > 0.f && weight(q.x) < r.least);
     };
+    bool eighths = bits < 0;
+    uint32_t width;          // of the last level's bin
     int shift = max(0, bits - 8);
     for (;;) {
       sh.sub_n[threadIdx.x] = sh.sub_hi[threadIdx.x] = sh.sub_lo[threadIdx.x] = 0;
@@ -435,8 +456,8 @@ struct Sampler {
       for (int i = threadIdx.x; i < n; i += kThreads) {
         uint2 q;
         uint32_t key;
-        if (in(i, q, key) && key - lo < (256u << shift)) {
-          const uint32_t b = (key - lo) >> shift;
+        if (in(i, q, key) && (eighths || key - lo < (256u << shift))) {
+          const uint32_t b = eighths ? (uint32_t)(__uint_as_float(key) * 8.f) : (key - lo) >> shift;
           atomicAdd(&sh.sub_n[b], 1u);
           if (by_sum) {  // (64-bit atomics on one word hold each other up; a digit's sums stay below 2^31)
             atomicAdd(&sh.sub_hi[b], (uint32_t)(sh.all_w[i] >> 20));
@@ -469,7 +490,15 @@ struct Sampler {
       const int count = (int)sh.sub_count;
       before_n += sh.sub_before_n;
       before_s = sh.sub_before_s;
-      lo += (uint32_t)sh.sub_bin << shift;
+      if (eighths) {
+        lo = __float_as_uint((float)sh.sub_bin * 0.125f);
+        width = __float_as_uint((float)(sh.sub_bin + 1) * 0.125f) - lo;
+        shift = 32 - __clz((int)(width - 1));
+        eighths = false;
+      } else {
+        lo += (uint32_t)sh.sub_bin << shift;
+        width = 1u << shift;
+      }
       if (count <= 32) break;
       if (shift == 0) {  // many of one |x|: by index
         fixed = lo;
@@ -485,7 +514,7 @@ struct Sampler {
     for (int i = threadIdx.x; i < n; i += kThreads) {
       uint2 q;
       uint32_t key;
-      if (in(i, q, key) && key - lo < (1u << shift)) sh.few[atomicAdd(&sh.few_n, 1) & 31] = i;
+      if (in(i, q, key) && key - lo < width) sh.few[atomicAdd(&sh.few_n, 1) & 31] = i;
     }
     __syncthreads();
     const int count = min(sh.few_n, 32), mine = lane < count ? sh.few[lane] : 0;
@@ -506,17 +535,18 @@ struct Sampler {
     return found;
   }
 
-  // The sum of W of the list's tokens that lie inside the border (and weigh `least`), and of this piece's alone.
-  __device__ u64 list_sum(int n, u64 &mine) {
+  // The sum of W of the list's tokens that lie inside the border (and weigh `least`); part: of those with |x|'s bits
+  // below d, or (d 0) of this piece's.
+  __device__ u64 list_sum(int n, uint32_t d, u64 &part) {
     u64 x = 0, y = 0;
     for (int j = lane; j < n; j += 32) {
       const uint2 q = sh.all[j];
       if (!r.inside(q.x, q.y) || (r.least > 0.f && weight(q.x) < r.least)) continue;
       const int at = (int)q.y + r.skip;
       x += sh.all_w[j];
-      if (at >= r.lo && at < r.hi) y += sh.all_w[j];
+      if (d ? q.x < d : at >= r.lo && at < r.hi) y += sh.all_w[j];
     }
-    mine = warp_sum(y);
+    part = warp_sum(y);
     return warp_sum(x);
   }
 
@@ -542,116 +572,174 @@ struct Sampler {
     r.last = sh.border[1];
   }
 
-  // The level's counts, of the tokens with |x|'s bits in [from, to).
-  __device__ void count(const Level &lv, uint32_t from, uint32_t to) {
+  // The counts of q's level, of the tokens with |x|'s bits in [from, to).
+  __device__ void count() {
     for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
     __syncthreads();
+    const uint32_t from = sh.q.from, to = sh.q.to;
+    const int shift = sh.q.lv.shift;
     r.each(r.alive(to), lane, [&](float l, int) {
       const uint32_t d = depth(l, r.M, r.inv);
-      if (d - from < to - from) {
-        const int b = lv.shift < 0 ? Level::first_bin(d) : (int)((d - from) >> lv.shift);
-        atomicAdd(&sh.hist[b], 1u);
-      }
-    }, [](bool) {});
+      if (d - from < to - from) atomicAdd(&sh.hist[shift < 0 ? Level::first_bin(d) : (int)((d - from) >> shift)], 1u);
+    }, [](int) {});
     cluster_barrier();
     add_up();
   }
 
   // Move the border to the last token of the order's first part: the `limit` first ones (by_sum false), or the
   // shortest part whose W sum to `limit` at least (1 .. their sum); S: the sum of all W.  sum: that part's, mine:
-  // this piece's share of it.  Returns how many tokens are listed when the list holds all of that part (sum and
-  // mine then say nothing where the border is not moved), else 0.
-  __device__ int find_border(bool by_sum, u64 limit, u64 S, u64 &sum, u64 &mine) {
-    Level lv{0u, 0u, -1};
-    int first = 0, last = kBins - 1, tries = 0;
-    if (!coarse) count(lv, 0u, kDeep + 1);
-    coarse = true;
-    int bin = seek(lv, by_sum, limit, 0.f, (float)limit, S, first, last);
-    u64 skipped = 0;  // tokens before the level's first bin
-    for (;;) {
-      if (!by_sum && lv.shift < 0 && bin == kBins - 1) return 0;  // nothing with weight is left out
-      const uint32_t to = lv.begin(bin + 1);
-      const u64 before = skipped + sh.before_n;
-      const float e_before = sh.before_e;
-      // the whole first part is listed where it fits
-      const bool whole_part = before + sh.total[bin] <= kList;
-      const uint32_t from = whole_part ? 0u : lv.begin(bin);
-      // ---- exact sums, and the bin's tokens
-      if (threadIdx.x == 0) sh.listed = 0;
+  // this piece's share of it.  listed: how many tokens are listed where the list holds all that lies inside the
+  // border, else 0, before and after.  Where nothing with weight would be left out the border, sum and mine stay.
+  // (One loop with each step in it once: the code is long, and it is fetched from memory when a call is the first.)
+  __device__ void find_border(bool by_sum, u64 limit, u64 S, u64 &sum, u64 &mine, int &listed) {
+    Search &q = sh.q;
+    const bool lead = threadIdx.x == 0;
+    u64 A = 0, above_here = 0;
+    uint32_t lo = 0;
+    int bits = -1;
+    u64 start = 0;
+    if (!listed) {
+      if (lead) {
+        q.lv = Level{0u, 0u, -1};
+        q.by_sum = by_sum;
+        q.counted = counted;
+        q.first = q.tries = 0;
+        q.last = kBins - 1;
+        q.limit = q.many = limit;
+        q.S = S;
+        q.skipped = 0;
+        q.e0 = 0.f;
+        q.w = (float)limit;
+        q.slack = kSlack;
+        q.from = 0;
+        q.to = kDeep + 1;
+      }
+      counted = true;
       __syncthreads();
-      Sum above, within;
-      uint32_t n = 0;
-      int queued = 0;
-      float *queue = sh.queue[warp];
-      r.each(r.alive(to), lane, [&](float l, int v) {
-        const float x = depth_of(l, r.M, r.inv);
-        const uint32_t d = __float_as_uint(x);
-        // tokens before the bin are packed first: mostly few of a warp's are
-        const uint32_t who = __ballot_sync(0xffffffffu, d < from);
-        if (d < from) queue[queued + __popc(who & ((1u << lane) - 1))] = x;
-        queued += __popc(who);
-        if (d - from < to - from && r.inside(d, (uint32_t)v)) {
-          within.add(weight(d));
-          ++n;
-          append(d, v);
-        }
-      }, [&](bool) {
-        __syncwarp();
-        while (queued >= 32) above.add(expf(-queue[(queued -= 32) + lane]));
-        __syncwarp();
-        above.carry();
-        within.carry();
-      });
-      if (lane < queued) above.add(expf(-queue[lane]));
-      above.carry();
-      const u64 above_here = warp_sum(above.total), here = __reduce_add_sync(0xffffffffu, n);
-      exchange<3>(above_here, warp_sum(within.total), here);
-      const u64 A = told(0), B = told(1), N = told(2);
-      if (by_sum && !(A < limit && limit <= A + B)) {
-        // the estimate was off: on from the exact sum, after some tries by halves
-        if (A >= limit)
-          last = bin - 1;
-        else
-          first = bin + 1;
-        if (first > last) return 0;  // (cannot be)
-        if (++tries < 5) {
-          // (of a whole part the sum ends at the bin's end)
-          const float off = A >= limit ? -(float)(A - limit) : whole_part ? (float)(limit - B) : (float)(limit - A);
-          bin = seek(lv, true, 0, e_before, off, S, first, last);
-        } else {
-          const int middle = (first + last) / 2;
-          bin = seek(lv, true, 0, 0.f, 0.f, S, middle, middle);
-        }
+    }
+    while (!listed) {
+      if (!q.counted) count();
+      seek();
+      if (!q.by_sum && q.lv.shift < 0 && q.bin == kBins - 1) return;
+      // the whole first part is listed where it fits
+      const bool whole = q.skipped + sh.until_n <= kList;
+      const uint32_t begin = q.lv.begin(q.bin), from = whole ? 0u : begin, to = q.lv.begin(q.bin_to + 1);
+      if (!whole && q.bin < q.bin_to && sh.until_n - sh.before_n > kList && q.slack > 0.f) {
+        __syncthreads();
+        if (lead) q.counted = true, q.slack = 0.f;
+        __syncthreads();
         continue;
       }
+      if (lead) {
+        q.counted = true;
+        q.whole = whole;
+        q.before = q.skipped + sh.before_n;
+        q.e_before = sh.before_e;
+        q.from = from;
+        q.to = to;
+        sh.listed = 0;
+      }
+      __syncthreads();
+      // ---- the exact sum of what lies before the bins, and their tokens
+      Sum above;
+      uint32_t n = 0, marked = 0;  // bit j: element j of the lane's step is to be listed
+      int j = 0;
+      r.each(r.alive(to), lane, [&](float l, int) {
+        const uint32_t d = depth(l, r.M, r.inv);
+        if (from) {  // (without a branch on d: in most warps some lane has a token before the bins)
+          const float w = weight(d);
+          above.add(d < from ? w : 0.f);
+        }
+        marked |= (uint32_t)(d - from < to - from) << j++;
+      }, [&](int at) {
+        above.carry();
+        j = 0;
+        while (marked) {
+          const int v = r.index(at, __ffs(marked) - 1, lane);
+          marked &= marked - 1;
+          const uint32_t d = depth(Row<T>::value(r.base[v + r.skip]), r.M, r.inv);
+          if (!r.inside(d, (uint32_t)v)) continue;
+          ++n;
+          const int place = atomicAdd(&sh.listed, 1);
+          if (place < kList) sh.list[place] = make_uint2(d, (uint32_t)v);
+        }
+        __syncwarp();
+      });
+      above_here = warp_sum(above.total);
+      const uint32_t here = __reduce_add_sync(0xffffffffu, n);
+      exchange<2>(above_here, (u64)here);
+      A = told(0);
+      const u64 N = told(1), N_before = told_before(1);
+      // ---- their own sum
+      int in_list = 0;
+      u64 B = 0;
       if (N <= kList) {
-        const int listed = gather();
-        const uint2 b = pick(listed, false, by_sum, by_sum ? limit : limit - (whole_part ? 0 : before), A, from,
-                             32 - __clz((int)(to - from - 1) | 255), sum);
-        r.border = b.x;
-        r.last = b.y;
-        sum = A + list_sum(listed, mine);
-        mine += above_here;
-        return whole_part ? listed : 0;
+        in_list = gather();
+        if (q.by_sum) B = list_sum(in_list, begin, mine);
+      } else if (q.by_sum) {
+        Sum within;
+        r.each(r.alive(to), lane, [&](float l, int v) {
+          const uint32_t d = depth(l, r.M, r.inv);
+          within.add(d - from < to - from && r.inside(d, (uint32_t)v) ? weight(d) : 0.f);
+        }, [&](int) { within.carry(); });
+        exchange<1>(warp_sum(within.total));
+        B = told(0);
       }
-      if (to - from == 1) {
-        const u64 w = whole(weight(from)), ties = by_sum ? (limit - A + w - 1) / w : limit - before;
-        const u64 N_before = told_before(2);
-        rank_ties(from, ties, N_before, here);
-        sum = A + ties * w;
-        mine = above_here + (ties > N_before ? min(ties - N_before, here) : 0) * w;
-        return 0;
+      const bool low = q.by_sum && A >= q.limit, high = q.by_sum && A + B < q.limit;
+      const bool ties = !low && !high && N > kList && to - from == 1;
+      if (ties) {
+        const u64 W = whole_weight(weight(from)), stay = q.by_sum ? (q.limit - A + W - 1) / W : q.limit - q.before;
+        rank_ties(from, stay, N_before, here);
+        sum = A + stay * W;
+        mine = above_here + (stay > N_before ? min(stay - N_before, (u64)here) : 0) * W;
+        counted = q.lv.shift < 0;
+        return;
       }
-      // ---- finer bins
-      skipped = before;
-      lv = Level{from, to, max(0, 21 - __clz((int)(to - from - 1)))};
-      coarse = false;
-      count(lv, from, to);
-      first = tries = 0;
-      last = (int)((to - 1 - from) >> lv.shift);
-      S = B > 0 ? B : 1;  // (without what top-k left out: a first guess that this puts off is tried again)
-      bin = seek(lv, by_sum, limit - skipped, 0.f, by_sum ? (float)(limit - A) : 0.f, S, first, last);
+      __syncthreads();
+      if (low || high) {
+        // the estimate was off: on from the exact sum (of a whole part: at its end)
+        if (lead) {
+          if (low)
+            q.last = max(q.bin - 1, 0);
+          else
+            q.first = min(q.bin_to + 1, kBins - 1);
+          q.e0 = q.e_before;
+          q.w = low ? -(float)(A - q.limit) : (float)(q.limit - (q.whole ? B : A));
+          q.slack = kSlack;
+          ++q.tries;
+        }
+      } else if (N <= kList) {
+        listed = in_list;
+        // (by number: what lies before the bins is counted; by weight: `mine` is its sum)
+        const u64 base = q.by_sum ? A + (begin ? mine : 0) : 0;
+        if (base < limit) {
+          lo = begin;
+          bits = 32 - __clz((int)(to - begin - 1) | 255);
+          start = q.by_sum ? base : q.before;
+        }
+      } else if (lead) {
+        // finer bins
+        q.skipped = q.before;
+        q.lv = Level{from, to, max(0, 21 - __clz((int)(to - from - 1)))};
+        q.counted = false;
+        q.first = q.tries = 0;
+        q.last = (int)((to - 1 - from) >> q.lv.shift);
+        q.many = q.limit - q.before;
+        q.e0 = 0.f;
+        q.w = q.by_sum ? (float)(q.limit - A) : 0.f;
+        q.S = B > 0 ? B : 1;  // (without what top-k left out: a first guess that this puts off is tried again)
+        q.slack = kSlack;
+      }
+      __syncthreads();
+      counted = q.lv.shift < 0;
+      if (q.tries > 40) return;  // (never)
     }
+    const uint2 b = pick(listed, false, by_sum, limit, start, lo, bits, sum);
+    r.border = b.x;
+    r.last = b.y;
+    sum = A + list_sum(listed, 0u, mine);
+    mine += above_here;
+    if (!q.whole) listed = 0;
   }
 };
 
@@ -681,29 +769,22 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   const int seg = ((r.end + s.pieces - 1) / s.pieces + kN - 1) / kN * kN;
   r.lo = min(s.piece * seg, r.end);
   r.hi = min(r.lo + seg, r.end);
-  r.per_chunk = max(1, (seg + 32 * kStep - 1) / (32 * kStep));
+  r.chunk_log = max(0, 32 - __clz(max(seg - 1, 0) / (32 * kStep)));  // at most 32 chunks
   const int req = row / a.per_request;
   float heat = a.temperature ? a.temperature[req] : 1.f, p = a.top_p ? a.top_p[req] : 1.f;
   float least = a.min_p ? a.min_p[req] : 0.f;
   int k = a.top_k ? a.top_k[req] : 0;
-  const float u = a.u ? a.u[row] : 0.f;
   // ---- M
   r.chunk_top = -CUDART_INF_F;
   {
     float chunk = -CUDART_INF_F;
-    int left = r.per_chunk, c = 0;
-    r.each(~0u, lane, [&](float x, int) { chunk = fmaxf(chunk, x); }, [&](bool done) {
-      if (!done || --left > 0) return;
+    r.each(~0u, lane, [&](float x, int) { chunk = fmaxf(chunk, x); }, [&](int at) {
+      const int step = (at - r.lo) / kStep + 1;
+      if (step & ((1 << r.chunk_log) - 1) && at + kStep < r.hi) return;
       chunk = warp_max(chunk);
-      if (lane == c) r.chunk_top = chunk;
+      if (lane == (step - 1) >> r.chunk_log) r.chunk_top = chunk;
       chunk = -CUDART_INF_F;
-      left = r.per_chunk;
-      ++c;
     });
-    if (left < r.per_chunk) {
-      chunk = warp_max(chunk);
-      if (lane == c) r.chunk_top = chunk;
-    }
   }
   float top = warp_max(r.chunk_top);
   __syncwarp();
@@ -738,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     // ---- the likeliest token, the lowest index of M
     r.inv = endless ? CUDART_INF_F : 1.f;
     uint32_t at = UINT_MAX;
-    r.each(r.alive(1u), lane, [&](float x, int v) { at = x == top ? min(at, (uint32_t)v) : at; }, [](bool) {});
+    r.each(r.alive(1u), lane, [&](float x, int v) { at = x == top ? min(at, (uint32_t)v) : at; }, [](int) {});
     s.template exchange<1>((u64)__reduce_min_sync(0xffffffffu, at));
     const u64 *ats = sh.post[1][0];
     if (lane < s.pieces) at = min(at, (uint32_t)ats[lane]);
@@ -766,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
       } else {
         all.add(w >= r.least ? w : 0.f);
       }
-    }, [&](bool done) { if (done) all.carry(); });
+    }, [&](int) { all.carry(); });
     u64 mine = warp_sum(all.total);
     s.template exchange<1>(mine);
     total = s.told(0);
@@ -775,25 +856,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
       const u64 S = total;
       const float least_w = r.least;  // (min_p comes last)
       r.least = 0.f;
-      if (some) listed = s.find_border(false, (u64)k, S, total, mine);
-      if (part) {
-        const u64 limit = max(share(p, total), 1ull);
-        if (listed) {
-          const uint2 b = s.pick(listed, false, true, limit, 0, 0u, 31, total);
-          r.border = b.x;
-          r.last = b.y;
-        } else {
-          listed = s.find_border(true, limit, S, total, mine);
-        }
-      }
+#pragma unroll 1
+      for (int by_sum = some ? 0 : 1; by_sum < (part ? 2 : 1); ++by_sum)
+        s.find_border(by_sum, by_sum ? max(share(p, total), 1ull) : (u64)k, S, total, mine, listed);
       r.least = least_w;
       if (listed) {
-        if (r.least > 0.f) total = s.list_sum(listed, mine);
+        if (r.least > 0.f) total = s.list_sum(listed, 0u, mine);
       } else {
         if (r.least > 0.f) {
           Sum kept;
           r.each(r.alive(r.border + 1), lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); },
-                 [&](bool done) { if (done) kept.carry(); });
+                 [&](int) { kept.carry(); });
           mine = warp_sum(kept.total);
         }
         s.template exchange<1>(mine);
@@ -801,21 +874,22 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
       }
     }
     // ---- the draw: where the running sum passes u's share
+    const float u = a.u ? a.u[row] : 0.f;
     const u64 thr = u >= 1.f ? total - 1 : share(u, total);
     if (a.tokens && listed) {
       u64 with;
-      const uint2 t = s.pick(listed, true, true, thr + 1, 0, 0u, 22, with);
+      const uint2 t = s.pick(listed, true, true, thr + 1, 0, 0u, 32 - __clz((a.vocab - 1) | 255), with);
       if (s.rank == 0 && threadIdx.x == 0) a.tokens[row] = (int)t.y;
     } else if (a.tokens) {
       const u64 before = s.told_before(0);
-      if (threadIdx.x == 0) sh.bin = -1;
+      if (threadIdx.x == 0) sh.hit = -1;
       __syncthreads();
       if (lane == 0 && before <= thr && thr < before + mine) {
-        sh.bin = s.piece;
+        sh.hit = s.piece;
         sh.sub_before_s = thr - before;
       }
       __syncthreads();
-      const int hit = sh.bin;
+      const int hit = sh.hit;
       if (hit >= 0) {
         // its CTA: an eighth a warp
         const u64 left = sh.sub_before_s;
@@ -823,9 +897,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
         const int sub = ((p1 - p0 + kWarps - 1) / kWarps + kN - 1) / kN * kN;
         r.lo = min(p0 + warp * sub, p1);
         r.hi = min(r.lo + sub, p1);
-        r.per_chunk = INT_MAX;
+        r.chunk_log = 30;
         Sum kept;
-        r.each(1u, lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); }, [&](bool done) { if (done) kept.carry(); });
+        r.each(1u, lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); }, [&](int) { kept.carry(); });
         const u64 own = warp_sum(kept.total);
         if (lane == 0) sh.scan_s[warp] = own;
         __syncthreads();
@@ -839,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
             for (int e = 0; e < kN; ++e) {
               const bool real = i + e >= r.skip && i + e < r.hi;
               const float x = real ? Row<T>::value(r.base[i + e]) : -CUDART_INF_F;
-              w[e] = real ? whole(r.kept(depth(x, r.M, r.inv), i + e - r.skip)) : 0;
+              w[e] = real ? whole_weight(r.kept(depth(x, r.M, r.inv), i + e - r.skip)) : 0;
               w_all += w[e];
             }
             const u64 incl = at + warp_scan(w_all, lane);
@@ -874,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
       float w = 0.f;
       if (!empty && !listed) {
         const uint32_t d = depth(Row<T>::value(r.base[i]), r.M, r.inv);
-        if (r.inside(d, (uint32_t)v)) w = (float)whole(r.kept(d, v));
+        if (r.inside(d, (uint32_t)v)) w = (float)whole_weight(r.kept(d, v));
       }
       put(v, w);
     }
@@ -882,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     for (int j = lane; j < listed; j += 32) {
       const uint2 q = sh.all[j];
       const int i = (int)q.y + r.skip;
-      if (i >= r.lo && i < r.hi) put((int)q.y, (float)whole(r.kept(q.x, (int)q.y)));
+      if (i >= r.lo && i < r.hi) put((int)q.y, (float)whole_weight(r.kept(q.x, (int)q.y)));
     }
   }
 }
