@@ -11,15 +11,16 @@
 //   1  M, and the largest logit of each of a piece's 32 chunks: later passes leave out chunks below what they look for
 //   2  the sum of W, and a histogram of |x| in steps of 1/64 (counts: a shared-memory atomic a token,
 //      beside the exponentials)
-//   3  the bin that holds the border: by the counts (top-k), or by the bins' estimated weight (top-p).
-//      If all tokens up to that bin's end fit in a list, they are listed, and all that is left
-//      (top-k's border, top-p's, the draw) is found in the list by every CTA for itself.  Else the pass
-//      sums W exactly over what lies before the bin and lists the bin alone; an estimate that was off shows in the
-//      exact sum, and another bin is tried from there.  A bin that does not fit is cut into
-//      2,048 finer ones, down to a single |x|, whose tokens' border is a matter of counting
-//   4  the drawn token's piece again, and the probabilities where they are asked for.
+//   3  the bin that holds the border: by the counts (top-k), or by the bins' estimated weight (top-p); each CTA
+//      looks through a share of the bins.  The pass sums W exactly over what lies before the bin and lists the
+//      bin's own tokens; or, where they are few enough, all tokens up to the bin's end.  An estimate that was off
+//      shows in the exact sums, and another bin is tried from there.  A bin that does not fit the list is
+//      cut into 2,048 finer ones, down to a single |x|, whose tokens' border is a matter of counting.
+//      The listed tokens go to the first CTA, which finds the border among them (256 bins of a token's key at a
+//      time: |x|'s bits, then the index).  Where they are all that is kept, it finds top-p's border and draws
+//      from them, too, and the other CTAs are done
+//   4  else the drawn token's piece again; and the probabilities where they are asked for.
 // Between passes the warps' results cross the cluster through distributed shared memory, one barrier each.
-// A token in a list is found by 256 bins of its key (|x|'s bits, then the index) at a time.
 #include <float.h>
 #include <limits.h>
 #include <math_constants.h>
@@ -39,7 +40,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxPieces = kMaxCluster * kWarps;
 constexpr int kPerSm = 4;        // CTAs an SM holds (registers)
 constexpr int kBins = 2048;
-constexpr int kList = 1024;      // listed tokens of a cluster
+constexpr int kList = 1024;      // listed tokens of a cluster,
+constexpr int kWarpList = kList / kWarps;  // and of a warp
 constexpr int kEach = 8;         // elements a lane takes in a step
 constexpr int kStep = 32 * kEach;
 constexpr float kSlack = 2.5e-4f;  // of an estimated sum: half a bin's width off in some of the likeliest tokens
@@ -129,17 +131,9 @@ __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
 __device__ __forceinline__ void store_remote(uint32_t at, u64 x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
-__device__ __forceinline__ void store_remote(uint32_t at, uint32_t x) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
-}
-__device__ __forceinline__ uint32_t load_remote_word(uint32_t at) {
+__device__ __forceinline__ uint32_t load_remote(uint32_t at) {
   uint32_t x;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-  return x;
-}
-__device__ __forceinline__ uint2 load_remote(uint32_t at) {
-  uint2 x;
-  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
   return x;
 }
 __device__ __forceinline__ void cluster_arrive_started() {  // nothing written yet: no release
@@ -159,17 +153,21 @@ __device__ __forceinline__ void cluster_barrier() {
 struct Level {
   uint32_t lo, hi;
   int shift;  // -1: the first level
-  __device__ static int first_bin(uint32_t d) {
-    return (int)(__float_as_uint(__uint_as_float(d) + 131072.f) - 0x48000000u);  // (a last place of 1/64)
+  __device__ int bin(uint32_t d) const {
+    // (a float add whose last place is 1/64)
+    return shift < 0 ? (int)(__float_as_uint(__uint_as_float(d) + 131072.f) - 0x48000000u) : (int)((d - lo) >> shift);
   }
   __device__ uint32_t begin(int b) const {
     if (shift >= 0) return min((uint32_t)b << shift, hi - lo) + lo;
     // halfway goes to the even bin
     return b == 0 ? 0u : b == kBins ? kDeep + 1 : __float_as_uint(((float)b - 0.5f) * 0x1p-6f) + (b & 1);
   }
-  // an estimate of a bin's weights: the middle's
-  __device__ float middle(int b) const {
-    return shift < 0 ? expf((float)b * -0x1p-6f) : weight(min(lo + ((uint32_t)b << shift) + ((1u << shift) >> 1), hi));
+  // an estimate of n weights of a bin, in units of 2^-20: the middle's.  (Whole numbers: running sums that do not
+  // depend on their order go up from bin to bin, whoever forms them.)
+  __device__ u64 estimate(int b, uint32_t n) const {
+    const float x = shift < 0 ? (float)b * 0x1p-6f
+                              : __uint_as_float(min(lo + ((uint32_t)b << shift) + ((1u << shift) >> 1), hi));
+    return n ? __float2ull_rn((float)n * expf(-x) * 0x1p20f) : 0;
   }
 };
 
@@ -177,37 +175,37 @@ struct Level {
 // need the registers).  Written by one thread between barriers.
 struct Search {
   Level lv;
-  bool by_sum, counted;  // the border is one of weight, not of number; the level's counts are in
-  bool whole;            // from is 0: the list is to hold all of the first part
+  bool by_sum;             // the border is one of weight, not of number
+  bool counted, reduced;   // the level's counts are in, and its shares added up
+  bool whole;              // the list is to hold all of the first part
   int first, last, tries;  // bins in question
-  int bin, bin_to;         // those taken
-  u64 limit, many;       // the border's sum or number, and its number within the level
-  u64 S;                 // the sum of the level's W
-  u64 skipped, before;   // tokens before the level's first bin, and before the taken ones
-  float e0, w, slack, e_before;  // the estimate looked for: e0 + w's share, give or take slack
-  uint32_t from, to;     // |x|'s bits of the taken bins
+  u64 limit, many;         // the border's sum or number, and its number within the level
+  u64 S;                   // the sum of the level's W
+  u64 skipped, before;     // tokens before the level's first bin, and before the taken ones
+  u64 e_before;            // the estimate before these
+  float e0, w, slack;      // the estimate looked for: e0 + w's share, give or take slack
+  uint32_t from, to;       // |x|'s bits of the taken bins
 };
 
 struct Shared {
   union {
     uint32_t hist[kBins];          // this CTA's counts
-    uint2 all[kList];              // the cluster's listed tokens, once the counts are read
+    uint2 all[kList];              // the first CTA: the cluster's listed tokens (|x|'s bits, index)
   };
-  uint32_t total[kBins];           // the cluster's counts
-  uint2 list[kList];               // this CTA's listed tokens (|x|'s bits, index)
   u64 all_w[kList];                // W of `all`
+  uint32_t share_n[kBins];         // the cluster's counts of this CTA's share of the bins
+  uint32_t at_n[kThreads];         // counts and estimates before a thread's bins of the share
+  u64 at_e[kThreads];
+  u64 share[2][kMaxCluster];       // count and estimate of each CTA's share
+  uint2 list[kWarps][kWarpList];   // listed tokens
   u64 post[2][3][kMaxPieces];      // what the pieces' warps told last, and before that
-  uint32_t border[2];
+  u64 taken[3];                    // first bin and count before it, last bin and count to its end, estimate before
+  u64 result[2];                   // the border, the sum up to it
+  Search q;
   u64 scan_s[kWarps];
   uint32_t scan_n[kWarps];
-  float scan_e[kWarps];
-  Search q;
-  int listed, hit;
-  uint32_t before_n, until_n;
-  float before_e;
   uint32_t sub_n[kThreads], sub_hi[kThreads], sub_lo[kThreads];  // a list's bins: tokens, W by 20-bit digits
-  int first_of[kMaxCluster + 1];   // where a CTA's listed tokens lie in `all`
-  int sub_bin, few_n;
+  int sub_bin, few_n, hit;
   u64 sub_before_s;
   uint32_t sub_before_n, sub_count;
   int few[32];
@@ -235,8 +233,8 @@ struct Row {
       return x;
   }
   __device__ bool inside(uint32_t d, uint32_t v) const { return d < border || (d == border && v <= last); }
-  __device__ float kept(uint32_t d, int v) const {  // weight, 0 where it is not kept
-    if (!inside(d, (uint32_t)v)) return 0.f;
+  __device__ float kept(uint32_t d, uint32_t v) const {  // weight, 0 where it is not kept
+    if (!inside(d, v)) return 0.f;
     const float w = weight(d);
     return w >= least ? w : 0.f;
   }
@@ -268,8 +266,8 @@ struct Row {
     while (s < steps && !((alive >> (s >> chunk_log)) & 1u)) ++s;
     return s;
   }
-  // f(logit, index) for this piece's elements in live chunks, one step's loads ahead; g(its place) after each
-  // step.
+  // f(logit) for this piece's elements in live chunks, one step's loads ahead; g(the step's place, its logits) after
+  // each step.
   template <typename F, typename G>
   __device__ void each(uint32_t alive, int lane, F f, G g) const {
     const int steps = (hi - lo + kStep - 1) / kStep;
@@ -283,9 +281,15 @@ struct Row {
       s = next(s + 1, steps, alive);
       if (s < steps) load(lo + s * kStep, hi, lane, y);
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) f(x[j], index(at, j, lane));
-      g(at);
+      for (int j = 0; j < kEach; ++j) f(x[j]);
+      g(at, x);
     }
+  }
+  // f(bits of |x|, index) for the elements [a, b), a lane's one after another: where speed does not count.
+  template <typename F>
+  __device__ void each_slowly(int a, int b, int lane, F f) const {
+#pragma unroll 1
+    for (int i = max(a, skip) + lane; i < b; i += 32) f(depth(value(base[i]), M, inv), (uint32_t)(i - skip));
   }
   // The chunks that have tokens with |x|'s bits below d.
   __device__ uint32_t alive(uint32_t d) const { return __ballot_sync(0xffffffffu, depth(chunk_top, M, inv) < d); }
@@ -297,8 +301,9 @@ struct Sampler {
   Shared &sh;
   Row<T> r;
   int cluster, rank, warp, lane, piece, pieces;
-  int turn = 0;  // exchanges so far: their buffers alternate
-  bool counted = true;  // sh.total has the first level's counts
+  int turn = 0;         // exchanges so far: their buffers alternate
+  bool counted = true;  // sh.hist has (or had) the first level's counts
+  uint32_t n = 0;       // this warp's listed tokens
 
   // Tell the cluster up to three numbers of this piece; afterwards all of them are in post.
   template <int kNumbers>
@@ -319,177 +324,150 @@ struct Sampler {
     return warp_sum((lane < piece ? posted(k, lane) : 0) + (lane + 32 < piece ? posted(k, lane + 32) : 0));
   }
 
-  // The cluster's counts of each bin, from the CTAs' (each sums a share of them and hands it to all).
-  __device__ void add_up() {
-    const int share_of = kBins / cluster;
-    for (int i = threadIdx.x; i < share_of; i += kThreads) {
-      const int b = rank * share_of + i;
-      uint32_t n = 0, x[kMaxCluster];
+  // ---- bins
+
+  // Counts of q's level in sh.hist, of the tokens with |x|'s bits in [from, to).
+  __device__ void count() {
+    const Search &q = sh.q;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
+    __syncthreads();
+    const uint32_t from = q.from, to = q.to;
+    const Level lv = q.lv;
+    r.each_slowly(r.lo, r.hi, lane, [&](uint32_t d, uint32_t) {
+      if (d - from < to - from) atomicAdd(&sh.hist[lv.bin(d)], 1u);
+    });
+    cluster_barrier();
+  }
+
+  // A thread's bins of its CTA's share: their number, and the first.
+  __device__ int each_bins() const { return kBins / kThreads / cluster; }
+  __device__ int first_bin() const { return (rank * kThreads + threadIdx.x) * each_bins(); }
+
+  // The cluster's counts of this CTA's share of the bins, and what lies before each thread's; all shares' sums to all.
+  __device__ void reduce() {
+    const int k = each_bins(), b0 = first_bin();
+    uint32_t n_run = 0;
+    u64 e_run = 0;
+#pragma unroll 1
+    for (int b = 0; b < k; ++b) {
+      uint32_t x[kMaxCluster], c = 0;
 #pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) x[c] = c < cluster ? load_remote_word(remote(&sh.hist[b], c)) : 0;
+      for (int i = 0; i < kMaxCluster; ++i) x[i] = i < cluster ? load_remote(remote(&sh.hist[b0 + b], i)) : 0;
 #pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) n += x[c];
-      for (int c = 0; c < cluster; ++c) store_remote(remote(&sh.total[b], c), n);
+      for (int i = 0; i < kMaxCluster; ++i) c += x[i];
+      sh.share_n[threadIdx.x * k + b] = c;
+      n_run += c;
+      e_run += sh.q.lv.estimate(b0 + b, c);
+    }
+    const uint32_t n_mine = n_run;
+    const u64 e_mine = e_run;
+    e_run = warp_scan(e_run, lane);
+    n_run = (uint32_t)warp_scan(n_run, lane);
+    if (lane == 31) sh.scan_n[warp] = n_run, sh.scan_s[warp] = e_run;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) n_run += sh.scan_n[i], e_run += sh.scan_s[i];
+    sh.at_n[threadIdx.x] = n_run - n_mine;
+    sh.at_e[threadIdx.x] = e_run - e_mine;
+    if (warp == kWarps - 1) {
+      n_run = __shfl_sync(0xffffffffu, n_run, 31);
+      e_run = __shfl_sync(0xffffffffu, e_run, 31);
+      if (lane < cluster) {
+        store_remote(remote(&sh.share[0][rank], lane), (u64)n_run);
+        store_remote(remote(&sh.share[1][rank], lane), e_run);
+      }
     }
     cluster_barrier();
   }
 
   // Takes the bins that may hold the border: the one at which the running count reaches q.many, or (by_sum) those at
-  // which the running estimate may pass q.e0 + q.w's share of all bins' (S), give or take q.slack of it.
+  // which the running estimate may pass q.e0 + q.w's share of all bins' (S), give or take q.slack of it; within
+  // [q.first, q.last] (after some wrong guesses the middle one).  The threads that hold them tell all CTAs.
   __device__ void seek() {
-    Search &q = sh.q;
-    constexpr int kMine = kBins / kThreads;
-    const int b0 = threadIdx.x * kMine;
-    const bool by_sum = q.by_sum;
-    uint32_t n[kMine], n_run = 0;
-    float m[kMine], e_run = 0.f;  // (by number: the counts, below 2^23)
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) n[k] = sh.total[b0 + k];
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      m[k] = (float)n[k];
-      if (by_sum && n[k]) m[k] *= q.lv.middle(b0 + k);
-      n_run += n[k];
-      e_run += m[k];
+    const Search &q = sh.q;
+    uint32_t n_run = sh.at_n[threadIdx.x];
+    u64 e_run = sh.at_e[threadIdx.x], everything = 0;
+    for (int c = 0; c < cluster; ++c) {
+      if (c < rank) n_run += (uint32_t)sh.share[0][c], e_run += sh.share[1][c];
+      everything += sh.share[1][c];
     }
-    const uint32_t n_all = n_run;
-    const float e_all = e_run;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, n_run, d);
-      const float z = __shfl_up_sync(0xffffffffu, e_run, d);
-      if (lane >= d) n_run += y, e_run += z;
+    u64 low = q.many, high = q.many;
+    if (q.by_sum) {
+      const float e = q.e0 + q.w * ((float)everything / (float)q.S), slack = e * q.slack;
+      low = __float2ull_rn(fmaxf(e - slack, 1.f));
+      high = __float2ull_rn(fmaxf(e + slack, 1.f));
     }
-    if (lane == 31) sh.scan_n[warp] = n_run, sh.scan_e[warp] = e_run;
-    // (after some wrong guesses by halves)
     const int first = q.tries < 5 ? q.first : (q.first + q.last) / 2, last = q.tries < 5 ? q.last : first;
-    if (threadIdx.x == 0) q.bin = q.bin_to = last;
-    __syncthreads();
-    n_run -= n_all;
-    e_run -= e_all;
-    float everything = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k < warp) n_run += sh.scan_n[k], e_run += sh.scan_e[k];
-      everything += sh.scan_e[k];
+    const int k = each_bins(), b0 = first_bin();
+#pragma unroll 1
+    for (int i = 0; i < k; ++i) {
+      const int b = b0 + i;
+      const uint32_t c = sh.share_n[threadIdx.x * k + i], n_to = n_run + c;
+      const u64 e_to = e_run + q.lv.estimate(b, c), was = q.by_sum ? e_run : n_run, is = q.by_sum ? e_to : n_to;
+      auto here = [&](u64 t) { return b >= first && b <= last && (b == first || was < t) && (b == last || is >= t); };
+      if (here(low))
+        for (int x = 0; x < cluster; ++x) {
+          store_remote(remote(&sh.taken[0], x), (u64)b << 32 | n_run);
+          store_remote(remote(&sh.taken[2], x), e_run);
+        }
+      if (here(high))
+        for (int x = 0; x < cluster; ++x) store_remote(remote(&sh.taken[1], x), (u64)b << 32 | n_to);
+      n_run = n_to;
+      e_run = e_to;
     }
-    float e = (float)q.many, slack = 0.f;
-    if (by_sum) {
-      e = q.e0 + q.w * (everything / (float)q.S);
-      slack = e * q.slack;
-    }
-    float run = e_run;
-    int low = kBins, high = kBins;
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      run += m[k];
-      if (n[k] && run >= e - slack) low = min(low, b0 + k);
-      if (n[k] && run >= e + slack) high = min(high, b0 + k);
-    }
-    if (low < kBins) atomicMin(&q.bin, max(low, first));
-    if (high < kBins) atomicMin(&q.bin_to, max(high, first));
-    __syncthreads();
-    const int bin = q.bin - b0, bin_to = q.bin_to - b0;
-    if ((uint32_t)bin < kMine || (uint32_t)bin_to < kMine)
-#pragma unroll
-      for (int k = 0; k < kMine; ++k) {
-        if (k == bin) sh.before_n = n_run, sh.before_e = e_run;
-        n_run += n[k];
-        e_run += m[k];
-        if (k == bin_to) sh.until_n = n_run;
-      }
-    __syncthreads();
+    cluster_barrier();
   }
 
-  // ---- lists
+  // ---- lists (of the first CTA)
 
-  // All CTAs' lists in one (number 1 of the last exchange: each piece's tokens): returns how many.
-  __device__ int gather() {
-    int n = 0, incl;
-    if (lane < cluster)
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) n += (int)posted(1, lane * kWarps + i);
-    incl = n;
-#pragma unroll
-    for (int d = 1; d < kMaxCluster; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += y;
-    }
-    const int all = __shfl_sync(0xffffffffu, incl, kMaxCluster - 1);
-    if (warp == 0 && lane < kMaxCluster) sh.first_of[lane] = incl - n;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kList / kThreads; ++k) {
-      const int i = threadIdx.x + k * kThreads;
-      if (i < all) {
-        int c = 0;
-        while (c + 1 < cluster && sh.first_of[c + 1] <= i) ++c;
-        const uint2 q = load_remote(remote(&sh.list[i - sh.first_of[c]], c));
-        sh.all[i] = q;
-        sh.all_w[i] = whole_weight(weight(q.x));
-      }
-    }
-    __syncthreads();
-    return all;
-  }
-
-  // Of the list's n tokens that lie inside the border (and weigh `least`), in their order (or by index), the one at
+  // Of the list's tokens that lie inside the border (and weigh `least`), in their order (or by index), the one at
   // which their running number (or the sum of their W) reaches `target`.  base: the number (sum) before those with
   // key lo; `with`: the sum up to that token, it included (by number: left as it is).  [lo, lo + 2^bits): where its
   // key lies; bits -1: anywhere, by |x| in steps of 1/8 first.
-  __device__ uint2 pick(int n, bool by_index, bool by_sum, u64 target, u64 base, uint32_t lo, int bits, u64 &with) {
+  __device__ uint2 pick(int listed, bool by_index, bool by_sum, u64 target, u64 base, uint32_t lo, int bits, u64 &with) {
     u64 before_n = by_sum ? 0 : base, before_s = by_sum ? base : 0;
     uint32_t fixed = 0;      // |x|'s bits, once these are down to one value
-    bool on_v = by_index, tied = false;
+    bool on_v = by_index, tied = false, eighths = bits < 0;
     auto in = [&](int i, uint2 &q, uint32_t &key) {
       q = sh.all[i];
       key = on_v ? q.y : q.x;
       return r.inside(q.x, q.y) && (!tied || q.x == fixed) && !(r.least > 0.f && weight(q.x) < r.least);
     };
-    bool eighths = bits < 0;
     uint32_t width;          // of the last level's bin
     int shift = max(0, bits - 8);
+#pragma unroll 1
     for (;;) {
       sh.sub_n[threadIdx.x] = sh.sub_hi[threadIdx.x] = sh.sub_lo[threadIdx.x] = 0;
       if (threadIdx.x == 0) sh.sub_bin = kThreads - 1, sh.few_n = 0, sh.sub_count = 0;
       __syncthreads();
-      for (int i = threadIdx.x; i < n; i += kThreads) {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < listed; i += kThreads) {
         uint2 q;
         uint32_t key;
         if (in(i, q, key) && (eighths || key - lo < (256u << shift))) {
           const uint32_t b = eighths ? (uint32_t)(__uint_as_float(key) * 8.f) : (key - lo) >> shift;
           atomicAdd(&sh.sub_n[b], 1u);
-          if (by_sum) {  // (64-bit atomics on one word hold each other up; a digit's sums stay below 2^31)
-            atomicAdd(&sh.sub_hi[b], (uint32_t)(sh.all_w[i] >> 20));
-            atomicAdd(&sh.sub_lo[b], (uint32_t)sh.all_w[i] & 0xfffffu);
-          }
+          // (64-bit atomics on one word hold each other up; a digit's sums stay below 2^31)
+          atomicAdd(&sh.sub_hi[b], (uint32_t)(sh.all_w[i] >> 20));
+          atomicAdd(&sh.sub_lo[b], (uint32_t)sh.all_w[i] & 0xfffffu);
         }
       }
       __syncthreads();
       const uint32_t my_n = sh.sub_n[threadIdx.x];
       const u64 my_s = ((u64)sh.sub_hi[threadIdx.x] << 20) + sh.sub_lo[threadIdx.x];
-      uint32_t n_run = my_n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, n_run, d);
-        if (lane >= d) n_run += y;
-      }
-      u64 s_run = by_sum ? warp_scan(my_s, lane) : 0;
-      if (lane == 31) sh.scan_n[warp] = n_run, sh.scan_s[warp] = s_run;
+      u64 run = warp_scan(by_sum ? my_s : (u64)my_n, lane);
+      if (lane == 31) sh.scan_s[warp] = run;
       __syncthreads();
-      s_run += before_s;
-      for (int k = 0; k < warp; ++k) n_run += sh.scan_n[k], s_run += sh.scan_s[k];
-      const u64 at = by_sum ? s_run : before_n + n_run, was = by_sum ? s_run - my_s : before_n + n_run - my_n;
-      if (was < target && target <= at) {
+      run += by_sum ? before_s : before_n;
+      for (int k = 0; k < warp; ++k) run += sh.scan_s[k];
+      const u64 was = run - (by_sum ? my_s : (u64)my_n);
+      if (was < target && target <= run) {
         sh.sub_bin = threadIdx.x;
-        sh.sub_before_n = n_run - my_n;
-        sh.sub_before_s = s_run - my_s;
+        sh.sub_before_s = was;
         sh.sub_count = my_n;
       }
       __syncthreads();
       const int count = (int)sh.sub_count;
-      before_n += sh.sub_before_n;
-      before_s = sh.sub_before_s;
+      (by_sum ? before_s : before_n) = sh.sub_before_s;
       if (eighths) {
         lo = __float_as_uint((float)sh.sub_bin * 0.125f);
         width = __float_as_uint((float)(sh.sub_bin + 1) * 0.125f) - lo;
@@ -511,7 +489,7 @@ struct Sampler {
       __syncthreads();
     }
     // a few: ranked in every warp's lanes
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = threadIdx.x; i < listed; i += kThreads) {
       uint2 q;
       uint32_t key;
       if (in(i, q, key) && key - lo < width) sh.few[atomicAdd(&sh.few_n, 1) & 31] = i;
@@ -521,6 +499,7 @@ struct Sampler {
     const uint2 q = sh.all[mine];
     const u64 w = sh.all_w[mine];
     u64 sum = before_s + w, place = before_n + 1;
+#pragma unroll 1
     for (int k = 0; k < count; ++k) {
       const uint32_t d = __shfl_sync(0xffffffffu, q.x, k), v = __shfl_sync(0xffffffffu, q.y, k);
       const u64 o = __shfl_sync(0xffffffffu, w, k);
@@ -535,18 +514,14 @@ struct Sampler {
     return found;
   }
 
-  // The sum of W of the list's tokens that lie inside the border (and weigh `least`); part: of those with |x|'s bits
-  // below d, or (d 0) of this piece's.
-  __device__ u64 list_sum(int n, uint32_t d, u64 &part) {
-    u64 x = 0, y = 0;
-    for (int j = lane; j < n; j += 32) {
+  // The sum of W of the list's tokens that lie inside the border (and weigh `least`), with |x|'s bits below d.
+  __device__ u64 list_sum(int listed, uint32_t d) {
+    u64 x = 0;
+#pragma unroll 1
+    for (int j = lane; j < listed; j += 32) {
       const uint2 q = sh.all[j];
-      if (!r.inside(q.x, q.y) || (r.least > 0.f && weight(q.x) < r.least)) continue;
-      const int at = (int)q.y + r.skip;
-      x += sh.all_w[j];
-      if (d ? q.x < d : at >= r.lo && at < r.hi) y += sh.all_w[j];
+      if (q.x < d && r.inside(q.x, q.y) && !(r.least > 0.f && weight(q.x) < r.least)) x += sh.all_w[j];
     }
-    part = warp_sum(y);
     return warp_sum(x);
   }
 
@@ -554,6 +529,7 @@ struct Sampler {
   __device__ void rank_ties(uint32_t d, u64 ties, u64 before_here, u64 here) {
     if (before_here < ties && ties <= before_here + here) {
       u64 run = before_here;
+#pragma unroll 1
       for (int i = r.lo; i < r.hi; i += 32) {
         const int at = i + lane;
         const bool eq = at >= r.skip && at < r.hi && r.inside(d, (uint32_t)(at - r.skip)) &&
@@ -561,7 +537,8 @@ struct Sampler {
         uint32_t who = __ballot_sync(0xffffffffu, eq);
         if (ties <= run + __popc(who)) {
           while (++run < ties) who &= who - 1;
-          if (lane < cluster) store_remote(remote(&sh.border[1], lane), (uint32_t)(i + __ffs(who) - 1 - r.skip));
+          if (lane < cluster)
+            store_remote(remote(&sh.result[0], lane), (u64)d << 32 | (uint32_t)(i + __ffs(who) - 1 - r.skip));
           break;
         }
         run += __popc(who);
@@ -569,40 +546,27 @@ struct Sampler {
     }
     cluster_barrier();
     r.border = d;
-    r.last = sh.border[1];
-  }
-
-  // The counts of q's level, of the tokens with |x|'s bits in [from, to).
-  __device__ void count() {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
-    __syncthreads();
-    const uint32_t from = sh.q.from, to = sh.q.to;
-    const int shift = sh.q.lv.shift;
-    r.each(r.alive(to), lane, [&](float l, int) {
-      const uint32_t d = depth(l, r.M, r.inv);
-      if (d - from < to - from) atomicAdd(&sh.hist[shift < 0 ? Level::first_bin(d) : (int)((d - from) >> shift)], 1u);
-    }, [](int) {});
-    cluster_barrier();
-    add_up();
+    r.last = (uint32_t)sh.result[0];
   }
 
   // Move the border to the last token of the order's first part: the `limit` first ones (by_sum false), or the
   // shortest part whose W sum to `limit` at least (1 .. their sum); S: the sum of all W.  sum: that part's, mine:
   // this piece's share of it.  listed: how many tokens are listed where the list holds all that lies inside the
-  // border, else 0, before and after.  Where nothing with weight would be left out the border, sum and mine stay.
+  // border, else 0, before and after: then only the first CTA moves its border, and knows sum.
+  // Where nothing with weight would be left out the border, sum and mine stay.
   // (One loop with each step in it once: the code is long, and it is fetched from memory when a call is the first.)
   __device__ void find_border(bool by_sum, u64 limit, u64 S, u64 &sum, u64 &mine, int &listed) {
     Search &q = sh.q;
     const bool lead = threadIdx.x == 0;
-    u64 A = 0, above_here = 0;
+    u64 A = 0, above_here = 0, start = 0;
     uint32_t lo = 0;
     int bits = -1;
-    u64 start = 0;
     if (!listed) {
       if (lead) {
         q.lv = Level{0u, 0u, -1};
         q.by_sum = by_sum;
         q.counted = counted;
+        q.reduced = false;
         q.first = q.tries = 0;
         q.last = kBins - 1;
         q.limit = q.many = limit;
@@ -617,111 +581,116 @@ struct Sampler {
       counted = true;
       __syncthreads();
     }
+#pragma unroll 1
     while (!listed) {
       if (!q.counted) count();
+      if (!q.reduced) reduce();
       seek();
-      if (!q.by_sum && q.lv.shift < 0 && q.bin == kBins - 1) return;
+      const int bin = (int)(sh.taken[0] >> 32), bin_to = (int)(sh.taken[1] >> 32);
+      const uint32_t before_n = (uint32_t)sh.taken[0], until_n = (uint32_t)sh.taken[1];
+      if (!q.by_sum && q.lv.shift < 0 && bin == kBins - 1) return;
       // the whole first part is listed where it fits
-      const bool whole = q.skipped + sh.until_n <= kList;
-      const uint32_t begin = q.lv.begin(q.bin), from = whole ? 0u : begin, to = q.lv.begin(q.bin_to + 1);
-      if (!whole && q.bin < q.bin_to && sh.until_n - sh.before_n > kList && q.slack > 0.f) {
-        __syncthreads();
-        if (lead) q.counted = true, q.slack = 0.f;
-        __syncthreads();
-        continue;
-      }
+      const bool whole = q.skipped + until_n <= kList;
+      const bool wide = !whole && bin < bin_to && until_n - before_n > kList && q.slack > 0.f;
+      const uint32_t begin = q.lv.begin(bin), from = whole ? 0u : begin, to = q.lv.begin(bin_to + 1);
+      __syncthreads();
       if (lead) {
-        q.counted = true;
+        q.counted = q.reduced = true;
         q.whole = whole;
-        q.before = q.skipped + sh.before_n;
-        q.e_before = sh.before_e;
+        q.before = q.skipped + before_n;
+        q.e_before = sh.taken[2];
         q.from = from;
         q.to = to;
-        sh.listed = 0;
+        if (wide) q.slack = 0.f;
       }
-      __syncthreads();
+      if (wide) {
+        cluster_barrier();
+        continue;
+      }
       // ---- the exact sum of what lies before the bins, and their tokens
       Sum above;
-      uint32_t n = 0, marked = 0;  // bit j: element j of the lane's step is to be listed
+      uint32_t marked = 0;  // bit j: element j of the lane's step is to be listed
       int j = 0;
-      r.each(r.alive(to), lane, [&](float l, int) {
+      n = 0;
+      uint2 *list = sh.list[warp];
+      r.each(r.alive(to), lane, [&](float l) {
         const uint32_t d = depth(l, r.M, r.inv);
         if (from) {  // (without a branch on d: in most warps some lane has a token before the bins)
           const float w = weight(d);
           above.add(d < from ? w : 0.f);
         }
         marked |= (uint32_t)(d - from < to - from) << j++;
-      }, [&](int at) {
+      }, [&](int at, const float(&x)[kEach]) {
         above.carry();
         j = 0;
-        while (marked) {
-          const int v = r.index(at, __ffs(marked) - 1, lane);
-          marked &= marked - 1;
-          const uint32_t d = depth(Row<T>::value(r.base[v + r.skip]), r.M, r.inv);
-          if (!r.inside(d, (uint32_t)v)) continue;
-          ++n;
-          const int place = atomicAdd(&sh.listed, 1);
-          if (place < kList) sh.list[place] = make_uint2(d, (uint32_t)v);
+        if (__any_sync(0xffffffffu, marked)) {
+#pragma unroll
+          for (int k = 0; k < kEach; ++k) {
+            const uint32_t d = depth(x[k], r.M, r.inv), v = (uint32_t)r.index(at, k, lane);
+            const bool mine = (marked >> k) & 1u && r.inside(d, v);
+            const uint32_t who = __ballot_sync(0xffffffffu, mine), place = n + __popc(who & ((1u << lane) - 1));
+            if (mine && place < kWarpList) list[place] = make_uint2(d, v);
+            n += __popc(who);
+          }
         }
-        __syncwarp();
+        marked = 0;
       });
       above_here = warp_sum(above.total);
-      const uint32_t here = __reduce_add_sync(0xffffffffu, n);
-      exchange<2>(above_here, (u64)here);
-      A = told(0);
-      const u64 N = told(1), N_before = told_before(1);
-      // ---- their own sum
-      int in_list = 0;
-      u64 B = 0;
-      if (N <= kList) {
-        in_list = gather();
-        if (q.by_sum) B = list_sum(in_list, begin, mine);
-      } else if (q.by_sum) {
-        Sum within;
-        r.each(r.alive(to), lane, [&](float l, int v) {
-          const uint32_t d = depth(l, r.M, r.inv);
-          within.add(d - from < to - from && r.inside(d, (uint32_t)v) ? weight(d) : 0.f);
-        }, [&](int) { within.carry(); });
-        exchange<1>(warp_sum(within.total));
-        B = told(0);
+      __syncwarp();
+      // their own sum
+      u64 within = 0;
+      if (q.by_sum) {
+        if (n <= kWarpList)
+          for (int i = lane; i < (int)n; i += 32) within += whole_weight(weight(list[i].x));
+        else
+          r.each_slowly(r.lo, r.hi, lane, [&](uint32_t d, uint32_t v) {
+            if (d - from < to - from && r.inside(d, v)) within += whole_weight(weight(d));
+          });
+        within = warp_sum(within);
       }
+      exchange<3>(above_here, (u64)n, within);
+      A = told(0);
+      const u64 N = told(1), N_before = told_before(1), B = told(2);
       const bool low = q.by_sum && A >= q.limit, high = q.by_sum && A + B < q.limit;
-      const bool ties = !low && !high && N > kList && to - from == 1;
-      if (ties) {
+      const bool fits = N <= kList && !__any_sync(0xffffffffu, posted(1, lane) > kWarpList || posted(1, lane + 32) > kWarpList);
+      if (!low && !high && fits) {
+        // to the first CTA
+        for (int i = lane; i < (int)n; i += 32) {
+          const uint2 t = list[i];
+          store_remote(remote(&sh.all[N_before + i], 0), (u64)t.y << 32 | t.x);
+          store_remote(remote(&sh.all_w[N_before + i], 0), whole_weight(weight(t.x)));
+        }
+        listed = (int)N;
+        lo = begin;
+        bits = 32 - __clz((int)(to - begin - 1) | 255);
+        start = q.by_sum ? A : q.before;
+        cluster_barrier();
+        break;
+      }
+      if (!low && !high && to - from == 1) {
         const u64 W = whole_weight(weight(from)), stay = q.by_sum ? (q.limit - A + W - 1) / W : q.limit - q.before;
-        rank_ties(from, stay, N_before, here);
+        rank_ties(from, stay, N_before, n);
         sum = A + stay * W;
-        mine = above_here + (stay > N_before ? min(stay - N_before, (u64)here) : 0) * W;
+        mine = above_here + (stay > N_before ? min(stay - N_before, (u64)n) : 0) * W;
         counted = q.lv.shift < 0;
         return;
       }
       __syncthreads();
-      if (low || high) {
+      if (lead && (low || high)) {
         // the estimate was off: on from the exact sum (of a whole part: at its end)
-        if (lead) {
-          if (low)
-            q.last = max(q.bin - 1, 0);
-          else
-            q.first = min(q.bin_to + 1, kBins - 1);
-          q.e0 = q.e_before;
-          q.w = low ? -(float)(A - q.limit) : (float)(q.limit - (q.whole ? B : A));
-          q.slack = kSlack;
-          ++q.tries;
-        }
-      } else if (N <= kList) {
-        listed = in_list;
-        // (by number: what lies before the bins is counted; by weight: `mine` is its sum)
-        const u64 base = q.by_sum ? A + (begin ? mine : 0) : 0;
-        if (base < limit) {
-          lo = begin;
-          bits = 32 - __clz((int)(to - begin - 1) | 255);
-          start = q.by_sum ? base : q.before;
-        }
+        if (low)
+          q.last = max(bin - 1, 0);
+        else
+          q.first = min(bin_to + 1, kBins - 1);
+        q.e0 = (float)q.e_before;
+        q.w = low ? -(float)(A - q.limit) : (float)(q.limit - (whole ? B : A));
+        q.slack = kSlack;
+        ++q.tries;
       } else if (lead) {
         // finer bins
         q.skipped = q.before;
         q.lv = Level{from, to, max(0, 21 - __clz((int)(to - from - 1)))};
-        q.counted = false;
+        q.counted = q.reduced = false;
         q.first = q.tries = 0;
         q.last = (int)((to - 1 - from) >> q.lv.shift);
         q.many = q.limit - q.before;
@@ -734,12 +703,33 @@ struct Sampler {
       counted = q.lv.shift < 0;
       if (q.tries > 40) return;  // (never)
     }
-    const uint2 b = pick(listed, false, by_sum, limit, start, lo, bits, sum);
-    r.border = b.x;
-    r.last = b.y;
-    sum = A + list_sum(listed, 0u, mine);
-    mine += above_here;
-    if (!q.whole) listed = 0;
+    // ---- the border among the listed tokens
+    if (rank == 0) {
+      if (bits >= 0 && q.whole && by_sum) {  // (what lies before the bins: by weight it is summed up here)
+        start = list_sum(listed, lo);
+        if (start >= limit) lo = 0, start = 0, bits = -1;
+      }
+      const uint2 b = pick(listed, false, by_sum, limit, start, lo, bits, sum);
+      r.border = b.x;
+      r.last = b.y;
+      sum = A + list_sum(listed, UINT_MAX);
+      if (!q.whole && warp == 0 && lane < cluster) {
+        store_remote(remote(&sh.result[0], lane), (u64)b.x << 32 | b.y);
+        store_remote(remote(&sh.result[1], lane), sum);
+      }
+    }
+    if (q.whole) return;
+    listed = 0;
+    cluster_barrier();
+    r.border = (uint32_t)(sh.result[0] >> 32);
+    r.last = (uint32_t)sh.result[0];
+    sum = sh.result[1];
+    u64 x = 0;
+    for (int i = lane; i < (int)n; i += 32) {
+      const uint2 t = sh.list[warp][i];
+      if (r.inside(t.x, t.y)) x += whole_weight(weight(t.x));
+    }
+    mine = above_here + warp_sum(x);
   }
 };
 
@@ -778,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   r.chunk_top = -CUDART_INF_F;
   {
     float chunk = -CUDART_INF_F;
-    r.each(~0u, lane, [&](float x, int) { chunk = fmaxf(chunk, x); }, [&](int at) {
+    r.each(~0u, lane, [&](float x) { chunk = fmaxf(chunk, x); }, [&](int at, const float(&)[kEach]) {
       const int step = (at - r.lo) / kStep + 1;
       if (step & ((1 << r.chunk_log) - 1) && at + kStep < r.hi) return;
       chunk = warp_max(chunk);
@@ -800,12 +790,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   if (lane < s.pieces) top = fmaxf(top, __uint_as_float((uint32_t)tops[lane]));
   if (lane + 32 < s.pieces) top = fmaxf(top, __uint_as_float((uint32_t)tops[lane + 32]));
   top = warp_max(top);
-  const bool empty = top == -CUDART_INF_F;
+  const bool empty = top == -CUDART_INF_F, endless = top == CUDART_INF_F;
   if (empty && s.rank == 0 && threadIdx.x == 0) {
     if (a.tokens) a.tokens[row] = -1;
     raise_fault(a.status, PSKV_FAULT_EMPTY_ROW);
   }
-  const bool endless = top == CUDART_INF_F;
   r.M = endless ? FLT_MAX : top;
   r.inv = __fdiv_rn(1.f, heat);
   r.border = kDeep;
@@ -819,7 +808,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     // ---- the likeliest token, the lowest index of M
     r.inv = endless ? CUDART_INF_F : 1.f;
     uint32_t at = UINT_MAX;
-    r.each(r.alive(1u), lane, [&](float x, int v) { at = x == top ? min(at, (uint32_t)v) : at; }, [](int) {});
+    if (r.alive(1u))
+      for (int i = max(r.lo, r.skip) + lane; i < r.hi && at == UINT_MAX; i += 32)
+        if (Row<T>::value(r.base[i]) == top) at = (uint32_t)(i - r.skip);
     s.template exchange<1>((u64)__reduce_min_sync(0xffffffffu, at));
     const u64 *ats = sh.post[1][0];
     if (lane < s.pieces) at = min(at, (uint32_t)ats[lane]);
@@ -830,58 +821,70 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     total = 1ull << 40;
     if (a.tokens && s.rank == 0 && threadIdx.x == 0) a.tokens[row] = (int)at;
   } else {
-    const bool some = k > 0 && k < a.vocab, part = p < 1.f, filters = some || part;
     if (endless) r.inv = CUDART_INF_F;
+    const bool some = k > 0 && k < a.vocab, part = p < 1.f, filters = some || part;
     // ---- the sum of W, and where the tokens lie
     if (filters) {
       for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
       __syncthreads();
     }
+    const Level first{0u, 0u, -1};
     Sum all;
-    r.each(~0u, lane, [&](float x, int) {
+    r.each(~0u, lane, [&](float x) {
       const uint32_t d = depth(x, r.M, r.inv);
       const float w = weight(d);
       if (filters) {
         all.add(w);
-        atomicAdd(&sh.hist[Level::first_bin(d)], 1u);
+        atomicAdd(&sh.hist[first.bin(d)], 1u);
       } else {
         all.add(w >= r.least ? w : 0.f);
       }
-    }, [&](int) { all.carry(); });
+    }, [&](int, const float(&)[kEach]) { all.carry(); });
     u64 mine = warp_sum(all.total);
     s.template exchange<1>(mine);
     total = s.told(0);
     if (filters) {
-      s.add_up();
       const u64 S = total;
       const float least_w = r.least;  // (min_p comes last)
       r.least = 0.f;
 #pragma unroll 1
       for (int by_sum = some ? 0 : 1; by_sum < (part ? 2 : 1); ++by_sum)
-        s.find_border(by_sum, by_sum ? max(share(p, total), 1ull) : (u64)k, S, total, mine, listed);
+        if (!listed || s.rank == 0)
+          s.find_border(by_sum, by_sum ? max(share(p, total), 1ull) : (u64)k, S, total, mine, listed);
       r.least = least_w;
       if (listed) {
-        if (r.least > 0.f) total = s.list_sum(listed, 0u, mine);
+        if (r.least > 0.f && s.rank == 0) total = s.list_sum(listed, UINT_MAX);
       } else {
         if (r.least > 0.f) {
-          Sum kept;
-          r.each(r.alive(r.border + 1), lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); },
-                 [&](int) { kept.carry(); });
-          mine = warp_sum(kept.total);
+          mine = 0;
+          r.each_slowly(r.lo, r.hi, lane, [&](uint32_t d, uint32_t v) { mine += whole_weight(r.kept(d, v)); });
+          mine = warp_sum(mine);
         }
         s.template exchange<1>(mine);
         total = s.told(0);
       }
     }
     // ---- the draw: where the running sum passes u's share
-    const float u = a.u ? a.u[row] : 0.f;
-    const u64 thr = u >= 1.f ? total - 1 : share(u, total);
-    if (a.tokens && listed) {
-      u64 with;
-      const uint2 t = s.pick(listed, true, true, thr + 1, 0, 0u, 32 - __clz((a.vocab - 1) | 255), with);
-      if (s.rank == 0 && threadIdx.x == 0) a.tokens[row] = (int)t.y;
+    if (listed) {
+      if (s.rank == 0 && a.tokens) {
+        const float u = a.u[row];
+        u64 with;
+        const uint2 t = s.pick(listed, true, true, (u >= 1.f ? total - 1 : share(u, total)) + 1, 0, 0u,
+                               32 - __clz((a.vocab - 1) | 255), with);
+        if (threadIdx.x == 0) a.tokens[row] = (int)t.y;
+      }
+      if (!a.probs) return;
+      if (s.rank == 0 && warp == 0 && lane < cluster) {
+        store_remote(remote(&sh.result[0], lane), (u64)r.border << 32 | r.last);
+        store_remote(remote(&sh.result[1], lane), total);
+      }
+      cluster_barrier();
+      r.border = (uint32_t)(sh.result[0] >> 32);
+      r.last = (uint32_t)sh.result[0];
+      total = sh.result[1];
     } else if (a.tokens) {
-      const u64 before = s.told_before(0);
+      const float u = a.u[row];
+      const u64 thr = u >= 1.f ? total - 1 : share(u, total), before = s.told_before(0);
       if (threadIdx.x == 0) sh.hit = -1;
       __syncthreads();
       if (lane == 0 && before <= thr && thr < before + mine) {
@@ -889,45 +892,28 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
         sh.sub_before_s = thr - before;
       }
       __syncthreads();
-      const int hit = sh.hit;
-      if (hit >= 0) {
+      if (sh.hit >= 0) {
         // its CTA: an eighth a warp
         const u64 left = sh.sub_before_s;
-        const int p0 = min(hit * seg, r.end), p1 = min(p0 + seg, r.end);
-        const int sub = ((p1 - p0 + kWarps - 1) / kWarps + kN - 1) / kN * kN;
-        r.lo = min(p0 + warp * sub, p1);
-        r.hi = min(r.lo + sub, p1);
-        r.chunk_log = 30;
-        Sum kept;
-        r.each(1u, lane, [&](float x, int v) { kept.add(r.kept(depth(x, r.M, r.inv), v)); }, [&](int) { kept.carry(); });
-        const u64 own = warp_sum(kept.total);
+        const int p0 = min(sh.hit * seg, r.end), p1 = min(p0 + seg, r.end), sub = (p1 - p0 + kWarps - 1) / kWarps;
+        const int s0 = min(p0 + warp * sub, p1), s1 = min(s0 + sub, p1);
+        u64 own = 0;
+        r.each_slowly(s0, s1, lane, [&](uint32_t d, uint32_t v) { own += whole_weight(r.kept(d, v)); });
+        own = warp_sum(own);
         if (lane == 0) sh.scan_s[warp] = own;
         __syncthreads();
         u64 at = 0;
         for (int i = 0; i < warp; ++i) at += sh.scan_s[i];
         if (at <= left && left < at + own) {
-          for (int i0 = r.lo; i0 < r.hi && at <= left; i0 += 32 * kN) {
-            const int i = i0 + lane * kN;
-            u64 w[kN], w_all = 0;
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-              const bool real = i + e >= r.skip && i + e < r.hi;
-              const float x = real ? Row<T>::value(r.base[i + e]) : -CUDART_INF_F;
-              w[e] = real ? whole_weight(r.kept(depth(x, r.M, r.inv), i + e - r.skip)) : 0;
-              w_all += w[e];
-            }
-            const u64 incl = at + warp_scan(w_all, lane);
-            u64 run = incl - w_all;
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-              if (run <= left && left < run + w[e]) a.tokens[row] = i + e - r.skip;
-              run += w[e];
-            }
+#pragma unroll 1
+          for (int i0 = max(s0, r.skip); i0 < s1 && at <= left; i0 += 32) {
+            const int i = i0 + lane;
+            const u64 w = i < s1 ? whole_weight(r.kept(depth(Row<T>::value(r.base[i]), r.M, r.inv), (uint32_t)(i - r.skip))) : 0;
+            const u64 incl = at + warp_scan(w, lane);
+            if (incl - w <= left && left < incl) a.tokens[row] = i - r.skip;
             at = __shfl_sync(0xffffffffu, incl, 31);
           }
         }
-        r.lo = min(s.piece * seg, r.end);
-        r.hi = min(r.lo + seg, r.end);
       }
     }
   }
@@ -936,27 +922,27 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     const double inv = 1.0 / (double)total;
     const float hi = (float)inv, lo = (float)(inv - (double)hi);
     const size_t out = (size_t)row * a.vocab;
-    auto put = [&](int v, float w) {
+    auto put = [&](uint32_t v, float w) {
       const float q = fmaf(w, hi, w * lo);
       if (a.probs_dtype == PSKV_DTYPE_BF16)
         static_cast<__nv_bfloat16 *>(a.probs)[out + v] = __float2bfloat16_rn(q);
       else
         static_cast<float *>(a.probs)[out + v] = q;
     };
-    for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) {
-      const int v = i - r.skip;
-      float w = 0.f;
-      if (!empty && !listed) {
-        const uint32_t d = depth(Row<T>::value(r.base[i]), r.M, r.inv);
-        if (r.inside(d, (uint32_t)v)) w = (float)whole_weight(r.kept(d, v));
+    if (empty || listed) {
+      for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) put((uint32_t)(i - r.skip), 0.f);
+      __syncwarp();
+      if (listed)
+        for (int i = lane; i < (int)s.n; i += 32) {
+          const uint2 t = sh.list[warp][i];
+          const float w = r.kept(t.x, t.y);
+          if (w > 0.f) put(t.y, (float)whole_weight(w));
+        }
+    } else {
+      for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) {
+        const uint32_t d = depth(Row<T>::value(r.base[i]), r.M, r.inv), v = (uint32_t)(i - r.skip);
+        put(v, r.inside(d, v) ? (float)whole_weight(r.kept(d, v)) : 0.f);
       }
-      put(v, w);
-    }
-    __syncwarp();
-    for (int j = lane; j < listed; j += 32) {
-      const uint2 q = sh.all[j];
-      const int i = (int)q.y + r.skip;
-      if (i >= r.lo && i < r.hi) put((int)q.y, (float)whole_weight(r.kept(q.x, (int)q.y)));
     }
   }
 }
