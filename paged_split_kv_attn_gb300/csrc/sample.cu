@@ -302,7 +302,7 @@ struct Sampler {
   Row<T> r;
   int cluster, rank, warp, lane, piece, pieces;
   int turn = 0;         // exchanges so far: their buffers alternate
-  bool counted = true;  // sh.hist has (or had) the first level's counts
+  enum { kCounted, kReduced, kGone } first_level = kCounted;  // its counts in sh.hist; its shares added up; neither
   uint32_t n = 0;       // this warp's listed tokens
 
   // Tell the cluster up to three numbers of this piece; afterwards all of them are in post.
@@ -525,6 +525,41 @@ struct Sampler {
     return warp_sum(x);
   }
 
+  // Lists this piece's tokens with |x|'s bits in [from, to); the sum of W of those before (kSum false: there are none).
+  template <bool kSum>
+  __device__ u64 list_pass(uint32_t from, uint32_t to) {
+    uint2 *list = sh.list[warp];
+    Sum above;
+    uint32_t marked = 0;  // bit j: element j of the lane's step is to be listed
+    int j = 0;
+    n = 0;
+    r.each(r.alive(to), lane, [&](float l) {
+      const uint32_t d = depth(l, r.M, r.inv);
+      if (kSum) {  // (without a branch: in most warps some lane has a token before the bins)
+        const float w = weight(d);
+        above.add(d < from ? w : 0.f);
+      }
+      marked |= (uint32_t)(kSum ? d - from < to - from : d < to) << j++;
+    }, [&](int at, const float(&x)[kEach]) {
+      above.carry();
+      j = 0;
+      const uint32_t some = __reduce_or_sync(0xffffffffu, marked);
+      if (some) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          if ((some >> k) & 1u) {
+            const uint32_t d = depth(x[k], r.M, r.inv), v = (uint32_t)r.index(at, k, lane);
+            const bool mine = (marked >> k) & 1u && r.inside(d, v);
+            const uint32_t who = __ballot_sync(0xffffffffu, mine), place = n + __popc(who & ((1u << lane) - 1));
+            if (mine && place < kWarpList) list[place] = make_uint2(d, v);
+            n += __popc(who);
+          }
+      }
+      marked = 0;
+    });
+    return kSum ? warp_sum(above.total) : 0;
+  }
+
   // The border among tokens of one |x| (bits d): the first `ties` of them stay.
   __device__ void rank_ties(uint32_t d, u64 ties, u64 before_here, u64 here) {
     if (before_here < ties && ties <= before_here + here) {
@@ -565,8 +600,8 @@ struct Sampler {
       if (lead) {
         q.lv = Level{0u, 0u, -1};
         q.by_sum = by_sum;
-        q.counted = counted;
-        q.reduced = false;
+        q.counted = first_level != kGone;
+        q.reduced = first_level == kReduced;
         q.first = q.tries = 0;
         q.last = kBins - 1;
         q.limit = q.many = limit;
@@ -578,7 +613,7 @@ struct Sampler {
         q.from = 0;
         q.to = kDeep + 1;
       }
-      counted = true;
+      first_level = kReduced;
       __syncthreads();
     }
 #pragma unroll 1
@@ -608,34 +643,8 @@ struct Sampler {
         continue;
       }
       // ---- the exact sum of what lies before the bins, and their tokens
-      Sum above;
-      uint32_t marked = 0;  // bit j: element j of the lane's step is to be listed
-      int j = 0;
-      n = 0;
       uint2 *list = sh.list[warp];
-      r.each(r.alive(to), lane, [&](float l) {
-        const uint32_t d = depth(l, r.M, r.inv);
-        if (from) {  // (without a branch on d: in most warps some lane has a token before the bins)
-          const float w = weight(d);
-          above.add(d < from ? w : 0.f);
-        }
-        marked |= (uint32_t)(d - from < to - from) << j++;
-      }, [&](int at, const float(&x)[kEach]) {
-        above.carry();
-        j = 0;
-        if (__any_sync(0xffffffffu, marked)) {
-#pragma unroll
-          for (int k = 0; k < kEach; ++k) {
-            const uint32_t d = depth(x[k], r.M, r.inv), v = (uint32_t)r.index(at, k, lane);
-            const bool mine = (marked >> k) & 1u && r.inside(d, v);
-            const uint32_t who = __ballot_sync(0xffffffffu, mine), place = n + __popc(who & ((1u << lane) - 1));
-            if (mine && place < kWarpList) list[place] = make_uint2(d, v);
-            n += __popc(who);
-          }
-        }
-        marked = 0;
-      });
-      above_here = warp_sum(above.total);
+      above_here = whole ? list_pass<false>(from, to) : list_pass<true>(from, to);
       __syncwarp();
       // their own sum
       u64 within = 0;
@@ -672,7 +681,7 @@ struct Sampler {
         rank_ties(from, stay, N_before, n);
         sum = A + stay * W;
         mine = above_here + (stay > N_before ? min(stay - N_before, (u64)n) : 0) * W;
-        counted = q.lv.shift < 0;
+        first_level = q.lv.shift < 0 ? kReduced : kGone;
         return;
       }
       __syncthreads();
@@ -700,7 +709,7 @@ struct Sampler {
         q.slack = kSlack;
       }
       __syncthreads();
-      counted = q.lv.shift < 0;
+      first_level = q.lv.shift < 0 ? kReduced : kGone;
       if (q.tries > 40) return;  // (never)
     }
     // ---- the border among the listed tokens
@@ -895,23 +904,47 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
       if (sh.hit >= 0) {
         // its CTA: an eighth a warp
         const u64 left = sh.sub_before_s;
-        const int p0 = min(sh.hit * seg, r.end), p1 = min(p0 + seg, r.end), sub = (p1 - p0 + kWarps - 1) / kWarps;
+        const int p0 = min(sh.hit * seg, r.end), p1 = min(p0 + seg, r.end);
+        const int sub = ((p1 - p0 + kWarps - 1) / kWarps + kN - 1) / kN * kN;
         const int s0 = min(p0 + warp * sub, p1), s1 = min(s0 + sub, p1);
         u64 own = 0;
-        r.each_slowly(s0, s1, lane, [&](uint32_t d, uint32_t v) { own += whole_weight(r.kept(d, v)); });
+        float x[kEach];
+#pragma unroll 1
+        for (int at = s0; at < s1; at += kStep) {
+          r.load(at, s1, lane, x);
+          Sum step;
+#pragma unroll
+          for (int j = 0; j < kEach; ++j)
+            step.add(r.kept(depth(x[j], r.M, r.inv), (uint32_t)r.index(at, j, lane)));
+          step.carry();
+          own += step.total;
+        }
         own = warp_sum(own);
         if (lane == 0) sh.scan_s[warp] = own;
         __syncthreads();
-        u64 at = 0;
-        for (int i = 0; i < warp; ++i) at += sh.scan_s[i];
-        if (at <= left && left < at + own) {
+        u64 run = 0;
+        for (int i = 0; i < warp; ++i) run += sh.scan_s[i];
+        if (run <= left && left < run + own) {
 #pragma unroll 1
-          for (int i0 = max(s0, r.skip); i0 < s1 && at <= left; i0 += 32) {
-            const int i = i0 + lane;
-            const u64 w = i < s1 ? whole_weight(r.kept(depth(Row<T>::value(r.base[i]), r.M, r.inv), (uint32_t)(i - r.skip))) : 0;
-            const u64 incl = at + warp_scan(w, lane);
-            if (incl - w <= left && left < incl) a.tokens[row] = i - r.skip;
-            at = __shfl_sync(0xffffffffu, incl, 31);
+          for (int at = s0; at < s1 && run <= left; at += kStep) {
+            if (sub > kStep) r.load(at, s1, lane, x);
+#pragma unroll
+            for (int j0 = 0; j0 < kEach; j0 += kN) {  // a vector's elements lie one after another, then the next lane's
+              u64 w[kN], w_all = 0;
+#pragma unroll
+              for (int e = 0; e < kN; ++e) {
+                w[e] = whole_weight(r.kept(depth(x[j0 + e], r.M, r.inv), (uint32_t)r.index(at, j0 + e, lane)));
+                w_all += w[e];
+              }
+              u64 incl = run + warp_scan(w_all, lane), at_e = incl - w_all;
+              if (at_e <= left && left < incl)
+#pragma unroll
+                for (int e = 0; e < kN; ++e) {
+                  if (at_e <= left && left < at_e + w[e]) a.tokens[row] = r.index(at, j0 + e, lane);
+                  at_e += w[e];
+                }
+              run = __shfl_sync(0xffffffffu, incl, 31);
+            }
           }
         }
       }
