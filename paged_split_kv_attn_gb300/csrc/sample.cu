@@ -266,20 +266,15 @@ struct Row {
     while (s < steps && !((alive >> (s >> chunk_log)) & 1u)) ++s;
     return s;
   }
-  // f(logit) for this piece's elements in live chunks, one step's loads ahead; g(the step's place, its logits) after
-  // each step.
+  // f(logit) for this piece's elements in live chunks; g(the step's place, its logits) after each step.  (The next
+  // step's loads ahead of it were no faster: an SM's other warps cover them, and the registers spill.)
   template <typename F, typename G>
-  __device__ void each(uint32_t alive, int lane, F f, G g) const {
-    const int steps = (hi - lo + kStep - 1) / kStep;
-    int s = next(0, steps, alive);
-    float x[kEach], y[kEach];
-    if (s < steps) load(lo + s * kStep, hi, lane, y);
-    while (s < steps) {
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) x[j] = y[j];
+  __device__ void each(uint32_t alive, F f, G g) const {
+    const int steps = (hi - lo + kStep - 1) / kStep, lane = threadIdx.x & 31;
+    for (int s = next(0, steps, alive); s < steps; s = next(s + 1, steps, alive)) {
+      float x[kEach];
       const int at = lo + s * kStep;
-      s = next(s + 1, steps, alive);
-      if (s < steps) load(lo + s * kStep, hi, lane, y);
+      load(at, hi, lane, x);
 #pragma unroll
       for (int j = 0; j < kEach; ++j) f(x[j]);
       g(at, x);
@@ -533,7 +528,7 @@ struct Sampler {
     uint32_t marked = 0;  // bit j: element j of the lane's step is to be listed
     int j = 0;
     n = 0;
-    r.each(r.alive(to), lane, [&](float l) {
+    r.each(r.alive(to), [&](float l) {
       const uint32_t d = depth(l, r.M, r.inv);
       if (kSum) {  // (without a branch: in most warps some lane has a token before the bins)
         const float w = weight(d);
@@ -643,7 +638,7 @@ struct Sampler {
         continue;
       }
       // ---- the exact sum of what lies before the bins, and their tokens
-      uint2 *list = sh.list[warp];
+      const uint2 *list = sh.list[warp];
       above_here = whole ? list_pass<false>(from, to) : list_pass<true>(from, to);
       __syncwarp();
       // their own sum
@@ -777,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   r.chunk_top = -CUDART_INF_F;
   {
     float chunk = -CUDART_INF_F;
-    r.each(~0u, lane, [&](float x) { chunk = fmaxf(chunk, x); }, [&](int at, const float(&)[kEach]) {
+    r.each(~0u, [&](float x) { chunk = fmaxf(chunk, x); }, [&](int at, const float(&)[kEach]) {
       const int step = (at - r.lo) / kStep + 1;
       if (step & ((1 << r.chunk_log) - 1) && at + kStep < r.hi) return;
       chunk = warp_max(chunk);
@@ -839,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     }
     const Level first{0u, 0u, -1};
     Sum all;
-    r.each(~0u, lane, [&](float x) {
+    r.each(~0u, [&](float x) {
       const uint32_t d = depth(x, r.M, r.inv);
       const float w = weight(d);
       if (filters) {
