@@ -216,7 +216,7 @@ template <typename T>
 struct Row {
   const T *base;
   int skip, end;
-  int lo, hi;         // this warp's piece, whole vectors (but for the last one's end)
+  int lo, hi;         // this warp's piece, whole steps (but for the last one's end)
   int chunk_log;      // steps of a chunk: 2^chunk_log
   float chunk_top;    // lane c: the largest logit of chunk c
   float M, inv;
@@ -249,20 +249,28 @@ struct Row {
         for (int e = 0; e < kN; ++e) x[k * kN + e] = value(reinterpret_cast<const T *>(&q)[e]);
       }
     } else {
+      const int i = i0 + lane * kN;
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k) {
-        const int i = i0 + (32 * k + lane) * kN;
-#pragma unroll
-        for (int e = 0; e < kN; ++e)
-          x[k * kN + e] = i + e >= skip && i + e < b ? value(base[i + e]) : -CUDART_INF_F;
+      for (int j = 0; j < kEach; ++j) {
+        const int at = i + 32 * kN * (j / kN) + j % kN;
+        const float v = value(base[min(max(at, skip), end - 1)]);
+        x[j] = at >= skip && at < b ? v : -CUDART_INF_F;
       }
     }
+  }
+  // Element k of a lane's step (its registers cannot be indexed).
+  __device__ static float element(const float (&x)[kEach], int k) {
+    float l = x[0];
+#pragma unroll
+    for (int i = 1; i < kEach; ++i) l = i == k ? x[i] : l;
+    return l;
   }
   // The index of element j of a lane's step at i0.
   __device__ int index(int i0, int j, int lane) const { return i0 + (32 * (j / kN) + lane) * kN + j % kN - skip; }
 
   // The first step from s on whose chunk is alive.
   __device__ int next(int s, int steps, uint32_t alive) const {
+#pragma unroll 1
     while (s < steps && !((alive >> (s >> chunk_log)) & 1u)) ++s;
     return s;
   }
@@ -271,6 +279,7 @@ struct Row {
   template <typename F, typename G>
   __device__ void each(uint32_t alive, F f, G g) const {
     const int steps = (hi - lo + kStep - 1) / kStep, lane = threadIdx.x & 31;
+#pragma unroll 1
     for (int s = next(0, steps, alive); s < steps; s = next(s + 1, steps, alive)) {
       float x[kEach];
       const int at = lo + s * kStep;
@@ -324,6 +333,7 @@ struct Sampler {
   // Counts of q's level in sh.hist, of the tokens with |x|'s bits in [from, to).
   __device__ void count() {
     const Search &q = sh.q;
+#pragma unroll 1
     for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
     __syncthreads();
     const uint32_t from = q.from, to = q.to;
@@ -360,6 +370,7 @@ struct Sampler {
     n_run = (uint32_t)warp_scan(n_run, lane);
     if (lane == 31) sh.scan_n[warp] = n_run, sh.scan_s[warp] = e_run;
     __syncthreads();
+#pragma unroll 1
     for (int i = 0; i < warp; ++i) n_run += sh.scan_n[i], e_run += sh.scan_s[i];
     sh.at_n[threadIdx.x] = n_run - n_mine;
     sh.at_e[threadIdx.x] = e_run - e_mine;
@@ -381,6 +392,7 @@ struct Sampler {
     const Search &q = sh.q;
     uint32_t n_run = sh.at_n[threadIdx.x];
     u64 e_run = sh.at_e[threadIdx.x], everything = 0;
+#pragma unroll 1
     for (int c = 0; c < cluster; ++c) {
       if (c < rank) n_run += (uint32_t)sh.share[0][c], e_run += sh.share[1][c];
       everything += sh.share[1][c];
@@ -400,11 +412,13 @@ struct Sampler {
       const u64 e_to = e_run + q.lv.estimate(b, c), was = q.by_sum ? e_run : n_run, is = q.by_sum ? e_to : n_to;
       auto here = [&](u64 t) { return b >= first && b <= last && (b == first || was < t) && (b == last || is >= t); };
       if (here(low))
+#pragma unroll 1
         for (int x = 0; x < cluster; ++x) {
           store_remote(remote(&sh.taken[0], x), (u64)b << 32 | n_run);
           store_remote(remote(&sh.taken[2], x), e_run);
         }
       if (here(high))
+#pragma unroll 1
         for (int x = 0; x < cluster; ++x) store_remote(remote(&sh.taken[1], x), (u64)b << 32 | n_to);
       n_run = n_to;
       e_run = e_to;
@@ -453,6 +467,7 @@ struct Sampler {
       if (lane == 31) sh.scan_s[warp] = run;
       __syncthreads();
       run += by_sum ? before_s : before_n;
+#pragma unroll 1
       for (int k = 0; k < warp; ++k) run += sh.scan_s[k];
       const u64 was = run - (by_sum ? my_s : (u64)my_n);
       if (was < target && target <= run) {
@@ -484,6 +499,7 @@ struct Sampler {
       __syncthreads();
     }
     // a few: ranked in every warp's lanes
+#pragma unroll 1
     for (int i = threadIdx.x; i < listed; i += kThreads) {
       uint2 q;
       uint32_t key;
@@ -520,8 +536,7 @@ struct Sampler {
     return warp_sum(x);
   }
 
-  // Lists this piece's tokens with |x|'s bits in [from, to); the sum of W of those before (kSum false: there are none).
-  template <bool kSum>
+  // Lists this piece's tokens with |x|'s bits in [from, to); the sum of W of those before.
   __device__ u64 list_pass(uint32_t from, uint32_t to) {
     uint2 *list = sh.list[warp];
     Sum above;
@@ -530,29 +545,28 @@ struct Sampler {
     n = 0;
     r.each(r.alive(to), [&](float l) {
       const uint32_t d = depth(l, r.M, r.inv);
-      if (kSum) {  // (without a branch: in most warps some lane has a token before the bins)
+      if (from) {  // (without a branch on d: in most warps some lane has a token before the bins)
         const float w = weight(d);
         above.add(d < from ? w : 0.f);
       }
-      marked |= (uint32_t)(kSum ? d - from < to - from : d < to) << j++;
+      marked |= (uint32_t)(d - from < to - from) << j++;
     }, [&](int at, const float(&x)[kEach]) {
       above.carry();
       j = 0;
-      const uint32_t some = __reduce_or_sync(0xffffffffu, marked);
-      if (some) {
-#pragma unroll
-        for (int k = 0; k < kEach; ++k)
-          if ((some >> k) & 1u) {
-            const uint32_t d = depth(x[k], r.M, r.inv), v = (uint32_t)r.index(at, k, lane);
-            const bool mine = (marked >> k) & 1u && r.inside(d, v);
-            const uint32_t who = __ballot_sync(0xffffffffu, mine), place = n + __popc(who & ((1u << lane) - 1));
-            if (mine && place < kWarpList) list[place] = make_uint2(d, v);
-            n += __popc(who);
-          }
+      // (one copy of this, not eight: the kernel's code has to stay in the instruction caches)
+      uint32_t some = __reduce_or_sync(0xffffffffu, marked);
+#pragma unroll 1
+      for (; some; some &= some - 1) {
+        const int k = __ffs(some) - 1;
+        const uint32_t d = depth(Row<T>::element(x, k), r.M, r.inv), v = (uint32_t)r.index(at, k, lane);
+        const bool mine = (marked >> k) & 1u && r.inside(d, v);
+        const uint32_t who = __ballot_sync(0xffffffffu, mine), place = n + __popc(who & ((1u << lane) - 1));
+        if (mine && place < kWarpList) list[place] = make_uint2(d, v);
+        n += __popc(who);
       }
       marked = 0;
     });
-    return kSum ? warp_sum(above.total) : 0;
+    return warp_sum(above.total);
   }
 
   // The border among tokens of one |x| (bits d): the first `ties` of them stay.
@@ -566,6 +580,7 @@ struct Sampler {
                         depth(Row<T>::value(r.base[at]), r.M, r.inv) == d;
         uint32_t who = __ballot_sync(0xffffffffu, eq);
         if (ties <= run + __popc(who)) {
+#pragma unroll 1
           while (++run < ties) who &= who - 1;
           if (lane < cluster)
             store_remote(remote(&sh.result[0], lane), (u64)d << 32 | (uint32_t)(i + __ffs(who) - 1 - r.skip));
@@ -639,12 +654,13 @@ struct Sampler {
       }
       // ---- the exact sum of what lies before the bins, and their tokens
       const uint2 *list = sh.list[warp];
-      above_here = whole ? list_pass<false>(from, to) : list_pass<true>(from, to);
+      above_here = list_pass(from, to);
       __syncwarp();
       // their own sum
       u64 within = 0;
       if (q.by_sum) {
         if (n <= kWarpList)
+#pragma unroll 1
           for (int i = lane; i < (int)n; i += 32) within += whole_weight(weight(list[i].x));
         else
           r.each_slowly(r.lo, r.hi, lane, [&](uint32_t d, uint32_t v) {
@@ -659,6 +675,7 @@ struct Sampler {
       const bool fits = N <= kList && !__any_sync(0xffffffffu, posted(1, lane) > kWarpList || posted(1, lane + 32) > kWarpList);
       if (!low && !high && fits) {
         // to the first CTA
+#pragma unroll 1
         for (int i = lane; i < (int)n; i += 32) {
           const uint2 t = list[i];
           store_remote(remote(&sh.all[N_before + i], 0), (u64)t.y << 32 | t.x);
@@ -729,6 +746,7 @@ struct Sampler {
     r.last = (uint32_t)sh.result[0];
     sum = sh.result[1];
     u64 x = 0;
+#pragma unroll 1
     for (int i = lane; i < (int)n; i += 32) {
       const uint2 t = sh.list[warp][i];
       if (r.inside(t.x, t.y)) x += whole_weight(weight(t.x));
@@ -760,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   r.base = l - r.skip;
   r.end = r.skip + a.vocab;
   constexpr int kN = Row<T>::kN;
-  const int seg = ((r.end + s.pieces - 1) / s.pieces + kN - 1) / kN * kN;
+  const int seg = ((r.end + s.pieces - 1) / s.pieces + kStep - 1) / kStep * kStep;
   r.lo = min(s.piece * seg, r.end);
   r.hi = min(r.lo + seg, r.end);
   r.chunk_log = max(0, 32 - __clz(max(seg - 1, 0) / (32 * kStep)));  // at most 32 chunks
@@ -813,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     r.inv = endless ? CUDART_INF_F : 1.f;
     uint32_t at = UINT_MAX;
     if (r.alive(1u))
+#pragma unroll 1
       for (int i = max(r.lo, r.skip) + lane; i < r.hi && at == UINT_MAX; i += 32)
         if (Row<T>::value(r.base[i]) == top) at = (uint32_t)(i - r.skip);
     s.template exchange<1>((u64)__reduce_min_sync(0xffffffffu, at));
@@ -829,28 +848,25 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     const bool some = k > 0 && k < a.vocab, part = p < 1.f, filters = some || part;
     // ---- the sum of W, and where the tokens lie
     if (filters) {
+#pragma unroll 1
       for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
       __syncthreads();
     }
     const Level first{0u, 0u, -1};
+    const float least_w = r.least;
+    if (filters) r.least = 0.f;  // (min_p comes last)
     Sum all;
     r.each(~0u, [&](float x) {
       const uint32_t d = depth(x, r.M, r.inv);
       const float w = weight(d);
-      if (filters) {
-        all.add(w);
-        atomicAdd(&sh.hist[first.bin(d)], 1u);
-      } else {
-        all.add(w >= r.least ? w : 0.f);
-      }
+      all.add(w >= r.least ? w : 0.f);
+      if (filters) atomicAdd(&sh.hist[first.bin(d)], 1u);
     }, [&](int, const float(&)[kEach]) { all.carry(); });
     u64 mine = warp_sum(all.total);
     s.template exchange<1>(mine);
     total = s.told(0);
     if (filters) {
       const u64 S = total;
-      const float least_w = r.least;  // (min_p comes last)
-      r.least = 0.f;
 #pragma unroll 1
       for (int by_sum = some ? 0 : 1; by_sum < (part ? 2 : 1); ++by_sum)
         if (!listed || s.rank == 0)
@@ -902,42 +918,54 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
         const int p0 = min(sh.hit * seg, r.end), p1 = min(p0 + seg, r.end);
         const int sub = ((p1 - p0 + kWarps - 1) / kWarps + kN - 1) / kN * kN;
         const int s0 = min(p0 + warp * sub, p1), s1 = min(s0 + sub, p1);
-        u64 own = 0;
+        // (a vector's elements lie one after another, then the next lane's: sums of each vector of a lane)
+        constexpr int kVecs = Row<T>::kVecs;
+        u64 own = 0, part[kVecs] = {};
         float x[kEach];
+        auto weigh = [&](int at, int j) {
+          return whole_weight(r.kept(depth(Row<T>::element(x, j), r.M, r.inv), (uint32_t)r.index(at, j, lane)));
+        };
+        auto sums = [&](int at) {
+          r.load(at, s1, lane, x);
+#pragma unroll
+          for (int k = 0; k < kVecs; ++k) part[k] = 0;
+#pragma unroll 1
+          for (int j = 0; j < kEach; ++j) {
+            const u64 w = weigh(at, j);
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) part[k] += j / kN == k ? w : 0;
+          }
+        };
 #pragma unroll 1
         for (int at = s0; at < s1; at += kStep) {
-          r.load(at, s1, lane, x);
-          Sum step;
+          sums(at);
 #pragma unroll
-          for (int j = 0; j < kEach; ++j)
-            step.add(r.kept(depth(x[j], r.M, r.inv), (uint32_t)r.index(at, j, lane)));
-          step.carry();
-          own += step.total;
+          for (int k = 0; k < kVecs; ++k) own += part[k];
         }
         own = warp_sum(own);
         if (lane == 0) sh.scan_s[warp] = own;
         __syncthreads();
         u64 run = 0;
+#pragma unroll 1
         for (int i = 0; i < warp; ++i) run += sh.scan_s[i];
         if (run <= left && left < run + own) {
 #pragma unroll 1
           for (int at = s0; at < s1 && run <= left; at += kStep) {
-            if (sub > kStep) r.load(at, s1, lane, x);
+            if (sub > kStep) sums(at);
 #pragma unroll
-            for (int j0 = 0; j0 < kEach; j0 += kN) {  // a vector's elements lie one after another, then the next lane's
-              u64 w[kN], w_all = 0;
-#pragma unroll
-              for (int e = 0; e < kN; ++e) {
-                w[e] = whole_weight(r.kept(depth(x[j0 + e], r.M, r.inv), (uint32_t)r.index(at, j0 + e, lane)));
-                w_all += w[e];
-              }
-              u64 incl = run + warp_scan(w_all, lane), at_e = incl - w_all;
-              if (at_e <= left && left < incl)
-#pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                  if (at_e <= left && left < at_e + w[e]) a.tokens[row] = r.index(at, j0 + e, lane);
-                  at_e += w[e];
+            for (int k = 0; k < kVecs; ++k) {
+              const u64 incl = run + warp_scan(part[k], lane);
+              u64 before_it = incl - part[k];
+              if (before_it <= left && left < incl) {
+#pragma unroll 1
+                for (int j = k * kN; j < (k + 1) * kN; ++j) {
+                  before_it += weigh(at, j);
+                  if (left < before_it) {
+                    a.tokens[row] = r.index(at, j, lane);
+                    break;
+                  }
                 }
+              }
               run = __shfl_sync(0xffffffffu, incl, 31);
             }
           }
@@ -958,15 +986,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
         static_cast<float *>(a.probs)[out + v] = q;
     };
     if (empty || listed) {
+#pragma unroll 1
       for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) put((uint32_t)(i - r.skip), 0.f);
       __syncwarp();
       if (listed)
+#pragma unroll 1
         for (int i = lane; i < (int)s.n; i += 32) {
           const uint2 t = sh.list[warp][i];
           const float w = r.kept(t.x, t.y);
           if (w > 0.f) put(t.y, (float)whole_weight(w));
         }
     } else {
+#pragma unroll 1
       for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) {
         const uint32_t d = depth(Row<T>::value(r.base[i]), r.M, r.inv), v = (uint32_t)(i - r.skip);
         put(v, r.inside(d, v) ? (float)whole_weight(r.kept(d, v)) : 0.f);
@@ -1000,6 +1031,7 @@ cudaError_t launch(const SampleArgs &a, int cluster, cudaStream_t s) {
 cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t s) {
   // the largest cluster with which all rows run at once
   int cluster = kMaxCluster;
+#pragma unroll 1
   while (cluster > 1 && (long long)a.rows * cluster > (long long)kPerSm * sms) cluster /= 2;
   return a.dtype == PSKV_DTYPE_BF16 ? launch<uint16_t>(a, cluster, s) : launch<float>(a, cluster, s);
 }
