@@ -186,14 +186,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 class _PythonCalls:
     """Stands for the compiled calls where there are none: each leaves its call to the Python form."""
 
-    append = decode = prefill = verify = staticmethod(lambda *args: None)
+    append = decode = prefill = verify = sample = walk = keep = fork = staticmethod(lambda *args: None)
 
 
-_calls = None  # bound by the first call of a latent operator
+_calls = None  # bound by the first call of an operator that has a compiled form
 
 
 def _bind_calls(lib):
-    """The compiled forms of the latent operators' calls, entering this library; where they are missing
+    """The compiled forms of the operators' calls, entering this library; where they are missing
     or were built for another Python or PyTorch, the Python forms do their work."""
     global _calls
     from . import build
@@ -203,7 +203,8 @@ def _bind_calls(lib):
         try:
             from . import _calls as calls
             calls.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-                lib.kv_prep_append_latent, lib.decode_attn_latent, lib.prefill_attn_expanded, lib.verify_drafts)])
+                lib.kv_prep_append_latent, lib.decode_attn_latent, lib.prefill_attn_expanded, lib.verify_drafts,
+                lib.decode_attn_latent_tree, lib.sample_tokens, lib.verify_tree, lib.kv_keep_tokens, lib.kv_fork_rows)])
         except ImportError as e:
             calls, why = _PythonCalls, str(e)
     if calls is _PythonCalls:
@@ -879,6 +880,13 @@ def decode_attn_latent_tree(layout: Layout, q, page_tables, seq_lens, seq_lens_h
     (device int64 or uint64 [batch, tokens]), each token's ancestor bits, itself included.  Token t
     attends every key before the window and the window tokens its mask marks.  Workspaces are
     decode_attn_latent's."""
+    lib = _LIB or load_library()
+    if not merge_group and events is None:
+        r = (_calls or _bind_calls(lib)).decode(*layout._pool, q, page_tables, seq_lens, seq_lens_host, scale, num_splits, workspace, out,
+                          PSKV_DTYPE_BF16 if out_dtype is None else _OUT_CODES.get(out_dtype, -1),
+                          None if stream is None else _stream(stream), tree_mask)
+        if r is not None:
+            return r if type(r) is not int else _check(r, "decode_attn_latent_tree")
     return _decode_latent(True, layout, q, page_tables, seq_lens, seq_lens_host, tree_mask, scale, num_splits,
                           workspace, out, out_dtype, merge_group, events, stream)
 
@@ -1001,6 +1009,10 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
     ``probs`` (f32 or bf16, of logits' shape) is filled with the filtered distribution, as
     verify_drafts takes it.  Returns ``tokens`` int32 of u's shape; with ``u`` None only ``probs`` is made."""
     lib = _LIB or load_library()
+    r = (_calls or _bind_calls(lib)).sample(logits, u, temperature, top_k, top_p, min_p, tokens, probs, status,
+                                            None if stream is None else _stream(stream))
+    if r is not None:
+        return r if type(r) is not int else _check(r, "sample_tokens")
     dev = _current_device()
     shape = logits.shape
     if len(shape) not in (2, 3):
@@ -1033,6 +1045,10 @@ def verify_tree(drafts, tree_mask, sampled, tokens=None, path=None, kept=None, s
     token behind each (sample_tokens).  Returns (``tokens`` int32 [batch, tokens]: what the text goes on with, then
     -1s; ``path`` int32 [batch, tokens]: the standing tokens' places, then -1s; ``kept`` int32 [batch])."""
     lib = _LIB or load_library()
+    r = (_calls or _bind_calls(lib)).walk(drafts, tree_mask, sampled, tokens, path, kept, status,
+                                          None if stream is None else _stream(stream))
+    if r is not None:
+        return r if type(r) is not int else _check(r, "verify_tree")
     dev, i32 = _current_device(), torch.int32
     if drafts.dim() != 2:
         raise ValueError("drafts must be [batch, tokens]")
@@ -1048,13 +1064,19 @@ def verify_tree(drafts, tree_mask, sampled, tokens=None, path=None, kept=None, s
     return tokens, path, kept
 
 
-def _handles(layouts, dev: int):
-    """The handles of one layout or a list of them (layers that share the page tables)."""
-    layouts = [layouts] if isinstance(layouts, Layout) else layouts
-    for l in layouts:
-        if l._pool[1] != dev:
-            raise ValueError(f"a pool is on {l.k_pool.device}, the current device is cuda:{dev}")
-    return (ctypes.c_void_p * len(layouts))(*[l._pool[0] for l in layouts]), len(layouts)
+def _handles(layouts):
+    """The handles of one layout or a list of them (layers that share the page tables), and their device
+    (-1: not one device)."""
+    if isinstance(layouts, Layout):
+        return (layouts._pool[0],), layouts._pool[1]
+    devices = {l._pool[1] for l in layouts}
+    return tuple([l._pool[0] for l in layouts]), devices.pop() if len(devices) == 1 else -1
+
+
+def _on_device(handles, of: int, dev: int):
+    if of != dev and handles:
+        raise ValueError(f"the pools are not open on the current device, cuda:{dev}")
+    return (ctypes.c_void_p * len(handles))(*handles), len(handles)
 
 
 def kv_keep_tokens(layouts, page_tables, seq_lens, path, kept, new_lens=None, stream=None) -> torch.Tensor:
@@ -1063,8 +1085,13 @@ def kv_keep_tokens(layouts, page_tables, seq_lens, path, kept, new_lens=None, st
     that share ``page_tables``).  ``path`` int32 [batch, tokens] and ``kept`` int32 [batch] are
     verify_tree's.  Returns ``new_lens`` int32 [batch], w0 + kept (its own memory, not ``seq_lens``)."""
     lib = _LIB or load_library()
+    handles, of = _handles(layouts)
+    r = (_calls or _bind_calls(lib)).keep(handles, of, page_tables, seq_lens, path, kept, new_lens,
+                                          None if stream is None else _stream(stream))
+    if r is not None:
+        return r if type(r) is not int else _check(r, "kv_keep_tokens")
     dev, i32 = _current_device(), torch.int32
-    handles, n = _handles(layouts, dev)
+    handles, n = _on_device(handles, of, dev)
     if path.dim() != 2 or page_tables.dim() != 2:
         raise ValueError("path must be [batch, tokens], page_tables [batch, stride]")
     batch, t = path.shape
@@ -1083,8 +1110,13 @@ def kv_fork_rows(layouts, src, dst, new_pages, page_tables, seq_lens, pages_of_r
     keys end inside of is copied into ``new_pages`` [n], in the pools of ``layouts`` (a Layout, or a list of layers').
     ``page_tables``, ``seq_lens`` and ``pages_of_row`` (int32, on the device) are updated in place."""
     lib = _LIB or load_library()
+    handles, of = _handles(layouts)
+    r = (_calls or _bind_calls(lib)).fork(handles, of, src, dst, new_pages, page_tables, seq_lens, pages_of_row,
+                                          None if stream is None else _stream(stream))
+    if r is not None:
+        return _check(r, "kv_fork_rows")
     dev, i32 = _current_device(), torch.int32
-    handles, layers = _handles(layouts, dev)
+    handles, layers = _on_device(handles, of, dev)
     if page_tables.dim() != 2:
         raise ValueError("page_tables must be [batch, stride]")
     batch, stride = page_tables.shape

@@ -4,8 +4,6 @@
 // Both move 16-byte vectors as they are: a stored row of one head is k_vecs vectors in the K region
 // and v_vecs in the V region, and a token's row of one layer heads * (k_vecs + v_vecs) of them
 // (8 KB at head dim 512 with four KV heads, 1,152 bytes of a latent row).
-#include <algorithm>
-
 #include "pskv_internal.cuh"
 #include "tree.h"
 
@@ -29,6 +27,11 @@ struct Column {
   }
   __device__ uint4 *at(long long row) const { return base + row * vecs; }
 };
+
+// Pieces of a page's rows of one head.
+__host__ __device__ int pieces(int vecs, int page_size) {
+  return (vecs * page_size + kThreads * kAhead - 1) / (kThreads * kAhead);
+}
 
 }  // namespace
 
@@ -83,8 +86,9 @@ __global__ void __launch_bounds__(kThreads) pskv_keep_tokens(const KeepArgs a, c
   }
 }
 
-// Grid (pieces of a page, forks, layers).  As above, every block checks its fork alike; the first one reports,
-// and writes the row's table, length and lease.  Sources are rows that no fork of the call writes.
+// Grid (pieces of a page, forks, layers): a piece is kThreads * kAhead vectors of one region's head, whose rows lie
+// one after another.  As above, every block checks its fork alike; the first one reports, and writes the row's table,
+// length and lease.  Sources are rows that no fork of the call writes.
 __global__ void __launch_bounds__(kThreads) pskv_fork_rows(const ForkArgs a, const __grid_constant__ Pools p) {
   const int f = blockIdx.y, i = threadIdx.x;
   const bool first = blockIdx.x == 0 && blockIdx.z == 0;
@@ -128,29 +132,22 @@ __global__ void __launch_bounds__(kThreads) pskv_fork_rows(const ForkArgs a, con
       a.pages_of_row[dst] = pages;
     }
   }
-  // the rows in a page's order: of each region and head, rest * vecs vectors in one run
-  const int k_run = rest * p.k_vecs, v_run = rest * p.v_vecs, all = p.heads * (k_run + v_run);
-  const long long old_row = (long long)old_page * p.heads * p.page_size, new_row = (long long)new_page * p.heads * p.page_size;
-  for (int u0 = blockIdx.x * kThreads * kAhead + i; u0 < all; u0 += gridDim.x * kThreads * kAhead) {
-    uint4 x[kAhead];
-    uint4 *where[kAhead];
+  // this block's piece: of a K head, or behind these of a V head
+  const int k_pieces = pieces(p.k_vecs, p.page_size), v_pieces = pieces(p.v_vecs, p.page_size);
+  const bool is_k = (int)blockIdx.x < p.heads * k_pieces;
+  const int x = is_k ? blockIdx.x : blockIdx.x - p.heads * k_pieces, each = is_k ? k_pieces : v_pieces;
+  const int head = x / each, vecs = is_k ? p.k_vecs : p.v_vecs, run = rest * vecs;
+  const int u0 = (x - head * each) * kThreads * kAhead + i;
+  uint4 *pool = static_cast<uint4 *>(is_k ? p.k[blockIdx.z] : p.v[blockIdx.z]);
+  const uint4 *old_run = pool + ((size_t)old_page * p.heads + head) * p.page_size * vecs;
+  uint4 *new_run = pool + ((size_t)new_page * p.heads + head) * p.page_size * vecs;
+  uint4 q[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int u = u0 + k * kThreads;
-      if (u < all) {
-        const bool is_k = u < p.heads * k_run;
-        const int run = is_k ? k_run : v_run, vecs = is_k ? p.k_vecs : p.v_vecs;
-        const int e = is_k ? u : u - p.heads * k_run, head = e / run;
-        uint4 *pool = static_cast<uint4 *>(is_k ? p.k[blockIdx.z] : p.v[blockIdx.z]);
-        const size_t off = (size_t)head * p.page_size * vecs + (e - head * run);
-        x[k] = __ldcs(pool + (size_t)old_row * vecs + off);
-        where[k] = pool + (size_t)new_row * vecs + off;
-      }
-    }
+  for (int k = 0; k < kAhead; ++k)
+    if (u0 + k * kThreads < run) q[k] = old_run[u0 + k * kThreads];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (u0 + k * kThreads < all) *where[k] = x[k];
-  }
+  for (int k = 0; k < kAhead; ++k)
+    if (u0 + k * kThreads < run) new_run[u0 + k * kThreads] = q[k];
 }
 
 cudaError_t launch_keep(const KeepArgs &a, const Pools &p, cudaStream_t s) {
@@ -160,9 +157,8 @@ cudaError_t launch_keep(const KeepArgs &a, const Pools &p, cudaStream_t s) {
 }
 
 cudaError_t launch_fork(const ForkArgs &a, const Pools &p, cudaStream_t s) {
-  const long long vecs = (long long)p.heads * (p.k_vecs + p.v_vecs) * p.page_size;
-  const long long blocks = (vecs + kThreads * kAhead - 1) / (kThreads * kAhead);
-  const dim3 grid((unsigned)std::min(blocks, 1024LL), (unsigned)a.n, (unsigned)p.count);
+  const dim3 grid((unsigned)(p.heads * (pieces(p.k_vecs, p.page_size) + pieces(p.v_vecs, p.page_size))),
+                  (unsigned)a.n, (unsigned)p.count);
   return launch_pdl(pskv_fork_rows, grid, dim3(kThreads), 0, s, a, p);
 }
 

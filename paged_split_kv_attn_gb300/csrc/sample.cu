@@ -545,10 +545,8 @@ struct Sampler {
     n = 0;
     r.each(r.alive(to), [&](float l) {
       const uint32_t d = depth(l, r.M, r.inv);
-      if (from) {  // (without a branch on d: in most warps some lane has a token before the bins)
-        const float w = weight(d);
-        above.add(d < from ? w : 0.f);
-      }
+      const float w = weight(d);  // (without a branch: in most warps some lane has a token before the bins)
+      above.add(d < from ? w : 0.f);
       marked |= (uint32_t)(d - from < to - from) << j++;
     }, [&](int at, const float(&x)[kEach]) {
       above.carry();

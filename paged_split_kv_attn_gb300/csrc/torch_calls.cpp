@@ -1,4 +1,4 @@
-// torch_calls.cpp -- the latent operators' Python calls, compiled (module _calls).
+// torch_calls.cpp -- the Python calls of the latent, sampling, tree and row operators, compiled (module _calls).
 //
 // A decode step's kernels take 3 to 20 us, and the same calls through ctypes took 15 to 19 us of
 // host time: the output's allocation and the checks of a dozen tensors run cold after every
@@ -27,6 +27,11 @@ decltype(&::kv_prep_append_latent) g_append = nullptr;
 decltype(&::decode_attn_latent) g_decode = nullptr;
 decltype(&::prefill_attn_expanded) g_prefill = nullptr;
 decltype(&::verify_drafts) g_verify = nullptr;
+decltype(&::decode_attn_latent_tree) g_tree = nullptr;
+decltype(&::sample_tokens) g_sample = nullptr;
+decltype(&::verify_tree) g_walk = nullptr;
+decltype(&::kv_keep_tokens) g_keep = nullptr;
+decltype(&::kv_fork_rows) g_fork = nullptr;
 
 constexpr auto kBf16 = at::kBFloat16;
 constexpr auto kI32 = at::kInt;
@@ -180,11 +185,16 @@ struct Pool {
   }
 };
 
-// q, page_tables, seq_lens, seq_lens_host, scale, num_splits, workspace, out, code, stream
+// A window's ancestor masks: 64-bit integers, signed or not.
+bool masks(PyObject *o, int dev, Shape shape, void **p) {
+  return whole(o, at::kLong, dev, shape, p) || whole(o, at::kUInt64, dev, shape, p);
+}
+
+// q, page_tables, seq_lens, seq_lens_host, scale, num_splits, workspace, out, code, stream[, tree_mask]
 PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     Pool pool;
-    NEED(n == 14 && pool.read(a));
+    NEED((n == 14 || n == 15) && pool.read(a));
     const int dev = (int)pool.dev;
     const at::Tensor *q = tensor(a[4]), *table = tensor(a[5]);
     NEED(q && table && q->dim() == 4 && table->dim() == 2);
@@ -198,6 +208,8 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     NEED(whole(a[5], kI32, dev, {batch, stride}, &tp) && whole(a[6], kI32, dev, {batch}, &lp));
     NEED(whole_numbers(a[7], lens) && (int64_t)lens.size() == batch && number(a[8], &scale));
     NEED(integer(a[9], INT32_MIN, INT32_MAX, &splits) && integer(a[12], -1, 1 << 20, &code));
+    void *mp = nullptr;
+    NEED(n == 14 || masks(a[14], dev, {batch, tokens}, &mp));
     void *wp = nullptr;  // without a workspace: for plans that need none
     size_t bytes = 0;
     if (a[10] != Py_None) {
@@ -214,9 +226,12 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *op = out.data_ptr();
     int rc;
     Py_BEGIN_ALLOW_THREADS
-    rc = g_decode(static_cast<const pskv_layout *>(pool.layout), qp, (const int32_t *)tp, (int32_t)stride,
-                  lens.data(), (const int32_t *)lp, (int32_t)batch, (int32_t)tokens, (int32_t)heads,
-                  (float)scale, (int32_t)splits, wp, bytes, op, dtype, nullptr, s);
+    rc = n == 14 ? g_decode(static_cast<const pskv_layout *>(pool.layout), qp, (const int32_t *)tp, (int32_t)stride,
+                            lens.data(), (const int32_t *)lp, (int32_t)batch, (int32_t)tokens, (int32_t)heads,
+                            (float)scale, (int32_t)splits, wp, bytes, op, dtype, nullptr, s)
+                 : g_tree(static_cast<const pskv_layout *>(pool.layout), qp, (const int32_t *)tp, (int32_t)stride,
+                          lens.data(), (const int32_t *)lp, (const uint64_t *)mp, (int32_t)batch, (int32_t)tokens,
+                          (int32_t)heads, (float)scale, (int32_t)splits, wp, bytes, op, dtype, nullptr, s);
     Py_END_ALLOW_THREADS
     NEED(wp || rc != PSKV_ERR_WORKSPACE_TOO_SMALL);
     return result(rc, a[11], out);
@@ -373,15 +388,188 @@ PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// A fault word, or None.
+bool fault_word(PyObject *o, int dev, void **p) {
+  *p = nullptr;
+  if (o == Py_None) return true;
+  const at::Tensor *t = tensor(o);
+  if (!t || !t->is_cuda() || t->get_device() != dev || t->scalar_type() != kI32 || !t->is_contiguous()) return false;
+  *p = t->data_ptr();
+  return true;
+}
+
+// A given int32 tensor of this shape, or a new one: its address, and the Python object that the call returns.
+bool result_i32(PyObject *given, const at::Tensor &like, int dev, Shape shape, PyObject *stream, pskv_stream_t s,
+                at::Tensor *made, void **p) {
+  if (given != Py_None) return whole(given, kI32, dev, shape, p);
+  *made = fresh(like, kI32, shape, stream, s, dev);
+  *p = made->data_ptr();
+  return true;
+}
+
+// logits, u, temperature, top_k, top_p, min_p, tokens, probs, status, stream
+PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    NEED(n == 10);
+    const int dev = c10::cuda::current_device();
+    const at::Tensor *l = tensor(a[0]);
+    NEED(l && (l->dim() == 2 || l->dim() == 3) && l->is_cuda() && l->layout() == at::kStrided && l->get_device() == dev);
+    const at::ScalarType kind = l->scalar_type();
+    const bool three = l->dim() == 3;
+    const int64_t batch = l->size(0), each = three ? l->size(1) : 1, vocab = l->size(three ? 2 : 1);
+    NEED((kind == kBf16 || kind == at::kFloat) && batch >= 1 && each >= 1 && vocab >= 1);
+    NEED(batch <= INT32_MAX && each <= INT32_MAX && vocab <= INT32_MAX && (vocab == 1 || l->stride(-1) == 1));
+    // one step from row to row (a stride over a single one says nothing)
+    int64_t step = vocab;
+    if (each > 1) step = l->stride(1);
+    if (batch > 1) {
+      NEED(l->stride(0) % each == 0 && (each == 1 || l->stride(0) / each == step));
+      step = l->stride(0) / each;
+    }
+    NEED(step >= vocab && a[1] != Py_None);
+    void *up, *kp, *hp, *tp, *pp, *mp, *sp, *qp = nullptr;
+    pskv_stream_t s;
+    auto head = [&](PyObject *o, at::ScalarType t, void **p) {
+      return three ? whole(o, t, dev, {batch, each}, p) : whole(o, t, dev, {batch}, p);
+    };
+    NEED(head(a[1], at::kFloat, &up) && maybe(a[2], at::kFloat, dev, {batch}, &hp) && maybe(a[3], kI32, dev, {batch}, &tp));
+    NEED(maybe(a[4], at::kFloat, dev, {batch}, &pp) && maybe(a[5], at::kFloat, dev, {batch}, &mp));
+    NEED(fault_word(a[8], dev, &sp) && stream_of(a[9], dev, &s));
+    int32_t code = PSKV_DTYPE_F32;
+    if (a[7] != Py_None) {
+      const at::Tensor *q = tensor(a[7]);
+      NEED(q && (q->scalar_type() == kBf16 || q->scalar_type() == at::kFloat));
+      NEED(three ? whole(a[7], q->scalar_type(), dev, {batch, each, vocab}, &qp)
+                 : whole(a[7], q->scalar_type(), dev, {batch, vocab}, &qp));
+      code = q->scalar_type() == kBf16 ? PSKV_DTYPE_BF16 : PSKV_DTYPE_F32;
+    }
+    at::Tensor tokens;
+    if (a[6] == Py_None) {
+      tokens = three ? fresh(*l, kI32, {batch, each}, a[9], s, dev) : fresh(*l, kI32, {batch}, a[9], s, dev);
+      kp = tokens.data_ptr();
+    } else {
+      NEED(head(a[6], kI32, &kp));
+    }
+    const pskv_sample_desc f = {(const float *)hp, (const int32_t *)tp, (const float *)pp, (const float *)mp};
+    void *lp = l->data_ptr();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_sample(lp, kind == kBf16 ? PSKV_DTYPE_BF16 : PSKV_DTYPE_F32, step, (int32_t)batch, (int32_t)each,
+                  (int32_t)vocab, &f, (const float *)up, (int32_t *)kp, qp, code, (int32_t *)sp, s);
+    Py_END_ALLOW_THREADS
+    return result(rc, a[6], tokens);
+  });
+}
+
+// drafts, tree_mask, sampled, tokens, path, kept, status, stream
+PyObject *walk(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    NEED(n == 8);
+    const int dev = c10::cuda::current_device();
+    const at::Tensor *drafts = tensor(a[0]);
+    NEED(drafts && drafts->dim() == 2);
+    const int64_t batch = drafts->size(0), t = drafts->size(1);
+    void *dp, *mp, *sp, *kp, *pp, *np, *fp;
+    pskv_stream_t s;
+    NEED(batch <= INT32_MAX && t <= INT32_MAX);
+    NEED(whole(a[0], kI32, dev, {batch, t}, &dp) && masks(a[1], dev, {batch, t}, &mp) && whole(a[2], kI32, dev, {batch, t}, &sp));
+    NEED(fault_word(a[6], dev, &fp) && stream_of(a[7], dev, &s));
+    at::Tensor tokens, path, kept;
+    NEED(result_i32(a[3], *drafts, dev, {batch, t}, a[7], s, &tokens, &kp));
+    NEED(result_i32(a[4], *drafts, dev, {batch, t}, a[7], s, &path, &pp));
+    NEED(result_i32(a[5], *drafts, dev, {batch}, a[7], s, &kept, &np));
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_walk((const int32_t *)dp, (const uint64_t *)mp, (const int32_t *)sp, (int32_t)batch, (int32_t)t,
+                (int32_t *)kp, (int32_t *)pp, (int32_t *)np, (int32_t *)fp, s);
+    Py_END_ALLOW_THREADS
+    if (rc != PSKV_OK) return PyLong_FromLong(rc);
+    PyObject *x = result(rc, a[3], tokens), *y = result(rc, a[4], path), *z = result(rc, a[5], kept), *r = nullptr;
+    if (x && y && z) r = PyTuple_Pack(3, x, y, z);
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    Py_XDECREF(z);
+    return r;
+  });
+}
+
+// Layout addresses of a tuple that Python made of the layouts.
+bool layouts_of(PyObject *o, std::vector<const pskv_layout *> &v) {
+  if (!PyTuple_CheckExact(o)) return false;
+  const Py_ssize_t n = PyTuple_GET_SIZE(o);
+  v.resize((size_t)n);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject *x = PyTuple_GET_ITEM(o, i);
+    if (!PyLong_CheckExact(x)) return false;
+    v[(size_t)i] = static_cast<const pskv_layout *>(PyLong_AsVoidPtr(x));
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      return false;
+    }
+  }
+  return n >= 1 && n <= INT32_MAX;
+}
+
+// layouts (all on device), device, page_tables, seq_lens, path, kept, new_lens, stream
+PyObject *keep(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    std::vector<const pskv_layout *> layouts;
+    long long dev64;
+    NEED(n == 8 && layouts_of(a[0], layouts) && integer(a[1], 0, 1 << 20, &dev64) && dev64 == c10::cuda::current_device());
+    const int dev = (int)dev64;
+    const at::Tensor *table = tensor(a[2]), *path = tensor(a[4]);
+    NEED(table && path && table->dim() == 2 && path->dim() == 2);
+    const int64_t batch = path->size(0), t = path->size(1), stride = table->size(1);
+    void *tp, *lp, *pp, *kp, *np;
+    pskv_stream_t s;
+    NEED(batch <= INT32_MAX && t <= INT32_MAX && stride <= INT32_MAX);
+    NEED(whole(a[2], kI32, dev, {batch, stride}, &tp) && whole(a[3], kI32, dev, {batch}, &lp));
+    NEED(whole(a[4], kI32, dev, {batch, t}, &pp) && whole(a[5], kI32, dev, {batch}, &kp) && stream_of(a[7], dev, &s));
+    at::Tensor lens;
+    NEED(result_i32(a[6], *path, dev, {batch}, a[7], s, &lens, &np));
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_keep(layouts.data(), (int32_t)layouts.size(), (const int32_t *)tp, (int32_t)stride, (const int32_t *)lp,
+                (const int32_t *)pp, (const int32_t *)kp, (int32_t)batch, (int32_t)t, (int32_t *)np, s);
+    Py_END_ALLOW_THREADS
+    return result(rc, a[6], lens);
+  });
+}
+
+// layouts, device, src, dst, new_pages, page_tables, seq_lens, pages_of_row, stream
+PyObject *fork_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    std::vector<const pskv_layout *> layouts;
+    long long dev64;
+    NEED(n == 9 && layouts_of(a[0], layouts) && integer(a[1], 0, 1 << 20, &dev64) && dev64 == c10::cuda::current_device());
+    const int dev = (int)dev64;
+    const at::Tensor *src = tensor(a[2]), *table = tensor(a[5]);
+    NEED(src && table && src->dim() == 1 && table->dim() == 2);
+    const int64_t k = src->size(0), batch = table->size(0), stride = table->size(1);
+    void *sp, *dp, *np, *tp, *lp, *gp;
+    pskv_stream_t s;
+    NEED(k <= INT32_MAX && batch <= INT32_MAX && stride <= INT32_MAX);
+    NEED(whole(a[2], kI32, dev, {k}, &sp) && whole(a[3], kI32, dev, {k}, &dp) && whole(a[4], kI32, dev, {k}, &np));
+    NEED(whole(a[5], kI32, dev, {batch, stride}, &tp) && whole(a[6], kI32, dev, {batch}, &lp));
+    NEED(whole(a[7], kI32, dev, {batch}, &gp) && stream_of(a[8], dev, &s));
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_fork(layouts.data(), (int32_t)layouts.size(), (const int32_t *)sp, (const int32_t *)dp, (const int32_t *)np,
+                (int32_t)k, (int32_t *)tp, (int32_t)stride, (int32_t *)lp, (int32_t *)gp, (int32_t)batch, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+  });
+}
+
 // Addresses of the C entry points: kv_prep_append_latent, decode_attn_latent, prefill_attn_expanded,
-// verify_drafts.
+// verify_drafts, decode_attn_latent_tree, sample_tokens, verify_tree, kv_keep_tokens, kv_fork_rows.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  void *p[4];
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "four addresses");
+  void *p[9];
+  if (n != 9) {
+    PyErr_SetString(PyExc_TypeError, "nine addresses");
     return nullptr;
   }
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 9; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -389,6 +577,11 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   g_decode = reinterpret_cast<decltype(g_decode)>(p[1]);
   g_prefill = reinterpret_cast<decltype(g_prefill)>(p[2]);
   g_verify = reinterpret_cast<decltype(g_verify)>(p[3]);
+  g_tree = reinterpret_cast<decltype(g_tree)>(p[4]);
+  g_sample = reinterpret_cast<decltype(g_sample)>(p[5]);
+  g_walk = reinterpret_cast<decltype(g_walk)>(p[6]);
+  g_keep = reinterpret_cast<decltype(g_keep)>(p[7]);
+  g_fork = reinterpret_cast<decltype(g_fork)>(p[8]);
   Py_RETURN_NONE;
 }
 
@@ -402,6 +595,10 @@ PyMethodDef methods[] = {{"bind", fast<bind>(), METH_FASTCALL, nullptr},
                          {"decode", fast<decode>(), METH_FASTCALL, nullptr},
                          {"prefill", fast<prefill>(), METH_FASTCALL, nullptr},
                          {"verify", fast<verify>(), METH_FASTCALL, nullptr},
+                         {"sample", fast<sample>(), METH_FASTCALL, nullptr},
+                         {"walk", fast<walk>(), METH_FASTCALL, nullptr},
+                         {"keep", fast<keep>(), METH_FASTCALL, nullptr},
+                         {"fork", fast<fork_rows>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
