@@ -972,36 +972,53 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     }
   }
   if (a.probs) {
-    // W / S, W being floats: 1 / S as a float pair
+    // W / S, W being floats: 1 / S as a float pair.  A step's values go through shared memory, so that they leave in
+    // whole lines wherever the row begins
     const double inv = 1.0 / (double)total;
     const float hi = (float)inv, lo = (float)(inv - (double)hi);
     const size_t out = (size_t)row * a.vocab;
-    auto put = [&](uint32_t v, float w) {
-      const float q = fmaf(w, hi, w * lo);
+    auto put = [&](int v, float q) {
       if (a.probs_dtype == PSKV_DTYPE_BF16)
         static_cast<__nv_bfloat16 *>(a.probs)[out + v] = __float2bfloat16_rn(q);
       else
         static_cast<float *>(a.probs)[out + v] = q;
     };
-    if (empty || listed) {
+    auto share_of = [&](float w) {
+      const float W = rintf(w * 0x1p40f);
+      return fmaf(W, hi, W * lo);
+    };
+    const uint32_t alive = empty || listed ? 0 : r.alive(r.border + 1);
+    float *stage = reinterpret_cast<float *>(sh.list[warp]);  // (of a listed row nothing is staged)
+    static_assert(sizeof sh.list[0] >= kStep * sizeof(float), "room for a step");
 #pragma unroll 1
-      for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) put((uint32_t)(i - r.skip), 0.f);
-      __syncwarp();
-      if (listed)
-#pragma unroll 1
-        for (int i = lane; i < (int)s.n; i += 32) {
-          const uint2 t = sh.list[warp][i];
-          const float w = r.kept(t.x, t.y);
-          if (w > 0.f) put(t.y, (float)whole_weight(w));
+    for (int s0 = r.lo, step = 0; s0 < r.hi; s0 += kStep, ++step) {
+      const bool live = (alive >> (step >> r.chunk_log)) & 1u;
+      if (live) {
+        float x[kEach];
+        r.load(s0, r.hi, lane, x);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const int at = 32 * kN * (j / kN) + lane * kN + j % kN;
+          stage[at] = share_of(r.kept(depth(x[j], r.M, r.inv), (uint32_t)(s0 + at - r.skip)));
         }
-    } else {
-#pragma unroll 1
-      for (int i = max(r.lo, r.skip) + lane; i < r.hi; i += 32) {
-        const uint32_t d = depth(Row<T>::value(r.base[i]), r.M, r.inv), v = (uint32_t)(i - r.skip);
-        put(v, r.inside(d, v) ? (float)whole_weight(r.kept(d, v)) : 0.f);
+        __syncwarp();
       }
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int at = s0 + 32 * j + lane;
+        if (at >= r.skip && at < r.hi) put(at - r.skip, live ? stage[32 * j + lane] : 0.f);
+      }
+      __syncwarp();
     }
+    if (listed)
+#pragma unroll 1
+      for (int i = lane; i < (int)s.n; i += 32) {
+        const uint2 t = sh.list[warp][i];
+        const float w = r.kept(t.x, t.y);
+        if (w > 0.f) put((int)t.y, share_of(w));
+      }
   }
+
 }
 
 namespace {
