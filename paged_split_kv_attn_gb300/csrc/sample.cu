@@ -42,6 +42,7 @@ constexpr int kPerSm = 4;        // CTAs an SM holds (registers)
 constexpr int kBins = 2048;
 constexpr int kList = 1024;      // listed tokens of a cluster,
 constexpr int kWarpList = kList / kWarps;  // and of a warp
+constexpr int kCountBits = 23;   // of a number that holds a count (up to 2^22) and an estimate (up to 2^40)
 constexpr int kEach = 8;         // elements a lane takes in a step
 constexpr int kStep = 32 * kEach;
 constexpr float kSlack = 2.5e-4f;  // of an estimated sum: half a bin's width off in some of the likeliest tokens
@@ -162,12 +163,12 @@ struct Level {
     // halfway goes to the even bin
     return b == 0 ? 0u : b == kBins ? kDeep + 1 : __float_as_uint(((float)b - 0.5f) * 0x1p-6f) + (b & 1);
   }
-  // an estimate of n weights of a bin, in units of 2^-20: the middle's.  (Whole numbers: running sums that do not
-  // depend on their order go up from bin to bin, whoever forms them.)
-  __device__ u64 estimate(int b, uint32_t n) const {
+  // n tokens of a bin and an estimate of their weights, the middle's, in units of 2^-18: both in one number.  (Running
+  // sums of whole numbers go up from bin to bin, whoever forms them in what order.)
+  __device__ u64 both(int b, uint32_t n) const {
     const float x = shift < 0 ? (float)b * 0x1p-6f
                               : __uint_as_float(min(lo + ((uint32_t)b << shift) + ((1u << shift) >> 1), hi));
-    return n ? __float2ull_rn((float)n * expf(-x) * 0x1p20f) : 0;
+    return n ? __float2ull_rn((float)n * expf(-x) * 0x1p18f) << kCountBits | n : 0;
   }
 };
 
@@ -194,16 +195,14 @@ struct Shared {
   };
   u64 all_w[kList];                // W of `all`
   uint32_t share_n[kBins];         // the cluster's counts of this CTA's share of the bins
-  uint32_t at_n[kThreads];         // counts and estimates before a thread's bins of the share
-  u64 at_e[kThreads];
-  u64 share[2][kMaxCluster];       // count and estimate of each CTA's share
+  u64 at[kThreads];                // counts and estimates before a thread's bins of the share
+  u64 share[kMaxCluster];          // of each CTA's share
   uint2 list[kWarps][kWarpList];   // listed tokens
   u64 post[2][3][kMaxPieces];      // what the pieces' warps told last, and before that
-  u64 taken[3];                    // first bin and count before it, last bin and count to its end, estimate before
+  u64 taken[4];                    // first bin, what lies before it, last bin, what lies up to its end
   u64 result[2];                   // the border, the sum up to it
   Search q;
   u64 scan_s[kWarps];
-  uint32_t scan_n[kWarps];
   uint32_t sub_n[kThreads], sub_hi[kThreads], sub_lo[kThreads];  // a list's bins: tokens, W by 20-bit digits
   int sub_bin, few_n, hit;
   u64 sub_before_s;
@@ -351,8 +350,7 @@ struct Sampler {
   // The cluster's counts of this CTA's share of the bins, and what lies before each thread's; all shares' sums to all.
   __device__ void reduce() {
     const int k = each_bins(), b0 = first_bin();
-    uint32_t n_run = 0;
-    u64 e_run = 0;
+    u64 run = 0;
 #pragma unroll 1
     for (int b = 0; b < k; ++b) {
       uint32_t x[kMaxCluster], c = 0;
@@ -361,26 +359,18 @@ struct Sampler {
 #pragma unroll
       for (int i = 0; i < kMaxCluster; ++i) c += x[i];
       sh.share_n[threadIdx.x * k + b] = c;
-      n_run += c;
-      e_run += sh.q.lv.estimate(b0 + b, c);
+      run += sh.q.lv.both(b0 + b, c);
     }
-    const uint32_t n_mine = n_run;
-    const u64 e_mine = e_run;
-    e_run = warp_scan(e_run, lane);
-    n_run = (uint32_t)warp_scan(n_run, lane);
-    if (lane == 31) sh.scan_n[warp] = n_run, sh.scan_s[warp] = e_run;
+    const u64 mine = run;
+    run = warp_scan(run, lane);
+    if (lane == 31) sh.scan_s[warp] = run;
     __syncthreads();
 #pragma unroll 1
-    for (int i = 0; i < warp; ++i) n_run += sh.scan_n[i], e_run += sh.scan_s[i];
-    sh.at_n[threadIdx.x] = n_run - n_mine;
-    sh.at_e[threadIdx.x] = e_run - e_mine;
+    for (int i = 0; i < warp; ++i) run += sh.scan_s[i];
+    sh.at[threadIdx.x] = run - mine;
     if (warp == kWarps - 1) {
-      n_run = __shfl_sync(0xffffffffu, n_run, 31);
-      e_run = __shfl_sync(0xffffffffu, e_run, 31);
-      if (lane < cluster) {
-        store_remote(remote(&sh.share[0][rank], lane), (u64)n_run);
-        store_remote(remote(&sh.share[1][rank], lane), e_run);
-      }
+      run = __shfl_sync(0xffffffffu, run, 31);
+      if (lane < cluster) store_remote(remote(&sh.share[rank], lane), run);
     }
     cluster_barrier();
   }
@@ -390,16 +380,15 @@ struct Sampler {
   // [q.first, q.last] (after some wrong guesses the middle one).  The threads that hold them tell all CTAs.
   __device__ void seek() {
     const Search &q = sh.q;
-    uint32_t n_run = sh.at_n[threadIdx.x];
-    u64 e_run = sh.at_e[threadIdx.x], everything = 0;
+    u64 run = sh.at[threadIdx.x], everything = 0;
 #pragma unroll 1
     for (int c = 0; c < cluster; ++c) {
-      if (c < rank) n_run += (uint32_t)sh.share[0][c], e_run += sh.share[1][c];
-      everything += sh.share[1][c];
+      if (c < rank) run += sh.share[c];
+      everything += sh.share[c];
     }
     u64 low = q.many, high = q.many;
     if (q.by_sum) {
-      const float e = q.e0 + q.w * ((float)everything / (float)q.S), slack = e * q.slack;
+      const float e = q.e0 + q.w * ((float)(everything >> kCountBits) / (float)q.S), slack = e * q.slack;
       low = __float2ull_rn(fmaxf(e - slack, 1.f));
       high = __float2ull_rn(fmaxf(e + slack, 1.f));
     }
@@ -408,20 +397,24 @@ struct Sampler {
 #pragma unroll 1
     for (int i = 0; i < k; ++i) {
       const int b = b0 + i;
-      const uint32_t c = sh.share_n[threadIdx.x * k + i], n_to = n_run + c;
-      const u64 e_to = e_run + q.lv.estimate(b, c), was = q.by_sum ? e_run : n_run, is = q.by_sum ? e_to : n_to;
-      auto here = [&](u64 t) { return b >= first && b <= last && (b == first || was < t) && (b == last || is >= t); };
+      const u64 to = run + q.lv.both(b, sh.share_n[threadIdx.x * k + i]);
+      auto number = [&](u64 x) { return q.by_sum ? x >> kCountBits : x & ((1ull << kCountBits) - 1); };
+      auto here = [&](u64 t) {
+        return b >= first && b <= last && (b == first || number(run) < t) && (b == last || number(to) >= t);
+      };
       if (here(low))
 #pragma unroll 1
         for (int x = 0; x < cluster; ++x) {
-          store_remote(remote(&sh.taken[0], x), (u64)b << 32 | n_run);
-          store_remote(remote(&sh.taken[2], x), e_run);
+          store_remote(remote(&sh.taken[0], x), (u64)b);
+          store_remote(remote(&sh.taken[1], x), run);
         }
       if (here(high))
 #pragma unroll 1
-        for (int x = 0; x < cluster; ++x) store_remote(remote(&sh.taken[1], x), (u64)b << 32 | n_to);
-      n_run = n_to;
-      e_run = e_to;
+        for (int x = 0; x < cluster; ++x) {
+          store_remote(remote(&sh.taken[2], x), (u64)b);
+          store_remote(remote(&sh.taken[3], x), to);
+        }
+      run = to;
     }
     cluster_barrier();
   }
@@ -529,11 +522,16 @@ struct Sampler {
   __device__ u64 list_sum(int listed, uint32_t d) {
     u64 x = 0;
 #pragma unroll 1
-    for (int j = lane; j < listed; j += 32) {
+    for (int j = threadIdx.x; j < listed; j += kThreads) {
       const uint2 q = sh.all[j];
       if (q.x < d && r.inside(q.x, q.y) && !(r.least > 0.f && weight(q.x) < r.least)) x += sh.all_w[j];
     }
-    return warp_sum(x);
+    x = warp_sum(x);
+    if (lane == 0) sh.scan_s[warp] = x;
+    __syncthreads();
+    x = warp_sum(lane < kWarps ? sh.scan_s[lane] : 0);
+    __syncthreads();
+    return x;
   }
 
   // Lists this piece's tokens with |x|'s bits in [from, to); the sum of W of those before.
@@ -629,8 +627,9 @@ struct Sampler {
       if (!q.counted) count();
       if (!q.reduced) reduce();
       seek();
-      const int bin = (int)(sh.taken[0] >> 32), bin_to = (int)(sh.taken[1] >> 32);
-      const uint32_t before_n = (uint32_t)sh.taken[0], until_n = (uint32_t)sh.taken[1];
+      const int bin = (int)sh.taken[0], bin_to = (int)sh.taken[2];
+      constexpr uint32_t kCount = (1u << kCountBits) - 1;
+      const uint32_t before_n = (uint32_t)sh.taken[1] & kCount, until_n = (uint32_t)sh.taken[3] & kCount;
       if (!q.by_sum && q.lv.shift < 0 && bin == kBins - 1) return;
       // the whole first part is listed where it fits
       const bool whole = q.skipped + until_n <= kList;
@@ -641,7 +640,7 @@ struct Sampler {
         q.counted = q.reduced = true;
         q.whole = whole;
         q.before = q.skipped + before_n;
-        q.e_before = sh.taken[2];
+        q.e_before = sh.taken[1] >> kCountBits;
         q.from = from;
         q.to = to;
         if (wide) q.slack = 0.f;
