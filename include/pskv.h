@@ -600,7 +600,7 @@ typedef struct pskv_sample_desc {
  *   u             device float[rows] in [0, 1) (values outside count as the nearer end, NaN as 0), or NULL:
  *                 no token is drawn
  *   tokens        device int32[rows], or NULL when u is
- *   probs         device [rows][vocab] of probs_dtype (F32 or BF16), or NULL
+ *   probs         device [rows][vocab] of probs_dtype (F32 or BF16), apart from the logits, or NULL
  *   status        device int32[4] fault word or NULL
  * A row without any finite or +inf logit gives token -1, zeros and PSKV_FAULT_EMPTY_ROW; several logits
  * of +inf share the weight.  vocab 1 .. 2^22.  No workspace.  Errors: INVALID_ARG (also neither tokens

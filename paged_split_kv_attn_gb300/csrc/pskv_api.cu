@@ -958,11 +958,15 @@ int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t
   if (!aligned(logits, dtype == PSKV_DTYPE_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(tokens, 4) ||
       !aligned(probs, probs_dtype == PSKV_DTYPE_BF16 ? 2 : 4) || !aligned(status, 4))
     return PSKV_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)requests * tokens_per_request;
+  if (probs && overlap(logits, ((size_t)(rows - 1) * logits_row + vocab) * (dtype == PSKV_DTYPE_BF16 ? 2 : 4), probs,
+                       (size_t)rows * vocab * (probs_dtype == PSKV_DTYPE_BF16 ? 2 : 4)))
+    return PSKV_ERR_INVALID_ARG;  // (a row is read again while another one's is written)
   SampleArgs a;
   a.logits = logits;
   a.logits_row = logits_row;
   a.dtype = dtype;
-  a.rows = requests * tokens_per_request;
+  a.rows = (int)rows;
   a.per_request = tokens_per_request;
   a.vocab = vocab;
   a.temperature = filters ? filters->temperature : nullptr;

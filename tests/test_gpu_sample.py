@@ -233,3 +233,57 @@ def test_python_refusals():
                            probs=torch.zeros(2, 2, 50, device="cuda"))
     with pytest.raises(ValueError):
         pskv.sample_tokens(l[0, 0], u[0, 0])
+
+
+def test_top_k_past_the_tokens_with_weight():
+    """More places than tokens that weigh anything: nothing is left out, min_p and top_p still count."""
+    l, u = inputs(14, 4, 1, 3000, torch.float32, spread=1.0)
+    l[:, :, 40:] -= 60.0  # expf(-60) is under 2^-41
+    k = torch.tensor([41, 500, 2999, 40], dtype=torch.int32, device="cuda")
+    for kw in (dict(), dict(min_p=torch.full((4,), 0.05, device="cuda")), dict(top_p=torch.full((4,), 0.7, device="cuda")),
+               dict(min_p=torch.full((4,), 0.02, device="cuda"), top_p=torch.full((4,), 0.9, device="cuda"))):
+        assert check(l, u, torch.float32, top_k=k, **kw) == 0
+
+
+@pytest.mark.parametrize("k,p,least", [(1500, 0.5, 0.0), (1500, 0.97, 0.01), (4000, 0.999, 0.0), (12000, 0.9, 0.001), (1020, 0.99, 0.0)])
+def test_borders_behind_what_a_list_holds(k, p, least):
+    """Flat rows whose kept tokens do not fit a list: borders by number and then by weight, draws over the whole row."""
+    for dtype, lattice in ((torch.float32, None), (torch.bfloat16, None), (torch.float32, 8)):
+        l, u = inputs(15 + k, 3, 1, 32001, dtype, spread=0.7, lattice=lattice)
+        kw = dict(top_k=torch.tensor([k, k + 1, k + 7], dtype=torch.int32, device="cuda"), top_p=torch.full((3,), p, device="cuda"))
+        if least:
+            kw["min_p"] = torch.full((3,), least, device="cuda")
+        assert check(l, u, torch.float32, **kw) == 0
+
+
+def test_many_rows():
+    """Batches that take clusters of eight, four, two and one."""
+    for rows in (70, 100, 200, 700):
+        l, u = inputs(rows, rows, 1, 600, torch.float32)
+        assert check(l, u, **filters(rows, top_k=30, top_p=0.9)) == 0
+        assert check(l, u, **filters(rows, top_p=0.95)) == 0
+
+
+def test_two_streams_at_once():
+    """Calls that run beside each other on two streams, replayed and eager."""
+    a, b = inputs(40, 24, 1, 40000, torch.float32), inputs(41, 40, 2, 9000, torch.bfloat16)
+    kw = [filters(24, top_p=0.9), filters(40, top_k=60, top_p=0.8)]
+    want = [sample_reference(*x, **{k: v.tolist() for k, v in w.items()})[0] for x, w in zip((a, b), kw)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (x, w) in enumerate(zip((a, b), kw)):
+            got[i].append(pskv.sample_tokens(*x, stream=streams[i], **w))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(np.array_equal(t.cpu().numpy(), w) for t in g)
+
+
+def test_python_forms_give_the_same(monkeypatch):
+    """Without the compiled calls."""
+    from paged_split_kv_attn_gb300 import _binding
+    monkeypatch.setattr(_binding, "_calls", _binding._PythonCalls)
+    l, u = inputs(42, 3, 2, 700, torch.float32)
+    assert check(l, u, torch.bfloat16, **filters(3, top_k=20, top_p=0.9, min_p=0.01)) == 0
+    assert check(l[:, 0], u[:, 0].contiguous()) == 0

@@ -472,3 +472,72 @@ def test_a_step_of_drafted_trees_over_forked_rows():
         w = torch.softmax(q1[b, 0].double() @ mine.T * 0.07, -1)
         ref = (w @ mine[:, :512])[None, None]
         check_attention(out[b:b + 1], ref, float(mine.abs().max()))
+
+
+def test_python_forms_give_the_same(monkeypatch):
+    """Without the compiled calls: the step above, the chain, the refusals."""
+    from paged_split_kv_attn_gb300 import _binding
+    monkeypatch.setattr(_binding, "_calls", _binding._PythonCalls)
+    test_a_step_of_drafted_trees_over_forked_rows()
+    test_a_chain_is_the_causal_window(0)
+    test_tree_refusals()
+    test_walk_refusals_and_given_outputs()
+    test_keep_refusals()
+    test_fork_capture_and_refusals()
+
+
+def test_uint64_masks():
+    case = LatentCase(8, [200], 256, 64, 8, 5)
+    masks = random_masks(np.random.default_rng(6), 1, 5)
+    unsigned = torch.from_numpy(masks).cuda()
+    assert unsigned.dtype == torch.uint64
+    out = pskv.decode_attn_latent_tree(case.layout, case.q, case.table, case.lens, case.lens_host, unsigned, case.scale)
+    assert torch.equal(out, run_tree(case, masks))
+    d = i32(np.zeros((1, 5)))
+    assert all(torch.equal(a, b) for a, b in zip(pskv.verify_tree(d, unsigned, d), pskv.verify_tree(d, i64(masks), d)))
+
+
+def test_workspaces_shared_by_two_graphs():
+    """Two captured calls that use one workspace, replayed one after another in either order."""
+    a, b = LatentCase(9, [3000], 512, 256, 16, 6), LatentCase(10, [2500, 700], 512, 256, 16, 4)
+    need = max(pskv.decode_attn_latent_workspace_bytes(c.layout, c.lens_host, c.table.shape[1], c.tokens, c.heads) for c in (a, b))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    calls = []
+    for c in (a, b):
+        masks = i64(random_masks(np.random.default_rng(c.tokens), len(c.lens_host), c.tokens))
+        out = torch.empty(len(c.lens_host), c.tokens, 16, 512, dtype=torch.bfloat16, device="cuda")
+        args = (c.layout, c.q, c.table, c.lens, c.lens_host, masks, c.scale)
+        want = pskv.decode_attn_latent_tree(*args)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pskv.decode_attn_latent_tree(*args, workspace=ws, out=out)
+        calls.append((graph, out, want))
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1)):
+        for k in order:
+            calls[k][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(calls[k][1], calls[k][2]) for k in order)
+
+
+def test_keep_and_fork_far_into_a_pool():
+    """Pages whose rows lie past 2^31 elements of a region."""
+    heads, page, d = 16, 64, 256
+    pages = (1 << 31) // (heads * page * d) + 9
+    k = torch.zeros(pages, heads, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    layout = pskv.paged_kv_layout_create(k, v)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    far = [pages - 2, pages - 3, pages - 5]
+    for p in far[:2]:
+        k[p] = torch.randn(k[p].shape, generator=gen, device="cuda").to(torch.bfloat16)
+        v[p] = torch.randn(k[p].shape, generator=gen, device="cuda").to(torch.bfloat16)
+    table, lens, leases = i32([far[:2], [-1, -1]]), i32([100, 0]), i32([2, 0])
+    pskv.kv_fork_rows(layout, i32([0]), i32([1]), i32(far[2:]), table, lens, leases)
+    assert table.tolist() == [far[:2], [far[0], far[2]]] and lens.tolist() == [100, 100]
+    for pool in (k, v):
+        assert torch.equal(pool[far[2], :, :36], pool[far[1], :, :36]) and not pool[far[2], :, 36:].any()
+    want = [torch.cat([pool[far[0]], pool[far[2]]], 1)[:, [90, 93, 99]].clone() for pool in (k, v)]
+    new = pskv.kv_keep_tokens(layout, table, lens, i32([[0] * 10, [0, 3, 9] + [-1] * 7]), i32([0, 3]))
+    assert new.tolist() == [90, 93]
+    for pool, w in zip((k, v), want):
+        assert torch.equal(pool[far[2], :, 26:29], w)

@@ -53,8 +53,9 @@ def sample(lib, **kw):
 @pytest.mark.parametrize("kw", [
     dict(logits=None), dict(dtype=2), dict(dtype=-1), dict(row=99), dict(row=-1), dict(requests=0), dict(each=0),
     dict(vocab=0), dict(vocab=(1 << 22) + 1, row=1 << 23), dict(requests=1 << 13, each=1 << 12), dict(u=None),
-    dict(tokens=None), dict(u=None, tokens=None), dict(probs=P, probs_dtype=5), dict(logits=P + 2), dict(u=P + 1),
-    dict(tokens=P + 2), dict(probs=P + 2), dict(probs=P + 1, probs_dtype=1), dict(status=P + 1),
+    dict(tokens=None), dict(u=None, tokens=None), dict(probs=P + (1 << 20), probs_dtype=5), dict(probs=P),
+    dict(probs=P + 2396), dict(probs=P - 1198, probs_dtype=1, row=200), dict(logits=P + 2400, probs=P + 4), dict(logits=P + 2), dict(u=P + 1),
+    dict(tokens=P + 2), dict(probs=P + (1 << 20) + 2), dict(probs=P + (1 << 20) + 1, probs_dtype=1), dict(status=P + 1),
     dict(filters=(P + 2, None, None, None)), dict(filters=(None, P + 1, None, None)),
     dict(filters=(None, None, P + 3, None)), dict(filters=(None, None, None, P + 2))])
 def test_sample_refusals(lib, kw):
