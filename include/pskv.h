@@ -600,11 +600,11 @@ typedef struct pskv_sample_desc {
  *   u             device float[rows] in [0, 1) (values outside count as the nearer end, NaN as 0), or NULL:
  *                 no token is drawn
  *   tokens        device int32[rows], or NULL when u is
- *   probs         device [rows][vocab] of probs_dtype (F32 or BF16), apart from the logits, or NULL
+ *   probs         device [rows][vocab] of probs_dtype (F32 or BF16), or NULL
  *   status        device int32[4] fault word or NULL
  * A row without any finite or +inf logit gives token -1, zeros and PSKV_FAULT_EMPTY_ROW; several logits
  * of +inf share the weight.  vocab 1 .. 2^22.  No workspace.  Errors: INVALID_ARG (also neither tokens
- * nor probs asked for), CUDA. */
+ * nor probs asked for, or these not apart from each other and from what is read), CUDA. */
 int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t requests,
                   int32_t tokens_per_request, int32_t vocab, const pskv_sample_desc *filters,
                   const float *u, int32_t *tokens, void *probs, int32_t probs_dtype,
@@ -623,7 +623,8 @@ int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t
  *   path       device int32[batch][num_tokens]: the standing tokens' places, going up, then -1
  *   kept       device int32[batch]: how many stand (1 at least)
  *   status     device int32[4] fault word or NULL
- * num_tokens 1..PSKV_MAX_WINDOW_TOKENS.  No workspace.  Errors: INVALID_ARG, CUDA. */
+ * num_tokens 1..PSKV_MAX_WINDOW_TOKENS.  No workspace.  Errors: INVALID_ARG (also outputs that are not apart
+ * from each other and from what is read), CUDA. */
 int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t *sampled,
                 int32_t batch, int32_t num_tokens, int32_t *tokens, int32_t *path, int32_t *kept,
                 int32_t *status, pskv_stream_t stream);
@@ -633,7 +634,8 @@ int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t 
  * num_tokens, in the pools of all the layouts (layers that share the page tables), bit for bit, and the
  * row's new length is w0 + kept[b].
  *   layouts    host array of num_layouts (1..PSKV_MAX_LAYOUTS) layouts of one description but for
- *              their pools and status words; any format.  Faults go to the first one's status word
+ *              their pools, which share no memory, and status words; any format.  Faults go to the
+ *              first one's status word
  *   path       device int32[batch][num_tokens]: path[b][0 .. kept[b]) goes up, within [0, num_tokens);
  *              the rest is not looked at.  Else PSKV_FAULT_BAD_PATH
  *   kept       device int32[batch], 0..num_tokens each (else PSKV_FAULT_BAD_PATH)
@@ -642,7 +644,7 @@ int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t 
  *   new_lens   device int32[batch]; not one of the arrays read
  * A row refused (these, or a page id outside the pool: PSKV_FAULT_BAD_PAGE) keeps its rows and its
  * length.  The window's pages must belong to the row alone (kv_fork_rows' last pages do).  num_tokens
- * 1..PSKV_MAX_WINDOW_TOKENS.  Errors: INVALID_ARG (also layouts that differ), UNSUPPORTED (pages of more
+ * 1..PSKV_MAX_WINDOW_TOKENS.  Errors: INVALID_ARG (also layouts that differ or share memory), UNSUPPORTED (pages of more
  * than 16 GB), CUDA. */
 int kv_keep_tokens(const pskv_layout *const *layouts, int32_t num_layouts,
                    const int32_t *page_tables, int32_t table_stride, const int32_t *seq_lens,
@@ -661,11 +663,11 @@ int kv_keep_tokens(const pskv_layout *const *layouts, int32_t num_layouts,
  *                 (PSKV_FAULT_BAD_ROW), and so is a src out of range
  *   new_pages     device int32[n]: pages no row holds, distinct; not looked at where the keys fill their pages
  *   page_tables   device int32[batch][table_stride], read and written; seq_lens, pages_of_row device
- *                 int32[batch], too
+ *                 int32[batch], too; these three apart from each other and from src, dst and new_pages
  * A fork is also refused for a length outside [0, table_stride * page_size] (PSKV_FAULT_BAD_LENGTH), a lease
  * of fewer pages than its keys need (PSKV_FAULT_PAST_PAGES), or a page to copy from or to that is outside the
  * pool or the same (PSKV_FAULT_BAD_PAGE).  A refused fork writes nothing.  n 0..65535.
- * Errors: INVALID_ARG (also layouts that differ), UNSUPPORTED (pages of more than 16 GB), CUDA. */
+ * Errors: INVALID_ARG (also layouts that differ or share memory), UNSUPPORTED (pages of more than 16 GB), CUDA. */
 int kv_fork_rows(const pskv_layout *const *layouts, int32_t num_layouts, const int32_t *src,
                  const int32_t *dst, const int32_t *new_pages, int32_t n, int32_t *page_tables,
                  int32_t table_stride, int32_t *seq_lens, int32_t *pages_of_row, int32_t batch,

@@ -8,6 +8,8 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <functional>
+#include <initializer_list>
 #include <new>
 
 #include "attn_tc.h"
@@ -149,7 +151,7 @@ int decode_common(const pskv_layout *layout, const void *q, const int32_t *page_
                   int32_t batch, const QuerySpec &qs, int32_t num_q_heads, float scale,
                   int32_t num_splits, void *workspace, size_t workspace_bytes, void *out,
                   int32_t out_dtype, const pskv_decode_opts *opts, pskv_stream_t stream,
-                  size_t *plan_bytes = nullptr, const uint64_t *tree_mask = nullptr) {
+                  size_t *plan_bytes = nullptr) {
   if (!layout || !seq_lens_host) return PSKV_ERR_INVALID_ARG;
   if (!plan_bytes && (!q || !page_tables || !seq_lens || !out)) return PSKV_ERR_INVALID_ARG;
   if (windowed && !plan_bytes && (!first_pos || !window_lo)) return PSKV_ERR_INVALID_ARG;
@@ -468,7 +470,31 @@ int decode_latent(const pskv_layout *layout, const void *q, const int32_t *page_
   return PSKV_OK;
 }
 
-// The pools of layers that share page tables: one description but for pools and status words.
+// Memory that a call reads or writes (size 0: none).
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+
+bool overlap(const Span &x, const Span &y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return a < b + y.bytes && b < a + x.bytes;
+}
+
+// Whether what is written shares nothing with what is read, nor with each other.  (Blocks read at any time what other
+// ones write.)
+bool apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span *w = written.begin(); w != written.end(); ++w) {
+    for (const Span *o = w + 1; o != written.end(); ++o)
+      if (overlap(*w, *o)) return false;
+    for (const Span &r : read)
+      if (overlap(*w, r)) return false;
+  }
+  return true;
+}
+
+// The pools of layers that share page tables: one description but for pools and status words, and no memory in
+// two of them (their rows are moved by blocks of their own).
 int gather_pools(const pskv_layout *const *layouts, int32_t num_layouts, Pools *p) {
   if (!layouts || num_layouts < 1 || num_layouts > PSKV_MAX_LAYOUTS) return PSKV_ERR_INVALID_ARG;
   for (int32_t i = 0; i < num_layouts; ++i) {
@@ -491,13 +517,17 @@ int gather_pools(const pskv_layout *const *layouts, int32_t num_layouts, Pools *
   p->status = d.status;
   // a page's vectors are counted in 32 bits
   if ((int64_t)p->heads * (p->k_vecs + p->v_vecs) > (1 << 30) / p->page_size) return PSKV_ERR_UNSUPPORTED;
+  Span regions[2 * PSKV_MAX_LAYOUTS];
+  int n = 0;
+  const size_t rows = (size_t)p->num_pages * p->heads * p->page_size;
+  for (int32_t i = 0; i < num_layouts; ++i) {
+    regions[n++] = {p->k[i], rows * p->k_vecs * 16};
+    if (p->v_vecs > 0) regions[n++] = {p->v[i], rows * p->v_vecs * 16};
+  }
+  std::sort(regions, regions + n, [](const Span &x, const Span &y) { return std::less<const void *>()(x.p, y.p); });
+  for (int i = 1; i < n; ++i)
+    if (overlap(regions[i - 1], regions[i])) return PSKV_ERR_INVALID_ARG;
   return PSKV_OK;
-}
-
-// Whether [p, p + n) and [q, q + m) (bytes) share any.
-bool overlap(const void *p, size_t n, const void *q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + m && b < a + n;
 }
 
 }  // namespace
@@ -959,9 +989,16 @@ int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t
       !aligned(probs, probs_dtype == PSKV_DTYPE_BF16 ? 2 : 4) || !aligned(status, 4))
     return PSKV_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)requests * tokens_per_request;
-  if (probs && overlap(logits, ((size_t)(rows - 1) * logits_row + vocab) * (dtype == PSKV_DTYPE_BF16 ? 2 : 4), probs,
-                       (size_t)rows * vocab * (probs_dtype == PSKV_DTYPE_BF16 ? 2 : 4)))
-    return PSKV_ERR_INVALID_ARG;  // (a row is read again while another one's is written)
+  const size_t of_requests = 4 * (size_t)requests, of_rows = 4 * (size_t)rows;
+  const pskv_sample_desc f = filters ? *filters : pskv_sample_desc{};
+  if (!apart({{tokens, tokens ? of_rows : 0}, {probs, probs ? (size_t)rows * vocab * (probs_dtype == PSKV_DTYPE_BF16 ? 2 : 4) : 0}},
+             {{logits, ((size_t)(rows - 1) * logits_row + vocab) * (dtype == PSKV_DTYPE_BF16 ? 2 : 4)},
+              {u, u ? of_rows : 0},
+              {f.temperature, f.temperature ? of_requests : 0},
+              {f.top_k, f.top_k ? of_requests : 0},
+              {f.top_p, f.top_p ? of_requests : 0},
+              {f.min_p, f.min_p ? of_requests : 0}}))
+    return PSKV_ERR_INVALID_ARG;
   SampleArgs a;
   a.logits = logits;
   a.logits_row = logits_row;
@@ -969,10 +1006,10 @@ int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t
   a.rows = (int)rows;
   a.per_request = tokens_per_request;
   a.vocab = vocab;
-  a.temperature = filters ? filters->temperature : nullptr;
-  a.top_k = filters ? filters->top_k : nullptr;
-  a.top_p = filters ? filters->top_p : nullptr;
-  a.min_p = filters ? filters->min_p : nullptr;
+  a.temperature = f.temperature;
+  a.top_k = f.top_k;
+  a.top_p = f.top_p;
+  a.min_p = f.min_p;
   if (!aligned(a.temperature, 4) || !aligned(a.top_k, 4) || !aligned(a.top_p, 4) || !aligned(a.min_p, 4))
     return PSKV_ERR_INVALID_ARG;
   a.u = u;
@@ -997,6 +1034,9 @@ int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t 
     return PSKV_ERR_INVALID_ARG;
   if (!aligned(tree_mask, 8) || !aligned(drafts, 4) || !aligned(sampled, 4) || !aligned(tokens, 4) ||
       !aligned(path, 4) || !aligned(kept, 4) || !aligned(status, 4))
+    return PSKV_ERR_INVALID_ARG;
+  const size_t row = 4 * (size_t)batch, all = row * num_tokens;
+  if (!apart({{tokens, all}, {path, all}, {kept, row}}, {{drafts, all}, {tree_mask, 2 * all}, {sampled, all}}))
     return PSKV_ERR_INVALID_ARG;
   VerifyTreeArgs a;
   a.drafts = drafts;
@@ -1028,9 +1068,9 @@ int kv_keep_tokens(const pskv_layout *const *layouts, int32_t num_layouts,
       !aligned(new_lens, 4))
     return PSKV_ERR_INVALID_ARG;
   const size_t row = 4 * (size_t)batch;
-  if (overlap(new_lens, row, seq_lens, row) || overlap(new_lens, row, kept, row) ||
-      overlap(new_lens, row, path, row * num_tokens) || overlap(new_lens, row, page_tables, row * table_stride))
-    return PSKV_ERR_INVALID_ARG;  // (blocks of a row read what another one writes)
+  if (!apart({{new_lens, row}},
+             {{seq_lens, row}, {kept, row}, {path, row * num_tokens}, {page_tables, row * table_stride}}))
+    return PSKV_ERR_INVALID_ARG;
   const KeepArgs a = {page_tables, table_stride, seq_lens, path, kept, batch, num_tokens, new_lens};
   const cudaError_t e = launch_keep(a, p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
@@ -1051,6 +1091,10 @@ int kv_fork_rows(const pskv_layout *const *layouts, int32_t num_layouts, const i
     return PSKV_ERR_INVALID_ARG;
   if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(new_pages, 4) || !aligned(page_tables, 4) ||
       !aligned(seq_lens, 4) || !aligned(pages_of_row, 4))
+    return PSKV_ERR_INVALID_ARG;
+  const size_t row = 4 * (size_t)batch, forks = 4 * (size_t)n;
+  if (!apart({{page_tables, row * table_stride}, {seq_lens, row}, {pages_of_row, row}},
+             {{src, forks}, {dst, forks}, {new_pages, forks}}))
     return PSKV_ERR_INVALID_ARG;
   const ForkArgs a = {src, dst, new_pages, n, page_tables, table_stride, seq_lens, pages_of_row, batch};
   const cudaError_t e = launch_fork(a, p, reinterpret_cast<cudaStream_t>(stream));
