@@ -40,8 +40,10 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxPieces = kMaxCluster * kWarps;
 constexpr int kPerSm = 4;        // CTAs an SM holds (registers)
 constexpr int kBins = 2048;
+constexpr int kOwn = kBins / kThreads;
 constexpr int kList = 1024;      // listed tokens of a cluster,
 constexpr int kWarpList = kList / kWarps;  // and of a warp
+constexpr int kFew = kThreads / 4;         // of a list whose tokens are compared with each other
 constexpr int kCountBits = 23;   // of a number that holds a count (up to 2^22) and an estimate (up to 2^40)
 constexpr int kEach = 8;         // elements a lane takes in a step
 constexpr int kStep = 32 * kEach;
@@ -132,6 +134,9 @@ __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
 __device__ __forceinline__ void store_remote(uint32_t at, u64 x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
+__device__ __forceinline__ void store_remote(uint32_t at, uint32_t x) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
 __device__ __forceinline__ uint32_t load_remote(uint32_t at) {
   uint32_t x;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
@@ -194,9 +199,8 @@ struct Shared {
     uint2 all[kList];              // the first CTA: the cluster's listed tokens (|x|'s bits, index)
   };
   u64 all_w[kList];                // W of `all`
-  uint32_t share_n[kBins];         // the cluster's counts of this CTA's share of the bins
-  u64 at[kThreads];                // counts and estimates before a thread's bins of the share
-  u64 share[kMaxCluster];          // of each CTA's share
+  uint32_t counts[kBins];          // the cluster's
+  u64 at[kThreads + 1];            // counts and estimates before each thread's bins, and of all
   uint2 list[kWarps][kWarpList];   // listed tokens
   u64 post[2][3][kMaxPieces];      // what the pieces' warps told last, and before that
   u64 taken[4];                    // first bin, what lies before it, last bin, what lies up to its end
@@ -343,13 +347,10 @@ struct Sampler {
     cluster_barrier();
   }
 
-  // A thread's bins of its CTA's share: their number, and the first.
-  __device__ int each_bins() const { return kBins / kThreads / cluster; }
-  __device__ int first_bin() const { return (rank * kThreads + threadIdx.x) * each_bins(); }
-
-  // The cluster's counts of this CTA's share of the bins, and what lies before each thread's; all shares' sums to all.
+  // The cluster's counts, to every CTA: each adds up a share of the bins.  Then, alike in all of them, what lies before
+  // each thread's bins.
   __device__ void reduce() {
-    const int k = each_bins(), b0 = first_bin();
+    const int k = kOwn / cluster, b0 = (rank * kThreads + threadIdx.x) * k;
     u64 run = 0;
 #pragma unroll 1
     for (int b = 0; b < k; ++b) {
@@ -358,81 +359,70 @@ struct Sampler {
       for (int i = 0; i < kMaxCluster; ++i) x[i] = i < cluster ? load_remote(remote(&sh.hist[b0 + b], i)) : 0;
 #pragma unroll
       for (int i = 0; i < kMaxCluster; ++i) c += x[i];
-      sh.share_n[threadIdx.x * k + b] = c;
+#pragma unroll 1
+      for (int i = 0; i < cluster; ++i) store_remote(remote(&sh.counts[b0 + b], i), c);
       run += sh.q.lv.both(b0 + b, c);
     }
-    const u64 mine = run;
-    run = warp_scan(run, lane);
+    // (kOwn bins lie in as many lanes as there are CTAs: each tells one)
+#pragma unroll 1
+    for (int d = 1; d < cluster; d <<= 1) run += __shfl_xor_sync(0xffffffffu, run, d);
+    store_remote(remote(&sh.at[b0 / kOwn], threadIdx.x & (cluster - 1)), run);
+    cluster_barrier();
+    const u64 mine = sh.at[threadIdx.x];
+    run = warp_scan(mine, lane);
     if (lane == 31) sh.scan_s[warp] = run;
     __syncthreads();
 #pragma unroll 1
     for (int i = 0; i < warp; ++i) run += sh.scan_s[i];
     sh.at[threadIdx.x] = run - mine;
-    if (warp == kWarps - 1) {
-      run = __shfl_sync(0xffffffffu, run, 31);
-      if (lane < cluster) store_remote(remote(&sh.share[rank], lane), run);
-    }
-    cluster_barrier();
+    if (threadIdx.x == kThreads - 1) sh.at[kThreads] = run;
+    __syncthreads();
   }
 
   // Takes the bins that may hold the border: the one at which the running count reaches q.many, or (by_sum) those at
   // which the running estimate may pass q.e0 + q.w's share of all bins' (S), give or take q.slack of it; within
-  // [q.first, q.last] (after some wrong guesses the middle one).  The threads that hold them tell all CTAs.
+  // [q.first, q.last] (after some wrong guesses the middle one).  Every CTA finds the same ones.
   __device__ void seek() {
     const Search &q = sh.q;
-    u64 run = sh.at[threadIdx.x], everything = 0;
-#pragma unroll 1
-    for (int c = 0; c < cluster; ++c) {
-      if (c < rank) run += sh.share[c];
-      everything += sh.share[c];
-    }
-    u64 low = q.many, high = q.many;
+    u64 target[2] = {q.many, q.many};
     if (q.by_sum) {
-      const float e = q.e0 + q.w * ((float)(everything >> kCountBits) / (float)q.S), slack = e * q.slack;
-      low = __float2ull_rn(fmaxf(e - slack, 1.f));
-      high = __float2ull_rn(fmaxf(e + slack, 1.f));
+      const float e = q.e0 + q.w * ((float)(sh.at[kThreads] >> kCountBits) / (float)q.S), slack = e * q.slack;
+      target[0] = __float2ull_rn(fmaxf(e - slack, 1.f));
+      target[1] = __float2ull_rn(fmaxf(e + slack, 1.f));
     }
     const int first = q.tries < 5 ? q.first : (q.first + q.last) / 2, last = q.tries < 5 ? q.last : first;
-    const int k = each_bins(), b0 = first_bin();
+    const int b0 = threadIdx.x * kOwn;
+    auto number = [&](u64 x) { return q.by_sum ? x >> kCountBits : x & ((1ull << kCountBits) - 1); };
+    // a bin (or a thread's bins b .. to) holds a target
+    auto here = [&](u64 t, int b, int to, u64 before, u64 until) {
+      return to >= first && b <= last && (b <= first || number(before) < t) && (to >= last || number(until) >= t);
+    };
+    u64 run = sh.at[threadIdx.x];
+    const u64 end = sh.at[threadIdx.x + 1];
+    if (here(target[0], b0, b0 + kOwn - 1, run, end) || here(target[1], b0, b0 + kOwn - 1, run, end))
 #pragma unroll 1
-    for (int i = 0; i < k; ++i) {
-      const int b = b0 + i;
-      const u64 to = run + q.lv.both(b, sh.share_n[threadIdx.x * k + i]);
-      auto number = [&](u64 x) { return q.by_sum ? x >> kCountBits : x & ((1ull << kCountBits) - 1); };
-      auto here = [&](u64 t) {
-        return b >= first && b <= last && (b == first || number(run) < t) && (b == last || number(to) >= t);
-      };
-      if (here(low))
-#pragma unroll 1
-        for (int x = 0; x < cluster; ++x) {
-          store_remote(remote(&sh.taken[0], x), (u64)b);
-          store_remote(remote(&sh.taken[1], x), run);
-        }
-      if (here(high))
-#pragma unroll 1
-        for (int x = 0; x < cluster; ++x) {
-          store_remote(remote(&sh.taken[2], x), (u64)b);
-          store_remote(remote(&sh.taken[3], x), to);
-        }
-      run = to;
-    }
-    cluster_barrier();
+      for (int b = b0; b < b0 + kOwn; ++b) {
+        const u64 to = run + q.lv.both(b, sh.counts[b]);
+        if (here(target[0], b, b, run, to)) sh.taken[0] = (u64)b, sh.taken[1] = run;
+        if (here(target[1], b, b, run, to)) sh.taken[2] = (u64)b, sh.taken[3] = to;
+        run = to;
+      }
+    __syncthreads();
   }
 
   // ---- lists (of the first CTA)
 
-  // Of the list's tokens that lie inside the border (and weigh `least`), in their order (or by index), the one at
-  // which their running number (or the sum of their W) reaches `target`.  base: the number (sum) before those with
-  // key lo; `with`: the sum up to that token, it included (by number: left as it is).  [lo, lo + 2^bits): where its
-  // key lies; bits -1: anywhere, by |x| in steps of 1/8 first.
-  __device__ uint2 pick(int listed, bool by_index, bool by_sum, u64 target, u64 base, uint32_t lo, int bits, u64 &with) {
+  // Of the list's tokens that lie inside the border, in their order, the one at which their running number (or the
+  // sum of their W) reaches `target`.  base: the number (sum) before those with |x|'s bits lo; [lo, lo + 2^bits):
+  // where its own lie; bits -1: anywhere, in steps of 1/8 first.
+  __device__ uint2 pick(int listed, bool by_sum, u64 target, u64 base, uint32_t lo, int bits) {
     u64 before_n = by_sum ? 0 : base, before_s = by_sum ? base : 0;
     uint32_t fixed = 0;      // |x|'s bits, once these are down to one value
-    bool on_v = by_index, tied = false, eighths = bits < 0;
+    bool tied = false, eighths = bits < 0;
     auto in = [&](int i, uint2 &q, uint32_t &key) {
       q = sh.all[i];
-      key = on_v ? q.y : q.x;
-      return r.inside(q.x, q.y) && (!tied || q.x == fixed) && !(r.least > 0.f && weight(q.x) < r.least);
+      key = tied ? q.y : q.x;
+      return r.inside(q.x, q.y) && (!tied || q.x == fixed);
     };
     uint32_t width;          // of the last level's bin
     int shift = max(0, bits - 8);
@@ -483,7 +473,7 @@ struct Sampler {
       if (count <= 32) break;
       if (shift == 0) {  // many of one |x|: by index
         fixed = lo;
-        tied = on_v = true;
+        tied = true;
         lo = 0;
         shift = 14;
       } else {
@@ -507,15 +497,73 @@ struct Sampler {
     for (int k = 0; k < count; ++k) {
       const uint32_t d = __shfl_sync(0xffffffffu, q.x, k), v = __shfl_sync(0xffffffffu, q.y, k);
       const u64 o = __shfl_sync(0xffffffffu, w, k);
-      if (by_index ? v < q.y : d < q.x || (d == q.x && v < q.y)) sum += o, ++place;
+      if (d < q.x || (d == q.x && v < q.y)) sum += o, ++place;
     }
     const bool hit = lane < count && (by_sum ? sum - w < target && target <= sum : place == target);
     const uint32_t who = __ballot_sync(0xffffffffu, hit);
     const int l = who ? __ffs(who) - 1 : 0;
-    if (by_sum) with = __shfl_sync(0xffffffffu, sum, l);
     const uint2 found = make_uint2(__shfl_sync(0xffffffffu, q.x, l), __shfl_sync(0xffffffffu, q.y, l));
     __syncthreads();
     return found;
+  }
+
+  // The same where the list is short and its tokens are all that counts (`before` the number, or the sum, before them):
+  // four threads compare each with all.  sum: that of the list's W up to that token.
+  __device__ uint2 pick_few(int listed, bool by_sum, u64 target, u64 before, u64 &sum) {
+    const int i = threadIdx.x >> 2;
+    const uint2 q = sh.all[i];  // (a place behind the list is no hit)
+    u64 w = 0;
+    uint32_t place = 0;
+#pragma unroll 1
+    for (int j = threadIdx.x & 3; j < listed; j += 4) {
+      const uint2 o = sh.all[j];
+      if (r.inside(o.x, o.y) && (o.x < q.x || (o.x == q.x && o.y <= q.y))) w += sh.all_w[j], ++place;
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      w += __shfl_xor_sync(0xffffffffu, w, d);
+      place += __shfl_xor_sync(0xffffffffu, place, d);
+    }
+    if (i < listed && r.inside(q.x, q.y) &&
+        (by_sum ? before + w - sh.all_w[i] < target && target <= before + w : before + place == target) &&
+        (threadIdx.x & 3) == 0) {
+      sh.taken[0] = (u64)q.x << 32 | q.y;
+      sh.taken[1] = w;
+    }
+    __syncthreads();
+    sum = sh.taken[1];
+    const u64 found = sh.taken[0];
+    __syncthreads();
+    return make_uint2((uint32_t)(found >> 32), (uint32_t)found);
+  }
+
+  // The first of the list's tokens that are kept at which the sum of their W passes `left`.
+  __device__ void draw(int listed, u64 left, int32_t *token) {
+    const int each = (listed + kThreads - 1) / kThreads, j0 = threadIdx.x * each;
+    auto w_of = [&](int j) {
+      if (j >= listed) return (u64)0;
+      const uint2 q = sh.all[j];
+      return r.kept(q.x, q.y) > 0.f ? sh.all_w[j] : 0;
+    };
+    u64 own = 0;
+#pragma unroll 1
+    for (int j = 0; j < each; ++j) own += w_of(j0 + j);
+    u64 run = warp_scan(own, lane);
+    if (lane == 31) sh.scan_s[warp] = run;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < warp; ++i) run += sh.scan_s[i];
+    if (left < run && run - own <= left) {
+      run -= own;
+#pragma unroll 1
+      for (int j = j0; j < j0 + each; ++j) {
+        run += w_of(j);
+        if (left < run) {
+          *token = (int)sh.all[j].y;
+          break;
+        }
+      }
+    }
   }
 
   // The sum of W of the list's tokens that lie inside the border (and weigh `least`), with |x|'s bits below d.
@@ -534,7 +582,7 @@ struct Sampler {
     return x;
   }
 
-  // Lists this piece's tokens with |x|'s bits in [from, to); the sum of W of those before.
+  // Lists this piece's tokens with |x|'s bits in [from, to), by index; the sum of W of those before.
   __device__ u64 list_pass(uint32_t from, uint32_t to) {
     uint2 *list = sh.list[warp];
     Sum above;
@@ -549,16 +597,35 @@ struct Sampler {
     }, [&](int at, const float(&x)[kEach]) {
       above.carry();
       j = 0;
-      // (one copy of this, not eight: the kernel's code has to stay in the instruction caches)
-      uint32_t some = __reduce_or_sync(0xffffffffu, marked);
+      if (to > r.border) {  // (a border among tokens of one |x| is one of indices, too)
 #pragma unroll 1
-      for (; some; some &= some - 1) {
-        const int k = __ffs(some) - 1;
-        const uint32_t d = depth(Row<T>::element(x, k), r.M, r.inv), v = (uint32_t)r.index(at, k, lane);
-        const bool mine = (marked >> k) & 1u && r.inside(d, v);
-        const uint32_t who = __ballot_sync(0xffffffffu, mine), place = n + __popc(who & ((1u << lane) - 1));
-        if (mine && place < kWarpList) list[place] = make_uint2(d, v);
-        n += __popc(who);
+        for (uint32_t m = marked; m; m &= m - 1) {
+          const int k = __ffs(m) - 1;
+          if (!r.inside(depth(Row<T>::element(x, k), r.M, r.inv), (uint32_t)r.index(at, k, lane))) marked &= ~(m & -m);
+        }
+      }
+      if (__any_sync(0xffffffffu, marked)) {
+        // in the order of their indices: a lane's vector behind the lanes' before it (16 bits of a count each)
+        uint32_t here = 0;
+#pragma unroll
+        for (int v = 0; v < Row<T>::kVecs; ++v) here |= __popc(marked >> (v * Row<T>::kN) & ((1u << Row<T>::kN) - 1)) << (16 * v);
+        uint32_t incl = here;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += y;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+        uint32_t place = n + (incl - here & 0xffffu), next = n + (all & 0xffffu) + (incl - here >> 16);
+#pragma unroll 1
+        for (uint32_t m = marked; m; m &= m - 1) {
+          const int k = __ffs(m) - 1;
+          if (k >= Row<T>::kN) place = next, next += 1;
+          if (place < kWarpList)
+            list[place] = make_uint2(depth(Row<T>::element(x, k), r.M, r.inv), (uint32_t)r.index(at, k, lane));
+          ++place;
+        }
+        n += (all & 0xffffu) + (all >> 16);
       }
       marked = 0;
     });
@@ -646,7 +713,7 @@ struct Sampler {
         if (wide) q.slack = 0.f;
       }
       if (wide) {
-        cluster_barrier();
+        __syncthreads();
         continue;
       }
       // ---- the exact sum of what lies before the bins, and their tokens
@@ -723,14 +790,20 @@ struct Sampler {
     }
     // ---- the border among the listed tokens
     if (rank == 0) {
-      if (bits >= 0 && q.whole && by_sum) {  // (what lies before the bins: by weight it is summed up here)
-        start = list_sum(listed, lo);
-        if (start >= limit) lo = 0, start = 0, bits = -1;
+      uint2 b;
+      if (listed <= kFew) {
+        b = pick_few(listed, by_sum, limit, q.whole ? 0 : start, sum);
+        sum += A;
+      } else {
+        if (bits >= 0 && q.whole && by_sum) {  // (what lies before the bins: by weight it is summed up here)
+          start = list_sum(listed, lo);
+          if (start >= limit) lo = 0, start = 0, bits = -1;
+        }
+        b = pick(listed, by_sum, limit, start, lo, bits);
       }
-      const uint2 b = pick(listed, false, by_sum, limit, start, lo, bits, sum);
       r.border = b.x;
       r.last = b.y;
-      sum = A + list_sum(listed, UINT_MAX);
+      if (listed > kFew) sum = A + list_sum(listed, UINT_MAX);
       if (!q.whole && warp == 0 && lane < cluster) {
         store_remote(remote(&sh.result[0], lane), (u64)b.x << 32 | b.y);
         store_remote(remote(&sh.result[1], lane), sum);
@@ -885,10 +958,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     if (listed) {
       if (s.rank == 0 && a.tokens) {
         const float u = a.u[row];
-        u64 with;
-        const uint2 t = s.pick(listed, true, true, (u >= 1.f ? total - 1 : share(u, total)) + 1, 0, 0u,
-                               32 - __clz((a.vocab - 1) | 255), with);
-        if (threadIdx.x == 0) a.tokens[row] = (int)t.y;
+        s.draw(listed, u >= 1.f ? total - 1 : share(u, total), a.tokens + row);
       }
       if (!a.probs) return;
       if (s.rank == 0 && warp == 0 && lane < cluster) {
