@@ -134,12 +134,9 @@ __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
 __device__ __forceinline__ void store_remote(uint32_t at, u64 x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
-__device__ __forceinline__ void store_remote(uint32_t at, uint32_t x) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
-}
-__device__ __forceinline__ uint32_t load_remote(uint32_t at) {
-  uint32_t x;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+__device__ __forceinline__ u64 load_remote(uint32_t at) {
+  u64 x;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
   return x;
 }
 __device__ __forceinline__ void cluster_arrive_started() {  // nothing written yet: no release
@@ -195,11 +192,11 @@ struct Search {
 
 struct Shared {
   union {
-    uint32_t hist[kBins];          // this CTA's counts
+    alignas(8) uint32_t hist[kBins];  // this CTA's counts
     uint2 all[kList];              // the first CTA: the cluster's listed tokens (|x|'s bits, index)
   };
   u64 all_w[kList];                // W of `all`
-  uint32_t counts[kBins];          // the cluster's
+  alignas(8) uint32_t counts[kBins];  // the cluster's
   u64 at[kThreads + 1];            // counts and estimates before each thread's bins, and of all
   uint2 list[kWarps][kWarpList];   // listed tokens
   u64 post[2][3][kMaxPieces];      // what the pieces' warps told last, and before that
@@ -350,26 +347,27 @@ struct Sampler {
   // The cluster's counts, to every CTA: each adds up a share of the bins.  Then, alike in all of them, what lies before
   // each thread's bins.
   __device__ void reduce() {
-    const int k = kOwn / cluster, b0 = (rank * kThreads + threadIdx.x) * k;
-    u64 run = 0;
+    const int pairs = kBins / 2 / cluster;  // whole warps of them
 #pragma unroll 1
-    for (int b = 0; b < k; ++b) {
-      uint32_t x[kMaxCluster], c = 0;
+    for (int i = threadIdx.x; i < pairs; i += kThreads) {
+      const int b = 2 * (rank * pairs + i);
+      u64 x[kMaxCluster], c = 0;  // (a count is below 2^23)
 #pragma unroll
-      for (int i = 0; i < kMaxCluster; ++i) x[i] = i < cluster ? load_remote(remote(&sh.hist[b0 + b], i)) : 0;
+      for (int r = 0; r < kMaxCluster; ++r) x[r] = r < cluster ? load_remote(remote(&sh.hist[b], r)) : 0;
 #pragma unroll
-      for (int i = 0; i < kMaxCluster; ++i) c += x[i];
+      for (int r = 0; r < kMaxCluster; ++r) c += x[r];
 #pragma unroll 1
-      for (int i = 0; i < cluster; ++i) store_remote(remote(&sh.counts[b0 + b], i), c);
-      run += sh.q.lv.both(b0 + b, c);
+      for (int r = 0; r < cluster; ++r) store_remote(remote(&sh.counts[b], r), c);
+      u64 sum = sh.q.lv.both(b, (uint32_t)c) + sh.q.lv.both(b + 1, (uint32_t)(c >> 32));
+      // a thread's own bins, in four lanes here
+#pragma unroll
+      for (int d = 1; d < kOwn / 2; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll 1
+      for (int r = lane & (kOwn / 2 - 1); r < cluster; r += kOwn / 2) store_remote(remote(&sh.at[b / kOwn], r), sum);
     }
-    // (kOwn bins lie in as many lanes as there are CTAs: each tells one)
-#pragma unroll 1
-    for (int d = 1; d < cluster; d <<= 1) run += __shfl_xor_sync(0xffffffffu, run, d);
-    store_remote(remote(&sh.at[b0 / kOwn], threadIdx.x & (cluster - 1)), run);
     cluster_barrier();
     const u64 mine = sh.at[threadIdx.x];
-    run = warp_scan(mine, lane);
+    u64 run = warp_scan(mine, lane);
     if (lane == 31) sh.scan_s[warp] = run;
     __syncthreads();
 #pragma unroll 1
