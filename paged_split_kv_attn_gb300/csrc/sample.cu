@@ -25,6 +25,9 @@
 #include <limits.h>
 #include <math_constants.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "pskv_internal.cuh"
 #include "tree.h"
 
@@ -39,6 +42,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxPieces = kMaxCluster * kWarps;
 constexpr int kPerSm = 4;        // CTAs an SM holds (registers)
+constexpr int kSmShared = 228 << 10;  // shared memory of an SM, and what a CTA may ask for beside its own 42 KB
+constexpr int kMostStaged = 180 << 10;
 constexpr int kBins = 2048;
 constexpr int kOwn = kBins / kThreads;
 constexpr int kList = 1024;      // listed tokens of a cluster,
@@ -211,10 +216,13 @@ struct Shared {
   int few[32];
 };
 
+extern __shared__ uint4 staged[];  // a CTA's pieces, where they fit, and a step
+
 // A row as a warp sees it: elements at `base`, 16-byte aligned, of which [skip, end) are the row.
-template <typename T>
+template <typename T, bool kStaged>
 struct Row {
   const T *base;
+  int origin;         // of the CTA's pieces: where `staged` begins
   int skip, end;
   int lo, hi;         // this warp's piece, whole steps (but for the last one's end)
   int chunk_log;      // steps of a chunk: 2^chunk_log
@@ -238,8 +246,9 @@ struct Row {
     const float w = weight(d);
     return w >= least ? w : 0.f;
   }
-  // Logits of a step's elements [i0, b): those that are not the row's or behind b: -inf.
-  __device__ void load(int i0, int b, int lane, float (&x)[kEach]) const {
+  // Logits of a step's elements [i0, b): those that are not the row's or behind b: -inf.  fetch: from memory; load:
+  // from where the first pass has put them.
+  __device__ void fetch(int i0, int b, int lane, float (&x)[kEach]) const {
     if (i0 >= skip && i0 + kStep <= b) {
       const uint4 *p = reinterpret_cast<const uint4 *>(base + i0) + lane;
 #pragma unroll
@@ -257,6 +266,42 @@ struct Row {
         x[j] = at >= skip && at < b ? v : -CUDART_INF_F;
       }
     }
+  }
+  __device__ void put(int i0, int lane, const float (&x)[kEach]) const {
+    uint4 *p = staged + (i0 - origin) / kN + lane;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      uint4 q;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        if constexpr (sizeof(T) == 2)
+          reinterpret_cast<T *>(&q)[e] = (T)(__float_as_uint(x[k * kN + e]) >> 16);
+        else
+          reinterpret_cast<T *>(&q)[e] = x[k * kN + e];
+      }
+      p[32 * k] = q;
+    }
+  }
+  __device__ void load(int i0, int b, int lane, float (&x)[kEach]) const {
+    if constexpr (!kStaged) {
+      fetch(i0, b, lane, x);
+    } else {
+      const uint4 *p = staged + (i0 - origin) / kN + lane;
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const uint4 q = p[32 * k];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) x[k * kN + e] = value(reinterpret_cast<const T *>(&q)[e]);
+      }
+      if (i0 + kStep > b)
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (i0 + (32 * (j / kN) + lane) * kN + j % kN >= b) x[j] = -CUDART_INF_F;
+    }
+  }
+  __device__ float at(int i) const {
+    if constexpr (kStaged) return value(reinterpret_cast<const T *>(staged)[i - origin]);
+    return value(base[i]);
   }
   // Element k of a lane's step (its registers cannot be indexed).
   __device__ static float element(const float (&x)[kEach], int k) {
@@ -276,14 +321,18 @@ struct Row {
   }
   // f(logit) for this piece's elements in live chunks; g(the step's place, its logits) after each step.  (The next
   // step's loads ahead of it were no faster: an SM's other warps cover them, and the registers spill.)
-  template <typename F, typename G>
+  template <bool kFirst = false, typename F, typename G>
   __device__ void each(uint32_t alive, F f, G g) const {
     const int steps = (hi - lo + kStep - 1) / kStep, lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int s = next(0, steps, alive); s < steps; s = next(s + 1, steps, alive)) {
       float x[kEach];
       const int at = lo + s * kStep;
-      load(at, hi, lane, x);
+      if constexpr (kFirst)
+        fetch(at, hi, lane, x);
+      else
+        load(at, hi, lane, x);
+      if constexpr (kFirst && kStaged) put(at, lane, x);
 #pragma unroll
       for (int j = 0; j < kEach; ++j) f(x[j]);
       g(at, x);
@@ -293,17 +342,18 @@ struct Row {
   template <typename F>
   __device__ void each_slowly(int a, int b, int lane, F f) const {
 #pragma unroll 1
-    for (int i = max(a, skip) + lane; i < b; i += 32) f(depth(value(base[i]), M, inv), (uint32_t)(i - skip));
+    for (int i = max(a, skip) + lane; i < b; i += 32) f(depth(at(i), M, inv), (uint32_t)(i - skip));
   }
   // The chunks that have tokens with |x|'s bits below d.
   __device__ uint32_t alive(uint32_t d) const { return __ballot_sync(0xffffffffu, depth(chunk_top, M, inv) < d); }
 };
 
-template <typename T>
+template <typename T, bool kStaged>
 struct Sampler {
+  using R = Row<T, kStaged>;
   const SampleArgs &a;
   Shared &sh;
-  Row<T> r;
+  R r;
   int cluster, rank, warp, lane, piece, pieces;
   int turn = 0;         // exchanges so far: their buffers alternate
   enum { kCounted, kReduced, kGone } first_level = kCounted;  // its counts in sh.hist; its shares added up; neither
@@ -599,14 +649,14 @@ struct Sampler {
 #pragma unroll 1
         for (uint32_t m = marked; m; m &= m - 1) {
           const int k = __ffs(m) - 1;
-          if (!r.inside(depth(Row<T>::element(x, k), r.M, r.inv), (uint32_t)r.index(at, k, lane))) marked &= ~(m & -m);
+          if (!r.inside(depth(R::element(x, k), r.M, r.inv), (uint32_t)r.index(at, k, lane))) marked &= ~(m & -m);
         }
       }
       if (__any_sync(0xffffffffu, marked)) {
         // in the order of their indices: a lane's vector behind the lanes' before it (16 bits of a count each)
         uint32_t here = 0;
 #pragma unroll
-        for (int v = 0; v < Row<T>::kVecs; ++v) here |= __popc(marked >> (v * Row<T>::kN) & ((1u << Row<T>::kN) - 1)) << (16 * v);
+        for (int v = 0; v < R::kVecs; ++v) here |= __popc(marked >> (v * R::kN) & ((1u << R::kN) - 1)) << (16 * v);
         uint32_t incl = here;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -618,9 +668,9 @@ struct Sampler {
 #pragma unroll 1
         for (uint32_t m = marked; m; m &= m - 1) {
           const int k = __ffs(m) - 1;
-          if (k >= Row<T>::kN) place = next, next += 1;
+          if (k >= R::kN) place = next, next += 1;
           if (place < kWarpList)
-            list[place] = make_uint2(depth(Row<T>::element(x, k), r.M, r.inv), (uint32_t)r.index(at, k, lane));
+            list[place] = make_uint2(depth(R::element(x, k), r.M, r.inv), (uint32_t)r.index(at, k, lane));
           ++place;
         }
         n += (all & 0xffffu) + (all >> 16);
@@ -638,7 +688,7 @@ struct Sampler {
       for (int i = r.lo; i < r.hi; i += 32) {
         const int at = i + lane;
         const bool eq = at >= r.skip && at < r.hi && r.inside(d, (uint32_t)(at - r.skip)) &&
-                        depth(Row<T>::value(r.base[at]), r.M, r.inv) == d;
+                        depth(r.at(at), r.M, r.inv) == d;
         uint32_t who = __ballot_sync(0xffffffffu, eq);
         if (ties <= run + __popc(who)) {
 #pragma unroll 1
@@ -825,11 +875,13 @@ struct Sampler {
 
 }  // namespace
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs a, const int cluster) {
+template <typename T, bool kStaged>
+__global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs a, const int cluster,
+                                                                     const bool beside) {
   __shared__ Shared sh;
-  Sampler<T> s{a, sh};
-  Row<T> &r = s.r;
+  Sampler<T, kStaged> s{a, sh};
+  using R = Row<T, kStaged>;
+  R &r = s.r;
   s.cluster = cluster;
   s.rank = (int)cluster_rank();
   s.warp = threadIdx.x >> 5;
@@ -839,14 +891,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   const int row = blockIdx.x / cluster, lane = s.lane, warp = s.warp;
   cluster_arrive_started();
   pdl_wait();
-  pdl_launch_dependents();
+  if (beside) pdl_launch_dependents();
   // ---- the row's pieces, from the 16-byte boundary before it
   const T *l = static_cast<const T *>(a.logits) + row * a.logits_row;
   r.skip = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
   r.base = l - r.skip;
   r.end = r.skip + a.vocab;
-  constexpr int kN = Row<T>::kN;
+  constexpr int kN = R::kN;
   const int seg = ((r.end + s.pieces - 1) / s.pieces + kStep - 1) / kStep * kStep;
+  r.origin = s.rank * kWarps * seg;
   r.lo = min(s.piece * seg, r.end);
   r.hi = min(r.lo + seg, r.end);
   r.chunk_log = max(0, 32 - __clz(max(seg - 1, 0) / (32 * kStep)));  // at most 32 chunks
@@ -858,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
   r.chunk_top = -CUDART_INF_F;
   {
     float chunk = -CUDART_INF_F;
-    r.each(~0u, [&](float x) { chunk = fmaxf(chunk, x); }, [&](int at, const float(&)[kEach]) {
+    r.template each<true>(~0u, [&](float x) { chunk = fmaxf(chunk, x); }, [&](int at, const float(&)[kEach]) {
       const int step = (at - r.lo) / kStep + 1;
       if (step & ((1 << r.chunk_log) - 1) && at + kStep < r.hi) return;
       chunk = warp_max(chunk);
@@ -901,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     if (r.alive(1u))
 #pragma unroll 1
       for (int i = max(r.lo, r.skip) + lane; i < r.hi && at == UINT_MAX; i += 32)
-        if (Row<T>::value(r.base[i]) == top) at = (uint32_t)(i - r.skip);
+        if (r.at(i) == top) at = (uint32_t)(i - r.skip);
     s.template exchange<1>((u64)__reduce_min_sync(0xffffffffu, at));
     const u64 *ats = sh.post[1][0];
     if (lane < s.pieces) at = min(at, (uint32_t)ats[lane]);
@@ -952,6 +1005,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
         total = s.told(0);
       }
     }
+    pdl_launch_dependents();
     // ---- the draw: where the running sum passes u's share
     if (listed) {
       if (s.rank == 0 && a.tokens) {
@@ -984,11 +1038,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
         const int sub = ((p1 - p0 + kWarps - 1) / kWarps + kN - 1) / kN * kN;
         const int s0 = min(p0 + warp * sub, p1), s1 = min(s0 + sub, p1);
         // (a vector's elements lie one after another, then the next lane's: sums of each vector of a lane)
-        constexpr int kVecs = Row<T>::kVecs;
+        constexpr int kVecs = R::kVecs;
         u64 own = 0, part[kVecs] = {};
         float x[kEach];
         auto weigh = [&](int at, int j) {
-          return whole_weight(r.kept(depth(Row<T>::element(x, j), r.M, r.inv), (uint32_t)r.index(at, j, lane)));
+          return whole_weight(r.kept(depth(R::element(x, j), r.M, r.inv), (uint32_t)r.index(at, j, lane)));
         };
         auto sums = [&](int at) {
           r.load(at, s1, lane, x);
@@ -1090,8 +1144,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
 
 namespace {
 
-template <typename T>
-cudaError_t launch(const SampleArgs &a, int cluster, cudaStream_t s) {
+template <typename T, bool kStaged>
+cudaError_t launch(const SampleArgs &a, int cluster, bool beside, size_t bytes, cudaStream_t s) {
+  if (kStaged) {
+    static std::atomic<bool> allowed[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(dev >= 0 && dev < 64 && allowed[dev])) {
+      e = cudaFuncSetAttribute(pskv_sample<T, kStaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostStaged);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) allowed[dev] = true;
+    }
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1102,10 +1167,26 @@ cudaError_t launch(const SampleArgs &a, int cluster, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.rows * cluster);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kStaged ? bytes : 0;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pskv_sample<T>, a, cluster);
+  return cudaLaunchKernelEx(&cfg, pskv_sample<T, kStaged>, a, cluster, beside);
+}
+
+template <typename T>
+cudaError_t launch(const SampleArgs &a, int cluster, int sms, cudaStream_t s) {
+  // A CTA's pieces stay in shared memory where all CTAs run at once all the same: at three or more an SM with an eighth
+  // of the places to spare, else half of them, as clusters do not fill every group of SMs (80 rows of 32,001 bf16, 17 KB:
+  // 33 -> 28 us; one of 131,072 f32, 66 KB: 9.8 -> 8.8; but 16 of these, 128 CTAs of one or two an SM: 11.2 -> 15.3).
+  const long long seg = ((a.vocab + 16 / (int)sizeof(T) - 1 + cluster * kWarps - 1) / (cluster * kWarps) + kStep - 1) / kStep * kStep;
+  const long long bytes = (kWarps * seg + kStep) * (long long)sizeof(T), ctas = (long long)a.rows * cluster;
+  const long long fit = bytes <= kMostStaged ? std::min<long long>(kPerSm, kSmShared / ((long long)sizeof(Shared) + bytes + 1024)) : 0;
+  const bool staged = fit >= 3 ? ctas + ctas / 8 <= fit * sms : fit > 0 && 2 * ctas <= sms;
+  // The next grid may start beside this one where both fit; else its CTAs would take what places there are, unevenly
+  // (40 rows of 131,072 bf16 one call after the other: 16.7 -> 14.2 us; but 32, where both fit: 12.1 -> 13.5)
+  const bool beside = 2 * ctas <= (staged ? fit : kPerSm) * sms;
+  return staged ? launch<T, true>(a, cluster, beside, (size_t)bytes, s) : launch<T, false>(a, cluster, beside, 0, s);
 }
 
 }  // namespace
@@ -1115,7 +1196,7 @@ cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t s) {
   int cluster = kMaxCluster;
 #pragma unroll 1
   while (cluster > 1 && (long long)a.rows * cluster > (long long)kPerSm * sms) cluster /= 2;
-  return a.dtype == PSKV_DTYPE_BF16 ? launch<uint16_t>(a, cluster, s) : launch<float>(a, cluster, s);
+  return a.dtype == PSKV_DTYPE_BF16 ? launch<uint16_t>(a, cluster, sms, s) : launch<float>(a, cluster, sms, s);
 }
 
 }  // namespace pskv

@@ -264,6 +264,28 @@ def test_many_rows():
         assert check(l, u, **filters(rows, top_p=0.95)) == 0
 
 
+@pytest.mark.parametrize("rows", [76, 150, 303, 620])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("which", range(len(FILTERS)))
+def test_batches_that_fill_the_chip(rows, dtype, which):
+    """Rows that are read from memory again, off 16 bytes, many equal logits and masked ones, some at temperature 0."""
+    l, u = inputs(rows + which, rows, 1, 1237, dtype, lattice=[None, 4, 2][which % 3])
+    l = l[:, 0, 1:1236]
+    l[:, 5::3] = -float("inf")
+    l[3] = 0.5  # all equal
+    l[4, 7:] = -float("inf")
+    kw = filters(rows, **FILTERS[which])
+    kw["temperature"][7::9] = 0.0
+    assert check(l, u[:, 0].contiguous(), torch.float32 if which % 2 else None, **kw) == 0
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(75, 131072, torch.bfloat16), (2, 1500001, torch.float32)])
+def test_pieces_larger_than_shared_memory(rows, vocab, dtype):
+    l, u = inputs(vocab, rows, 1, vocab, dtype)
+    assert check(l, u, **filters(rows, top_k=300, top_p=0.99, min_p=0.001)) == 0
+    assert check(l, u, **filters(rows, top_p=0.9)) == 0
+
+
 def test_two_streams_at_once():
     """Calls that run beside each other on two streams, replayed and eager."""
     a, b = inputs(40, 24, 1, 40000, torch.float32), inputs(41, 40, 2, 9000, torch.bfloat16)
