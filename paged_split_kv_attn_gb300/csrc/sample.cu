@@ -6,21 +6,28 @@
 // W are whole numbers and sums 64-bit integers, so nothing depends on how the work is split.
 //
 // A cluster of up to eight CTAs takes a row, each warp a piece of the vocabulary.  The row is
-// read from memory once, for M; the later passes find it in L1 and L2 (staged in shared memory, fewer
-// CTAs fit on an SM: 64 rows of 131,072 would take two waves).
+// read from memory once, for M; later passes find it in shared memory where the pieces fit (rows few or short), else
+// in L1 and L2 (64 rows of 131,072 f32 staged in shared memory would take two waves).
 //   1  M, and the largest logit of each of a piece's 32 chunks: later passes leave out chunks below what they look for
 //   2  the sum of W, and a histogram of |x| in steps of 1/64 (counts: a shared-memory atomic a token,
 //      beside the exponentials)
 //   3  the bin that holds the border: by the counts (top-k), or by the bins' estimated weight (top-p); each CTA
-//      looks through a share of the bins.  The pass sums W exactly over what lies before the bin and lists the
-//      bin's own tokens; or, where they are few enough, all tokens up to the bin's end.  An estimate that was off
-//      shows in the exact sums, and another bin is tried from there.  A bin that does not fit the list is
-//      cut into 2,048 finer ones, down to a single |x|, whose tokens' border is a matter of counting.
-//      The listed tokens go to the first CTA, which finds the border among them (256 bins of a token's key at a
-//      time: |x|'s bits, then the index).  Where they are all that is kept, it finds top-p's border and draws
-//      from them, too, and the other CTAs are done
+//      adds up a share of the bins and tells all, which then find the border alike.  The pass sums W exactly over what
+//      lies before the bin and lists the bin's own tokens; or, where they are few enough, all tokens up to the bin's
+//      end.  An estimate that was off shows in the exact sums, and another bin is tried from there.  A bin that does not
+//      fit the list is cut into 2,048 finer ones, down to a single |x|, whose tokens' border is a matter of counting.
+//      The listed tokens go to the first CTA, by index.  It finds the border among them (up to 64: each compared
+//      with all; more: 256 bins of a token's key at a time, |x|'s bits, then the index).  Where they are all
+//      that is kept, it finds top-p's border and draws from them, too, and the other CTAs are done
 //   4  else the drawn token's piece again; and the probabilities where they are asked for.
 // Between passes the warps' results cross the cluster through distributed shared memory, one barrier each.
+//
+// What bounds it (device time, calls one after the other): without top-k and top-p instructions, about 22 a token
+// for M, the exponential and two whole digits of it: 64 x 131,072 f32 16.3 us (2.1 TB/s), 256 x 32,001 16.4.  top-p over
+// weights that are spread out (64 x 131,072: 40.7 us) takes a second pass of exponentials, 7 of these us, and
+// nine cluster barriers of about 1 us each with what they wait for.  One row of 32,001 with top-k, top-p and min-p
+// (13.7 us) is that chain alone, and the first fetch of its code: hence loops that are not unrolled wherever speed
+// does not count (134 -> 97 KB of code: 64 x 131,072 49 -> 45 us, a row 16 -> 15).
 #include <float.h>
 #include <limits.h>
 #include <math_constants.h>
@@ -186,6 +193,7 @@ struct Search {
   bool by_sum;             // the border is one of weight, not of number
   bool counted, reduced;   // the level's counts are in, and its shares added up
   bool whole;              // the list is to hold all of the first part
+  bool spread;             // and may (no warp has yet had more tokens of it than its list holds)
   int first, last, tries;  // bins in question
   u64 limit, many;         // the border's sum or number, and its number within the level
   u64 S;                   // the sum of the level's W
@@ -724,6 +732,7 @@ struct Sampler {
         q.counted = first_level != kGone;
         q.reduced = first_level == kReduced;
         q.first = q.tries = 0;
+        q.spread = true;
         q.last = kBins - 1;
         q.limit = q.many = limit;
         q.S = S;
@@ -747,7 +756,7 @@ struct Sampler {
       const uint32_t before_n = (uint32_t)sh.taken[1] & kCount, until_n = (uint32_t)sh.taken[3] & kCount;
       if (!q.by_sum && q.lv.shift < 0 && bin == kBins - 1) return;
       // the whole first part is listed where it fits
-      const bool whole = q.skipped + until_n <= kList;
+      const bool whole = q.spread && q.skipped + until_n <= kList;
       const bool wide = !whole && bin < bin_to && until_n - before_n > kList && q.slack > 0.f;
       const uint32_t begin = q.lv.begin(bin), from = whole ? 0u : begin, to = q.lv.begin(bin_to + 1);
       __syncthreads();
@@ -819,6 +828,9 @@ struct Sampler {
         q.w = low ? -(float)(A - q.limit) : (float)(q.limit - (whole ? B : A));
         q.slack = kSlack;
         ++q.tries;
+      } else if (lead && q.whole) {
+        // (a warp has too many of them, as where a mask leaves a run of tokens: the bins' own, then)
+        q.spread = false;
       } else if (lead) {
         // finer bins
         q.skipped = q.before;

@@ -279,6 +279,20 @@ def test_batches_that_fill_the_chip(rows, dtype, which):
     assert check(l, u[:, 0].contiguous(), torch.float32 if which % 2 else None, **kw) == 0
 
 
+@pytest.mark.parametrize("vocab,start,n", [(1000, 0, 1000), (1000, 1, 998), (4000, 700, 150), (32001, 9000, 700), (131072, 40000, 2000)])
+@pytest.mark.parametrize("k,p", [(5, 1.0), (5, 0.5), (130, 1.0), (140, 0.9), (600, 1.0), (900, 0.7), (0, 0.3), (0, 0.999)])
+@pytest.mark.parametrize("lattice", [None, 4])
+def test_runs_of_allowed_tokens(vocab, start, n, k, p, lattice):
+    """What is kept lies in a few warps' pieces; likelier tokens before many equal ones."""
+    l, u = inputs(vocab + n + k, 3, 1, vocab, torch.float32, lattice=lattice)
+    l[..., :start] = l[..., start + n:] = -float("inf")
+    l[1, :, start:start + n] = torch.where(torch.arange(n, device="cuda") % 97 == 5, 9.0, 0.0)
+    kw = {} if k == 0 else dict(top_k=torch.full((3,), k, dtype=torch.int32, device="cuda"))
+    if p < 1:
+        kw["top_p"] = torch.full((3,), p, device="cuda")
+    assert check(l, u, torch.float32 if k % 2 else None, **kw) == 0
+
+
 @pytest.mark.parametrize("rows,vocab,dtype", [(75, 131072, torch.bfloat16), (2, 1500001, torch.float32)])
 def test_pieces_larger_than_shared_memory(rows, vocab, dtype):
     l, u = inputs(vocab, rows, 1, vocab, dtype)
