@@ -208,7 +208,7 @@ def _bind_calls(lib):
         except ImportError as e:
             calls, why = _PythonCalls, str(e)
     if calls is _PythonCalls:
-        warnings.warn(f"the latent operators run without their compiled calls ({why}), some microseconds slower a "
+        warnings.warn(f"the latent, sampling, tree and row operators run without their compiled calls ({why}), some microseconds slower a "
                       "call; `python -m paged_split_kv_attn_gb300.build` makes them", RuntimeWarning)
     _calls = calls
     return calls

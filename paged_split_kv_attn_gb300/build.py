@@ -1,6 +1,6 @@
 """Build ``libpskv.so`` in-tree: every CUDA source compiled for sm_103a with nvcc,
 in parallel, then linked into one shared library (static CUDA runtime), and ``_calls.so``, the
-latent operators' Python calls in compiled form.  The library needs nvcc alone; the compiled calls need
+Python calls of the latent, sampling, tree and row operators in compiled form.  The library needs nvcc alone; the compiled calls need
 PyTorch's and Python's headers and fit one version of both.  Without them the operators' Python forms
 do the same work, some microseconds of host time a call slower.
 
