@@ -57,6 +57,7 @@ constexpr int kList = 1024;      // listed tokens of a cluster,
 constexpr int kWarpList = kList / kWarps;  // and of a warp
 constexpr int kFew = kThreads / 4;         // of a list whose tokens are compared with each other
 constexpr int kCountBits = 23;   // of a number that holds a count (up to 2^22) and an estimate (up to 2^40)
+constexpr int kMostPasses = 256;  // (never reached: a search ends in less)
 constexpr int kEach = 8;         // elements a lane takes in a step
 constexpr int kStep = 32 * kEach;
 constexpr float kSlack = 2.5e-4f;  // of an estimated sum: half a bin's width off in some of the likeliest tokens
@@ -199,7 +200,7 @@ struct Search {
   u64 S;                   // the sum of the level's W
   u64 skipped, before;     // tokens before the level's first bin, and before the taken ones
   u64 e_before;            // the estimate before these
-  float e0, w, slack;      // the estimate looked for: e0 + w's share, give or take slack
+  float e0, w, slack;      // the estimate looked for: e0 and what the weight w makes, give or take slack of that
   uint32_t from, to;       // |x|'s bits of the taken bins
 };
 
@@ -436,17 +437,21 @@ struct Sampler {
   }
 
   // Takes the bins that may hold the border: the one at which the running count reaches q.many, or (by_sum) those at
-  // which the running estimate may pass q.e0 + q.w's share of all bins' (S), give or take q.slack of it; within
-  // [q.first, q.last] (after some wrong guesses the middle one).  Every CTA finds the same ones.
+  // which the running estimate may pass q.e0 and what q.w (a sum of W) makes, give or take q.slack of that; within
+  // [q.first, q.last] (from the third wrong guess on the middle one).  Every CTA finds the same ones.
   __device__ void seek() {
     const Search &q = sh.q;
     u64 target[2] = {q.many, q.many};
     if (q.by_sum) {
-      const float e = q.e0 + q.w * ((float)(sh.at[kThreads] >> kCountBits) / (float)q.S), slack = e * q.slack;
+      // (an estimate's unit is 2^22 of W's; within a hundredth of that the level's own ratio is better: else it has
+      // tokens that top-k left out)
+      float unit = (float)(sh.at[kThreads] >> kCountBits) / (float)q.S;
+      if (!(fabsf(unit * 0x1p22f - 1.f) <= 0.01f)) unit = 0x1p-22f;
+      const float part = q.w * unit, e = q.e0 + part, slack = fabsf(part) * q.slack;
       target[0] = __float2ull_rn(fmaxf(e - slack, 1.f));
       target[1] = __float2ull_rn(fmaxf(e + slack, 1.f));
     }
-    const int first = q.tries < 5 ? q.first : (q.first + q.last) / 2, last = q.tries < 5 ? q.last : first;
+    const int first = q.tries < 3 ? q.first : (q.first + q.last) / 2, last = q.tries < 3 ? q.last : first;
     const int b0 = threadIdx.x * kOwn;
     auto number = [&](u64 x) { return q.by_sum ? x >> kCountBits : x & ((1ull << kCountBits) - 1); };
     // a bin (or a thread's bins b .. to) holds a target
@@ -480,10 +485,10 @@ struct Sampler {
       key = tied ? q.y : q.x;
       return r.inside(q.x, q.y) && (!tied || q.x == fixed);
     };
-    uint32_t width;          // of the last level's bin
+    uint32_t width = 0;      // of the last level's bin
     int shift = max(0, bits - 8);
 #pragma unroll 1
-    for (;;) {
+    for (int level = 0; level < 16; ++level) {  // (five of |x| and three of the index at most)
       sh.sub_n[threadIdx.x] = sh.sub_hi[threadIdx.x] = sh.sub_lo[threadIdx.x] = 0;
       if (threadIdx.x == 0) sh.sub_bin = kThreads - 1, sh.few_n = 0, sh.sub_count = 0;
       __syncthreads();
@@ -746,15 +751,20 @@ struct Sampler {
       first_level = kReduced;
       __syncthreads();
     }
+    // A pass ends the search, goes to a level of one of its level's bins (up to three times), or narrows what it looks at
+    // within it: [first, last] in halves from the third wrong guess on, or once to one bin or to the bins alone
 #pragma unroll 1
-    while (!listed) {
+    for (int pass = 0; !listed && pass < kMostPasses; ++pass) {
       if (!q.counted) count();
       if (!q.reduced) reduce();
       seek();
       const int bin = (int)sh.taken[0], bin_to = (int)sh.taken[2];
       constexpr uint32_t kCount = (1u << kCountBits) - 1;
       const uint32_t before_n = (uint32_t)sh.taken[1] & kCount, until_n = (uint32_t)sh.taken[3] & kCount;
-      if (!q.by_sum && q.lv.shift < 0 && bin == kBins - 1) return;
+      if (!q.by_sum && q.lv.shift < 0 && bin == kBins - 1) {
+        __syncthreads();  // (the next search writes to q)
+        return;
+      }
       // the whole first part is listed where it fits
       const bool whole = q.spread && q.skipped + until_n <= kList;
       const bool wide = !whole && bin < bin_to && until_n - before_n > kList && q.slack > 0.f;
@@ -811,10 +821,10 @@ struct Sampler {
       }
       if (!low && !high && to - from == 1) {
         const u64 W = whole_weight(weight(from)), stay = q.by_sum ? (q.limit - A + W - 1) / W : q.limit - q.before;
-        rank_ties(from, stay, N_before, n);
+        first_level = q.lv.shift < 0 ? kReduced : kGone;
+        rank_ties(from, stay, N_before, n);  // (ends with a barrier, after which q may be written to)
         sum = A + stay * W;
         mine = above_here + (stay > N_before ? min(stay - N_before, (u64)n) : 0) * W;
-        first_level = q.lv.shift < 0 ? kReduced : kGone;
         return;
       }
       __syncthreads();
@@ -826,11 +836,14 @@ struct Sampler {
           q.first = min(bin_to + 1, kBins - 1);
         q.e0 = (float)q.e_before;
         q.w = low ? -(float)(A - q.limit) : (float)(q.limit - (whole ? B : A));
-        q.slack = kSlack;
+        q.slack = 8 * kSlack;
         ++q.tries;
       } else if (lead && q.whole) {
         // (a warp has too many of them, as where a mask leaves a run of tokens: the bins' own, then)
         q.spread = false;
+      } else if (lead && bin < bin_to) {
+        // (they may be all of the level: the one bin of the estimate, then)
+        q.slack = 0.f;
       } else if (lead) {
         // finer bins
         q.skipped = q.before;
@@ -841,12 +854,11 @@ struct Sampler {
         q.many = q.limit - q.before;
         q.e0 = 0.f;
         q.w = q.by_sum ? (float)(q.limit - A) : 0.f;
-        q.S = B > 0 ? B : 1;  // (without what top-k left out: a first guess that this puts off is tried again)
+        q.S = B > 0 ? B : 1;
         q.slack = kSlack;
       }
       __syncthreads();
       first_level = q.lv.shift < 0 ? kReduced : kGone;
-      if (q.tries > 40) return;  // (never)
     }
     // ---- the border among the listed tokens
     if (rank == 0) {
