@@ -575,10 +575,13 @@ struct Sampler {
     const uint2 q = sh.all[i];  // (a place behind the list is no hit)
     u64 w = 0;
     uint32_t place = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int j = threadIdx.x & 3; j < listed; j += 4) {
       const uint2 o = sh.all[j];
-      if (r.inside(o.x, o.y) && (o.x < q.x || (o.x == q.x && o.y <= q.y))) w += sh.all_w[j], ++place;
+      const u64 x = sh.all_w[j];
+      const bool before_it = r.inside(o.x, o.y) & (o.x < q.x || (o.x == q.x && o.y <= q.y));
+      w += before_it ? x : 0;
+      place += before_it;
     }
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) {
