@@ -65,7 +65,7 @@ def test_matches_the_definition(batch, each, vocab, dtype, which):
 
 
 @pytest.mark.parametrize("vocab,dtype", [(131072, torch.float32), (131072, torch.bfloat16), (262147, torch.float32),
-                                         (700001, torch.bfloat16)])
+                                         (350000, torch.float32), (700001, torch.bfloat16)])
 @pytest.mark.parametrize("which", [0, 2, 4, 5])
 def test_large_vocabularies(vocab, dtype, which):
     l, u = inputs(vocab + which, 2, 1, vocab, dtype)
@@ -291,6 +291,31 @@ def test_runs_of_allowed_tokens(vocab, start, n, k, p, lattice):
     if p < 1:
         kw["top_p"] = torch.full((3,), p, device="cuda")
     assert check(l, u, torch.float32 if k % 2 else None, **kw) == 0
+
+
+@pytest.mark.parametrize("vocab,start,n", [(600, 0, 600), (4000, 1500, 300), (40000, 7, 1000)])
+@pytest.mark.parametrize("p", [0.9999, 0.999999, 0.99999994])
+@pytest.mark.parametrize("above", [6.0, 15.0, 22.0])
+def test_a_dominating_token_and_a_run_of_light_ones(vocab, start, n, p, above):
+    """top-p's border among weights that its estimates do not tell apart."""
+    l, u = inputs(vocab, 3, 1, vocab, torch.float32, spread=0.2)
+    l[..., :start] = l[..., start + n:] = -float("inf")
+    l[:, :, start + n // 2] = above
+    l[2] = torch.round(l[2])
+    kw = dict(top_p=torch.full((3,), p, device="cuda"))
+    assert check(l, u, torch.float32, **kw) == 0
+    assert check(l, u, top_k=torch.tensor([n // 2, n - 1, n + 5], dtype=torch.int32, device="cuda"), **kw) == 0
+
+
+def test_top_k_that_keeps_all_with_weight_then_top_p():
+    """The first search ends at once and the second begins: many times over, on a filled chip."""
+    l, u = inputs(5, 76, 1, 1500, torch.float32)
+    l[..., 100:] = -float("inf")
+    kw = dict(top_k=torch.full((76,), 120, dtype=torch.int32, device="cuda"), top_p=torch.full((76,), 0.7, device="cuda"))
+    first = pskv.sample_tokens(l, u, **kw)
+    for _ in range(300):
+        again = pskv.sample_tokens(l, u, **kw)
+    assert torch.equal(first, again) and check(l, u, **kw) == 0
 
 
 @pytest.mark.parametrize("rows,vocab,dtype", [(75, 131072, torch.bfloat16), (2, 1500001, torch.float32)])
