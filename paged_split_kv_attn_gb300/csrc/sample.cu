@@ -458,16 +458,19 @@ struct Sampler {
     auto here = [&](u64 t, int b, int to, u64 before, u64 until) {
       return to >= first && b <= last && (b <= first || number(before) < t) && (to >= last || number(until) >= t);
     };
-    u64 run = sh.at[threadIdx.x];
-    const u64 end = sh.at[threadIdx.x + 1];
-    if (here(target[0], b0, b0 + kOwn - 1, run, end) || here(target[1], b0, b0 + kOwn - 1, run, end))
+    const u64 run = sh.at[threadIdx.x], end = sh.at[threadIdx.x + 1];
+    // (its bins a lane each)
 #pragma unroll 1
-      for (int b = b0; b < b0 + kOwn; ++b) {
-        const u64 to = run + q.lv.both(b, sh.counts[b]);
-        if (here(target[0], b, b, run, to)) sh.taken[0] = (u64)b, sh.taken[1] = run;
-        if (here(target[1], b, b, run, to)) sh.taken[2] = (u64)b, sh.taken[3] = to;
-        run = to;
+    for (uint32_t who = __ballot_sync(0xffffffffu, here(target[0], b0, b0 + kOwn - 1, run, end) ||
+                                                       here(target[1], b0, b0 + kOwn - 1, run, end));
+         who; who &= who - 1) {
+      const int l = __ffs(who) - 1, b = (warp * 32 + l) * kOwn + (lane & (kOwn - 1));
+      const u64 x = lane < kOwn ? q.lv.both(b, sh.counts[b]) : 0, to = __shfl_sync(0xffffffffu, run, l) + warp_scan(x, lane);
+      if (lane < kOwn) {
+        if (here(target[0], b, b, to - x, to)) sh.taken[0] = (u64)b, sh.taken[1] = to - x;
+        if (here(target[1], b, b, to - x, to)) sh.taken[2] = (u64)b, sh.taken[3] = to;
       }
+    }
     __syncthreads();
   }
 
