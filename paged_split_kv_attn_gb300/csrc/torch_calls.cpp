@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -124,7 +124,8 @@ at::Tensor fresh(const at::Tensor &like, at::ScalarType kind, Shape shape, PyObj
                            ? c10::cuda::getDefaultCUDAStream((c10::DeviceIndex)dev)
                            : c10::cuda::getStreamFromExternal(raw, (c10::DeviceIndex)dev));
   }
-  return at::empty(shape, like.options().dtype(kind));
+  // (straight from the allocator: three of them through at::empty took 0.6 us more)
+  return at::Tensor(at::detail::empty_cuda(shape, kind, like.device(), std::nullopt));
 }
 
 // The output: the given tensor, or a new one of `code`'s type (-1: the caller's to refuse).
