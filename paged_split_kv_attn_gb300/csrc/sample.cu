@@ -397,9 +397,10 @@ struct Sampler {
     __syncthreads();
     const uint32_t from = q.from, to = q.to;
     const Level lv = q.lv;
-    r.each_slowly(r.lo, r.hi, lane, [&](uint32_t d, uint32_t) {
+    r.each(r.alive(to), [&](float l) {
+      const uint32_t d = depth(l, r.M, r.inv);
       if (d - from < to - from) atomicAdd(&sh.hist[lv.bin(d)], 1u);
-    });
+    }, [&](int, const float(&)[kEach]) {});
     cluster_barrier();
   }
 
@@ -671,7 +672,9 @@ struct Sampler {
           if (!r.inside(depth(R::element(x, k), r.M, r.inv), (uint32_t)r.index(at, k, lane))) marked &= ~(m & -m);
         }
       }
-      if (__any_sync(0xffffffffu, marked)) {
+      if (n > kWarpList) {  // (too many already)
+        n += __reduce_add_sync(0xffffffffu, (uint32_t)__popc(marked));
+      } else if (__any_sync(0xffffffffu, marked)) {
         // in the order of their indices: a lane's vector behind the lanes' before it (16 bits of a count each)
         uint32_t here = 0;
 #pragma unroll
@@ -1026,7 +1029,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
       if (listed) {
         if (r.least > 0.f && s.rank == 0) total = s.list_sum(listed, UINT_MAX);
       } else {
-        if (r.least > 0.f) {
+        // (where the border's weight is above it, so are all: expf is right to 2^-22)
+        if (r.least > 0.f && weight(r.border) < r.least * 1.000001f) {
           mine = 0;
           r.each_slowly(r.lo, r.hi, lane, [&](uint32_t d, uint32_t v) { mine += whole_weight(r.kept(d, v)); });
           mine = warp_sum(mine);
