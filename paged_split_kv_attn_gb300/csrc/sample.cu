@@ -1031,9 +1031,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
       } else {
         // (where the border's weight is above it, so are all: expf is right to 2^-22)
         if (r.least > 0.f && weight(r.border) < r.least * 1.000001f) {
+          Sum some;
+          uint32_t tied = 0;  // bit j: element j of the lane's step is as deep as the border
+          int j = 0;
           mine = 0;
-          r.each_slowly(r.lo, r.hi, lane, [&](uint32_t d, uint32_t v) { mine += whole_weight(r.kept(d, v)); });
-          mine = warp_sum(mine);
+          r.each(r.alive(r.border + 1), [&](float x) {
+            const uint32_t d = depth(x, r.M, r.inv);
+            const float w = weight(d);
+            some.add(d < r.border && w >= r.least ? w : 0.f);
+            tied |= (uint32_t)(d == r.border) << j++;
+          }, [&](int at, const float(&)[kEach]) {
+            some.carry();
+            j = 0;
+#pragma unroll 1
+            for (; tied; tied &= tied - 1)
+              mine += whole_weight(r.kept(r.border, (uint32_t)r.index(at, __ffs(tied) - 1, lane)));
+          });
+          mine = warp_sum(mine + some.total);
         }
         s.template exchange<1>(mine);
         total = s.told(0);
