@@ -25,7 +25,7 @@
 // What bounds it (device time, calls one after the other): without top-k and top-p instructions, about 22 a token
 // for M, the exponential and two whole digits of it: 64 x 131,072 f32 16.3 us (2.1 TB/s), 256 x 32,001 16.4.  top-p over
 // weights that are spread out (64 x 131,072: 39.9 us) takes a second pass of exponentials, 7 of these us, and
-// nine cluster barriers of about 1 us each with what they wait for.  One row of 32,001 with top-k, top-p and min-p
+// eight cluster barriers of about 1 us each with what they wait for.  One row of 32,001 with top-k, top-p and min-p
 // (12.6 us) is that chain alone, and the first fetch of its code: hence loops that are not unrolled wherever speed
 // does not count (134 -> 97 KB of code: 64 x 131,072 49 -> 45 us, a row 16 -> 15).
 #include <float.h>
