@@ -36,13 +36,14 @@
 #include <atomic>
 
 #include "pskv_internal.cuh"
+#include "sample_search.h"
 #include "tree.h"
 
 namespace pskv {
 
 namespace {
 
-using u64 = unsigned long long;
+using namespace border;
 
 constexpr int kMaxCluster = 8;
 constexpr int kWarps = 8;
@@ -51,18 +52,12 @@ constexpr int kMaxPieces = kMaxCluster * kWarps;
 constexpr int kPerSm = 4;        // CTAs an SM holds (registers)
 constexpr int kSmShared = 228 << 10;  // shared memory of an SM, and what a CTA may ask for beside its own 42 KB
 constexpr int kMostStaged = 180 << 10;
-constexpr int kBins = 2048;
 constexpr int kOwn = kBins / kThreads;
-constexpr int kList = 1024;      // listed tokens of a cluster,
-constexpr int kWarpList = kList / kWarps;  // and of a warp
+constexpr int kWarpList = kList / kWarps;  // listed tokens of a warp
 constexpr int kFew = kThreads / 4;         // of a list whose tokens are compared with each other
-constexpr int kCountBits = 23;   // of a number that holds a count (up to 2^22) and an estimate (up to 2^40)
 constexpr int kMostPasses = 256;  // (never reached: a search ends in less)
 constexpr int kEach = 8;         // elements a lane takes in a step
 constexpr int kStep = 32 * kEach;
-constexpr float kSlack = 2.5e-4f;  // of an estimated sum: half a bin's width off in some of the likeliest tokens
-constexpr float kDeepest = 31.98f;        // what lies deeper has no weight: expf(-31.98) is under 2^-46
-constexpr uint32_t kDeep = 0x41ffd70au;   // its bits
 
 // |x| of a logit, up to kDeepest (NaN and -inf: that), M the row's largest and inv = 1 / T.  (M = +inf: its
 // tokens have 0, all others kDeepest, by the largest finite number as M and inv = +inf.)
@@ -163,46 +158,6 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   cluster_wait();
 }
-
-// A level of bins.  The first: |x| to the nearest 1/64, up to 2,047; finer ones: |x|'s bits d in [lo, hi), bin
-// (d - lo) >> shift.
-struct Level {
-  uint32_t lo, hi;
-  int shift;  // -1: the first level
-  __device__ int bin(uint32_t d) const {
-    // (a float add whose last place is 1/64)
-    return shift < 0 ? (int)(__float_as_uint(__uint_as_float(d) + 131072.f) - 0x48000000u) : (int)((d - lo) >> shift);
-  }
-  __device__ uint32_t begin(int b) const {
-    if (shift >= 0) return min((uint32_t)b << shift, hi - lo) + lo;
-    // halfway goes to the even bin
-    return b == 0 ? 0u : b == kBins ? kDeep + 1 : __float_as_uint(((float)b - 0.5f) * 0x1p-6f) + (b & 1);
-  }
-  // n tokens of a bin and an estimate of their weights, the middle's, in units of 2^-18: both in one number.  (Running
-  // sums of whole numbers go up from bin to bin, whoever forms them in what order.)
-  __device__ u64 both(int b, uint32_t n) const {
-    const float x = shift < 0 ? (float)b * 0x1p-6f
-                              : __uint_as_float(min(lo + ((uint32_t)b << shift) + ((1u << shift) >> 1), hi));
-    return n ? __float2ull_rn((float)n * expf(-x) * 0x1p18f) << kCountBits | n : 0;
-  }
-};
-
-// Where the search for a border stands (the same in all CTAs; in shared memory, as the passes over the logits
-// need the registers).  Written by one thread between barriers.
-struct Search {
-  Level lv;
-  bool by_sum;             // the border is one of weight, not of number
-  bool counted, reduced;   // the level's counts are in, and its shares added up
-  bool whole;              // the list is to hold all of the first part
-  bool spread;             // and may (no warp has yet had more tokens of it than its list holds)
-  int first, last, tries;  // bins in question
-  u64 limit, many;         // the border's sum or number, and its number within the level
-  u64 S;                   // the sum of the level's W
-  u64 skipped, before;     // tokens before the level's first bin, and before the taken ones
-  u64 e_before;            // the estimate before these
-  float e0, w, slack;      // the estimate looked for: e0 and what the weight w makes, give or take slack of that
-  uint32_t from, to;       // |x|'s bits of the taken bins
-};
 
 struct Shared {
   union {
@@ -438,27 +393,14 @@ struct Sampler {
   }
 
   // Takes the bins that may hold the border: the one at which the running count reaches q.many, or (by_sum) those at
-  // which the running estimate may pass q.e0 and what q.w (a sum of W) makes, give or take q.slack of that; within
-  // [q.first, q.last] (from the third wrong guess on the middle one).  Every CTA finds the same ones.
+  // which the running estimate may pass q.e0 and what q.w (a sum of W) makes, give or take q.slack of that; of the bins
+  // in question.  Every CTA finds the same ones.
   __device__ void seek() {
     const Search &q = sh.q;
-    u64 target[2] = {q.many, q.many};
-    if (q.by_sum) {
-      // (an estimate's unit is 2^22 of W's; within a hundredth of that the level's own ratio is better: else it has
-      // tokens that top-k left out)
-      float unit = (float)(sh.at[kThreads] >> kCountBits) / (float)q.S;
-      if (!(fabsf(unit * 0x1p22f - 1.f) <= 0.01f)) unit = 0x1p-22f;
-      const float part = q.w * unit, e = q.e0 + part, slack = fabsf(part) * q.slack;
-      target[0] = __float2ull_rn(fmaxf(e - slack, 1.f));
-      target[1] = __float2ull_rn(fmaxf(e + slack, 1.f));
-    }
-    const int first = q.tries < 3 ? q.first : (q.first + q.last) / 2, last = q.tries < 3 ? q.last : first;
-    const int b0 = threadIdx.x * kOwn;
-    auto number = [&](u64 x) { return q.by_sum ? x >> kCountBits : x & ((1ull << kCountBits) - 1); };
-    // a bin (or a thread's bins b .. to) holds a target
-    auto here = [&](u64 t, int b, int to, u64 before, u64 until) {
-      return to >= first && b <= last && (b <= first || number(before) < t) && (to >= last || number(until) >= t);
-    };
+    u64 target[2];
+    q.aim(sh.at[kThreads], target[0], target[1]);
+    const int lowest = q.lowest(), highest = q.highest(), b0 = threadIdx.x * kOwn;
+    auto here = [&](u64 t, int b, int to, u64 before, u64 until) { return q.holds(t, b, to, before, until, lowest, highest); };
     const u64 run = sh.at[threadIdx.x], end = sh.at[threadIdx.x + 1];
     // (its bins a lane each)
 #pragma unroll 1
@@ -740,23 +682,7 @@ struct Sampler {
     uint32_t lo = 0;
     int bits = -1;
     if (!listed) {
-      if (lead) {
-        q.lv = Level{0u, 0u, -1};
-        q.by_sum = by_sum;
-        q.counted = first_level != kGone;
-        q.reduced = first_level == kReduced;
-        q.first = q.tries = 0;
-        q.spread = true;
-        q.last = kBins - 1;
-        q.limit = q.many = limit;
-        q.S = S;
-        q.skipped = 0;
-        q.e0 = 0.f;
-        q.w = (float)limit;
-        q.slack = kSlack;
-        q.from = 0;
-        q.to = kDeep + 1;
-      }
+      if (lead) q.start(by_sum, limit, S, first_level != kGone, first_level == kReduced);
       first_level = kReduced;
       __syncthreads();
     }
@@ -767,34 +693,20 @@ struct Sampler {
       if (!q.counted) count();
       if (!q.reduced) reduce();
       seek();
-      const int bin = (int)sh.taken[0], bin_to = (int)sh.taken[2];
-      constexpr uint32_t kCount = (1u << kCountBits) - 1;
-      const uint32_t before_n = (uint32_t)sh.taken[1] & kCount, until_n = (uint32_t)sh.taken[3] & kCount;
-      if (!q.by_sum && q.lv.shift < 0 && bin == kBins - 1) {
+      if (q.none(sh.taken)) {  // (asked first: among the bins below one row took 0.5 us longer)
         __syncthreads();  // (the next search writes to q)
         return;
       }
-      // the whole first part is listed where it fits
-      const bool whole = q.spread && q.skipped + until_n <= kList;
-      const bool wide = !whole && bin < bin_to && until_n - before_n > kList && q.slack > 0.f;
-      const uint32_t begin = q.lv.begin(bin), from = whole ? 0u : begin, to = q.lv.begin(bin_to + 1);
+      const Bins t = q.bins(sh.taken);
       __syncthreads();
-      if (lead) {
-        q.counted = q.reduced = true;
-        q.whole = whole;
-        q.before = q.skipped + before_n;
-        q.e_before = sh.taken[1] >> kCountBits;
-        q.from = from;
-        q.to = to;
-        if (wide) q.slack = 0.f;
-      }
-      if (wide) {
+      if (lead) q.take(t, sh.taken);
+      if (t.wide) {
         __syncthreads();
         continue;
       }
       // ---- the exact sum of what lies before the bins, and their tokens
       const uint2 *list = sh.list[warp];
-      above_here = list_pass(from, to);
+      above_here = list_pass(t.from, t.to);
       __syncwarp();
       // their own sum
       u64 within = 0;
@@ -804,68 +716,40 @@ struct Sampler {
           for (int i = lane; i < (int)n; i += 32) within += whole_weight(weight(list[i].x));
         else
           r.each_slowly(r.lo, r.hi, lane, [&](uint32_t d, uint32_t v) {
-            if (d - from < to - from && r.inside(d, v)) within += whole_weight(weight(d));
+            if (d - t.from < t.to - t.from && r.inside(d, v)) within += whole_weight(weight(d));
           });
         within = warp_sum(within);
       }
       exchange<3>(above_here, (u64)n, within);
       A = told(0);
       const u64 N = told(1), N_before = told_before(1), B = told(2);
-      const bool low = q.by_sum && A >= q.limit, high = q.by_sum && A + B < q.limit;
+      const bool missed = q.low(A) || q.high(A, B);
       const bool fits = N <= kList && !__any_sync(0xffffffffu, posted(1, lane) > kWarpList || posted(1, lane + 32) > kWarpList);
-      if (!low && !high && fits) {
+      if (!missed && fits) {
         // to the first CTA
 #pragma unroll 1
         for (int i = lane; i < (int)n; i += 32) {
-          const uint2 t = list[i];
-          store_remote(remote(&sh.all[N_before + i], 0), (u64)t.y << 32 | t.x);
-          store_remote(remote(&sh.all_w[N_before + i], 0), whole_weight(weight(t.x)));
+          const uint2 x = list[i];
+          store_remote(remote(&sh.all[N_before + i], 0), (u64)x.y << 32 | x.x);
+          store_remote(remote(&sh.all_w[N_before + i], 0), whole_weight(weight(x.x)));
         }
         listed = (int)N;
-        lo = begin;
-        bits = 32 - __clz((int)(to - begin - 1) | 255);
+        lo = t.begin;
+        bits = 32 - __clz((int)(t.to - t.begin - 1) | 255);
         start = q.by_sum ? A : q.before;
         cluster_barrier();
         break;
       }
-      if (!low && !high && to - from == 1) {
-        const u64 W = whole_weight(weight(from)), stay = q.by_sum ? (q.limit - A + W - 1) / W : q.limit - q.before;
+      if (!missed && t.to - t.from == 1) {
+        const u64 W = whole_weight(weight(t.from)), stay = q.by_sum ? (q.limit - A + W - 1) / W : q.limit - q.before;
         first_level = q.lv.shift < 0 ? kReduced : kGone;
-        rank_ties(from, stay, N_before, n);  // (ends with a barrier, after which q may be written to)
+        rank_ties(t.from, stay, N_before, n);  // (ends with a barrier, after which q may be written to)
         sum = A + stay * W;
         mine = above_here + (stay > N_before ? min(stay - N_before, (u64)n) : 0) * W;
         return;
       }
       __syncthreads();
-      if (lead && (low || high)) {
-        // the estimate was off: on from the exact sum (of a whole part: at its end)
-        if (low)
-          q.last = max(bin - 1, 0);
-        else
-          q.first = min(bin_to + 1, kBins - 1);
-        q.e0 = (float)q.e_before;
-        q.w = low ? -(float)(A - q.limit) : (float)(q.limit - (whole ? B : A));
-        q.slack = 8 * kSlack;
-        ++q.tries;
-      } else if (lead && q.whole) {
-        // (a warp has too many of them, as where a mask leaves a run of tokens: the bins' own, then)
-        q.spread = false;
-      } else if (lead && bin < bin_to) {
-        // (they may be all of the level: the one bin of the estimate, then)
-        q.slack = 0.f;
-      } else if (lead) {
-        // finer bins
-        q.skipped = q.before;
-        q.lv = Level{from, to, max(0, 21 - __clz((int)(to - from - 1)))};
-        q.counted = q.reduced = false;
-        q.first = q.tries = 0;
-        q.last = (int)((to - 1 - from) >> q.lv.shift);
-        q.many = q.limit - q.before;
-        q.e0 = 0.f;
-        q.w = q.by_sum ? (float)(q.limit - A) : 0.f;
-        q.S = B > 0 ? B : 1;
-        q.slack = kSlack;
-      }
+      if (lead) q.narrow(t, A, B);
       __syncthreads();
       first_level = q.lv.shift < 0 ? kReduced : kGone;
     }
