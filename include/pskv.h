@@ -78,7 +78,8 @@ typedef struct CUevent_st *pskv_event_t;
 #define PSKV_FAULT_BAD_LENGTH 4u    /* a device length outside [tokens, table_stride * page_size]: clamped */
 #define PSKV_FAULT_WAIT_TIMEOUT 8u  /* a bounded wait on a copy expired: the partition was dropped */
 #define PSKV_FAULT_EMPTY_ROW 16u    /* a row had no attended key: its output was written as zeros */
-#define PSKV_FAULT_BAD_STATE 32u    /* merge input with m = -inf but l != 0, or a NaN m: treated as empty */
+#define PSKV_FAULT_BAD_STATE 32u    /* merge input with m = -inf but l != 0, or a NaN m; a sampled row whose filters' border
+                                       was not found in the passes that it may take: treated as empty */
 #define PSKV_FAULT_BAD_POSITION 64u /* a prep token whose rotation position is outside the table: skipped */
 #define PSKV_FAULT_BAD_MASK 128u    /* a tree mask without its own bit or with a later one: later bits ignored */
 #define PSKV_FAULT_BAD_TOKEN 256u   /* a drafted token outside the vocabulary: refused like any other */
@@ -603,7 +604,8 @@ typedef struct pskv_sample_desc {
  *   probs         device [rows][vocab] of probs_dtype (F32 or BF16), or NULL
  *   status        device int32[4] fault word or NULL
  * A row without any finite or +inf logit gives token -1, zeros and PSKV_FAULT_EMPTY_ROW; several logits
- * of +inf share the weight.  vocab 1 .. 2^22.  No workspace.  Errors: INVALID_ARG (also neither tokens
+ * of +inf share the weight.  (The search for a border is bounded, far above what any row is known to take; one that
+ * would pass the bound gives token -1, zeros and PSKV_FAULT_BAD_STATE.)  vocab 1 .. 2^22.  No workspace.  Errors: INVALID_ARG (also neither tokens
  * nor probs asked for, or these not apart from each other and from what is read), CUDA. */
 int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t requests,
                   int32_t tokens_per_request, int32_t vocab, const pskv_sample_desc *filters,

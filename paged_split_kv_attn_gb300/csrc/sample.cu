@@ -55,7 +55,6 @@ constexpr int kMostStaged = 180 << 10;
 constexpr int kOwn = kBins / kThreads;
 constexpr int kWarpList = kList / kWarps;  // listed tokens of a warp
 constexpr int kFew = kThreads / 4;         // of a list whose tokens are compared with each other
-constexpr int kMostPasses = 256;  // (never reached: a search ends in less)
 constexpr int kEach = 8;         // elements a lane takes in a step
 constexpr int kStep = 32 * kEach;
 
@@ -673,7 +672,7 @@ struct Sampler {
   // shortest part whose W sum to `limit` at least (1 .. their sum); S: the sum of all W.  sum: that part's, mine:
   // this piece's share of it.  listed: how many tokens are listed where the list holds all that lies inside the
   // border, else 0, before and after: then only the first CTA moves its border, and knows sum.
-  // Where nothing with weight would be left out the border, sum and mine stay.
+  // Where nothing with weight would be left out the border, sum and mine stay.  sum 0: the border was not found.
   // (One loop with each step in it once: the code is long, and it is fetched from memory when a call is the first.)
   __device__ void find_border(bool by_sum, u64 limit, u64 S, u64 &sum, u64 &mine, int &listed) {
     Search &q = sh.q;
@@ -689,7 +688,11 @@ struct Sampler {
     // A pass ends the search, goes to a level of one of its level's bins (up to three times), or narrows what it looks at
     // within it: [first, last] in halves from the third wrong guess on, or once to one bin or to the bins alone
 #pragma unroll 1
-    for (int pass = 0; !listed && pass < kMostPasses; ++pass) {
+    for (int pass = 0; !listed; ++pass) {
+      if (pass == kMostPasses) {
+        sum = 0;
+        return;
+      }
       if (!q.counted) count();
       if (!q.reduced) reduce();
       seek();
@@ -906,11 +909,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pskv_sample(const SampleArgs
     if (filters) {
       const u64 S = total;
 #pragma unroll 1
-      for (int by_sum = some ? 0 : 1; by_sum < (part ? 2 : 1); ++by_sum)
+      for (int by_sum = some ? 0 : 1; by_sum < (part ? 2 : 1) && total; ++by_sum)
         if (!listed || s.rank == 0)
           s.find_border(by_sum, by_sum ? max(share(p, total), 1ull) : (u64)k, S, total, mine, listed);
       r.least = least_w;
-      if (listed) {
+      if (!total) {
+        // (as of an empty row, nothing is kept: no piece has a share)
+        total = 1;
+        mine = 0;
+        r.least = 2.f;
+        if (s.rank == 0 && threadIdx.x == 0) {
+          if (a.tokens) a.tokens[row] = -1;
+          raise_fault(a.status, PSKV_FAULT_BAD_STATE);
+        }
+      } else if (listed) {
         if (r.least > 0.f && s.rank == 0) total = s.list_sum(listed, UINT_MAX);
       } else {
         // (where the border's weight is above it, so are all: expf is right to 2^-22)

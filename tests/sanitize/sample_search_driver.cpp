@@ -17,6 +17,7 @@ using namespace pskv::border;
 namespace {
 
 constexpr int kMost = 48;  // passes of a search
+static_assert(kMost < kMostPasses, "the kernel's own bound is not reached");
 constexpr int kWarpList = kList / 8, kStep = 256;
 
 u64 whole_weight(uint32_t d) { return (u64)std::nearbyint((double)exp_of(-float_of(d)) * 0x1p40); }
