@@ -9,6 +9,7 @@
 // KV heads) 3.1 us for 6.6 MB; of one latent window of 8 2.1 us.  kv_fork_rows of 64 forks of 16 rows over four layers (571 MB)
 // 86 us, 6.6 TB/s or 97 % of a plain copy's rate; one latent row's three forks 2.9 us.
 #include "pskv_internal.cuh"
+#include "pskv_plan.h"
 #include "tree.h"
 
 namespace pskv {
@@ -91,68 +92,142 @@ __global__ void __launch_bounds__(kThreads) pskv_keep_tokens(const KeepArgs a, c
   }
 }
 
-// Grid (pieces of a page, forks, layers): a piece is kThreads * kAhead vectors of one region's head, whose rows lie
-// one after another (a block of one column of every row, as above, wrote short runs: 111 instead of 86 us).  As above, every block checks its fork alike; the first one reports, and writes the row's table,
-// length and lease.  Sources are rows that no fork of the call writes.
-__global__ void __launch_bounds__(kThreads) pskv_fork_rows(const ForkArgs a, const __grid_constant__ Pools p) {
-  const int f = blockIdx.y, i = threadIdx.x;
-  const bool first = blockIdx.x == 0 && blockIdx.z == 0;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int src = a.src[f], dst = a.dst[f];
-  uint32_t fault = 0;
-  if (src < 0 || src >= a.batch || dst < 0 || dst >= a.batch || src == dst) fault = PSKV_FAULT_BAD_ROW;
-  for (int k = i; k < a.n; k += kThreads)
-    if (k != f && (a.dst[k] == dst || a.src[k] == dst)) fault = PSKV_FAULT_BAD_ROW;
-  if (__syncthreads_or(fault != 0)) {
-    if (first && fault) raise_fault(p.status, fault);
-    return;
+// ---- forks
+
+namespace {
+
+// One fork: from where its row goes on, and the page its last keys are copied from and to.
+struct Fork {
+  int src, dst, len, whole, rest, old_page, new_page;
+
+  // Its rows exist.  (Not yet: that no other fork of the call has dst.)
+  __device__ bool names_rows(const ForkArgs &a, int f) {
+    src = a.src[f];
+    dst = a.dst[f];
+    return src >= 0 && src < a.batch && dst >= 0 && dst < a.batch && src != dst;
   }
-  const int len = a.seq_lens[src], lease = a.pages_of_row[src];
-  if (len < 0 || (long long)len > (long long)a.table_stride * p.page_size) {
-    if (first && i == 0) raise_fault(p.status, PSKV_FAULT_BAD_LENGTH);
-    return;
-  }
-  const int whole = len / p.page_size, rest = len - whole * p.page_size, pages = whole + (rest > 0);
-  if (lease < pages || lease > a.table_stride) {
-    if (first && i == 0) raise_fault(p.status, PSKV_FAULT_PAST_PAGES);
-    return;
-  }
-  const int32_t *from = a.page_tables + (size_t)src * a.table_stride;
-  int old_page = 0, new_page = 0;
-  if (rest > 0) {
-    old_page = from[whole];
+  // What it is refused for beside its rows, or 0.
+  __device__ uint32_t look(const ForkArgs &a, const Pools &p, int f) {
+    len = a.seq_lens[src];
+    const int lease = a.pages_of_row[src];
+    if (len < 0 || (long long)len > (long long)a.table_stride * p.page_size) return PSKV_FAULT_BAD_LENGTH;
+    whole = len / p.page_size;
+    rest = len - whole * p.page_size;
+    if (lease < whole + (rest > 0) || lease > a.table_stride) return PSKV_FAULT_PAST_PAGES;
+    old_page = new_page = 0;
+    if (rest == 0) return 0;
+    old_page = a.page_tables[(size_t)src * a.table_stride + whole];
     new_page = a.new_pages[f];
-    if (old_page < 0 || old_page >= p.num_pages || new_page < 0 || new_page >= p.num_pages || old_page == new_page) {
-      if (first && i == 0) raise_fault(p.status, PSKV_FAULT_BAD_PAGE);
-      return;
-    }
+    return old_page < 0 || old_page >= p.num_pages || new_page < 0 || new_page >= p.num_pages || old_page == new_page
+               ? PSKV_FAULT_BAD_PAGE
+               : 0;
   }
-  if (first) {
+  // The row's table, length and lease, by a block.
+  __device__ void write_row(const ForkArgs &a, int i) const {
+    const int32_t *from = a.page_tables + (size_t)src * a.table_stride;
     int32_t *table = a.page_tables + (size_t)dst * a.table_stride;
     for (int s = i; s < whole; s += kThreads) table[s] = from[s];
     if (i == 0) {
       if (rest > 0) table[whole] = new_page;
       a.seq_lens[dst] = len;
-      a.pages_of_row[dst] = pages;
+      a.pages_of_row[dst] = whole + (rest > 0);
     }
   }
-  // this block's piece: of a K head, or behind these of a V head
-  const int k_pieces = pieces(p.k_vecs, p.page_size), v_pieces = pieces(p.v_vecs, p.page_size);
-  const bool is_k = (int)blockIdx.x < p.heads * k_pieces;
-  const int x = is_k ? blockIdx.x : blockIdx.x - p.heads * k_pieces, each = is_k ? k_pieces : v_pieces;
-  const int head = x / each, vecs = is_k ? p.k_vecs : p.v_vecs, run = rest * vecs;
-  const int u0 = (x - head * each) * kThreads * kAhead + i;
-  uint4 *pool = static_cast<uint4 *>(is_k ? p.k[blockIdx.z] : p.v[blockIdx.z]);
-  const uint4 *old_run = pool + ((size_t)old_page * p.heads + head) * p.page_size * vecs;
-  uint4 *new_run = pool + ((size_t)new_page * p.heads + head) * p.page_size * vecs;
-  uint4 q[kAhead];
+  // Piece x of a layer's page, K heads before V heads: kThreads * kAhead vectors of one head's rows, which lie one after
+  // another (a block of one column of every row, as above, wrote short runs: 111 instead of 86 us).
+  __device__ void copy(const Pools &p, int layer, int x, int i) const {
+    const int k_pieces = pieces(p.k_vecs, p.page_size), v_pieces = pieces(p.v_vecs, p.page_size);
+    const bool is_k = x < p.heads * k_pieces;
+    const int y = is_k ? x : x - p.heads * k_pieces, each = is_k ? k_pieces : v_pieces;
+    const int head = y / each, vecs = is_k ? p.k_vecs : p.v_vecs, run = rest * vecs;
+    const int u0 = (y - head * each) * kThreads * kAhead + i;
+    uint4 *pool = static_cast<uint4 *>(is_k ? p.k[layer] : p.v[layer]);
+    const uint4 *old_run = pool + ((size_t)old_page * p.heads + head) * p.page_size * vecs;
+    uint4 *new_run = pool + ((size_t)new_page * p.heads + head) * p.page_size * vecs;
+    uint4 q[kAhead];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k)
-    if (u0 + k * kThreads < run) q[k] = old_run[u0 + k * kThreads];
+    for (int k = 0; k < kAhead; ++k)
+      if (u0 + k * kThreads < run) q[k] = old_run[u0 + k * kThreads];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k)
-    if (u0 + k * kThreads < run) new_run[u0 + k * kThreads] = q[k];
+    for (int k = 0; k < kAhead; ++k)
+      if (u0 + k * kThreads < run) new_run[u0 + k * kThreads] = q[k];
+  }
+};
+
+}  // namespace
+
+// Grid (pieces of a layer's page, forks, layers).  As above, every block checks its fork alike; the first one
+// reports, and writes the row's table, length and lease.  Sources are rows that no fork of the call writes.
+__global__ void __launch_bounds__(kThreads) pskv_fork_rows(const ForkArgs a, const __grid_constant__ Pools p) {
+  const int f = blockIdx.y, i = threadIdx.x;
+  const bool first = blockIdx.x == 0 && blockIdx.z == 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  Fork fork;
+  uint32_t fault = fork.names_rows(a, f) ? 0 : PSKV_FAULT_BAD_ROW;
+  for (int k = i; k < a.n; k += kThreads)
+    if (k != f && (a.dst[k] == fork.dst || a.src[k] == fork.dst)) fault = PSKV_FAULT_BAD_ROW;
+  if (__syncthreads_or(fault != 0)) {
+    if (first && fault) raise_fault(p.status, fault);
+    return;
+  }
+  fault = fork.look(a, p, f);
+  if (fault) {
+    if (first && i == 0) raise_fault(p.status, fault);
+    return;
+  }
+  if (first) fork.write_row(a, i);
+  fork.copy(p, blockIdx.z, blockIdx.x, i);
+}
+
+// The same for many forks.  Each is compared with all others, so that a block for each piece reads the call's n forks n *
+// pieces times: 59.7 ms for 65,535 forks of 16-row pages in eight layers, 7.6 in one.  Here a block takes more pieces (of any
+// layer) as n goes up, then several forks with all of theirs, which it compares at once: 1.6 and 1.5.
+// Grid (blocks of a fork's pieces, groups of forks).
+__global__ void __launch_bounds__(kThreads) pskv_fork_many(const ForkArgs a, const __grid_constant__ Pools p, int all_pieces,
+                                                           const ForkBlocks of) {
+  __shared__ uint32_t found[kThreads / 32];
+  const int f0 = blockIdx.y * of.forks, i = threadIdx.x;
+  const int x0 = blockIdx.x * of.pieces, x1 = min(x0 + of.pieces, all_pieces), of_layer = all_pieces / p.count;
+  const bool first = blockIdx.x == 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!first) {  // (of one fork) nothing to copy, nothing to compare
+    Fork fork;
+    if (!fork.names_rows(a, f0) || fork.look(a, p, f0) || fork.rest == 0) return;
+  }
+  int rows[kForksTogether];
+#pragma unroll
+  for (int g = 0; g < kForksTogether; ++g) rows[g] = g < of.forks && f0 + g < a.n ? a.dst[f0 + g] : -1;
+  uint32_t taken = 0;  // bit g: another fork has the row of fork f0 + g (or that fork reads it itself)
+#pragma unroll 2
+  for (int k = i; k < a.n; k += kThreads) {
+    const int s = a.src[k], d = a.dst[k];
+#pragma unroll
+    for (int g = 0; g < kForksTogether; ++g) taken |= (uint32_t)(s == rows[g] || (d == rows[g] && k != f0 + g)) << g;
+  }
+  taken = __reduce_or_sync(0xffffffffu, taken);
+  if ((i & 31) == 0) found[i >> 5] = taken;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) taken |= found[w];
+#pragma unroll 1
+  for (int g = 0; g < of.forks && f0 + g < a.n; ++g) {
+    Fork fork;
+    uint32_t fault = fork.names_rows(a, f0 + g) && !((taken >> g) & 1u) ? 0 : PSKV_FAULT_BAD_ROW;
+    if (!fault) fault = fork.look(a, p, f0 + g);
+    if (fault) {
+      if (first && i == 0) raise_fault(p.status, fault);
+      continue;
+    }
+    if (first) fork.write_row(a, i);
+    int layer = x0 / of_layer, x = x0 - layer * of_layer;
+#pragma unroll 1
+    for (int k = fork.rest > 0 ? x0 : x1; k < x1; ++k) {
+      fork.copy(p, layer, x, i);
+      if (++x == of_layer) x = 0, ++layer;
+    }
+  }
 }
 
 cudaError_t launch_keep(const KeepArgs &a, const Pools &p, cudaStream_t s) {
@@ -162,9 +237,12 @@ cudaError_t launch_keep(const KeepArgs &a, const Pools &p, cudaStream_t s) {
 }
 
 cudaError_t launch_fork(const ForkArgs &a, const Pools &p, cudaStream_t s) {
-  const dim3 grid((unsigned)(p.heads * (pieces(p.k_vecs, p.page_size) + pieces(p.v_vecs, p.page_size))),
-                  (unsigned)a.n, (unsigned)p.count);
-  return launch_pdl(pskv_fork_rows, grid, dim3(kThreads), 0, s, a, p);
+  const int of_layer = p.heads * (pieces(p.k_vecs, p.page_size) + pieces(p.v_vecs, p.page_size)), all = p.count * of_layer;
+  if (a.n <= kFewForks)
+    return launch_pdl(pskv_fork_rows, dim3((unsigned)of_layer, (unsigned)a.n, (unsigned)p.count), dim3(kThreads), 0, s, a, p);
+  const ForkBlocks b = fork_blocks(a.n, all);
+  const dim3 grid((unsigned)((all + b.pieces - 1) / b.pieces), (unsigned)((a.n + b.forks - 1) / b.forks));
+  return launch_pdl(pskv_fork_many, grid, dim3(kThreads), 0, s, a, p, all, b);
 }
 
 }  // namespace pskv

@@ -3,6 +3,8 @@
 
 #include <stdlib.h>
 
+#include <algorithm>
+
 namespace pskv {
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -70,6 +72,12 @@ int check_lengths(const pskv_layout *layout, int32_t batch, int32_t table_stride
   for (int32_t b = 0; b < batch; ++b)
     if (seq_lens_host[b] < min_len || (int64_t)seq_lens_host[b] > cap) return PSKV_ERR_INVALID_ARG;
   return PSKV_OK;
+}
+
+ForkBlocks fork_blocks(int32_t n, int64_t pieces) {
+  const int64_t each = ((int64_t)n + kForkScan - 1) / kForkScan;
+  if (each <= pieces) return {(int)std::max<int64_t>(each, 1), 1};
+  return {(int)pieces, (int)std::min<int64_t>(each / pieces, kForksTogether)};
 }
 
 int plan_splits(int slots, int32_t batch, int32_t num_kv_heads, const int32_t *seq_lens_host,

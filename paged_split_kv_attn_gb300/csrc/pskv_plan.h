@@ -79,6 +79,17 @@ LatentPlan plan_latent(int clusters, int head_dim_v, int32_t batch, const int32_
 // not grow with the lengths: a batch of even rows that fills the pairs is left whole, and one
 // long row between short ones is cut.)
 int latent_most_splits(int clusters, int32_t batch, int64_t longest, int64_t blocks, int32_t num_splits);
+// kv_fork_rows' blocks.  A block compares its forks with the n of the call.  Up to kFewForks of them it has one piece of a
+// fork's page (2,048 forks of 16-row pages in four layers: 31 us, by the rule below 38; 4,096: 72 and 62; 16,384: 716 and
+// 220).  Then a piece more (`pieces` of them, all layers) for every kForkScan forks of the call, about as long as a
+// piece's copy takes; where a block has all of a fork's pieces, up to kForksTogether forks.
+constexpr int kFewForks = 2048;
+constexpr int kForkScan = 1024;
+constexpr int kForksTogether = 8;
+struct ForkBlocks {
+  int pieces, forks;  // of a block (several forks: all pieces of each)
+};
+ForkBlocks fork_blocks(int32_t n, int64_t pieces);
 int plan_splits(int slots, int32_t batch, int32_t num_kv_heads, const int32_t *seq_lens_host,
                 int fill32 = 32);
 
