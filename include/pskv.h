@@ -97,6 +97,11 @@ typedef struct CUevent_st *pskv_event_t;
 #define PSKV_EXPANDED_NOPE 128     /* unrotated columns of an expanded query or key */
 #define PSKV_EXPANDED_V 128        /* columns of an expanded value */
 #define PSKV_MAX_LAYOUTS 128       /* layouts (layers) of one kv_keep_tokens or kv_fork_rows call */
+#define PSKV_MAX_VOCAB 4194304     /* tokens of a row of sample_tokens */
+#define PSKV_MAX_SAMPLED 16777216  /* rows (requests * tokens_per_request) of one sample_tokens call */
+#define PSKV_MAX_TREES 1048576     /* rows of one verify_tree call */
+#define PSKV_MAX_KEPT_ROWS 65535   /* rows of one kv_keep_tokens call */
+#define PSKV_MAX_FORKS 65535       /* forks of one kv_fork_rows call */
 
 /* Description of one paged KV pool.
  *
@@ -605,7 +610,8 @@ typedef struct pskv_sample_desc {
  *   status        device int32[4] fault word or NULL
  * A row without any finite or +inf logit gives token -1, zeros and PSKV_FAULT_EMPTY_ROW; several logits
  * of +inf share the weight.  (The search for a border is bounded, far above what any row is known to take; one that
- * would pass the bound gives token -1, zeros and PSKV_FAULT_BAD_STATE.)  vocab 1 .. 2^22.  No workspace.  Errors: INVALID_ARG (also neither tokens
+ * would pass the bound gives token -1, zeros and PSKV_FAULT_BAD_STATE.)  vocab
+ * 1..PSKV_MAX_VOCAB, requests and tokens_per_request 1 at least, their product PSKV_MAX_SAMPLED at most.  No workspace.  Errors: INVALID_ARG (also neither tokens
  * nor probs asked for, or these not apart from each other and from what is read), CUDA. */
 int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t requests,
                   int32_t tokens_per_request, int32_t vocab, const pskv_sample_desc *filters,
@@ -625,7 +631,7 @@ int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t
  *   path       device int32[batch][num_tokens]: the standing tokens' places, going up, then -1
  *   kept       device int32[batch]: how many stand (1 at least)
  *   status     device int32[4] fault word or NULL
- * num_tokens 1..PSKV_MAX_WINDOW_TOKENS.  No workspace.  Errors: INVALID_ARG (also outputs that are not apart
+ * batch 1..PSKV_MAX_TREES, num_tokens 1..PSKV_MAX_WINDOW_TOKENS.  No workspace.  Errors: INVALID_ARG (also outputs that are not apart
  * from each other and from what is read), CUDA. */
 int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t *sampled,
                 int32_t batch, int32_t num_tokens, int32_t *tokens, int32_t *path, int32_t *kept,
@@ -642,11 +648,11 @@ int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t 
  *              the rest is not looked at.  Else PSKV_FAULT_BAD_PATH
  *   kept       device int32[batch], 0..num_tokens each (else PSKV_FAULT_BAD_PATH)
  *   seq_lens   device int32[batch]: each at least num_tokens, or 0 (a padded batch's row: nothing is
- *              done, its new length is 0); else PSKV_FAULT_BAD_LENGTH
+ *              done, its new length is 0), table_stride * page_size at most; else PSKV_FAULT_BAD_LENGTH
  *   new_lens   device int32[batch]; not one of the arrays read
  * A row refused (these, or a page id outside the pool: PSKV_FAULT_BAD_PAGE) keeps its rows and its
- * length.  The window's pages must belong to the row alone (kv_fork_rows' last pages do).  num_tokens
- * 1..PSKV_MAX_WINDOW_TOKENS.  Errors: INVALID_ARG (also layouts that differ or share memory), UNSUPPORTED (pages of more
+ * length.  The window's pages must belong to the row alone (kv_fork_rows' last pages do).  batch
+ * 1..PSKV_MAX_KEPT_ROWS, num_tokens 1..PSKV_MAX_WINDOW_TOKENS.  Errors: INVALID_ARG (also layouts that differ or share memory), UNSUPPORTED (pages of more
  * than 16 GB), CUDA. */
 int kv_keep_tokens(const pskv_layout *const *layouts, int32_t num_layouts,
                    const int32_t *page_tables, int32_t table_stride, const int32_t *seq_lens,
@@ -667,8 +673,9 @@ int kv_keep_tokens(const pskv_layout *const *layouts, int32_t num_layouts,
  *   page_tables   device int32[batch][table_stride], read and written; seq_lens, pages_of_row device
  *                 int32[batch], too; these three apart from each other and from src, dst and new_pages
  * A fork is also refused for a length outside [0, table_stride * page_size] (PSKV_FAULT_BAD_LENGTH), a lease
- * of fewer pages than its keys need (PSKV_FAULT_PAST_PAGES), or a page to copy from or to that is outside the
- * pool or the same (PSKV_FAULT_BAD_PAGE).  A refused fork writes nothing.  n 0..65535.
+ * of fewer pages than its keys need or of more than table_stride (PSKV_FAULT_PAST_PAGES), or a page to copy from or to that is outside the
+ * pool or the same (PSKV_FAULT_BAD_PAGE).  A refused fork writes nothing.  n 0..PSKV_MAX_FORKS (each is
+ * compared with all others: 65,535 forks take 1.5 ms beside what they copy).
  * Errors: INVALID_ARG (also layouts that differ or share memory), UNSUPPORTED (pages of more than 16 GB), CUDA. */
 int kv_fork_rows(const pskv_layout *const *layouts, int32_t num_layouts, const int32_t *src,
                  const int32_t *dst, const int32_t *new_pages, int32_t n, int32_t *page_tables,

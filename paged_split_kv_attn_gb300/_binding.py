@@ -56,6 +56,11 @@ PSKV_LATENT_MAX_HEADS = 128
 PSKV_EXPANDED_NOPE = 128
 PSKV_EXPANDED_V = 128
 PSKV_MAX_LAYOUTS = 128
+PSKV_MAX_VOCAB = 1 << 22
+PSKV_MAX_SAMPLED = 1 << 24
+PSKV_MAX_TREES = 1 << 20
+PSKV_MAX_KEPT_ROWS = 65535
+PSKV_MAX_FORKS = 65535
 PSKV_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 # Every function the header declares, in the header's order.

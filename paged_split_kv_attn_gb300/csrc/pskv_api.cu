@@ -977,8 +977,8 @@ int sample_tokens(const void *logits, int32_t dtype, int64_t logits_row, int32_t
                   int32_t tokens_per_request, int32_t vocab, const pskv_sample_desc *filters,
                   const float *u, int32_t *tokens, void *probs, int32_t probs_dtype,
                   int32_t *status, pskv_stream_t stream) {
-  if (!logits || requests < 1 || tokens_per_request < 1 || vocab < 1 || vocab > (1 << 22) ||
-      logits_row < vocab || (int64_t)requests * tokens_per_request > (1 << 24))
+  if (!logits || requests < 1 || tokens_per_request < 1 || vocab < 1 || vocab > PSKV_MAX_VOCAB ||
+      logits_row < vocab || (int64_t)requests * tokens_per_request > PSKV_MAX_SAMPLED)
     return PSKV_ERR_INVALID_ARG;
   if ((dtype != PSKV_DTYPE_F32 && dtype != PSKV_DTYPE_BF16) || (!tokens && !probs) ||
       (tokens == nullptr) != (u == nullptr))
@@ -1030,7 +1030,7 @@ int verify_tree(const int32_t *drafts, const uint64_t *tree_mask, const int32_t 
                 int32_t batch, int32_t num_tokens, int32_t *tokens, int32_t *path, int32_t *kept,
                 int32_t *status, pskv_stream_t stream) {
   if (!drafts || !tree_mask || !sampled || !tokens || !path || !kept || batch < 1 ||
-      batch > (1 << 20) || num_tokens < 1 || num_tokens > PSKV_MAX_WINDOW_TOKENS)
+      batch > PSKV_MAX_TREES || num_tokens < 1 || num_tokens > PSKV_MAX_WINDOW_TOKENS)
     return PSKV_ERR_INVALID_ARG;
   if (!aligned(tree_mask, 8) || !aligned(drafts, 4) || !aligned(sampled, 4) || !aligned(tokens, 4) ||
       !aligned(path, 4) || !aligned(kept, 4) || !aligned(status, 4))
@@ -1062,7 +1062,7 @@ int kv_keep_tokens(const pskv_layout *const *layouts, int32_t num_layouts,
   const int rc = gather_pools(layouts, num_layouts, &p);
   if (rc) return rc;
   if (!page_tables || !seq_lens || !path || !kept || !new_lens || table_stride < 1 || batch < 1 ||
-      batch > 65535 || num_tokens < 1 || num_tokens > PSKV_MAX_WINDOW_TOKENS)
+      batch > PSKV_MAX_KEPT_ROWS || num_tokens < 1 || num_tokens > PSKV_MAX_WINDOW_TOKENS)
     return PSKV_ERR_INVALID_ARG;
   if (!aligned(page_tables, 4) || !aligned(seq_lens, 4) || !aligned(path, 4) || !aligned(kept, 4) ||
       !aligned(new_lens, 4))
@@ -1085,7 +1085,7 @@ int kv_fork_rows(const pskv_layout *const *layouts, int32_t num_layouts, const i
   Pools p;
   const int rc = gather_pools(layouts, num_layouts, &p);
   if (rc) return rc;
-  if (n < 0 || n > 65535 || table_stride < 1 || batch < 1) return PSKV_ERR_INVALID_ARG;
+  if (n < 0 || n > PSKV_MAX_FORKS || table_stride < 1 || batch < 1) return PSKV_ERR_INVALID_ARG;
   if (n == 0) return PSKV_OK;
   if (!src || !dst || !new_pages || !page_tables || !seq_lens || !pages_of_row)
     return PSKV_ERR_INVALID_ARG;
