@@ -428,13 +428,14 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
       NEED(l->stride(0) % each == 0 && (each == 1 || l->stride(0) / each == step));
       step = l->stride(0) / each;
     }
-    NEED(step >= vocab && a[1] != Py_None);
-    void *up, *kp, *hp, *tp, *pp, *mp, *sp, *qp = nullptr;
+    NEED(step >= vocab);
+    const bool draw = a[1] != Py_None;  // (else only the distribution is asked for)
+    void *up = nullptr, *kp = nullptr, *hp, *tp, *pp, *mp, *sp, *qp = nullptr;
     pskv_stream_t s;
     auto head = [&](PyObject *o, at::ScalarType t, void **p) {
       return three ? whole(o, t, dev, {batch, each}, p) : whole(o, t, dev, {batch}, p);
     };
-    NEED(head(a[1], at::kFloat, &up) && maybe(a[2], at::kFloat, dev, {batch}, &hp) && maybe(a[3], kI32, dev, {batch}, &tp));
+    NEED((!draw || head(a[1], at::kFloat, &up)) && maybe(a[2], at::kFloat, dev, {batch}, &hp) && maybe(a[3], kI32, dev, {batch}, &tp));
     NEED(maybe(a[4], at::kFloat, dev, {batch}, &pp) && maybe(a[5], at::kFloat, dev, {batch}, &mp));
     NEED(fault_word(a[8], dev, &sp) && stream_of(a[9], dev, &s));
     int32_t code = PSKV_DTYPE_F32;
@@ -446,11 +447,11 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
       code = q->scalar_type() == kBf16 ? PSKV_DTYPE_BF16 : PSKV_DTYPE_F32;
     }
     at::Tensor tokens;
-    if (a[6] == Py_None) {
+    if (a[6] != Py_None) {
+      NEED(head(a[6], kI32, &kp));
+    } else if (draw) {
       tokens = three ? fresh(*l, kI32, {batch, each}, a[9], s, dev) : fresh(*l, kI32, {batch}, a[9], s, dev);
       kp = tokens.data_ptr();
-    } else {
-      NEED(head(a[6], kI32, &kp));
     }
     const pskv_sample_desc f = {(const float *)hp, (const int32_t *)tp, (const float *)pp, (const float *)mp};
     void *lp = l->data_ptr();
@@ -459,7 +460,7 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
     rc = g_sample(lp, kind == kBf16 ? PSKV_DTYPE_BF16 : PSKV_DTYPE_F32, step, (int32_t)batch, (int32_t)each,
                   (int32_t)vocab, &f, (const float *)up, (int32_t *)kp, qp, code, (int32_t *)sp, s);
     Py_END_ALLOW_THREADS
-    return result(rc, a[6], tokens);
+    return draw ? result(rc, a[6], tokens) : PyLong_FromLong(rc);
   });
 }
 

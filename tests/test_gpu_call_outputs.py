@@ -93,3 +93,25 @@ def test_deterministic_mode_fills_what_a_call_leaves(form):
     finally:
         torch.use_deterministic_algorithms(False)
     assert torch.equal(out[:60], want) and bool(out[60:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_distribution_alone_is_a_compiled_call(monkeypatch, dtype):
+    """Without uniform numbers sample_tokens makes only probabilities: by the compiled call, to the Python form's bits."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(63)
+    l = torch.randn(3, 2, 900, generator=gen, device="cuda").to(dtype)
+    kw = dict(top_k=i32([5, 0, 900]), top_p=torch.tensor([0.5, 0.9, 1.0], device="cuda"))
+    want, got = (torch.empty(3, 2, 900, dtype=dtype, device="cuda") for _ in range(2))
+    with monkeypatch.context() as m:
+        m.setattr(B, "_calls", B._PythonCalls)
+        assert pskv.sample_tokens(l, None, probs=want, **kw) is None
+    assert B._bind_calls(pskv.load_library()) is not B._PythonCalls, "the compiled calls were not built"
+    with pytest.raises(pskv.PskvError):
+        pskv.sample_tokens(l, None, **kw)
+    with pytest.raises(pskv.PskvError):
+        pskv.sample_tokens(l, None, tokens=torch.zeros(3, 2, dtype=torch.int32, device="cuda"), probs=got)
+    monkeypatch.setattr(B, "_LIB", object())  # (what the Python form calls)
+    assert pskv.sample_tokens(l, None, probs=got, **kw) is None
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
