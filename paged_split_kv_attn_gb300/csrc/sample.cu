@@ -22,12 +22,16 @@
 //   4  else the drawn token's piece again; and the probabilities where they are asked for.
 // Between passes the warps' results cross the cluster through distributed shared memory, one barrier each.
 //
-// What bounds it (device time, calls one after the other): without top-k and top-p instructions, about 22 a token
-// for M, the exponential and two whole digits of it: 64 x 131,072 f32 16.3 us (2.1 TB/s), 256 x 32,001 16.4.  top-p over
-// weights that are spread out (64 x 131,072: 39.9 us) takes a second pass of exponentials, 7 of these us, and
-// eight cluster barriers of about 1 us each with what they wait for.  One row of 32,001 with top-k, top-p and min-p
-// (12.6 us) is that chain alone, and the first fetch of its code: hence loops that are not unrolled wherever speed
-// does not count (134 -> 97 KB of code: 64 x 131,072 49 -> 45 us, a row 16 -> 15).
+// What bounds it (device time, calls one after the other; stages by clock readings in each row's first CTA).  Without top-k and
+// top-p (64 x 131,072 f32 16.4 us, 2.0 TB/s; 256 x 32,001 16.7) reading and computing take turns, as all rows are resident and
+// begin at once: M 3.4 us, the exponentials and their sums 5.7, two exchanges 3.9, the draw 0.9 to 1.9, launch and start 2;
+// 40 warp instructions for 32 tokens over the whole call, issue slots 44 % busy.
+// top-p over weights that are spread out (64 x 131,072: 40.3 us): M 3.5, sum and histogram 7.2, the list's pass with its
+// exponentials again 7.5; eight cluster barriers with their exchanges 14, under 1 us each where nothing is late and nothing is
+// to be sent; bins, list and border sought 5.7; the draw 1.  One row of 32,001 with top-k, top-p and min-p
+// (12.7 us) is that chain alone, and the first fetch of its code: hence loops that are not unrolled wherever speed
+// does not count (134 -> 97 KB of code at the time: 64 x 131,072 49 -> 45 us, a row 16 -> 15).
+// Temperature 0 seeks M's lowest index token by token: 64 x 131,072 17.2 us, 600 rows (one CTA each) 278 against 148 of a draw.
 #include <float.h>
 #include <limits.h>
 #include <math_constants.h>
